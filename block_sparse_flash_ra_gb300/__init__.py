@@ -8,8 +8,9 @@ runs in the library's CUDA kernels; there is no fallback: if the library has
 not been built, every call raises.
 
 The helpers at the bottom (``make_params``, ``build_mask``, ``forward``,
-``backward``, ``permute``, ``unpermute``) allocate outputs with torch and
-call the same entry points.
+``backward``, ``permute``, ``unpermute``; for a paged cache ``new_kv_cache``,
+``make_kv_cache``, ``kv_write``, ``kv_read``, ``make_paged_params``,
+``paged_forward``) allocate outputs with torch and call the same entry points.
 """
 from __future__ import annotations
 
@@ -30,6 +31,9 @@ __all__ = [
     "ra_attn_fwd_step", "ra_attn_bwd_step", "ra_cast_from_f32", "ra_add_f32",
     "ra_get_device_status", "ra_launch_count", "ra_selftest_wait_timeout", "make_params", "build_mask", "forward", "backward", "permute",
     "unpermute",
+    "RA_E4M3", "RaKvCache", "RaPagedParams", "ra_kv_write", "ra_kv_read",
+    "ra_attn_paged_workspace_size", "ra_attn_paged", "new_kv_cache", "make_kv_cache", "kv_write",
+    "kv_read", "make_paged_params", "paged_forward",
 ]
 
 RA_OK = 0
@@ -40,6 +44,7 @@ RA_ERR_WORKSPACE = -4
 RA_ERR_TIMEOUT = -5
 RA_BF16 = 0
 RA_FP32 = 1
+RA_E4M3 = 2
 RA_TILE = 128
 RA_STEP_SINKS = 1
 RA_STEP_FIRST = 2
@@ -81,6 +86,27 @@ class RaBlockMask(ctypes.Structure):
         ("B", ctypes.c_int), ("nq", ctypes.c_int),
         ("nk", ctypes.c_int), ("n_shards", ctypes.c_int), ("part_cap", ctypes.c_int),
         ("key", ctypes.c_uint64),
+    ]
+
+
+class RaKvCache(ctypes.Structure):
+    """A paged cache; made by ``make_kv_cache``, the tensors are its attributes
+    ``k_pages``, ``v_pages``, ``k_exps``, ``v_exps`` (the last two None for bf16)."""
+    _fields_ = [
+        ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int),
+        ("D", ctypes.c_int), ("dtype", ctypes.c_int), ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+    ]
+
+
+class RaPagedParams(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("Lq", ctypes.c_int), ("Hq", ctypes.c_int), ("dtype", ctypes.c_int),
+        ("scale", ctypes.c_float), ("soft_cap", ctypes.c_float), ("causal", ctypes.c_int),
+        ("max_pages", ctypes.c_int), ("prefix_pages", ctypes.c_int),
+        ("page_table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("q_len", ctypes.c_void_p),
+        ("prefix_table", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p),
+        ("sinks", ctypes.c_void_p),
     ]
 
 
@@ -129,6 +155,12 @@ def lib():
             L.ra_get_device_status.argtypes = [vp]
             L.ra_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp, vp]
             L.ra_launch_count.restype = ctypes.c_uint64
+            KC, PP = ctypes.POINTER(RaKvCache), ctypes.POINTER(RaPagedParams)
+            L.ra_kv_write.argtypes = [KC, vp, vp, ci, ci, ci, sz, sz, vp, ci, vp, vp, vp]
+            L.ra_kv_read.argtypes = [KC, vp, ci, vp, ci, ci, vp, vp, ci, vp]
+            L.ra_attn_paged_workspace_size.argtypes = [KC, PP]
+            L.ra_attn_paged_workspace_size.restype = sz
+            L.ra_attn_paged.argtypes = [KC, PP, vp, vp, vp, vp, sz, vp]
             _lib = L
     return _lib
 
@@ -286,6 +318,30 @@ def ra_selftest_wait_timeout(timeout_ns, gave_up, stream=None) -> None:
     _check(lib().ra_selftest_wait_timeout(int(timeout_ns), _ptr(gave_up), _stream(stream)))
 
 
+def ra_kv_write(cache, k, v, dtype, B, L, k_stride, v_stride, page_table, max_pages, start,
+                count=None, stream=None) -> None:
+    _check(lib().ra_kv_write(ctypes.byref(cache), _ptr(k), _ptr(v), dtype, B, L, k_stride,
+                             v_stride, _ptr(page_table), max_pages, _ptr(start), _ptr(count),
+                             _stream(stream)))
+
+
+def ra_kv_read(cache, page_table, max_pages, kv_len, B, L, k, v, dtype, stream=None) -> None:
+    _check(lib().ra_kv_read(ctypes.byref(cache), _ptr(page_table), max_pages, _ptr(kv_len), B, L,
+                            _ptr(k), _ptr(v), dtype, _stream(stream)))
+
+
+def ra_attn_paged_workspace_size(cache, params) -> int:
+    n = lib().ra_attn_paged_workspace_size(ctypes.byref(cache), ctypes.byref(params))
+    if n == 0:  # also refused by ra_attn_paged, with the code of the refusal
+        raise RaError(RA_ERR_INVALID_ARG, ra_last_error())
+    return int(n)
+
+
+def ra_attn_paged(cache, params, q, out, lse, ws, stream=None) -> None:
+    _check(lib().ra_attn_paged(ctypes.byref(cache), ctypes.byref(params), _ptr(q), _ptr(out),
+                               _ptr(lse), _ptr(ws), _wsb(ws), _stream(stream)))
+
+
 # ------------------------------------------------------------- helpers
 _DT = {torch.bfloat16: RA_BF16, torch.float32: RA_FP32}
 
@@ -356,3 +412,190 @@ def unpermute(x, n_shards, stream=None):
     B, L, rb = _rows(x)
     ra_unpermute_tokens(x, out, B, L, rb, n_shards, stream=stream)
     return out
+
+
+# ------------------------------------------------------------- paged cache
+_CACHE_DT = {torch.bfloat16: RA_BF16, torch.float8_e4m3fn: RA_E4M3}
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _ints(x, shape, name, device):
+    """int32 tensors that the kernels read: dense, on the cache's device."""
+    if x.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32, not {x.dtype}")
+    _need(tuple(x.shape) == shape, f"{name} has shape {tuple(x.shape)}, not {shape}")
+    _need(x.is_contiguous() and x.device == device,
+          f"{name} must be contiguous and on the cache's device")
+
+
+class _On:
+    """Runs a helper's allocations and launches on the tensors' device and on the caller's
+    stream, so that what is allocated here is reused in that stream's order."""
+
+    def __init__(self, device, stream):
+        self.guards = []
+        if device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            self.guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+
+    def __exit__(self, *e):
+        for g in reversed(self.guards):
+            g.__exit__(*e)
+
+
+def make_kv_cache(k, v, k_exp=None, v_exp=None) -> RaKvCache:
+    """A cache over existing tensors: k, v (n_pages, Hkv, page_size, D), bf16 or float8_e4m3fn,
+    and for the latter k_exp, v_exp (n_pages, Hkv, page_size) uint8."""
+    if k.dtype not in _CACHE_DT or v.dtype != k.dtype:
+        raise TypeError(f"a cache is bfloat16 or float8_e4m3fn, not {k.dtype} and {v.dtype}")
+    _need(k.dim() == 4 and k.shape == v.shape, "k and v must be (n_pages, Hkv, page_size, D)")
+    quantised = k.dtype != torch.bfloat16
+    _need((k_exp is not None) == quantised and (v_exp is not None) == quantised,
+          "k_exp and v_exp belong to float8_e4m3fn caches")
+    for x in (k, v, k_exp, v_exp):
+        _need(x is None or (x.is_contiguous() and x.device == k.device),
+              "cache tensors must be contiguous and on one device")
+    for x in (k_exp, v_exp):
+        if x is not None:
+            if x.dtype != torch.uint8:
+                raise TypeError(f"k_exp and v_exp must be uint8, not {x.dtype}")
+            _need(x.shape == k.shape[:3], "k_exp and v_exp must be (n_pages, Hkv, page_size)")
+    n, h, page, d = k.shape
+    c = RaKvCache(n, page, h, d, _CACHE_DT[k.dtype], _ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp))
+    c.k_pages, c.v_pages, c.k_exps, c.v_exps, c.device = k, v, k_exp, v_exp, k.device
+    return c
+
+
+def new_kv_cache(n_pages, page_size, n_kv_heads, head_dim, dtype=torch.float8_e4m3fn,
+                 device=None) -> RaKvCache:
+    """An empty cache of ``n_pages`` pages (see ``make_kv_cache``)."""
+    device = device or "cuda"
+    shape = (n_pages, n_kv_heads, page_size, head_dim)
+    if dtype not in _CACHE_DT:
+        raise TypeError(f"a cache is bfloat16 or float8_e4m3fn, not {dtype}")
+    k, v = (torch.zeros(shape, dtype=torch.uint8 if dtype != torch.bfloat16 else dtype,
+                        device=device).view(dtype) for _ in range(2))
+    exps = [None, None] if dtype == torch.bfloat16 else [
+        torch.zeros(shape[:3], dtype=torch.uint8, device=device) for _ in range(2)]
+    return make_kv_cache(k, v, *exps)
+
+
+def _token_stride(x, cache, name):
+    _need(x.dim() == 4 and tuple(x.shape[2:]) == (cache.Hkv, cache.D),
+          f"{name} must be (B, L, {cache.Hkv}, {cache.D})")
+    _need(x.device == cache.device, f"{name} must be on the cache's device")
+    B, L = x.shape[:2]
+    row = cache.Hkv * cache.D
+    st = x.stride(1) if L > 1 else (x.stride(0) if B > 1 else row)
+    _need(x.stride(3) == 1 and (cache.Hkv == 1 or x.stride(2) == cache.D)
+          and (B == 1 or x.stride(0) == L * st) and st >= row,
+          f"{name}: a token's heads must be contiguous, and tokens and batches evenly spaced")
+    return st
+
+
+def kv_write(cache, k, v, page_table, start, count=None, stream=None) -> None:
+    """Appends k, v (B, L, Hkv, D), bf16 or fp32, at positions start[b] + i of the sequences whose
+    pages are in page_table (B, max_pages); of sequence b the first count[b] tokens (None: all).
+    k and v may be slices along the head axis of a wider tensor."""
+    if k.dtype not in _DT or v.dtype != k.dtype:
+        raise TypeError(f"k and v must both be bfloat16 or float32, not {k.dtype} and {v.dtype}")
+    _need(k.shape == v.shape, "k and v must have the same shape")
+    ks, vs = _token_stride(k, cache, "k"), _token_stride(v, cache, "v")
+    B, L = k.shape[:2]
+    if B == 0 or L == 0:
+        return
+    _ints(page_table, (B, page_table.shape[-1]), "page_table", cache.device)
+    _ints(start, (B,), "start", cache.device)
+    if count is not None:
+        _ints(count, (B,), "count", cache.device)
+    with _On(cache.device, stream):
+        ra_kv_write(cache, k, v, _DT[k.dtype], B, L, ks, vs, page_table, page_table.shape[1], start,
+                    count)
+
+
+def kv_read(cache, page_table, kv_len, L, dtype=torch.bfloat16, stream=None):
+    """k, v (B, L, Hkv, D) of the sequences' cached tokens; rows behind kv_len[b] are 0."""
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype}")
+    B = page_table.shape[0]
+    _ints(page_table, (B, page_table.shape[-1]), "page_table", cache.device)
+    _ints(kv_len, (B,), "kv_len", cache.device)
+    with _On(cache.device, stream):
+        k, v = (torch.empty((B, L, cache.Hkv, cache.D), dtype=dtype, device=cache.device)
+                for _ in range(2))
+        if B and L:
+            ra_kv_read(cache, page_table, page_table.shape[1], kv_len, B, L, k, v, _DT[dtype])
+    return k, v
+
+
+def make_paged_params(cache, q, page_table, kv_len, *, scale, causal=True, soft_cap=0.0, q_len=None,
+                      sinks=None, prefix_table=None, prefix_len=None) -> RaPagedParams:
+    """Params for queries like q (B, Lq, Hq, D) over ``cache``; they hold the tensors, which may be
+    changed in place between calls (a page added, a length grown), and serve every layer whose
+    cache has the same sizes.  prefix_len: an int32 tensor of one element."""
+    if q.dtype not in _DT:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    _need(q.dim() == 4 and q.shape[3] == cache.D, f"q must be (B, Lq, Hq, {cache.D})")
+    B, Lq, Hq, _ = q.shape
+    dev = cache.device
+    _ints(page_table, (B, page_table.shape[-1]), "page_table", dev)
+    _ints(kv_len, (B,), "kv_len", dev)
+    if q_len is not None:
+        _ints(q_len, (B,), "q_len", dev)
+    _need((prefix_table is None) == (prefix_len is None),
+          "prefix_table and prefix_len must come together")
+    if prefix_table is not None:
+        _ints(prefix_table, (prefix_table.shape[-1],), "prefix_table", dev)
+        _ints(prefix_len, (1,), "prefix_len", dev)
+    if sinks is not None:
+        if sinks.dtype != torch.float32:
+            raise TypeError(f"sinks must be float32, not {sinks.dtype}")
+        _need(tuple(sinks.shape) == (Hq,) and sinks.is_contiguous() and sinks.device == dev,
+              "sinks must be (Hq,), contiguous and on the cache's device")
+    p = RaPagedParams(B, Lq, Hq, _DT[q.dtype], float(scale), float(soft_cap or 0.0),
+                      int(bool(causal)), page_table.shape[1],
+                      0 if prefix_table is None else prefix_table.shape[0], _ptr(page_table),
+                      _ptr(kv_len), _ptr(q_len), _ptr(prefix_table), _ptr(prefix_len), _ptr(sinks))
+    p._keep = (page_table, kv_len, q_len, prefix_table, prefix_len, sinks)
+    p._like = (tuple(q.shape), q.dtype)
+    p._ws = ra_attn_paged_workspace_size(cache, p) if B and Lq else 0
+    p._cache = (cache.n_pages, cache.page_size, cache.Hkv, cache.D, cache.dtype)
+    return p
+
+
+def paged_forward(params, q, cache, out=None, lse=None, ws=None, stream=None):
+    """Attention of q (B, Lq, Hq, D) over the cached tokens -> (out like q, lse (B, Hq, Lq) fp32).
+    Given ``out`` / ``lse`` are written in place (rows behind q_len stay as they are); ``ws``: a
+    workspace to use instead of a new one, uint8, of ra_attn_paged_workspace_size elements."""
+    _need((tuple(q.shape), q.dtype) == params._like and q.is_contiguous(),
+          "q must be contiguous, of the shape and dtype the params were made for")
+    _need((cache.n_pages, cache.page_size, cache.Hkv, cache.D, cache.dtype) == params._cache,
+          "the params were made for a cache of other sizes")
+    _need(q.device == cache.device, "q must be on the cache's device")
+    B, Lq, Hq, _ = q.shape
+    if out is not None:
+        _need(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()
+              and out.device == q.device, "out must be like q")
+    if lse is not None:
+        _need(tuple(lse.shape) == (B, Hq, Lq) and lse.dtype == torch.float32 and lse.is_contiguous()
+              and lse.device == q.device, "lse must be (B, Hq, Lq) fp32")
+    with _On(q.device, stream):
+        out = torch.empty_like(q) if out is None else out
+        lse = (torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device) if lse is None
+               else lse)
+        if B and Lq:
+            if ws is None:
+                ws = torch.empty(params._ws, dtype=torch.uint8, device=q.device)
+            ra_attn_paged(cache, params, q, out, lse, ws)
+    return out, lse

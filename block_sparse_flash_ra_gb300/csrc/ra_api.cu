@@ -329,6 +329,21 @@ int encode_rows(CUtensorMap *map, const void *base, int B, int L, int H, int D, 
 } // namespace
 
 int set_last_error(int code, const char *msg) { return fail(code, "%s", msg); }
+int set_cuda_error(cudaError_t e, const char *what) { return cuda_fail(e, what); }
+
+int device_info(DeviceInfo *out)
+{
+    DevCache *dc = nullptr;
+    const int rc = device_cache(&dc);
+    if (rc) return rc;
+    out->index = (int)(dc - g_dev);
+    out->num_sms = dc->num_sms;
+    out->status = dc->status;
+    out->timeout_ns = g_timeout_ns.load();
+    return RA_OK;
+}
+
+void count_launches(int n) { count(n); }
 
 } // namespace ra
 
@@ -914,6 +929,8 @@ RA_API int ra_get_device_status(ra_stream_t stream)
     e = cudaMemcpy(dc->status, &zero, sizeof(int), cudaMemcpyHostToDevice);
     if (e != cudaSuccess) return cuda_fail(e, "status reset");
     if (v == RA_STATUS_TIMEOUT) return fail(RA_ERR_TIMEOUT, "a kernel wait timed out");
+    if (v == RA_STATUS_BAD_PAGE)
+        return fail(RA_ERR_INVALID_ARG, "a paged call met a page, position or length out of range");
     return RA_OK;
 }
 

@@ -11,6 +11,7 @@ namespace ra {
 
 constexpr int kTile = RA_TILE;            // canonical tile edge (tokens)
 constexpr int RA_STATUS_TIMEOUT = 1;      // device status word value on a timed-out wait
+constexpr int RA_STATUS_BAD_PAGE = 2;     // a page, position or length out of range (paged calls)
 
 // Everything a kernel needs to know about the problem, in device-friendly form.
 struct Problem {
@@ -145,5 +146,17 @@ int bwd_all_validate(const ra_attn_params *p, const void *q, const void *k, cons
 
 // Records `msg` as this thread's last error message and returns `code`.
 int set_last_error(int code, const char *msg);
+int set_cuda_error(cudaError_t e, const char *what);
+
+// What the entry points outside ra_api.cu share with it: the current device's
+// properties (checked to be a GPU this library is built for), the limit of an
+// in-kernel wait and the launch counter.
+struct DeviceInfo {
+    int index, num_sms;
+    int *status;
+    uint64_t timeout_ns;
+};
+int device_info(DeviceInfo *out);
+void count_launches(int n);
 
 } // namespace ra

@@ -1,0 +1,218 @@
+// ra_paged.cuh -- device parts shared by the paged attention kernels: the
+// spread of the work over CTAs, the numbering of partial results, and the
+// cached rows' scales.
+//
+// Work.  A source's keys are cut into tiles of `tile` tokens; an item is a
+// tile of one (sequence, row block, kv head).  All items lie on one line --
+// sequences in order, in each its row blocks, in each its kv heads, in each
+// its tiles -- and CTA c of C takes the c-th share of ceil(N / C) of them.
+// Shares are equal whatever the lengths are, and lengths stay on the device:
+// every CTA adds up the lengths of the batch itself (B integers out of L2)
+// to find where its share begins.  A segment is the run of items of one
+// (sequence, row block, kv head).
+//
+// Partial results.  CTA c's part of segment s goes to slot c + s: along the
+// line both numbers only grow, and each new (CTA, segment) pair raises at
+// least one of them, so no two pairs share a slot, and C + S slots are
+// enough.  The join finds a segment's slots from the same sums.
+#pragma once
+
+#include "ra_device.cuh"
+#include "ra_paged.h"
+
+namespace ra {
+
+// 2^(b - 127) of a cached row's scale byte; 255 marks a row without a value.
+// (0, which ra_kv_write does not store, is a subnormal power of two.)
+__device__ __forceinline__ float exp_byte_scale(uint32_t b)
+{
+    return __uint_as_float(b == 255u ? 0x7fc00000u : b == 0u ? 0x00400000u : b << 23);
+}
+
+// Two e4m3 codes (low and high byte of a 16-bit word) as two halves.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+
+__device__ __forceinline__ int paged_q_len(const PagedProblem &p, int b)
+{
+    if (!p.q_len) return p.Lq;
+    return min(max(p.q_len[b], 0), p.Lq);
+}
+
+__device__ __forceinline__ int paged_kv_len(const PagedProblem &p, int b)
+{
+    const long long cap = (long long)p.max_pages << p.c.page_shift;
+    return (int)min((long long)max(p.kv_len[b], 0), cap);
+}
+
+__device__ __forceinline__ int paged_prefix_len(const PagedProblem &p)
+{
+    const long long cap = (long long)p.prefix_pages << p.c.page_shift;
+    return (int)min((long long)max(*p.prefix_len, 0), cap);
+}
+
+// Tiles of one segment of sequence b (own keys; 0 when it has no queries).
+__device__ __forceinline__ int own_tiles(const PagedProblem &p, const PagedPart &part, int b)
+{
+    if (paged_q_len(p, b) == 0) return 0;
+    return (paged_kv_len(p, b) + part.tile - 1) / part.tile;
+}
+
+// Sum of own_tiles over sequences [0, b_end), by one converged warp.
+__device__ __forceinline__ long long own_tiles_before(const PagedProblem &p, const PagedPart &part,
+                                                      int b_end)
+{
+    long long n = 0;
+    for (int b = threadIdx.x & 31; b < b_end; b += 32) n += own_tiles(p, part, b);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n;
+}
+
+// A cursor on the line of items, kept by every thread of a CTA alike.
+struct PagedCursor {
+    long long at, end; // the CTA's share
+    int b, rb, h;      // the segment that `at` lies in
+    int t0, tiles;     // its next tile, and its tiles
+    long long seg;     // its number
+};
+
+// Places the cursor at CTA `cta`'s share.  Called by one converged warp (all
+// lanes get the result); false when the share is empty.
+__device__ __forceinline__ bool cursor_begin(const PagedProblem &p, const PagedPart &part, int cta,
+                                             PagedCursor &c)
+{
+    const int per_seq = part.n_rb * p.c.Hkv; // segments of one sequence
+    const int lane = threadIdx.x & 31;
+    const int prefix_tiles =
+        part.prefix ? (paged_prefix_len(p) + part.tile - 1) / part.tile : 0;
+    const long long total =
+        per_seq * (part.prefix ? (long long)prefix_tiles : own_tiles_before(p, part, p.B));
+    const long long share = (total + part.ctas - 1) / part.ctas;
+    c.at = share * cta;
+    c.end = c.at + share < total ? c.at + share : total;
+    if (c.at >= c.end) return false;
+    long long before = 0;
+    c.b = 0;
+    c.tiles = prefix_tiles;
+    if (!part.prefix) {
+        // 32 sequences at a time: the first whose running total passes `at`
+        for (int b0 = 0;; b0 += 32) {
+            const int b = b0 + lane;
+            const int n = b < p.B ? own_tiles(p, part, b) : 0;
+            long long run = (long long)n * per_seq;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long x = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += x;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, before + run > c.at);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                c.b = b0 + l;
+                c.tiles = __shfl_sync(0xffffffffu, n, l);
+                before += __shfl_sync(0xffffffffu, run, l) - (long long)c.tiles * per_seq;
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, run, 31);
+        }
+    }
+    const int in_seq = (int)((c.at - before) / c.tiles);
+    c.t0 = (int)(c.at - before - (long long)in_seq * c.tiles);
+    c.rb = in_seq / p.c.Hkv;
+    c.h = in_seq - c.rb * p.c.Hkv;
+    c.seg = (long long)c.b * per_seq + in_seq;
+    return true;
+}
+
+// Tiles of the present segment that fall into the share.
+__device__ __forceinline__ int cursor_take(const PagedCursor &c)
+{
+    const long long left = c.end - c.at;
+    const int n = c.tiles - c.t0;
+    return n < left ? n : (int)left;
+}
+
+// Moves past `n` tiles of the present segment (all that cursor_take gave);
+// false at the share's end.
+__device__ __forceinline__ bool cursor_next(const PagedProblem &p, const PagedPart &part,
+                                            PagedCursor &c, int n)
+{
+    c.at += n;
+    if (c.at >= c.end) return false;
+    c.t0 = 0;
+    ++c.seg;
+    if (++c.h == p.c.Hkv) {
+        c.h = 0;
+        if (++c.rb == part.n_rb) {
+            c.rb = 0;
+            do { // a share that goes on has a sequence with tiles ahead
+                ++c.b;
+                c.tiles = own_tiles(p, part, c.b);
+                if (!c.tiles) c.seg += (long long)part.n_rb * p.c.Hkv;
+            } while (!c.tiles);
+        }
+    }
+    return true;
+}
+
+// Where query row `row` of an item's row block lies, and which of the
+// source's keys it sees: [0, limit), 0 for rows that are not computed.
+struct PagedRow {
+    int b, i, g, limit;
+};
+
+__device__ __forceinline__ PagedRow paged_row(const PagedProblem &p, const PagedPart &part,
+                                              const PagedCursor &c, int row)
+{
+    PagedRow r;
+    const int n = c.rb * part.row_block + row;
+    r.b = part.prefix ? n / (p.Lq * p.G) : c.b;
+    const int in_seq = part.prefix ? n - r.b * (p.Lq * p.G) : n;
+    r.i = in_seq / p.G;
+    r.g = in_seq - r.i * p.G;
+    r.limit = 0;
+    if (n < part.rows) {
+        const int qn = paged_q_len(p, r.b);
+        if (r.i < qn) {
+            if (part.prefix) {
+                r.limit = paged_prefix_len(p);
+            } else {
+                const int len = paged_kv_len(p, r.b);
+                r.limit = p.causal ? max(len - qn + r.i + 1, 0) : len;
+            }
+        }
+    }
+    return r;
+}
+
+// Page number of token position t of the item's source, or -1.
+__device__ __forceinline__ int paged_page(const PagedProblem &p, const PagedPart &part, int b, int t)
+{
+    const int n = t >> p.c.page_shift;
+    const int page =
+        part.prefix ? p.prefix_table[n] : p.page_table[(size_t)b * p.max_pages + n];
+    if (page >= 0 && page < p.c.n_pages) return page;
+    atomicMax(p.status, RA_STATUS_BAD_PAGE);
+    return -1;
+}
+
+// The lengths that had to be clamped are reported once per launch.
+__device__ __forceinline__ void report_lengths(const PagedProblem &p, const PagedPart &part)
+{
+    if (blockIdx.x != 0 || threadIdx.x >= 32) return;
+    bool bad = false;
+    if (part.prefix) {
+        bad = paged_prefix_len(p) != *p.prefix_len;
+    } else {
+        for (int b = threadIdx.x; b < p.B; b += 32)
+            bad |= paged_kv_len(p, b) != p.kv_len[b] || (p.q_len && paged_q_len(p, b) != p.q_len[b]);
+    }
+    if (bad) atomicMax(p.status, RA_STATUS_BAD_PAGE);
+}
+
+} // namespace ra

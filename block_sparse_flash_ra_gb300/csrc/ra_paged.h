@@ -1,0 +1,67 @@
+// ra_paged.h -- declarations shared by the paged entry points and kernels.
+#pragma once
+
+#include "ra_internal.h"
+
+namespace ra {
+
+// A paged cache in device-friendly form; page sizes are powers of two.
+struct PagedCache {
+    const void *k, *v;
+    const uint8_t *k_exp, *v_exp; // e4m3 only
+    int n_pages, page, page_shift, Hkv, D;
+};
+
+// One cached-attention problem.  Query rows of one kv head are numbered
+// i * G + g inside a sequence, and (b * Lq + i) * G + g over the batch.
+struct PagedProblem {
+    PagedCache c;
+    int B, Lq, Hq, G;
+    float scale, soft_cap; // soft_cap 0 = none
+    int causal;
+    const int32_t *page_table;
+    int max_pages;
+    const int32_t *kv_len, *q_len;
+    const int32_t *prefix_table;
+    int prefix_pages;
+    const int32_t *prefix_len;
+    const float *sinks;
+    const void *q;
+    void *out;
+    float *lse;
+    int *status;
+    uint64_t timeout_ns;
+};
+
+// How one launch spreads a source of keys (the sequences' own pages, or the
+// shared prefix) over its CTAs; see ra_paged.cuh.
+struct PagedPart {
+    int prefix;    // 1: the shared prefix, every sequence's rows together
+    int rows;      // query rows per kv head of one sequence, or of the batch
+    int row_block; // rows of one work item
+    int n_rb;      // ceil(rows / row_block)
+    int tile;      // keys of one tile
+    int ctas;
+    int slot_rows; // rows that one partial result holds
+    float *o;      // (slots, slot_rows, D) unnormalised outputs
+    float *ml;     // (slots, slot_rows, 2) row maximum (base-2 logits) and sum
+};
+
+cudaError_t launch_kv_write(const PagedCache &c, int cache_dtype, const void *k, const void *v,
+                            int dtype, int B, int L, size_t k_stride, size_t v_stride,
+                            const int32_t *page_table, int max_pages, const int32_t *start,
+                            const int32_t *count, int *status, int num_sms, cudaStream_t s);
+cudaError_t launch_kv_read(const PagedCache &c, int cache_dtype, const int32_t *page_table,
+                           int max_pages, const int32_t *kv_len, int B, int L, void *k, void *v,
+                           int dtype, int *status, int num_sms, cudaStream_t s);
+
+// fp32 arithmetic throughout: the path of fp32 queries
+constexpr int kPagedF32Rows = 8, kPagedF32Tile = 32;
+cudaError_t launch_paged_f32(const PagedProblem &p, const PagedPart &part, int cache_dtype,
+                             int dtype, bool direct, cudaStream_t s);
+
+// joins the partial results of both sources (n_parts of them) into out, lse
+cudaError_t launch_paged_join(const PagedProblem &p, const PagedPart *parts, int n_parts, int dtype,
+                              cudaStream_t s);
+
+} // namespace ra

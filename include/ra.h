@@ -74,9 +74,11 @@ enum {
     RA_ERR_CUDA = -3,        /* a CUDA runtime call failed */
     RA_ERR_WORKSPACE = -4,   /* workspace missing or smaller than required */
     RA_ERR_TIMEOUT = -5      /* a kernel's bounded wait ran out (device status) */
+    /* the device status also reports RA_ERR_INVALID_ARG: a page number, a
+     * position or a length in device memory was out of range (paged calls) */
 };
 
-enum { RA_BF16 = 0, RA_FP32 = 1 };
+enum { RA_BF16 = 0, RA_FP32 = 1, RA_E4M3 = 2 /* paged caches only */ };
 enum { RA_TILE_EMPTY = 0, RA_TILE_PARTIAL = 1, RA_TILE_FULL = 2 };
 #define RA_TILE 128
 
@@ -446,8 +448,138 @@ RA_API int ra_unpermute_tokens(const void *in, void *out, int B, int L, size_t r
                                int n_shards, ra_stream_t stream);
 
 /*
+ * The paged key/value cache: serving's counterpart of the dense k, v of
+ * ra_attn_fwd.  A page holds page_size consecutive tokens of one sequence; a
+ * sequence's pages are listed in its row of a page table, and the token at
+ * position t is token t % page_size of page page_table[b][t / page_size].
+ *   n_pages, page_size  pages of the cache; 16, 32, 64 or 128 tokens each
+ *   Hkv, D              kv heads, head size in {64, 128}
+ *   dtype               RA_BF16: the values; RA_E4M3: 8-bit codes with a
+ *                       power-of-two scale per row (one token of one kv head)
+ *   k, v                (n_pages, Hkv, page_size, D) bf16 or e4m3, 16-byte
+ *                       aligned: the tokens of one head of a page lie
+ *                       together, so that one tile load fetches them
+ *   k_exp, v_exp        RA_E4M3: (n_pages, Hkv, page_size) uint8, 16-byte
+ *                       aligned; RA_BF16: NULL
+ * An e4m3 row stands for code * 2^(exp - 127), where e = exp - 127 is the
+ * smallest exponent >= -110 with max|row| <= 448 * 2^e: scaling by a power of
+ * two is exact, so the one rounding is that of the code (to nearest even,
+ * 2^-4 relative above 2^(e-6), 2^(e-10) absolute below).  A row holding an
+ * infinity or a NaN gets exp = 255 and codes 0, and stands for NaN.
+ */
+typedef struct {
+    int n_pages, page_size, Hkv, D;
+    int dtype;
+    void *k, *v;
+    uint8_t *k_exp, *v_exp;
+} ra_kv_cache;
+
+/*
+ * Appends tokens to the cache, quantising them on the way (RA_E4M3) or
+ * rounding them to bf16.
+ *   k, v        (B, L, Hkv, D) in `dtype` (RA_BF16 or RA_FP32), the rows of a
+ *               token contiguous; k_stride / v_stride: elements from one
+ *               token to the next (>= Hkv * D; a batch is L tokens), so that
+ *               k and v may be slices of a fused projection's output.
+ *               16-byte aligned, the strides in bytes multiples of 16.
+ *   page_table  (B, max_pages) int32
+ *   start       (B) int32: sequence b's token i goes to position start[b] + i
+ *   count       (B) int32, or NULL for L: tokens i >= count[b] are left out
+ *               (count is clamped to [0, L])
+ * A token whose position lies outside [0, max_pages * page_size), or whose
+ * page is outside [0, n_pages), is skipped and reported by
+ * ra_get_device_status (RA_ERR_INVALID_ARG).  Nothing else of the cache is
+ * touched.  If two tokens name the same place, either may stay.
+ * Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED, RA_ERR_CUDA.
+ */
+RA_API int ra_kv_write(const ra_kv_cache *cache, const void *k, const void *v, int dtype, int B,
+                       int L, size_t k_stride, size_t v_stride, const int32_t *page_table,
+                       int max_pages, const int32_t *start, const int32_t *count,
+                       ra_stream_t stream);
+
+/*
+ * Gathers sequences out of the cache into dense tensors, as ra_attn_fwd and
+ * ra_attn_bwd take them.
+ *   k, v        (B, L, Hkv, D) in `dtype` (RA_BF16 or RA_FP32), 16-byte
+ *               aligned, contiguous: row j of sequence b is the value of its
+ *               cached token j for j < kv_len[b], and 0 behind it (a cached
+ *               value beyond the type's range becomes an infinity)
+ *   page_table  (B, max_pages) int32;  kv_len (B) int32
+ * kv_len is clamped to [0, L]; a token whose page is missing from the table or
+ * out of range reads as 0 and is reported by ra_get_device_status.
+ * Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED, RA_ERR_CUDA.
+ */
+RA_API int ra_kv_read(const ra_kv_cache *cache, const int32_t *page_table, int max_pages,
+                      const int32_t *kv_len, int B, int L, void *k, void *v, int dtype,
+                      ra_stream_t stream);
+
+/*
+ * Attention of a batch's last tokens over a paged cache, with an optional
+ * prefix that every sequence shares.
+ *   B, Lq, Hq     sequences, query tokens per sequence (1 for a decoding
+ *                 step), query heads (a multiple of the cache's Hkv)
+ *   dtype         RA_BF16 or RA_FP32: element type of q and out
+ *   scale, soft_cap, sinks   as in ra_attn_params
+ *   causal        1: the queries are the sequence's last tokens, and query i
+ *                 sees own positions up to kv_len - q_len + i; 0: all of them
+ *   page_table    (B, max_pages) int32: the sequences' own pages
+ *   kv_len        (B) int32: cached own tokens (those of the queries among
+ *                 them), clamped to [0, max_pages * page_size]
+ *   q_len         (B) int32, or NULL for Lq: valid query rows of each
+ *                 sequence, clamped to [0, Lq]; rows behind them are neither
+ *                 computed nor written
+ *   prefix_table  (prefix_pages) int32 pages of the shared prefix, or NULL
+ *                 with prefix_pages == 0
+ *   prefix_len    (1) int32: tokens of the prefix, clamped to
+ *                 [0, prefix_pages * page_size].  The prefix precedes every
+ *                 sequence's own tokens; every query sees all of it.
+ * Every length and table is read on the device when the kernels run, so a
+ * captured graph serves sequences that grow.  A page number outside
+ * [0, n_pages) or a length that had to be clamped is reported by
+ * ra_get_device_status (RA_ERR_INVALID_ARG); the keys of such a page read as 0.
+ */
+typedef struct {
+    int B, Lq, Hq;
+    int dtype;
+    float scale, soft_cap;
+    int causal;
+    int max_pages, prefix_pages;
+    const int32_t *page_table;
+    const int32_t *kv_len;
+    const int32_t *q_len;
+    const int32_t *prefix_table;
+    const int32_t *prefix_len;
+    const float *sinks;
+} ra_paged_params;
+
+/* Workspace bytes of ra_attn_paged (0 if the arguments are invalid;
+ * ra_last_error says why): the partial results that several CTAs give for
+ * one query row.  It depends on the sizes only, not on the lengths. */
+RA_API size_t ra_attn_paged_workspace_size(const ra_kv_cache *cache, const ra_paged_params *p);
+
+/*
+ * out and lse of the formula at the top of this file, over the sequence's own
+ * cached tokens behind the shared prefix.
+ *   q, out  (B, Lq, Hq, D) in p->dtype;  lse (B, Hq, Lq) fp32, natural log
+ *           (-inf, with out = 0, for a row with nothing visible and no sink)
+ *   ws      ra_attn_paged_workspace_size bytes, 256-byte aligned; its
+ *           contents need not survive the call.  Calls that may overlap in
+ *           time (other streams, graphs replayed at once) need one each.
+ * Keys and values behind a sequence's length are never used, whatever the
+ * memory holds; inside it, a value row that only some of a sequence's
+ * queries see has to be finite.
+ * The prefix is read once for the whole batch.  Results do not depend on how
+ * the work was timed: partial results are joined in a fixed order.
+ * Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED, RA_ERR_WORKSPACE, RA_ERR_CUDA.
+ */
+RA_API int ra_attn_paged(const ra_kv_cache *cache, const ra_paged_params *p, const void *q,
+                         void *out, float *lse, void *ws, size_t ws_bytes, ra_stream_t stream);
+
+/*
  * Synchronises `stream`, then returns and clears the current device's status
- * word: RA_OK, or RA_ERR_TIMEOUT if a kernel gave up a bounded wait.
+ * word: RA_OK, RA_ERR_TIMEOUT if a kernel gave up a bounded wait, or
+ * RA_ERR_INVALID_ARG if a paged call met a page, position or length out of
+ * range.
  * The library caches, per device, the device address of this word and the
  * kernels' attributes on first use; resetting the device (cudaDeviceReset)
  * after the library's first call on it is not supported.
