@@ -16,12 +16,6 @@ namespace {
 
 constexpr int kRows = kPagedF32Rows, kKeys = kPagedF32Tile, kThreads = 128;
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T x)
-{
-    return (float)x;
-}
-
 // A tile of keys or values, fp32, rows of D + 4 floats.
 template <int D, bool FP8>
 __device__ __forceinline__ void fill_tile(float *dst, const void *base, const uint8_t *exps,
@@ -33,8 +27,8 @@ __device__ __forceinline__ void fill_tile(float *dst, const void *base, const ui
         const int j = e / PER, x = e % PER;
         float r[8] = {};
         if (t + j < len) {
-            const int page = paged_page(p, part, b, t + j);
-            if (page >= 0) {
+            const int page = page_entry(p, part, b, t + j);
+            if (page_valid(p, page)) {
                 const size_t row =
                     (((size_t)page * p.c.Hkv + h) << p.c.page_shift) + ((t + j) & (p.c.page - 1));
                 if (FP8) {
@@ -67,7 +61,7 @@ __device__ __forceinline__ void fill_tile(float *dst, const void *base, const ui
     }
 }
 
-template <int D, bool FP8, typename T>
+template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads)
     paged_f32_kernel(PagedProblem p, PagedPart part, bool direct)
 {
@@ -80,7 +74,7 @@ __global__ void __launch_bounds__(kThreads)
     float *k_s = reinterpret_cast<float *>(k_s4), *v_s = reinterpret_cast<float *>(v_s4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = threadIdx.x % D, row0 = threadIdx.x / D * OR;
-    const T *q = static_cast<const T *>(p.q);
+    const float *q = static_cast<const float *>(p.q);
     report_lengths(p, part);
     PagedCursor c;
     if (!cursor_begin(p, part, blockIdx.x, c)) return;
@@ -90,7 +84,7 @@ __global__ void __launch_bounds__(kThreads)
         __syncthreads(); // the last segment's shared arrays have been read
         for (int e = threadIdx.x; e < kRows * D; e += kThreads) {
             const PagedRow r = paged_row(p, part, c, e / D);
-            q_s[e] = r.limit > 0 ? to_f32(q[(((size_t)r.b * p.Lq + r.i) * p.Hq + c.h * p.G + r.g) * D + e % D])
+            q_s[e] = r.limit > 0 ? q[(((size_t)r.b * p.Lq + r.i) * p.Hq + c.h * p.G + r.g) * D + e % D]
                                  : 0.f;
         }
         // warp w owns the softmax of rows 2w and 2w + 1, lane = key
@@ -163,7 +157,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
             for (int r = 0; r < OR; ++r) {
                 const PagedRow x = paged_row(p, part, c, row0 + r);
-                if (c.rb * kRows + row0 + r >= part.rows || x.i >= paged_q_len(p, x.b)) continue;
+                if (!x.counts) continue;
                 float mr = m_s[row0 + r], lr = l_s[row0 + r], f = 1.f;
                 const int hq = c.h * p.G + x.g;
                 if (p.sinks) {
@@ -173,7 +167,7 @@ __global__ void __launch_bounds__(kThreads)
                     mr = top;
                 }
                 const float val = lr == 0.f ? 0.f : o[r] * f / lr;
-                static_cast<T *>(p.out)[(((size_t)x.b * p.Lq + x.i) * p.Hq + hq) * D + col] = (T)val;
+                static_cast<float *>(p.out)[(((size_t)x.b * p.Lq + x.i) * p.Hq + hq) * D + col] = val;
                 if (col == 0)
                     p.lse[((size_t)x.b * p.Hq + hq) * p.Lq + x.i] = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * kLn2;
             }
@@ -195,23 +189,15 @@ __global__ void __launch_bounds__(kThreads)
 
 } // namespace
 
-cudaError_t launch_paged_f32(const PagedProblem &p, const PagedPart &part, int cache_dtype, int dtype,
-                             bool direct, cudaStream_t s)
+cudaError_t launch_paged_f32(const PagedProblem &p, const PagedPart &part, int cache_dtype, bool direct,
+                             cudaStream_t s)
 {
     auto go = [&](auto kern) {
         kern<<<part.ctas, kThreads, 0, s>>>(p, part, direct);
         return cudaGetLastError();
     };
-    if (dtype == RA_BF16) {
-        if (cache_dtype == RA_E4M3)
-            return p.c.D == 64 ? go(paged_f32_kernel<64, true, __nv_bfloat16>)
-                               : go(paged_f32_kernel<128, true, __nv_bfloat16>);
-        return p.c.D == 64 ? go(paged_f32_kernel<64, false, __nv_bfloat16>)
-                           : go(paged_f32_kernel<128, false, __nv_bfloat16>);
-    }
-    if (cache_dtype == RA_E4M3)
-        return p.c.D == 64 ? go(paged_f32_kernel<64, true, float>) : go(paged_f32_kernel<128, true, float>);
-    return p.c.D == 64 ? go(paged_f32_kernel<64, false, float>) : go(paged_f32_kernel<128, false, float>);
+    if (cache_dtype == RA_E4M3) return p.c.D == 64 ? go(paged_f32_kernel<64, true>) : go(paged_f32_kernel<128, true>);
+    return p.c.D == 64 ? go(paged_f32_kernel<64, false>) : go(paged_f32_kernel<128, false>);
 }
 
 } // namespace ra

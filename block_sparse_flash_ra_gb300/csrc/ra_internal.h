@@ -159,4 +159,9 @@ struct DeviceInfo {
 int device_info(DeviceInfo *out);
 void count_launches(int n);
 
+// A 3-D TMA map (a CUtensorMap) over a paged cache: (D, page, n_pages * Hkv)
+// elements of `dtype`, boxes of `rows` tokens by 128 bytes (or D, if that is
+// less), swizzled over the box's width.
+int encode_paged(void *map, const ra_kv_cache *c, const void *base, int rows);
+
 } // namespace ra

@@ -164,6 +164,7 @@ __device__ __forceinline__ bool cursor_next(const PagedProblem &p, const PagedPa
 // source's keys it sees: [0, limit), 0 for rows that are not computed.
 struct PagedRow {
     int b, i, g, limit;
+    bool counts; // a row that is computed (it may see nothing all the same)
 };
 
 __device__ __forceinline__ PagedRow paged_row(const PagedProblem &p, const PagedPart &part,
@@ -176,9 +177,11 @@ __device__ __forceinline__ PagedRow paged_row(const PagedProblem &p, const Paged
     r.i = in_seq / p.G;
     r.g = in_seq - r.i * p.G;
     r.limit = 0;
+    r.counts = false;
     if (n < part.rows) {
         const int qn = paged_q_len(p, r.b);
         if (r.i < qn) {
+            r.counts = true;
             if (part.prefix) {
                 r.limit = paged_prefix_len(p);
             } else {
@@ -190,15 +193,19 @@ __device__ __forceinline__ PagedRow paged_row(const PagedProblem &p, const Paged
     return r;
 }
 
-// Page number of token position t of the item's source, or -1.
-__device__ __forceinline__ int paged_page(const PagedProblem &p, const PagedPart &part, int b, int t)
+// The table's entry for token position t of the item's source.
+__device__ __forceinline__ int page_entry(const PagedProblem &p, const PagedPart &part, int b, int t)
 {
     const int n = t >> p.c.page_shift;
-    const int page =
-        part.prefix ? p.prefix_table[n] : p.page_table[(size_t)b * p.max_pages + n];
-    if (page >= 0 && page < p.c.n_pages) return page;
+    return part.prefix ? p.prefix_table[n] : p.page_table[(size_t)b * p.max_pages + n];
+}
+
+// Whether an entry names a page of the cache; if not, that is reported.
+__device__ __forceinline__ bool page_valid(const PagedProblem &p, int page)
+{
+    if (page >= 0 && page < p.c.n_pages) return true;
     atomicMax(p.status, RA_STATUS_BAD_PAGE);
-    return -1;
+    return false;
 }
 
 // The lengths that had to be clamped are reported once per launch.

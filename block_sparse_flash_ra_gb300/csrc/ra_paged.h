@@ -31,6 +31,7 @@ struct PagedProblem {
     float *lse;
     int *status;
     uint64_t timeout_ns;
+    int device;
 };
 
 // How one launch spreads a source of keys (the sequences' own pages, or the
@@ -58,7 +59,15 @@ cudaError_t launch_kv_read(const PagedCache &c, int cache_dtype, const int32_t *
 // fp32 arithmetic throughout: the path of fp32 queries
 constexpr int kPagedF32Rows = 8, kPagedF32Tile = 32;
 cudaError_t launch_paged_f32(const PagedProblem &p, const PagedPart &part, int cache_dtype,
-                             int dtype, bool direct, cudaStream_t s);
+                             bool direct, cudaStream_t s);
+
+// bf16 queries, row_block 8 or 16: tensor cores fed from registers.  Keys of a
+// tile, and token rows of one TMA box, by head size, cache type and page size;
+// tm_k, tm_v: maps of encode_paged over the cache with that box.
+int paged_few_tile(int D, int cache_dtype);
+int paged_few_box(int D, int cache_dtype, int page);
+cudaError_t launch_paged_few(const PagedProblem &p, const PagedPart &part, int cache_dtype,
+                             const void *tm_k, const void *tm_v, bool direct, cudaStream_t s);
 
 // joins the partial results of both sources (n_parts of them) into out, lse
 cudaError_t launch_paged_join(const PagedProblem &p, const PagedPart *parts, int n_parts, int dtype,

@@ -1,5 +1,7 @@
 // ra_paged_api.cu -- the C ABI of the paged cache (include/ra.h): argument
 // checks, the choice of kernels and the workspace's layout.
+#include <cuda.h>
+
 #include <cstdio>
 
 #include "ra_paged.h"
@@ -100,12 +102,15 @@ int check_paged(const ra_kv_cache *c, const ra_paged_params *p)
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// CTAs of one attention launch: a fixed figure, so that the workspace's size
-// does not depend on the device (GB300 has 152 SMs).
+// CTAs of one attention launch are a fixed figure, so that the workspace's
+// size does not depend on the device (GB300 has 152 SMs).
 constexpr int kSms = 152;
+
+enum { kF32, kFew };
 
 struct Plan {
     PagedPart part[2];
+    int kernel[2];
     int n_parts;
     size_t bytes; // of the workspace
 };
@@ -116,12 +121,21 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
     Plan pl{};
     const int G = p->Hq / c->Hkv;
     for (int k = 0; k < (p->prefix_pages ? 2 : 1); ++k) {
-        PagedPart &a = pl.part[pl.n_parts++];
+        PagedPart &a = pl.part[pl.n_parts];
+        int &kernel = pl.kernel[pl.n_parts++];
         a.prefix = k;
         a.rows = (k ? p->B * p->Lq : p->Lq) * G;
-        a.row_block = kPagedF32Rows;
-        a.tile = kPagedF32Tile;
-        a.ctas = 4 * kSms;
+        if (p->dtype == RA_FP32) {
+            kernel = kF32;
+            a.row_block = kPagedF32Rows;
+            a.tile = kPagedF32Tile;
+            a.ctas = 4 * kSms;
+        } else {
+            kernel = kFew;
+            a.row_block = a.rows <= 8 ? 8 : 16;
+            a.tile = paged_few_tile(c->D, c->dtype);
+            a.ctas = 2 * kSms;
+        }
         a.n_rb = (a.rows + a.row_block - 1) / a.row_block;
         a.slot_rows = a.rows < a.row_block ? a.rows : a.row_block;
         const size_t slots = (size_t)a.ctas + (size_t)(k ? 1 : p->B) * a.n_rb * c->Hkv;
@@ -225,10 +239,20 @@ RA_API int ra_attn_paged(const ra_kv_cache *cache, const ra_paged_params *p, con
     x.lse = lse;
     x.status = d.status;
     x.timeout_ns = d.timeout_ns;
+    x.device = d.index;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
+    CUtensorMap tm[2];
+    const bool direct = pl.n_parts == 1; // a row whose keys one CTA sees is stored by it
+    if (p->dtype == RA_BF16) {
+        const int rows = paged_few_box(cache->D, cache->dtype, cache->page_size);
+        if ((rc = encode_paged(&tm[0], cache, cache->k, rows)) || (rc = encode_paged(&tm[1], cache, cache->v, rows)))
+            return rc;
+    }
     for (int k = 0; k < pl.n_parts && e == cudaSuccess; ++k)
-        e = launch_paged_f32(x, pl.part[k], cache->dtype, p->dtype, pl.n_parts == 1, s);
+        e = pl.kernel[k] == kF32
+                ? launch_paged_f32(x, pl.part[k], cache->dtype, direct, s)
+                : launch_paged_few(x, pl.part[k], cache->dtype, &tm[0], &tm[1], direct, s);
     if (e == cudaSuccess) e = launch_paged_join(x, pl.part, pl.n_parts, p->dtype, s);
     if (e != cudaSuccess) return set_cuda_error(e, "paged attention launch");
     count_launches(pl.n_parts + 1);
