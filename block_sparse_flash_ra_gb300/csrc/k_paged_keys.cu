@@ -1,0 +1,694 @@
+// k_paged_keys.cu -- attention over a paged cache for up to 32 query rows per
+// kv head and item at D = 128: decoding steps, drafts, multi-query heads; bf16
+// queries.  The keys are the M side of the tensor-core products.
+//
+// With few rows a cached byte is used a few times, so the bound is memory:
+// 128 keys of 8 bit are 32 KB, 0.74 us of one SM's share of 6.77 TB/s.  What
+// stands beside that is made small:
+//   S^T (128 keys x rows) = K (128 x D, shared memory) x Q^T
+//   O^T (D x rows)       += V^T (D x 128, the same bytes read MN-major) x P^T
+// are tcgen05 products with the cached tile as A, exactly as TMA laid it down:
+// cached bytes never pass through registers.  Rows are the N side, where 16
+// to 96 columns cost no more than reading A does.  (With the rows as M they
+// would be padded to 128; mma.sync.m16n8k16 measured 32 cycles each per
+// sub-core, and a kernel on it stopped at 46% of memory speed.)
+//
+// 8-bit caches run kind::f8f6f4 on the codes.  The other operand is split
+// into e4m3 terms, each in columns of its own, so that nothing is lost to it:
+//   q 2^-e = q1 + q2 / 16 (a bf16's 8 bits are two e4m3 significands; error
+//            2^-21 of the row's maximum), and the key's scale multiplies s;
+//   p 2^(e_v - E) = x1 + x2 / 16 + x3 / 256 out of f16 (2^-11 relative, 2^-26
+//            of the row's largest weight at the least), E the largest value
+//            exponent so far, so that the values' scales ride on p.
+// 16-bit caches run kind::f16 in bf16, q as it is, p = x1 + x2 (2^-16).
+// Logits, maxima, sums and O are fp32.
+//
+//   warps 0-3  softmax: thread = key = TMEM lane of S^T.  A row's maximum is
+//              over all threads, so it is only looked for when some logit
+//              passes the present reference by 2^4 (one barrier with an or);
+//              O (TMEM lane = d) is rescaled then and only then.
+//   warp 4     issues the products, S(i + 1) before P(i) V(i)
+//   warp 5     loads: a lane per page, K and V in rings of their own
+// Two CTAs per SM for 8-bit caches, so that one's softmax hides the other's
+// waits; one with twice the tile bytes for 16-bit ones.
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include <atomic>
+
+#include "ra_paged.cuh"
+#include "ra_sched.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kKeys = 128, kD = 128;
+constexpr int kSoftThreads = 128, kThreads = 192;
+constexpr float kLazy = 4.f;   // growth of a row maximum (base 2) that is let pass
+constexpr float kPBias = 4.f;  // 8-bit caches: weights times 2^4 are at most 2^8 < 448
+constexpr float kMinExp = 12.f; // least E: 2^(127 + kPBias - E) stays finite
+
+template <bool FP8, int RP>
+struct Cfg {
+    static constexpr int kMat = kKeys * kD * (FP8 ? 1 : 2); // bytes of a K or V tile
+    static constexpr int kHalves = FP8 ? 1 : 2;             // 128-byte wide blocks of a tile
+    static constexpr int kCtasPerSm = FP8 ? 2 : 1;
+    static constexpr int kStages = RP <= 16 ? (FP8 && RP == 16 ? 2 : 3) : 2;
+    static constexpr int kVStages = RP <= 16 ? 3 : 2;
+    static constexpr int kQTerms = FP8 ? 2 : 1, kPTerms = FP8 ? 3 : 2;
+    static constexpr int kNS = RP * kQTerms < 16 ? 16 : RP * kQTerms;     // columns of S^T
+    static constexpr int kNO = (RP * kPTerms + 15) / 16 * 16;             // columns of O^T
+    static constexpr int kQBytes = kNS * kD * (FP8 ? 1 : 2);
+    static constexpr int kPBytes = kNO * kKeys * (FP8 ? 1 : 2);
+    static constexpr int kKOff = 0;
+    static constexpr int kVOff = kKOff + kStages * kMat;
+    static constexpr int kQOff = kVOff + kVStages * kMat;
+    static constexpr int kPOff = kQOff + kQBytes;
+    static constexpr int kExpOff = kPOff + 2 * kPBytes; // per V stage: scale bytes of K, of V
+    static constexpr int kRowOff = kExpOff + (FP8 ? kVStages * 2 * kKeys : 0);
+    static constexpr int kRedOff = kRowOff + RP * 24;   // rows: qs, limit, place; then [4 warps][RP + 1]
+    static constexpr int kBarOff = kRedOff + 4 * (RP + 2) * 4;
+    static constexpr int kNumBars = 2 * kStages + 3 * kVStages + 2 + 2 + 2 + 2 + 1 + 1;
+    static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+    static constexpr int kSmem = kMiscOff + 16 + 1024;
+    static constexpr uint32_t kColO = 2 * kNS;
+    static constexpr uint32_t kCols = kColO + kNO <= 64 ? 64 : kColO + kNO <= 128 ? 128 : 256;
+    static constexpr uint32_t kIdescS = ((FP8 ? 0u : (1u << 7) | (1u << 10)) | (1u << 4)) |
+                                        ((uint32_t)(kNS >> 3) << 17) | ((uint32_t)(kKeys >> 4) << 24);
+    static constexpr uint32_t kIdescO = ((FP8 ? 0u : (1u << 7) | (1u << 10)) | (1u << 4)) | (1u << 15) |
+                                        ((uint32_t)(kNO >> 3) << 17) | ((uint32_t)(kD >> 4) << 24);
+    static_assert(kSmem <= (kCtasPerSm == 2 ? 113 : 227) * 1024, "shared memory");
+    static_assert(kBarOff % 8 == 0 && kRowOff % 8 == 0 && kPOff % 1024 == 0 && kExpOff % 128 == 0, "layout");
+};
+
+struct Bars {
+    uint64_t *k_full, *k_empty, *v_full, *v_empty, *e_full, *s_full, *s_empty, *p_full, *pv_done, *q_full, *drain;
+};
+
+template <class C>
+__device__ __forceinline__ Bars carve(uint8_t *smem)
+{
+    Bars b;
+    b.k_full = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
+    b.k_empty = b.k_full + C::kStages;
+    b.v_full = b.k_empty + C::kStages;
+    b.v_empty = b.v_full + C::kVStages;
+    b.e_full = b.v_empty + C::kVStages;
+    b.s_full = b.e_full + C::kVStages;
+    b.s_empty = b.s_full + 2;
+    b.p_full = b.s_empty + 2;
+    b.pv_done = b.p_full + 2;
+    b.q_full = b.pv_done + 2;
+    b.drain = b.q_full + 1;
+    return b;
+}
+
+// One product step by the whole warp (an elected lane issues).
+template <bool FP8>
+__device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    if (FP8)
+        asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                     "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                     : "memory");
+    else
+        mma_ss_w(d, a, b, idesc, accumulate);
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float *v)
+{
+    if (N == 32) tmem_ld32(addr, v);
+    else if (N == 16) tmem_ld16(addr, v);
+    else {
+        uint32_t *r = reinterpret_cast<uint32_t *>(v);
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(addr));
+    }
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint8_t *dst, const void *tmap, uint64_t *bar, int c0, int c1, int c2)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
+// The softmax warps' own barrier; all 128 threads pass it the same number of
+// times whatever happens, so it needs no time limit.
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool soft_or(bool x)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                 "barrier.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)x)
+                 : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ float warp_max(float x)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
+// e4m3x2 codes of two halves, and two halves back from codes
+__device__ __forceinline__ uint32_t to_codes(__half2 x)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 h;\n\tcvt.rn.satfinite.e4m3x2.f16x2 h, %1;\n\tcvt.u32.u16 %0, h;\n\t}"
+        : "=r"(r)
+        : "r"(*reinterpret_cast<uint32_t *>(&x)));
+    return r;
+}
+__device__ __forceinline__ __half2 from_codes(uint32_t c)
+{
+    const uint32_t r = e4m3x2_to_f16x2(c);
+    return *reinterpret_cast<const __half2 *>(&r);
+}
+
+__device__ __forceinline__ void sts8(uint32_t a, uint32_t x) { asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(x) : "memory"); }
+__device__ __forceinline__ void sts16(uint32_t a, uint32_t x)
+{
+    asm volatile("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tst.shared.u16 [%0], h;\n\t}" ::"r"(a), "r"(x) : "memory");
+}
+
+struct RowInfo {
+    float qs;  // logit scale of the row, base 2
+    int limit; // keys it sees
+    long long place; // (b * Lq + i) * Hq + hq, or -1
+    long long lse;   // place of its lse
+};
+
+template <bool FP8, int RP>
+__global__ void __launch_bounds__(kThreads, Cfg<FP8, RP>::kCtasPerSm)
+    paged_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      PagedProblem p, PagedPart part, bool direct)
+{
+    using C = Cfg<FP8, RP>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const Bars bars = carve<C>(smem);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::kMiscOff);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kMiscOff + 4);
+    const WaitCtx ctx{abort_flag, p.status, p.timeout_ns};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(bars.k_full + s, 1);
+            mbar_init(bars.k_empty + s, 1);
+        }
+        for (int s = 0; s < C::kVStages; ++s) {
+            mbar_init(bars.v_full + s, 1);
+            mbar_init(bars.v_empty + s, 1);
+            mbar_init(bars.e_full + s, 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bars.s_full + s, 1);
+            mbar_init(bars.s_empty + s, kSoftThreads);
+            mbar_init(bars.p_full + s, kSoftThreads);
+            mbar_init(bars.pv_done + s, 1);
+        }
+        mbar_init(bars.q_full, kSoftThreads);
+        mbar_init(bars.drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 4) {
+        tmem_alloc(tmem_holder, C::kCols);
+        tmem_relinquish();
+    }
+    if (warp == 5 && lane == 0) {
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
+    report_lengths(p, part);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctx)) != 0;
+    };
+    auto source_len = [&](int b) { return part.prefix ? paged_prefix_len(p) : paged_kv_len(p, b); };
+
+    PagedCursor c;
+    const bool any = cursor_begin(p, part, blockIdx.x, c);
+    if (any && warp == 5) {
+        // ------------------------------------------------------------ loads
+        // lane x fetches box x of a tile: its page number, then its K and V
+        const int box = min(p.c.page, kKeys), per = kKeys / box;
+        uint32_t i = 0;
+        bool ok = true;
+        auto entry = [&](int tile, int len) {
+            const int first = tile * kKeys + lane * box;
+            return lane < per && first < len ? page_entry(p, part, c.b, first) : 0;
+        };
+        for (;;) {
+            const int n = cursor_take(c), len = source_len(c.b);
+            int next = entry(c.t0, len);
+            for (int t = c.t0; ok && t < c.t0 + n; ++t, ++i) {
+                const int page = next, first = t * kKeys;
+                const int boxes = (min(len - first, kKeys) + box - 1) / box;
+                if (t + 1 < c.t0 + n) next = entry(t + 1, len);
+                const bool mine = lane < boxes;
+                const bool good = mine && page_valid(p, page);
+                const int z = good ? page * p.c.Hkv + c.h : p.c.n_pages * p.c.Hkv; // out of range: zeros
+                const int off = (first + lane * box) & (p.c.page - 1);
+                const int sv = i % C::kVStages, sk = i % C::kStages;
+                if (!(ok = wait_all(bars.k_empty + sk, ((i / C::kStages) & 1) ^ 1))) break;
+                if (lane == 0) mbar_expect_tx(bars.k_full + sk, boxes * box * (C::kMat / kKeys));
+                __syncwarp();
+                uint8_t *kd = smem + C::kKOff + sk * C::kMat + lane * box * 128;
+                if (mine)
+                    for (int hf = 0; hf < C::kHalves; ++hf)
+                        tma_load_3d(kd + hf * (kKeys * 128), &tm_k, bars.k_full + sk, hf * 64, off, z);
+                if (!(ok = wait_all(bars.v_empty + sv, ((i / C::kVStages) & 1) ^ 1))) {
+                    ++i; // this tile's K is on its way, its V is not
+                    break;
+                }
+                const int n_good = __popc(__ballot_sync(0xffffffffu, good));
+                if (FP8) {
+                    uint8_t *e = smem + C::kExpOff + sv * 2 * kKeys + lane * box;
+                    if (mine && !good) { // zeros, at a scale of one
+                        for (int j = 0; j < box; ++j) e[j] = e[kKeys + j] = 127;
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_expect_tx(bars.e_full + sv, 2 * n_good * box);
+                    __syncwarp();
+                    if (good) {
+                        const size_t row = ((size_t)z << p.c.page_shift) + off;
+                        bulk_load(e, p.c.k_exp + row, box, bars.e_full + sv);
+                        bulk_load(e + kKeys, p.c.v_exp + row, box, bars.e_full + sv);
+                    }
+                }
+                if (lane == 0) mbar_expect_tx(bars.v_full + sv, boxes * box * (C::kMat / kKeys));
+                __syncwarp();
+                uint8_t *vd = smem + C::kVOff + sv * C::kMat + lane * box * 128;
+                if (mine)
+                    for (int hf = 0; hf < C::kHalves; ++hf)
+                        tma_load_3d(vd + hf * (kKeys * 128), &tm_v, bars.v_full + sv, hf * 64, off, z);
+            }
+            if (!ok || !cursor_next(p, part, c, n)) break;
+        }
+        if (!ok) {
+            // copies on their way land before the CTA ends: tile j's phase of
+            // its stage, for the last tiles of each ring (a phase that already
+            // passed, or the V that was not asked for, only runs the clock)
+            for (uint32_t j = i > (uint32_t)C::kStages ? i - C::kStages : 0; j < i; ++j)
+                wait_drain(bars.k_full + j % C::kStages, (j / C::kStages) & 1, kDrainNs);
+            for (uint32_t j = i > (uint32_t)C::kVStages ? i - C::kVStages : 0; j < i; ++j) {
+                wait_drain(bars.v_full + j % C::kVStages, (j / C::kVStages) & 1, kDrainNs);
+                if (FP8) wait_drain(bars.e_full + j % C::kVStages, (j / C::kVStages) & 1, kDrainNs);
+            }
+        }
+    } else if (any && warp == 4) {
+        // ------------------------------------------------------------ products
+        const uint64_t kd0 = sdesc_sw128(smem_u32(smem + C::kKOff), 16, 1024);
+        const uint64_t vd0 = sdesc_sw128(smem_u32(smem + C::kVOff), kKeys * 128, 1024);
+        const uint64_t qd0 = sdesc_sw128(smem_u32(smem + C::kQOff), 16, 1024);
+        const uint64_t pd0 = sdesc_sw128(smem_u32(smem + C::kPOff), 16, 1024);
+        uint32_t i = 0, segs = 0;
+        bool ok = true;
+        auto issue_pv = [&](uint32_t j, bool first) -> bool {
+            const int sb = j & 1, sv = j % C::kVStages;
+            if (!wait_all(bars.v_full + sv, (j / C::kVStages) & 1)) return false;
+            if (!wait_all(bars.p_full + sb, (j >> 1) & 1)) return false;
+            tc_fence_after();
+            const uint64_t vd = vd0 + (uint32_t)((sv * C::kMat) >> 4), pd = pd0 + (uint32_t)((sb * C::kPBytes) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < (FP8 ? 4 : 8); ++kk) {
+                // A: 32 or 16 keys further down the tile; B: 32 bytes further along the keys
+                const uint32_t bo = FP8 ? kk * 32 : (kk >> 2) * (C::kNO * 128) + (kk & 3) * 32;
+                mma_step<FP8>(tmem + C::kColO, vd + (uint32_t)((kk * (FP8 ? 4096 : 2048)) >> 4), pd + (bo >> 4), C::kIdescO,
+                              (kk > 0 || !first) ? 1u : 0u);
+            }
+            tc_commit_w(bars.v_empty + sv);
+            tc_commit_w(bars.pv_done + sb);
+            return true;
+        };
+        for (;;) {
+            const int n = cursor_take(c);
+            if (!(ok = wait_all(bars.q_full, segs++ & 1))) break;
+            for (int t = 0; ok && t < n; ++t, ++i) {
+                const int sk = i % C::kStages, sb = i & 1;
+                if (!(ok = wait_all(bars.k_full + sk, (i / C::kStages) & 1))) break;
+                if (!(ok = wait_all(bars.s_empty + sb, ((i >> 1) & 1) ^ 1))) break;
+                tc_fence_after();
+                const uint64_t kd = kd0 + (uint32_t)((sk * C::kMat) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < (FP8 ? 4 : 8); ++kk) {
+                    const uint32_t ao = FP8 ? kk * 32 : (kk >> 2) * (kKeys * 128) + (kk & 3) * 32;
+                    const uint32_t bo = FP8 ? kk * 32 : (kk >> 2) * (C::kNS * 128) + (kk & 3) * 32;
+                    mma_step<FP8>(tmem + sb * C::kNS, kd + (ao >> 4), qd0 + (bo >> 4), C::kIdescS, kk > 0 ? 1u : 0u);
+                }
+                tc_commit_w(bars.k_empty + sk);
+                tc_commit_w(bars.s_full + sb);
+                if (t > 0) ok = issue_pv(i - 1, t == 1);
+            }
+            if (!ok || !(ok = issue_pv(i - 1, n == 1))) break;
+            if (!cursor_next(p, part, c, n)) break;
+        }
+        tc_commit_w(bars.drain);
+        wait_drain(bars.drain, 0, kDrainNs);
+    } else if (any && warp < 4) {
+        // ------------------------------------------------------------ softmax
+        // From the first wait that gave up on, no wait is made any more, and
+        // the loops run out on whatever is there: every barrier of these
+        // warps is still met by all of them.
+        const int tid = threadIdx.x;
+        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+        RowInfo *rows = reinterpret_cast<RowInfo *>(smem + C::kRowOff);
+        float *red = reinterpret_cast<float *>(smem + C::kRedOff); // [4][RP + 2]
+        const uint32_t p_base = smem_u32(smem + C::kPOff);
+        const float cap2 = p.soft_cap * kLog2e, to_cap = p.soft_cap > 0.f ? kLn2 / p.soft_cap : 0.f;
+        uint32_t i = 0, pv_seen = 0;
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            if (ok) ok = wait_all(bar, parity);
+        };
+        auto wait_pv = [&](uint32_t n) { // products of tiles below n are complete
+            for (; ok && pv_seen < n; ++pv_seen) wait(bars.pv_done + (pv_seen & 1), (pv_seen >> 1) & 1);
+        };
+        for (;;) {
+            const int n = cursor_take(c), len = source_len(c.b);
+            // ---- the query rows: 16 threads take one, 8 values each
+#pragma unroll
+            for (int r0 = 0; r0 < C::kNS / C::kQTerms; r0 += 8) {
+                const int r = r0 + (tid >> 4), x = tid & 15;
+                const PagedRow row = paged_row(p, part, c, r);
+                const bool live = r < RP && row.counts;
+                const int hq = c.h * p.G + row.g;
+                const long long place = ((long long)row.b * p.Lq + row.i) * p.Hq + hq;
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (live)
+                    w = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + (size_t)place * kD + x * 8);
+                float qs = p.scale * kLog2e;
+                if (FP8) {
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t top = 0; // largest magnitude, as bf16 bits
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) top = max(top, max(u[y] & 0x7fffu, (u[y] >> 16) & 0x7fffu));
+#pragma unroll
+                    for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    // the maximum goes to [128, 256); 2^+-e stay normal
+                    const int e = min(max((int)(top >> 7) - 134, -120), 120);
+                    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+                    qs *= __uint_as_float((uint32_t)(127 + e) << 23);
+                    if (top >= 0x7f80u) qs = __uint_as_float(0x7fc00000u); // e4m3 has no infinity
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        // f16 holds the 8 bits; below 2^-14 it rounds at 2^-25
+                        const __half2 q2 = __floats2half2_rn(__uint_as_float(u[y] << 16) * inv,
+                                                             __uint_as_float(u[y] & 0xffff0000u) * inv);
+                        hi[y] = to_codes(q2);
+                        lo[y] = to_codes(__hmul2(__hsub2(q2, from_codes(hi[y])), __float2half2_rn(16.f)));
+                    }
+                    const uint32_t at = smem_u32(smem + C::kQOff) + (((x >> 1) ^ (r & 7)) << 4) + (x & 1) * 8;
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + r * 128), "r"(hi[0] | hi[1] << 16),
+                                 "r"(hi[2] | hi[3] << 16)
+                                 : "memory");
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + (RP + r) * 128), "r"(lo[0] | lo[1] << 16),
+                                 "r"(lo[2] | lo[3] << 16)
+                                 : "memory");
+                } else {
+                    const uint32_t at = smem_u32(smem + C::kQOff) + (x >> 3) * (C::kNS * 128) + r * 128 +
+                                        (((x & 7) ^ (r & 7)) << 4);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
+                                 : "memory");
+                }
+                if (x == 0 && r < RP) {
+                    RowInfo &o = rows[r];
+                    o.qs = qs;
+                    o.limit = live ? row.limit : 0x7fffffff; // rows of no use need no mask
+                    o.place = live ? place : -1;
+                    o.lse = ((long long)row.b * p.Hq + hq) * p.Lq + row.i;
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive(bars.q_full);
+            soft_sync();
+            int all = 0x7fffffff; // keys below it are seen by every row
+#pragma unroll
+            for (int r = 0; r < RP; ++r) all = min(all, rows[r].limit);
+
+            float m[RP], l[RP], ev_top = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < RP; ++r) m[r] = -INFINITY, l[r] = 0.f;
+            for (int t = c.t0; t < c.t0 + n; ++t, ++i) {
+                const int sb = i & 1, sv = i % C::kVStages;
+                const int key = t * kKeys + tid;
+                const int valid = min(len - t * kKeys, kKeys);
+                const bool masked = t * kKeys + kKeys > min(all, len);
+                float s[RP];
+                wait(bars.s_full + sb, (i >> 1) & 1);
+                tc_fence_after();
+                if (FP8) {
+                    float s2[RP];
+                    tmem_ld<RP>(lane_base + sb * C::kNS, s);
+                    tmem_ld<RP>(lane_base + sb * C::kNS + RP, s2);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) s[r] = fmaf(s2[r], 1.f / 16.f, s[r]);
+                } else {
+                    tmem_ld<RP>(lane_base + sb * C::kNS, s);
+                    tmem_ld_wait();
+                }
+                tc_fence_before();
+                mbar_arrive(bars.s_empty + sb);
+                float ks = 1.f, vs = 1.f, ev = -INFINITY;
+                if (FP8) {
+                    wait(bars.e_full + sv, (i / C::kVStages) & 1);
+                    const uint8_t *e = smem + C::kExpOff + sv * 2 * kKeys + tid;
+                    const uint32_t vb = e[kKeys];
+                    ks = exp_byte_scale(e[0]);
+                    vs = exp_byte_scale(vb);
+                    // bytes behind the length and rows without a value do not count
+                    if (tid < valid && vb != 255u) ev = fmaxf((float)vb, kMinExp);
+                }
+                // ---- logits in base 2
+                bool grow = FP8 && ev > ev_top;
+#pragma unroll
+                for (int r = 0; r < RP; ++r) {
+                    float x = s[r] * (FP8 ? rows[r].qs * ks : rows[r].qs);
+                    if (to_cap > 0.f) x = cap2 * tanh_fast(x * to_cap);
+                    if (masked && (tid >= valid || key >= rows[r].limit)) x = -INFINITY;
+                    s[r] = x;
+                    grow |= x > m[r] + kLazy;
+                }
+                if (soft_or(grow)) {
+                    // new references: the maxima so far
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) {
+                        const float x = warp_max(s[r]);
+                        if (lane == 0) red[warp * (RP + 2) + r] = x;
+                    }
+                    if (FP8) {
+                        ev = warp_max(ev);
+                        if (lane == 0) red[warp * (RP + 2) + RP] = ev;
+                    }
+                    wait_pv(i); // O is still
+                    soft_sync();
+                    float fe = 1.f;
+                    if (FP8) {
+                        float top = ev_top;
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) top = fmaxf(top, red[w * (RP + 2) + RP]);
+                        fe = ev_top == -INFINITY ? 0.f : ex2_approx(ev_top - top);
+                        ev_top = top;
+                    }
+                    float f[RP];
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) {
+                        float top = m[r];
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) top = fmaxf(top, red[w * (RP + 2) + r]);
+                        const float x = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - top);
+                        l[r] *= x;
+                        f[r] = x * fe;
+                        m[r] = top;
+                    }
+                    if (t > c.t0) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < C::kPTerms; ++k)
+#pragma unroll
+                            for (int r = 0; r < RP; r += 8) {
+                                float o[8];
+                                uint32_t w[8];
+                                tmem_ld<8>(lane_base + C::kColO + k * RP + r, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int y = 0; y < 8; ++y) w[y] = __float_as_uint(o[y] * f[r + y]);
+                                tmem_st8(lane_base + C::kColO + k * RP + r, w);
+                            }
+                        tmem_st_wait();
+                    }
+                    soft_sync(); // red is free again
+                }
+                // ---- weights, as the terms of P^T: row of term k and query row
+                // r is k * RP + r, this thread's column is its key
+                const float pb = FP8 ? (ev_top == -INFINITY ? 1.f : ex2_approx(127.f + kPBias - ev_top)) * vs : 1.f;
+                if (i >= 2) wait_pv(i - 1); // the tile before last has been read
+                const uint32_t pt = p_base + sb * C::kPBytes;
+#pragma unroll
+                for (int r = 0; r < RP; r += 2) {
+                    float x[2];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float base = m[r + y] == -INFINITY ? 0.f : m[r + y];
+                        x[y] = ex2_approx(s[r + y] - base);
+                        l[r + y] += x[y];
+                        // a masked key's scale may be anything
+                        if (FP8) x[y] = masked && s[r + y] == -INFINITY ? 0.f : x[y] * pb;
+                    }
+                    if (FP8) {
+                        __half2 h = __floats2half2_rn(x[0], x[1]);
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) {
+                            const uint32_t w = to_codes(h);
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const int row = k * RP + r + y;
+                                sts8(pt + row * 128 + (((tid >> 4) ^ (row & 7)) << 4) + (tid & 15), y ? w >> 8 : w & 0xffu);
+                            }
+                            if (k < 2) h = __hmul2(__hsub2(h, from_codes(w)), __float2half2_rn(16.f));
+                        }
+                    } else {
+                        const uint32_t hi = pack_bf16x2(x[0], x[1]);
+                        const uint32_t lo = pack_bf16x2(x[0] - __uint_as_float(hi << 16),
+                                                        x[1] - __uint_as_float(hi & 0xffff0000u));
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const int row = k * RP + r + y;
+                                const uint32_t w = k ? lo : hi;
+                                sts16(pt + (tid >> 6) * (C::kNO * 128) + row * 128 + ((((tid >> 3) & 7) ^ (row & 7)) << 4) +
+                                          (tid & 7) * 2,
+                                      y ? w >> 16 : w & 0xffffu);
+                            }
+                    }
+                }
+                if (valid < kKeys) {
+                    // values behind the length: whatever is there, weight 0 must give 0
+                    wait(bars.v_full + sv, (i / C::kVStages) & 1);
+                    if (tid >= valid)
+#pragma unroll
+                        for (int x = 0; x < C::kHalves * 8; ++x)
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                             smem_u32(smem + C::kVOff + sv * C::kMat) + (x >> 3) * (kKeys * 128) + tid * 128 +
+                                             (x & 7) * 16),
+                                         "r"(0)
+                                         : "memory");
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                tc_fence_before();
+                mbar_arrive(bars.p_full + sb);
+            }
+            // ---- the segment's end: sums over the keys' threads, O out of TMEM
+#pragma unroll
+            for (int r = 0; r < RP; ++r) {
+                float x = l[r];
+#pragma unroll
+                for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                if (lane == 0) red[warp * (RP + 2) + r] = x;
+            }
+            soft_sync();
+            wait_pv(i);
+            tc_fence_after();
+            const float fe = FP8 ? (ev_top == -INFINITY ? 0.f : ex2_approx(ev_top - 127.f - kPBias)) : 1.f;
+            const bool final = direct && c.t0 == 0 && n == c.tiles;
+            const size_t slot = ((size_t)blockIdx.x + c.seg) * part.slot_rows;
+#pragma unroll
+            for (int r = 0; r < RP; r += 8) {
+                float o[C::kPTerms][8];
+#pragma unroll
+                for (int k = 0; k < C::kPTerms; ++k) tmem_ld<8>(lane_base + C::kColO + k * RP + r, o[k]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                    float lr = 0.f, mr = m[r + y], v = o[0][y];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) lr += red[w * (RP + 2) + r + y];
+                    if (FP8) v = (v + (o[1][y] + o[2][y] * (1.f / 16.f)) * (1.f / 16.f)) * fe;
+                    else v += o[1][y];
+                    const RowInfo &row = rows[r + y];
+                    if (row.place < 0) continue;
+                    if (final) {
+                        if (p.sinks) {
+                            const float sink = p.sinks[row.place % p.Hq] * kLog2e, top = fmaxf(mr, sink);
+                            const float f = ex2_approx(mr - top);
+                            lr = lr * f + ex2_approx(sink - top);
+                            v *= f;
+                            mr = top;
+                        }
+                        static_cast<__nv_bfloat16 *>(p.out)[(size_t)row.place * kD + tid] =
+                            __float2bfloat16_rn(lr == 0.f ? 0.f : v / lr);
+                        if (tid == 0) p.lse[row.lse] = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * kLn2;
+                    } else {
+                        part.o[(slot + r + y) * kD + tid] = v;
+                        if (tid == 0) *reinterpret_cast<float2 *>(part.ml + (slot + r + y) * 2) = make_float2(mr, lr);
+                    }
+                }
+            }
+            tc_fence_before();
+            soft_sync(); // rows and red are free again
+            if (!cursor_next(p, part, c, n)) break;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 4) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kCols);
+    }
+}
+
+template <bool FP8, int RP>
+cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &k, const CUtensorMap &v, bool direct,
+               cudaStream_t s)
+{
+    auto kern = paged_keys_kernel<FP8, RP>;
+    static std::atomic<uint64_t> set{0}; // devices whose copy of the kernel has its attribute
+    const uint64_t bit = 1ull << p.device;
+    if (!(set.load(std::memory_order_acquire) & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<FP8, RP>::kSmem);
+        if (e != cudaSuccess) return e;
+        set.fetch_or(bit, std::memory_order_release);
+    }
+    kern<<<part.ctas, kThreads, Cfg<FP8, RP>::kSmem, s>>>(k, v, p, part, direct);
+    return cudaGetLastError();
+}
+
+} // namespace
+
+cudaError_t launch_paged_keys(const PagedProblem &p, const PagedPart &part, int cache_dtype, const void *tm_k,
+                              const void *tm_v, bool direct, cudaStream_t s)
+{
+    const CUtensorMap &k = *static_cast<const CUtensorMap *>(tm_k), &v = *static_cast<const CUtensorMap *>(tm_v);
+    if (cache_dtype == RA_E4M3) {
+        if (part.row_block == 8) return go<true, 8>(p, part, k, v, direct, s);
+        return part.row_block == 16 ? go<true, 16>(p, part, k, v, direct, s) : go<true, 32>(p, part, k, v, direct, s);
+    }
+    if (part.row_block == 8) return go<false, 8>(p, part, k, v, direct, s);
+    return part.row_block == 16 ? go<false, 16>(p, part, k, v, direct, s) : go<false, 32>(p, part, k, v, direct, s);
+}
+
+} // namespace ra

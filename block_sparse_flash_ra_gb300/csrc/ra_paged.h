@@ -69,6 +69,12 @@ int paged_few_box(int D, int cache_dtype, int page);
 cudaError_t launch_paged_few(const PagedProblem &p, const PagedPart &part, int cache_dtype,
                              const void *tm_k, const void *tm_v, bool direct, cudaStream_t s);
 
+// bf16 queries, D = 128, row_block 8, 16 or 32: the keys as the M side of
+// tcgen05 products (boxes of min(page, 128) tokens)
+constexpr int kPagedKeysTile = 128;
+cudaError_t launch_paged_keys(const PagedProblem &p, const PagedPart &part, int cache_dtype,
+                              const void *tm_k, const void *tm_v, bool direct, cudaStream_t s);
+
 // joins the partial results of both sources (n_parts of them) into out, lse
 cudaError_t launch_paged_join(const PagedProblem &p, const PagedPart *parts, int n_parts, int dtype,
                               cudaStream_t s);

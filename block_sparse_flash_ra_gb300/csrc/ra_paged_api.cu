@@ -106,7 +106,7 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 // size does not depend on the device (GB300 has 152 SMs).
 constexpr int kSms = 152;
 
-enum { kF32, kFew };
+enum { kF32, kFew, kKeysM };
 
 struct Plan {
     PagedPart part[2];
@@ -130,6 +130,11 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
             a.row_block = kPagedF32Rows;
             a.tile = kPagedF32Tile;
             a.ctas = 4 * kSms;
+        } else if (c->D == 128) {
+            kernel = kKeysM;
+            a.row_block = a.rows <= 8 ? 8 : a.rows <= 16 ? 16 : 32;
+            a.tile = kPagedKeysTile;
+            a.ctas = (c->dtype == RA_E4M3 ? 2 : 1) * kSms;
         } else {
             kernel = kFew;
             a.row_block = a.rows <= 8 ? 8 : 16;
@@ -245,14 +250,16 @@ RA_API int ra_attn_paged(const ra_kv_cache *cache, const ra_paged_params *p, con
     CUtensorMap tm[2];
     const bool direct = pl.n_parts == 1; // a row whose keys one CTA sees is stored by it
     if (p->dtype == RA_BF16) {
-        const int rows = paged_few_box(cache->D, cache->dtype, cache->page_size);
+        const int rows = cache->D == 128 ? cache->page_size : paged_few_box(cache->D, cache->dtype, cache->page_size);
         if ((rc = encode_paged(&tm[0], cache, cache->k, rows)) || (rc = encode_paged(&tm[1], cache, cache->v, rows)))
             return rc;
     }
     for (int k = 0; k < pl.n_parts && e == cudaSuccess; ++k)
         e = pl.kernel[k] == kF32
                 ? launch_paged_f32(x, pl.part[k], cache->dtype, direct, s)
-                : launch_paged_few(x, pl.part[k], cache->dtype, &tm[0], &tm[1], direct, s);
+            : pl.kernel[k] == kFew
+                ? launch_paged_few(x, pl.part[k], cache->dtype, &tm[0], &tm[1], direct, s)
+                : launch_paged_keys(x, pl.part[k], cache->dtype, &tm[0], &tm[1], direct, s);
     if (e == cudaSuccess) e = launch_paged_join(x, pl.part, pl.n_parts, p->dtype, s);
     if (e != cudaSuccess) return set_cuda_error(e, "paged attention launch");
     count_launches(pl.n_parts + 1);
