@@ -63,7 +63,7 @@ __device__ __forceinline__ void fill_tile(float *dst, const void *base, const ui
 
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads)
-    paged_f32_kernel(PagedProblem p, PagedPart part, bool direct)
+    paged_f32_kernel(PagedProblem p, PagedPart part)
 {
     // o: thread t holds column t % D of rows (t / D) * OR .. + OR - 1
     constexpr int OR = kRows * D / kThreads;
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads)
             }
         }
         __syncthreads();
-        if (direct && c.t0 == 0 && n == c.tiles) {
+        if (stores_whole(part, c, n)) {
             // the whole segment was here: the rows' final values
 #pragma unroll
             for (int r = 0; r < OR; ++r) {
@@ -172,14 +172,14 @@ __global__ void __launch_bounds__(kThreads)
                     p.lse[((size_t)x.b * p.Hq + hq) * p.Lq + x.i] = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * kLn2;
             }
         } else {
-            const size_t slot = (size_t)(blockIdx.x + c.seg);
+            const size_t at = slot_row(part, c) + row0;
 #pragma unroll
             for (int r = 0; r < OR; ++r)
                 if (row0 + r < part.slot_rows) {
-                    part.o[(slot * part.slot_rows + row0 + r) * D + col] = o[r];
+                    part.o[(at + r) * D + col] = o[r];
                     if (col == 0) {
-                        part.ml[(slot * part.slot_rows + row0 + r) * 2] = m_s[row0 + r];
-                        part.ml[(slot * part.slot_rows + row0 + r) * 2 + 1] = l_s[row0 + r];
+                        part.ml[(at + r) * 2] = m_s[row0 + r];
+                        part.ml[(at + r) * 2 + 1] = l_s[row0 + r];
                     }
                 }
         }
@@ -189,11 +189,10 @@ __global__ void __launch_bounds__(kThreads)
 
 } // namespace
 
-cudaError_t launch_paged_f32(const PagedProblem &p, const PagedPart &part, int cache_dtype, bool direct,
-                             cudaStream_t s)
+cudaError_t launch_paged_f32(const PagedProblem &p, const PagedPart &part, int cache_dtype, cudaStream_t s)
 {
     auto go = [&](auto kern) {
-        kern<<<part.ctas, kThreads, 0, s>>>(p, part, direct);
+        kern<<<part.ctas, kThreads, 0, s>>>(p, part);
         return cudaGetLastError();
     };
     if (cache_dtype == RA_E4M3) return p.c.D == 64 ? go(paged_f32_kernel<64, true>) : go(paged_f32_kernel<128, true>);

@@ -155,7 +155,7 @@ struct Ahead {
 template <int D, bool FP8, int ROWS>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                     PagedProblem p, PagedPart part, bool direct)
+                     PagedProblem p, PagedPart part)
 {
     using C = Cfg<D, FP8>;
     constexpr int NB = C::kKeys / 8;   // key groups of a stage
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
             // column n, block x: d = n * (D / 8) + x for codes, and for bf16
             // d = (x / 8) * 64 + n * 8 + x % 8
             constexpr int RUN = FP8 ? OB : 8;
-            if (direct && c.t0 == 0 && n == c.tiles) {
+            if (stores_whole(part, c, n)) {
                 if (!row.counts) continue;
                 const int hq = c.h * p.G + row.g;
                 float fs = 1.f, lr = lt[r], mr = mt[r];
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
                 if (t4 == 0)
                     p.lse[((size_t)row.b * p.Hq + hq) * p.Lq + row.i] = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * kLn2;
             } else if (in_block < part.slot_rows) {
-                const size_t at = (size_t)(blockIdx.x + c.seg) * part.slot_rows + in_block;
+                const size_t at = slot_row(part, c) + in_block;
                 float *dst = part.o + at * D;
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
@@ -618,8 +618,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 }
 
 template <int D, bool FP8, int ROWS>
-cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &k, const CUtensorMap &v, bool direct,
-               cudaStream_t s)
+cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s)
 {
     auto kern = paged_few_kernel<D, FP8, ROWS>;
     static std::atomic<uint64_t> set{0}; // devices whose copy of the kernel has its attribute
@@ -630,7 +629,7 @@ cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &
         if (e != cudaSuccess) return e;
         set.fetch_or(bit, std::memory_order_release);
     }
-    kern<<<part.ctas, kWarps * 32, Cfg<D, FP8>::kSmem, s>>>(k, v, p, part, direct);
+    kern<<<part.ctas, kWarps * 32, Cfg<D, FP8>::kSmem, s>>>(k, v, p, part);
     return cudaGetLastError();
 }
 
@@ -649,16 +648,16 @@ int paged_few_box(int D, int cache_dtype, int page)
 }
 
 cudaError_t launch_paged_few(const PagedProblem &p, const PagedPart &part, int cache_dtype, const void *tm_k,
-                             const void *tm_v, bool direct, cudaStream_t s)
+                             const void *tm_v, cudaStream_t s)
 {
     const CUtensorMap &k = *static_cast<const CUtensorMap *>(tm_k), &v = *static_cast<const CUtensorMap *>(tm_v);
     const bool few = part.row_block == 8;
     if (cache_dtype == RA_E4M3) {
-        if (p.c.D == 64) return few ? go<64, true, 8>(p, part, k, v, direct, s) : go<64, true, 16>(p, part, k, v, direct, s);
-        return few ? go<128, true, 8>(p, part, k, v, direct, s) : go<128, true, 16>(p, part, k, v, direct, s);
+        if (p.c.D == 64) return few ? go<64, true, 8>(p, part, k, v, s) : go<64, true, 16>(p, part, k, v, s);
+        return few ? go<128, true, 8>(p, part, k, v, s) : go<128, true, 16>(p, part, k, v, s);
     }
-    if (p.c.D == 64) return few ? go<64, false, 8>(p, part, k, v, direct, s) : go<64, false, 16>(p, part, k, v, direct, s);
-    return few ? go<128, false, 8>(p, part, k, v, direct, s) : go<128, false, 16>(p, part, k, v, direct, s);
+    if (p.c.D == 64) return few ? go<64, false, 8>(p, part, k, v, s) : go<64, false, 16>(p, part, k, v, s);
+    return few ? go<128, false, 8>(p, part, k, v, s) : go<128, false, 16>(p, part, k, v, s);
 }
 
 } // namespace ra

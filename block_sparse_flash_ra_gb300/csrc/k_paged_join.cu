@@ -18,11 +18,17 @@ namespace {
 
 constexpr int kWarps = 4;
 
-// The slots [first, first + n) that hold partial results of a row.
+// The partial results of a row: CTAs c0 .. c0 + n - 1, and where they lie.
 struct Slots {
-    long long first;
+    long long c0, seg;
     int n, row;
-    bool whole; // one CTA saw all tiles of the segment
+    bool opens; // the segment is the first of c0's share
+
+    __device__ __forceinline__ size_t at(const PagedPart &part, int x) const
+    {
+        const long long slot = part.direct ? 2 * (c0 + x) + (x == 0 && !opens ? 1 : 0) : c0 + x + seg;
+        return (size_t)slot * part.slot_rows + row;
+    }
 };
 
 __device__ __forceinline__ Slots find_slots(const PagedProblem &p, const PagedPart &part, int b, int i, int h,
@@ -35,26 +41,23 @@ __device__ __forceinline__ Slots find_slots(const PagedProblem &p, const PagedPa
     int tiles;
     if (part.prefix) {
         tiles = (paged_prefix_len(p) + part.tile - 1) / part.tile;
-        total = per_seq * tiles;
-        start = seg * tiles;
+        total = per_seq * (tiles + part.seg_cost);
+        start = seg * (tiles + part.seg_cost);
     } else {
         tiles = own_tiles(p, part, b);
-        const long long before = own_tiles_before(p, part, b);
-        long long after = 0;
-        for (int x = b + (threadIdx.x & 31); x < p.B; x += 32) after += own_tiles(p, part, x);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) after += __shfl_xor_sync(0xffffffffu, after, o);
-        total = per_seq * (before + after);
-        start = per_seq * before + seg * tiles;
+        long long before;
+        total = per_seq * own_places_sum(p, part, b, before);
+        start = per_seq * before + seg * (tiles + part.seg_cost);
         seg += per_seq * b;
     }
-    Slots s{0, 0, n - rb * part.row_block, false};
+    Slots s{0, seg, 0, n - rb * part.row_block, false};
     if (tiles == 0) return s;
     const long long share = (total + part.ctas - 1) / part.ctas;
-    const long long c0 = start / share, c1 = (start + tiles - 1) / share;
-    s.first = c0 + seg;
-    s.n = (int)(c1 - c0) + 1;
-    s.whole = s.n == 1;
+    const long long first = start + part.seg_cost; // place of the first tile
+    s.c0 = first / share;
+    s.n = (int)((first + tiles - 1) / share - s.c0) + 1;
+    // a share that begins before `start` begins with another segment's tile
+    s.opens = start <= s.c0 * share;
     return s;
 }
 
@@ -72,9 +75,9 @@ __global__ void __launch_bounds__(kWarps * 32) paged_join_kernel(PagedProblem p,
     for (int k = 0; k < n_parts; ++k) {
         const PagedPart &part = k ? b2 : a;
         const Slots s = find_slots(p, part, b, i, hq / p.G, hq % p.G);
-        if (n_parts == 1 && s.whole) return; // stored by the attention kernel
+        if (part.direct && s.n == 1) return; // stored by the attention kernel
         for (int x = warp; x < s.n; x += kWarps) {
-            const size_t at = (size_t)(s.first + x) * part.slot_rows + s.row;
+            const size_t at = s.at(part, x);
             const float mx = part.ml[at * 2], lx = part.ml[at * 2 + 1];
             float ox[V];
 #pragma unroll

@@ -196,7 +196,7 @@ struct RowInfo {
 template <bool FP8, int RP>
 __global__ void __launch_bounds__(kThreads, Cfg<FP8, RP>::kCtasPerSm)
     paged_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                      PagedProblem p, PagedPart part, bool direct)
+                      PagedProblem p, PagedPart part)
 {
     using C = Cfg<FP8, RP>;
     extern __shared__ uint8_t smem_raw[];
@@ -613,8 +613,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, RP>::kCtasPerSm)
             wait_pv(i);
             tc_fence_after();
             const float fe = FP8 ? (ev_top == -INFINITY ? 0.f : ex2_approx(ev_top - 127.f - kPBias)) : 1.f;
-            const bool final = direct && c.t0 == 0 && n == c.tiles;
-            const size_t slot = ((size_t)blockIdx.x + c.seg) * part.slot_rows;
+            const bool final = stores_whole(part, c, n);
+            const size_t slot = slot_row(part, c);
 #pragma unroll
             for (int r = 0; r < RP; r += 8) {
                 float o[C::kPTerms][8];
@@ -662,8 +662,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, RP>::kCtasPerSm)
 }
 
 template <bool FP8, int RP>
-cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &k, const CUtensorMap &v, bool direct,
-               cudaStream_t s)
+cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s)
 {
     auto kern = paged_keys_kernel<FP8, RP>;
     static std::atomic<uint64_t> set{0}; // devices whose copy of the kernel has its attribute
@@ -673,22 +672,22 @@ cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &
         if (e != cudaSuccess) return e;
         set.fetch_or(bit, std::memory_order_release);
     }
-    kern<<<part.ctas, kThreads, Cfg<FP8, RP>::kSmem, s>>>(k, v, p, part, direct);
+    kern<<<part.ctas, kThreads, Cfg<FP8, RP>::kSmem, s>>>(k, v, p, part);
     return cudaGetLastError();
 }
 
 } // namespace
 
 cudaError_t launch_paged_keys(const PagedProblem &p, const PagedPart &part, int cache_dtype, const void *tm_k,
-                              const void *tm_v, bool direct, cudaStream_t s)
+                              const void *tm_v, cudaStream_t s)
 {
     const CUtensorMap &k = *static_cast<const CUtensorMap *>(tm_k), &v = *static_cast<const CUtensorMap *>(tm_v);
     if (cache_dtype == RA_E4M3) {
-        if (part.row_block == 8) return go<true, 8>(p, part, k, v, direct, s);
-        return part.row_block == 16 ? go<true, 16>(p, part, k, v, direct, s) : go<true, 32>(p, part, k, v, direct, s);
+        if (part.row_block == 8) return go<true, 8>(p, part, k, v, s);
+        return part.row_block == 16 ? go<true, 16>(p, part, k, v, s) : go<true, 32>(p, part, k, v, s);
     }
-    if (part.row_block == 8) return go<false, 8>(p, part, k, v, direct, s);
-    return part.row_block == 16 ? go<false, 16>(p, part, k, v, direct, s) : go<false, 32>(p, part, k, v, direct, s);
+    if (part.row_block == 8) return go<false, 8>(p, part, k, v, s);
+    return part.row_block == 16 ? go<false, 16>(p, part, k, v, s) : go<false, 32>(p, part, k, v, s);
 }
 
 } // namespace ra

@@ -1,0 +1,706 @@
+// k_paged_rows.cu -- attention over a paged cache for many query rows per kv
+// head at D = 128: the shared prefix of a batch, and chunks of a prompt; bf16
+// queries.  The rows are the M side of the tensor-core products.
+//
+// With hundreds of rows on the same keys the bound is the tensor pipe (4 D
+// operations per row and key) and, nearly level with it, the exponents.  An
+// item is 256 rows of one kv head -- query heads, draft tokens and, for the
+// prefix, sequences side by side -- as two tiles of 128 that share every K and
+// V tile: while one tile's softmax runs, the pipe computes the other's
+// products (PV_A(g), S_A(g+1), PV_B(g), S_B(g+1)); a thread owns a row, and P
+// goes back to TMEM over the S it came from.
+//
+//   warps 0-3, 4-7  softmax of tiles A and B; they also gather the rows of Q
+//                   into shared memory and store the results
+//   warps 8-11      8-bit caches: widen K and V tiles to f16.  16-bit caches:
+//                   clear the values behind a sequence's end
+//   warp 12         loads (a lane per page); warp 13 issues the products
+// TMEM: S_A [0,128), S_B [128,256), O_A [256,384), O_B [384,512).
+//
+// 8-bit caches: codes times a power of two are exact in f16, so a key becomes
+// code * 2^(e - E) with E the largest exponent of its 64-key half tile, which
+// then scales that half's logits as one number; a value becomes
+// code * 2^(e_v - EV), EV one exponent for the whole segment (raised, and O
+// rescaled, when a tile's largest passes it by 2^7; f16 holds 448 * 2^7).
+// What f16 loses is below 2^-33 of the largest.  The rows of Q are scaled by a
+// power of two into f16's range, and P is f16 (2^-11 relative), times 2^7 so
+// that weights down to 2^-21 of the largest keep all bits.  Widening costs
+// 1.6 instructions per pair and 96 KB of shared-memory traffic per tile of
+// 2048 tensor cycles; the alternative, e4m3 terms for P as the M side of the
+// few-row kernel uses, has no room in a compute-bound loop.
+// 16-bit caches: the tiles go to the products as they are, P is bf16 (2^-8).
+// Logits, maxima, sums and O are fp32.
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include <atomic>
+
+#include "ra_paged.cuh"
+#include "ra_sched.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kKeys = 128, kHalf = 64, kD = 128;
+constexpr int kThreads = 512;
+constexpr int kWideWarp0 = 8, kLoadWarp = 12, kMmaWarp = 13;
+constexpr float kLazy = 8.f;
+// setmaxnreg split: 256 x 184 + 128 x 64 + 128 x 80 = 65536 = 512 x 128
+constexpr int kLaunchRegs = 128;
+constexpr uint32_t kSoftRegs = 184, kWideRegs = 64, kSideRegs = 80;
+static_assert(256 * kSoftRegs + 128 * kWideRegs + 128 * kSideRegs <= kThreads * kLaunchRegs,
+              "register split exceeds the block's launch registers");
+
+template <bool FP8>
+struct Cfg {
+    static constexpr int kMat = kKeys * kD * 2; // a 16-bit tile, 32 KB: two blocks of 128 rows x 128 bytes
+    static constexpr int kRaw = kHalf * kD;     // half a tile of codes
+    static constexpr int kRaws = FP8 ? 4 : 0;   // K low, K high, V low, V high of a tile, in turn
+    static constexpr int kQOff = 0;
+    static constexpr int kKOff = 2 * kMat;
+    static constexpr int kVOff = kKOff + 2 * kMat;
+    static constexpr int kRawOff = kVOff + 2 * kMat;
+    static constexpr int kExpOff = kRawOff + kRaws * kRaw; // 64 scale bytes per half
+    static constexpr int kBarOff = kExpOff + kRaws * kHalf;
+    // k_full[2], k_empty[2], v_full[2], v_empty[2], raw_full[4], raw_empty[4],
+    // q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], v_clear[2], drain
+    static constexpr int kNumBars = 8 + 8 + 12 + 1;
+    static constexpr int kMiscOff = kBarOff + kNumBars * 8 + 8;
+    static constexpr int kScaleOff = kMiscOff + 16; // E of K half tiles [4][2], EV of V tiles [2]
+    static constexpr int kSmem = kScaleOff + 48 + 1024;
+    static_assert(kSmem <= 232448 && kMiscOff % 16 == 0, "shared memory");
+    static constexpr uint32_t kFmt = FP8 ? 0u : (1u << 7) | (1u << 10); // f16 or bf16 operands
+    static constexpr uint32_t kIdescS = (1u << 4) | kFmt | (128u >> 3 << 17) | (128u >> 4 << 24);
+    static constexpr uint32_t kIdescO = kIdescS | (1u << 16); // V is MN-major
+    static constexpr float kPBias = FP8 ? 7.f : 0.f;
+};
+
+struct Bars {
+    uint64_t *k_full, *k_empty, *v_full, *v_empty, *raw_full, *raw_empty, *q_full, *s_full, *p_half, *p_full, *o_full,
+        *v_clear, *drain;
+};
+
+template <class C>
+__device__ __forceinline__ Bars carve(uint8_t *smem)
+{
+    Bars b;
+    b.k_full = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
+    b.k_empty = b.k_full + 2;
+    b.v_full = b.k_empty + 2;
+    b.v_empty = b.v_full + 2;
+    b.raw_full = b.v_empty + 2;
+    b.raw_empty = b.raw_full + 4;
+    b.q_full = b.raw_empty + 4;
+    b.s_full = b.q_full + 2;
+    b.p_half = b.s_full + 2;
+    b.p_full = b.p_half + 2;
+    b.o_full = b.p_full + 2;
+    b.v_clear = b.o_full + 2;
+    b.drain = b.v_clear + 2;
+    return b;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint8_t *dst, const void *tmap, uint64_t *bar, int c0, int c1, int c2)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+template <bool FP8>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi)
+{
+    if (!FP8) return pack_bf16x2(lo, hi);
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// 2^(b - e) of a scale byte b as a pair of halves; NaN for a row without a value
+__device__ __forceinline__ __half2 half_scale(uint32_t b, int e)
+{
+    const int d = (int)b - e;
+    return __float2half2_rn(b == 255u ? __uint_as_float(0x7fc00000u) : d < -126 ? 0.f : __uint_as_float((uint32_t)(127 + d) << 23));
+}
+
+// Rows [row0, row0 + 64) of a 16-bit tile from half a tile of codes, by 4
+// warps.  A thread takes 16 codes: lanes 0-3 of a group of 8 a row's four
+// chunks, lanes 4-7 those of the row 5 apart (by exclusive or), which puts the
+// eight 16-byte accesses of a shared-memory phase on different banks both in
+// the codes (one 128-byte row, chunks permuted by the row) and in the f16 tile
+// (two per chunk).  Rows from `valid` on become 0.
+__device__ __forceinline__ void widen_half(uint32_t tile, uint32_t raw, const uint8_t *exps, int row0, int valid, int e,
+                                           int warp, int lane)
+{
+    const int x = lane & 3, in8 = (lane >> 3) ^ (lane & 4 ? 5 : 0);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int j = (warp * 2 + (it >> 1)) * 8 + in8; // row of the half tile
+        const int c = (it & 1) * 4 + x;                 // its chunk of codes
+        const uint4 w = lds128(raw + j * 128 + ((c ^ (j & 7)) << 4));
+        const __half2 s = half_scale(exps[j], e);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+            const uint32_t h = e4m3x2_to_f16x2(y & 1 ? u[y >> 1] >> 16 : u[y >> 1] & 0xffffu);
+            const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&h), s);
+            o[y] = row0 + j < valid ? *reinterpret_cast<const uint32_t *>(&r) : 0u;
+        }
+        const uint32_t at = tile + (it & 1) * (kKeys * 128) + (row0 + j) * 128;
+        sts128(at + (((2 * x) ^ (j & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+        sts128(at + (((2 * x + 1) ^ (j & 7)) << 4), make_uint4(o[4], o[5], o[6], o[7]));
+    }
+}
+
+// The largest scale byte of rows below `valid` that have a value (0: none).
+__device__ __forceinline__ int top_exp(const uint8_t *exps, int valid, int lane)
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        const int j = lane + 32 * y;
+        const uint32_t b = exps[j];
+        if (j < valid && b != 255u) top = max(top, b);
+    }
+    return (int)__reduce_max_sync(0xffffffffu, top);
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      PagedProblem p, PagedPart part)
+{
+    using C = Cfg<FP8>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const Bars bars = carve<C>(smem);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::kMiscOff);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kMiscOff + 4);
+    const WaitCtx ctx{abort_flag, p.status, p.timeout_ns};
+    // E by tile mod 4 and half: tile g + 4 is widened only after P V of tile
+    // g + 1, which both softmaxes of g precede; EV by V buffer
+    volatile int *k_scale = reinterpret_cast<volatile int *>(smem + C::kScaleOff);
+    volatile int *v_scale = k_scale + 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bars.k_full + s, FP8 ? 128 : 1);
+            mbar_init(bars.k_empty + s, 1);
+            mbar_init(bars.v_full + s, FP8 ? 128 : 1);
+            mbar_init(bars.v_empty + s, 1);
+            mbar_init(bars.q_full + s, 128);
+            mbar_init(bars.s_full + s, 1);
+            mbar_init(bars.p_half + s, 128);
+            mbar_init(bars.p_full + s, 128);
+            mbar_init(bars.o_full + s, 1);
+            mbar_init(bars.v_clear + s, 128);
+        }
+        for (int s = 0; s < 4; ++s) {
+            mbar_init(bars.raw_full + s, 1);
+            mbar_init(bars.raw_empty + s, 128);
+        }
+        mbar_init(bars.drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(tmem_holder, 512);
+        tmem_relinquish();
+    }
+    if (warp == kLoadWarp && lane == 0) {
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
+    report_lengths(p, part);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctx)) != 0;
+    };
+    auto source_len = [&](int b) { return part.prefix ? paged_prefix_len(p) : paged_kv_len(p, b); };
+    // an item with at most 128 rows has no tile B
+    auto two_tiles = [&](const PagedCursor &c) { return part.rows - c.rb * part.row_block > 128; };
+    PagedCursor c;
+    const bool any = cursor_begin(p, part, blockIdx.x, c);
+
+    if (warp >= kLoadWarp) {
+        regs_shrink<kSideRegs>();
+        if (any && warp == kLoadWarp) {
+            // ------------------------------------------------------------ loads
+            // lane x fetches box x of a half tile (codes) or of a tile
+            constexpr int kPart = FP8 ? kHalf : kKeys, kParts = kKeys / kPart;
+            const int box = min(p.c.page, kPart), per = kPart / box;
+            uint32_t g = 0;
+            bool ok = true;
+            for (;;) {
+                const int n = cursor_take(c), len = source_len(c.b);
+                for (int t = c.t0; ok && t < c.t0 + n; ++t, ++g) {
+                    // page entries of the tile: lane x of half y
+                    int page[kParts];
+#pragma unroll
+                    for (int y = 0; y < kParts; ++y) {
+                        const int first = t * kKeys + y * kPart + lane * box;
+                        page[y] = lane < per && first < len ? page_entry(p, part, c.b, first) : 0;
+                    }
+#pragma unroll
+                    for (int m = 0; m < 2 && ok; ++m) {
+#pragma unroll
+                        for (int y = 0; y < kParts && ok; ++y) {
+                            const int first = t * kKeys + y * kPart;
+                            const int boxes = max(0, (min(len - first, kPart) + box - 1) / box);
+                            const bool mine = lane < boxes, good = mine && page_valid(p, page[y]);
+                            const int z = good ? page[y] * p.c.Hkv + c.h : p.c.n_pages * p.c.Hkv; // out of range: zeros
+                            const int off = (first + lane * box) & (p.c.page - 1);
+                            if (FP8) {
+                                const int st = 2 * m + y;
+                                if (!(ok = wait_all(bars.raw_empty + st, (g & 1) ^ 1))) break;
+                                uint8_t *e = smem + C::kExpOff + st * kHalf + lane * box;
+                                const int n_good = __popc(__ballot_sync(0xffffffffu, good));
+                                if (mine && !good) { // zeros, at a scale of one
+                                    for (int j = 0; j < box; ++j) e[j] = 127;
+                                    proxy_fence();
+                                }
+                                __syncwarp();
+                                if (lane == 0) mbar_expect_tx(bars.raw_full + st, boxes * box * kD + n_good * box);
+                                __syncwarp();
+                                if (mine)
+                                    tma_load_3d(smem + C::kRawOff + st * C::kRaw + lane * box * 128, m ? &tm_v : &tm_k,
+                                                bars.raw_full + st, 0, off, z);
+                                if (good)
+                                    bulk_load(e, (m ? p.c.v_exp : p.c.k_exp) + ((size_t)z << p.c.page_shift) + off, box,
+                                              bars.raw_full + st);
+                            } else {
+                                const int st = g & 1;
+                                if (!(ok = wait_all((m ? bars.v_empty : bars.k_empty) + st, ((g >> 1) & 1) ^ 1))) break;
+                                uint64_t *full = (m ? bars.v_full : bars.k_full) + st;
+                                if (lane == 0) mbar_expect_tx(full, boxes * box * kD * 2);
+                                __syncwarp();
+                                uint8_t *dst = smem + (m ? C::kVOff : C::kKOff) + st * C::kMat + lane * box * 128;
+                                if (mine)
+                                    for (int hf = 0; hf < 2; ++hf)
+                                        tma_load_3d(dst + hf * (kKeys * 128), m ? &tm_v : &tm_k, full, hf * 64, off, z);
+                            }
+                        }
+                    }
+                }
+                if (!ok || !cursor_next(p, part, c, n)) break;
+            }
+            if (!ok) {
+                // copies on their way land before the CTA ends (a phase that
+                // passed already, or was not begun, only runs the clock)
+                for (int s = 0; s < (FP8 ? 4 : 2); ++s)
+                    for (uint32_t x = 0; x < 2 && x <= g; ++x) {
+                        const uint32_t ph = FP8 ? (g - x) & 1 : ((g - x) >> 1) & 1;
+                        if (FP8) {
+                            wait_drain(bars.raw_full + s, ph, kDrainNs);
+                        } else {
+                            wait_drain(bars.k_full + s, ph, kDrainNs);
+                            wait_drain(bars.v_full + s, ph, kDrainNs);
+                        }
+                    }
+            }
+        } else if (any && warp == kMmaWarp) {
+            // ------------------------------------------------------------ products
+            const uint64_t qd0 = sdesc_sw128(smem_u32(smem + C::kQOff), 16, 1024);
+            const uint64_t kd0 = sdesc_sw128(smem_u32(smem + C::kKOff), 16, 1024);
+            const uint64_t vd0 = sdesc_sw128(smem_u32(smem + C::kVOff), kKeys * 128, 1024);
+            constexpr uint32_t kStep = C::kMat >> 4;
+            uint32_t g = 0, segs = 0, parts_b = 0;
+            bool ok = true;
+            auto issue_s = [&](int x, uint32_t j) {
+                const uint64_t qd = qd0 + (uint32_t)(x * kStep), kd = kd0 + (j & 1) * kStep;
+#pragma unroll
+                for (int kk = 0; kk < kD / 16; ++kk) {
+                    const uint32_t o = ((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) >> 4;
+                    mma_ss_w(tmem + x * 128, qd + o, kd + o, C::kIdescS, kk > 0 ? 1u : 0u);
+                }
+                tc_commit_w(bars.s_full + x);
+            };
+            auto issue_pv = [&](int x, uint32_t j, uint32_t ph, bool first) -> bool {
+                const uint64_t vd = vd0 + (j & 1) * kStep;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    // keys 0-63 as soon as their weights are in TMEM
+                    if (!wait_all((hf ? bars.p_full : bars.p_half) + x, ph)) return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k4 = 0; k4 < 4; ++k4) {
+                        const int kk = hf * 4 + k4;
+                        mma_ts_w(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, vd + (uint32_t)((kk * 2048) >> 4), C::kIdescO,
+                                 (kk > 0 || !first) ? 1u : 0u);
+                    }
+                }
+                return true;
+            };
+            for (;;) {
+                const int n = cursor_take(c);
+                const bool both = two_tiles(c);
+                // first S products of the segment
+                if (!(ok = wait_all(bars.q_full + 0, segs & 1))) break;
+                if (!(ok = wait_all(bars.q_full + 1, segs & 1))) break;
+                ++segs;
+                if (!(ok = wait_all(bars.k_full + (g & 1), (g >> 1) & 1))) break;
+                tc_fence_after();
+                issue_s(0, g);
+                if (both) issue_s(1, g);
+                tc_commit_w(bars.k_empty + (g & 1));
+                for (int t = 0; t < n; ++t, ++g) {
+                    const bool more = t + 1 < n;
+                    if (!(ok = wait_all((FP8 ? bars.v_full : bars.v_clear) + (g & 1), (g >> 1) & 1))) break;
+                    if (!(ok = issue_pv(0, g, g & 1, t == 0))) break;
+                    if (!more) tc_commit_w(bars.o_full + 0);
+                    if (more) {
+                        if (!(ok = wait_all(bars.k_full + ((g + 1) & 1), ((g + 1) >> 1) & 1))) break;
+                        tc_fence_after();
+                        issue_s(0, g + 1);
+                    }
+                    if (both) {
+                        if (!(ok = issue_pv(1, g, parts_b++ & 1, t == 0))) break;
+                        if (!more) tc_commit_w(bars.o_full + 1);
+                    }
+                    tc_commit_w(bars.v_empty + (g & 1));
+                    if (more) {
+                        if (both) issue_s(1, g + 1);
+                        tc_commit_w(bars.k_empty + ((g + 1) & 1));
+                    }
+                }
+                if (!ok || !cursor_next(p, part, c, n)) break;
+            }
+            tc_commit_w(bars.drain);
+            wait_drain(bars.drain, 0, kDrainNs);
+        }
+    } else if (warp >= kWideWarp0) {
+        regs_shrink<kWideRegs>();
+        // ---------------------------------------------------------------- tiles
+        const int w = warp - kWideWarp0;
+        uint32_t g = 0;
+        bool ok = true;
+        while (any && ok) {
+            const int n = cursor_take(c), len = source_len(c.b);
+            int ev = -1; // EV of the segment
+            for (int t = c.t0; ok && t < c.t0 + n; ++t, ++g) {
+                const int valid = min(len - t * kKeys, kKeys), st = g & 1;
+                if (!FP8) {
+                    // values behind the length: whatever is there, weight 0 must give 0
+                    if (!(ok = wait_all(bars.v_full + st, (g >> 1) & 1))) break;
+                    const int j = threadIdx.x - kWideWarp0 * 32;
+                    if (j >= valid)
+                        for (int x = 0; x < 16; ++x)
+                            sts128(smem_u32(smem + C::kVOff + st * C::kMat) + (x >> 3) * (kKeys * 128) + j * 128 + (x & 7) * 16,
+                                   make_uint4(0, 0, 0, 0));
+                    if (valid < kKeys) proxy_fence();
+                    mbar_arrive(bars.v_clear + st);
+                    continue;
+                }
+                const uint8_t *ex = smem + C::kExpOff;
+                const uint32_t raw = smem_u32(smem + C::kRawOff);
+                if (!(ok = wait_all(bars.k_empty + st, ((g >> 1) & 1) ^ 1))) break;
+                for (int y = 0; y < 2; ++y) {
+                    if (!(ok = wait_all(bars.raw_full + y, g & 1))) break;
+                    const int e = max(top_exp(ex + y * kHalf, valid - y * kHalf, lane), 1);
+                    widen_half(smem_u32(smem + C::kKOff + st * C::kMat), raw + y * C::kRaw, ex + y * kHalf, y * kHalf, valid, e, w,
+                               lane);
+                    if (w == 0 && lane == 0) k_scale[(g & 3) * 2 + y] = e;
+                    mbar_arrive(bars.raw_empty + y);
+                }
+                if (!ok) break;
+                proxy_fence();
+                mbar_arrive(bars.k_full + st);
+                if (!(ok = wait_all(bars.v_empty + st, ((g >> 1) & 1) ^ 1))) break;
+                if (!(ok = wait_all(bars.raw_full + 2, g & 1))) break;
+                if (!(ok = wait_all(bars.raw_full + 3, g & 1))) break;
+                const int e = max(top_exp(ex + 2 * kHalf, valid, lane), top_exp(ex + 3 * kHalf, valid - kHalf, lane));
+                // 448 * 2^7 is the most that f16 holds; rows without a value do not count
+                if (ev < 0 || e > ev + 7) ev = max(e, 1);
+                for (int y = 0; y < 2; ++y) {
+                    widen_half(smem_u32(smem + C::kVOff + st * C::kMat), raw + (2 + y) * C::kRaw, ex + (2 + y) * kHalf, y * kHalf,
+                               valid, ev, w, lane);
+                    mbar_arrive(bars.raw_empty + 2 + y);
+                }
+                if (w == 0 && lane == 0) v_scale[st] = ev;
+                proxy_fence();
+                mbar_arrive(bars.v_full + st);
+            }
+            if (!ok || !cursor_next(p, part, c, n)) break;
+        }
+    } else {
+        regs_grow<kSoftRegs>();
+        // ---------------------------------------------------------------- softmax
+        const int x = warp >> 2; // tile A or B
+        const int row_in = (warp & 3) * 32 + lane;
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const float cap2 = p.soft_cap * kLog2e, to_cap = p.soft_cap > 0.f ? kLn2 / p.soft_cap : 0.f;
+        uint32_t g = 0, gx = 0, segs = 0;
+        bool ok = true;
+        while (any && ok) {
+            const int n = cursor_take(c), len = source_len(c.b);
+            const PagedRow row = paged_row(p, part, c, x * 128 + row_in);
+            const bool mine = x == 0 || two_tiles(c); // uniform in the warpgroup
+            const int hq = c.h * p.G + row.g;
+            const size_t place = ((size_t)row.b * p.Lq + row.i) * p.Hq + hq;
+            const int limit = row.counts ? row.limit : 0x7fffffff; // rows of no use need no mask
+            // ---- this thread's row of Q
+            float a_row = p.scale * kLog2e;
+            if (mine) {
+                const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + place * kD);
+                const uint32_t at = smem_u32(smem + C::kQOff + x * C::kMat) + row_in * 128;
+                float inv = 1.f;
+                if (FP8) {
+                    uint32_t top = 0; // largest magnitude, as bf16 bits
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) {
+                        const uint4 u = row.counts ? q[y] : make_uint4(0, 0, 0, 0);
+                        const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) top = max(top, max(v[k] & 0x7fffu, (v[k] >> 16) & 0x7fffu));
+                    }
+                    const int e = top == 0 ? 0 : min(max((int)(top >> 7) - 127, -120), 120);
+                    inv = __uint_as_float((uint32_t)(127 - e) << 23);
+                    a_row *= __uint_as_float((uint32_t)(127 + e) << 23);
+                }
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {
+                    uint4 u = row.counts ? q[y] : make_uint4(0, 0, 0, 0);
+                    if (FP8) {
+                        uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            v[k] = pack16<true>(__uint_as_float(v[k] << 16) * inv, __uint_as_float(v[k] & 0xffff0000u) * inv);
+                        u = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                    sts128(at + (y >> 3) * (kKeys * 128) + (((y & 7) ^ (row_in & 7)) << 4), u);
+                }
+                proxy_fence();
+            }
+            mbar_arrive(bars.q_full + x);
+            const int all = __reduce_min_sync(0xffffffffu, limit);
+
+            float m = -INFINITY, l = 0.f;
+            int ev = 0;
+            for (int t = c.t0; mine && ok && t < c.t0 + n; ++t) {
+                const uint32_t gt = g + (t - c.t0); // the tile's number in this CTA
+                const int st = gt & 1;
+                const int first = t * kKeys, seen = min(limit, len) - first; // keys of the tile that the row sees
+                const bool masked = min(all, len) < first + kKeys;
+                if (!(ok = wait_all(bars.s_full + x, gx & 1))) break;
+                tc_fence_after();
+                float s[128];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tmem_ld32(lane_base + x * 128 + k * 32, s + 32 * k);
+                float am[2] = {a_row, a_row};
+                float fv = 1.f;
+                if (FP8) {
+                    // the tile's values are wide by now or soon: P V waits for them anyway
+                    if (!(ok = wait_all(bars.v_full + st, (gt >> 1) & 1))) break;
+                    am[0] *= __uint_as_float((uint32_t)k_scale[(gt & 3) * 2] << 23);
+                    am[1] *= __uint_as_float((uint32_t)k_scale[(gt & 3) * 2 + 1] << 23);
+                    const int e = v_scale[st];
+                    if (t == c.t0) ev = e;
+                    if (e != ev) fv = ex2_approx((float)(ev - e));
+                    ev = e;
+                }
+                tmem_ld_wait();
+                if (to_cap > 0.f) {
+                    float xa = 0.f;
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        float t4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int j = 0; j < 64; j += 8)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                t4[k] = max3(t4[k], fabsf(s[hf * 64 + j + 2 * k]), fabsf(s[hf * 64 + j + 2 * k + 1]));
+                        xa = fmaxf(xa, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * am[hf] * to_cap);
+                    }
+                    if (__all_sync(0xffffffffu, xa < kTanhSmall)) {
+                        // the odd series, two lanes per instruction: 3.4e-7 relative
+                        const float2 d7 = make_float2(cap2 * kTanhC7, cap2 * kTanhC7), d5 = make_float2(cap2 * kTanhC5, cap2 * kTanhC5);
+                        const float2 d3 = make_float2(cap2 * kTanhC3, cap2 * kTanhC3), d1 = make_float2(cap2, cap2);
+#pragma unroll
+                        for (int j = 0; j < 128; j += 2) {
+                            const float k1 = am[j >> 6] * to_cap;
+                            const float2 xx = fmul2(make_float2(s[j], s[j + 1]), make_float2(k1, k1));
+                            const float2 x2 = fmul2(xx, xx);
+                            const float2 r = fmul2(xx, ffma2(x2, ffma2(x2, ffma2(x2, d7, d5), d3), d1));
+                            s[j] = r.x;
+                            s[j + 1] = r.y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 128; ++j) s[j] = cap2 * tanh_fast(s[j] * (am[j >> 6] * to_cap));
+                    }
+                    am[0] = am[1] = 1.f;
+                }
+                if (masked) {
+#pragma unroll
+                    for (int j = 0; j < 128; ++j)
+                        if (j >= seen) s[j] = -INFINITY;
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    float mx[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float *v = s + hf * 64 + k;
+                        mx[k] = max3(v[0], v[4], v[8]);
+#pragma unroll
+                        for (int j = 12; j < 60; j += 8) mx[k] = max3(mx[k], v[j], v[j + 4]);
+                        mx[k] = fmaxf(mx[k], v[60]);
+                    }
+                    // am > 0, so scaling commutes with the maximum
+                    top = fmaxf(top, am[hf] * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                }
+                const float m_new = fmaxf(m, top);
+                const bool need = m_new > m + kLazy; // also a first maximum
+                if (__any_sync(0xffffffffu, need) || fv != 1.f) {
+                    const float f = !need ? 1.f : m == -INFINITY ? 0.f : ex2_approx(m - m_new);
+                    l *= f;
+                    if (need) m = m_new;
+                    if (t > c.t0) {
+                        // S of this tile completed after P V of the one before
+                        const float fo = f * fv;
+#pragma unroll 1
+                        for (int k = 0; k < 4; ++k) {
+                            float o[32];
+                            tmem_ld32(lane_base + 256 + x * 128 + k * 32, o);
+                            tmem_ld_wait();
+                            uint32_t u[32];
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(o[j] * fo);
+                            tmem_st32(lane_base + 256 + x * 128 + k * 32, u);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                const float base = (m == -INFINITY ? 0.f : m) - C::kPBias;
+                const float2 nm = make_float2(-base, -base);
+                float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const float2 a2 = make_float2(am[hf], am[hf]);
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int j = 0; j < 64; j += 2) {
+                        const float2 y = ffma2(make_float2(s[hf * 64 + j], s[hf * 64 + j + 1]), a2, nm);
+                        const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                        ls[(j >> 1) & 3] = fadd2(ls[(j >> 1) & 3], e);
+                        pk[j >> 1] = pack16<FP8>(e.x, e.y);
+                    }
+                    // over columns of S that this thread has read
+                    tmem_st32(lane_base + x * 128 + hf * 32, pk);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive((hf ? bars.p_full : bars.p_half) + x);
+                }
+                const float2 l2 = fadd2(fadd2(ls[0], ls[1]), fadd2(ls[2], ls[3]));
+                l += l2.x + l2.y;
+                ++gx;
+            }
+            g += n;
+            if (!ok) break;
+            // ---- the segment's end: this row's result
+            if (mine) {
+                if (!(ok = wait_all(bars.o_full + x, segs & 1))) break;
+                ++segs;
+                tc_fence_after();
+                float mr = m - C::kPBias; // l and O are relative to 2^mr
+                const float fv = FP8 ? __uint_as_float((uint32_t)ev << 23) : 1.f;
+                const bool final = stores_whole(part, c, n);
+                const size_t at = slot_row(part, c) + x * 128 + row_in;
+                float f = fv;
+                if (final) {
+                    if (p.sinks && row.counts) {
+                        const float sink = p.sinks[hq] * kLog2e, top = fmaxf(mr, sink);
+                        f *= ex2_approx(mr - top);
+                        l = l * ex2_approx(mr - top) + ex2_approx(sink - top);
+                        mr = top;
+                    }
+                    f = l == 0.f ? 0.f : f / l;
+                }
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    float o[32];
+                    tmem_ld32(lane_base + 256 + x * 128 + k * 32, o);
+                    tmem_ld_wait();
+                    if (row.counts && final) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + place * kD + k * 32);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            dst[j] = make_uint4(pack_bf16x2(o[8 * j] * f, o[8 * j + 1] * f), pack_bf16x2(o[8 * j + 2] * f, o[8 * j + 3] * f),
+                                                pack_bf16x2(o[8 * j + 4] * f, o[8 * j + 5] * f), pack_bf16x2(o[8 * j + 6] * f, o[8 * j + 7] * f));
+                    } else if (row.counts) {
+                        float4 *dst = reinterpret_cast<float4 *>(part.o + at * kD + k * 32);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            dst[j] = make_float4(o[4 * j] * f, o[4 * j + 1] * f, o[4 * j + 2] * f, o[4 * j + 3] * f);
+                    }
+                    __syncwarp(); // the next read of TMEM is the whole warp's
+                }
+                tc_fence_before();
+                if (row.counts) {
+                    if (final)
+                        p.lse[((size_t)row.b * p.Hq + hq) * p.Lq + row.i] = l == 0.f ? -INFINITY : (mr + log2f(l)) * kLn2;
+                    else
+                        *reinterpret_cast<float2 *>(part.ml + at * 2) = make_float2(mr, l);
+                }
+            }
+            if (!cursor_next(p, part, c, n)) break;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <bool FP8>
+cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s)
+{
+    auto kern = paged_rows_kernel<FP8>;
+    static std::atomic<uint64_t> set{0}; // devices whose copy of the kernel has its attribute
+    const uint64_t bit = 1ull << p.device;
+    if (!(set.load(std::memory_order_acquire) & bit)) {
+        cudaFuncAttributes fa;
+        cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+        if (e != cudaSuccess) return e;
+        // the setmaxnreg split draws on the registers the block is launched with
+        if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<FP8>::kSmem);
+        if (e != cudaSuccess) return e;
+        set.fetch_or(bit, std::memory_order_release);
+    }
+    kern<<<part.ctas, kThreads, Cfg<FP8>::kSmem, s>>>(k, v, p, part);
+    return cudaGetLastError();
+}
+
+} // namespace
+
+cudaError_t launch_paged_rows(const PagedProblem &p, const PagedPart &part, int cache_dtype, const void *tm_k,
+                              const void *tm_v, cudaStream_t s)
+{
+    const CUtensorMap &k = *static_cast<const CUtensorMap *>(tm_k), &v = *static_cast<const CUtensorMap *>(tm_v);
+    return cache_dtype == RA_E4M3 ? go<true>(p, part, k, v, s) : go<false>(p, part, k, v, s);
+}
+
+} // namespace ra

@@ -2,19 +2,22 @@
 // spread of the work over CTAs, the numbering of partial results, and the
 // cached rows' scales.
 //
-// Work.  A source's keys are cut into tiles of `tile` tokens; an item is a
-// tile of one (sequence, row block, kv head).  All items lie on one line --
-// sequences in order, in each its row blocks, in each its kv heads, in each
-// its tiles -- and CTA c of C takes the c-th share of ceil(N / C) of them.
-// Shares are equal whatever the lengths are, and lengths stay on the device:
-// every CTA adds up the lengths of the batch itself (B integers out of L2)
-// to find where its share begins.  A segment is the run of items of one
-// (sequence, row block, kv head).
+// Work.  A source's keys are cut into tiles of `tile` tokens; a segment is the
+// run of tiles of one (sequence, row block, kv head).  All segments lie on one
+// line -- sequences in order, in each its row blocks, in each its kv heads --
+// each as `seg_cost` empty places (what taking up a segment costs, in tiles)
+// and then its tiles, and CTA c of C takes the c-th share of ceil(N / C)
+// places.  Shares cost about the same whatever the lengths are, and lengths
+// stay on the device: every CTA adds up the lengths of the batch itself (B
+// integers out of L2) to find where its share begins.
 //
-// Partial results.  CTA c's part of segment s goes to slot c + s: along the
-// line both numbers only grow, and each new (CTA, segment) pair raises at
-// least one of them, so no two pairs share a slot, and C + S slots are
-// enough.  The join finds a segment's slots from the same sums.
+// Partial results.  Where whole segments are stored by the CTA that has them
+// (`direct`), a CTA leaves at most two partial results, of the first and the
+// last segment of its share: slots 2c and 2c + 1.  Otherwise CTA c's part of
+// segment s goes to slot c + s: along the line both numbers only grow, and
+// each new (CTA, segment) pair raises at least one of them, so no two pairs
+// share a slot, and C + S slots are enough.  The join finds a segment's slots
+// from the same sums.
 #pragma once
 
 #include "ra_device.cuh"
@@ -62,48 +65,68 @@ __device__ __forceinline__ int own_tiles(const PagedProblem &p, const PagedPart 
     return (paged_kv_len(p, b) + part.tile - 1) / part.tile;
 }
 
-// Sum of own_tiles over sequences [0, b_end), by one converged warp.
-__device__ __forceinline__ long long own_tiles_before(const PagedProblem &p, const PagedPart &part,
-                                                      int b_end)
+// Places on the line of one segment of sequence b.
+__device__ __forceinline__ int own_places(const PagedProblem &p, const PagedPart &part, int b)
 {
-    long long n = 0;
-    for (int b = threadIdx.x & 31; b < b_end; b += 32) n += own_tiles(p, part, b);
+    const int n = own_tiles(p, part, b);
+    return n ? n + part.seg_cost : 0;
+}
+
+// Sums of own_places over all sequences and, in `before`, over those below
+// `b_end`; by one converged warp.
+__device__ __forceinline__ long long own_places_sum(const PagedProblem &p, const PagedPart &part,
+                                                    int b_end, long long &before)
+{
+    long long n = 0, lo = 0;
+    for (int b = threadIdx.x & 31; b < p.B; b += 32) {
+        const int x = own_places(p, part, b);
+        n += x;
+        if (b < b_end) lo += x;
+    }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    for (int o = 16; o; o >>= 1) {
+        n += __shfl_xor_sync(0xffffffffu, n, o);
+        lo += __shfl_xor_sync(0xffffffffu, lo, o);
+    }
+    before = lo;
     return n;
 }
 
-// A cursor on the line of items, kept by every thread of a CTA alike.
+// A place on the line, kept by every thread of a CTA alike.
 struct PagedCursor {
-    long long at, end; // the CTA's share
-    int b, rb, h;      // the segment that `at` lies in
+    long long at, end; // place of the next tile; the end of the CTA's share
+    int b, rb, h;      // the segment
     int t0, tiles;     // its next tile, and its tiles
     long long seg;     // its number
+    bool first;        // the first of the share
 };
 
-// Places the cursor at CTA `cta`'s share.  Called by one converged warp (all
-// lanes get the result); false when the share is empty.
+// Places the cursor at CTA `cta`'s first tile.  Called by one converged warp
+// (all lanes get the result); false when the share has no tile.
 __device__ __forceinline__ bool cursor_begin(const PagedProblem &p, const PagedPart &part, int cta,
                                              PagedCursor &c)
 {
     const int per_seq = part.n_rb * p.c.Hkv; // segments of one sequence
     const int lane = threadIdx.x & 31;
-    const int prefix_tiles =
-        part.prefix ? (paged_prefix_len(p) + part.tile - 1) / part.tile : 0;
-    const long long total =
-        per_seq * (part.prefix ? (long long)prefix_tiles : own_tiles_before(p, part, p.B));
+    int prefix_tiles = 0;
+    long long total, before = 0;
+    if (part.prefix) {
+        prefix_tiles = (paged_prefix_len(p) + part.tile - 1) / part.tile;
+        total = prefix_tiles ? (long long)per_seq * (prefix_tiles + part.seg_cost) : 0;
+    } else {
+        total = own_places_sum(p, part, 0, before) * per_seq;
+    }
     const long long share = (total + part.ctas - 1) / part.ctas;
     c.at = share * cta;
     c.end = c.at + share < total ? c.at + share : total;
     if (c.at >= c.end) return false;
-    long long before = 0;
     c.b = 0;
     c.tiles = prefix_tiles;
     if (!part.prefix) {
         // 32 sequences at a time: the first whose running total passes `at`
         for (int b0 = 0;; b0 += 32) {
             const int b = b0 + lane;
-            const int n = b < p.B ? own_tiles(p, part, b) : 0;
+            const int n = b < p.B ? own_places(p, part, b) : 0;
             long long run = (long long)n * per_seq;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -112,21 +135,25 @@ __device__ __forceinline__ bool cursor_begin(const PagedProblem &p, const PagedP
             }
             const unsigned past = __ballot_sync(0xffffffffu, before + run > c.at);
             if (past) {
-                const int l = __ffs(past) - 1;
+                const int l = __ffs(past) - 1, places = __shfl_sync(0xffffffffu, n, l);
                 c.b = b0 + l;
-                c.tiles = __shfl_sync(0xffffffffu, n, l);
-                before += __shfl_sync(0xffffffffu, run, l) - (long long)c.tiles * per_seq;
+                c.tiles = places - part.seg_cost;
+                before += __shfl_sync(0xffffffffu, run, l) - (long long)places * per_seq;
                 break;
             }
             before += __shfl_sync(0xffffffffu, run, 31);
         }
     }
-    const int in_seq = (int)((c.at - before) / c.tiles);
-    c.t0 = (int)(c.at - before - (long long)in_seq * c.tiles);
+    const int places = c.tiles + part.seg_cost;
+    const int in_seq = (int)((c.at - before) / places);
+    const int off = (int)(c.at - before - (long long)in_seq * places);
+    c.t0 = off > part.seg_cost ? off - part.seg_cost : 0;
+    if (off < part.seg_cost) c.at += part.seg_cost - off;
     c.rb = in_seq / p.c.Hkv;
     c.h = in_seq - c.rb * p.c.Hkv;
     c.seg = (long long)c.b * per_seq + in_seq;
-    return true;
+    c.first = true;
+    return c.at < c.end;
 }
 
 // Tiles of the present segment that fall into the share.
@@ -137,14 +164,15 @@ __device__ __forceinline__ int cursor_take(const PagedCursor &c)
     return n < left ? n : (int)left;
 }
 
-// Moves past `n` tiles of the present segment (all that cursor_take gave);
-// false at the share's end.
+// Moves on to the segment after the `n` tiles that cursor_take gave; false at
+// the share's end.
 __device__ __forceinline__ bool cursor_next(const PagedProblem &p, const PagedPart &part,
                                             PagedCursor &c, int n)
 {
-    c.at += n;
+    c.at += n + part.seg_cost;
     if (c.at >= c.end) return false;
     c.t0 = 0;
+    c.first = false;
     ++c.seg;
     if (++c.h == p.c.Hkv) {
         c.h = 0;
@@ -158,6 +186,19 @@ __device__ __forceinline__ bool cursor_next(const PagedProblem &p, const PagedPa
         }
     }
     return true;
+}
+
+// The first row of the partial result of the present segment.
+__device__ __forceinline__ size_t slot_row(const PagedPart &part, const PagedCursor &c)
+{
+    const size_t slot = part.direct ? 2 * (size_t)blockIdx.x + (c.first ? 0 : 1) : (size_t)blockIdx.x + c.seg;
+    return slot * part.slot_rows;
+}
+
+// Whether this CTA has the whole segment and stores its rows itself.
+__device__ __forceinline__ bool stores_whole(const PagedPart &part, const PagedCursor &c, int n)
+{
+    return part.direct && c.t0 == 0 && n == c.tiles;
 }
 
 // Where query row `row` of an item's row block lies, and which of the

@@ -43,6 +43,8 @@ struct PagedPart {
     int n_rb;      // ceil(rows / row_block)
     int tile;      // keys of one tile
     int ctas;
+    int seg_cost;  // what taking up a segment costs, in tiles
+    int direct;    // 1: rows whose keys one CTA sees are stored by it
     int slot_rows; // rows that one partial result holds
     float *o;      // (slots, slot_rows, D) unnormalised outputs
     float *ml;     // (slots, slot_rows, 2) row maximum (base-2 logits) and sum
@@ -59,7 +61,7 @@ cudaError_t launch_kv_read(const PagedCache &c, int cache_dtype, const int32_t *
 // fp32 arithmetic throughout: the path of fp32 queries
 constexpr int kPagedF32Rows = 8, kPagedF32Tile = 32;
 cudaError_t launch_paged_f32(const PagedProblem &p, const PagedPart &part, int cache_dtype,
-                             bool direct, cudaStream_t s);
+                             cudaStream_t s);
 
 // bf16 queries, row_block 8 or 16: tensor cores fed from registers.  Keys of a
 // tile, and token rows of one TMA box, by head size, cache type and page size;
@@ -67,13 +69,19 @@ cudaError_t launch_paged_f32(const PagedProblem &p, const PagedPart &part, int c
 int paged_few_tile(int D, int cache_dtype);
 int paged_few_box(int D, int cache_dtype, int page);
 cudaError_t launch_paged_few(const PagedProblem &p, const PagedPart &part, int cache_dtype,
-                             const void *tm_k, const void *tm_v, bool direct, cudaStream_t s);
+                             const void *tm_k, const void *tm_v, cudaStream_t s);
 
 // bf16 queries, D = 128, row_block 8, 16 or 32: the keys as the M side of
 // tcgen05 products (boxes of min(page, 128) tokens)
 constexpr int kPagedKeysTile = 128;
 cudaError_t launch_paged_keys(const PagedProblem &p, const PagedPart &part, int cache_dtype,
-                              const void *tm_k, const void *tm_v, bool direct, cudaStream_t s);
+                              const void *tm_k, const void *tm_v, cudaStream_t s);
+
+// bf16 queries, D = 128, row_block 256: the rows as the M side (boxes of
+// min(page, 64) tokens of an 8-bit cache, min(page, 128) of a 16-bit one)
+constexpr int kPagedRowsTile = 128;
+cudaError_t launch_paged_rows(const PagedProblem &p, const PagedPart &part, int cache_dtype,
+                              const void *tm_k, const void *tm_v, cudaStream_t s);
 
 // joins the partial results of both sources (n_parts of them) into out, lse
 cudaError_t launch_paged_join(const PagedProblem &p, const PagedPart *parts, int n_parts, int dtype,

@@ -106,7 +106,7 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 // size does not depend on the device (GB300 has 152 SMs).
 constexpr int kSms = 152;
 
-enum { kF32, kFew, kKeysM };
+enum { kF32, kFew, kKeysM, kRowsM };
 
 struct Plan {
     PagedPart part[2];
@@ -127,23 +127,34 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
         a.rows = (k ? p->B * p->Lq : p->Lq) * G;
         if (p->dtype == RA_FP32) {
             kernel = kF32;
+            a.seg_cost = 1;
             a.row_block = kPagedF32Rows;
             a.tile = kPagedF32Tile;
             a.ctas = 4 * kSms;
+        } else if (c->D == 128 && a.rows > 32) {
+            kernel = kRowsM;
+            a.seg_cost = 3;
+            a.row_block = 256;
+            a.tile = kPagedRowsTile;
+            a.ctas = kSms;
         } else if (c->D == 128) {
             kernel = kKeysM;
+            a.seg_cost = 3;
             a.row_block = a.rows <= 8 ? 8 : a.rows <= 16 ? 16 : 32;
             a.tile = kPagedKeysTile;
             a.ctas = (c->dtype == RA_E4M3 ? 2 : 1) * kSms;
         } else {
             kernel = kFew;
+            a.seg_cost = 2;
             a.row_block = a.rows <= 8 ? 8 : 16;
             a.tile = paged_few_tile(c->D, c->dtype);
             a.ctas = 2 * kSms;
         }
         a.n_rb = (a.rows + a.row_block - 1) / a.row_block;
         a.slot_rows = a.rows < a.row_block ? a.rows : a.row_block;
-        const size_t slots = (size_t)a.ctas + (size_t)(k ? 1 : p->B) * a.n_rb * c->Hkv;
+        a.direct = p->prefix_pages == 0;
+        const size_t slots =
+            a.direct ? 2 * (size_t)a.ctas : (size_t)a.ctas + (size_t)(k ? 1 : p->B) * a.n_rb * c->Hkv;
         a.o = reinterpret_cast<float *>(ws + pl.bytes);
         pl.bytes += up256(slots * a.slot_rows * c->D * 4);
         a.ml = reinterpret_cast<float *>(ws + pl.bytes);
@@ -247,19 +258,22 @@ RA_API int ra_attn_paged(const ra_kv_cache *cache, const ra_paged_params *p, con
     x.device = d.index;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    CUtensorMap tm[2];
-    const bool direct = pl.n_parts == 1; // a row whose keys one CTA sees is stored by it
-    if (p->dtype == RA_BF16) {
-        const int rows = cache->D == 128 ? cache->page_size : paged_few_box(cache->D, cache->dtype, cache->page_size);
-        if ((rc = encode_paged(&tm[0], cache, cache->k, rows)) || (rc = encode_paged(&tm[1], cache, cache->v, rows)))
-            return rc;
+    for (int k = 0; k < pl.n_parts && e == cudaSuccess; ++k) {
+        const PagedPart &part = pl.part[k];
+        if (pl.kernel[k] == kF32) {
+            e = launch_paged_f32(x, part, cache->dtype, s);
+            continue;
+        }
+        const int most = pl.kernel[k] == kFew ? paged_few_box(cache->D, cache->dtype, cache->page_size)
+                         : pl.kernel[k] == kRowsM && cache->dtype == RA_E4M3 ? 64
+                                                                           : 128;
+        const int rows = cache->page_size < most ? cache->page_size : most;
+        CUtensorMap tk, tv;
+        if ((rc = encode_paged(&tk, cache, cache->k, rows)) || (rc = encode_paged(&tv, cache, cache->v, rows))) return rc;
+        e = pl.kernel[k] == kFew     ? launch_paged_few(x, part, cache->dtype, &tk, &tv, s)
+            : pl.kernel[k] == kKeysM ? launch_paged_keys(x, part, cache->dtype, &tk, &tv, s)
+                                     : launch_paged_rows(x, part, cache->dtype, &tk, &tv, s);
     }
-    for (int k = 0; k < pl.n_parts && e == cudaSuccess; ++k)
-        e = pl.kernel[k] == kF32
-                ? launch_paged_f32(x, pl.part[k], cache->dtype, direct, s)
-            : pl.kernel[k] == kFew
-                ? launch_paged_few(x, pl.part[k], cache->dtype, &tm[0], &tm[1], direct, s)
-                : launch_paged_keys(x, pl.part[k], cache->dtype, &tm[0], &tm[1], direct, s);
     if (e == cudaSuccess) e = launch_paged_join(x, pl.part, pl.n_parts, p->dtype, s);
     if (e != cudaSuccess) return set_cuda_error(e, "paged attention launch");
     count_launches(pl.n_parts + 1);
