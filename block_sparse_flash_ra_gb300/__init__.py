@@ -155,7 +155,7 @@ def lib():
             L.ra_get_device_status.argtypes = [vp]
             L.ra_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp, vp]
             L.ra_launch_count.restype = ctypes.c_uint64
-            KC, PP = ctypes.POINTER(RaKvCache), ctypes.POINTER(RaPagedParams)
+            KC = PP = vp  # RaKvCache, RaPagedParams: by reference or by address
             L.ra_kv_write.argtypes = [KC, vp, vp, ci, ci, ci, sz, sz, vp, ci, vp, vp, vp]
             L.ra_kv_read.argtypes = [KC, vp, ci, vp, ci, ci, vp, vp, ci, vp]
             L.ra_attn_paged_workspace_size.argtypes = [KC, PP]
@@ -425,33 +425,41 @@ def _need(ok, what):
 
 def _ints(x, shape, name, device):
     """int32 tensors that the kernels read: dense, on the cache's device."""
+    if x.dtype is torch.int32 and x.shape == shape and x.device == device and x.is_contiguous():
+        return
     if x.dtype != torch.int32:
         raise TypeError(f"{name} must be int32, not {x.dtype}")
-    _need(tuple(x.shape) == shape, f"{name} has shape {tuple(x.shape)}, not {shape}")
-    _need(x.is_contiguous() and x.device == device,
-          f"{name} must be contiguous and on the cache's device")
+    _need(x.shape == shape, f"{name} has shape {tuple(x.shape)}, not {shape}")
+    raise ValueError(f"{name} must be contiguous and on the cache's device")
 
 
 class _On:
     """Runs a helper's allocations and launches on the tensors' device and on the caller's
-    stream, so that what is allocated here is reused in that stream's order."""
+    stream, so that what is allocated here is reused in that stream's order.  ``with`` gives
+    the stream's handle."""
 
     def __init__(self, device, stream):
-        self.guards = []
-        if device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device)
-            self.guards.append(torch.cuda.stream(stream))
+        self.device, self.guards = device, ()
+        if stream is not None or device.index != torch.cuda.current_device():
+            self.guards = [torch.cuda.device(device)]
+            if stream is not None:
+                if isinstance(stream, int):
+                    stream = torch.cuda.ExternalStream(stream, device=device)
+                self.guards.append(torch.cuda.stream(stream))
 
     def __enter__(self):
         for g in self.guards:
             g.__enter__()
+        return _raw_stream(self.device.index)
 
     def __exit__(self, *e):
         for g in reversed(self.guards):
             g.__exit__(*e)
+
+
+def _raw_stream(index):
+    # the handle without a Stream object around it: a small call's time is mostly Python's
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def make_kv_cache(k, v, k_exp=None, v_exp=None) -> RaKvCache:
@@ -474,6 +482,9 @@ def make_kv_cache(k, v, k_exp=None, v_exp=None) -> RaKvCache:
     n, h, page, d = k.shape
     c = RaKvCache(n, page, h, d, _CACHE_DT[k.dtype], _ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp))
     c.k_pages, c.v_pages, c.k_exps, c.v_exps, c.device = k, v, k_exp, v_exp, k.device
+    c._row = (h, d)
+    c._sizes = (n, page, h, d, c.dtype)
+    c._ref = ctypes.addressof(c)
     return c
 
 
@@ -492,50 +503,52 @@ def new_kv_cache(n_pages, page_size, n_kv_heads, head_dim, dtype=torch.float8_e4
 
 
 def _token_stride(x, cache, name):
-    _need(x.dim() == 4 and tuple(x.shape[2:]) == (cache.Hkv, cache.D),
-          f"{name} must be (B, L, {cache.Hkv}, {cache.D})")
+    sh, st = x.shape, x.stride()
+    _need(len(sh) == 4 and sh[2:] == cache._row, f"{name} must be (B, L, {cache.Hkv}, {cache.D})")
     _need(x.device == cache.device, f"{name} must be on the cache's device")
-    B, L = x.shape[:2]
-    row = cache.Hkv * cache.D
-    st = x.stride(1) if L > 1 else (x.stride(0) if B > 1 else row)
-    _need(x.stride(3) == 1 and (cache.Hkv == 1 or x.stride(2) == cache.D)
-          and (B == 1 or x.stride(0) == L * st) and st >= row,
+    (B, L, H, D), row = sh, cache.Hkv * cache.D
+    step = st[1] if L > 1 else (st[0] if B > 1 else row)
+    _need(st[3] == 1 and (H == 1 or st[2] == D) and (B == 1 or st[0] == L * step) and step >= row,
           f"{name}: a token's heads must be contiguous, and tokens and batches evenly spaced")
-    return st
+    return step
 
 
 def kv_write(cache, k, v, page_table, start, count=None, stream=None) -> None:
     """Appends k, v (B, L, Hkv, D), bf16 or fp32, at positions start[b] + i of the sequences whose
     pages are in page_table (B, max_pages); of sequence b the first count[b] tokens (None: all).
     k and v may be slices along the head axis of a wider tensor."""
-    if k.dtype not in _DT or v.dtype != k.dtype:
+    dt = _DT.get(k.dtype)
+    if dt is None or v.dtype != k.dtype:
         raise TypeError(f"k and v must both be bfloat16 or float32, not {k.dtype} and {v.dtype}")
     _need(k.shape == v.shape, "k and v must have the same shape")
     ks, vs = _token_stride(k, cache, "k"), _token_stride(v, cache, "v")
     B, L = k.shape[:2]
     if B == 0 or L == 0:
         return
-    _ints(page_table, (B, page_table.shape[-1]), "page_table", cache.device)
+    pages = page_table.shape[-1]
+    _ints(page_table, (B, pages), "page_table", cache.device)
     _ints(start, (B,), "start", cache.device)
     if count is not None:
         _ints(count, (B,), "count", cache.device)
-    with _On(cache.device, stream):
-        ra_kv_write(cache, k, v, _DT[k.dtype], B, L, ks, vs, page_table, page_table.shape[1], start,
-                    count)
+    with _On(cache.device, stream) as s:
+        _check(lib().ra_kv_write(cache._ref, k.data_ptr(), v.data_ptr(), dt, B, L, ks, vs,
+                                 page_table.data_ptr(), pages, start.data_ptr(), _ptr(count), s))
 
 
 def kv_read(cache, page_table, kv_len, L, dtype=torch.bfloat16, stream=None):
     """k, v (B, L, Hkv, D) of the sequences' cached tokens; rows behind kv_len[b] are 0."""
-    if dtype not in _DT:
+    dt = _DT.get(dtype)
+    if dt is None:
         raise TypeError(f"unsupported dtype {dtype}")
-    B = page_table.shape[0]
-    _ints(page_table, (B, page_table.shape[-1]), "page_table", cache.device)
+    B, pages = page_table.shape[0], page_table.shape[-1]
+    _ints(page_table, (B, pages), "page_table", cache.device)
     _ints(kv_len, (B,), "kv_len", cache.device)
-    with _On(cache.device, stream):
-        k, v = (torch.empty((B, L, cache.Hkv, cache.D), dtype=dtype, device=cache.device)
+    with _On(cache.device, stream) as s:
+        k, v = (torch.empty((B, L) + cache._row, dtype=dtype, device=cache.device)
                 for _ in range(2))
         if B and L:
-            ra_kv_read(cache, page_table, page_table.shape[1], kv_len, B, L, k, v, _DT[dtype])
+            _check(lib().ra_kv_read(cache._ref, page_table.data_ptr(), pages, kv_len.data_ptr(), B,
+                                    L, k.data_ptr(), v.data_ptr(), dt, s))
     return k, v
 
 
@@ -568,9 +581,10 @@ def make_paged_params(cache, q, page_table, kv_len, *, scale, causal=True, soft_
                       0 if prefix_table is None else prefix_table.shape[0], _ptr(page_table),
                       _ptr(kv_len), _ptr(q_len), _ptr(prefix_table), _ptr(prefix_len), _ptr(sinks))
     p._keep = (page_table, kv_len, q_len, prefix_table, prefix_len, sinks)
-    p._like = (tuple(q.shape), q.dtype)
+    p._like, p._lse = (q.shape, q.dtype), (B, Hq, Lq)
     p._ws = ra_attn_paged_workspace_size(cache, p) if B and Lq else 0
-    p._cache = (cache.n_pages, cache.page_size, cache.Hkv, cache.D, cache.dtype)
+    p._cache = cache._sizes
+    p._ref = ctypes.addressof(p)
     return p
 
 
@@ -578,24 +592,25 @@ def paged_forward(params, q, cache, out=None, lse=None, ws=None, stream=None):
     """Attention of q (B, Lq, Hq, D) over the cached tokens -> (out like q, lse (B, Hq, Lq) fp32).
     Given ``out`` / ``lse`` are written in place (rows behind q_len stay as they are); ``ws``: a
     workspace to use instead of a new one, uint8, of ra_attn_paged_workspace_size elements."""
-    _need((tuple(q.shape), q.dtype) == params._like and q.is_contiguous(),
+    dev = cache.device
+    _need((q.shape, q.dtype) == params._like and q.is_contiguous(),
           "q must be contiguous, of the shape and dtype the params were made for")
-    _need((cache.n_pages, cache.page_size, cache.Hkv, cache.D, cache.dtype) == params._cache,
-          "the params were made for a cache of other sizes")
-    _need(q.device == cache.device, "q must be on the cache's device")
-    B, Lq, Hq, _ = q.shape
+    _need(cache._sizes == params._cache, "the params were made for a cache of other sizes")
+    _need(q.device == dev, "q must be on the cache's device")
     if out is not None:
-        _need(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()
-              and out.device == q.device, "out must be like q")
+        _need((out.shape, out.dtype) == params._like and out.device == dev and out.is_contiguous(),
+              "out must be like q")
     if lse is not None:
-        _need(tuple(lse.shape) == (B, Hq, Lq) and lse.dtype == torch.float32 and lse.is_contiguous()
-              and lse.device == q.device, "lse must be (B, Hq, Lq) fp32")
-    with _On(q.device, stream):
+        _need(lse.shape == params._lse and lse.dtype is torch.float32 and lse.device == dev
+              and lse.is_contiguous(), "lse must be (B, Hq, Lq) fp32")
+    if ws is not None:
+        _need(ws.device == dev and ws.is_contiguous(), "ws must be contiguous and on the cache's device")
+    with _On(dev, stream) as s:
         out = torch.empty_like(q) if out is None else out
-        lse = (torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device) if lse is None
-               else lse)
-        if B and Lq:
+        lse = torch.empty(params._lse, dtype=torch.float32, device=dev) if lse is None else lse
+        if params._ws:
             if ws is None:
-                ws = torch.empty(params._ws, dtype=torch.uint8, device=q.device)
-            ra_attn_paged(cache, params, q, out, lse, ws)
+                ws = torch.empty(params._ws, dtype=torch.uint8, device=dev)
+            _check(lib().ra_attn_paged(cache._ref, params._ref, q.data_ptr(), out.data_ptr(),
+                                       lse.data_ptr(), ws.data_ptr(), _wsb(ws), s))
     return out, lse
