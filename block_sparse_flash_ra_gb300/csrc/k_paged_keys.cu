@@ -23,14 +23,16 @@
 // 16-bit caches run kind::f16 in bf16, q as it is, p = x1 + x2 (2^-16).
 // Logits, maxima, sums and O are fp32.
 //
-//   warps 0-3  softmax: thread = key = TMEM lane of S^T.  A row's maximum is
-//              over all threads, so it is only looked for when some logit
-//              passes the present reference by 2^4 (one barrier with an or);
-//              O (TMEM lane = d) is rescaled then and only then.
-//   warp 4     issues the products, S(i + 1) before P(i) V(i)
-//   warp 5     loads: a lane per page, K and V in rings of their own
-// Two CTAs per SM for 8-bit caches, so that one's softmax hides the other's
-// waits; one with twice the tile bytes for 16-bit ones.
+//   warps 0-3 of each warpgroup
+//              softmax of 8 rows: thread = key = TMEM lane of S^T.  A row's
+//              maximum is over all threads, so it is only looked for when some
+//              logit passes the present reference by 2^4 (one barrier with an
+//              or); O (TMEM lane = d) is rescaled then and only then.
+//   one warp   issues the products, S(i + 1) before P(i) V(i)
+//   one warp   loads: a lane per page, K and V in rings of their own
+// A tile's softmax is a chain of a few hundred instructions in few warps, so
+// rows are spread over warpgroups (8 each) to keep it short, and up to 16 rows
+// of an 8-bit cache run two CTAs per SM, one's chain under the other's.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -43,8 +45,9 @@ namespace ra {
 namespace {
 
 constexpr int kKeys = 128, kD = 128;
-constexpr int kSoftThreads = 128, kThreads = 192;
+constexpr int kRT = 8;         // rows of a softmax warpgroup
 constexpr float kLazy = 4.f;   // growth of a row maximum (base 2) that is let pass
+constexpr float kNone = -3e38f; // the maximum of no logits: finite, so that no difference is a NaN
 constexpr float kPBias = 4.f;  // 8-bit caches: weights times 2^4 are at most 2^8 < 448
 constexpr float kMinExp = 12.f; // least E: 2^(127 + kPBias - E) stays finite
 
@@ -52,9 +55,11 @@ template <bool FP8, int RP>
 struct Cfg {
     static constexpr int kMat = kKeys * kD * (FP8 ? 1 : 2); // bytes of a K or V tile
     static constexpr int kHalves = FP8 ? 1 : 2;             // 128-byte wide blocks of a tile
-    static constexpr int kCtasPerSm = FP8 ? 2 : 1;
-    static constexpr int kStages = RP <= 16 ? (FP8 && RP == 16 ? 2 : 3) : 2;
-    static constexpr int kVStages = RP <= 16 ? 3 : 2;
+    static constexpr int kGroups = RP / kRT, kSoftThreads = 128 * kGroups, kThreads = kSoftThreads + 64;
+    static constexpr int kMmaWarp = 4 * kGroups, kLoadWarp = kMmaWarp + 1;
+    static constexpr int kCtasPerSm = FP8 && RP <= 16 ? 2 : 1;
+    static constexpr int kStages = FP8 ? (RP == 8 ? 3 : RP == 16 ? 2 : 5) : 3;
+    static constexpr int kVStages = FP8 ? (RP == 32 ? 5 : 3) : RP == 32 ? 2 : 3;
     static constexpr int kQTerms = FP8 ? 2 : 1, kPTerms = FP8 ? 3 : 2;
     static constexpr int kNS = RP * kQTerms < 16 ? 16 : RP * kQTerms;     // columns of S^T
     static constexpr int kNO = (RP * kPTerms + 15) / 16 * 16;             // columns of O^T
@@ -66,8 +71,9 @@ struct Cfg {
     static constexpr int kPOff = kQOff + kQBytes;
     static constexpr int kExpOff = kPOff + 2 * kPBytes; // per V stage: scale bytes of K, of V
     static constexpr int kRowOff = kExpOff + (FP8 ? kVStages * 2 * kKeys : 0);
-    static constexpr int kRedOff = kRowOff + RP * 24;   // rows: qs, limit, place; then [4 warps][RP + 1]
-    static constexpr int kBarOff = kRedOff + 4 * (RP + 2) * 4;
+    // per row: logit scale, keys it sees, place of its output (two words), of its lse, its factor
+    static constexpr int kRedOff = kRowOff + RP * 32;
+    static constexpr int kBarOff = kRedOff + 4 * kGroups * (kRT + 4) * 4;
     static constexpr int kNumBars = 2 * kStages + 3 * kVStages + 2 + 2 + 2 + 2 + 1 + 1;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kSmem = kMiscOff + 16 + 1024;
@@ -144,25 +150,31 @@ __device__ __forceinline__ void tma_load_3d(uint8_t *dst, const void *tmap, uint
                  : "memory");
 }
 
-// The softmax warps' own barrier; all 128 threads pass it the same number of
+// The softmax warps' own barrier; all N threads pass it the same number of
 // times whatever happens, so it needs no time limit.
-__device__ __forceinline__ void soft_sync() { asm volatile("barrier.sync 1, 128;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void soft_sync()
+{
+    asm volatile("barrier.sync 1, %0;" ::"n"(N) : "memory");
+}
+template <int N>
 __device__ __forceinline__ bool soft_or(bool x)
 {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-                 "barrier.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 "barrier.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                  : "=r"(r)
-                 : "r"((uint32_t)x)
+                 : "r"((uint32_t)x), "n"(N)
                  : "memory");
     return r != 0;
 }
 
+// The largest of a warp's values (NaN does not count).
 __device__ __forceinline__ float warp_max(float x)
 {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-    return x;
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 // e4m3x2 codes of two halves, and two halves back from codes
@@ -186,15 +198,8 @@ __device__ __forceinline__ void sts16(uint32_t a, uint32_t x)
     asm volatile("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tst.shared.u16 [%0], h;\n\t}" ::"r"(a), "r"(x) : "memory");
 }
 
-struct RowInfo {
-    float qs;  // logit scale of the row, base 2
-    int limit; // keys it sees
-    long long place; // (b * Lq + i) * Hq + hq, or -1
-    long long lse;   // place of its lse
-};
-
 template <bool FP8, int RP>
-__global__ void __launch_bounds__(kThreads, Cfg<FP8, RP>::kCtasPerSm)
+__global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPerSm)
     paged_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       PagedProblem p, PagedPart part)
 {
@@ -218,20 +223,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, RP>::kCtasPerSm)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(bars.s_full + s, 1);
-            mbar_init(bars.s_empty + s, kSoftThreads);
-            mbar_init(bars.p_full + s, kSoftThreads);
+            mbar_init(bars.s_empty + s, C::kSoftThreads);
+            mbar_init(bars.p_full + s, C::kSoftThreads);
             mbar_init(bars.pv_done + s, 1);
         }
-        mbar_init(bars.q_full, kSoftThreads);
+        mbar_init(bars.q_full, C::kSoftThreads);
         mbar_init(bars.drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 4) {
+    if (warp == C::kMmaWarp) {
         tmem_alloc(tmem_holder, C::kCols);
         tmem_relinquish();
     }
-    if (warp == 5 && lane == 0) {
+    if (warp == C::kLoadWarp && lane == 0) {
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
@@ -247,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, RP>::kCtasPerSm)
 
     PagedCursor c;
     const bool any = cursor_begin(p, part, blockIdx.x, c);
-    if (any && warp == 5) {
+    if (any && warp == C::kLoadWarp) {
         // ------------------------------------------------------------ loads
         // lane x fetches box x of a tile: its page number, then its K and V
         const int box = min(p.c.page, kKeys), per = kKeys / box;
@@ -316,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, RP>::kCtasPerSm)
                 if (FP8) wait_drain(bars.e_full + j % C::kVStages, (j / C::kVStages) & 1, kDrainNs);
             }
         }
-    } else if (any && warp == 4) {
+    } else if (any && warp == C::kMmaWarp) {
         // ------------------------------------------------------------ products
         const uint64_t kd0 = sdesc_sw128(smem_u32(smem + C::kKOff), 16, 1024);
         const uint64_t vd0 = sdesc_sw128(smem_u32(smem + C::kVOff), kKeys * 128, 1024);
@@ -365,31 +370,34 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, RP>::kCtasPerSm)
         }
         tc_commit_w(bars.drain);
         wait_drain(bars.drain, 0, kDrainNs);
-    } else if (any && warp < 4) {
+    } else if (any) {
         // ------------------------------------------------------------ softmax
-        // From the first wait that gave up on, no wait is made any more, and
-        // the loops run out on whatever is there: every barrier of these
-        // warps is still met by all of them.
-        const int tid = threadIdx.x;
-        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-        RowInfo *rows = reinterpret_cast<RowInfo *>(smem + C::kRowOff);
-        float *red = reinterpret_cast<float *>(smem + C::kRedOff); // [4][RP + 2]
+        // From the first wait that gave up on, a thread makes no wait any more
+        // and runs its loops out on whatever is there: every barrier of these
+        // warps is still met by all of them, converged.
+        constexpr int NT = C::kSoftThreads, RS = kRT + 4; // words of a warp in red
+        const int tid = threadIdx.x & 127, grp = threadIdx.x >> 7, row0 = grp * kRT, wq = warp & 3;
+        const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
+        float *row_qs = reinterpret_cast<float *>(smem + C::kRowOff);
+        int *row_limit = reinterpret_cast<int *>(row_qs + RP);
+        long long *row_place = reinterpret_cast<long long *>(row_limit + RP); // (b * Lq + i) * Hq + hq, or -1
+        long long *row_lse = row_place + RP;
+        float *row_f = reinterpret_cast<float *>(row_lse + RP);
+        float *red = reinterpret_cast<float *>(smem + C::kRedOff) + grp * 4 * RS; // [4 warps][RS]
         const uint32_t p_base = smem_u32(smem + C::kPOff);
         const float cap2 = p.soft_cap * kLog2e, to_cap = p.soft_cap > 0.f ? kLn2 / p.soft_cap : 0.f;
-        uint32_t i = 0, pv_seen = 0;
+        uint32_t i = 0;
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            if (ok) ok = wait_all(bar, parity);
-        };
-        auto wait_pv = [&](uint32_t n) { // products of tiles below n are complete
-            for (; ok && pv_seen < n; ++pv_seen) wait(bars.pv_done + (pv_seen & 1), (pv_seen >> 1) & 1);
+            if (ok) ok = mbar_wait(bar, parity, ctx);
+            __syncwarp();
         };
         for (;;) {
             const int n = cursor_take(c), len = source_len(c.b);
             // ---- the query rows: 16 threads take one, 8 values each
-#pragma unroll
-            for (int r0 = 0; r0 < C::kNS / C::kQTerms; r0 += 8) {
-                const int r = r0 + (tid >> 4), x = tid & 15;
+#pragma unroll 1
+            for (int r = threadIdx.x >> 4; r < C::kNS / C::kQTerms; r += NT / 16) {
+                const int x = threadIdx.x & 15;
                 const PagedRow row = paged_row(p, part, c, r);
                 const bool live = r < RP && row.counts;
                 const int hq = c.h * p.G + row.g;
@@ -433,45 +441,47 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, RP>::kCtasPerSm)
                                  : "memory");
                 }
                 if (x == 0 && r < RP) {
-                    RowInfo &o = rows[r];
-                    o.qs = qs;
-                    o.limit = live ? row.limit : 0x7fffffff; // rows of no use need no mask
-                    o.place = live ? place : -1;
-                    o.lse = ((long long)row.b * p.Hq + hq) * p.Lq + row.i;
+                    row_qs[r] = qs;
+                    row_limit[r] = live ? row.limit : 0x7fffffff; // rows of no use need no mask
+                    row_place[r] = live ? place : -1;
+                    row_lse[r] = ((long long)row.b * p.Hq + hq) * p.Lq + row.i;
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             mbar_arrive(bars.q_full);
-            soft_sync();
-            int all = 0x7fffffff; // keys below it are seen by every row
+            soft_sync<NT>();
+            float qs[kRT];
+            int all = len; // keys below it are seen by every row
 #pragma unroll
-            for (int r = 0; r < RP; ++r) all = min(all, rows[r].limit);
+            for (int r = 0; r < kRT; ++r) {
+                qs[r] = row_qs[row0 + r];
+                all = min(all, row_limit[row0 + r]);
+            }
 
-            float m[RP], l[RP], ev_top = -INFINITY;
+            float m[kRT], l[kRT], ev_top = 0.f; // E: 0 while no value was seen
 #pragma unroll
-            for (int r = 0; r < RP; ++r) m[r] = -INFINITY, l[r] = 0.f;
+            for (int r = 0; r < kRT; ++r) m[r] = kNone, l[r] = 0.f;
             for (int t = c.t0; t < c.t0 + n; ++t, ++i) {
                 const int sb = i & 1, sv = i % C::kVStages;
                 const int key = t * kKeys + tid;
                 const int valid = min(len - t * kKeys, kKeys);
-                const bool masked = t * kKeys + kKeys > min(all, len);
-                float s[RP];
+                const bool masked = t * kKeys + kKeys > all;
+                float s[kRT];
                 wait(bars.s_full + sb, (i >> 1) & 1);
                 tc_fence_after();
+                tmem_ld<8>(lane_base + sb * C::kNS + row0, s);
                 if (FP8) {
-                    float s2[RP];
-                    tmem_ld<RP>(lane_base + sb * C::kNS, s);
-                    tmem_ld<RP>(lane_base + sb * C::kNS + RP, s2);
+                    float s2[kRT];
+                    tmem_ld<8>(lane_base + sb * C::kNS + RP + row0, s2);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) s[r] = fmaf(s2[r], 1.f / 16.f, s[r]);
+                    for (int r = 0; r < kRT; ++r) s[r] = fmaf(s2[r], 1.f / 16.f, s[r]);
                 } else {
-                    tmem_ld<RP>(lane_base + sb * C::kNS, s);
                     tmem_ld_wait();
                 }
                 tc_fence_before();
                 mbar_arrive(bars.s_empty + sb);
-                float ks = 1.f, vs = 1.f, ev = -INFINITY;
+                float ks = 1.f, vs = 1.f, ev = 0.f;
                 if (FP8) {
                     wait(bars.e_full + sv, (i / C::kVStages) & 1);
                     const uint8_t *e = smem + C::kExpOff + sv * 2 * kKeys + tid;
@@ -484,78 +494,87 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, RP>::kCtasPerSm)
                 // ---- logits in base 2
                 bool grow = FP8 && ev > ev_top;
 #pragma unroll
-                for (int r = 0; r < RP; ++r) {
-                    float x = s[r] * (FP8 ? rows[r].qs * ks : rows[r].qs);
-                    if (to_cap > 0.f) x = cap2 * tanh_fast(x * to_cap);
-                    if (masked && (tid >= valid || key >= rows[r].limit)) x = -INFINITY;
-                    s[r] = x;
-                    grow |= x > m[r] + kLazy;
+                for (int r = 0; r < kRT; ++r) s[r] *= FP8 ? qs[r] * ks : qs[r];
+                if (to_cap > 0.f) {
+#pragma unroll
+                    for (int r = 0; r < kRT; ++r) s[r] = cap2 * tanh_fast(s[r] * to_cap);
                 }
-                if (soft_or(grow)) {
+                if (masked) {
+#pragma unroll
+                    for (int r = 0; r < kRT; ++r)
+                        if (tid >= valid || key >= row_limit[row0 + r]) s[r] = -INFINITY;
+                }
+#pragma unroll
+                for (int r = 0; r < kRT; ++r) grow |= s[r] > m[r] + kLazy;
+                if (soft_or<NT>(grow)) {
                     // new references: the maxima so far
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) {
+                    for (int r = 0; r < kRT; ++r) {
                         const float x = warp_max(s[r]);
-                        if (lane == 0) red[warp * (RP + 2) + r] = x;
+                        if (lane == 0) red[wq * RS + r] = x;
                     }
                     if (FP8) {
                         ev = warp_max(ev);
-                        if (lane == 0) red[warp * (RP + 2) + RP] = ev;
+                        if (lane == 0) red[wq * RS + kRT] = ev;
                     }
-                    wait_pv(i); // O is still
-                    soft_sync();
+                    // O is still: P V of the tile before has completed
+                    if (t > c.t0) wait(bars.pv_done + (sb ^ 1), ((i - 1) >> 1) & 1);
+                    soft_sync<NT>();
                     float fe = 1.f;
                     if (FP8) {
                         float top = ev_top;
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) top = fmaxf(top, red[w * (RP + 2) + RP]);
-                        fe = ev_top == -INFINITY ? 0.f : ex2_approx(ev_top - top);
+                        for (int w = 0; w < 4; ++w) top = fmaxf(top, red[w * RS + kRT]);
+                        fe = ex2_approx(ev_top - top);
                         ev_top = top;
                     }
-                    float f[RP];
+                    float f[kRT];
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) {
+                    for (int r = 0; r < kRT; ++r) {
                         float top = m[r];
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) top = fmaxf(top, red[w * (RP + 2) + r]);
-                        const float x = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - top);
+                        for (int w = 0; w < 4; ++w) top = fmaxf(top, red[w * RS + r]);
+                        const float x = ex2_approx(m[r] - top);
                         l[r] *= x;
                         f[r] = x * fe;
                         m[r] = top;
                     }
                     if (t > c.t0) {
                         tc_fence_after();
+#pragma unroll 1
+                        for (int k = 0; k < C::kPTerms; ++k) {
+                            float o[8];
+                            uint32_t w[8];
+                            tmem_ld<8>(lane_base + C::kColO + k * RP + row0, o);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < C::kPTerms; ++k)
-#pragma unroll
-                            for (int r = 0; r < RP; r += 8) {
-                                float o[8];
-                                uint32_t w[8];
-                                tmem_ld<8>(lane_base + C::kColO + k * RP + r, o);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int y = 0; y < 8; ++y) w[y] = __float_as_uint(o[y] * f[r + y]);
-                                tmem_st8(lane_base + C::kColO + k * RP + r, w);
-                            }
+                            for (int y = 0; y < 8; ++y) w[y] = __float_as_uint(o[y] * f[y]);
+                            tmem_st8(lane_base + C::kColO + k * RP + row0, w);
+                        }
                         tmem_st_wait();
                     }
-                    soft_sync(); // red is free again
+                    soft_sync<NT>(); // red is free again
                 }
                 // ---- weights, as the terms of P^T: row of term k and query row
-                // r is k * RP + r, this thread's column is its key
-                const float pb = FP8 ? (ev_top == -INFINITY ? 1.f : ex2_approx(127.f + kPBias - ev_top)) * vs : 1.f;
-                if (i >= 2) wait_pv(i - 1); // the tile before last has been read
+                // r is k * RP + r, this thread's column is its key.  S of this
+                // tile was issued after P V of the tile before last, so that
+                // tile's weights have been read.
+                const float pb = FP8 ? ex2_approx(127.f + kPBias - fmaxf(ev_top, kMinExp)) * vs : 1.f;
                 const uint32_t pt = p_base + sb * C::kPBytes;
 #pragma unroll
-                for (int r = 0; r < RP; r += 2) {
+                for (int r = 0; r < kRT; r += 2) {
                     float x[2];
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const float base = m[r + y] == -INFINITY ? 0.f : m[r + y];
-                        x[y] = ex2_approx(s[r + y] - base);
+                        x[y] = ex2_approx(s[r + y] - m[r + y]);
                         l[r + y] += x[y];
+                        if (FP8) x[y] *= pb;
+                    }
+                    if (FP8 && masked) {
                         // a masked key's scale may be anything
-                        if (FP8) x[y] = masked && s[r + y] == -INFINITY ? 0.f : x[y] * pb;
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            if (s[r + y] == -INFINITY) x[y] = 0.f;
                     }
                     if (FP8) {
                         __half2 h = __floats2half2_rn(x[0], x[1]);
@@ -564,8 +583,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, RP>::kCtasPerSm)
                             const uint32_t w = to_codes(h);
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
-                                const int row = k * RP + r + y;
-                                sts8(pt + row * 128 + (((tid >> 4) ^ (row & 7)) << 4) + (tid & 15), y ? w >> 8 : w & 0xffu);
+                                const int row = k * RP + row0 + r + y;
+                                sts8(pt + row * 128 + (((tid >> 4) ^ ((r + y) & 7)) << 4) + (tid & 15), y ? w >> 8 : w);
                             }
                             if (k < 2) h = __hmul2(__hsub2(h, from_codes(w)), __float2half2_rn(16.f));
                         }
@@ -577,19 +596,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, RP>::kCtasPerSm)
                         for (int k = 0; k < 2; ++k)
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
-                                const int row = k * RP + r + y;
+                                const int row = k * RP + row0 + r + y;
                                 const uint32_t w = k ? lo : hi;
-                                sts16(pt + (tid >> 6) * (C::kNO * 128) + row * 128 + ((((tid >> 3) & 7) ^ (row & 7)) << 4) +
-                                          (tid & 7) * 2,
-                                      y ? w >> 16 : w & 0xffffu);
+                                sts16(pt + (tid >> 6) * (C::kNO * 128) + row * 128 +
+                                          ((((tid >> 3) & 7) ^ ((r + y) & 7)) << 4) + (tid & 7) * 2,
+                                      y ? w >> 16 : w);
                             }
                     }
                 }
                 if (valid < kKeys) {
                     // values behind the length: whatever is there, weight 0 must give 0
                     wait(bars.v_full + sv, (i / C::kVStages) & 1);
-                    if (tid >= valid)
-#pragma unroll
+                    if (grp == 0 && tid >= valid)
+#pragma unroll 1
                         for (int x = 0; x < C::kHalves * 8; ++x)
                             asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
                                              smem_u32(smem + C::kVOff + sv * C::kMat) + (x >> 3) * (kKeys * 128) + tid * 128 +
@@ -598,63 +617,67 @@ __global__ void __launch_bounds__(kThreads, Cfg<FP8, RP>::kCtasPerSm)
                                          : "memory");
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                tc_fence_before();
                 mbar_arrive(bars.p_full + sb);
             }
-            // ---- the segment's end: sums over the keys' threads, O out of TMEM
+            // ---- the segment's end: sums over the keys' threads
 #pragma unroll
-            for (int r = 0; r < RP; ++r) {
+            for (int r = 0; r < kRT; ++r) {
                 float x = l[r];
 #pragma unroll
                 for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                if (lane == 0) red[warp * (RP + 2) + r] = x;
+                if (lane == 0) red[wq * RS + r] = x;
+                if (tid == 0) row_f[row0 + r] = m[r];
             }
-            soft_sync();
-            wait_pv(i);
-            tc_fence_after();
-            const float fe = FP8 ? (ev_top == -INFINITY ? 0.f : ex2_approx(ev_top - 127.f - kPBias)) : 1.f;
+            soft_sync<NT>();
             const bool final = stores_whole(part, c, n);
-            const size_t slot = slot_row(part, c);
+            const size_t slot = slot_row(part, c) + row0;
+            if (tid < kRT) {
+                // a thread per row: its factor, and what is stored beside O
+                const long long place = row_place[row0 + tid];
+                float lr = 0.f, mr = row_f[row0 + tid], f = 1.f;
 #pragma unroll
-            for (int r = 0; r < RP; r += 8) {
-                float o[C::kPTerms][8];
-#pragma unroll
-                for (int k = 0; k < C::kPTerms; ++k) tmem_ld<8>(lane_base + C::kColO + k * RP + r, o[k]);
-                tmem_ld_wait();
-#pragma unroll
-                for (int y = 0; y < 8; ++y) {
-                    float lr = 0.f, mr = m[r + y], v = o[0][y];
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) lr += red[w * (RP + 2) + r + y];
-                    if (FP8) v = (v + (o[1][y] + o[2][y] * (1.f / 16.f)) * (1.f / 16.f)) * fe;
-                    else v += o[1][y];
-                    const RowInfo &row = rows[r + y];
-                    if (row.place < 0) continue;
-                    if (final) {
-                        if (p.sinks) {
-                            const float sink = p.sinks[row.place % p.Hq] * kLog2e, top = fmaxf(mr, sink);
-                            const float f = ex2_approx(mr - top);
-                            lr = lr * f + ex2_approx(sink - top);
-                            v *= f;
-                            mr = top;
-                        }
-                        static_cast<__nv_bfloat16 *>(p.out)[(size_t)row.place * kD + tid] =
-                            __float2bfloat16_rn(lr == 0.f ? 0.f : v / lr);
-                        if (tid == 0) p.lse[row.lse] = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * kLn2;
-                    } else {
-                        part.o[(slot + r + y) * kD + tid] = v;
-                        if (tid == 0) *reinterpret_cast<float2 *>(part.ml + (slot + r + y) * 2) = make_float2(mr, lr);
+                for (int w = 0; w < 4; ++w) lr += red[w * RS + tid];
+                if (final) {
+                    if (p.sinks && place >= 0) {
+                        const float sink = p.sinks[place % p.Hq] * kLog2e, top = fmaxf(mr, sink);
+                        f = ex2_approx(mr - top);
+                        lr = lr * f + ex2_approx(sink - top);
+                        mr = top;
                     }
+                    f = lr == 0.f ? 0.f : f / lr;
+                    if (place >= 0) p.lse[row_lse[row0 + tid]] = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * kLn2;
+                } else if (place >= 0) {
+                    *reinterpret_cast<float2 *>(part.ml + (slot + tid) * 2) = make_float2(mr, lr);
                 }
+                if (FP8) f *= ex2_approx(fmaxf(ev_top, kMinExp) - 127.f - kPBias);
+                row_f[row0 + tid] = f;
             }
+            wait(bars.pv_done + ((i - 1) & 1), ((i - 1) >> 1) & 1);
+            soft_sync<NT>();
+            tc_fence_after();
+            float o[C::kPTerms][8];
+#pragma unroll
+            for (int k = 0; k < C::kPTerms; ++k) tmem_ld<8>(lane_base + C::kColO + k * RP + row0, o[k]);
+            tmem_ld_wait();
             tc_fence_before();
-            soft_sync(); // rows and red are free again
+#pragma unroll
+            for (int y = 0; y < kRT; ++y) {
+                const long long place = row_place[row0 + y];
+                if (place < 0) continue;
+                float v = o[0][y];
+                if (FP8) v += (o[1][y] + o[C::kPTerms - 1][y] * (1.f / 16.f)) * (1.f / 16.f);
+                else v += o[1][y];
+                v *= row_f[row0 + y];
+                if (final) static_cast<__nv_bfloat16 *>(p.out)[(size_t)place * kD + tid] = __float2bfloat16_rn(v);
+                else part.o[(slot + y) * kD + tid] = v;
+            }
+            soft_sync<NT>(); // the rows' arrays and red are free again
             if (!cursor_next(p, part, c, n)) break;
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 4) {
+    if (warp == C::kMmaWarp) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, C::kCols);
@@ -672,7 +695,7 @@ cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &
         if (e != cudaSuccess) return e;
         set.fetch_or(bit, std::memory_order_release);
     }
-    kern<<<part.ctas, kThreads, Cfg<FP8, RP>::kSmem, s>>>(k, v, p, part);
+    kern<<<part.ctas, Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kSmem, s>>>(k, v, p, part);
     return cudaGetLastError();
 }
 

@@ -142,7 +142,7 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
             a.seg_cost = 3;
             a.row_block = a.rows <= 8 ? 8 : a.rows <= 16 ? 16 : 32;
             a.tile = kPagedKeysTile;
-            a.ctas = (c->dtype == RA_E4M3 ? 2 : 1) * kSms;
+            a.ctas = (c->dtype == RA_E4M3 && a.row_block <= 16 ? 2 : 1) * kSms;
         } else {
             kernel = kFew;
             a.seg_cost = 2;
