@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     auto onward = [&]() {
         if (--a.n > 0) {
             ++a.c.t0;
-            ++a.c.at;
+            --a.c.left;
         } else if ((a.live = cursor_next(p, part, a.c, 1))) {
             a.n = cursor_take(a.c);
             a.len = source_len(a.c.b);

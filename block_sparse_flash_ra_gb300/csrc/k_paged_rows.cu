@@ -12,9 +12,10 @@
 //
 //   warps 0-3, 4-7  softmax of tiles A and B; they also gather the rows of Q
 //                   into shared memory and store the results
-//   warps 8-11      8-bit caches: widen K and V tiles to f16.  16-bit caches:
-//                   clear the values behind a sequence's end
-//   warp 12         loads (a lane per page); warp 13 issues the products
+//   warps 8-11      8-bit caches: widen K tiles to f16
+//   warps 12-15     the same for V; 16-bit caches: clear the values behind a
+//                   sequence's end
+//   warp 16         loads (a lane per page); warp 17 issues the products
 // TMEM: S_A [0,128), S_B [128,256), O_A [256,384), O_B [384,512).
 //
 // 8-bit caches: codes times a power of two are exact in f16, so a key becomes
@@ -42,14 +43,13 @@ namespace ra {
 namespace {
 
 constexpr int kKeys = 128, kHalf = 64, kD = 128;
-constexpr int kThreads = 512;
-constexpr int kWideWarp0 = 8, kLoadWarp = 12, kMmaWarp = 13;
+constexpr int kThreads = 640;
+constexpr int kWideWarpK = 8, kWideWarpV = 12, kLoadWarp = 16, kMmaWarp = 17;
 constexpr float kLazy = 8.f;
-// setmaxnreg split: 256 x 184 + 128 x 64 + 128 x 80 = 65536 = 512 x 128
-constexpr int kLaunchRegs = 128;
-constexpr uint32_t kSoftRegs = 184, kWideRegs = 64, kSideRegs = 80;
-static_assert(256 * kSoftRegs + 128 * kWideRegs + 128 * kSideRegs <= kThreads * kLaunchRegs,
-              "register split exceeds the block's launch registers");
+// S is read from TMEM twice, 32 columns at a time, once for the maximum and
+// once for the weights: every warp gets by with the 96 registers of 640
+// threads (with all 128 logits of a row in registers the kernel spilled, and
+// its unrolled loops starved on instruction fetches).
 
 template <bool FP8>
 struct Cfg {
@@ -147,23 +147,30 @@ __device__ __forceinline__ void widen_half(uint32_t tile, uint32_t raw, const ui
                                            int warp, int lane)
 {
     const int x = lane & 3, in8 = (lane >> 3) ^ (lane & 4 ? 5 : 0);
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-        const int j = (warp * 2 + (it >> 1)) * 8 + in8; // row of the half tile
-        const int c = (it & 1) * 4 + x;                 // its chunk of codes
-        const uint4 w = lds128(raw + j * 128 + ((c ^ (j & 7)) << 4));
+#pragma unroll 1
+    for (int jg = 0; jg < 2; ++jg) {
+        const int j = (warp * 2 + jg) * 8 + in8; // row of the half tile
         const __half2 s = half_scale(exps[j], e);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-        uint32_t o[8];
+        const bool live = row0 + j < valid;
 #pragma unroll
-        for (int y = 0; y < 8; ++y) {
-            const uint32_t h = e4m3x2_to_f16x2(y & 1 ? u[y >> 1] >> 16 : u[y >> 1] & 0xffffu);
-            const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&h), s);
-            o[y] = row0 + j < valid ? *reinterpret_cast<const uint32_t *>(&r) : 0u;
+        for (int it = 0; it < 2; ++it) { // chunks of codes x and 4 + x
+            const uint4 w = lds128(raw + j * 128 + (((it * 4 + x) ^ (j & 7)) << 4));
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                const uint32_t h = e4m3x2_to_f16x2(y & 1 ? u[y >> 1] >> 16 : u[y >> 1] & 0xffffu);
+                const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&h), s);
+                o[y] = *reinterpret_cast<const uint32_t *>(&r);
+            }
+            if (!live) {
+#pragma unroll
+                for (int y = 0; y < 8; ++y) o[y] = 0u;
+            }
+            const uint32_t at = tile + it * (kKeys * 128) + (row0 + j) * 128;
+            sts128(at + (((2 * x) ^ (j & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+            sts128(at + (((2 * x + 1) ^ (j & 7)) << 4), make_uint4(o[4], o[5], o[6], o[7]));
         }
-        const uint32_t at = tile + (it & 1) * (kKeys * 128) + (row0 + j) * 128;
-        sts128(at + (((2 * x) ^ (j & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
-        sts128(at + (((2 * x + 1) ^ (j & 7)) << 4), make_uint4(o[4], o[5], o[6], o[7]));
     }
 }
 
@@ -204,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bars.v_full + s, FP8 ? 128 : 1);
             mbar_init(bars.v_empty + s, 1);
             mbar_init(bars.q_full + s, 128);
-            mbar_init(bars.s_full + s, 1);
+            mbar_init(bars.s_full + s, FP8 ? 2 : 1);
             mbar_init(bars.p_half + s, 128);
             mbar_init(bars.p_full + s, 128);
             mbar_init(bars.o_full + s, 1);
@@ -241,7 +248,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool any = cursor_begin(p, part, blockIdx.x, c);
 
     if (warp >= kLoadWarp) {
-        regs_shrink<kSideRegs>();
         if (any && warp == kLoadWarp) {
             // ------------------------------------------------------------ loads
             // lane x fetches box x of a half tile (codes) or of a tile
@@ -331,6 +337,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t o = ((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) >> 4;
                     mma_ss_w(tmem + x * 128, qd + o, kd + o, C::kIdescS, kk > 0 ? 1u : 0u);
                 }
+                // the softmax reads the tile's E as well as S: this arrival passes on
+                // what the wait for the wide tile has seen
+                if (FP8 && lane == 0) mbar_arrive(bars.s_full + x);
                 tc_commit_w(bars.s_full + x);
             };
             auto issue_pv = [&](int x, uint32_t j, uint32_t ph, bool first) -> bool {
@@ -386,10 +395,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_commit_w(bars.drain);
             wait_drain(bars.drain, 0, kDrainNs);
         }
-    } else if (warp >= kWideWarp0) {
-        regs_shrink<kWideRegs>();
+    } else if (warp >= kWideWarpK) {
         // ---------------------------------------------------------------- tiles
-        const int w = warp - kWideWarp0;
+        const int w = warp & 3, st_raw = warp >= kWideWarpV ? 2 : 0;
+        const uint8_t *ex = smem + C::kExpOff + st_raw * kHalf;
+        const uint32_t raw = smem_u32(smem + C::kRawOff + st_raw * C::kRaw);
+        uint64_t *raw_full = bars.raw_full + st_raw, *raw_empty = bars.raw_empty + st_raw;
         uint32_t g = 0;
         bool ok = true;
         while (any && ok) {
@@ -398,50 +409,51 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = c.t0; ok && t < c.t0 + n; ++t, ++g) {
                 const int valid = min(len - t * kKeys, kKeys), st = g & 1;
                 if (!FP8) {
+                    if (st_raw == 0) continue;
                     // values behind the length: whatever is there, weight 0 must give 0
                     if (!(ok = wait_all(bars.v_full + st, (g >> 1) & 1))) break;
-                    const int j = threadIdx.x - kWideWarp0 * 32;
+                    const int j = threadIdx.x - kWideWarpV * 32;
                     if (j >= valid)
                         for (int x = 0; x < 16; ++x)
                             sts128(smem_u32(smem + C::kVOff + st * C::kMat) + (x >> 3) * (kKeys * 128) + j * 128 + (x & 7) * 16,
                                    make_uint4(0, 0, 0, 0));
                     if (valid < kKeys) proxy_fence();
                     mbar_arrive(bars.v_clear + st);
-                    continue;
+                } else if (st_raw == 0) {
+                    const uint32_t tile = smem_u32(smem + C::kKOff + st * C::kMat);
+                    if (!(ok = wait_all(bars.k_empty + st, ((g >> 1) & 1) ^ 1))) break;
+#pragma unroll 1
+                    for (int y = 0; y < 2; ++y) {
+                        if (!(ok = wait_all(raw_full + y, g & 1))) break;
+                        const int e = max(top_exp(ex + y * kHalf, valid - y * kHalf, lane), 1);
+                        widen_half(tile, raw + y * C::kRaw, ex + y * kHalf, y * kHalf, valid, e, w, lane);
+                        if (w == 0 && lane == 0) k_scale[(g & 3) * 2 + y] = e;
+                        mbar_arrive(raw_empty + y);
+                    }
+                    if (!ok) break;
+                    proxy_fence();
+                    mbar_arrive(bars.k_full + st);
+                } else {
+                    const uint32_t tile = smem_u32(smem + C::kVOff + st * C::kMat);
+                    if (!(ok = wait_all(bars.v_empty + st, ((g >> 1) & 1) ^ 1))) break;
+                    if (!(ok = wait_all(raw_full + 0, g & 1))) break;
+                    if (!(ok = wait_all(raw_full + 1, g & 1))) break;
+                    const int e = max(top_exp(ex, valid, lane), top_exp(ex + kHalf, valid - kHalf, lane));
+                    // 448 * 2^7 is the most that f16 holds; rows without a value do not count
+                    if (ev < 0 || e > ev + 7) ev = max(e, 1);
+#pragma unroll 1
+                    for (int y = 0; y < 2; ++y) {
+                        widen_half(tile, raw + y * C::kRaw, ex + y * kHalf, y * kHalf, valid, ev, w, lane);
+                        mbar_arrive(raw_empty + y);
+                    }
+                    if (w == 0 && lane == 0) v_scale[st] = ev;
+                    proxy_fence();
+                    mbar_arrive(bars.v_full + st);
                 }
-                const uint8_t *ex = smem + C::kExpOff;
-                const uint32_t raw = smem_u32(smem + C::kRawOff);
-                if (!(ok = wait_all(bars.k_empty + st, ((g >> 1) & 1) ^ 1))) break;
-                for (int y = 0; y < 2; ++y) {
-                    if (!(ok = wait_all(bars.raw_full + y, g & 1))) break;
-                    const int e = max(top_exp(ex + y * kHalf, valid - y * kHalf, lane), 1);
-                    widen_half(smem_u32(smem + C::kKOff + st * C::kMat), raw + y * C::kRaw, ex + y * kHalf, y * kHalf, valid, e, w,
-                               lane);
-                    if (w == 0 && lane == 0) k_scale[(g & 3) * 2 + y] = e;
-                    mbar_arrive(bars.raw_empty + y);
-                }
-                if (!ok) break;
-                proxy_fence();
-                mbar_arrive(bars.k_full + st);
-                if (!(ok = wait_all(bars.v_empty + st, ((g >> 1) & 1) ^ 1))) break;
-                if (!(ok = wait_all(bars.raw_full + 2, g & 1))) break;
-                if (!(ok = wait_all(bars.raw_full + 3, g & 1))) break;
-                const int e = max(top_exp(ex + 2 * kHalf, valid, lane), top_exp(ex + 3 * kHalf, valid - kHalf, lane));
-                // 448 * 2^7 is the most that f16 holds; rows without a value do not count
-                if (ev < 0 || e > ev + 7) ev = max(e, 1);
-                for (int y = 0; y < 2; ++y) {
-                    widen_half(smem_u32(smem + C::kVOff + st * C::kMat), raw + (2 + y) * C::kRaw, ex + (2 + y) * kHalf, y * kHalf,
-                               valid, ev, w, lane);
-                    mbar_arrive(bars.raw_empty + 2 + y);
-                }
-                if (w == 0 && lane == 0) v_scale[st] = ev;
-                proxy_fence();
-                mbar_arrive(bars.v_full + st);
             }
             if (!ok || !cursor_next(p, part, c, n)) break;
         }
     } else {
-        regs_grow<kSoftRegs>();
         // ---------------------------------------------------------------- softmax
         const int x = warp >> 2; // tile A or B
         const int row_in = (warp & 3) * 32 + lane;
@@ -451,14 +463,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         while (any && ok) {
             const int n = cursor_take(c), len = source_len(c.b);
-            const PagedRow row = paged_row(p, part, c, x * 128 + row_in);
             const bool mine = x == 0 || two_tiles(c); // uniform in the warpgroup
-            const int hq = c.h * p.G + row.g;
-            const size_t place = ((size_t)row.b * p.Lq + row.i) * p.Hq + hq;
-            const int limit = row.counts ? row.limit : 0x7fffffff; // rows of no use need no mask
+            int limit = 0x7fffffff; // rows of no use need no mask
             // ---- this thread's row of Q
             float a_row = p.scale * kLog2e;
             if (mine) {
+                const PagedRow row = paged_row(p, part, c, x * 128 + row_in);
+                const size_t place = ((size_t)row.b * p.Lq + row.i) * p.Hq + c.h * p.G + row.g;
+                if (row.counts) limit = min(row.limit, len);
                 const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + place * kD);
                 const uint32_t at = smem_u32(smem + C::kQOff + x * C::kMat) + row_in * 128;
                 float inv = 1.f;
@@ -490,21 +502,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 proxy_fence();
             }
             mbar_arrive(bars.q_full + x);
-            const int all = __reduce_min_sync(0xffffffffu, limit);
+            const int all = min(__reduce_min_sync(0xffffffffu, limit), len);
 
             float m = -INFINITY, l = 0.f;
             int ev = 0;
             for (int t = c.t0; mine && ok && t < c.t0 + n; ++t) {
                 const uint32_t gt = g + (t - c.t0); // the tile's number in this CTA
                 const int st = gt & 1;
-                const int first = t * kKeys, seen = min(limit, len) - first; // keys of the tile that the row sees
-                const bool masked = min(all, len) < first + kKeys;
+                const int first = t * kKeys;
+                const bool masked = all < first + kKeys;
                 if (!(ok = wait_all(bars.s_full + x, gx & 1))) break;
                 tc_fence_after();
-                float s[128];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_ld32(lane_base + x * 128 + k * 32, s + 32 * k);
-                float am[2] = {a_row, a_row};
+                float am[2] = {a_row, a_row}; // logit scale of each half of the keys
                 float fv = 1.f;
                 if (FP8) {
                     // the tile's values are wide by now or soon: P V waits for them anyway
@@ -516,58 +525,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (e != ev) fv = ex2_approx((float)(ev - e));
                     ev = e;
                 }
-                tmem_ld_wait();
-                if (to_cap > 0.f) {
-                    float xa = 0.f;
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        float t4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int j = 0; j < 64; j += 8)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                t4[k] = max3(t4[k], fabsf(s[hf * 64 + j + 2 * k]), fabsf(s[hf * 64 + j + 2 * k + 1]));
-                        xa = fmaxf(xa, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * am[hf] * to_cap);
-                    }
-                    if (__all_sync(0xffffffffu, xa < kTanhSmall)) {
-                        // the odd series, two lanes per instruction: 3.4e-7 relative
-                        const float2 d7 = make_float2(cap2 * kTanhC7, cap2 * kTanhC7), d5 = make_float2(cap2 * kTanhC5, cap2 * kTanhC5);
-                        const float2 d3 = make_float2(cap2 * kTanhC3, cap2 * kTanhC3), d1 = make_float2(cap2, cap2);
-#pragma unroll
-                        for (int j = 0; j < 128; j += 2) {
-                            const float k1 = am[j >> 6] * to_cap;
-                            const float2 xx = fmul2(make_float2(s[j], s[j + 1]), make_float2(k1, k1));
-                            const float2 x2 = fmul2(xx, xx);
-                            const float2 r = fmul2(xx, ffma2(x2, ffma2(x2, ffma2(x2, d7, d5), d3), d1));
-                            s[j] = r.x;
-                            s[j + 1] = r.y;
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 128; ++j) s[j] = cap2 * tanh_fast(s[j] * (am[j >> 6] * to_cap));
-                    }
-                    am[0] = am[1] = 1.f;
-                }
-                if (masked) {
-#pragma unroll
-                    for (int j = 0; j < 128; ++j)
-                        if (j >= seen) s[j] = -INFINITY;
-                }
+                const int seen = limit - first; // keys of the tile that the row sees
+                const uint32_t s_col = lane_base + x * 128;
+                // ---- the row's maximum (scaling and the cap keep the order)
                 float top = -INFINITY;
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    float s[32];
+                    tmem_ld32(s_col + k * 32, s);
+                    tmem_ld_wait();
+                    if (masked) {
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
+                        for (int j = 0; j < 32; ++j)
+                            if (k * 32 + j >= seen) s[j] = -INFINITY;
+                    }
                     float mx[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float *v = s + hf * 64 + k;
-                        mx[k] = max3(v[0], v[4], v[8]);
-#pragma unroll
-                        for (int j = 12; j < 60; j += 8) mx[k] = max3(mx[k], v[j], v[j + 4]);
-                        mx[k] = fmaxf(mx[k], v[60]);
+                    for (int y = 0; y < 4; ++y) {
+                        mx[y] = max3(s[y], s[y + 4], s[y + 8]);
+                        mx[y] = max3(mx[y], s[y + 12], s[y + 16]);
+                        mx[y] = max3(mx[y], s[y + 20], s[y + 24]);
+                        mx[y] = fmaxf(mx[y], s[y + 28]);
                     }
-                    // am > 0, so scaling commutes with the maximum
-                    top = fmaxf(top, am[hf] * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                    top = fmaxf(top, (k < 2 ? am[0] : am[1]) * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
                 }
+                if (to_cap > 0.f && top != -INFINITY) top = cap2 * tanh_fast(top * to_cap);
                 const float m_new = fmaxf(m, top);
                 const bool need = m_new > m + kLazy; // also a first maximum
                 if (__any_sync(0xffffffffu, need) || fv != 1.f) {
@@ -593,22 +575,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float base = (m == -INFINITY ? 0.f : m) - C::kPBias;
                 const float2 nm = make_float2(-base, -base);
                 float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                // ---- the weights, over columns of S that were read before
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    float s[32];
+                    tmem_ld32(s_col + k * 32, s);
+                    float a = k < 2 ? am[0] : am[1];
+                    tmem_ld_wait();
+                    if (to_cap > 0.f) {
+                        // the odd series where it holds (3.4e-7 relative), two lanes
+                        // per instruction; else 1 - 2 / (1 + e^2x)
+                        const float a1 = a * to_cap;
+                        float xa = 0.f;
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const float2 a2 = make_float2(am[hf], am[hf]);
-                    uint32_t pk[32];
+                        for (int j = 0; j < 32; j += 2) xa = max3(xa, fabsf(s[j]), fabsf(s[j + 1]));
+                        if (__all_sync(0xffffffffu, xa * a1 < kTanhSmall)) {
+                            const float2 k1 = make_float2(a1, a1), d7 = make_float2(cap2 * kTanhC7, cap2 * kTanhC7);
+                            const float2 d5 = make_float2(cap2 * kTanhC5, cap2 * kTanhC5);
+                            const float2 d3 = make_float2(cap2 * kTanhC3, cap2 * kTanhC3), d1 = make_float2(cap2, cap2);
 #pragma unroll
-                    for (int j = 0; j < 64; j += 2) {
-                        const float2 y = ffma2(make_float2(s[hf * 64 + j], s[hf * 64 + j + 1]), a2, nm);
+                            for (int j = 0; j < 32; j += 2) {
+                                const float2 xx = fmul2(make_float2(s[j], s[j + 1]), k1), x2 = fmul2(xx, xx);
+                                const float2 r = fmul2(xx, ffma2(x2, ffma2(x2, ffma2(x2, d7, d5), d3), d1));
+                                s[j] = r.x;
+                                s[j + 1] = r.y;
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) s[j] = cap2 * tanh_fast(s[j] * a1);
+                        }
+                        a = 1.f;
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (k * 32 + j >= seen) s[j] = -INFINITY;
+                    }
+                    const float2 a2 = make_float2(a, a);
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 y = ffma2(make_float2(s[j], s[j + 1]), a2, nm);
                         const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
                         ls[(j >> 1) & 3] = fadd2(ls[(j >> 1) & 3], e);
                         pk[j >> 1] = pack16<FP8>(e.x, e.y);
                     }
-                    // over columns of S that this thread has read
-                    tmem_st32(lane_base + x * 128 + hf * 32, pk);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    mbar_arrive((hf ? bars.p_full : bars.p_half) + x);
+                    tmem_st16(s_col + k * 16, pk);
+                    if (k & 1) {
+                        // keys 0-63, then 64-127: half of P V may start
+                        tmem_st_wait();
+                        tc_fence_before();
+                        mbar_arrive((k == 1 ? bars.p_half : bars.p_full) + x);
+                    }
                 }
                 const float2 l2 = fadd2(fadd2(ls[0], ls[1]), fadd2(ls[2], ls[3]));
                 l += l2.x + l2.y;
@@ -621,6 +639,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = wait_all(bars.o_full + x, segs & 1))) break;
                 ++segs;
                 tc_fence_after();
+                const PagedRow row = paged_row(p, part, c, x * 128 + row_in);
+                const int hq = c.h * p.G + row.g;
+                const size_t place = ((size_t)row.b * p.Lq + row.i) * p.Hq + hq;
                 float mr = m - C::kPBias; // l and O are relative to 2^mr
                 const float fv = FP8 ? __uint_as_float((uint32_t)ev << 23) : 1.f;
                 const bool final = stores_whole(part, c, n);
@@ -681,12 +702,7 @@ cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &
     static std::atomic<uint64_t> set{0}; // devices whose copy of the kernel has its attribute
     const uint64_t bit = 1ull << p.device;
     if (!(set.load(std::memory_order_acquire) & bit)) {
-        cudaFuncAttributes fa;
-        cudaError_t e = cudaFuncGetAttributes(&fa, kern);
-        if (e != cudaSuccess) return e;
-        // the setmaxnreg split draws on the registers the block is launched with
-        if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<FP8>::kSmem);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<FP8>::kSmem);
         if (e != cudaSuccess) return e;
         set.fetch_or(bit, std::memory_order_release);
     }

@@ -92,13 +92,14 @@ __device__ __forceinline__ long long own_places_sum(const PagedProblem &p, const
     return n;
 }
 
-// A place on the line, kept by every thread of a CTA alike.
+// A place on the line, kept by every thread of a CTA alike.  (A share is far
+// below 2^31 places: that many tiles would keep a CTA busy for hours.)
 struct PagedCursor {
-    long long at, end; // place of the next tile; the end of the CTA's share
-    int b, rb, h;      // the segment
-    int t0, tiles;     // its next tile, and its tiles
-    long long seg;     // its number
-    bool first;        // the first of the share
+    int left;      // places from the next tile on that are the CTA's
+    int b, rb, h;  // the segment
+    int t0, tiles; // its next tile, and its tiles
+    int seg;       // its number
+    bool first;    // the first of the share
 };
 
 // Places the cursor at CTA `cta`'s first tile.  Called by one converged warp
@@ -117,9 +118,8 @@ __device__ __forceinline__ bool cursor_begin(const PagedProblem &p, const PagedP
         total = own_places_sum(p, part, 0, before) * per_seq;
     }
     const long long share = (total + part.ctas - 1) / part.ctas;
-    c.at = share * cta;
-    c.end = c.at + share < total ? c.at + share : total;
-    if (c.at >= c.end) return false;
+    const long long at = share * cta, end = at + share < total ? at + share : total;
+    if (at >= end) return false;
     c.b = 0;
     c.tiles = prefix_tiles;
     if (!part.prefix) {
@@ -133,7 +133,7 @@ __device__ __forceinline__ bool cursor_begin(const PagedProblem &p, const PagedP
                 const long long x = __shfl_up_sync(0xffffffffu, run, o);
                 if (lane >= o) run += x;
             }
-            const unsigned past = __ballot_sync(0xffffffffu, before + run > c.at);
+            const unsigned past = __ballot_sync(0xffffffffu, before + run > at);
             if (past) {
                 const int l = __ffs(past) - 1, places = __shfl_sync(0xffffffffu, n, l);
                 c.b = b0 + l;
@@ -145,23 +145,21 @@ __device__ __forceinline__ bool cursor_begin(const PagedProblem &p, const PagedP
         }
     }
     const int places = c.tiles + part.seg_cost;
-    const int in_seq = (int)((c.at - before) / places);
-    const int off = (int)(c.at - before - (long long)in_seq * places);
-    c.t0 = off > part.seg_cost ? off - part.seg_cost : 0;
-    if (off < part.seg_cost) c.at += part.seg_cost - off;
+    const int in_seq = (int)((at - before) / places);
+    const int off = (int)(at - before - (long long)in_seq * places);
+    c.t0 = max(off - part.seg_cost, 0);
+    c.left = (int)(end - at) - max(part.seg_cost - off, 0);
     c.rb = in_seq / p.c.Hkv;
     c.h = in_seq - c.rb * p.c.Hkv;
-    c.seg = (long long)c.b * per_seq + in_seq;
+    c.seg = c.b * per_seq + in_seq;
     c.first = true;
-    return c.at < c.end;
+    return c.left > 0;
 }
 
 // Tiles of the present segment that fall into the share.
 __device__ __forceinline__ int cursor_take(const PagedCursor &c)
 {
-    const long long left = c.end - c.at;
-    const int n = c.tiles - c.t0;
-    return n < left ? n : (int)left;
+    return min(c.tiles - c.t0, c.left);
 }
 
 // Moves on to the segment after the `n` tiles that cursor_take gave; false at
@@ -169,8 +167,8 @@ __device__ __forceinline__ int cursor_take(const PagedCursor &c)
 __device__ __forceinline__ bool cursor_next(const PagedProblem &p, const PagedPart &part,
                                             PagedCursor &c, int n)
 {
-    c.at += n + part.seg_cost;
-    if (c.at >= c.end) return false;
+    c.left -= n + part.seg_cost;
+    if (c.left <= 0) return false;
     c.t0 = 0;
     c.first = false;
     ++c.seg;
@@ -181,7 +179,7 @@ __device__ __forceinline__ bool cursor_next(const PagedProblem &p, const PagedPa
             do { // a share that goes on has a sequence with tiles ahead
                 ++c.b;
                 c.tiles = own_tiles(p, part, c.b);
-                if (!c.tiles) c.seg += (long long)part.n_rb * p.c.Hkv;
+                if (!c.tiles) c.seg += part.n_rb * p.c.Hkv;
             } while (!c.tiles);
         }
     }

@@ -95,6 +95,9 @@ int check_paged(const ra_kv_cache *c, const ra_paged_params *p)
     if (p->prefix_pages < 0 || (p->prefix_pages > 0) != (p->prefix_table != nullptr) ||
         (p->prefix_pages > 0) != (p->prefix_len != nullptr))
         return refuse(RA_ERR_INVALID_ARG, "prefix_pages, prefix_table and prefix_len must come together");
+    // segments are counted in 32 bits: at most one per 8 query rows of a kv head
+    if ((double)p->B * ((double)p->Lq * p->Hq / c->Hkv / 8 + 1) * c->Hkv > 1e9)
+        return refuse(RA_ERR_UNSUPPORTED, "too many query rows (B=%d Lq=%d Hq=%d)", p->B, p->Lq, p->Hq);
     if (((long long)p->max_pages + p->prefix_pages) * c->page_size > 0x7fffffffll)
         return refuse(RA_ERR_UNSUPPORTED, "sequences must be shorter than 2^31 tokens");
     return RA_OK;
