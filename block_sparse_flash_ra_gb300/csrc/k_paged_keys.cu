@@ -46,7 +46,6 @@ namespace {
 
 constexpr int kKeys = 128, kD = 128;
 constexpr int kRT = 8;         // rows of a softmax warpgroup
-constexpr float kLazy = 4.f;   // growth of a row maximum (base 2) that is let pass
 constexpr float kNone = -3e38f; // the maximum of no logits: finite, so that no difference is a NaN
 constexpr float kPBias = 4.f;  // 8-bit caches: weights times 2^4 are at most 2^8 < 448
 constexpr float kMinExp = 12.f; // least E: 2^(127 + kPBias - E) stays finite
@@ -83,6 +82,9 @@ struct Cfg {
                                         ((uint32_t)(kNS >> 3) << 17) | ((uint32_t)(kKeys >> 4) << 24);
     static constexpr uint32_t kIdescO = ((FP8 ? 0u : (1u << 7) | (1u << 10)) | (1u << 4)) | (1u << 15) |
                                         ((uint32_t)(kNO >> 3) << 17) | ((uint32_t)(kD >> 4) << 24);
+    // growth of a row's logits above its reference (base 2) that is let pass:
+    // 8-bit weights end at 448, bf16 has fp32's range
+    static constexpr float kLazy = FP8 ? 4.f : 60.f;
     static_assert(kSmem <= (kCtasPerSm == 2 ? 113 : 227) * 1024, "shared memory");
     static_assert(kBarOff % 8 == 0 && kRowOff % 8 == 0 && kPOff % 1024 == 0 && kExpOff % 128 == 0, "layout");
 };
@@ -505,7 +507,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                         if (tid >= valid || key >= row_limit[row0 + r]) s[r] = -INFINITY;
                 }
 #pragma unroll
-                for (int r = 0; r < kRT; ++r) grow |= s[r] > m[r] + kLazy;
+                for (int r = 0; r < kRT; ++r) grow |= s[r] > m[r] + C::kLazy;
                 if (soft_or<NT>(grow)) {
                     // new references: the maxima so far
 #pragma unroll

@@ -24,8 +24,8 @@
 // code * 2^(e_v - EV), EV one exponent for the whole segment (raised, and O
 // rescaled, when a tile's largest passes it by 2^7; f16 holds 448 * 2^7).
 // What f16 loses is below 2^-33 of the largest.  The rows of Q are scaled by a
-// power of two into f16's range, and P is f16 (2^-11 relative), times 2^7 so
-// that weights down to 2^-21 of the largest keep all bits.  Widening costs
+// power of two into f16's range, and P is f16 (2^-11 relative; weights below
+// 2^-16 of the row's reference lose bits, below 2^-26 all of them).  Widening costs
 // 1.6 instructions per pair and 96 KB of shared-memory traffic per tile of
 // 2048 tensor cycles; the alternative, e4m3 terms for P as the M side of the
 // few-row kernel uses, has no room in a compute-bound loop.
@@ -35,6 +35,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "ra_paged.cuh"
 #include "ra_sched.cuh"
@@ -43,13 +44,15 @@ namespace ra {
 namespace {
 
 constexpr int kKeys = 128, kHalf = 64, kD = 128;
-constexpr int kThreads = 640;
+constexpr int kThreads = 576;
 constexpr int kWideWarpK = 8, kWideWarpV = 12, kLoadWarp = 16, kMmaWarp = 17;
-constexpr float kLazy = 8.f;
-// S is read from TMEM twice, 32 columns at a time, once for the maximum and
-// once for the weights: every warp gets by with the 96 registers of 640
-// threads (with all 128 logits of a row in registers the kernel spilled, and
-// its unrolled loops starved on instruction fetches).
+// The softmax of a quarter tile (32 keys) takes the row's present reference
+// for granted: weights are computed at once, and only when a logit passes the
+// reference by 2^13 (2^60 in bf16) is it raised, O rescaled and the quarter
+// computed again from S, which its weights have not yet overwritten.  S comes 16 columns at a
+// time, the next on their way, so that every warp gets by with the 96
+// registers of 18 warps (with all 128 logits of a row in registers the
+// kernel spilled, and its unrolled loops starved on instruction fetches).
 
 template <bool FP8>
 struct Cfg {
@@ -63,8 +66,8 @@ struct Cfg {
     static constexpr int kExpOff = kRawOff + kRaws * kRaw; // 64 scale bytes per half
     static constexpr int kBarOff = kExpOff + kRaws * kHalf;
     // k_full[2], k_empty[2], v_full[2], v_empty[2], raw_full[4], raw_empty[4],
-    // q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], v_clear[2], drain
-    static constexpr int kNumBars = 8 + 8 + 12 + 1;
+    // q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], v_clear[2], pv_half[2], drain
+    static constexpr int kNumBars = 8 + 8 + 14 + 1;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8 + 8;
     static constexpr int kScaleOff = kMiscOff + 16; // E of K half tiles [4][2], EV of V tiles [2]
     static constexpr int kSmem = kScaleOff + 48 + 1024;
@@ -72,12 +75,14 @@ struct Cfg {
     static constexpr uint32_t kFmt = FP8 ? 0u : (1u << 7) | (1u << 10); // f16 or bf16 operands
     static constexpr uint32_t kIdescS = (1u << 4) | kFmt | (128u >> 3 << 17) | (128u >> 4 << 24);
     static constexpr uint32_t kIdescO = kIdescS | (1u << 16); // V is MN-major
-    static constexpr float kPBias = FP8 ? 7.f : 0.f;
+    // Weights are 2^kPBias at the row's reference and may grow by 2^kLazy: f16
+    // holds 2^15 and keeps all bits down to 2^-14; bf16 has fp32's range.
+    static constexpr float kPBias = FP8 ? 2.f : 0.f, kLazy = FP8 ? 13.f : 60.f;
 };
 
 struct Bars {
     uint64_t *k_full, *k_empty, *v_full, *v_empty, *raw_full, *raw_empty, *q_full, *s_full, *p_half, *p_full, *o_full,
-        *v_clear, *drain;
+        *v_clear, *pv_half, *drain;
 };
 
 template <class C>
@@ -96,7 +101,8 @@ __device__ __forceinline__ Bars carve(uint8_t *smem)
     b.p_full = b.p_half + 2;
     b.o_full = b.p_full + 2;
     b.v_clear = b.o_full + 2;
-    b.drain = b.v_clear + 2;
+    b.pv_half = b.v_clear + 2;
+    b.drain = b.pv_half + 2;
     return b;
 }
 
@@ -187,7 +193,7 @@ __device__ __forceinline__ int top_exp(const uint8_t *exps, int valid, int lane)
     return (int)__reduce_max_sync(0xffffffffu, top);
 }
 
-template <bool FP8>
+template <bool FP8, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       PagedProblem p, PagedPart part)
@@ -216,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bars.p_full + s, 128);
             mbar_init(bars.o_full + s, 1);
             mbar_init(bars.v_clear + s, 128);
+            mbar_init(bars.pv_half + s, 1);
         }
         for (int s = 0; s < 4; ++s) {
             mbar_init(bars.raw_full + s, 1);
@@ -355,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mma_ts_w(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, vd + (uint32_t)((kk * 2048) >> 4), C::kIdescO,
                                  (kk > 0 || !first) ? 1u : 0u);
                     }
+                    if (hf == 0) tc_commit_w(bars.pv_half + x);
                 }
                 return true;
             };
@@ -465,39 +473,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n = cursor_take(c), len = source_len(c.b);
             const bool mine = x == 0 || two_tiles(c); // uniform in the warpgroup
             int limit = 0x7fffffff; // rows of no use need no mask
-            // ---- this thread's row of Q
+            // ---- Q: 16 lanes take a row, 8 values each; row 2 it + y of the warp
+            // belongs to lane 2 it + y
             float a_row = p.scale * kLog2e;
             if (mine) {
                 const PagedRow row = paged_row(p, part, c, x * 128 + row_in);
-                const size_t place = ((size_t)row.b * p.Lq + row.i) * p.Hq + c.h * p.G + row.g;
+                const int place = row.counts ? (row.b * p.Lq + row.i) * p.Hq + c.h * p.G + row.g : -1;
                 if (row.counts) limit = min(row.limit, len);
-                const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + place * kD);
-                const uint32_t at = smem_u32(smem + C::kQOff + x * C::kMat) + row_in * 128;
-                float inv = 1.f;
-                if (FP8) {
-                    uint32_t top = 0; // largest magnitude, as bf16 bits
-#pragma unroll
-                    for (int y = 0; y < 16; ++y) {
-                        const uint4 u = row.counts ? q[y] : make_uint4(0, 0, 0, 0);
-                        const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+                const int ch = lane & 15;
+#pragma unroll 4
+                for (int it = 0; it < 16; ++it) {
+                    const int r = 2 * it + (lane >> 4), r_in = (warp & 3) * 32 + r;
+                    const int src = __shfl_sync(0xffffffffu, place, r);
+                    uint4 u = make_uint4(0, 0, 0, 0);
+                    if (src >= 0)
+                        u = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + (size_t)src * kD)[ch];
+                    if (FP8) {
+                        uint32_t v[4] = {u.x, u.y, u.z, u.w}, top = 0; // largest magnitude, as bf16 bits
 #pragma unroll
                         for (int k = 0; k < 4; ++k) top = max(top, max(v[k] & 0x7fffu, (v[k] >> 16) & 0x7fffu));
-                    }
-                    const int e = top == 0 ? 0 : min(max((int)(top >> 7) - 127, -120), 120);
-                    inv = __uint_as_float((uint32_t)(127 - e) << 23);
-                    a_row *= __uint_as_float((uint32_t)(127 + e) << 23);
-                }
 #pragma unroll
-                for (int y = 0; y < 16; ++y) {
-                    uint4 u = row.counts ? q[y] : make_uint4(0, 0, 0, 0);
-                    if (FP8) {
-                        uint32_t v[4] = {u.x, u.y, u.z, u.w};
+                        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const int e = top == 0 ? 0 : min(max((int)(top >> 7) - 127, -120), 120);
+                        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             v[k] = pack16<true>(__uint_as_float(v[k] << 16) * inv, __uint_as_float(v[k] & 0xffff0000u) * inv);
                         u = make_uint4(v[0], v[1], v[2], v[3]);
+                        const int e_row = __shfl_sync(0xffffffffu, e, (lane & 1) * 16);
+                        if (lane >> 1 == it) a_row *= __uint_as_float((uint32_t)(127 + e_row) << 23);
                     }
-                    sts128(at + (y >> 3) * (kKeys * 128) + (((y & 7) ^ (row_in & 7)) << 4), u);
+                    sts128(smem_u32(smem + C::kQOff + x * C::kMat) + (ch >> 3) * (kKeys * 128) + r_in * 128 +
+                               (((ch & 7) ^ (r_in & 7)) << 4),
+                           u);
                 }
                 proxy_fence();
             }
@@ -506,131 +514,153 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             float m = -INFINITY, l = 0.f;
             int ev = 0;
-            for (int t = c.t0; mine && ok && t < c.t0 + n; ++t) {
+            // O of this row times f (every product into it has completed)
+            auto scale_o = [&](float f) {
+#pragma unroll 1
+                for (int k = 0; k < 8; ++k) {
+                    float o[16];
+                    tmem_ld16(lane_base + 256 + x * 128 + k * 16, o);
+                    tmem_ld_wait();
+                    uint32_t u[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(o[j] * f);
+                    tmem_st16(lane_base + 256 + x * 128 + k * 16, u);
+                }
+                tmem_st_wait();
+            };
+            for (int t = c.t0; mine && ok && t < c.t0 + n; ++t, ++gx) {
                 const uint32_t gt = g + (t - c.t0); // the tile's number in this CTA
                 const int st = gt & 1;
-                const int first = t * kKeys;
-                const bool masked = all < first + kKeys;
+                const bool masked = all < (t + 1) * kKeys;
                 if (!(ok = wait_all(bars.s_full + x, gx & 1))) break;
                 tc_fence_after();
-                float am[2] = {a_row, a_row}; // logit scale of each half of the keys
-                float fv = 1.f;
                 if (FP8) {
                     // the tile's values are wide by now or soon: P V waits for them anyway
                     if (!(ok = wait_all(bars.v_full + st, (gt >> 1) & 1))) break;
-                    am[0] *= __uint_as_float((uint32_t)k_scale[(gt & 3) * 2] << 23);
-                    am[1] *= __uint_as_float((uint32_t)k_scale[(gt & 3) * 2 + 1] << 23);
                     const int e = v_scale[st];
-                    if (t == c.t0) ev = e;
-                    if (e != ev) fv = ex2_approx((float)(ev - e));
+                    // S of this tile completed after P V of the one before
+                    if (t > c.t0 && e != ev) scale_o(ex2_approx((float)(ev - e)));
                     ev = e;
                 }
-                const int seen = limit - first; // keys of the tile that the row sees
-                const uint32_t s_col = lane_base + x * 128;
-                // ---- the row's maximum (scaling and the cap keep the order)
-                float top = -INFINITY;
+                float a = a_row; // logit scale of the half's keys
 #pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
-                    float s[32];
-                    tmem_ld32(s_col + k * 32, s);
-                    tmem_ld_wait();
-                    if (masked) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (k * 32 + j >= seen) s[j] = -INFINITY;
-                    }
-                    float mx[4];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        mx[y] = max3(s[y], s[y + 4], s[y + 8]);
-                        mx[y] = max3(mx[y], s[y + 12], s[y + 16]);
-                        mx[y] = max3(mx[y], s[y + 20], s[y + 24]);
-                        mx[y] = fmaxf(mx[y], s[y + 28]);
-                    }
-                    top = fmaxf(top, (k < 2 ? am[0] : am[1]) * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-                }
-                if (to_cap > 0.f && top != -INFINITY) top = cap2 * tanh_fast(top * to_cap);
-                const float m_new = fmaxf(m, top);
-                const bool need = m_new > m + kLazy; // also a first maximum
-                if (__any_sync(0xffffffffu, need) || fv != 1.f) {
-                    const float f = !need ? 1.f : m == -INFINITY ? 0.f : ex2_approx(m - m_new);
-                    l *= f;
-                    if (need) m = m_new;
-                    if (t > c.t0) {
-                        // S of this tile completed after P V of the one before
-                        const float fo = f * fv;
-#pragma unroll 1
-                        for (int k = 0; k < 4; ++k) {
-                            float o[32];
-                            tmem_ld32(lane_base + 256 + x * 128 + k * 32, o);
-                            tmem_ld_wait();
-                            uint32_t u[32];
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(o[j] * fo);
-                            tmem_st32(lane_base + 256 + x * 128 + k * 32, u);
-                        }
-                        tmem_st_wait();
-                    }
-                }
-                const float base = (m == -INFINITY ? 0.f : m) - C::kPBias;
-                const float2 nm = make_float2(-base, -base);
-                float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                // ---- the weights, over columns of S that were read before
-#pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
-                    float s[32];
-                    tmem_ld32(s_col + k * 32, s);
-                    float a = k < 2 ? am[0] : am[1];
-                    tmem_ld_wait();
-                    if (to_cap > 0.f) {
-                        // the odd series where it holds (3.4e-7 relative), two lanes
-                        // per instruction; else 1 - 2 / (1 + e^2x)
-                        const float a1 = a * to_cap;
-                        float xa = 0.f;
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) xa = max3(xa, fabsf(s[j]), fabsf(s[j + 1]));
-                        if (__all_sync(0xffffffffu, xa * a1 < kTanhSmall)) {
-                            const float2 k1 = make_float2(a1, a1), d7 = make_float2(cap2 * kTanhC7, cap2 * kTanhC7);
-                            const float2 d5 = make_float2(cap2 * kTanhC5, cap2 * kTanhC5);
-                            const float2 d3 = make_float2(cap2 * kTanhC3, cap2 * kTanhC3), d1 = make_float2(cap2, cap2);
-#pragma unroll
-                            for (int j = 0; j < 32; j += 2) {
-                                const float2 xx = fmul2(make_float2(s[j], s[j + 1]), k1), x2 = fmul2(xx, xx);
-                                const float2 r = fmul2(xx, ffma2(x2, ffma2(x2, ffma2(x2, d7, d5), d3), d1));
-                                s[j] = r.x;
-                                s[j + 1] = r.y;
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) s[j] = cap2 * tanh_fast(s[j] * a1);
-                        }
-                        a = 1.f;
-                    }
-                    if (masked) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (k * 32 + j >= seen) s[j] = -INFINITY;
-                    }
-                    const float2 a2 = make_float2(a, a);
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    const uint32_t s_col = lane_base + x * 128 + q4 * 32, p_col = lane_base + x * 128 + q4 * 16;
+                    if (FP8 && !(q4 & 1))
+                        a = a_row * __uint_as_float((uint32_t)k_scale[(gt & 3) * 2 + (q4 >> 1)] << 23);
                     uint32_t pk[16];
+                    float top = -INFINITY, sum = 0.f;
+                    // The weights of 32 keys, at most 2^(kPBias + kLazy), with the
+                    // exponent's offset nm.  Masked tiles are rare and have code of
+                    // their own, so that the common path is short and in one piece.
+                    auto weights = [&](auto masked_tag, float nm) {
+                        constexpr bool MASKED = decltype(masked_tag)::value;
+                        float s[2][16];
+                        top = -INFINITY;
+                        sum = 0.f;
+                        tmem_ld16(s_col, s[0]);
+                        tmem_ld_wait();
+                        tmem_ld16(s_col + 16, s[1]);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float2 y = ffma2(make_float2(s[j], s[j + 1]), a2, nm);
-                        const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-                        ls[(j >> 1) & 3] = fadd2(ls[(j >> 1) & 3], e);
-                        pk[j >> 1] = pack16<FP8>(e.x, e.y);
+                        for (int k = 0; k < 2; ++k) {
+                            float *v = s[k];
+                            if (k) tmem_ld_wait();
+                            if (CAP) {
+                                // the odd series where it holds (3.4e-7 relative), two
+                                // lanes per instruction; else 1 - 2 / (1 + e^2x)
+                                const float a1 = a * to_cap;
+                                float xa = 0.f;
+#pragma unroll
+                                for (int j = 0; j < 16; j += 2) xa = max3(xa, fabsf(v[j]), fabsf(v[j + 1]));
+                                if (__all_sync(0xffffffffu, xa * a1 < kTanhSmall)) {
+                                    const float2 k1 = make_float2(a1, a1), d7 = make_float2(cap2 * kTanhC7, cap2 * kTanhC7);
+                                    const float2 d5 = make_float2(cap2 * kTanhC5, cap2 * kTanhC5);
+                                    const float2 d3 = make_float2(cap2 * kTanhC3, cap2 * kTanhC3), d1 = make_float2(cap2, cap2);
+#pragma unroll
+                                    for (int j = 0; j < 16; j += 2) {
+                                        const float2 xx = fmul2(make_float2(v[j], v[j + 1]), k1), x2 = fmul2(xx, xx);
+                                        const float2 r = fmul2(xx, ffma2(x2, ffma2(x2, ffma2(x2, d7, d5), d3), d1));
+                                        v[j] = r.x;
+                                        v[j + 1] = r.y;
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j) v[j] = cap2 * tanh_fast(v[j] * a1);
+                                }
+                            }
+                            if (MASKED) {
+                                const int seen = limit - t * kKeys - q4 * 32 - k * 16; // of the 16
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    if (j >= seen) v[j] = -INFINITY;
+                            }
+                            const float b = CAP ? 1.f : a;
+                            const float2 a2 = make_float2(b, b), n2 = make_float2(nm, nm);
+                            float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                            for (int j = 0; j < 16; j += 2) {
+                                const float2 y = ffma2(make_float2(v[j], v[j + 1]), a2, n2);
+                                mx[(j >> 1) & 1] = max3(mx[(j >> 1) & 1], y.x, y.y);
+                                const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                                ls[(j >> 1) & 1] = fadd2(ls[(j >> 1) & 1], e);
+                                pk[k * 8 + (j >> 1)] = pack16<FP8>(e.x, e.y);
+                            }
+                            const float2 l2 = fadd2(ls[0], ls[1]);
+                            sum += l2.x + l2.y;
+                            top = max3(top, mx[0], mx[1]);
+                        }
+                    };
+#pragma unroll 1
+                    for (;;) {
+                        const float base = m == -INFINITY ? 0.f : m;
+                        if (masked) weights(std::true_type{}, C::kPBias - base);
+                        else weights(std::false_type{}, C::kPBias - base);
+                        // a first logit, or one far above the reference
+                        const bool need = top > (m == -INFINITY ? -INFINITY : C::kPBias + C::kLazy);
+                        if (!__any_sync(0xffffffffu, need)) break;
+                        float f = 1.f;
+                        if (need) {
+                            const float m_new = base + (top - C::kPBias);
+                            f = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
+                            m = m_new;
+                            l *= f;
+                        }
+                        if (q4 >= 2) { // keys 0-63 of this tile are in O, or on their way
+                            if (!(ok = wait_all(bars.pv_half + x, gx & 1))) break;
+                            tc_fence_after();
+                        }
+                        if (q4 >= 2 || t > c.t0) scale_o(f);
+                        if (q4 & 1) {
+                            // the quarter before is stored, but not handed over
+                            float w[16];
+                            uint32_t u[16];
+                            const uint32_t f2 = pack16<FP8>(f, f);
+                            tmem_ld16(p_col - 16, w);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                if (FP8) {
+                                    const uint32_t wi = __float_as_uint(w[j]);
+                                    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&wi), *reinterpret_cast<const __half2 *>(&f2));
+                                    u[j] = *reinterpret_cast<const uint32_t *>(&r);
+                                } else {
+                                    u[j] = mul_bf16x2(__float_as_uint(w[j]), f2);
+                                }
+                            }
+                            tmem_st16(p_col - 16, u);
+                        }
                     }
-                    tmem_st16(s_col + k * 16, pk);
-                    if (k & 1) {
-                        // keys 0-63, then 64-127: half of P V may start
+                    if (!ok) break;
+                    l += sum;
+                    // over columns of S that this thread is done with
+                    tmem_st16(p_col, pk);
+                    if (q4 & 1) {
                         tmem_st_wait();
                         tc_fence_before();
-                        mbar_arrive((k == 1 ? bars.p_half : bars.p_full) + x);
+                        mbar_arrive((q4 == 1 ? bars.p_half : bars.p_full) + x);
                     }
                 }
-                const float2 l2 = fadd2(fadd2(ls[0], ls[1]), fadd2(ls[2], ls[3]));
-                l += l2.x + l2.y;
-                ++gx;
             }
             g += n;
             if (!ok) break;
@@ -695,10 +725,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <bool FP8>
+template <bool FP8, bool CAP>
 cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s)
 {
-    auto kern = paged_rows_kernel<FP8>;
+    auto kern = paged_rows_kernel<FP8, CAP>;
     static std::atomic<uint64_t> set{0}; // devices whose copy of the kernel has its attribute
     const uint64_t bit = 1ull << p.device;
     if (!(set.load(std::memory_order_acquire) & bit)) {
@@ -716,7 +746,9 @@ cudaError_t launch_paged_rows(const PagedProblem &p, const PagedPart &part, int 
                               const void *tm_v, cudaStream_t s)
 {
     const CUtensorMap &k = *static_cast<const CUtensorMap *>(tm_k), &v = *static_cast<const CUtensorMap *>(tm_v);
-    return cache_dtype == RA_E4M3 ? go<true>(p, part, k, v, s) : go<false>(p, part, k, v, s);
+    if (p.soft_cap > 0.f)
+        return cache_dtype == RA_E4M3 ? go<true, true>(p, part, k, v, s) : go<false, true>(p, part, k, v, s);
+    return cache_dtype == RA_E4M3 ? go<true, false>(p, part, k, v, s) : go<false, false>(p, part, k, v, s);
 }
 
 } // namespace ra
