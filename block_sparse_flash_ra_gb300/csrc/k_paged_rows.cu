@@ -19,8 +19,8 @@
 // TMEM: S_A [0,128), S_B [128,256), O_A [256,384), O_B [384,512).
 //
 // 8-bit caches: codes times a power of two are exact in f16, so a key becomes
-// code * 2^(e - E) with E the largest exponent of its 64-key half tile, which
-// then scales that half's logits as one number; a value becomes
+// code * 2^(e - E) with E the largest exponent of its tile, which then scales
+// the tile's logits as one number; a value becomes
 // code * 2^(e_v - EV), EV one exponent for the whole segment (raised, and O
 // rescaled, when a tile's largest passes it by 2^7; f16 holds 448 * 2^7).
 // What f16 loses is below 2^-33 of the largest.  The rows of Q are scaled by a
@@ -69,15 +69,15 @@ struct Cfg {
     // q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], v_clear[2], pv_half[2], drain
     static constexpr int kNumBars = 8 + 8 + 14 + 1;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8 + 8;
-    static constexpr int kScaleOff = kMiscOff + 16; // E of K half tiles [4][2], EV of V tiles [2]
+    static constexpr int kScaleOff = kMiscOff + 16; // E of K tiles [4], EV of V tiles [2]
     static constexpr int kSmem = kScaleOff + 48 + 1024;
     static_assert(kSmem <= 232448 && kMiscOff % 16 == 0, "shared memory");
     static constexpr uint32_t kFmt = FP8 ? 0u : (1u << 7) | (1u << 10); // f16 or bf16 operands
     static constexpr uint32_t kIdescS = (1u << 4) | kFmt | (128u >> 3 << 17) | (128u >> 4 << 24);
     static constexpr uint32_t kIdescO = kIdescS | (1u << 16); // V is MN-major
-    // Weights are 2^kPBias at the row's reference and may grow by 2^kLazy: f16
-    // holds 2^15 and keeps all bits down to 2^-14; bf16 has fp32's range.
-    static constexpr float kPBias = FP8 ? 2.f : 0.f, kLazy = FP8 ? 13.f : 60.f;
+    // Weights are 2^kPBias at the row's reference and may grow to kMost (2^15,
+    // 2^60): f16 holds 2^15 and keeps all bits down to 2^-14; bf16 has fp32's range.
+    static constexpr float kPBias = FP8 ? 2.f : 0.f, kMost = FP8 ? 32768.f : 1.152921504606846976e18f;
 };
 
 struct Bars {
@@ -205,10 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::kMiscOff);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kMiscOff + 4);
     const WaitCtx ctx{abort_flag, p.status, p.timeout_ns};
-    // E by tile mod 4 and half: tile g + 4 is widened only after P V of tile
-    // g + 1, which both softmaxes of g precede; EV by V buffer
+    // E by tile mod 4: tile g + 4 is widened only after P V of tile g + 1, which
+    // both softmaxes of g precede; EV by V buffer
     volatile int *k_scale = reinterpret_cast<volatile int *>(smem + C::kScaleOff);
-    volatile int *v_scale = k_scale + 8;
+    volatile int *v_scale = k_scale + 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
@@ -427,36 +427,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    make_uint4(0, 0, 0, 0));
                     if (valid < kKeys) proxy_fence();
                     mbar_arrive(bars.v_clear + st);
-                } else if (st_raw == 0) {
-                    const uint32_t tile = smem_u32(smem + C::kKOff + st * C::kMat);
-                    if (!(ok = wait_all(bars.k_empty + st, ((g >> 1) & 1) ^ 1))) break;
-#pragma unroll 1
-                    for (int y = 0; y < 2; ++y) {
-                        if (!(ok = wait_all(raw_full + y, g & 1))) break;
-                        const int e = max(top_exp(ex + y * kHalf, valid - y * kHalf, lane), 1);
-                        widen_half(tile, raw + y * C::kRaw, ex + y * kHalf, y * kHalf, valid, e, w, lane);
-                        if (w == 0 && lane == 0) k_scale[(g & 3) * 2 + y] = e;
-                        mbar_arrive(raw_empty + y);
-                    }
-                    if (!ok) break;
-                    proxy_fence();
-                    mbar_arrive(bars.k_full + st);
                 } else {
-                    const uint32_t tile = smem_u32(smem + C::kVOff + st * C::kMat);
-                    if (!(ok = wait_all(bars.v_empty + st, ((g >> 1) & 1) ^ 1))) break;
+                    const uint32_t tile = smem_u32(smem + (st_raw ? C::kVOff : C::kKOff) + st * C::kMat);
+                    if (!(ok = wait_all((st_raw ? bars.v_empty : bars.k_empty) + st, ((g >> 1) & 1) ^ 1))) break;
                     if (!(ok = wait_all(raw_full + 0, g & 1))) break;
                     if (!(ok = wait_all(raw_full + 1, g & 1))) break;
-                    const int e = max(top_exp(ex, valid, lane), top_exp(ex + kHalf, valid - kHalf, lane));
-                    // 448 * 2^7 is the most that f16 holds; rows without a value do not count
-                    if (ev < 0 || e > ev + 7) ev = max(e, 1);
+                    // the tile's largest exponent (1 at least: its float is normal);
+                    // rows without a value do not count
+                    int e = max(max(top_exp(ex, valid, lane), top_exp(ex + kHalf, valid - kHalf, lane)), 1);
+                    if (st_raw) {
+                        // values keep the segment's: 448 * 2^7 is the most that f16 holds
+                        if (ev >= 0 && e <= ev + 7) e = ev;
+                        ev = e;
+                    }
 #pragma unroll 1
                     for (int y = 0; y < 2; ++y) {
-                        widen_half(tile, raw + y * C::kRaw, ex + y * kHalf, y * kHalf, valid, ev, w, lane);
+                        widen_half(tile, raw + y * C::kRaw, ex + y * kHalf, y * kHalf, valid, e, w, lane);
                         mbar_arrive(raw_empty + y);
                     }
-                    if (w == 0 && lane == 0) v_scale[st] = ev;
+                    if (w == 0 && lane == 0) {
+                        if (st_raw) v_scale[st] = e;
+                        else k_scale[g & 3] = e;
+                    }
                     proxy_fence();
-                    mbar_arrive(bars.v_full + st);
+                    mbar_arrive((st_raw ? bars.v_full : bars.k_full) + st);
                 }
             }
             if (!ok || !cursor_next(p, part, c, n)) break;
@@ -542,125 +536,143 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (t > c.t0 && e != ev) scale_o(ex2_approx((float)(ev - e)));
                     ev = e;
                 }
-                float a = a_row; // logit scale of the half's keys
-#pragma unroll 1
-                for (int q4 = 0; q4 < 4; ++q4) {
-                    const uint32_t s_col = lane_base + x * 128 + q4 * 32, p_col = lane_base + x * 128 + q4 * 16;
-                    if (FP8 && !(q4 & 1))
-                        a = a_row * __uint_as_float((uint32_t)k_scale[(gt & 3) * 2 + (q4 >> 1)] << 23);
-                    uint32_t pk[16];
-                    float top = -INFINITY, sum = 0.f;
-                    // The weights of 32 keys, at most 2^(kPBias + kLazy), with the
-                    // exponent's offset nm.  Masked tiles are rare and have code of
-                    // their own, so that the common path is short and in one piece.
-                    auto weights = [&](auto masked_tag, float nm) {
-                        constexpr bool MASKED = decltype(masked_tag)::value;
-                        float s[2][16];
-                        top = -INFINITY;
-                        sum = 0.f;
-                        tmem_ld16(s_col, s[0]);
-                        tmem_ld_wait();
-                        tmem_ld16(s_col + 16, s[1]);
+                float a = a_row; // the tile's logit scale
+                if (FP8) a *= __uint_as_float((uint32_t)k_scale[gt & 3] << 23);
+                const uint32_t s_tile = lane_base + x * 128;
+                uint32_t pk[16];
+                float sum = 0.f;
+                // Capped and masked logits of 16 keys from key j0 of the tile on, in
+                // units of b.  Masked tiles are rare and have code of their own, so
+                // that the common path is short and in one piece.
+                const float b = CAP ? 1.f : a;
+                auto logits = [&](auto masked_tag, float *v, int j0) {
+                    if (CAP) {
+                        // the odd series where it holds (3.4e-7 relative), two lanes
+                        // per instruction; else 1 - 2 / (1 + e^2x)
+                        const float a1 = a * to_cap;
+                        float xa = 0.f;
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            float *v = s[k];
-                            if (k) tmem_ld_wait();
-                            if (CAP) {
-                                // the odd series where it holds (3.4e-7 relative), two
-                                // lanes per instruction; else 1 - 2 / (1 + e^2x)
-                                const float a1 = a * to_cap;
-                                float xa = 0.f;
-#pragma unroll
-                                for (int j = 0; j < 16; j += 2) xa = max3(xa, fabsf(v[j]), fabsf(v[j + 1]));
-                                if (__all_sync(0xffffffffu, xa * a1 < kTanhSmall)) {
-                                    const float2 k1 = make_float2(a1, a1), d7 = make_float2(cap2 * kTanhC7, cap2 * kTanhC7);
-                                    const float2 d5 = make_float2(cap2 * kTanhC5, cap2 * kTanhC5);
-                                    const float2 d3 = make_float2(cap2 * kTanhC3, cap2 * kTanhC3), d1 = make_float2(cap2, cap2);
-#pragma unroll
-                                    for (int j = 0; j < 16; j += 2) {
-                                        const float2 xx = fmul2(make_float2(v[j], v[j + 1]), k1), x2 = fmul2(xx, xx);
-                                        const float2 r = fmul2(xx, ffma2(x2, ffma2(x2, ffma2(x2, d7, d5), d3), d1));
-                                        v[j] = r.x;
-                                        v[j + 1] = r.y;
-                                    }
-                                } else {
-#pragma unroll
-                                    for (int j = 0; j < 16; ++j) v[j] = cap2 * tanh_fast(v[j] * a1);
-                                }
-                            }
-                            if (MASKED) {
-                                const int seen = limit - t * kKeys - q4 * 32 - k * 16; // of the 16
-#pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    if (j >= seen) v[j] = -INFINITY;
-                            }
-                            const float b = CAP ? 1.f : a;
-                            const float2 a2 = make_float2(b, b), n2 = make_float2(nm, nm);
-                            float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                            float mx[2] = {-INFINITY, -INFINITY};
+                        for (int j = 0; j < 16; j += 2) xa = max3(xa, fabsf(v[j]), fabsf(v[j + 1]));
+                        if (__all_sync(0xffffffffu, xa * a1 < kTanhSmall)) {
+                            const float2 k1 = make_float2(a1, a1), d7 = make_float2(cap2 * kTanhC7, cap2 * kTanhC7);
+                            const float2 d5 = make_float2(cap2 * kTanhC5, cap2 * kTanhC5);
+                            const float2 d3 = make_float2(cap2 * kTanhC3, cap2 * kTanhC3), d1 = make_float2(cap2, cap2);
 #pragma unroll
                             for (int j = 0; j < 16; j += 2) {
-                                const float2 y = ffma2(make_float2(v[j], v[j + 1]), a2, n2);
-                                mx[(j >> 1) & 1] = max3(mx[(j >> 1) & 1], y.x, y.y);
-                                const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-                                ls[(j >> 1) & 1] = fadd2(ls[(j >> 1) & 1], e);
-                                pk[k * 8 + (j >> 1)] = pack16<FP8>(e.x, e.y);
+                                const float2 xx = fmul2(make_float2(v[j], v[j + 1]), k1), x2 = fmul2(xx, xx);
+                                const float2 r = fmul2(xx, ffma2(x2, ffma2(x2, ffma2(x2, d7, d5), d3), d1));
+                                v[j] = r.x;
+                                v[j + 1] = r.y;
                             }
-                            const float2 l2 = fadd2(ls[0], ls[1]);
-                            sum += l2.x + l2.y;
-                            top = max3(top, mx[0], mx[1]);
-                        }
-                    };
-#pragma unroll 1
-                    for (;;) {
-                        const float base = m == -INFINITY ? 0.f : m;
-                        if (masked) weights(std::true_type{}, C::kPBias - base);
-                        else weights(std::false_type{}, C::kPBias - base);
-                        // a first logit, or one far above the reference
-                        const bool need = top > (m == -INFINITY ? -INFINITY : C::kPBias + C::kLazy);
-                        if (!__any_sync(0xffffffffu, need)) break;
-                        float f = 1.f;
-                        if (need) {
-                            const float m_new = base + (top - C::kPBias);
-                            f = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
-                            m = m_new;
-                            l *= f;
-                        }
-                        if (q4 >= 2) { // keys 0-63 of this tile are in O, or on their way
-                            if (!(ok = wait_all(bars.pv_half + x, gx & 1))) break;
-                            tc_fence_after();
-                        }
-                        if (q4 >= 2 || t > c.t0) scale_o(f);
-                        if (q4 & 1) {
-                            // the quarter before is stored, but not handed over
-                            float w[16];
-                            uint32_t u[16];
-                            const uint32_t f2 = pack16<FP8>(f, f);
-                            tmem_ld16(p_col - 16, w);
-                            tmem_ld_wait();
+                        } else {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                if (FP8) {
-                                    const uint32_t wi = __float_as_uint(w[j]);
-                                    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&wi), *reinterpret_cast<const __half2 *>(&f2));
-                                    u[j] = *reinterpret_cast<const uint32_t *>(&r);
-                                } else {
-                                    u[j] = mul_bf16x2(__float_as_uint(w[j]), f2);
-                                }
-                            }
-                            tmem_st16(p_col - 16, u);
+                            for (int j = 0; j < 16; ++j) v[j] = cap2 * tanh_fast(v[j] * a1);
                         }
                     }
-                    if (!ok) break;
-                    l += sum;
-                    // over columns of S that this thread is done with
-                    tmem_st16(p_col, pk);
-                    if (q4 & 1) {
-                        tmem_st_wait();
-                        tc_fence_before();
-                        mbar_arrive((q4 == 1 ? bars.p_half : bars.p_full) + x);
+                    if (decltype(masked_tag)::value) {
+                        const int seen = limit - t * kKeys - j0; // of the 16
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (j >= seen) v[j] = -INFINITY;
                     }
-                }
+                };
+                // their weights, with the exponent's offset nm
+                auto weights = [&](const float *v, float nm, int k) {
+                    const float2 a2 = make_float2(b, b), n2 = make_float2(nm, nm);
+                    float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float2 y = ffma2(make_float2(v[j], v[j + 1]), a2, n2);
+                        const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                        ls[(j >> 1) & 1] = fadd2(ls[(j >> 1) & 1], e);
+                        pk[k * 8 + (j >> 1)] = pack16<FP8>(e.x, e.y);
+                    }
+                    const float2 l2 = fadd2(ls[0], ls[1]);
+                    sum += l2.x + l2.y;
+                };
+                auto quarters = [&](auto masked_tag) {
+                    float s0[16], s1[16];
+                    tmem_ld16(s_tile, s0);
+#pragma unroll 1
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        const uint32_t s_col = s_tile + q4 * 32, p_col = s_tile + q4 * 16;
+                        float nm = C::kPBias - (m == -INFINITY ? 0.f : m);
+                        sum = 0.f;
+                        tmem_ld_wait();
+                        tmem_ld16(s_col + 16, s1);
+                        logits(masked_tag, s0, q4 * 32);
+                        weights(s0, nm, 0);
+                        tmem_ld_wait();
+                        if (q4 < 3) tmem_ld16(s_col + 32, s0); // the next quarter's
+                        logits(masked_tag, s1, q4 * 32 + 16);
+                        weights(s1, nm, 1);
+                        // No weight is above kMost when their sum is not.  A
+                        // first logit sets the reference, one far above it raises it.
+                        const bool need = m == -INFINITY || !(sum <= C::kMost);
+                        if (__any_sync(0xffffffffu, need)) {
+                            float top = -INFINITY;
+#pragma unroll 1
+                            for (int k = 0; k < 2; ++k) {
+                                tmem_ld16(s_col + k * 16, s1);
+                                tmem_ld_wait();
+                                logits(masked_tag, s1, q4 * 32 + k * 16);
+#pragma unroll
+                                for (int j = 0; j < 16; j += 2) top = max3(top, s1[j], s1[j + 1]);
+                            }
+                            float f = 1.f;
+                            if (need && top * b > m) {
+                                f = ex2_approx(m - top * b); // 0 for a first one
+                                m = top * b;
+                                l *= f;
+                            }
+                            if (q4 >= 2) { // keys 0-63 of this tile are in O, or on their way
+                                if (!(ok = wait_all(bars.pv_half + x, gx & 1))) return;
+                                tc_fence_after();
+                            }
+                            if (q4 >= 2 || t > c.t0) scale_o(f);
+                            if (q4 & 1) {
+                                // the quarter before is stored, but not handed over
+                                float w[16];
+                                uint32_t u[16];
+                                const uint32_t f2 = pack16<FP8>(f, f);
+                                tmem_ld16(p_col - 16, w);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) {
+                                    if (FP8) {
+                                        const uint32_t wi = __float_as_uint(w[j]);
+                                        const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&wi),
+                                                                  *reinterpret_cast<const __half2 *>(&f2));
+                                        u[j] = *reinterpret_cast<const uint32_t *>(&r);
+                                    } else {
+                                        u[j] = mul_bf16x2(__float_as_uint(w[j]), f2);
+                                    }
+                                }
+                                tmem_st16(p_col - 16, u);
+                            }
+                            nm = C::kPBias - (m == -INFINITY ? 0.f : m);
+                            sum = 0.f;
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                tmem_ld16(s_col + k * 16, s1);
+                                tmem_ld_wait();
+                                logits(masked_tag, s1, q4 * 32 + k * 16);
+                                weights(s1, nm, k);
+                            }
+                        }
+                        l += sum;
+                        // over columns of S that this thread is done with
+                        tmem_st16(p_col, pk);
+                        if (q4 & 1) {
+                            tmem_st_wait();
+                            tc_fence_before();
+                            mbar_arrive((q4 == 1 ? bars.p_half : bars.p_full) + x);
+                        }
+                    }
+                };
+                if (masked) quarters(std::true_type{});
+                else quarters(std::false_type{});
+                if (!ok) break;
             }
             g += n;
             if (!ok) break;
