@@ -75,10 +75,11 @@ __global__ void __launch_bounds__(kThreads)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = threadIdx.x % D, row0 = threadIdx.x / D * OR;
     const float *q = static_cast<const float *>(p.q);
+    allow_next();
     report_lengths(p, part);
     PagedCursor c;
-    if (!cursor_begin(p, part, blockIdx.x, c)) return;
-    for (int n;; ) {
+    const bool any = cursor_begin(p, part, blockIdx.x, c);
+    for (int n; any;) {
         n = cursor_take(c);
         const int len = part.prefix ? paged_prefix_len(p) : paged_kv_len(p, c.b);
         __syncthreads(); // the last segment's shared arrays have been read
@@ -185,6 +186,7 @@ __global__ void __launch_bounds__(kThreads)
         }
         if (!cursor_next(p, part, c, n)) break;
     }
+    await_previous();
 }
 
 } // namespace
@@ -192,8 +194,7 @@ __global__ void __launch_bounds__(kThreads)
 cudaError_t launch_paged_f32(const PagedProblem &p, const PagedPart &part, int cache_dtype, cudaStream_t s)
 {
     auto go = [&](auto kern) {
-        kern<<<part.ctas, kThreads, 0, s>>>(p, part);
-        return cudaGetLastError();
+        return launch_paged(kern, p, part, kThreads, 0, s, p, part);
     };
     if (cache_dtype == RA_E4M3) return p.c.D == 64 ? go(paged_f32_kernel<64, true>) : go(paged_f32_kernel<128, true>);
     return p.c.D == 64 ? go(paged_f32_kernel<64, false>) : go(paged_f32_kernel<128, false>);

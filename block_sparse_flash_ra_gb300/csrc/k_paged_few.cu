@@ -180,10 +180,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
+    allow_next();
     report_lengths(p, part);
     __syncthreads();
     PagedCursor c;
-    if (!cursor_begin(p, part, blockIdx.x, c)) return;
+    if (!cursor_begin(p, part, blockIdx.x, c)) {
+        await_previous();
+        return;
+    }
 
     // ---- the loads ahead.  A box is as many keys as a page and a stage share.
     const int box = min(p.c.page, C::kKeys);
@@ -615,6 +619,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     if (!ok) // copies in flight land before the CTA's shared memory goes
         for (; used < issued; ++used)
             wait_drain(bars + used % C::kStages, (used / C::kStages) & 1, kDrainNs);
+    await_previous();
 }
 
 template <int D, bool FP8, int ROWS>
@@ -629,8 +634,7 @@ cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &
         if (e != cudaSuccess) return e;
         set.fetch_or(bit, std::memory_order_release);
     }
-    kern<<<part.ctas, kWarps * 32, Cfg<D, FP8>::kSmem, s>>>(k, v, p, part);
-    return cudaGetLastError();
+    return launch_paged(kern, p, part, kWarps * 32, Cfg<D, FP8>::kSmem, s, k, v, p, part);
 }
 
 } // namespace

@@ -7,8 +7,11 @@
 //   lse = (M + log2 L) ln 2,
 // summed in the order of the slots, so the result is the same every time.
 // A sink enters here or in the attention kernel's own final store, once.
-// One CTA per query row: its 4 warps take every fourth slot and meet in
-// shared memory.  Bound by latency: a few slots of D floats per row.
+// A CTA of 256 threads takes 8 rows, a thread four columns of one, or, when
+// there are few rows and their partial results many, one row, whose slots
+// are dealt to 8 warps that meet in shared memory.  Bound by latency, or by
+// reading the slots once.  Launched so that it starts while the attention
+// kernels drain (their results are waited for behind the search for slots).
 #include <math.h>
 
 #include "ra_paged.cuh"
@@ -16,7 +19,7 @@
 namespace ra {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kThreads = 256;
 
 // The partial results of a row: CTAs c0 .. c0 + n - 1, and where they lie.
 struct Slots {
@@ -24,10 +27,9 @@ struct Slots {
     int n, row;
     bool opens; // the segment is the first of c0's share
 
-    __device__ __forceinline__ size_t at(const PagedPart &part, int x) const
+    __device__ __forceinline__ size_t slot(const PagedPart &part, int x) const
     {
-        const long long slot = part.direct ? 2 * (c0 + x) + (x == 0 && !opens ? 1 : 0) : c0 + x + seg;
-        return (size_t)slot * part.slot_rows + row;
+        return (size_t)(part.direct ? 2 * (c0 + x) + (x == 0 && !opens ? 1 : 0) : c0 + x + seg);
     }
 };
 
@@ -61,84 +63,131 @@ __device__ __forceinline__ Slots find_slots(const PagedProblem &p, const PagedPa
     return s;
 }
 
-template <int D, typename T>
-__global__ void __launch_bounds__(kWarps * 32) paged_join_kernel(PagedProblem p, PagedPart a, PagedPart b2,
-                                                                 int n_parts)
+// Four output columns.
+__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v)
 {
-    constexpr int V = D / 32; // values per lane
-    __shared__ float o_s[kWarps][D], m_s[kWarps], l_s[kWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int hq = blockIdx.x % p.Hq, bi = blockIdx.x / p.Hq;
-    const int b = bi / p.Lq, i = bi - b * p.Lq;
-    if (i >= paged_q_len(p, b)) return;
-    float o[V] = {}, m = -INFINITY, l = 0.f;
-    for (int k = 0; k < n_parts; ++k) {
-        const PagedPart &part = k ? b2 : a;
-        const Slots s = find_slots(p, part, b, i, hq / p.G, hq % p.G);
-        if (part.direct && s.n == 1) return; // stored by the attention kernel
-        for (int x = warp; x < s.n; x += kWarps) {
-            const size_t at = s.at(part, x);
-            const float mx = part.ml[at * 2], lx = part.ml[at * 2 + 1];
-            float ox[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) ox[j] = part.o[at * D + j * 32 + lane];
-            const float top = fmaxf(m, mx), base = top == -INFINITY ? 0.f : top;
-            const float f = exp2f(m - base), fx = exp2f(mx - base);
-            l = l * f + lx * fx;
-#pragma unroll
-            for (int j = 0; j < V; ++j) o[j] = o[j] * f + ox[j] * fx;
-            m = top;
-        }
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
+// One source's contribution to a row's (o, m, l), by every `by`-th slot from
+// `from` on.
+template <int D>
+__device__ __forceinline__ void add_slots(const PagedPart &part, const Slots &s, int from, int by, int grp, float4 &o,
+                                          float &m, float &l)
+{
+#pragma unroll 4
+    for (int x = from; x < s.n; x += by) {
+        const size_t slot = s.slot(part, x);
+        const float2 ml = *reinterpret_cast<const float2 *>(part.ml + (slot * part.slot_rows + s.row) * 2);
+        // rows' columns lie together, or, from kernels with a thread per row,
+        // groups of four columns lie together over the rows
+        const size_t at = part.by_groups ? (slot * (D / 4) + grp) * part.slot_rows + s.row
+                                         : (slot * part.slot_rows + s.row) * (D / 4) + grp;
+        const float4 v = reinterpret_cast<const float4 *>(part.o)[at];
+        const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.f : top;
+        const float f = exp2f(m - base), fx = exp2f(ml.x - base);
+        l = l * f + ml.y * fx;
+        o = make_float4(o.x * f + v.x * fx, o.y * f + v.y * fx, o.z * f + v.z * fx, o.w * f + v.w * fx);
+        m = top;
     }
-    if (warp) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) o_s[warp][j * 32 + lane] = o[j];
-        if (lane == 0) {
-            m_s[warp] = m;
-            l_s[warp] = l;
+}
+
+template <int D, typename T, int ROWS>
+__global__ void __launch_bounds__(kThreads) paged_join_kernel(PagedProblem p, PagedPart a, PagedPart b2, int n_parts)
+{
+    constexpr int G4 = D / 4, SPLIT = kThreads / (ROWS * G4); // threads per row; shares of its slots
+    static_assert(SPLIT >= 1, "a CTA holds its rows");
+    __shared__ Slots slots_s[ROWS][2];
+    __shared__ int place_s[ROWS]; // (b * Lq + i) * Hq + hq, or -1
+    __shared__ float4 o_s[SPLIT > 1 ? kThreads : 1];
+    __shared__ float2 ml_s[SPLIT > 1 ? SPLIT * ROWS : 1];
+    // rows are numbered as the prefix has them, ((b * Lq + i) * G + g), by kv
+    // head, so that neighbours share a segment
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per_head = p.B * p.Lq * p.G, blocks = (per_head + ROWS - 1) / ROWS;
+    const int h = blockIdx.x / blocks, n0 = (blockIdx.x - h * blocks) * ROWS;
+    if (warp < ROWS) { // a warp per row looks for its slots
+        const int n = n0 + warp;
+        int place = -1;
+        if (n < per_head) {
+            const int b = n / (p.Lq * p.G), in_seq = n - b * p.Lq * p.G, i = in_seq / p.G, g = in_seq - i * p.G;
+            if (i < paged_q_len(p, b)) {
+                place = (b * p.Lq + i) * p.Hq + h * p.G + g;
+                for (int k = 0; k < n_parts; ++k) {
+                    const PagedPart &part = k ? b2 : a;
+                    const Slots s = find_slots(p, part, b, i, h, g);
+                    if (part.direct && s.n == 1) place = -1; // stored by the attention kernel
+                    if (lane == 0) slots_s[warp][k] = s;
+                }
+            }
         }
+        if (lane == 0) place_s[warp] = place;
     }
     __syncthreads();
-    if (warp) return;
-    float top = m;
+    // the attention kernels' results from here on
+    await_previous();
+    const int r = threadIdx.x % ROWS, grp = threadIdx.x / ROWS % G4, split = threadIdx.x / (ROWS * G4);
+    const int place = place_s[r];
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = -INFINITY, l = 0.f;
+    if (place >= 0)
+        for (int k = 0; k < n_parts; ++k) add_slots<D>(k ? b2 : a, slots_s[r][k], split, SPLIT, grp, o, m, l);
+    if (SPLIT > 1) {
+        o_s[threadIdx.x] = o;
+        if (grp == 0) ml_s[split * ROWS + r] = make_float2(m, l);
+        __syncthreads();
+        if (split) return;
+        float top = m;
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, m_s[w]);
-    const float sink = p.sinks ? p.sinks[hq] * kLog2e : -INFINITY;
-    top = fmaxf(top, sink);
-    const float base = top == -INFINITY ? 0.f : top;
-    const float f = exp2f(m - base);
-    l = l * f + exp2f(sink - base);
+        for (int x = 1; x < SPLIT; ++x) top = fmaxf(top, ml_s[x * ROWS + r].x);
+        const float base = top == -INFINITY ? 0.f : top, f = exp2f(m - base);
+        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+        l *= f;
 #pragma unroll
-    for (int j = 0; j < V; ++j) o[j] *= f;
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-        const float fw = exp2f(m_s[w] - base);
-        l += l_s[w] * fw;
-#pragma unroll
-        for (int j = 0; j < V; ++j) o[j] += o_s[w][j * 32 + lane] * fw;
+        for (int x = 1; x < SPLIT; ++x) {
+            const float2 ml = ml_s[x * ROWS + r];
+            const float4 v = o_s[x * ROWS * G4 + threadIdx.x];
+            const float fx = exp2f(ml.x - base);
+            l += ml.y * fx;
+            o = make_float4(o.x + v.x * fx, o.y + v.y * fx, o.z + v.z * fx, o.w + v.w * fx);
+        }
+        m = top;
     }
-    T *out = static_cast<T *>(p.out) + (size_t)blockIdx.x * D;
-#pragma unroll
-    for (int j = 0; j < V; ++j) out[j * 32 + lane] = (T)(l == 0.f ? 0.f : o[j] / l);
-    if (lane == 0)
-        p.lse[((size_t)b * p.Hq + hq) * p.Lq + i] = l == 0.f ? -INFINITY : (base + log2f(l)) * kLn2;
+    if (place < 0) return;
+    const int hq = place % p.Hq, bi = place / p.Hq;
+    if (p.sinks) {
+        const float sink = p.sinks[hq] * kLog2e, top = fmaxf(m, sink), f = exp2f(m - top);
+        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+        l = l * f + exp2f(sink - top);
+        m = top;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    store4(static_cast<T *>(p.out) + (size_t)place * D + grp * 4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    if (grp == 0) p.lse[((size_t)(bi / p.Lq) * p.Hq + hq) * p.Lq + bi % p.Lq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+template <int D, typename T>
+cudaError_t go(const PagedProblem &p, const PagedPart *parts, int n_parts, cudaStream_t s)
+{
+    const PagedPart &a = parts[0], &b = parts[n_parts - 1];
+    const long long per_head = (long long)p.B * p.Lq * p.G, rows = per_head * p.c.Hkv;
+    // 8 rows in a CTA read whole sectors and share the search for slots; below
+    // one such CTA per SM, a row's own slots are what there is to spread
+    // (2048 rows: 12-24 us with a row per CTA, 7-12 us with 8; 256 rows: 7 us)
+    if (rows >= 8 * 152)
+        return launch_dependent(paged_join_kernel<D, T, 8>, (unsigned)((per_head + 7) / 8 * p.c.Hkv), kThreads, 0, s, p, a, b,
+                                n_parts);
+    return launch_dependent(paged_join_kernel<D, T, 1>, (unsigned)rows, kThreads, 0, s, p, a, b, n_parts);
 }
 
 } // namespace
 
-cudaError_t launch_paged_join(const PagedProblem &p, const PagedPart *parts, int n_parts, int dtype,
-                              cudaStream_t s)
+cudaError_t launch_paged_join(const PagedProblem &p, const PagedPart *parts, int n_parts, int dtype, cudaStream_t s)
 {
-    const unsigned grid = (unsigned)p.B * p.Lq * p.Hq;
-    const PagedPart &a = parts[0], &b = parts[n_parts - 1];
-    if (dtype == RA_BF16) {
-        if (p.c.D == 64) paged_join_kernel<64, __nv_bfloat16><<<grid, kWarps * 32, 0, s>>>(p, a, b, n_parts);
-        else paged_join_kernel<128, __nv_bfloat16><<<grid, kWarps * 32, 0, s>>>(p, a, b, n_parts);
-    } else {
-        if (p.c.D == 64) paged_join_kernel<64, float><<<grid, kWarps * 32, 0, s>>>(p, a, b, n_parts);
-        else paged_join_kernel<128, float><<<grid, kWarps * 32, 0, s>>>(p, a, b, n_parts);
-    }
-    return cudaGetLastError();
+    if (dtype == RA_BF16)
+        return p.c.D == 64 ? go<64, __nv_bfloat16>(p, parts, n_parts, s) : go<128, __nv_bfloat16>(p, parts, n_parts, s);
+    return p.c.D == 64 ? go<64, float>(p, parts, n_parts, s) : go<128, float>(p, parts, n_parts, s);
 }
 
 } // namespace ra

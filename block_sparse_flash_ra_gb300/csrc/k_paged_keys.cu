@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
+    allow_next();
     report_lengths(p, part);
     tc_fence_before();
     __syncthreads();
@@ -677,6 +678,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
             if (!cursor_next(p, part, c, n)) break;
         }
     }
+    await_previous();
     tc_fence_before();
     __syncthreads();
     if (warp == C::kMmaWarp) {
@@ -697,8 +699,7 @@ cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &
         if (e != cudaSuccess) return e;
         set.fetch_or(bit, std::memory_order_release);
     }
-    kern<<<part.ctas, Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kSmem, s>>>(k, v, p, part);
-    return cudaGetLastError();
+    return launch_paged(kern, p, part, Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kSmem, s, k, v, p, part);
 }
 
 } // namespace

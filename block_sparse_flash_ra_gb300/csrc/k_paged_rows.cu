@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
+    allow_next();
     report_lengths(p, part);
     tc_fence_before();
     __syncthreads();
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int place = row.counts ? (row.b * p.Lq + row.i) * p.Hq + c.h * p.G + row.g : -1;
                 if (row.counts) limit = min(row.limit, len);
                 const int ch = lane & 15;
-#pragma unroll 4
+#pragma unroll 8
                 for (int it = 0; it < 16; ++it) {
                     const int r = 2 * it + (lane >> 4), r_in = (warp & 3) * 32 + r;
                     const int src = __shfl_sync(0xffffffffu, place, r);
@@ -687,7 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float mr = m - C::kPBias; // l and O are relative to 2^mr
                 const float fv = FP8 ? __uint_as_float((uint32_t)ev << 23) : 1.f;
                 const bool final = stores_whole(part, c, n);
-                const size_t at = slot_row(part, c) + x * 128 + row_in;
+                const size_t slot = slot_row(part, c);
+                const int in_slot = x * 128 + row_in;
                 float f = fv;
                 if (final) {
                     if (p.sinks && row.counts) {
@@ -710,10 +712,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             dst[j] = make_uint4(pack_bf16x2(o[8 * j] * f, o[8 * j + 1] * f), pack_bf16x2(o[8 * j + 2] * f, o[8 * j + 3] * f),
                                                 pack_bf16x2(o[8 * j + 4] * f, o[8 * j + 5] * f), pack_bf16x2(o[8 * j + 6] * f, o[8 * j + 7] * f));
                     } else if (row.counts) {
-                        float4 *dst = reinterpret_cast<float4 *>(part.o + at * kD + k * 32);
+                        // groups of four columns over the rows: a warp's rows lie together
+                        float4 *dst = reinterpret_cast<float4 *>(part.o) + slot * (kD / 4) + (size_t)(k * 8) * part.slot_rows + in_slot;
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            dst[j] = make_float4(o[4 * j] * f, o[4 * j + 1] * f, o[4 * j + 2] * f, o[4 * j + 3] * f);
+                            dst[j * part.slot_rows] = make_float4(o[4 * j] * f, o[4 * j + 1] * f, o[4 * j + 2] * f, o[4 * j + 3] * f);
                     }
                     __syncwarp(); // the next read of TMEM is the whole warp's
                 }
@@ -722,12 +725,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (final)
                         p.lse[((size_t)row.b * p.Hq + hq) * p.Lq + row.i] = l == 0.f ? -INFINITY : (mr + log2f(l)) * kLn2;
                     else
-                        *reinterpret_cast<float2 *>(part.ml + at * 2) = make_float2(mr, l);
+                        *reinterpret_cast<float2 *>(part.ml + (slot + in_slot) * 2) = make_float2(mr, l);
                 }
             }
             if (!cursor_next(p, part, c, n)) break;
         }
     }
+    await_previous();
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
@@ -748,8 +752,7 @@ cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &
         if (e != cudaSuccess) return e;
         set.fetch_or(bit, std::memory_order_release);
     }
-    kern<<<part.ctas, kThreads, Cfg<FP8>::kSmem, s>>>(k, v, p, part);
-    return cudaGetLastError();
+    return launch_paged(kern, p, part, kThreads, Cfg<FP8>::kSmem, s, k, v, p, part);
 }
 
 } // namespace

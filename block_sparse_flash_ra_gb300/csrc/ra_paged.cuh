@@ -25,6 +25,11 @@
 
 namespace ra {
 
+// The next kernel of the stream may be placed beside this one.
+__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// The kernels before this one in the stream have ended (see launch_dependent).
+__device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // 2^(b - 127) of a cached row's scale byte; 255 marks a row without a value.
 // (0, which ra_kv_write does not store, is a subnormal power of two.)
 __device__ __forceinline__ float exp_byte_scale(uint32_t b)

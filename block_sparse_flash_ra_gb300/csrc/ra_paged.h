@@ -46,9 +46,44 @@ struct PagedPart {
     int seg_cost;  // what taking up a segment costs, in tiles
     int direct;    // 1: rows whose keys one CTA sees are stored by it
     int slot_rows; // rows that one partial result holds
-    float *o;      // (slots, slot_rows, D) unnormalised outputs
+    int by_groups; // o is (slots, D / 4, slot_rows, 4), not (slots, slot_rows, D)
+    float *o;      // unnormalised outputs
     float *ml;     // (slots, slot_rows, 2) row maximum (base-2 logits) and sum
 };
+
+// Launches a kernel that may start before its predecessor in the stream has
+// ended, once all of that kernel's CTAs have allowed it or are gone.  It
+// waits (griddepcontrol.wait) before it touches what came before it, and
+// every CTA waits before it ends, so that a kernel's end implies the end of
+// all before it.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                             const A &...args)
+{
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// An attention kernel's launch.  The sequences' own part comes first and is an
+// ordinary launch; the prefix's part depends on nothing of it and may run
+// beside its end.
+template <typename... P, typename... A>
+cudaError_t launch_paged(void (*kernel)(P...), const PagedProblem &, const PagedPart &part, unsigned block, size_t smem,
+                         cudaStream_t s, const A &...args)
+{
+    if (part.prefix) return launch_dependent(kernel, (unsigned)part.ctas, block, smem, s, args...);
+    kernel<<<part.ctas, block, smem, s>>>(args...);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_kv_write(const PagedCache &c, int cache_dtype, const void *k, const void *v,
                             int dtype, int B, int L, size_t k_stride, size_t v_stride,

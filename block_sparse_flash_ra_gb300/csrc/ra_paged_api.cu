@@ -138,6 +138,7 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
             kernel = kRowsM;
             a.seg_cost = 3;
             a.row_block = 256;
+            a.by_groups = 1;
             a.tile = kPagedRowsTile;
             a.ctas = kSms;
         } else if (c->D == 128) {
