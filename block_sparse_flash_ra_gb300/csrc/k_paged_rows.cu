@@ -10,12 +10,13 @@
 // products (PV_A(g), S_A(g+1), PV_B(g), S_B(g+1)); a thread owns a row, and P
 // goes back to TMEM over the S it came from.
 //
-//   warps 0-3, 4-7  softmax of tiles A and B; they also gather the rows of Q
-//                   into shared memory and store the results
-//   warps 8-11      8-bit caches: widen K tiles to f16
-//   warps 12-15     the same for V; 16-bit caches: clear the values behind a
+//   warps 0-7, 8-15 softmax of tiles A and B, two threads to a row, 64 keys of
+//                   a tile each; they also gather the rows of Q into shared
+//                   memory and store the results
+//   warps 16-19     8-bit caches: widen K tiles to f16
+//   warps 20-23     the same for V; 16-bit caches: clear the values behind a
 //                   sequence's end
-//   warp 16         loads (a lane per page); warp 17 issues the products
+//   warp 24         loads (a lane per page); warp 25 issues the products
 // TMEM: S_A [0,128), S_B [128,256), O_A [256,384), O_B [384,512).
 //
 // 8-bit caches: codes times a power of two are exact in f16, so a key becomes
@@ -44,15 +45,15 @@ namespace ra {
 namespace {
 
 constexpr int kKeys = 128, kHalf = 64, kD = 128;
-constexpr int kThreads = 576;
-constexpr int kWideWarpK = 8, kWideWarpV = 12, kLoadWarp = 16, kMmaWarp = 17;
-// The softmax of a quarter tile (32 keys) takes the row's present reference
-// for granted: weights are computed at once, and only when a logit passes the
-// reference by 2^13 (2^60 in bf16) is it raised, O rescaled and the quarter
-// computed again from S, which its weights have not yet overwritten.  S comes 16 columns at a
-// time, the next on their way, so that every warp gets by with the 96
-// registers of 18 warps (with all 128 logits of a row in registers the
-// kernel spilled, and its unrolled loops starved on instruction fetches).
+constexpr int kThreads = 832;
+constexpr int kWideWarpK = 16, kWideWarpV = 20, kLoadWarp = 24, kMmaWarp = 25;
+// The softmax of 32 keys takes the row's present reference for granted:
+// weights are computed at once, and only when a logit passes the reference by
+// 2^13 (2^60 in bf16) -- one barrier with an or over the tile's 256 threads --
+// is it raised, O rescaled and the 32 keys computed again from S, which their
+// weights have not yet overwritten.  Two threads to a row halve the chain from
+// S to P, which the ping-pong of two tiles does not hide (one thread per row
+// took 2200 cycles of a tile's 4000; the products need 2460).
 
 template <bool FP8>
 struct Cfg {
@@ -66,11 +67,12 @@ struct Cfg {
     static constexpr int kExpOff = kRawOff + kRaws * kRaw; // 64 scale bytes per half
     static constexpr int kBarOff = kExpOff + kRaws * kHalf;
     // k_full[2], k_empty[2], v_full[2], v_empty[2], raw_full[4], raw_empty[4],
-    // q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], v_clear[2], pv_half[2], drain
-    static constexpr int kNumBars = 8 + 8 + 14 + 1;
+    // q_full[2], s_full[2], p_full[2][2], o_full[2], v_clear[2], drain
+    static constexpr int kNumBars = 8 + 8 + 12 + 1;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8 + 8;
     static constexpr int kScaleOff = kMiscOff + 16; // E of K tiles [4], EV of V tiles [2]
-    static constexpr int kSmem = kScaleOff + 48 + 1024;
+    static constexpr int kPairOff = kScaleOff + 48; // [tile][half][128] of the threads of a row
+    static constexpr int kSmem = kPairOff + 2 * 2 * 128 * 4;
     static_assert(kSmem <= 232448 && kMiscOff % 16 == 0, "shared memory");
     static constexpr uint32_t kFmt = FP8 ? 0u : (1u << 7) | (1u << 10); // f16 or bf16 operands
     static constexpr uint32_t kIdescS = (1u << 4) | kFmt | (128u >> 3 << 17) | (128u >> 4 << 24);
@@ -81,8 +83,8 @@ struct Cfg {
 };
 
 struct Bars {
-    uint64_t *k_full, *k_empty, *v_full, *v_empty, *raw_full, *raw_empty, *q_full, *s_full, *p_half, *p_full, *o_full,
-        *v_clear, *pv_half, *drain;
+    uint64_t *k_full, *k_empty, *v_full, *v_empty, *raw_full, *raw_empty, *q_full, *s_full, *p_full, *o_full,
+        *v_clear, *drain;
 };
 
 template <class C>
@@ -97,12 +99,10 @@ __device__ __forceinline__ Bars carve(uint8_t *smem)
     b.raw_empty = b.raw_full + 4;
     b.q_full = b.raw_empty + 4;
     b.s_full = b.q_full + 2;
-    b.p_half = b.s_full + 2;
-    b.p_full = b.p_half + 2;
-    b.o_full = b.p_full + 2;
+    b.p_full = b.s_full + 2; // [tile][half of the keys]
+    b.o_full = b.p_full + 4;
     b.v_clear = b.o_full + 2;
-    b.pv_half = b.v_clear + 2;
-    b.drain = b.pv_half + 2;
+    b.drain = b.v_clear + 2;
     return b;
 }
 
@@ -199,8 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       PagedProblem p, PagedPart part)
 {
     using C = Cfg<FP8>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     const Bars bars = carve<C>(smem);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::kMiscOff);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kMiscOff + 4);
@@ -216,13 +215,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bars.k_empty + s, 1);
             mbar_init(bars.v_full + s, FP8 ? 128 : 1);
             mbar_init(bars.v_empty + s, 1);
-            mbar_init(bars.q_full + s, 128);
+            mbar_init(bars.q_full + s, 256);
             mbar_init(bars.s_full + s, FP8 ? 2 : 1);
-            mbar_init(bars.p_half + s, 128);
-            mbar_init(bars.p_full + s, 128);
+            mbar_init(bars.p_full + 2 * s, 128);
+            mbar_init(bars.p_full + 2 * s + 1, 128);
             mbar_init(bars.o_full + s, 1);
             mbar_init(bars.v_clear + s, 128);
-            mbar_init(bars.pv_half + s, 1);
         }
         for (int s = 0; s < 4; ++s) {
             mbar_init(bars.raw_full + s, 1);
@@ -354,16 +352,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t vd = vd0 + (j & 1) * kStep;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    // keys 0-63 as soon as their weights are in TMEM
-                    if (!wait_all((hf ? bars.p_full : bars.p_half) + x, ph)) return false;
+                    // each half of the keys as soon as its weights are in TMEM
+                    if (!wait_all(bars.p_full + 2 * x + hf, ph)) return false;
                     tc_fence_after();
 #pragma unroll
                     for (int k4 = 0; k4 < 4; ++k4) {
                         const int kk = hf * 4 + k4;
-                        mma_ts_w(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, vd + (uint32_t)((kk * 2048) >> 4), C::kIdescO,
+                        mma_ts_w(tmem + 256 + x * 128, tmem + x * 128 + hf * 64 + k4 * 8, vd + (uint32_t)((kk * 2048) >> 4), C::kIdescO,
                                  (kk > 0 || !first) ? 1u : 0u);
                     }
-                    if (hf == 0) tc_commit_w(bars.pv_half + x);
                 }
                 return true;
             };
@@ -458,33 +455,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ---------------------------------------------------------------- softmax
-        const int x = warp >> 2; // tile A or B
+        // From the first wait that gave up on, a thread makes no wait any more
+        // and runs its loops out on whatever is there: the barrier of a tile's
+        // threads is still met by all of them, converged.
+        const int x = warp >> 3, y = (warp >> 2) & 1; // tile A or B; keys 64 y .. 64 y + 63
         const int row_in = (warp & 3) * 32 + lane;
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t s_half = lane_base + x * 128 + y * 64, o_half = lane_base + 256 + x * 128 + y * 64;
+        float *pair = reinterpret_cast<float *>(smem + C::kPairOff) + x * 256 + row_in; // + 128 for the other half
         const float cap2 = p.soft_cap * kLog2e, to_cap = p.soft_cap > 0.f ? kLn2 / p.soft_cap : 0.f;
         uint32_t g = 0, gx = 0, segs = 0;
         bool ok = true;
-        while (any && ok) {
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            if (ok) ok = mbar_wait(bar, parity, ctx);
+            __syncwarp();
+        };
+        // the tile's 256 threads meet
+        auto tile_sync = [&]() { asm volatile("barrier.sync %0, 256;" ::"r"(x + 1) : "memory"); };
+        auto tile_or = [&](bool v) {
+            uint32_t r;
+            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                         "barrier.red.or.pred q, %2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                         : "=r"(r)
+                         : "r"((uint32_t)v), "r"(x + 1)
+                         : "memory");
+            return r != 0;
+        };
+        while (any) {
             const int n = cursor_take(c), len = source_len(c.b);
-            const bool mine = x == 0 || two_tiles(c); // uniform in the warpgroup
-            int limit = 0x7fffffff; // rows of no use need no mask
-            // ---- Q: 16 lanes take a row, 8 values each; row 2 it + y of the warp
-            // belongs to lane 2 it + y
+            const bool mine = x == 0 || two_tiles(c); // uniform over the tile's threads
+            int limit = len; // keys that the row sees
+            // ---- Q: 16 lanes take a row, 8 values each; a warp loads 16 rows,
+            // the other half's warp the other 16
             float a_row = p.scale * kLog2e;
             if (mine) {
                 const PagedRow row = paged_row(p, part, c, x * 128 + row_in);
                 const int place = row.counts ? (row.b * p.Lq + row.i) * p.Hq + c.h * p.G + row.g : -1;
                 if (row.counts) limit = min(row.limit, len);
                 const int ch = lane & 15;
-#pragma unroll 8
-                for (int it = 0; it < 16; ++it) {
-                    const int r = 2 * it + (lane >> 4), r_in = (warp & 3) * 32 + r;
-                    const int src = __shfl_sync(0xffffffffu, place, r);
-                    uint4 u = make_uint4(0, 0, 0, 0);
+                uint4 u[8];
+#pragma unroll
+                for (int it = 0; it < 8; ++it) {
+                    const int src = __shfl_sync(0xffffffffu, place, y * 16 + 2 * it + (lane >> 4));
+                    u[it] = make_uint4(0, 0, 0, 0);
                     if (src >= 0)
-                        u = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + (size_t)src * kD)[ch];
+                        u[it] = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + (size_t)src * kD)[ch];
+                }
+#pragma unroll
+                for (int it = 0; it < 8; ++it) {
+                    const int r_in = (warp & 3) * 32 + y * 16 + 2 * it + (lane >> 4);
                     if (FP8) {
-                        uint32_t v[4] = {u.x, u.y, u.z, u.w}, top = 0; // largest magnitude, as bf16 bits
+                        uint32_t v[4] = {u[it].x, u[it].y, u[it].z, u[it].w}, top = 0; // largest magnitude, as bf16 bits
 #pragma unroll
                         for (int k = 0; k < 4; ++k) top = max(top, max(v[k] & 0x7fffu, (v[k] >> 16) & 0x7fffu));
 #pragma unroll
@@ -494,57 +515,60 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             v[k] = pack16<true>(__uint_as_float(v[k] << 16) * inv, __uint_as_float(v[k] & 0xffff0000u) * inv);
-                        u = make_uint4(v[0], v[1], v[2], v[3]);
-                        const int e_row = __shfl_sync(0xffffffffu, e, (lane & 1) * 16);
-                        if (lane >> 1 == it) a_row *= __uint_as_float((uint32_t)(127 + e_row) << 23);
+                        u[it] = make_uint4(v[0], v[1], v[2], v[3]);
+                        if (ch == 0) pair[r_in - row_in] = __uint_as_float((uint32_t)(127 + e) << 23);
                     }
                     sts128(smem_u32(smem + C::kQOff + x * C::kMat) + (ch >> 3) * (kKeys * 128) + r_in * 128 +
                                (((ch & 7) ^ (r_in & 7)) << 4),
-                           u);
+                           u[it]);
                 }
                 proxy_fence();
             }
             mbar_arrive(bars.q_full + x);
-            const int all = min(__reduce_min_sync(0xffffffffu, limit), len);
+            if (FP8 && mine) {
+                tile_sync();
+                a_row *= pair[0];
+            }
+            const int all = __reduce_min_sync(0xffffffffu, limit);
 
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f; // l: of this thread's keys
             int ev = 0;
-            // O of this row times f (every product into it has completed)
+            // this thread's half of O's columns times f (every product into O
+            // has completed)
             auto scale_o = [&](float f) {
 #pragma unroll 1
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 4; ++k) {
                     float o[16];
-                    tmem_ld16(lane_base + 256 + x * 128 + k * 16, o);
+                    tmem_ld16(o_half + k * 16, o);
                     tmem_ld_wait();
                     uint32_t u[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(o[j] * f);
-                    tmem_st16(lane_base + 256 + x * 128 + k * 16, u);
+                    tmem_st16(o_half + k * 16, u);
                 }
                 tmem_st_wait();
             };
-            for (int t = c.t0; mine && ok && t < c.t0 + n; ++t, ++gx) {
+            for (int t = c.t0; mine && t < c.t0 + n; ++t, ++gx) {
                 const uint32_t gt = g + (t - c.t0); // the tile's number in this CTA
                 const int st = gt & 1;
                 const bool masked = all < (t + 1) * kKeys;
-                if (!(ok = wait_all(bars.s_full + x, gx & 1))) break;
+                wait(bars.s_full + x, gx & 1);
                 tc_fence_after();
+                float a = a_row; // the tile's logit scale
                 if (FP8) {
                     // the tile's values are wide by now or soon: P V waits for them anyway
-                    if (!(ok = wait_all(bars.v_full + st, (gt >> 1) & 1))) break;
+                    wait(bars.v_full + st, (gt >> 1) & 1);
                     const int e = v_scale[st];
                     // S of this tile completed after P V of the one before
                     if (t > c.t0 && e != ev) scale_o(ex2_approx((float)(ev - e)));
                     ev = e;
+                    a *= __uint_as_float((uint32_t)k_scale[gt & 3] << 23);
                 }
-                float a = a_row; // the tile's logit scale
-                if (FP8) a *= __uint_as_float((uint32_t)k_scale[gt & 3] << 23);
-                const uint32_t s_tile = lane_base + x * 128;
                 uint32_t pk[16];
                 float sum = 0.f;
-                // Capped and masked logits of 16 keys from key j0 of the tile on, in
-                // units of b.  Masked tiles are rare and have code of their own, so
-                // that the common path is short and in one piece.
+                // Capped and masked logits of 16 of the thread's keys, from its key j0
+                // on, in units of b.  Masked tiles are rare and have code of their own,
+                // so that the common path is short and in one piece.
                 const float b = CAP ? 1.f : a;
                 auto logits = [&](auto masked_tag, float *v, int j0) {
                     if (CAP) {
@@ -571,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (decltype(masked_tag)::value) {
-                        const int seen = limit - t * kKeys - j0; // of the 16
+                        const int seen = limit - t * kKeys - y * 64 - j0; // of the 16
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
                             if (j >= seen) v[j] = -INFINITY;
@@ -583,60 +607,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int j = 0; j < 16; j += 2) {
-                        const float2 y = ffma2(make_float2(v[j], v[j + 1]), a2, n2);
-                        const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                        const float2 e2 = ffma2(make_float2(v[j], v[j + 1]), a2, n2);
+                        const float2 e = make_float2(ex2_approx(e2.x), ex2_approx(e2.y));
                         ls[(j >> 1) & 1] = fadd2(ls[(j >> 1) & 1], e);
                         pk[k * 8 + (j >> 1)] = pack16<FP8>(e.x, e.y);
                     }
                     const float2 l2 = fadd2(ls[0], ls[1]);
                     sum += l2.x + l2.y;
                 };
-                auto quarters = [&](auto masked_tag) {
-                    float s0[16], s1[16];
-                    tmem_ld16(s_tile, s0);
+                auto keys32 = [&](auto masked_tag, int q) { // the thread's keys 32 q .. 32 q + 31
+                    const float nm = C::kPBias - (m == -INFINITY ? 0.f : m);
+                    sum = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float s[16];
+                        tmem_ld16(s_half + q * 32 + k * 16, s);
+                        tmem_ld_wait();
+                        logits(masked_tag, s, q * 32 + k * 16);
+                        weights(s, nm, k);
+                    }
+                };
+                auto half = [&](auto masked_tag) {
 #pragma unroll 1
-                    for (int q4 = 0; q4 < 4; ++q4) {
-                        const uint32_t s_col = s_tile + q4 * 32, p_col = s_tile + q4 * 16;
-                        float nm = C::kPBias - (m == -INFINITY ? 0.f : m);
-                        sum = 0.f;
-                        tmem_ld_wait();
-                        tmem_ld16(s_col + 16, s1);
-                        logits(masked_tag, s0, q4 * 32);
-                        weights(s0, nm, 0);
-                        tmem_ld_wait();
-                        if (q4 < 3) tmem_ld16(s_col + 32, s0); // the next quarter's
-                        logits(masked_tag, s1, q4 * 32 + 16);
-                        weights(s1, nm, 1);
-                        // No weight is above kMost when their sum is not.  A
-                        // first logit sets the reference, one far above it raises it.
-                        const bool need = m == -INFINITY || !(sum <= C::kMost);
-                        if (__any_sync(0xffffffffu, need)) {
+                    for (int q = 0; q < 2; ++q) {
+                        keys32(masked_tag, q);
+                        // No weight is above kMost when their sum is not.  A first logit
+                        // sets the reference, one far above it raises it.
+                        if (tile_or(m == -INFINITY || !(sum <= C::kMost))) {
                             float top = -INFINITY;
 #pragma unroll 1
                             for (int k = 0; k < 2; ++k) {
-                                tmem_ld16(s_col + k * 16, s1);
+                                float s[16];
+                                tmem_ld16(s_half + q * 32 + k * 16, s);
                                 tmem_ld_wait();
-                                logits(masked_tag, s1, q4 * 32 + k * 16);
+                                logits(masked_tag, s, q * 32 + k * 16);
 #pragma unroll
-                                for (int j = 0; j < 16; j += 2) top = max3(top, s1[j], s1[j + 1]);
+                                for (int j = 0; j < 16; j += 2) top = max3(top, s[j], s[j + 1]);
                             }
-                            float f = 1.f;
-                            if (need && top * b > m) {
-                                f = ex2_approx(m - top * b); // 0 for a first one
-                                m = top * b;
-                                l *= f;
-                            }
-                            if (q4 >= 2) { // keys 0-63 of this tile are in O, or on their way
-                                if (!(ok = wait_all(bars.pv_half + x, gx & 1))) return;
-                                tc_fence_after();
-                            }
-                            if (q4 >= 2 || t > c.t0) scale_o(f);
-                            if (q4 & 1) {
-                                // the quarter before is stored, but not handed over
+                            pair[y * 128] = top * b;
+                            tile_sync();
+                            const float m_new = max3(m, top * b, pair[(y ^ 1) * 128]);
+                            const float f = m == m_new ? 1.f : ex2_approx(m - m_new); // 0 for a first one
+                            m = m_new;
+                            l *= f;
+                            if (t > c.t0) scale_o(f);
+                            if (q) {
+                                // the thread's first 32 keys are stored, but not handed over
                                 float w[16];
                                 uint32_t u[16];
                                 const uint32_t f2 = pack16<FP8>(f, f);
-                                tmem_ld16(p_col - 16, w);
+                                tmem_ld16(s_half, w);
                                 tmem_ld_wait();
 #pragma unroll
                                 for (int j = 0; j < 16; ++j) {
@@ -649,48 +669,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         u[j] = mul_bf16x2(__float_as_uint(w[j]), f2);
                                     }
                                 }
-                                tmem_st16(p_col - 16, u);
+                                tmem_st16(s_half, u);
                             }
-                            nm = C::kPBias - (m == -INFINITY ? 0.f : m);
-                            sum = 0.f;
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                tmem_ld16(s_col + k * 16, s1);
-                                tmem_ld_wait();
-                                logits(masked_tag, s1, q4 * 32 + k * 16);
-                                weights(s1, nm, k);
-                            }
+                            keys32(masked_tag, q);
                         }
                         l += sum;
                         // over columns of S that this thread is done with
-                        tmem_st16(p_col, pk);
-                        if (q4 & 1) {
-                            tmem_st_wait();
-                            tc_fence_before();
-                            mbar_arrive((q4 == 1 ? bars.p_half : bars.p_full) + x);
-                        }
+                        tmem_st16(s_half + q * 16, pk);
                     }
                 };
-                if (masked) quarters(std::true_type{});
-                else quarters(std::false_type{});
-                if (!ok) break;
+                if (masked) half(std::true_type{});
+                else half(std::false_type{});
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(bars.p_full + 2 * x + y);
             }
             g += n;
-            if (!ok) break;
-            // ---- the segment's end: this row's result
+            // ---- the segment's end: this row's result, half of its columns
             if (mine) {
-                if (!(ok = wait_all(bars.o_full + x, segs & 1))) break;
+                wait(bars.o_full + x, segs & 1);
                 ++segs;
+                pair[y * 128] = l; // both threads of the row are done with its tiles
+                tile_sync();
+                l = pair[0] + pair[128];
                 tc_fence_after();
                 const PagedRow row = paged_row(p, part, c, x * 128 + row_in);
                 const int hq = c.h * p.G + row.g;
                 const size_t place = ((size_t)row.b * p.Lq + row.i) * p.Hq + hq;
                 float mr = m - C::kPBias; // l and O are relative to 2^mr
-                const float fv = FP8 ? __uint_as_float((uint32_t)ev << 23) : 1.f;
                 const bool final = stores_whole(part, c, n);
                 const size_t slot = slot_row(part, c);
                 const int in_slot = x * 128 + row_in;
-                float f = fv;
+                float f = FP8 ? __uint_as_float((uint32_t)ev << 23) : 1.f;
                 if (final) {
                     if (p.sinks && row.counts) {
                         const float sink = p.sinks[hq] * kLog2e, top = fmaxf(mr, sink);
@@ -702,31 +712,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll 1
                 for (int k = 0; k < 4; ++k) {
-                    float o[32];
-                    tmem_ld32(lane_base + 256 + x * 128 + k * 32, o);
+                    float o[16];
+                    tmem_ld16(o_half + k * 16, o);
                     tmem_ld_wait();
+                    const int col = y * 64 + k * 16;
                     if (row.counts && final) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + place * kD + k * 32);
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + place * kD + col);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
+                        for (int j = 0; j < 2; ++j)
                             dst[j] = make_uint4(pack_bf16x2(o[8 * j] * f, o[8 * j + 1] * f), pack_bf16x2(o[8 * j + 2] * f, o[8 * j + 3] * f),
                                                 pack_bf16x2(o[8 * j + 4] * f, o[8 * j + 5] * f), pack_bf16x2(o[8 * j + 6] * f, o[8 * j + 7] * f));
                     } else if (row.counts) {
                         // groups of four columns over the rows: a warp's rows lie together
-                        float4 *dst = reinterpret_cast<float4 *>(part.o) + slot * (kD / 4) + (size_t)(k * 8) * part.slot_rows + in_slot;
+                        float4 *dst = reinterpret_cast<float4 *>(part.o) + slot * (kD / 4) + (size_t)(col / 4) * part.slot_rows + in_slot;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
+                        for (int j = 0; j < 4; ++j)
                             dst[j * part.slot_rows] = make_float4(o[4 * j] * f, o[4 * j + 1] * f, o[4 * j + 2] * f, o[4 * j + 3] * f);
                     }
                     __syncwarp(); // the next read of TMEM is the whole warp's
                 }
                 tc_fence_before();
-                if (row.counts) {
+                if (row.counts && y == 0) {
                     if (final)
                         p.lse[((size_t)row.b * p.Hq + hq) * p.Lq + row.i] = l == 0.f ? -INFINITY : (mr + log2f(l)) * kLn2;
                     else
                         *reinterpret_cast<float2 *>(part.ml + (slot + in_slot) * 2) = make_float2(mr, l);
                 }
+                tile_sync(); // pair is free again
             }
             if (!cursor_next(p, part, c, n)) break;
         }
