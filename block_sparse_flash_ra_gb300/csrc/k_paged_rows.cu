@@ -49,8 +49,8 @@ constexpr int kThreads = 832;
 constexpr int kWideWarpK = 16, kWideWarpV = 20, kLoadWarp = 24, kMmaWarp = 25;
 // The softmax of 32 keys takes the row's present reference for granted:
 // weights are computed at once, and only when a logit passes the reference by
-// 2^13 (2^60 in bf16) -- one barrier with an or over the tile's 256 threads --
-// is it raised, O rescaled and the 32 keys computed again from S, which their
+// 2^13 (2^60 in bf16) -- one barrier with an or over the two warps of 32 rows
+// -- is it raised, O rescaled and the 32 keys computed again from S, which their
 // weights have not yet overwritten.  Two threads to a row halve the chain from
 // S to P, which the ping-pong of two tiles does not hide (one thread per row
 // took 2200 cycles of a tile's 4000; the products need 2460).
@@ -67,8 +67,8 @@ struct Cfg {
     static constexpr int kExpOff = kRawOff + kRaws * kRaw; // 64 scale bytes per half
     static constexpr int kBarOff = kExpOff + kRaws * kHalf;
     // k_full[2], k_empty[2], v_full[2], v_empty[2], raw_full[4], raw_empty[4],
-    // q_full[2], s_full[2], p_full[2][2], o_full[2], v_clear[2], drain
-    static constexpr int kNumBars = 8 + 8 + 12 + 1;
+    // q_full[2], s_full[2], p_full[2], o_full[2], v_clear[2], drain
+    static constexpr int kNumBars = 8 + 8 + 10 + 1;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8 + 8;
     static constexpr int kScaleOff = kMiscOff + 16; // E of K tiles [4], EV of V tiles [2]
     static constexpr int kPairOff = kScaleOff + 48; // [tile][half][128] of the threads of a row
@@ -99,8 +99,8 @@ __device__ __forceinline__ Bars carve(uint8_t *smem)
     b.raw_empty = b.raw_full + 4;
     b.q_full = b.raw_empty + 4;
     b.s_full = b.q_full + 2;
-    b.p_full = b.s_full + 2; // [tile][half of the keys]
-    b.o_full = b.p_full + 4;
+    b.p_full = b.s_full + 2;
+    b.o_full = b.p_full + 2;
     b.v_clear = b.o_full + 2;
     b.drain = b.v_clear + 2;
     return b;
@@ -217,8 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bars.v_empty + s, 1);
             mbar_init(bars.q_full + s, 256);
             mbar_init(bars.s_full + s, FP8 ? 2 : 1);
-            mbar_init(bars.p_full + 2 * s, 128);
-            mbar_init(bars.p_full + 2 * s + 1, 128);
+            mbar_init(bars.p_full + s, 256);
             mbar_init(bars.o_full + s, 1);
             mbar_init(bars.v_clear + s, 128);
         }
@@ -350,18 +349,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto issue_pv = [&](int x, uint32_t j, uint32_t ph, bool first) -> bool {
                 const uint64_t vd = vd0 + (j & 1) * kStep;
+                if (!wait_all(bars.p_full + x, ph)) return false;
+                tc_fence_after();
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    // each half of the keys as soon as its weights are in TMEM
-                    if (!wait_all(bars.p_full + 2 * x + hf, ph)) return false;
-                    tc_fence_after();
-#pragma unroll
-                    for (int k4 = 0; k4 < 4; ++k4) {
-                        const int kk = hf * 4 + k4;
-                        mma_ts_w(tmem + 256 + x * 128, tmem + x * 128 + hf * 64 + k4 * 8, vd + (uint32_t)((kk * 2048) >> 4), C::kIdescO,
-                                 (kk > 0 || !first) ? 1u : 0u);
-                    }
-                }
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_ts_w(tmem + 256 + x * 128, tmem + x * 128 + (kk >> 2) * 64 + (kk & 3) * 8, vd + (uint32_t)((kk * 2048) >> 4),
+                             C::kIdescO, (kk > 0 || !first) ? 1u : 0u);
                 return true;
             };
             for (;;) {
@@ -378,7 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_commit_w(bars.k_empty + (g & 1));
                 for (int t = 0; t < n; ++t, ++g) {
                     const bool more = t + 1 < n;
-                    if (!(ok = wait_all((FP8 ? bars.v_full : bars.v_clear) + (g & 1), (g >> 1) & 1))) break;
+                    // (8-bit: the softmax waited for the wide V before it handed over P)
+                    if (!FP8 && !(ok = wait_all(bars.v_clear + (g & 1), (g >> 1) & 1))) break;
                     if (!(ok = issue_pv(0, g, g & 1, t == 0))) break;
                     if (!more) tc_commit_w(bars.o_full + 0);
                     if (more) {
@@ -456,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ---------------------------------------------------------------- softmax
         // From the first wait that gave up on, a thread makes no wait any more
-        // and runs its loops out on whatever is there: the barrier of a tile's
-        // threads is still met by all of them, converged.
+        // and runs its loops out on whatever is there: the barrier of two warps
+        // is still met by all of their threads, converged.
         const int x = warp >> 3, y = (warp >> 2) & 1; // tile A or B; keys 64 y .. 64 y + 63
         const int row_in = (warp & 3) * 32 + lane;
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -470,14 +464,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) ok = mbar_wait(bar, parity, ctx);
             __syncwarp();
         };
-        // the tile's 256 threads meet
-        auto tile_sync = [&]() { asm volatile("barrier.sync %0, 256;" ::"r"(x + 1) : "memory"); };
-        auto tile_or = [&](bool v) {
+        // the two warps of 32 rows meet
+        const int pair_bar = 1 + x * 4 + (warp & 3);
+        auto pair_sync = [&]() { asm volatile("barrier.sync %0, 64;" ::"r"(pair_bar) : "memory"); };
+        auto pair_or = [&](bool v) {
             uint32_t r;
             asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-                         "barrier.red.or.pred q, %2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                         "barrier.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                          : "=r"(r)
-                         : "r"((uint32_t)v), "r"(x + 1)
+                         : "r"((uint32_t)v), "r"(pair_bar)
                          : "memory");
             return r != 0;
         };
@@ -526,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             mbar_arrive(bars.q_full + x);
             if (FP8 && mine) {
-                tile_sync();
+                pair_sync();
                 a_row *= pair[0];
             }
             const int all = __reduce_min_sync(0xffffffffu, limit);
@@ -552,17 +547,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t gt = g + (t - c.t0); // the tile's number in this CTA
                 const int st = gt & 1;
                 const bool masked = all < (t + 1) * kKeys;
-                wait(bars.s_full + x, gx & 1);
-                tc_fence_after();
-                float a = a_row; // the tile's logit scale
+                float a = a_row, fv = 1.f; // the tile's logit scale; the change of EV
                 if (FP8) {
                     // the tile's values are wide by now or soon: P V waits for them anyway
                     wait(bars.v_full + st, (gt >> 1) & 1);
                     const int e = v_scale[st];
-                    // S of this tile completed after P V of the one before
-                    if (t > c.t0 && e != ev) scale_o(ex2_approx((float)(ev - e)));
+                    if (t > c.t0 && e != ev) fv = ex2_approx((float)(ev - e));
                     ev = e;
+                }
+                wait(bars.s_full + x, gx & 1);
+                tc_fence_after();
+                if (FP8) {
                     a *= __uint_as_float((uint32_t)k_scale[gt & 3] << 23);
+                    // S of this tile completed after P V of the one before
+                    if (fv != 1.f) scale_o(fv);
                 }
                 uint32_t pk[16];
                 float sum = 0.f;
@@ -633,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         keys32(masked_tag, q);
                         // No weight is above kMost when their sum is not.  A first logit
                         // sets the reference, one far above it raises it.
-                        if (tile_or(m == -INFINITY || !(sum <= C::kMost))) {
+                        if (pair_or(m == -INFINITY || !(sum <= C::kMost))) {
                             float top = -INFINITY;
 #pragma unroll 1
                             for (int k = 0; k < 2; ++k) {
@@ -645,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int j = 0; j < 16; j += 2) top = max3(top, s[j], s[j + 1]);
                             }
                             pair[y * 128] = top * b;
-                            tile_sync();
+                            pair_sync();
                             const float m_new = max3(m, top * b, pair[(y ^ 1) * 128]);
                             const float f = m == m_new ? 1.f : ex2_approx(m - m_new); // 0 for a first one
                             m = m_new;
@@ -682,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else half(std::false_type{});
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(bars.p_full + 2 * x + y);
+                mbar_arrive(bars.p_full + x);
             }
             g += n;
             // ---- the segment's end: this row's result, half of its columns
@@ -690,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(bars.o_full + x, segs & 1);
                 ++segs;
                 pair[y * 128] = l; // both threads of the row are done with its tiles
-                tile_sync();
+                pair_sync();
                 l = pair[0] + pair[128];
                 tc_fence_after();
                 const PagedRow row = paged_row(p, part, c, x * 128 + row_in);
@@ -738,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     else
                         *reinterpret_cast<float2 *>(part.ml + (slot + in_slot) * 2) = make_float2(mr, l);
                 }
-                tile_sync(); // pair is free again
+                pair_sync(); // pair is free again
             }
             if (!cursor_next(p, part, c, n)) break;
         }
