@@ -23,39 +23,38 @@ constexpr int kThreads = 256;
 
 // The partial results of a row: CTAs c0 .. c0 + n - 1, and where they lie.
 struct Slots {
-    long long c0, seg;
-    int n, row;
+    int c0, seg, n, row;
     bool opens; // the segment is the first of c0's share
 
     __device__ __forceinline__ size_t slot(const PagedPart &part, int x) const
     {
-        return (size_t)(part.direct ? 2 * (c0 + x) + (x == 0 && !opens ? 1 : 0) : c0 + x + seg);
+        return part.direct ? 2 * (c0 + x) + (x == 0 && !opens ? 1 : 0) : c0 + x + seg;
     }
 };
 
 __device__ __forceinline__ Slots find_slots(const PagedProblem &p, const PagedPart &part, int b, int i, int h,
                                             int g)
 {
-    const long long per_seq = (long long)part.n_rb * p.c.Hkv;
+    const int per_seq = part.n_rb * p.c.Hkv;
     const int n = (part.prefix ? b * p.Lq + i : i) * p.G + g;
     const int rb = n / part.row_block;
-    long long total, start, seg = (long long)rb * p.c.Hkv + h;
-    int tiles;
+    unsigned total, start;
+    int tiles, seg = rb * p.c.Hkv + h;
     if (part.prefix) {
         tiles = (paged_prefix_len(p) + part.tile - 1) / part.tile;
         total = per_seq * (tiles + part.seg_cost);
         start = seg * (tiles + part.seg_cost);
     } else {
         tiles = own_tiles(p, part, b);
-        long long before;
+        unsigned before;
         total = per_seq * own_places_sum(p, part, b, before);
         start = per_seq * before + seg * (tiles + part.seg_cost);
         seg += per_seq * b;
     }
     Slots s{0, seg, 0, n - rb * part.row_block, false};
     if (tiles == 0) return s;
-    const long long share = (total + part.ctas - 1) / part.ctas;
-    const long long first = start + part.seg_cost; // place of the first tile
+    const unsigned share = (total + part.ctas - 1) / part.ctas;
+    const unsigned first = start + part.seg_cost; // place of the first tile
     s.c0 = first / share;
     s.n = (int)((first + tiles - 1) / share - s.c0) + 1;
     // a share that begins before `start` begins with another segment's tile

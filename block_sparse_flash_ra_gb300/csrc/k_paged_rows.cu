@@ -496,11 +496,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (src >= 0)
                         u[it] = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + (size_t)src * kD)[ch];
                 }
-#pragma unroll
-                for (int it = 0; it < 8; ++it) {
+#pragma unroll 1
+                for (int it = 0; it < 8; ++it) { // one piece of code for all: a cold fetch costs more than it
                     const int r_in = (warp & 3) * 32 + y * 16 + 2 * it + (lane >> 4);
+                    uint32_t v[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+                    for (int k = 0; k < 7; ++k) u[k] = u[k + 1];
                     if (FP8) {
-                        uint32_t v[4] = {u[it].x, u[it].y, u[it].z, u[it].w}, top = 0; // largest magnitude, as bf16 bits
+                        uint32_t top = 0; // largest magnitude, as bf16 bits
 #pragma unroll
                         for (int k = 0; k < 4; ++k) top = max(top, max(v[k] & 0x7fffu, (v[k] >> 16) & 0x7fffu));
 #pragma unroll
@@ -510,12 +513,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             v[k] = pack16<true>(__uint_as_float(v[k] << 16) * inv, __uint_as_float(v[k] & 0xffff0000u) * inv);
-                        u[it] = make_uint4(v[0], v[1], v[2], v[3]);
                         if (ch == 0) pair[r_in - row_in] = __uint_as_float((uint32_t)(127 + e) << 23);
                     }
                     sts128(smem_u32(smem + C::kQOff + x * C::kMat) + (ch >> 3) * (kKeys * 128) + r_in * 128 +
                                (((ch & 7) ^ (r_in & 7)) << 4),
-                           u[it]);
+                           make_uint4(v[0], v[1], v[2], v[3]));
                 }
                 proxy_fence();
             }
@@ -628,10 +630,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto half = [&](auto masked_tag) {
 #pragma unroll 1
                     for (int q = 0; q < 2; ++q) {
-                        keys32(masked_tag, q);
-                        // No weight is above kMost when their sum is not.  A first logit
-                        // sets the reference, one far above it raises it.
-                        if (pair_or(m == -INFINITY || !(sum <= C::kMost))) {
+#pragma unroll 1
+                        for (int pass = 0;; ++pass) {
+                            keys32(masked_tag, q);
+                            // No weight is above kMost when their sum is not.  A first
+                            // logit sets the reference, one far above it raises it.
+                            if (pass || !pair_or(m == -INFINITY || !(sum <= C::kMost))) break;
                             float top = -INFINITY;
 #pragma unroll 1
                             for (int k = 0; k < 2; ++k) {
@@ -669,7 +673,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 }
                                 tmem_st16(s_half, u);
                             }
-                            keys32(masked_tag, q);
                         }
                         l += sum;
                         // over columns of S that this thread is done with

@@ -78,27 +78,23 @@ __device__ __forceinline__ int own_places(const PagedProblem &p, const PagedPart
 }
 
 // Sums of own_places over all sequences and, in `before`, over those below
-// `b_end`; by one converged warp.
-__device__ __forceinline__ long long own_places_sum(const PagedProblem &p, const PagedPart &part,
-                                                    int b_end, long long &before)
+// `b_end`; by one converged warp.  (The host refuses problems whose line could
+// have 2^31 places.)
+__device__ __forceinline__ unsigned own_places_sum(const PagedProblem &p, const PagedPart &part,
+                                                   int b_end, unsigned &before)
 {
-    long long n = 0, lo = 0;
+    unsigned n = 0, lo = 0;
+#pragma unroll 1
     for (int b = threadIdx.x & 31; b < p.B; b += 32) {
         const int x = own_places(p, part, b);
         n += x;
         if (b < b_end) lo += x;
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        n += __shfl_xor_sync(0xffffffffu, n, o);
-        lo += __shfl_xor_sync(0xffffffffu, lo, o);
-    }
-    before = lo;
-    return n;
+    before = __reduce_add_sync(0xffffffffu, lo);
+    return __reduce_add_sync(0xffffffffu, n);
 }
 
-// A place on the line, kept by every thread of a CTA alike.  (A share is far
-// below 2^31 places: that many tiles would keep a CTA busy for hours.)
+// A place on the line, kept by every thread of a CTA alike.
 struct PagedCursor {
     int left;      // places from the next tile on that are the CTA's
     int b, rb, h;  // the segment
@@ -115,27 +111,28 @@ __device__ __forceinline__ bool cursor_begin(const PagedProblem &p, const PagedP
     const int per_seq = part.n_rb * p.c.Hkv; // segments of one sequence
     const int lane = threadIdx.x & 31;
     int prefix_tiles = 0;
-    long long total, before = 0;
+    unsigned total, before = 0;
     if (part.prefix) {
         prefix_tiles = (paged_prefix_len(p) + part.tile - 1) / part.tile;
-        total = prefix_tiles ? (long long)per_seq * (prefix_tiles + part.seg_cost) : 0;
+        total = prefix_tiles ? per_seq * (prefix_tiles + part.seg_cost) : 0;
     } else {
         total = own_places_sum(p, part, 0, before) * per_seq;
     }
-    const long long share = (total + part.ctas - 1) / part.ctas;
-    const long long at = share * cta, end = at + share < total ? at + share : total;
+    const unsigned share = (total + part.ctas - 1) / part.ctas;
+    const unsigned at = share * cta, end = min(at + share, total);
     if (at >= end) return false;
     c.b = 0;
     c.tiles = prefix_tiles;
     if (!part.prefix) {
         // 32 sequences at a time: the first whose running total passes `at`
+#pragma unroll 1
         for (int b0 = 0;; b0 += 32) {
             const int b = b0 + lane;
             const int n = b < p.B ? own_places(p, part, b) : 0;
-            long long run = (long long)n * per_seq;
+            unsigned run = n * per_seq;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const long long x = __shfl_up_sync(0xffffffffu, run, o);
+                const unsigned x = __shfl_up_sync(0xffffffffu, run, o);
                 if (lane >= o) run += x;
             }
             const unsigned past = __ballot_sync(0xffffffffu, before + run > at);
@@ -143,15 +140,15 @@ __device__ __forceinline__ bool cursor_begin(const PagedProblem &p, const PagedP
                 const int l = __ffs(past) - 1, places = __shfl_sync(0xffffffffu, n, l);
                 c.b = b0 + l;
                 c.tiles = places - part.seg_cost;
-                before += __shfl_sync(0xffffffffu, run, l) - (long long)places * per_seq;
+                before += __shfl_sync(0xffffffffu, run, l) - places * per_seq;
                 break;
             }
             before += __shfl_sync(0xffffffffu, run, 31);
         }
     }
     const int places = c.tiles + part.seg_cost;
-    const int in_seq = (int)((at - before) / places);
-    const int off = (int)(at - before - (long long)in_seq * places);
+    const int in_seq = (at - before) / (unsigned)places;
+    const int off = at - before - in_seq * places;
     c.t0 = max(off - part.seg_cost, 0);
     c.left = (int)(end - at) - max(part.seg_cost - off, 0);
     c.rb = in_seq / p.c.Hkv;

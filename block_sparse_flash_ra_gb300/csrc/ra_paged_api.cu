@@ -9,6 +9,8 @@
 namespace ra {
 namespace {
 
+int refuse(int code, const char *msg) { return set_last_error(code, msg); }
+
 template <typename... A>
 int refuse(int code, const char *fmt, A... a)
 {
@@ -16,6 +18,8 @@ int refuse(int code, const char *fmt, A... a)
     snprintf(msg, sizeof(msg), fmt, a...);
     return set_last_error(code, msg);
 }
+
+const char *const kTooLarge = "too many query rows and pages for one call: split the batch";
 
 bool is_aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -95,12 +99,18 @@ int check_paged(const ra_kv_cache *c, const ra_paged_params *p)
     if (p->prefix_pages < 0 || (p->prefix_pages > 0) != (p->prefix_table != nullptr) ||
         (p->prefix_pages > 0) != (p->prefix_len != nullptr))
         return refuse(RA_ERR_INVALID_ARG, "prefix_pages, prefix_table and prefix_len must come together");
-    // segments are counted in 32 bits: at most one per 8 query rows of a kv head
-    if ((double)p->B * ((double)p->Lq * p->Hq / c->Hkv / 8 + 1) * c->Hkv > 1e9)
-        return refuse(RA_ERR_UNSUPPORTED, "too many query rows (B=%d Lq=%d Hq=%d)", p->B, p->Lq, p->Hq);
     if (((long long)p->max_pages + p->prefix_pages) * c->page_size > 0x7fffffffll)
         return refuse(RA_ERR_UNSUPPORTED, "sequences must be shorter than 2^31 tokens");
     return RA_OK;
+}
+
+// Places on the line of a part's work (ra_paged.cuh) at full tables: they are
+// counted in 32 bits.
+bool line_fits(const ra_kv_cache *c, const ra_paged_params *p, const PagedPart &a)
+{
+    const double tokens = (double)(a.prefix ? p->prefix_pages : p->max_pages) * c->page_size;
+    const double tiles = tokens / a.tile + 1 + a.seg_cost;
+    return tiles * (a.prefix ? 1 : p->B) * a.n_rb * c->Hkv < 2147483648.0;
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -112,6 +122,7 @@ constexpr int kSms = 152;
 enum { kF32, kFew, kKeysM, kRowsM };
 
 struct Plan {
+    bool fits; // no part is too large
     PagedPart part[2];
     int kernel[2];
     int n_parts;
@@ -122,6 +133,7 @@ struct Plan {
 Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
 {
     Plan pl{};
+    pl.fits = true;
     const int G = p->Hq / c->Hkv;
     for (int k = 0; k < (p->prefix_pages ? 2 : 1); ++k) {
         PagedPart &a = pl.part[pl.n_parts];
@@ -156,6 +168,7 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
         }
         a.n_rb = (a.rows + a.row_block - 1) / a.row_block;
         a.slot_rows = a.rows < a.row_block ? a.rows : a.row_block;
+        pl.fits &= line_fits(c, p, a);
         a.direct = p->prefix_pages == 0;
         const size_t slots =
             a.direct ? 2 * (size_t)a.ctas : (size_t)a.ctas + (size_t)(k ? 1 : p->B) * a.n_rb * c->Hkv;
@@ -218,7 +231,9 @@ RA_API int ra_kv_read(const ra_kv_cache *cache, const int32_t *page_table, int m
 RA_API size_t ra_attn_paged_workspace_size(const ra_kv_cache *cache, const ra_paged_params *p)
 {
     if (check_paged(cache, p) != RA_OK) return 0;
-    return make_plan(cache, p, nullptr).bytes;
+    const Plan pl = make_plan(cache, p, nullptr);
+    if (!pl.fits) return refuse(RA_ERR_UNSUPPORTED, kTooLarge), 0;
+    return pl.bytes;
 }
 
 RA_API int ra_attn_paged(const ra_kv_cache *cache, const ra_paged_params *p, const void *q, void *out, float *lse,
@@ -232,6 +247,7 @@ RA_API int ra_attn_paged(const ra_kv_cache *cache, const ra_paged_params *p, con
     const size_t n = (size_t)p->B * p->Lq * p->Hq * cache->D * (p->dtype == RA_BF16 ? 2 : 4);
     if (overlap(q, n, out, n)) return refuse(RA_ERR_INVALID_ARG, "q and out overlap");
     const Plan pl = make_plan(cache, p, static_cast<uint8_t *>(ws));
+    if (!pl.fits) return refuse(RA_ERR_UNSUPPORTED, kTooLarge);
     if (!ws || ws_bytes < pl.bytes)
         return refuse(RA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws ? ws_bytes : (size_t)0, pl.bytes);
     if (!is_aligned(ws, 256)) return refuse(RA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
