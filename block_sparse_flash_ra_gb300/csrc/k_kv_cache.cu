@@ -8,9 +8,10 @@
 //
 // Both are copies: bound by memory for prompts and histories, by latency for
 // one token per sequence.  D / 8 lanes take a row, 16 bytes of bf16 each, and
-// a group does its token's K row and V row together, so that two loads per
-// lane are in flight before the first is used; rows are found from the flat
-// index alone, and the table is read while they are on their way.
+// a group does the K and V rows of two (token, head) pairs together, so that
+// four loads per lane are in flight before the first is used; the new rows'
+// places come from the index alone, and the table is read while they are on
+// their way.
 #include <cuda_fp16.h>
 
 #include "ra_paged.cuh"
@@ -18,17 +19,31 @@
 namespace ra {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kUnroll = 2;
 
 // Eight consecutive values in registers.
 struct Eight {
     float x[8];
 };
 
-__device__ __forceinline__ Eight load8(const __nv_bfloat16 *p)
+// The same as loaded: fewer registers while they wait.
+template <typename T>
+struct Raw {
+    uint4 w[sizeof(T) / 2];
+};
+
+template <typename T>
+__device__ __forceinline__ Raw<T> load8(const T *p)
 {
-    const uint4 w = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+    Raw<T> r;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = reinterpret_cast<const uint4 *>(p)[i];
+    return r;
+}
+
+__device__ __forceinline__ Eight widen(const Raw<__nv_bfloat16> &w)
+{
+    const uint32_t a[4] = {w.w[0].x, w.w[0].y, w.w[0].z, w.w[0].w};
     Eight r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -38,10 +53,13 @@ __device__ __forceinline__ Eight load8(const __nv_bfloat16 *p)
     return r;
 }
 
-__device__ __forceinline__ Eight load8(const float *p)
+__device__ __forceinline__ Eight widen(const Raw<float> &w)
 {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    return Eight{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+    const uint32_t a[8] = {w.w[0].x, w.w[0].y, w.w[0].z, w.w[0].w, w.w[1].x, w.w[1].y, w.w[1].z, w.w[1].w};
+    Eight r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.x[i] = __uint_as_float(a[i]);
+    return r;
 }
 
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const Eight &r)
@@ -108,53 +126,88 @@ __device__ __forceinline__ void put_row(const Eight &r, void *base, uint8_t *exp
     }
 }
 
+// Blocks of kUnroll rows per group lie along x over one sequence's rows
+// (token, head), sequences along y.
 template <int D, bool FP8, typename T>
 __global__ void __launch_bounds__(kThreads)
-    kv_write_kernel(PagedCache c, const T *__restrict__ k, const T *__restrict__ v, int L, long long rows,
-                    size_t k_stride, size_t v_stride, const int32_t *__restrict__ table, int max_pages,
+    kv_write_kernel(PagedCache c, const T *__restrict__ k, const T *__restrict__ v, int B, int L, size_t k_stride,
+                    size_t v_stride, const int32_t *__restrict__ table, int max_pages,
                     const int32_t *__restrict__ start, const int32_t *__restrict__ count, int *status)
 {
-    constexpr int LANES = D / 8;
+    constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
     const int lane = threadIdx.x % LANES;
-    const long long groups = (long long)gridDim.x * (kThreads / LANES);
-    const long long first = (long long)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
-    // every group of a block makes the same number of turns: the shuffles
-    // inside a row need the whole warp
-    for (long long r0 = 0; r0 < rows; r0 += groups) {
-        const long long r = r0 + first;
-        const bool live = r < rows;
-        const long long tok = live ? r / c.Hkv : 0;
-        const int h = live ? (int)(r - tok * c.Hkv) : 0;
-        const int b = (int)(tok / L), i = (int)(tok - (long long)b * L);
-        const Eight kr = load8(k + tok * k_stride + h * D + lane * 8);
-        const Eight vr = load8(v + tok * v_stride + h * D + lane * 8);
-        bool put = live && i < (count ? min(count[b], L) : L);
-        size_t row = 0;
-        if (put) {
-            const long long pos = (long long)start[b] + i;
+    const unsigned r0 = blockIdx.x * (GROUPS * kUnroll) + threadIdx.x / LANES;
+    for (int b = blockIdx.y; b < B; b += gridDim.y) {
+        const int first = start[b];
+        const int n = count ? min(max(count[b], 0), L) : L;
+        if (blockIdx.x == 0 && threadIdx.x == 0 && count && n != count[b]) atomicMax(status, RA_STATUS_BAD_PAGE);
+        const unsigned rows = (unsigned)n * c.Hkv;
+        if (blockIdx.x * (unsigned)(GROUPS * kUnroll) >= rows) continue;
+        Raw<T> kr[kUnroll] = {}, vr[kUnroll] = {};
+        size_t row[kUnroll];
+        bool put[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const unsigned r = r0 + u * GROUPS;
+            put[u] = r < rows;
+            const unsigned i = put[u] ? r / c.Hkv : 0, h = put[u] ? r - i * c.Hkv : 0;
+            const size_t tok = (size_t)b * L + i;
+            if (put[u]) {
+                kr[u] = load8(k + tok * k_stride + h * D + lane * 8);
+                vr[u] = load8(v + tok * v_stride + h * D + lane * 8);
+            }
+            row[u] = h;
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (!put[u]) continue;
+            const long long pos = (long long)first + (r0 + u * GROUPS) / c.Hkv;
             int page = -1;
             if (pos >= 0 && (pos >> c.page_shift) < max_pages)
                 page = table[(size_t)b * max_pages + (pos >> c.page_shift)];
-            put = page >= 0 && page < c.n_pages;
-            if (put)
-                row = (((size_t)page * c.Hkv + h) << c.page_shift) + (size_t)(pos & (c.page - 1));
+            put[u] = page >= 0 && page < c.n_pages;
+            if (put[u])
+                row[u] = (((size_t)page * c.Hkv + row[u]) << c.page_shift) + (size_t)(pos & (c.page - 1));
             else
                 atomicMax(status, RA_STATUS_BAD_PAGE);
         }
-        put_row<LANES, FP8>(kr, put ? const_cast<void *>(c.k) : nullptr, const_cast<uint8_t *>(c.k_exp), row, lane);
-        put_row<LANES, FP8>(vr, put ? const_cast<void *>(c.v) : nullptr, const_cast<uint8_t *>(c.v_exp), row, lane);
-        if (count && lane == 0 && live && h == 0 && i == 0 && (count[b] < 0 || count[b] > L))
-            atomicMax(status, RA_STATUS_BAD_PAGE);
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            put_row<LANES, FP8>(widen(kr[u]), put[u] ? const_cast<void *>(c.k) : nullptr, const_cast<uint8_t *>(c.k_exp), row[u], lane);
+            put_row<LANES, FP8>(widen(vr[u]), put[u] ? const_cast<void *>(c.v) : nullptr, const_cast<uint8_t *>(c.v_exp), row[u], lane);
+        }
     }
 }
 
+// Eight values of a cached row as the cache has them, and its scale byte.
+template <bool FP8>
+struct Cached {
+    uint4 w; // codes: .x and .y
+    uint32_t e;
+};
+
 template <int D, bool FP8>
-__device__ __forceinline__ Eight get_row(const void *base, const uint8_t *exps, size_t row, int lane)
+__device__ __forceinline__ Cached<FP8> get_row(const void *base, const uint8_t *exps, size_t row, int lane)
 {
-    if (!FP8) return load8(static_cast<const __nv_bfloat16 *>(base) + row * D + lane * 8);
-    const uint2 w = reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(base) + row * D)[lane];
-    const float s = exp_byte_scale(exps[row]);
-    const uint32_t h[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
+    Cached<FP8> r{};
+    if (FP8) {
+        const uint2 w = reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(base) + row * D)[lane];
+        r.w.x = w.x;
+        r.w.y = w.y;
+        r.e = exps[row];
+    } else {
+        r.w = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + row * D)[lane];
+    }
+    return r;
+}
+
+template <bool FP8>
+__device__ __forceinline__ Eight widen(const Cached<FP8> &c)
+{
+    if (!FP8) return widen(Raw<__nv_bfloat16>{{c.w}});
+    const float s = exp_byte_scale(c.e);
+    const uint32_t h[4] = {c.w.x & 0xffffu, c.w.x >> 16, c.w.y & 0xffffu, c.w.y >> 16};
     Eight r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -168,43 +221,51 @@ __device__ __forceinline__ Eight get_row(const void *base, const uint8_t *exps, 
 
 template <int D, bool FP8, typename T>
 __global__ void __launch_bounds__(kThreads)
-    kv_read_kernel(PagedCache c, T *__restrict__ k, T *__restrict__ v, int L, long long rows,
-                   const int32_t *__restrict__ table, int max_pages, const int32_t *__restrict__ kv_len,
-                   int *status)
+    kv_read_kernel(PagedCache c, T *__restrict__ k, T *__restrict__ v, int B, int L, const int32_t *__restrict__ table,
+                   int max_pages, const int32_t *__restrict__ kv_len, int *status)
 {
-    constexpr int LANES = D / 8;
+    constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
     const int lane = threadIdx.x % LANES;
-    const long long groups = (long long)gridDim.x * (kThreads / LANES);
-    const long long first = (long long)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
-    for (long long r = first; r < rows; r += groups) {
-        const long long tok = r / c.Hkv;
-        const int h = (int)(r - tok * c.Hkv);
-        const int b = (int)(tok / L), j = (int)(tok - (long long)b * L);
+    const unsigned r0 = blockIdx.x * (GROUPS * kUnroll) + threadIdx.x / LANES, rows = (unsigned)L * c.Hkv;
+    for (int b = blockIdx.y; b < B; b += gridDim.y) {
         const int len = kv_len[b];
-        Eight kr{}, vr{};
-        if (j < len) {
-            int page = -1;
-            if ((j >> c.page_shift) < max_pages) page = table[(size_t)b * max_pages + (j >> c.page_shift)];
-            if (page >= 0 && page < c.n_pages) {
-                const size_t row = (((size_t)page * c.Hkv + h) << c.page_shift) + (j & (c.page - 1));
-                kr = get_row<D, FP8>(c.k, c.k_exp, row, lane);
-                vr = get_row<D, FP8>(c.v, c.v_exp, row, lane);
-            } else {
-                atomicMax(status, RA_STATUS_BAD_PAGE);
+        int page[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) { // beside the length, not behind it
+            const int n = (int)(((r0 + u * GROUPS) / c.Hkv) >> c.page_shift);
+            page[u] = n < max_pages ? table[(size_t)b * max_pages + n] : -1;
+        }
+        if (blockIdx.x == 0 && threadIdx.x == 0 && (len < 0 || len > L)) atomicMax(status, RA_STATUS_BAD_PAGE);
+        Cached<FP8> kr[kUnroll] = {}, vr[kUnroll] = {};
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const unsigned r = r0 + u * GROUPS, j = r / c.Hkv, h = r - j * c.Hkv;
+            if (r < rows && (int)j < len) {
+                if (page[u] >= 0 && page[u] < c.n_pages) {
+                    const size_t row = (((size_t)page[u] * c.Hkv + h) << c.page_shift) + (j & (c.page - 1));
+                    kr[u] = get_row<D, FP8>(c.k, c.k_exp, row, lane);
+                    vr[u] = get_row<D, FP8>(c.v, c.v_exp, row, lane);
+                } else {
+                    atomicMax(status, RA_STATUS_BAD_PAGE);
+                }
             }
         }
-        store8(k + r * D + lane * 8, kr);
-        store8(v + r * D + lane * 8, vr);
-        if (lane == 0 && h == 0 && j == 0 && (len < 0 || len > L)) atomicMax(status, RA_STATUS_BAD_PAGE);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const unsigned r = r0 + u * GROUPS;
+            if (r < rows) {
+                const size_t at = ((size_t)b * rows + r) * D + lane * 8;
+                store8(k + at, widen(kr[u]));
+                store8(v + at, widen(vr[u]));
+            }
+        }
     }
 }
 
-int grid_for(long long rows, int lanes, int num_sms)
+dim3 grid_for(int B, long long rows, int lanes)
 {
-    const long long per = kThreads / lanes;
-    const long long need = (rows + per - 1) / per;
-    const long long most = (long long)num_sms * (2048 / kThreads);
-    return (int)(need < most ? need : most);
+    const long long per = kThreads / lanes * kUnroll;
+    return dim3((unsigned)((rows + per - 1) / per), (unsigned)(B < 65535 ? B : 65535));
 }
 
 } // namespace
@@ -212,13 +273,12 @@ int grid_for(long long rows, int lanes, int num_sms)
 cudaError_t launch_kv_write(const PagedCache &c, int cache_dtype, const void *k, const void *v, int dtype,
                             int B, int L, size_t k_stride, size_t v_stride, const int32_t *page_table,
                             int max_pages, const int32_t *start, const int32_t *count, int *status,
-                            int num_sms, cudaStream_t s)
+                            cudaStream_t s)
 {
-    const long long rows = (long long)B * L * c.Hkv;
-    const int grid = grid_for(rows, c.D / 8, num_sms);
+    const dim3 grid = grid_for(B, (long long)L * c.Hkv, c.D / 8);
     auto go = [&](auto kern, auto *kp, auto *vp) {
-        kern<<<grid, kThreads, 0, s>>>(c, kp, vp, L, rows, k_stride, v_stride, page_table, max_pages, start,
-                                       count, status);
+        kern<<<grid, kThreads, 0, s>>>(c, kp, vp, B, L, k_stride, v_stride, page_table, max_pages, start, count,
+                                       status);
         return cudaGetLastError();
     };
     auto typed = [&](auto *kp, auto *vp) {
@@ -234,12 +294,11 @@ cudaError_t launch_kv_write(const PagedCache &c, int cache_dtype, const void *k,
 
 cudaError_t launch_kv_read(const PagedCache &c, int cache_dtype, const int32_t *page_table, int max_pages,
                            const int32_t *kv_len, int B, int L, void *k, void *v, int dtype, int *status,
-                           int num_sms, cudaStream_t s)
+                           cudaStream_t s)
 {
-    const long long rows = (long long)B * L * c.Hkv;
-    const int grid = grid_for(rows, c.D / 8, num_sms);
+    const dim3 grid = grid_for(B, (long long)L * c.Hkv, c.D / 8);
     auto go = [&](auto kern, auto *kp, auto *vp) {
-        kern<<<grid, kThreads, 0, s>>>(c, kp, vp, L, rows, page_table, max_pages, kv_len, status);
+        kern<<<grid, kThreads, 0, s>>>(c, kp, vp, B, L, page_table, max_pages, kv_len, status);
         return cudaGetLastError();
     };
     auto typed = [&](auto *kp, auto *vp) {

@@ -88,10 +88,10 @@ cudaError_t launch_paged(void (*kernel)(P...), const PagedProblem &, const Paged
 cudaError_t launch_kv_write(const PagedCache &c, int cache_dtype, const void *k, const void *v,
                             int dtype, int B, int L, size_t k_stride, size_t v_stride,
                             const int32_t *page_table, int max_pages, const int32_t *start,
-                            const int32_t *count, int *status, int num_sms, cudaStream_t s);
+                            const int32_t *count, int *status, cudaStream_t s);
 cudaError_t launch_kv_read(const PagedCache &c, int cache_dtype, const int32_t *page_table,
                            int max_pages, const int32_t *kv_len, int B, int L, void *k, void *v,
-                           int dtype, int *status, int num_sms, cudaStream_t s);
+                           int dtype, int *status, cudaStream_t s);
 
 // fp32 arithmetic throughout: the path of fp32 queries
 constexpr int kPagedF32Rows = 8, kPagedF32Tile = 32;

@@ -54,13 +54,14 @@ int check_cache(const ra_kv_cache *c)
     return RA_OK;
 }
 
-int check_dense(int B, int L, int dtype, const int32_t *page_table, int max_pages)
+int check_dense(int B, int L, int Hkv, int dtype, const int32_t *page_table, int max_pages)
 {
     if (B <= 0 || L <= 0 || max_pages <= 0)
         return refuse(RA_ERR_INVALID_ARG, "sizes must be positive (B=%d L=%d max_pages=%d)", B, L, max_pages);
     if (dtype != RA_BF16 && dtype != RA_FP32)
         return refuse(RA_ERR_INVALID_ARG, "dtype must be RA_BF16 or RA_FP32");
     if (!page_table) return refuse(RA_ERR_INVALID_ARG, "page_table is NULL");
+    if ((long long)L * Hkv > 0x7fffffffll) return refuse(RA_ERR_UNSUPPORTED, "L * Hkv must be below 2^31");
     return RA_OK;
 }
 
@@ -192,7 +193,7 @@ RA_API int ra_kv_write(const ra_kv_cache *cache, const void *k, const void *v, i
                        const int32_t *start, const int32_t *count, ra_stream_t stream)
 {
     int rc = check_cache(cache);
-    if (rc || (rc = check_dense(B, L, dtype, page_table, max_pages))) return rc;
+    if (rc || (rc = check_dense(B, L, cache->Hkv, dtype, page_table, max_pages))) return rc;
     if (!k || !v || !start) return refuse(RA_ERR_INVALID_ARG, "k, v and start are needed");
     const size_t row = (size_t)cache->Hkv * cache->D, item = dtype == RA_BF16 ? 2 : 4;
     if (k_stride < row || v_stride < row)
@@ -203,7 +204,7 @@ RA_API int ra_kv_write(const ra_kv_cache *cache, const void *k, const void *v, i
     if ((rc = device_info(&d))) return rc;
     const cudaError_t e =
         launch_kv_write(cache_of(cache), cache->dtype, k, v, dtype, B, L, k_stride, v_stride, page_table, max_pages,
-                        start, count, d.status, d.num_sms, reinterpret_cast<cudaStream_t>(stream));
+                        start, count, d.status, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return set_cuda_error(e, "kv write launch");
     count_launches(1);
     return RA_OK;
@@ -213,7 +214,7 @@ RA_API int ra_kv_read(const ra_kv_cache *cache, const int32_t *page_table, int m
                       int B, int L, void *k, void *v, int dtype, ra_stream_t stream)
 {
     int rc = check_cache(cache);
-    if (rc || (rc = check_dense(B, L, dtype, page_table, max_pages))) return rc;
+    if (rc || (rc = check_dense(B, L, cache->Hkv, dtype, page_table, max_pages))) return rc;
     if (!k || !v || !kv_len) return refuse(RA_ERR_INVALID_ARG, "k, v and kv_len are needed");
     if (!is_aligned(k, 16) || !is_aligned(v, 16)) return refuse(RA_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
     const size_t n = (size_t)B * L * cache->Hkv * cache->D * (dtype == RA_BF16 ? 2 : 4);
@@ -222,7 +223,7 @@ RA_API int ra_kv_read(const ra_kv_cache *cache, const int32_t *page_table, int m
     if ((rc = device_info(&d))) return rc;
     const cudaError_t e =
         launch_kv_read(cache_of(cache), cache->dtype, page_table, max_pages, kv_len, B, L, k, v, dtype, d.status,
-                       d.num_sms, reinterpret_cast<cudaStream_t>(stream));
+                       reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return set_cuda_error(e, "kv read launch");
     count_launches(1);
     return RA_OK;
