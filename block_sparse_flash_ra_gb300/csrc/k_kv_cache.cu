@@ -100,18 +100,45 @@ __device__ __forceinline__ uint32_t row_exp(uint32_t amax_bits)
     return (uint32_t)(max(e, -110) + 127);
 }
 
-// Quantises or rounds one row, spread over LANES lanes, into the cache.
+// Largest magnitudes, as fp32 bits, of a K row and a V row that LANES lanes hold.
+template <int LANES>
+__device__ __forceinline__ uint2 row_tops(const Raw<__nv_bfloat16> &k, const Raw<__nv_bfloat16> &v)
+{
+    // as pairs of 16-bit integers, the two rows in one word for the shuffles
+    const uint32_t m = 0x7fff7fffu;
+    const uint32_t a = __vmaxu2(__vmaxu2(k.w[0].x & m, k.w[0].y & m), __vmaxu2(k.w[0].z & m, k.w[0].w & m));
+    const uint32_t b = __vmaxu2(__vmaxu2(v.w[0].x & m, v.w[0].y & m), __vmaxu2(v.w[0].z & m, v.w[0].w & m));
+    uint32_t t = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, o));
+    return make_uint2(t << 16, t & 0xffff0000u);
+}
+
+template <int LANES>
+__device__ __forceinline__ uint2 row_tops(const Raw<float> &k, const Raw<float> &v)
+{
+    uint2 t = make_uint2(0, 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t m = 0x7fffffffu;
+        t.x = max(t.x, max(max(k.w[i].x & m, k.w[i].y & m), max(k.w[i].z & m, k.w[i].w & m)));
+        t.y = max(t.y, max(max(v.w[i].x & m, v.w[i].y & m), max(v.w[i].z & m, v.w[i].w & m)));
+    }
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) {
+        t.x = max(t.x, __shfl_xor_sync(0xffffffffu, t.x, o));
+        t.y = max(t.y, __shfl_xor_sync(0xffffffffu, t.y, o));
+    }
+    return t;
+}
+
+// Stores a lane's eight values of a row; 8-bit: as codes at the scale that the
+// row's largest magnitude asks for.
 template <int LANES, bool FP8>
-__device__ __forceinline__ void put_row(const Eight &r, void *base, uint8_t *exps, size_t row, int lane)
+__device__ __forceinline__ void put_row(const Eight &r, uint32_t top, const void *base, const uint8_t *exps, size_t row, int lane)
 {
     if (FP8) {
-        uint32_t a = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(r.x[i]) & 0x7fffffffu);
-#pragma unroll
-        for (int o = LANES / 2; o; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-        const uint32_t e = row_exp(a);
-        if (!base) return;
+        const uint32_t e = row_exp(top);
         // 2^-(e - 127): its exponent field is 254 - e, in [7, 237]
         const float inv = __uint_as_float((254u - e) << 23);
         uint2 w = make_uint2(0, 0);
@@ -119,10 +146,10 @@ __device__ __forceinline__ void put_row(const Eight &r, void *base, uint8_t *exp
             w.x = e4m3x4(r.x[0] * inv, r.x[1] * inv, r.x[2] * inv, r.x[3] * inv);
             w.y = e4m3x4(r.x[4] * inv, r.x[5] * inv, r.x[6] * inv, r.x[7] * inv);
         }
-        reinterpret_cast<uint2 *>(static_cast<uint8_t *>(base) + row * (LANES * 8))[lane] = w;
-        if (lane == 0) exps[row] = (uint8_t)e;
-    } else if (base) {
-        store8(static_cast<__nv_bfloat16 *>(base) + row * (LANES * 8) + lane * 8, r);
+        reinterpret_cast<uint2 *>(const_cast<uint8_t *>(static_cast<const uint8_t *>(base)) + row * (LANES * 8))[lane] = w;
+        if (lane == 0) const_cast<uint8_t *>(exps)[row] = (uint8_t)e;
+    } else {
+        store8(static_cast<__nv_bfloat16 *>(const_cast<void *>(base)) + row * (LANES * 8) + lane * 8, r);
     }
 }
 
@@ -145,23 +172,25 @@ __global__ void __launch_bounds__(kThreads)
         if (blockIdx.x * (unsigned)(GROUPS * kUnroll) >= rows) continue;
         Raw<T> kr[kUnroll] = {}, vr[kUnroll] = {};
         size_t row[kUnroll];
+        unsigned tok[kUnroll];
         bool put[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const unsigned r = r0 + u * GROUPS;
             put[u] = r < rows;
-            const unsigned i = put[u] ? r / c.Hkv : 0, h = put[u] ? r - i * c.Hkv : 0;
-            const size_t tok = (size_t)b * L + i;
+            tok[u] = r / c.Hkv;
+            const unsigned h = r - tok[u] * c.Hkv;
             if (put[u]) {
-                kr[u] = load8(k + tok * k_stride + h * D + lane * 8);
-                vr[u] = load8(v + tok * v_stride + h * D + lane * 8);
+                const size_t at = (size_t)b * L + tok[u];
+                kr[u] = load8(k + at * k_stride + h * D + lane * 8);
+                vr[u] = load8(v + at * v_stride + h * D + lane * 8);
             }
             row[u] = h;
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             if (!put[u]) continue;
-            const long long pos = (long long)first + (r0 + u * GROUPS) / c.Hkv;
+            const long long pos = (long long)first + tok[u];
             int page = -1;
             if (pos >= 0 && (pos >> c.page_shift) < max_pages)
                 page = table[(size_t)b * max_pages + (pos >> c.page_shift)];
@@ -174,8 +203,10 @@ __global__ void __launch_bounds__(kThreads)
         __syncwarp();
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            put_row<LANES, FP8>(widen(kr[u]), put[u] ? const_cast<void *>(c.k) : nullptr, const_cast<uint8_t *>(c.k_exp), row[u], lane);
-            put_row<LANES, FP8>(widen(vr[u]), put[u] ? const_cast<void *>(c.v) : nullptr, const_cast<uint8_t *>(c.v_exp), row[u], lane);
+            const uint2 top = FP8 ? row_tops<LANES>(kr[u], vr[u]) : make_uint2(0, 0);
+            if (!put[u]) continue;
+            put_row<LANES, FP8>(widen(kr[u]), top.x, c.k, c.k_exp, row[u], lane);
+            put_row<LANES, FP8>(widen(vr[u]), top.y, c.v, c.v_exp, row[u], lane);
         }
     }
 }
