@@ -64,6 +64,7 @@ struct Cfg {
     static constexpr int kNO = (RP * kPTerms + 15) / 16 * 16;             // columns of O^T
     static constexpr int kQBytes = kNS * kD * (FP8 ? 1 : 2);
     static constexpr int kPBytes = kNO * kKeys * (FP8 ? 1 : 2);
+    static constexpr int kPChunk = kKeys * 16; // 16 bytes of every key: 16 or 8 columns of P^T
     static constexpr int kKOff = 0;
     static constexpr int kVOff = kKOff + kStages * kMat;
     static constexpr int kQOff = kVOff + kVStages * kMat;
@@ -80,7 +81,8 @@ struct Cfg {
     static constexpr uint32_t kCols = kColO + kNO <= 64 ? 64 : kColO + kNO <= 128 ? 128 : 256;
     static constexpr uint32_t kIdescS = ((FP8 ? 0u : (1u << 7) | (1u << 10)) | (1u << 4)) |
                                         ((uint32_t)(kNS >> 3) << 17) | ((uint32_t)(kKeys >> 4) << 24);
-    static constexpr uint32_t kIdescO = ((FP8 ? 0u : (1u << 7) | (1u << 10)) | (1u << 4)) | (1u << 15) |
+    // both operands of O^T are MN-major
+    static constexpr uint32_t kIdescO = ((FP8 ? 0u : (1u << 7) | (1u << 10)) | (1u << 4)) | (1u << 15) | (1u << 16) |
                                         ((uint32_t)(kNO >> 3) << 17) | ((uint32_t)(kD >> 4) << 24);
     // growth of a row's logits above its reference (base 2) that is let pass:
     // 8-bit weights end at 448, bf16 has fp32's range
@@ -109,6 +111,15 @@ __device__ __forceinline__ Bars carve(uint8_t *smem)
     b.q_full = b.pv_done + 2;
     b.drain = b.q_full + 1;
     return b;
+}
+
+// Descriptor of an MN-major operand without swizzle: 16 bytes along MN of 8
+// K-rows lie together (128 bytes); `chunk` bytes on, the next 16 along MN;
+// `k8` bytes on, the next 8 K-rows.
+__device__ __forceinline__ uint64_t sdesc_plain_mn(uint32_t saddr, uint32_t chunk, uint32_t k8)
+{
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((k8 >> 4) & 0x3FFFu) << 16 |
+           (uint64_t)((chunk >> 4) & 0x3FFFu) << 32 | (uint64_t)1 << 46;
 }
 
 // One product step by the whole warp (an elected lane issues).
@@ -152,21 +163,22 @@ __device__ __forceinline__ void tma_load_3d(uint8_t *dst, const void *tmap, uint
                  : "memory");
 }
 
-// The softmax warps' own barrier; all N threads pass it the same number of
-// times whatever happens, so it needs no time limit.
+// The softmax warps' own barriers: 1 of all N threads, 2 + g of warpgroup g.
+// All pass them the same number of times whatever happens, so they need no
+// time limit.
 template <int N>
 __device__ __forceinline__ void soft_sync()
 {
     asm volatile("barrier.sync 1, %0;" ::"n"(N) : "memory");
 }
-template <int N>
-__device__ __forceinline__ bool soft_or(bool x)
+__device__ __forceinline__ void group_sync(int bar) { asm volatile("barrier.sync %0, 128;" ::"r"(bar) : "memory"); }
+__device__ __forceinline__ bool group_or(int bar, bool x)
 {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-                 "barrier.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 "barrier.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                  : "=r"(r)
-                 : "r"((uint32_t)x), "n"(N)
+                 : "r"((uint32_t)x), "r"(bar)
                  : "memory");
     return r != 0;
 }
@@ -192,12 +204,6 @@ __device__ __forceinline__ __half2 from_codes(uint32_t c)
 {
     const uint32_t r = e4m3x2_to_f16x2(c);
     return *reinterpret_cast<const __half2 *>(&r);
-}
-
-__device__ __forceinline__ void sts8(uint32_t a, uint32_t x) { asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(x) : "memory"); }
-__device__ __forceinline__ void sts16(uint32_t a, uint32_t x)
-{
-    asm volatile("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tst.shared.u16 [%0], h;\n\t}" ::"r"(a), "r"(x) : "memory");
 }
 
 template <bool FP8, int RP>
@@ -329,7 +335,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
         const uint64_t kd0 = sdesc_sw128(smem_u32(smem + C::kKOff), 16, 1024);
         const uint64_t vd0 = sdesc_sw128(smem_u32(smem + C::kVOff), kKeys * 128, 1024);
         const uint64_t qd0 = sdesc_sw128(smem_u32(smem + C::kQOff), 16, 1024);
-        const uint64_t pd0 = sdesc_sw128(smem_u32(smem + C::kPOff), 16, 1024);
+        const uint64_t pd0 = sdesc_plain_mn(smem_u32(smem + C::kPOff), C::kPChunk, 128);
         uint32_t i = 0, segs = 0;
         bool ok = true;
         auto issue_pv = [&](uint32_t j, bool first) -> bool {
@@ -340,8 +346,8 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
             const uint64_t vd = vd0 + (uint32_t)((sv * C::kMat) >> 4), pd = pd0 + (uint32_t)((sb * C::kPBytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < (FP8 ? 4 : 8); ++kk) {
-                // A: 32 or 16 keys further down the tile; B: 32 bytes further along the keys
-                const uint32_t bo = FP8 ? kk * 32 : (kk >> 2) * (C::kNO * 128) + (kk & 3) * 32;
+                // 32 or 16 keys further down both tiles
+                const uint32_t bo = kk * (FP8 ? 32 : 16) * 16;
                 mma_step<FP8>(tmem + C::kColO, vd + (uint32_t)((kk * (FP8 ? 4096 : 2048)) >> 4), pd + (bo >> 4), C::kIdescO,
                               (kk > 0 || !first) ? 1u : 0u);
             }
@@ -379,7 +385,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
         // and runs its loops out on whatever is there: every barrier of these
         // warps is still met by all of them, converged.
         constexpr int NT = C::kSoftThreads, RS = kRT + 4; // words of a warp in red
-        const int tid = threadIdx.x & 127, grp = threadIdx.x >> 7, row0 = grp * kRT, wq = warp & 3;
+        const int tid = threadIdx.x & 127, grp = threadIdx.x >> 7, row0 = grp * kRT, wq = warp & 3, bar = 2 + grp;
         const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
         float *row_qs = reinterpret_cast<float *>(smem + C::kRowOff);
         int *row_limit = reinterpret_cast<int *>(row_qs + RP);
@@ -470,6 +476,16 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                 const int valid = min(len - t * kKeys, kKeys);
                 const bool masked = t * kKeys + kKeys > all;
                 float s[kRT];
+                float ks = 1.f, vs = 1.f, ev = 0.f;
+                if (FP8) {
+                    wait(bars.e_full + sv, (i / C::kVStages) & 1);
+                    const uint8_t *e = smem + C::kExpOff + sv * 2 * kKeys + tid;
+                    const uint32_t vb = e[kKeys];
+                    ks = exp_byte_scale(e[0]);
+                    vs = exp_byte_scale(vb);
+                    // bytes behind the length and rows without a value do not count
+                    if (tid < valid && vb != 255u) ev = fmaxf((float)vb, kMinExp);
+                }
                 wait(bars.s_full + sb, (i >> 1) & 1);
                 tc_fence_after();
                 tmem_ld<8>(lane_base + sb * C::kNS + row0, s);
@@ -484,16 +500,6 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                 }
                 tc_fence_before();
                 mbar_arrive(bars.s_empty + sb);
-                float ks = 1.f, vs = 1.f, ev = 0.f;
-                if (FP8) {
-                    wait(bars.e_full + sv, (i / C::kVStages) & 1);
-                    const uint8_t *e = smem + C::kExpOff + sv * 2 * kKeys + tid;
-                    const uint32_t vb = e[kKeys];
-                    ks = exp_byte_scale(e[0]);
-                    vs = exp_byte_scale(vb);
-                    // bytes behind the length and rows without a value do not count
-                    if (tid < valid && vb != 255u) ev = fmaxf((float)vb, kMinExp);
-                }
                 // ---- logits in base 2
                 bool grow = FP8 && ev > ev_top;
 #pragma unroll
@@ -509,7 +515,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                 }
 #pragma unroll
                 for (int r = 0; r < kRT; ++r) grow |= s[r] > m[r] + C::kLazy;
-                if (soft_or<NT>(grow)) {
+                if (group_or(bar, grow)) {
                     // new references: the maxima so far
 #pragma unroll
                     for (int r = 0; r < kRT; ++r) {
@@ -522,7 +528,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                     }
                     // O is still: P V of the tile before has completed
                     if (t > c.t0) wait(bars.pv_done + (sb ^ 1), ((i - 1) >> 1) & 1);
-                    soft_sync<NT>();
+                    group_sync(bar);
                     float fe = 1.f;
                     if (FP8) {
                         float top = ev_top;
@@ -556,56 +562,57 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                         }
                         tmem_st_wait();
                     }
-                    soft_sync<NT>(); // red is free again
+                    group_sync(bar); // red is free again
                 }
-                // ---- weights, as the terms of P^T: row of term k and query row
-                // r is k * RP + r, this thread's column is its key.  S of this
-                // tile was issued after P V of the tile before last, so that
-                // tile's weights have been read.
+                // ---- weights, as the terms of P^T: column of term k and query row
+                // r is k * RP + r, this thread's row is its key.  S of this tile was
+                // issued after P V of the tile before last, so that tile's weights
+                // have been read.
                 const float pb = FP8 ? ex2_approx(127.f + kPBias - fmaxf(ev_top, kMinExp)) * vs : 1.f;
-                const uint32_t pt = p_base + sb * C::kPBytes;
+                float x[kRT];
 #pragma unroll
-                for (int r = 0; r < kRT; r += 2) {
-                    float x[2];
+                for (int r = 0; r < kRT; ++r) {
+                    x[r] = ex2_approx(s[r] - m[r]);
+                    l[r] += x[r];
+                    if (FP8) x[r] *= pb;
+                }
+                if (FP8 && masked) {
+                    // a masked key's scale may be anything
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        x[y] = ex2_approx(s[r + y] - m[r + y]);
-                        l[r + y] += x[y];
-                        if (FP8) x[y] *= pb;
-                    }
-                    if (FP8 && masked) {
-                        // a masked key's scale may be anything
+                    for (int r = 0; r < kRT; ++r)
+                        if (s[r] == -INFINITY) x[r] = 0.f;
+                }
+                const uint32_t pt = p_base + sb * C::kPBytes + tid * 16;
+                if (FP8) {
+                    __half2 h[4];
 #pragma unroll
-                        for (int y = 0; y < 2; ++y)
-                            if (s[r + y] == -INFINITY) x[y] = 0.f;
-                    }
-                    if (FP8) {
-                        __half2 h = __floats2half2_rn(x[0], x[1]);
+                    for (int y = 0; y < 4; ++y) h[y] = __floats2half2_rn(x[2 * y], x[2 * y + 1]);
 #pragma unroll
-                        for (int k = 0; k < 3; ++k) {
-                            const uint32_t w = to_codes(h);
+                    for (int k = 0; k < 3; ++k) {
+                        uint32_t w[4];
 #pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const int row = k * RP + row0 + r + y;
-                                sts8(pt + row * 128 + (((tid >> 4) ^ ((r + y) & 7)) << 4) + (tid & 15), y ? w >> 8 : w);
-                            }
-                            if (k < 2) h = __hmul2(__hsub2(h, from_codes(w)), __float2half2_rn(16.f));
+                        for (int y = 0; y < 4; ++y) {
+                            w[y] = to_codes(h[y]);
+                            if (k < 2) h[y] = __hmul2(__hsub2(h[y], from_codes(w[y])), __float2half2_rn(16.f));
                         }
-                    } else {
-                        const uint32_t hi = pack_bf16x2(x[0], x[1]);
-                        const uint32_t lo = pack_bf16x2(x[0] - __uint_as_float(hi << 16),
-                                                        x[1] - __uint_as_float(hi & 0xffff0000u));
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const int row = k * RP + row0 + r + y;
-                                const uint32_t w = k ? lo : hi;
-                                sts16(pt + (tid >> 6) * (C::kNO * 128) + row * 128 +
-                                          ((((tid >> 3) & 7) ^ ((r + y) & 7)) << 4) + (tid & 7) * 2,
-                                      y ? w >> 16 : w);
-                            }
+                        const int col = k * RP + row0; // 8 columns: half of a 16-byte chunk
+                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(pt + (col >> 4) * C::kPChunk + (col & 8)),
+                                     "r"(__byte_perm(w[0], w[1], 0x5410)), "r"(__byte_perm(w[2], w[3], 0x5410))
+                                     : "memory");
                     }
+                } else {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        hi[y] = pack_bf16x2(x[2 * y], x[2 * y + 1]);
+                        lo[y] = pack_bf16x2(x[2 * y] - __uint_as_float(hi[y] << 16), x[2 * y + 1] - __uint_as_float(hi[y] & 0xffff0000u));
+                    }
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(pt + (row0 >> 3) * C::kPChunk), "r"(hi[0]),
+                                 "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
+                                 : "memory");
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(pt + ((RP + row0) >> 3) * C::kPChunk), "r"(lo[0]),
+                                 "r"(lo[1]), "r"(lo[2]), "r"(lo[3])
+                                 : "memory");
                 }
                 if (valid < kKeys) {
                     // values behind the length: whatever is there, weight 0 must give 0

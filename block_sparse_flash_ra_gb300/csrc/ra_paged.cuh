@@ -112,11 +112,16 @@ __device__ __forceinline__ bool cursor_begin(const PagedProblem &p, const PagedP
     const int lane = threadIdx.x & 31;
     int prefix_tiles = 0;
     unsigned total, before = 0;
+    int first32 = 0; // places of one of the first 32 sequences
     if (part.prefix) {
         prefix_tiles = (paged_prefix_len(p) + part.tile - 1) / part.tile;
         total = prefix_tiles ? per_seq * (prefix_tiles + part.seg_cost) : 0;
     } else {
-        total = own_places_sum(p, part, 0, before) * per_seq;
+        first32 = lane < p.B ? own_places(p, part, lane) : 0;
+        unsigned sum = first32;
+#pragma unroll 1
+        for (int b = lane + 32; b < p.B; b += 32) sum += own_places(p, part, b);
+        total = __reduce_add_sync(0xffffffffu, sum) * per_seq;
     }
     const unsigned share = (total + part.ctas - 1) / part.ctas;
     const unsigned at = share * cta, end = min(at + share, total);
@@ -128,7 +133,7 @@ __device__ __forceinline__ bool cursor_begin(const PagedProblem &p, const PagedP
 #pragma unroll 1
         for (int b0 = 0;; b0 += 32) {
             const int b = b0 + lane;
-            const int n = b < p.B ? own_places(p, part, b) : 0;
+            const int n = b0 == 0 ? first32 : b < p.B ? own_places(p, part, b) : 0;
             unsigned run = n * per_seq;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
