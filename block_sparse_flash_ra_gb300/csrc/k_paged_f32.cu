@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = threadIdx.x % D, row0 = threadIdx.x / D * OR;
     const float *q = static_cast<const float *>(p.q);
-    allow_next();
+    begin_in_order(part);
     report_lengths(p, part);
     PagedCursor c;
     const bool any = cursor_begin(p, part, blockIdx.x, c);
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads)
 cudaError_t launch_paged_f32(const PagedProblem &p, const PagedPart &part, int cache_dtype, cudaStream_t s)
 {
     auto go = [&](auto kern) {
-        return launch_paged(kern, p, part, kThreads, 0, s, p, part);
+        return launch_dependent(kern, (unsigned)part.ctas, kThreads, 0, s, p, part);
     };
     if (cache_dtype == RA_E4M3) return p.c.D == 64 ? go(paged_f32_kernel<64, true>) : go(paged_f32_kernel<128, true>);
     return p.c.D == 64 ? go(paged_f32_kernel<64, false>) : go(paged_f32_kernel<128, false>);

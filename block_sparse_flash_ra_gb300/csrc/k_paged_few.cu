@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
-    allow_next();
+    begin_in_order(part);
     report_lengths(p, part);
     __syncthreads();
     PagedCursor c;
@@ -634,7 +634,7 @@ cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &
         if (e != cudaSuccess) return e;
         set.fetch_or(bit, std::memory_order_release);
     }
-    return launch_paged(kern, p, part, kWarps * 32, Cfg<D, FP8>::kSmem, s, k, v, p, part);
+    return launch_dependent(kern, (unsigned)part.ctas, kWarps * 32, Cfg<D, FP8>::kSmem, s, k, v, p, part);
 }
 
 } // namespace

@@ -68,13 +68,15 @@ struct Cfg {
     static constexpr int kKOff = 0;
     static constexpr int kVOff = kKOff + kStages * kMat;
     static constexpr int kQOff = kVOff + kVStages * kMat;
-    static constexpr int kPOff = kQOff + kQBytes;
+    static constexpr int kPOff = kQOff + 2 * kQBytes; // Q of the present and of the next segment
     static constexpr int kExpOff = kPOff + 2 * kPBytes; // per V stage: scale bytes of K, of V
     static constexpr int kRowOff = kExpOff + (FP8 ? kVStages * 2 * kKeys : 0);
-    // per row: logit scale, keys it sees, place of its output (two words), of its lse, its factor
-    static constexpr int kRedOff = kRowOff + RP * 32;
+    // per row of both segments: place of its output and of its lse (two words each), logit scale, keys it sees;
+    // then its factor
+    static constexpr int kRowBytes = RP * 24;
+    static constexpr int kRedOff = kRowOff + 2 * kRowBytes + RP * 4;
     static constexpr int kBarOff = kRedOff + 4 * kGroups * (kRT + 4) * 4;
-    static constexpr int kNumBars = 2 * kStages + 3 * kVStages + 2 + 2 + 2 + 2 + 1 + 1;
+    static constexpr int kNumBars = 2 * kStages + 3 * kVStages + 2 + 2 + 2 + 2 + 2 + 1;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kSmem = kMiscOff + 16 + 1024;
     static constexpr uint32_t kColO = 2 * kNS;
@@ -109,7 +111,7 @@ __device__ __forceinline__ Bars carve(uint8_t *smem)
     b.p_full = b.s_empty + 2;
     b.pv_done = b.p_full + 2;
     b.q_full = b.pv_done + 2;
-    b.drain = b.q_full + 1;
+    b.drain = b.q_full + 2; // q_full by segment parity
     return b;
 }
 
@@ -234,8 +236,8 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
             mbar_init(bars.s_empty + s, C::kSoftThreads);
             mbar_init(bars.p_full + s, C::kSoftThreads);
             mbar_init(bars.pv_done + s, 1);
+            mbar_init(bars.q_full + s, C::kSoftThreads);
         }
-        mbar_init(bars.q_full, C::kSoftThreads);
         mbar_init(bars.drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
-    allow_next();
+    begin_in_order(part);
     report_lengths(p, part);
     tc_fence_before();
     __syncthreads();
@@ -357,7 +359,8 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
         };
         for (;;) {
             const int n = cursor_take(c);
-            if (!(ok = wait_all(bars.q_full, segs++ & 1))) break;
+            if (!(ok = wait_all(bars.q_full + (segs & 1), (segs >> 1) & 1))) break;
+            const uint64_t qd = qd0 + (uint32_t)(((segs++ & 1) * C::kQBytes) >> 4);
             for (int t = 0; ok && t < n; ++t, ++i) {
                 const int sk = i % C::kStages, sb = i & 1;
                 if (!(ok = wait_all(bars.k_full + sk, (i / C::kStages) & 1))) break;
@@ -368,7 +371,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                 for (int kk = 0; kk < (FP8 ? 4 : 8); ++kk) {
                     const uint32_t ao = FP8 ? kk * 32 : (kk >> 2) * (kKeys * 128) + (kk & 3) * 32;
                     const uint32_t bo = FP8 ? kk * 32 : (kk >> 2) * (C::kNS * 128) + (kk & 3) * 32;
-                    mma_step<FP8>(tmem + sb * C::kNS, kd + (ao >> 4), qd0 + (bo >> 4), C::kIdescS, kk > 0 ? 1u : 0u);
+                    mma_step<FP8>(tmem + sb * C::kNS, kd + (ao >> 4), qd + (bo >> 4), C::kIdescS, kk > 0 ? 1u : 0u);
                 }
                 tc_commit_w(bars.k_empty + sk);
                 tc_commit_w(bars.s_full + sb);
@@ -387,11 +390,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
         constexpr int NT = C::kSoftThreads, RS = kRT + 4; // words of a warp in red
         const int tid = threadIdx.x & 127, grp = threadIdx.x >> 7, row0 = grp * kRT, wq = warp & 3, bar = 2 + grp;
         const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
-        float *row_qs = reinterpret_cast<float *>(smem + C::kRowOff);
-        int *row_limit = reinterpret_cast<int *>(row_qs + RP);
-        long long *row_place = reinterpret_cast<long long *>(row_limit + RP); // (b * Lq + i) * Hq + hq, or -1
-        long long *row_lse = row_place + RP;
-        float *row_f = reinterpret_cast<float *>(row_lse + RP);
+        float *row_f = reinterpret_cast<float *>(smem + C::kRowOff + 2 * C::kRowBytes);
         float *red = reinterpret_cast<float *>(smem + C::kRedOff) + grp * 4 * RS; // [4 warps][RS]
         const uint32_t p_base = smem_u32(smem + C::kPOff);
         const float cap2 = p.soft_cap * kLog2e, to_cap = p.soft_cap > 0.f ? kLn2 / p.soft_cap : 0.f;
@@ -401,15 +400,32 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
             if (ok) ok = mbar_wait(bar, parity, ctx);
             __syncwarp();
         };
-        for (;;) {
-            const int n = cursor_take(c), len = source_len(c.b);
-            // ---- the query rows: 16 threads take one, 8 values each
+        // what is known of the rows of segment number `par`
+        struct Rows {
+            long long *place, *lse; // (b * Lq + i) * Hq + hq, or -1; where its lse goes
+            float *qs;
+            int *limit;
+        };
+        auto rows_of = [&](uint32_t par) {
+            Rows r;
+            r.place = reinterpret_cast<long long *>(smem + C::kRowOff + (par & 1) * C::kRowBytes);
+            r.lse = r.place + RP;
+            r.qs = reinterpret_cast<float *>(r.lse + RP);
+            r.limit = reinterpret_cast<int *>(r.qs + RP);
+            return r;
+        };
+        // Q of the segment at `at`, number `par` of the CTA: 16 threads take a
+        // row, 8 values each.  It is fetched a segment ahead; the segment before
+        // last, whose place it takes, has all its S behind it.
+        auto load_q = [&](const PagedCursor &at, uint32_t par) {
+            const Rows ri = rows_of(par);
+            const uint32_t q_base = smem_u32(smem + C::kQOff + (par & 1) * C::kQBytes);
 #pragma unroll 1
             for (int r = threadIdx.x >> 4; r < C::kNS / C::kQTerms; r += NT / 16) {
                 const int x = threadIdx.x & 15;
-                const PagedRow row = paged_row(p, part, c, r);
+                const PagedRow row = paged_row(p, part, at, r);
                 const bool live = r < RP && row.counts;
-                const int hq = c.h * p.G + row.g;
+                const int hq = at.h * p.G + row.g;
                 const long long place = ((long long)row.b * p.Lq + row.i) * p.Hq + hq;
                 uint4 w = make_uint4(0, 0, 0, 0);
                 if (live)
@@ -436,35 +452,43 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                         hi[y] = to_codes(q2);
                         lo[y] = to_codes(__hmul2(__hsub2(q2, from_codes(hi[y])), __float2half2_rn(16.f)));
                     }
-                    const uint32_t at = smem_u32(smem + C::kQOff) + (((x >> 1) ^ (r & 7)) << 4) + (x & 1) * 8;
-                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + r * 128), "r"(hi[0] | hi[1] << 16),
+                    const uint32_t dst = q_base + (((x >> 1) ^ (r & 7)) << 4) + (x & 1) * 8;
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst + r * 128), "r"(hi[0] | hi[1] << 16),
                                  "r"(hi[2] | hi[3] << 16)
                                  : "memory");
-                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + (RP + r) * 128), "r"(lo[0] | lo[1] << 16),
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst + (RP + r) * 128), "r"(lo[0] | lo[1] << 16),
                                  "r"(lo[2] | lo[3] << 16)
                                  : "memory");
                 } else {
-                    const uint32_t at = smem_u32(smem + C::kQOff) + (x >> 3) * (C::kNS * 128) + r * 128 +
+                    const uint32_t dst = q_base + (x >> 3) * (C::kNS * 128) + r * 128 +
                                         (((x & 7) ^ (r & 7)) << 4);
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
                                  : "memory");
                 }
                 if (x == 0 && r < RP) {
-                    row_qs[r] = qs;
-                    row_limit[r] = live ? row.limit : 0x7fffffff; // rows of no use need no mask
-                    row_place[r] = live ? place : -1;
-                    row_lse[r] = ((long long)row.b * p.Hq + hq) * p.Lq + row.i;
+                    ri.qs[r] = qs;
+                    ri.limit[r] = live ? row.limit : 0x7fffffff; // rows of no use need no mask
+                    ri.place[r] = live ? place : -1;
+                    ri.lse[r] = ((long long)row.b * p.Hq + hq) * p.Lq + row.i;
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive(bars.q_full);
+            mbar_arrive(bars.q_full + (par & 1));
+        };
+        load_q(c, 0);
+        for (uint32_t seg = 0;; ++seg) {
+            const int n = cursor_take(c), len = source_len(c.b);
+            PagedCursor next = c;
+            const bool more = cursor_next(p, part, next, n);
+            if (more) load_q(next, seg + 1);
+            const Rows rows = rows_of(seg);
             soft_sync<NT>();
             float qs[kRT];
             int all = len; // keys below it are seen by every row
 #pragma unroll
             for (int r = 0; r < kRT; ++r) {
-                qs[r] = row_qs[row0 + r];
-                all = min(all, row_limit[row0 + r]);
+                qs[r] = rows.qs[row0 + r];
+                all = min(all, rows.limit[row0 + r]);
             }
 
             float m[kRT], l[kRT], ev_top = 0.f; // E: 0 while no value was seen
@@ -511,7 +535,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                 if (masked) {
 #pragma unroll
                     for (int r = 0; r < kRT; ++r)
-                        if (tid >= valid || key >= row_limit[row0 + r]) s[r] = -INFINITY;
+                        if (tid >= valid || key >= rows.limit[row0 + r]) s[r] = -INFINITY;
                 }
 #pragma unroll
                 for (int r = 0; r < kRT; ++r) grow |= s[r] > m[r] + C::kLazy;
@@ -643,7 +667,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
             const size_t slot = slot_row(part, c) + row0;
             if (tid < kRT) {
                 // a thread per row: its factor, and what is stored beside O
-                const long long place = row_place[row0 + tid];
+                const long long place = rows.place[row0 + tid];
                 float lr = 0.f, mr = row_f[row0 + tid], f = 1.f;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) lr += red[w * RS + tid];
@@ -655,7 +679,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                         mr = top;
                     }
                     f = lr == 0.f ? 0.f : f / lr;
-                    if (place >= 0) p.lse[row_lse[row0 + tid]] = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * kLn2;
+                    if (place >= 0) p.lse[rows.lse[row0 + tid]] = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * kLn2;
                 } else if (place >= 0) {
                     *reinterpret_cast<float2 *>(part.ml + (slot + tid) * 2) = make_float2(mr, lr);
                 }
@@ -672,7 +696,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
             tc_fence_before();
 #pragma unroll
             for (int y = 0; y < kRT; ++y) {
-                const long long place = row_place[row0 + y];
+                const long long place = rows.place[row0 + y];
                 if (place < 0) continue;
                 float v = o[0][y];
                 if (FP8) v += (o[1][y] + o[C::kPTerms - 1][y] * (1.f / 16.f)) * (1.f / 16.f);
@@ -682,7 +706,8 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                 else part.o[(slot + y) * kD + tid] = v;
             }
             soft_sync<NT>(); // the rows' arrays and red are free again
-            if (!cursor_next(p, part, c, n)) break;
+            if (!more) break;
+            c = next;
         }
     }
     await_previous();
@@ -706,7 +731,7 @@ cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &
         if (e != cudaSuccess) return e;
         set.fetch_or(bit, std::memory_order_release);
     }
-    return launch_paged(kern, p, part, Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kSmem, s, k, v, p, part);
+    return launch_dependent(kern, (unsigned)part.ctas, Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kSmem, s, k, v, p, part);
 }
 
 } // namespace

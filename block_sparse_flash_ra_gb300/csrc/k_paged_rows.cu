@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
-    allow_next();
+    begin_in_order(part);
     report_lengths(p, part);
     tc_fence_before();
     __syncthreads();
@@ -765,7 +765,7 @@ cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &
         if (e != cudaSuccess) return e;
         set.fetch_or(bit, std::memory_order_release);
     }
-    return launch_paged(kern, p, part, kThreads, Cfg<FP8>::kSmem, s, k, v, p, part);
+    return launch_dependent(kern, (unsigned)part.ctas, kThreads, Cfg<FP8>::kSmem, s, k, v, p, part);
 }
 
 } // namespace

@@ -30,6 +30,16 @@ __device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.laun
 // The kernels before this one in the stream have ended (see launch_dependent).
 __device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// An attention kernel's place in the stream.  The sequences' own part reads
+// what earlier kernels wrote (lengths, tables, queries, the cache) and reuses
+// the workspace, so it waits for them, and only then lets the next kernel in;
+// the prefix's part comes behind it, so all of that holds already.
+__device__ __forceinline__ void begin_in_order(const PagedPart &part)
+{
+    if (!part.prefix) await_previous();
+    allow_next();
+}
+
 // 2^(b - 127) of a cached row's scale byte; 255 marks a row without a value.
 // (0, which ra_kv_write does not store, is a subnormal power of two.)
 __device__ __forceinline__ float exp_byte_scale(uint32_t b)

@@ -54,8 +54,8 @@ struct PagedPart {
 // Launches a kernel that may start before its predecessor in the stream has
 // ended, once all of that kernel's CTAs have allowed it or are gone.  It
 // waits (griddepcontrol.wait) before it touches what came before it, and
-// every CTA waits before it ends, so that a kernel's end implies the end of
-// all before it.
+// every CTA of an attention kernel waits before it ends, so that its end
+// implies the end of all before it.
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
                              const A &...args)
@@ -71,18 +71,6 @@ cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block
     cfg.attrs = &at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-// An attention kernel's launch.  The sequences' own part comes first and is an
-// ordinary launch; the prefix's part depends on nothing of it and may run
-// beside its end.
-template <typename... P, typename... A>
-cudaError_t launch_paged(void (*kernel)(P...), const PagedProblem &, const PagedPart &part, unsigned block, size_t smem,
-                         cudaStream_t s, const A &...args)
-{
-    if (part.prefix) return launch_dependent(kernel, (unsigned)part.ctas, block, smem, s, args...);
-    kernel<<<part.ctas, block, smem, s>>>(args...);
-    return cudaGetLastError();
 }
 
 cudaError_t launch_kv_write(const PagedCache &c, int cache_dtype, const void *k, const void *v,
