@@ -67,10 +67,10 @@ struct Cfg {
     static constexpr int kExpOff = kRawOff + kRaws * kRaw; // 64 scale bytes per half
     static constexpr int kBarOff = kExpOff + kRaws * kHalf;
     // k_full[2], k_empty[2], v_full[2], v_empty[2], raw_full[4], raw_empty[4],
-    // q_full[2], s_full[2], p_full[2], o_full[2], v_clear[2], drain
-    static constexpr int kNumBars = 8 + 8 + 10 + 1;
+    // q_full[2], s_full[2], p_full[2], o_full[2], v_clear[2], ev_full[4], drain
+    static constexpr int kNumBars = 8 + 8 + 10 + 4 + 1;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8 + 8;
-    static constexpr int kScaleOff = kMiscOff + 16; // E of K tiles [4], EV of V tiles [2]
+    static constexpr int kScaleOff = kMiscOff + 16; // E of K tiles [4], EV of V tiles [4]
     static constexpr int kPairOff = kScaleOff + 48; // [tile][half][128] of the threads of a row
     static constexpr int kSmem = kPairOff + 2 * 2 * 128 * 4;
     static_assert(kSmem <= 232448 && kMiscOff % 16 == 0, "shared memory");
@@ -84,7 +84,7 @@ struct Cfg {
 
 struct Bars {
     uint64_t *k_full, *k_empty, *v_full, *v_empty, *raw_full, *raw_empty, *q_full, *s_full, *p_full, *o_full,
-        *v_clear, *drain;
+        *v_clear, *ev_full, *drain;
 };
 
 template <class C>
@@ -102,7 +102,8 @@ __device__ __forceinline__ Bars carve(uint8_t *smem)
     b.p_full = b.s_full + 2;
     b.o_full = b.p_full + 2;
     b.v_clear = b.o_full + 2;
-    b.drain = b.v_clear + 2;
+    b.ev_full = b.v_clear + 2;
+    b.drain = b.ev_full + 4;
     return b;
 }
 
@@ -204,8 +205,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::kMiscOff);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kMiscOff + 4);
     const WaitCtx ctx{abort_flag, p.status, p.timeout_ns};
-    // E by tile mod 4: tile g + 4 is widened only after P V of tile g + 1, which
-    // both softmaxes of g precede; EV by V buffer
+    // E and EV by tile mod 4: K of tile g + 4 is widened only after P V of tile
+    // g + 1, EV of tile g + 4 found only after P V of tile g + 1, and both
+    // softmaxes of g precede that
     volatile int *k_scale = reinterpret_cast<volatile int *>(smem + C::kScaleOff);
     volatile int *v_scale = k_scale + 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -224,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < 4; ++s) {
             mbar_init(bars.raw_full + s, 1);
             mbar_init(bars.raw_empty + s, 128);
+            mbar_init(bars.ev_full + s, 1);
         }
         mbar_init(bars.drain, 1);
         *abort_flag = 0;
@@ -371,8 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_commit_w(bars.k_empty + (g & 1));
                 for (int t = 0; t < n; ++t, ++g) {
                     const bool more = t + 1 < n;
-                    // (8-bit: the softmax waited for the wide V before it handed over P)
-                    if (!FP8 && !(ok = wait_all(bars.v_clear + (g & 1), (g >> 1) & 1))) break;
+                    if (!(ok = wait_all((FP8 ? bars.v_full : bars.v_clear) + (g & 1), (g >> 1) & 1))) break;
                     if (!(ok = issue_pv(0, g, g & 1, t == 0))) break;
                     if (!more) tc_commit_w(bars.o_full + 0);
                     if (more) {
@@ -421,7 +423,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(bars.v_clear + st);
                 } else {
                     const uint32_t tile = smem_u32(smem + (st_raw ? C::kVOff : C::kKOff) + st * C::kMat);
-                    if (!(ok = wait_all((st_raw ? bars.v_empty : bars.k_empty) + st, ((g >> 1) & 1) ^ 1))) break;
                     if (!(ok = wait_all(raw_full + 0, g & 1))) break;
                     if (!(ok = wait_all(raw_full + 1, g & 1))) break;
                     // the tile's largest exponent (1 at least: its float is normal);
@@ -432,14 +433,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (ev >= 0 && e <= ev + 7) e = ev;
                         ev = e;
                     }
+                    if (w == 0 && lane == 0) {
+                        (st_raw ? v_scale : k_scale)[g & 3] = e;
+                        // the softmax needs EV, but not the values
+                        if (st_raw) mbar_arrive(bars.ev_full + (g & 3));
+                    }
+                    if (!(ok = wait_all((st_raw ? bars.v_empty : bars.k_empty) + st, ((g >> 1) & 1) ^ 1))) break;
 #pragma unroll 1
                     for (int y = 0; y < 2; ++y) {
                         widen_half(tile, raw + y * C::kRaw, ex + y * kHalf, y * kHalf, valid, e, w, lane);
                         mbar_arrive(raw_empty + y);
-                    }
-                    if (w == 0 && lane == 0) {
-                        if (st_raw) v_scale[st] = e;
-                        else k_scale[g & 3] = e;
                     }
                     proxy_fence();
                     mbar_arrive((st_raw ? bars.v_full : bars.k_full) + st);
@@ -547,13 +550,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             for (int t = c.t0; mine && t < c.t0 + n; ++t, ++gx) {
                 const uint32_t gt = g + (t - c.t0); // the tile's number in this CTA
-                const int st = gt & 1;
                 const bool masked = all < (t + 1) * kKeys;
                 float a = a_row, fv = 1.f; // the tile's logit scale; the change of EV
                 if (FP8) {
-                    // the tile's values are wide by now or soon: P V waits for them anyway
-                    wait(bars.v_full + st, (gt >> 1) & 1);
-                    const int e = v_scale[st];
+                    wait(bars.ev_full + (gt & 3), (gt >> 2) & 1);
+                    const int e = v_scale[gt & 3];
                     if (t > c.t0 && e != ev) fv = ex2_approx((float)(ev - e));
                     ev = e;
                 }
