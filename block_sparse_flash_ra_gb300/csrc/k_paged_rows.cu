@@ -16,7 +16,7 @@
 //   warps 16-19     8-bit caches: widen K tiles to f16
 //   warps 20-23     the same for V; 16-bit caches: clear the values behind a
 //                   sequence's end
-//   warp 24         loads (a lane per page); warp 25 issues the products
+//   warps 24, 25    load K and V (a lane per page); warp 26 issues the products
 // TMEM: S_A [0,128), S_B [128,256), O_A [256,384), O_B [384,512).
 //
 // 8-bit caches: codes times a power of two are exact in f16, so a key becomes
@@ -45,8 +45,8 @@ namespace ra {
 namespace {
 
 constexpr int kKeys = 128, kHalf = 64, kD = 128;
-constexpr int kThreads = 832;
-constexpr int kWideWarpK = 16, kWideWarpV = 20, kLoadWarp = 24, kMmaWarp = 25;
+constexpr int kThreads = 864;
+constexpr int kWideWarpK = 16, kWideWarpV = 20, kLoadWarp = 24, kMmaWarp = 26;
 // The softmax of 32 keys takes the row's present reference for granted:
 // weights are computed at once, and only when a logit passes the reference by
 // 2^13 (2^60 in bf16) -- one barrier with an or over the two warps of 32 rows
@@ -64,11 +64,13 @@ struct Cfg {
     static constexpr int kKOff = 2 * kMat;
     static constexpr int kVOff = kKOff + 2 * kMat;
     static constexpr int kRawOff = kVOff + 2 * kMat;
-    static constexpr int kExpOff = kRawOff + kRaws * kRaw; // 64 scale bytes per half
-    static constexpr int kBarOff = kExpOff + kRaws * kHalf;
+    // scale bytes of K tiles [2] and V tiles [2]: a tile's come before its second half
+    static constexpr int kExpOff = kRawOff + kRaws * kRaw;
+    static constexpr int kBarOff = kExpOff + (FP8 ? 4 * kKeys : 0);
     // k_full[2], k_empty[2], v_full[2], v_empty[2], raw_full[4], raw_empty[4],
-    // q_full[2], s_full[2], p_full[2], o_full[2], v_clear[2], ev_full[4], drain
-    static constexpr int kNumBars = 8 + 8 + 10 + 4 + 1;
+    // q_full[2], s_full[2], p_full[2], o_full[2], v_clear[2], ev_full[4],
+    // e_full[4], drain
+    static constexpr int kNumBars = 8 + 8 + 10 + 4 + 4 + 1;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8 + 8;
     static constexpr int kScaleOff = kMiscOff + 16; // E of K tiles [4], EV of V tiles [4]
     static constexpr int kPairOff = kScaleOff + 48; // [tile][half][128] of the threads of a row
@@ -84,7 +86,7 @@ struct Cfg {
 
 struct Bars {
     uint64_t *k_full, *k_empty, *v_full, *v_empty, *raw_full, *raw_empty, *q_full, *s_full, *p_full, *o_full,
-        *v_clear, *ev_full, *drain;
+        *v_clear, *ev_full, *e_full, *drain;
 };
 
 template <class C>
@@ -103,7 +105,8 @@ __device__ __forceinline__ Bars carve(uint8_t *smem)
     b.o_full = b.p_full + 2;
     b.v_clear = b.o_full + 2;
     b.ev_full = b.v_clear + 2;
-    b.drain = b.ev_full + 4;
+    b.e_full = b.ev_full + 4; // by raw stage: K [2], V [2]
+    b.drain = b.e_full + 4;
     return b;
 }
 
@@ -227,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bars.raw_full + s, 1);
             mbar_init(bars.raw_empty + s, 128);
             mbar_init(bars.ev_full + s, 1);
+            mbar_init(bars.e_full + s, 1);
         }
         mbar_init(bars.drain, 1);
         *abort_flag = 0;
@@ -256,62 +260,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool any = cursor_begin(p, part, blockIdx.x, c);
 
     if (warp >= kLoadWarp) {
-        if (any && warp == kLoadWarp) {
+        if (any && warp < kMmaWarp) {
             // ------------------------------------------------------------ loads
-            // lane x fetches box x of a half tile (codes) or of a tile
+            // a warp for K, one for V; lane x fetches box x of a half tile (codes)
+            // or of a tile
             constexpr int kPart = FP8 ? kHalf : kKeys, kParts = kKeys / kPart;
+            const int m = warp - kLoadWarp;
+            const void *tm = m ? &tm_v : &tm_k;
+            const uint8_t *exps = m ? p.c.v_exp : p.c.k_exp;
             const int box = min(p.c.page, kPart), per = kPart / box;
             uint32_t g = 0;
             bool ok = true;
             for (;;) {
                 const int n = cursor_take(c), len = source_len(c.b);
                 for (int t = c.t0; ok && t < c.t0 + n; ++t, ++g) {
-                    // page entries of the tile: lane x of half y
-                    int page[kParts];
+                    const int valid = len - t * kKeys, st = g & 1;
+                    // the boxes of the tile's parts: where they are in the cache
+                    int z[kParts], boxes[kParts];
+                    bool good[kParts];
 #pragma unroll
                     for (int y = 0; y < kParts; ++y) {
-                        const int first = t * kKeys + y * kPart + lane * box;
-                        page[y] = lane < per && first < len ? page_entry(p, part, c.b, first) : 0;
+                        boxes[y] = max(0, (min(valid - y * kPart, kPart) + box - 1) / box);
+                        const bool mine = lane < boxes[y];
+                        const int page = mine ? page_entry(p, part, c.b, t * kKeys + y * kPart + lane * box) : 0;
+                        good[y] = mine && page_valid(p, page);
+                        z[y] = good[y] ? page * p.c.Hkv + c.h : p.c.n_pages * p.c.Hkv; // out of range: zeros
                     }
+                    const int in_page = (t * kKeys + lane * box) & (p.c.page - 1);
+                    if (FP8) {
 #pragma unroll
-                    for (int m = 0; m < 2 && ok; ++m) {
+                        for (int y = 0; y < kParts; ++y) {
+                            const int rs = 2 * m + y;
+                            if (!(ok = wait_all(bars.raw_empty + rs, (g & 1) ^ 1))) break;
+                            if (y == 0) {
+                                // the tile's scale bytes (this stage's last user is widened)
+                                uint8_t *e = smem + C::kExpOff + (2 * m + st) * kKeys + lane * box;
+                                int bytes = 0;
 #pragma unroll
-                        for (int y = 0; y < kParts && ok; ++y) {
-                            const int first = t * kKeys + y * kPart;
-                            const int boxes = max(0, (min(len - first, kPart) + box - 1) / box);
-                            const bool mine = lane < boxes, good = mine && page_valid(p, page[y]);
-                            const int z = good ? page[y] * p.c.Hkv + c.h : p.c.n_pages * p.c.Hkv; // out of range: zeros
-                            const int off = (first + lane * box) & (p.c.page - 1);
-                            if (FP8) {
-                                const int st = 2 * m + y;
-                                if (!(ok = wait_all(bars.raw_empty + st, (g & 1) ^ 1))) break;
-                                uint8_t *e = smem + C::kExpOff + st * kHalf + lane * box;
-                                const int n_good = __popc(__ballot_sync(0xffffffffu, good));
-                                if (mine && !good) { // zeros, at a scale of one
-                                    for (int j = 0; j < box; ++j) e[j] = 127;
-                                    proxy_fence();
+                                for (int q = 0; q < kParts; ++q) {
+                                    if (lane < boxes[q] && !good[q]) { // zeros, at a scale of one
+                                        for (int j = 0; j < box; ++j) e[q * kPart + j] = 127;
+                                        proxy_fence();
+                                    }
+                                    bytes += __popc(__ballot_sync(0xffffffffu, good[q])) * box;
                                 }
+                                if (lane == 0) mbar_expect_tx(bars.e_full + 2 * m + st, bytes);
                                 __syncwarp();
-                                if (lane == 0) mbar_expect_tx(bars.raw_full + st, boxes * box * kD + n_good * box);
-                                __syncwarp();
-                                if (mine)
-                                    tma_load_3d(smem + C::kRawOff + st * C::kRaw + lane * box * 128, m ? &tm_v : &tm_k,
-                                                bars.raw_full + st, 0, off, z);
-                                if (good)
-                                    bulk_load(e, (m ? p.c.v_exp : p.c.k_exp) + ((size_t)z << p.c.page_shift) + off, box,
-                                              bars.raw_full + st);
-                            } else {
-                                const int st = g & 1;
-                                if (!(ok = wait_all((m ? bars.v_empty : bars.k_empty) + st, ((g >> 1) & 1) ^ 1))) break;
-                                uint64_t *full = (m ? bars.v_full : bars.k_full) + st;
-                                if (lane == 0) mbar_expect_tx(full, boxes * box * kD * 2);
-                                __syncwarp();
-                                uint8_t *dst = smem + (m ? C::kVOff : C::kKOff) + st * C::kMat + lane * box * 128;
-                                if (mine)
-                                    for (int hf = 0; hf < 2; ++hf)
-                                        tma_load_3d(dst + hf * (kKeys * 128), m ? &tm_v : &tm_k, full, hf * 64, off, z);
+#pragma unroll
+                                for (int q = 0; q < kParts; ++q)
+                                    if (good[q])
+                                        bulk_load(e + q * kPart,
+                                                  exps + ((size_t)z[q] << p.c.page_shift) + ((in_page + q * kPart) & (p.c.page - 1)), box,
+                                                  bars.e_full + 2 * m + st);
                             }
+                            if (lane == 0) mbar_expect_tx(bars.raw_full + rs, boxes[y] * box * kD);
+                            __syncwarp();
+                            if (lane < boxes[y])
+                                tma_load_3d(smem + C::kRawOff + rs * C::kRaw + lane * box * 128, tm, bars.raw_full + rs, 0,
+                                            (in_page + y * kPart) & (p.c.page - 1), z[y]);
                         }
+                    } else {
+                        if (!(ok = wait_all((m ? bars.v_empty : bars.k_empty) + st, ((g >> 1) & 1) ^ 1))) break;
+                        uint64_t *full = (m ? bars.v_full : bars.k_full) + st;
+                        if (lane == 0) mbar_expect_tx(full, boxes[0] * box * kD * 2);
+                        __syncwarp();
+                        uint8_t *dst = smem + (m ? C::kVOff : C::kKOff) + st * C::kMat + lane * box * 128;
+                        if (lane < boxes[0])
+                            for (int hf = 0; hf < 2; ++hf)
+                                tma_load_3d(dst + hf * (kKeys * 128), tm, full, hf * 64, in_page, z[0]);
                     }
                 }
                 if (!ok || !cursor_next(p, part, c, n)) break;
@@ -319,14 +335,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) {
                 // copies on their way land before the CTA ends (a phase that
                 // passed already, or was not begun, only runs the clock)
-                for (int s = 0; s < (FP8 ? 4 : 2); ++s)
+                for (int s = 0; s < 2; ++s)
                     for (uint32_t x = 0; x < 2 && x <= g; ++x) {
-                        const uint32_t ph = FP8 ? (g - x) & 1 : ((g - x) >> 1) & 1;
+                        const uint32_t two = ((g - x) >> 1) & 1;
                         if (FP8) {
-                            wait_drain(bars.raw_full + s, ph, kDrainNs);
+                            wait_drain(bars.raw_full + 2 * m + s, (g - x) & 1, kDrainNs);
+                            wait_drain(bars.e_full + 2 * m + s, two, kDrainNs);
                         } else {
-                            wait_drain(bars.k_full + s, ph, kDrainNs);
-                            wait_drain(bars.v_full + s, ph, kDrainNs);
+                            wait_drain((m ? bars.v_full : bars.k_full) + s, two, kDrainNs);
                         }
                     }
             }
@@ -400,7 +416,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= kWideWarpK) {
         // ---------------------------------------------------------------- tiles
         const int w = warp & 3, st_raw = warp >= kWideWarpV ? 2 : 0;
-        const uint8_t *ex = smem + C::kExpOff + st_raw * kHalf;
         const uint32_t raw = smem_u32(smem + C::kRawOff + st_raw * C::kRaw);
         uint64_t *raw_full = bars.raw_full + st_raw, *raw_empty = bars.raw_empty + st_raw;
         uint32_t g = 0;
@@ -423,8 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(bars.v_clear + st);
                 } else {
                     const uint32_t tile = smem_u32(smem + (st_raw ? C::kVOff : C::kKOff) + st * C::kMat);
-                    if (!(ok = wait_all(raw_full + 0, g & 1))) break;
-                    if (!(ok = wait_all(raw_full + 1, g & 1))) break;
+                    const uint8_t *ex = smem + C::kExpOff + (st_raw + st) * kKeys;
+                    if (!(ok = wait_all(bars.e_full + st_raw + st, (g >> 1) & 1))) break;
                     // the tile's largest exponent (1 at least: its float is normal);
                     // rows without a value do not count
                     int e = max(max(top_exp(ex, valid, lane), top_exp(ex + kHalf, valid - kHalf, lane)), 1);
@@ -440,10 +455,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (!(ok = wait_all((st_raw ? bars.v_empty : bars.k_empty) + st, ((g >> 1) & 1) ^ 1))) break;
 #pragma unroll 1
-                    for (int y = 0; y < 2; ++y) {
+                    for (int y = 0; y < 2 && ok; ++y) {
+                        if (!(ok = wait_all(raw_full + y, g & 1))) break;
                         widen_half(tile, raw + y * C::kRaw, ex + y * kHalf, y * kHalf, valid, e, w, lane);
                         mbar_arrive(raw_empty + y);
                     }
+                    if (!ok) break;
                     proxy_fence();
                     mbar_arrive((st_raw ? bars.v_full : bars.k_full) + st);
                 }
