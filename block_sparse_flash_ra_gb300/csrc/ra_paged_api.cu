@@ -149,14 +149,14 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
             a.ctas = 4 * kSms;
         } else if (c->D == 128 && a.rows > 32) {
             kernel = kRowsM;
-            a.seg_cost = 3;
+            a.seg_cost = 5;
             a.row_block = 256;
             a.by_groups = 1;
             a.tile = kPagedRowsTile;
             a.ctas = kSms;
         } else if (c->D == 128) {
             kernel = kKeysM;
-            a.seg_cost = 3;
+            a.seg_cost = 4;
             a.row_block = a.rows <= 8 ? 8 : a.rows <= 16 ? 16 : 32;
             a.tile = kPagedKeysTile;
             a.ctas = (c->dtype == RA_E4M3 && a.row_block <= 16 ? 2 : 1) * kSms;
