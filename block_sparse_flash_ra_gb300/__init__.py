@@ -117,6 +117,8 @@ _lib = None
 def lib():
     """The loaded C library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -433,33 +435,17 @@ def _ints(x, shape, name, device):
     raise ValueError(f"{name} must be contiguous and on the cache's device")
 
 
-class _On:
-    """Runs a helper's allocations and launches on the tensors' device and on the caller's
-    stream, so that what is allocated here is reused in that stream's order.  ``with`` gives
-    the stream's handle."""
-
-    def __init__(self, device, stream):
-        self.device, self.guards = device, ()
-        if stream is not None or device.index != torch.cuda.current_device():
-            self.guards = [torch.cuda.device(device)]
-            if stream is not None:
-                if isinstance(stream, int):
-                    stream = torch.cuda.ExternalStream(stream, device=device)
-                self.guards.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return _raw_stream(self.device.index)
-
-    def __exit__(self, *e):
-        for g in reversed(self.guards):
-            g.__exit__(*e)
-
-
-def _raw_stream(index):
-    # the handle without a Stream object around it: a small call's time is mostly Python's
-    return torch._C._cuda_getCurrentRawStream(index)
+def _on(device, stream, run):
+    """run(handle of the stream) on the tensors' device and on the caller's stream, allocations
+    included, so that what is allocated is reused in that stream's order."""
+    if stream is None and device.index == torch.cuda.current_device():
+        # the handle without a Stream object around it: a small call's time is mostly Python's
+        return run(torch._C._cuda_getCurrentRawStream(device.index))
+    with torch.cuda.device(device):
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        with torch.cuda.stream(stream):
+            return run(torch.cuda.current_stream().cuda_stream)
 
 
 def make_kv_cache(k, v, k_exp=None, v_exp=None) -> RaKvCache:
@@ -503,13 +489,16 @@ def new_kv_cache(n_pages, page_size, n_kv_heads, head_dim, dtype=torch.float8_e4
 
 
 def _token_stride(x, cache, name):
-    sh, st = x.shape, x.stride()
-    _need(len(sh) == 4 and sh[2:] == cache._row, f"{name} must be (B, L, {cache.Hkv}, {cache.D})")
-    _need(x.device == cache.device, f"{name} must be on the cache's device")
-    (B, L, H, D), row = sh, cache.Hkv * cache.D
-    step = st[1] if L > 1 else (st[0] if B > 1 else row)
-    _need(st[3] == 1 and (H == 1 or st[2] == D) and (B == 1 or st[0] == L * step) and step >= row,
-          f"{name}: a token's heads must be contiguous, and tokens and batches evenly spaced")
+    B, L, H, D = x.shape
+    sb, step, sh, sd = x.stride()
+    if L == 1:
+        step = sb if B > 1 else H * D
+    if not (sd == 1 and (sh == D or H == 1) and (B == 1 or sb == L * step) and step >= H * D
+            and (H, D) == cache._row and x.device == cache.device):
+        _need((H, D) == cache._row, f"{name} must be (B, L, {cache.Hkv}, {cache.D})")
+        _need(x.device == cache.device, f"{name} must be on the cache's device")
+        raise ValueError(
+            f"{name}: a token's heads must be contiguous, and tokens and batches evenly spaced")
     return step
 
 
@@ -520,19 +509,19 @@ def kv_write(cache, k, v, page_table, start, count=None, stream=None) -> None:
     dt = _DT.get(k.dtype)
     if dt is None or v.dtype != k.dtype:
         raise TypeError(f"k and v must both be bfloat16 or float32, not {k.dtype} and {v.dtype}")
-    _need(k.shape == v.shape, "k and v must have the same shape")
+    _need(k.dim() == 4 and k.shape == v.shape, "k and v must be (B, L, Hkv, D), of the same shape")
     ks, vs = _token_stride(k, cache, "k"), _token_stride(v, cache, "v")
     B, L = k.shape[:2]
     if B == 0 or L == 0:
         return
-    pages = page_table.shape[-1]
-    _ints(page_table, (B, pages), "page_table", cache.device)
-    _ints(start, (B,), "start", cache.device)
+    dev, pages = cache.device, page_table.shape[-1]
+    _ints(page_table, (B, pages), "page_table", dev)
+    _ints(start, (B,), "start", dev)
     if count is not None:
-        _ints(count, (B,), "count", cache.device)
-    with _On(cache.device, stream) as s:
-        _check(lib().ra_kv_write(cache._ref, k.data_ptr(), v.data_ptr(), dt, B, L, ks, vs,
-                                 page_table.data_ptr(), pages, start.data_ptr(), _ptr(count), s))
+        _ints(count, (B,), "count", dev)
+    _check(_on(dev, stream, lambda s: lib().ra_kv_write(
+        cache._ref, k.data_ptr(), v.data_ptr(), dt, B, L, ks, vs, page_table.data_ptr(), pages,
+        start.data_ptr(), None if count is None else count.data_ptr(), s)))
 
 
 def kv_read(cache, page_table, kv_len, L, dtype=torch.bfloat16, stream=None):
@@ -540,16 +529,18 @@ def kv_read(cache, page_table, kv_len, L, dtype=torch.bfloat16, stream=None):
     dt = _DT.get(dtype)
     if dt is None:
         raise TypeError(f"unsupported dtype {dtype}")
-    B, pages = page_table.shape[0], page_table.shape[-1]
-    _ints(page_table, (B, pages), "page_table", cache.device)
-    _ints(kv_len, (B,), "kv_len", cache.device)
-    with _On(cache.device, stream) as s:
-        k, v = (torch.empty((B, L) + cache._row, dtype=dtype, device=cache.device)
-                for _ in range(2))
+    dev, (B, pages) = cache.device, page_table.shape
+    _ints(page_table, (B, pages), "page_table", dev)
+    _ints(kv_len, (B,), "kv_len", dev)
+
+    def run(s):
+        k = torch.empty((B, L) + cache._row, dtype=dtype, device=dev)
+        v = torch.empty_like(k)
         if B and L:
             _check(lib().ra_kv_read(cache._ref, page_table.data_ptr(), pages, kv_len.data_ptr(), B,
                                     L, k.data_ptr(), v.data_ptr(), dt, s))
-    return k, v
+        return k, v
+    return _on(dev, stream, run)
 
 
 def make_paged_params(cache, q, page_table, kv_len, *, scale, causal=True, soft_cap=0.0, q_len=None,
@@ -605,12 +596,13 @@ def paged_forward(params, q, cache, out=None, lse=None, ws=None, stream=None):
               and lse.is_contiguous(), "lse must be (B, Hq, Lq) fp32")
     if ws is not None:
         _need(ws.device == dev and ws.is_contiguous(), "ws must be contiguous and on the cache's device")
-    with _On(dev, stream) as s:
-        out = torch.empty_like(q) if out is None else out
-        lse = torch.empty(params._lse, dtype=torch.float32, device=dev) if lse is None else lse
+
+    def run(s):
+        o = torch.empty_like(q) if out is None else out
+        e = torch.empty(params._lse, dtype=torch.float32, device=dev) if lse is None else lse
         if params._ws:
-            if ws is None:
-                ws = torch.empty(params._ws, dtype=torch.uint8, device=dev)
-            _check(lib().ra_attn_paged(cache._ref, params._ref, q.data_ptr(), out.data_ptr(),
-                                       lse.data_ptr(), ws.data_ptr(), _wsb(ws), s))
-    return out, lse
+            w = torch.empty(params._ws, dtype=torch.uint8, device=dev) if ws is None else ws
+            _check(lib().ra_attn_paged(cache._ref, params._ref, q.data_ptr(), o.data_ptr(),
+                                       e.data_ptr(), w.data_ptr(), _wsb(w), s))
+        return o, e
+    return _on(dev, stream, run)

@@ -105,13 +105,12 @@ int check_paged(const ra_kv_cache *c, const ra_paged_params *p)
     return RA_OK;
 }
 
-// Places on the line of a part's work (ra_paged.cuh) at full tables: they are
-// counted in 32 bits.
-bool line_fits(const ra_kv_cache *c, const ra_paged_params *p, const PagedPart &a)
+// Places on the line of a part's work (ra_paged.cuh) at full tables.
+double most_places(const ra_kv_cache *c, const ra_paged_params *p, const PagedPart &a)
 {
-    const double tokens = (double)(a.prefix ? p->prefix_pages : p->max_pages) * c->page_size;
-    const double tiles = tokens / a.tile + 1 + a.seg_cost;
-    return tiles * (a.prefix ? 1 : p->B) * a.n_rb * c->Hkv < 2147483648.0;
+    const long long tokens = (long long)(a.prefix ? p->prefix_pages : p->max_pages) * c->page_size;
+    const long long tiles = (tokens + a.tile - 1) / a.tile + a.seg_cost;
+    return (double)tiles * (a.prefix ? 1 : p->B) * a.n_rb * c->Hkv;
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -169,7 +168,10 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
         }
         a.n_rb = (a.rows + a.row_block - 1) / a.row_block;
         a.slot_rows = a.rows < a.row_block ? a.rows : a.row_block;
-        pl.fits &= line_fits(c, p, a);
+        // places are counted in 32 bits; a CTA without a place has nothing to do
+        const double places = most_places(c, p, a);
+        pl.fits &= places < 2147483648.0;
+        if (places < a.ctas) a.ctas = (int)places;
         a.direct = p->prefix_pages == 0;
         const size_t slots =
             a.direct ? 2 * (size_t)a.ctas : (size_t)a.ctas + (size_t)(k ? 1 : p->B) * a.n_rb * c->Hkv;
