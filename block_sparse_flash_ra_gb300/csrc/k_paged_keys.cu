@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
             mbar_init(bars.e_full + s, 1);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(bars.s_full + s, 1);
+            mbar_init(bars.s_full + s, FP8 ? 2 : 1);
             mbar_init(bars.s_empty + s, C::kSoftThreads);
             mbar_init(bars.p_full + s, C::kSoftThreads);
             mbar_init(bars.pv_done + s, 1);
@@ -252,6 +252,8 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
     }
     begin_in_order(part);
     report_lengths(p, part);
+    PagedCursor c; // found beside the barriers' and TMEM's setting up
+    const bool any = cursor_begin(p, part, blockIdx.x, c);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -261,8 +263,6 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
     };
     auto source_len = [&](int b) { return part.prefix ? paged_prefix_len(p) : paged_kv_len(p, b); };
 
-    PagedCursor c;
-    const bool any = cursor_begin(p, part, blockIdx.x, c);
     if (any && warp == C::kLoadWarp) {
         // ------------------------------------------------------------ loads
         // lane x fetches box x of a tile: its page number, then its K and V
@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
             for (int t = 0; ok && t < n; ++t, ++i) {
                 const int sk = i % C::kStages, sb = i & 1;
                 if (!(ok = wait_all(bars.k_full + sk, (i / C::kStages) & 1))) break;
+                if (FP8 && !(ok = wait_all(bars.e_full + i % C::kVStages, (i / C::kVStages) & 1))) break;
                 if (!(ok = wait_all(bars.s_empty + sb, ((i >> 1) & 1) ^ 1))) break;
                 tc_fence_after();
                 const uint64_t kd = kd0 + (uint32_t)((sk * C::kMat) >> 4);
@@ -374,6 +375,9 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                     mma_step<FP8>(tmem + sb * C::kNS, kd + (ao >> 4), qd + (bo >> 4), C::kIdescS, kk > 0 ? 1u : 0u);
                 }
                 tc_commit_w(bars.k_empty + sk);
+                // the softmax reads the tile's scale bytes as well as S: this arrival
+                // passes on what the wait for them has seen
+                if (FP8 && lane == 0) mbar_arrive(bars.s_full + sb);
                 tc_commit_w(bars.s_full + sb);
                 if (t > 0) ok = issue_pv(i - 1, t == 1);
             }
@@ -501,8 +505,10 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                 const bool masked = t * kKeys + kKeys > all;
                 float s[kRT];
                 float ks = 1.f, vs = 1.f, ev = 0.f;
+                wait(bars.s_full + sb, (i >> 1) & 1);
+                tc_fence_after();
+                tmem_ld<8>(lane_base + sb * C::kNS + row0, s);
                 if (FP8) {
-                    wait(bars.e_full + sv, (i / C::kVStages) & 1);
                     const uint8_t *e = smem + C::kExpOff + sv * 2 * kKeys + tid;
                     const uint32_t vb = e[kKeys];
                     ks = exp_byte_scale(e[0]);
@@ -510,9 +516,6 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                     // bytes behind the length and rows without a value do not count
                     if (tid < valid && vb != 255u) ev = fmaxf((float)vb, kMinExp);
                 }
-                wait(bars.s_full + sb, (i >> 1) & 1);
-                tc_fence_after();
-                tmem_ld<8>(lane_base + sb * C::kNS + row0, s);
                 if (FP8) {
                     float s2[kRT];
                     tmem_ld<8>(lane_base + sb * C::kNS + RP + row0, s2);

@@ -246,6 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     begin_in_order(part);
     report_lengths(p, part);
+    PagedCursor c; // found beside the barriers' and TMEM's setting up
+    const bool any = cursor_begin(p, part, blockIdx.x, c);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -256,9 +258,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto source_len = [&](int b) { return part.prefix ? paged_prefix_len(p) : paged_kv_len(p, b); };
     // an item with at most 128 rows has no tile B
     auto two_tiles = [&](const PagedCursor &c) { return part.rows - c.rb * part.row_block > 128; };
-    PagedCursor c;
-    const bool any = cursor_begin(p, part, blockIdx.x, c);
-
     if (warp >= kLoadWarp) {
         if (any && warp < kMmaWarp) {
             // ------------------------------------------------------------ loads
@@ -517,27 +516,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                         u[it] = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + (size_t)src * kD)[ch];
                 }
 #pragma unroll 1
-                for (int it = 0; it < 8; ++it) { // one piece of code for all: a cold fetch costs more than it
-                    const int r_in = (warp & 3) * 32 + y * 16 + 2 * it + (lane >> 4);
-                    uint32_t v[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+                for (int it = 0; it < 8; it += 2) { // one piece of code for all: a cold fetch costs more than it
 #pragma unroll
-                    for (int k = 0; k < 7; ++k) u[k] = u[k + 1];
-                    if (FP8) {
-                        uint32_t top = 0; // largest magnitude, as bf16 bits
+                    for (int z = 0; z < 2; ++z) {
+                        const int r_in = (warp & 3) * 32 + y * 16 + 2 * (it + z) + (lane >> 4);
+                        uint32_t v[4] = {u[z].x, u[z].y, u[z].z, u[z].w};
+                        if (FP8) {
+                            // largest magnitude, as bf16 bits, two at a time
+                            const uint32_t m = 0x7fff7fffu;
+                            uint32_t top = __vmaxu2(__vmaxu2(v[0] & m, v[1] & m), __vmaxu2(v[2] & m, v[3] & m));
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) top = max(top, max(v[k] & 0x7fffu, (v[k] >> 16) & 0x7fffu));
+                            for (int o = 1; o < 16; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+                            top = max(top & 0xffffu, top >> 16);
+                            const int e = top == 0 ? 0 : min(max((int)(top >> 7) - 127, -120), 120);
+                            const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-                        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        const int e = top == 0 ? 0 : min(max((int)(top >> 7) - 127, -120), 120);
-                        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            v[k] = pack16<true>(__uint_as_float(v[k] << 16) * inv, __uint_as_float(v[k] & 0xffff0000u) * inv);
-                        if (ch == 0) pair[r_in - row_in] = __uint_as_float((uint32_t)(127 + e) << 23);
+                            for (int k = 0; k < 4; ++k)
+                                v[k] = pack16<true>(__uint_as_float(v[k] << 16) * inv, __uint_as_float(v[k] & 0xffff0000u) * inv);
+                            if (ch == 0) pair[r_in - row_in] = __uint_as_float((uint32_t)(127 + e) << 23);
+                        }
+                        sts128(smem_u32(smem + C::kQOff + x * C::kMat) + (ch >> 3) * (kKeys * 128) + r_in * 128 +
+                                   (((ch & 7) ^ (r_in & 7)) << 4),
+                               make_uint4(v[0], v[1], v[2], v[3]));
                     }
-                    sts128(smem_u32(smem + C::kQOff + x * C::kMat) + (ch >> 3) * (kKeys * 128) + r_in * 128 +
-                               (((ch & 7) ^ (r_in & 7)) << 4),
-                           make_uint4(v[0], v[1], v[2], v[3]));
+#pragma unroll
+                    for (int k = 0; k < 6; ++k) u[k] = u[k + 2];
                 }
                 proxy_fence();
             }
