@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t kd0 = sdesc_sw128(smem_u32(smem + C::kKOff), 16, 1024);
             const uint64_t vd0 = sdesc_sw128(smem_u32(smem + C::kVOff), kKeys * 128, 1024);
             constexpr uint32_t kStep = C::kMat >> 4;
-            uint32_t g = 0, segs = 0, parts_b = 0;
+            uint32_t g = 0, segs = 0, segs_b = 0, parts_b = 0;
             bool ok = true;
             auto issue_s = [&](int x, uint32_t j) {
                 const uint64_t qd = qd0 + (uint32_t)(x * kStep), kd = kd0 + (j & 1) * kStep;
@@ -379,9 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int n = cursor_take(c);
                 const bool both = two_tiles(c);
                 // first S products of the segment
-                if (!(ok = wait_all(bars.q_full + 0, segs & 1))) break;
-                if (!(ok = wait_all(bars.q_full + 1, segs & 1))) break;
-                ++segs;
+                if (!(ok = wait_all(bars.q_full + 0, segs++ & 1))) break;
+                if (both && !(ok = wait_all(bars.q_full + 1, segs_b++ & 1))) break;
                 if (!(ok = wait_all(bars.k_full + (g & 1), (g >> 1) & 1))) break;
                 tc_fence_after();
                 issue_s(0, g);
@@ -544,7 +543,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 proxy_fence();
             }
-            mbar_arrive(bars.q_full + x);
+            // (tile B's threads run ahead over segments that have none: no arrival,
+            // or the barrier could pass two phases before anyone waits)
+            if (mine) mbar_arrive(bars.q_full + x);
             if (FP8 && mine) {
                 pair_sync();
                 a_row *= pair[0];

@@ -258,6 +258,13 @@ CASES = {
     "group17": dict(lens=[130], Hq=17, Hkv=1),
     "long_split": dict(lens=[5000], Hq=8, page=64),
     "many_short": dict(lens=[(37 * b) % 91 for b in range(150)], Hq=4),
+    # several segments to a CTA, for each size of row block; blocks of one tile and of two
+    "many_short_16": dict(lens=[(37 * b) % 91 for b in range(330)], Hq=16, Hkv=1),
+    "many_short_32": dict(lens=[(31 * b) % 140 for b in range(330)], Hq=32, Hkv=1, page=32),
+    "many_short_64": dict(lens=[(37 * b) % 191 for b in range(200)], Hq=8, Lq=16),
+    "many_short_200": dict(lens=[60 + (37 * b) % 91 for b in range(110)], Hq=8, Lq=50),
+    "many_short_d64": dict(lens=[(37 * b) % 91 for b in range(200)], Hq=24, Hkv=2, D=64),
+    "long_40_rows": dict(lens=[3100, 2500, 1], Hq=8, Lq=10, page=128),
     "draft": dict(lens=[70, 3, 129, 0], Hq=4, Lq=5),
     "draft_full": dict(lens=[70, 3, 129], Hq=4, Lq=3, causal=False),
     "draft_ragged": dict(lens=[70, 3, 129, 20], Hq=4, Lq=5, q_len=[5, 1, 0, 4]),
