@@ -43,13 +43,14 @@ constexpr int kWarps = 4;
 constexpr float kLazy = 4.f;   // growth of a row maximum (base 2) that is let pass
 constexpr float kPBias = 11.f; // 8-bit caches: weights are kept times 2^11 (2^15 with kLazy)
 
-template <int D, bool FP8>
+constexpr int D = 64;
+constexpr int kKeys = 32; // keys of one stage (per warp)
+constexpr int kTile = kPagedFewTile;
+static_assert(kTile == kWarps * kKeys, "a warp takes a quarter of a tile");
+
+template <bool FP8>
 struct Cfg {
-    static constexpr int kRowBytes = D * (FP8 ? 1 : 2);
-    static constexpr int kKeys = (!FP8 && D == 128) ? 16 : 32; // keys of one stage (per warp)
-    static constexpr int kTile = kWarps * kKeys;
-    static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128; // one TMA box is this wide
-    static constexpr int kHalves = kRowBytes / kBoxBytes;
+    static constexpr int kRowBytes = D * (FP8 ? 1 : 2); // one TMA box is this wide
     static constexpr int kMatBytes = kKeys * kRowBytes;
     static constexpr int kStageBytes = 2 * kMatBytes;
     static constexpr int kStages = kStageBytes <= 4096 ? 4 : 3;
@@ -134,12 +135,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 }
 
 // Shared-memory address of 16-byte chunk c of row j of a staged matrix.
-template <int D, bool FP8>
+template <bool FP8>
 __device__ __forceinline__ uint32_t chunk_at(uint32_t base, int j, int c)
 {
-    using C = Cfg<D, FP8>;
-    if (C::kBoxBytes == 64) return base + j * 64 + ((c ^ ((j >> 1) & 3)) << 4);
-    return base + (c >> 3) * (C::kKeys * 128) + j * 128 + (((c & 7) ^ (j & 7)) << 4);
+    if (FP8) return base + j * 64 + ((c ^ ((j >> 1) & 3)) << 4);
+    return base + j * 128 + ((c ^ (j & 7)) << 4);
 }
 
 // What a warp loads next: its keys of one tile.
@@ -152,13 +152,13 @@ struct Ahead {
     bool live;
 };
 
-template <int D, bool FP8, int ROWS>
+template <bool FP8, int ROWS>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      PagedProblem p, PagedPart part)
 {
-    using C = Cfg<D, FP8>;
-    constexpr int NB = C::kKeys / 8;   // key groups of a stage
+    using C = Cfg<FP8>;
+    constexpr int NB = kKeys / 8;   // key groups of a stage
     constexpr int KS = D / 16;         // contraction steps of Q K^T
     constexpr int OB = D / 8;          // O blocks
     constexpr int RH = ROWS / 8;       // row halves that a thread holds
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     }
 
     // ---- the loads ahead.  A box is as many keys as a page and a stage share.
-    const int box = min(p.c.page, C::kKeys);
+    const int box = min(p.c.page, kKeys);
     Ahead a;
     a.c = c;
     auto source_len = [&](int b) { return part.prefix ? paged_prefix_len(p) : paged_kv_len(p, b); };
@@ -207,11 +207,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     // the read of their page numbers
     auto look = [&]() {
         while (a.live) {
-            const int first = a.c.t0 * C::kTile + warp * C::kKeys;
-            a.valid = min(a.len - first, C::kKeys);
+            const int first = a.c.t0 * kTile + warp * kKeys;
+            a.valid = min(a.len - first, kKeys);
             if (a.valid > 0) {
                 a.page[0] = page_entry(p, part, a.c.b, first);
-                if (box < C::kKeys && a.valid > box) a.page[1] = page_entry(p, part, a.c.b, first + box);
+                if (box < kKeys && a.valid > box) a.page[1] = page_entry(p, part, a.c.b, first + box);
                 return;
             }
             onward();
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         const int s = issued % C::kStages;
         if (lane == 0) {
             const int boxes = (a.valid + box - 1) / box;
-            const int first = a.c.t0 * C::kTile + warp * C::kKeys;
+            const int first = a.c.t0 * kTile + warp * kKeys;
             const int off = first & (p.c.page - 1);
             uint8_t *eb = smem + C::kExpOff + (warp * C::kStages + s) * C::kExpBytes;
             int bytes = boxes * box * C::kRowBytes * 2;
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
                 good[x] = x < boxes && page_valid(p, a.page[x]);
                 if (FP8 && good[x]) bytes += 2 * box;
                 if (FP8 && x < boxes && !good[x]) {
-                    for (int j = 0; j < box; ++j) eb[x * box + j] = eb[C::kKeys + x * box + j] = 127;
+                    for (int j = 0; j < box; ++j) eb[x * box + j] = eb[kKeys + x * box + j] = 127;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
             }
@@ -246,16 +246,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
             for (int x = 0; x < 2; ++x) {
                 if (x >= boxes) break;
                 const int z = good[x] ? a.page[x] * p.c.Hkv + a.c.h : p.c.n_pages * p.c.Hkv;
-#pragma unroll
-                for (int hf = 0; hf < C::kHalves; ++hf) {
-                    const uint32_t at = dst + hf * C::kKeys * 128 + x * box * C::kBoxBytes;
-                    tma_load_3d(at, &tm_k, bars + s, hf * 64, off, z);
-                    tma_load_3d(at + C::kMatBytes, &tm_v, bars + s, hf * 64, off, z);
-                }
+                const uint32_t at = dst + x * box * C::kRowBytes;
+                tma_load_3d(at, &tm_k, bars + s, 0, off, z);
+                tma_load_3d(at + C::kMatBytes, &tm_v, bars + s, 0, off, z);
                 if (FP8 && good[x]) {
                     const size_t row = ((size_t)z << p.c.page_shift) + off;
                     bulk_load(eb + x * box, p.c.k_exp + row, box, bars + s);
-                    bulk_load(eb + C::kKeys + x * box, p.c.v_exp + row, box, bars + s);
+                    bulk_load(eb + kKeys + x * box, p.c.v_exp + row, box, bars + s);
                 }
             }
         }
@@ -348,8 +345,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         all = __reduce_min_sync(0xffffffffu, all);
 
         for (int t = c.t0; t < c.t0 + n; ++t) {
-            const int first = t * C::kTile + warp * C::kKeys;
-            const int valid = min(len - first, C::kKeys);
+            const int first = t * kTile + warp * kKeys;
+            const int valid = min(len - first, kKeys);
             if (valid <= 0) continue;
             const int st = used % C::kStages;
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bars + st, (used / C::kStages) & 1, ctx)) != 0;
@@ -357,11 +354,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
             ++used;
             const uint32_t kb = ring + st * C::kStageBytes, vb = kb + C::kMatBytes;
             const uint32_t eb = exps + st * C::kExpBytes;
-            if (valid < C::kKeys) {
+            if (valid < kKeys) {
                 // values behind the length: whatever is there, weight 0 must give 0
-                for (int x = lane; x < (C::kKeys - valid) * (C::kRowBytes / 16); x += 32) {
+                for (int x = lane; x < (kKeys - valid) * (C::kRowBytes / 16); x += 32) {
                     const int j = valid + x / (C::kRowBytes / 16), ch = x % (C::kRowBytes / 16);
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(chunk_at<D, FP8>(vb, j, ch)), "r"(0) : "memory");
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(chunk_at<FP8>(vb, j, ch)), "r"(0) : "memory");
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -374,7 +371,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
                 s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
 #pragma unroll
                 for (int x = 0; x < C::kRowBytes / 64; ++x) {
-                    const uint4 v = lds128(chunk_at<D, FP8>(kb, j, t4 + 4 * x));
+                    const uint4 v = lds128(chunk_at<FP8>(kb, j, t4 + 4 * x));
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                     if (FP8) {
 #pragma unroll
@@ -388,7 +385,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
             }
             // ---- logits in base 2; the row maxima
             float vs[NB][2], top[2] = {-INFINITY, -INFINITY}, ev = -INFINITY;
-            const bool masked = first + valid > all || valid < C::kKeys;
+            const bool masked = first + valid > all || valid < kKeys;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -397,7 +394,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
                     float ks = 1.f;
                     if (FP8) {
                         ks = exp_byte_scale(lds8(eb + j));
-                        const uint32_t b = lds8(eb + C::kKeys + j);
+                        const uint32_t b = lds8(eb + kKeys + j);
                         vs[nb][y] = exp_byte_scale(b);
                         // bytes behind the length and rows without a value do not count;
                         // 12 keeps 2^(kPBias + 127 - E) finite
@@ -406,7 +403,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 #pragma unroll
                     for (int r = 0; r < RH; ++r) {
                         float x = s[nb][2 * r + y] * (FP8 ? qs[r] * ks : qs[r]);
-                        if (to_cap > 0.f) x = cap2 * tanh_fast(x * to_cap);
+                        if (to_cap > 0.f) x = cap2 * tanh_near(x * to_cap);
                         if (masked && !(first + j < limit[r])) x = -INFINITY;
                         s[nb][2 * r + y] = x;
                         top[r] = fmaxf(top[r], x);
@@ -474,49 +471,36 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
                     }
                 const int j0 = kk * 16 + key_perm(2 * t4), j1 = kk * 16 + key_perm(2 * t4 + 1);
                 if (FP8) {
-                    constexpr int W = D / 32; // words of a thread's D / 8 codes
-                    uint32_t v[4][4];
+                    uint2 v[4]; // a thread's D / 8 codes of a value
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const int j = (y & 1 ? j1 : j0) + (y >> 1) * 8;
-                        if (W == 4) {
-                            const uint4 q = lds128(chunk_at<D, FP8>(vb, j, g));
-                            v[y][0] = q.x, v[y][1] = q.y, v[y][2] = q.z, v[y][3] = q.w;
-                        } else {
-                            const uint2 q = lds64(chunk_at<D, FP8>(vb, j, g >> 1) + (g & 1) * 8);
-                            v[y][0] = q.x, v[y][1] = q.y;
-                        }
-                    }
+                    for (int y = 0; y < 4; ++y)
+                        v[y] = lds64(chunk_at<FP8>(vb, (y & 1 ? j1 : j0) + (y >> 1) * 8, g >> 1) + (g & 1) * 8);
 #pragma unroll
-                    for (int w = 0; w < W; ++w)
+                    for (int w = 0; w < 2; ++w)
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
                             const uint32_t sel = z ? 0x7362u : 0x5140u;
-                            const uint32_t x0 = __byte_perm(v[0][w], v[1][w], sel);
-                            const uint32_t x1 = __byte_perm(v[2][w], v[3][w], sel);
+                            const uint32_t x0 = w ? __byte_perm(v[0].y, v[1].y, sel) : __byte_perm(v[0].x, v[1].x, sel);
+                            const uint32_t x1 = w ? __byte_perm(v[2].y, v[3].y, sel) : __byte_perm(v[2].x, v[3].x, sel);
                             mma<FP8, ROWS>(o[4 * w + 2 * z], pa, e4m3x2_to_f16x2(x0 & 0xffffu), e4m3x2_to_f16x2(x1 & 0xffffu));
                             mma<FP8, ROWS>(o[4 * w + 2 * z + 1], pa, e4m3x2_to_f16x2(x0 >> 16), e4m3x2_to_f16x2(x1 >> 16));
                         }
                 } else {
+                    uint4 v[4];
 #pragma unroll
-                    for (int hv = 0; hv < OB / 8; ++hv) {
-                        uint4 v[4];
+                    for (int y = 0; y < 4; ++y) v[y] = lds128(chunk_at<FP8>(vb, (y & 1 ? j1 : j0) + (y >> 1) * 8, g));
+                    const uint32_t u[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w}, {v[1].x, v[1].y, v[1].z, v[1].w},
+                                              {v[2].x, v[2].y, v[2].z, v[2].w}, {v[3].x, v[3].y, v[3].z, v[3].w}};
 #pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            v[y] = lds128(chunk_at<D, FP8>(vb, (y & 1 ? j1 : j0) + (y >> 1) * 8, g + 8 * hv));
-                        const uint32_t u[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w}, {v[1].x, v[1].y, v[1].z, v[1].w},
-                                                  {v[2].x, v[2].y, v[2].z, v[2].w}, {v[3].x, v[3].y, v[3].z, v[3].w}};
+                    for (int w = 0; w < 4; ++w)
 #pragma unroll
-                        for (int w = 0; w < 4; ++w)
-#pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                const uint32_t sel = z ? 0x7632u : 0x5410u;
-                                const uint32_t b0 = __byte_perm(u[0][w], u[1][w], sel);
-                                const uint32_t b1 = __byte_perm(u[2][w], u[3][w], sel);
-                                mma<FP8, ROWS>(o[8 * hv + 2 * w + z], pa, b0, b1);
-                                mma<FP8, ROWS>(o[8 * hv + 2 * w + z], pl, b0, b1);
-                            }
-                    }
+                        for (int z = 0; z < 2; ++z) {
+                            const uint32_t sel = z ? 0x7632u : 0x5410u;
+                            const uint32_t b0 = __byte_perm(u[0][w], u[1][w], sel);
+                            const uint32_t b1 = __byte_perm(u[2][w], u[3][w], sel);
+                            mma<FP8, ROWS>(o[2 * w + z], pa, b0, b1);
+                            mma<FP8, ROWS>(o[2 * w + z], pl, b0, b1);
+                        }
                 }
             }
             __syncwarp(); // every lane has read the stage
@@ -573,9 +557,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
                 }
                 v[0][2 * x] = z.x, v[0][2 * x + 1] = z.y, v[1][2 * x] = z.z, v[1][2 * x + 1] = z.w;
             }
-            // column n, block x: d = n * (D / 8) + x for codes, and for bf16
-            // d = (x / 8) * 64 + n * 8 + x % 8
-            constexpr int RUN = FP8 ? OB : 8;
+            // column n, block x: d = n * 8 + x
             if (stores_whole(part, c, n)) {
                 if (!row.counts) continue;
                 const int hq = c.h * p.G + row.g;
@@ -589,16 +571,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
                 const float inv = lr == 0.f ? 0.f : fs / lr;
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + (((size_t)row.b * p.Lq + row.i) * p.Hq + hq) * D;
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
-#pragma unroll
-                    for (int x = 0; x < OB; x += 8) {
-                        uint4 w;
-                        w.x = pack_bf16x2(v[y][x] * inv, v[y][x + 1] * inv);
-                        w.y = pack_bf16x2(v[y][x + 2] * inv, v[y][x + 3] * inv);
-                        w.z = pack_bf16x2(v[y][x + 4] * inv, v[y][x + 5] * inv);
-                        w.w = pack_bf16x2(v[y][x + 6] * inv, v[y][x + 7] * inv);
-                        *reinterpret_cast<uint4 *>(out + (x / RUN) * 64 + (2 * t4 + y) * RUN + x % RUN) = w;
-                    }
+                for (int y = 0; y < 2; ++y) {
+                    uint4 w;
+                    w.x = pack_bf16x2(v[y][0] * inv, v[y][1] * inv);
+                    w.y = pack_bf16x2(v[y][2] * inv, v[y][3] * inv);
+                    w.z = pack_bf16x2(v[y][4] * inv, v[y][5] * inv);
+                    w.w = pack_bf16x2(v[y][6] * inv, v[y][7] * inv);
+                    *reinterpret_cast<uint4 *>(out + (2 * t4 + y) * 8) = w;
+                }
                 if (t4 == 0)
                     p.lse[((size_t)row.b * p.Hq + hq) * p.Lq + row.i] = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * kLn2;
             } else if (in_block < part.slot_rows) {
@@ -608,7 +588,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
                 for (int y = 0; y < 2; ++y)
 #pragma unroll
                     for (int x = 0; x < OB; x += 4)
-                        *reinterpret_cast<float4 *>(dst + (x / RUN) * 64 + (2 * t4 + y) * RUN + x % RUN) =
+                        *reinterpret_cast<float4 *>(dst + (2 * t4 + y) * 8 + x) =
                             make_float4(v[y][x], v[y][x + 1], v[y][x + 2], v[y][x + 3]);
                 if (t4 == 0) *reinterpret_cast<float2 *>(part.ml + at * 2) = make_float2(mt[r], lt[r]);
             }
@@ -622,46 +602,30 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     await_previous();
 }
 
-template <int D, bool FP8, int ROWS>
+template <bool FP8, int ROWS>
 cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s)
 {
-    auto kern = paged_few_kernel<D, FP8, ROWS>;
+    auto kern = paged_few_kernel<FP8, ROWS>;
     static std::atomic<uint64_t> set{0}; // devices whose copy of the kernel has its attribute
     const uint64_t bit = 1ull << p.device;
     if (!(set.load(std::memory_order_acquire) & bit)) {
         const cudaError_t e =
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, FP8>::kSmem);
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<FP8>::kSmem);
         if (e != cudaSuccess) return e;
         set.fetch_or(bit, std::memory_order_release);
     }
-    return launch_dependent(kern, (unsigned)part.ctas, kWarps * 32, Cfg<D, FP8>::kSmem, s, k, v, p, part);
+    return launch_dependent(kern, (unsigned)part.ctas, kWarps * 32, Cfg<FP8>::kSmem, s, k, v, p, part);
 }
 
 } // namespace
-
-int paged_few_tile(int D, int cache_dtype)
-{
-    if (cache_dtype == RA_E4M3) return D == 64 ? Cfg<64, true>::kTile : Cfg<128, true>::kTile;
-    return D == 64 ? Cfg<64, false>::kTile : Cfg<128, false>::kTile;
-}
-
-int paged_few_box(int D, int cache_dtype, int page)
-{
-    const int keys = paged_few_tile(D, cache_dtype) / kWarps;
-    return page < keys ? page : keys;
-}
 
 cudaError_t launch_paged_few(const PagedProblem &p, const PagedPart &part, int cache_dtype, const void *tm_k,
                              const void *tm_v, cudaStream_t s)
 {
     const CUtensorMap &k = *static_cast<const CUtensorMap *>(tm_k), &v = *static_cast<const CUtensorMap *>(tm_v);
     const bool few = part.row_block == 8;
-    if (cache_dtype == RA_E4M3) {
-        if (p.c.D == 64) return few ? go<64, true, 8>(p, part, k, v, s) : go<64, true, 16>(p, part, k, v, s);
-        return few ? go<128, true, 8>(p, part, k, v, s) : go<128, true, 16>(p, part, k, v, s);
-    }
-    if (p.c.D == 64) return few ? go<64, false, 8>(p, part, k, v, s) : go<64, false, 16>(p, part, k, v, s);
-    return few ? go<128, false, 8>(p, part, k, v, s) : go<128, false, 16>(p, part, k, v, s);
+    if (cache_dtype == RA_E4M3) return few ? go<true, 8>(p, part, k, v, s) : go<true, 16>(p, part, k, v, s);
+    return few ? go<false, 8>(p, part, k, v, s) : go<false, 16>(p, part, k, v, s);
 }
 
 } // namespace ra

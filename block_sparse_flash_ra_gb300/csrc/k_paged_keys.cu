@@ -532,8 +532,16 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
 #pragma unroll
                 for (int r = 0; r < kRT; ++r) s[r] *= FP8 ? qs[r] * ks : qs[r];
                 if (to_cap > 0.f) {
+                    float xa = 0.f;
 #pragma unroll
-                    for (int r = 0; r < kRT; ++r) s[r] = cap2 * tanh_fast(s[r] * to_cap);
+                    for (int r = 0; r < kRT; ++r) xa = fmaxf(xa, fabsf(s[r]));
+                    if (__all_sync(0xffffffffu, xa * to_cap < kTanhSmall)) {
+#pragma unroll
+                        for (int r = 0; r < kRT; ++r) s[r] = cap2 * tanh_series(s[r] * to_cap);
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < kRT; ++r) s[r] = cap2 * tanh_near(s[r] * to_cap);
+                    }
                 }
                 if (masked) {
 #pragma unroll

@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int m = warp - kLoadWarp;
             const void *tm = m ? &tm_v : &tm_k;
             const uint8_t *exps = m ? p.c.v_exp : p.c.k_exp;
-            const int box = min(p.c.page, kPart), per = kPart / box;
+            const int box = min(p.c.page, kPart);
             uint32_t g = 0;
             bool ok = true;
             for (;;) {
@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) v[j] = cap2 * tanh_fast(v[j] * a1);
+                            for (int j = 0; j < 16; ++j) v[j] = cap2 * tanh_near(v[j] * a1);
                         }
                     }
                     if (decltype(masked_tag)::value) {

@@ -47,6 +47,19 @@ __device__ __forceinline__ float exp_byte_scale(uint32_t b)
     return __uint_as_float(b == 255u ? 0x7fc00000u : b == 0u ? 0x00400000u : b << 23);
 }
 
+// tanh by its series, for |x| < kTanhSmall.
+__device__ __forceinline__ float tanh_series(float x)
+{
+    const float z = x * x;
+    return x * fmaf(z, fmaf(z, fmaf(z, kTanhC7, kTanhC5), kTanhC3), 1.f);
+}
+// For any x.  1 - 2 / (1 + e^2x) is off by some 2^-23 whatever x is: times a
+// soft cap of 50 that is 10^-5 of a logit near 1, so small x take the series.
+__device__ __forceinline__ float tanh_near(float x)
+{
+    return fabsf(x) < kTanhSmall ? tanh_series(x) : tanh_fast(x);
+}
+
 // Two e4m3 codes (low and high byte of a 16-bit word) as two halves.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w)
 {

@@ -86,11 +86,10 @@ constexpr int kPagedF32Rows = 8, kPagedF32Tile = 32;
 cudaError_t launch_paged_f32(const PagedProblem &p, const PagedPart &part, int cache_dtype,
                              cudaStream_t s);
 
-// bf16 queries, row_block 8 or 16: tensor cores fed from registers.  Keys of a
-// tile, and token rows of one TMA box, by head size, cache type and page size;
-// tm_k, tm_v: maps of encode_paged over the cache with that box.
-int paged_few_tile(int D, int cache_dtype);
-int paged_few_box(int D, int cache_dtype, int page);
+// bf16 queries, D = 64, row_block 8 or 16: tensor cores fed from registers;
+// tm_k, tm_v: maps of encode_paged over the cache (boxes of min(page, 32)
+// tokens)
+constexpr int kPagedFewTile = 128;
 cudaError_t launch_paged_few(const PagedProblem &p, const PagedPart &part, int cache_dtype,
                              const void *tm_k, const void *tm_v, cudaStream_t s);
 

@@ -163,7 +163,7 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
             kernel = kFew;
             a.seg_cost = 2;
             a.row_block = a.rows <= 8 ? 8 : 16;
-            a.tile = paged_few_tile(c->D, c->dtype);
+            a.tile = kPagedFewTile;
             a.ctas = 2 * kSms;
         }
         a.n_rb = (a.rows + a.row_block - 1) / a.row_block;
@@ -287,9 +287,9 @@ RA_API int ra_attn_paged(const ra_kv_cache *cache, const ra_paged_params *p, con
             e = launch_paged_f32(x, part, cache->dtype, s);
             continue;
         }
-        const int most = pl.kernel[k] == kFew ? paged_few_box(cache->D, cache->dtype, cache->page_size)
+        const int most = pl.kernel[k] == kFew                                ? 32
                          : pl.kernel[k] == kRowsM && cache->dtype == RA_E4M3 ? 64
-                                                                           : 128;
+                                                                             : 128; // of a box
         const int rows = cache->page_size < most ? cache->page_size : most;
         CUtensorMap tk, tv;
         if ((rc = encode_paged(&tk, cache, cache->k, rows)) || (rc = encode_paged(&tv, cache, cache->v, rows))) return rc;

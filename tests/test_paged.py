@@ -77,6 +77,7 @@ class Pool:
             at += m
         self.prefix = order[at:at + n_prefix].to(torch.int32)
         self.page, self.lens, self.prefix_len = page, list(lens), prefix
+        self.given = None  # the tables that a call gets, where they differ
         x = [torch.randn((self.n, Hkv, page, D), generator=g) * torch.exp(torch.randn((self.n, Hkv, page, 1), generator=g) * 0.3)
              for _ in range(2)]
         if dtype == F8:
@@ -87,6 +88,20 @@ class Pool:
             x = [t.to(torch.bfloat16) for t in x]
             self.val = [t.double() for t in x]
             self.cache = ra.make_kv_cache(*(t.cuda() for t in x))
+
+    def places(self, b):
+        """(page, offset) of sequence b's tokens, or of the prefix's for b = None."""
+        pages, n = (self.prefix, self.prefix_len) if b is None else (self.table[b], self.lens[b])
+        return [(int(pages[t // self.page]), slice(None), t % self.page) for t in range(n)]
+
+    def scale(self, which, at, e):
+        """Multiplies a token's row by 2^e."""
+        self.val[which][at] *= 2.0 ** e
+        pages, exps = ((self.cache.k_pages, self.cache.k_exps), (self.cache.v_pages, self.cache.v_exps))[which]
+        if exps is None:
+            pages[at] = self.val[which][at].to(torch.bfloat16).cuda()
+        else:
+            exps[at] += e
 
     def rows(self, which, pages, n):
         t = self.val[which][pages.long()]  # pages, Hkv, page, D
@@ -102,9 +117,9 @@ def check_attention(pool, q, *, causal=True, cap=0.0, q_len=None, sinks=None, se
     dev = lambda t: None if t is None else t.cuda()  # noqa: E731
     lens = torch.tensor(pool.lens, dtype=torch.int32)
     p = ra.make_paged_params(
-        pool.cache, q.cuda(), pool.table.cuda(), lens.cuda(), scale=D ** -0.5, causal=causal, soft_cap=cap,
-        q_len=dev(None if q_len is None else torch.tensor(q_len, dtype=torch.int32)), sinks=dev(sinks),
-        prefix_table=dev(pool.prefix) if pool.prefix_len else None,
+        pool.cache, q.cuda(), (pool.given or (pool.table, pool.prefix))[0].cuda(), lens.cuda(), scale=D ** -0.5, causal=causal,
+        soft_cap=cap, q_len=dev(None if q_len is None else torch.tensor(q_len, dtype=torch.int32)), sinks=dev(sinks),
+        prefix_table=dev((pool.given or (pool.table, pool.prefix))[1]) if pool.prefix_len else None,
         prefix_len=torch.tensor([pool.prefix_len], dtype=torch.int32).cuda() if pool.prefix_len else None)
     ws = torch.full((ra.ra_attn_paged_workspace_size(pool.cache, p),), 255, dtype=torch.uint8, device="cuda")
     out = torch.full_like(q, 7.0).cuda()
@@ -276,6 +291,10 @@ CASES = {
     "prefix_rows": dict(lens=[(13 * b) % 50 for b in range(40)], Hq=8, prefix=300, page=64),
     "prefix_many_rows": dict(lens=[b % 7 for b in range(70)], Hq=16, Lq=2, prefix=1000, page=128, q_len=[b % 3 for b in range(70)]),
     "prefix_long": dict(lens=[9, 2], Hq=16, prefix=4097, page=128),
+    "no_queries": dict(lens=[30, 2], Hq=4, Lq=2, prefix=20, q_len=[0, 0]),
+    "rows_cap": dict(lens=[300, 140], Hq=8, Lq=40, cap=3.0, sinks=True),
+    "rows_large_cap": dict(lens=[300, 140], Hq=8, Lq=70, Hkv=1, cap=50.0),
+    "prefix_rows_cap": dict(lens=[(13 * b) % 50 for b in range(70)], Hq=16, prefix=300, page=64, cap=20.0, Hkv=4),
 }
 
 
@@ -340,6 +359,195 @@ def test_large_logits_keep_their_weights():
         # |s| is up to a few thousand: 2^-24 * 128 terms * sum |q k| ~ 8000 / 11 -> 1e-2 of a nat at worst
         assert (lse[0].cpu().double() - e).abs().max() <= 1e-2
         assert (out[0].cpu().double() - o).abs().max() <= 2e-2 * float(v.abs().max())
+
+
+# heads, kv heads, query tokens and head size of a call that each kernel takes: rows per kv head decide
+KERNELS = {"d64": (4, 1, 1, 64), "rows8": (2, 1, 1, 128), "rows16": (16, 1, 1, 128), "rows32": (32, 1, 1, 128),
+           "rows80": (8, 1, 10, 128), "rows320": (8, 1, 40, 128)}
+each_kernel = pytest.mark.parametrize("name", KERNELS)
+each_cache = pytest.mark.parametrize("cache", [F8, torch.bfloat16], ids=["e4m3", "c16"])
+each_type = pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+
+
+def queries(name, B, dtype, seed):
+    Hq, _, Lq, D = KERNELS[name]
+    return torch.randn((B, Lq, Hq, D), generator=torch.Generator().manual_seed(seed)).to(dtype)
+
+
+@gpu
+@each_type
+@each_cache
+@each_kernel
+@pytest.mark.parametrize("way", ["up", "down"])
+def test_scales_that_change_along_a_sequence(way, name, cache, dtype):
+    """Values whose size runs over 2^18 within a sequence, keys over 2^3: references and common exponents move inside a
+    tile and between tiles."""
+    _, Hkv, _, D = KERNELS[name]
+    pool = Pool([700, 90, 0], Hkv=Hkv, D=D, page=32, dtype=cache, seed=31, prefix=333)
+    for b in (None, 0, 1):
+        at = pool.places(b)
+        for t in range(len(at)):
+            x = t if way == "up" else len(at) - 1 - t
+            pool.scale(1, at[t], 18 * x // len(at))
+            pool.scale(0, at[t], 3 * x // len(at))
+    check_attention(pool, queries(name, 3, dtype, 32))
+
+
+@gpu
+@each_type
+@each_cache
+@each_kernel
+def test_pages_out_of_range(name, cache, dtype):
+    """Their keys and values read as zeros, whatever the number, and the call reports them."""
+    _, Hkv, _, D = KERNELS[name]
+    pool = Pool([300, 130, 64], Hkv=Hkv, D=D, page=32, dtype=cache, seed=33, prefix=200)
+    table, prefix = pool.table.clone(), pool.prefix.clone()
+    for b, i, number in ((0, 0, -1), (0, 5, pool.n), (1, 4, 2 ** 31 - 1), (2, 1, -2 ** 31), (None, 2, 1 << 20), (None, 6, -5)):
+        pages, given = (pool.prefix, prefix) if b is None else (pool.table[b], table[b])
+        for w in (0, 1):
+            pool.val[w][int(pages[i])] = 0
+        given[i] = number
+    pool.given = table, prefix
+    check_attention(pool, queries(name, 3, dtype, 34))
+    assert ra.ra_get_device_status() == ra.RA_ERR_INVALID_ARG
+    assert ra.ra_get_device_status() == ra.RA_OK
+
+
+@gpu
+@each_type
+@each_cache
+@each_kernel
+def test_queries_that_are_not_finite(name, cache, dtype):
+    """A row with a NaN or an infinity is NaN; a row of zeros is a mean; the other rows are what they should be (to the
+    bounds above: rows of a block may move their references together, so not bit by bit)."""
+    _, Hkv, _, D = KERNELS[name]
+    pool = Pool([200, 75], Hkv=Hkv, D=D, page=16, dtype=cache, seed=35, prefix=60)
+    q = queries(name, 2, dtype, 36)
+    q[0, -1, 1] = 0
+    check_attention(pool, q)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    p = ra.make_paged_params(pool.cache, q.cuda(), pool.table.cuda(), i32(pool.lens), scale=D ** -0.5,
+                             prefix_table=pool.prefix.cuda(), prefix_len=i32([60]))
+    want, want_lse = ra.paged_forward(p, q.cuda(), pool.cache)
+    q[0, 0, 0, 5] = float("nan")
+    q[1, -1, 1, 7] = float("inf")
+    q[1, -1, 1, 8] = float("-inf")
+    got, lse = ra.paged_forward(p, q.cuda(), pool.cache)
+    bad = torch.zeros(q.shape[:3], dtype=torch.bool)
+    bad[0, 0, 0] = bad[1, -1, 1] = True
+    assert torch.isnan(got.cpu()[bad]).all() and torch.isnan(lse.cpu().transpose(1, 2)[bad]).all()
+    most = max(float(v.abs().max()) for v in (pool.dense(0)[1], pool.dense(1)[1]))
+    assert (got - want).cpu().float()[~bad].abs().max() <= 2 * (1e-4 if dtype == torch.float32 else 2 ** -7) * most
+    assert (lse - want_lse).cpu().transpose(1, 2)[~bad].abs().max() <= 2e-4
+
+
+@gpu
+@each_type
+@each_cache
+@each_kernel
+def test_lse_of_small_capped_logits(name, cache, dtype):
+    """One key: lse is the capped logit itself.  Without cancellation (q, k > 0) its relative error is at most
+    D * 2^-23 (products accumulated with truncation), 3.4e-7 for the series of tanh, a few 2^-24, and 2^-23 absolute where
+    the logit meets its reference: 2e-5 relative at logits of 0.05 and above."""
+    _, Hkv, _, D = KERNELS[name]
+    pool = Pool([1, 1], Hkv=Hkv, D=D, dtype=cache, seed=37)
+    at = [pool.places(b)[0] for b in (0, 1)]
+    for a in at:
+        x = pool.val[0][a].abs()
+        pool.val[0][a] = x
+        if cache == F8:
+            pool.cache.k_pages.view(torch.uint8)[a] &= 0x7f
+        else:
+            pool.cache.k_pages[a] = x.to(torch.bfloat16).cuda()
+    q = (queries(name, 2, torch.float32, 38).abs() * 0.05).to(dtype)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    p = ra.make_paged_params(pool.cache, q.cuda(), pool.table.cuda(), i32([1, 1]), scale=D ** -0.5, soft_cap=50.0, causal=False)
+    _, lse = ra.paged_forward(p, q.cuda(), pool.cache)
+    for b in (0, 1):
+        s = torch.einsum("ihd,hd->hi", q[b].double(), pool.val[0][at[b]].repeat_interleave(q.shape[2] // Hkv, 0)) * D ** -0.5
+        assert s.min() > 0.05
+        want = 50 * torch.tanh(s / 50)
+        assert ((lse[b].cpu().double() - want) / want).abs().max() <= 2e-5
+
+
+@gpu
+@each_type
+@pytest.mark.parametrize("cache,page,n", [(F8, 128, 34000), (torch.bfloat16, 64, 34000)], ids=["e4m3", "c16"])
+@pytest.mark.parametrize("Hq,Lq", [(8, 1), (80, 8)])
+def test_offsets_beyond_32_bits(Hq, Lq, cache, page, n, dtype):
+    """A cache of 4.4 GB per tensor: the same tokens in its first and in its last pages."""
+    c = ra.new_kv_cache(n, page, 8, 128, cache)
+    g = torch.Generator().manual_seed(41)
+    low = torch.arange(6, dtype=torch.int32).view(2, 3)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    lens = [3 * page - 5, page + 1]
+    k, v = (torch.randn((2, 3 * page, 8, 128), generator=g).to(dtype).cuda() for _ in range(2))
+    q = torch.randn((2, Lq, Hq, 128), generator=g).to(dtype).cuda()
+    got = []
+    for table in (low.cuda(), (n - 1 - low).cuda()):
+        ra.kv_write(c, k, v, table, i32([0, 0]), i32(lens))
+        p = ra.make_paged_params(c, q, table, i32(lens), scale=0.1, prefix_table=table[0, :2].contiguous(), prefix_len=i32([page + 3]))
+        got.append(ra.kv_read(c, table, i32(lens), 3 * page) + ra.paged_forward(p, q, c))
+    assert c.k_pages[n - 1].float().abs().sum() > 0
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+@gpu
+@each_cache
+@each_kernel
+def test_a_graph_serves_lengths_that_change(name, cache):
+    Hq, Hkv, Lq, D = KERNELS[name]
+    pool = Pool([400, 90, 64], Hkv=Hkv, D=D, page=32, dtype=cache, seed=43, prefix=333)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    kv, q_len, plen = i32([1, 90, 0]), i32([Lq, Lq, Lq]), i32([0])
+    q = queries(name, 3, torch.bfloat16, 44).cuda()
+    p = ra.make_paged_params(pool.cache, q, pool.table.cuda(), kv, scale=D ** -0.5, q_len=q_len, prefix_table=pool.prefix.cuda(),
+                             prefix_len=plen)
+    ws = torch.empty(ra.ra_attn_paged_workspace_size(pool.cache, p), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty((3, Hq, Lq), device="cuda")
+    ra.paged_forward(p, q, pool.cache, out=out, lse=lse, ws=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ra.paged_forward(p, q, pool.cache, out=out, lse=lse, ws=ws)
+    for lens, n_q, prefix in (([1, 90, 0], Lq, 0), ([400, 3, 64], Lq, 333), ([0, 0, 0], Lq, 0), ([0, 0, 0], Lq, 16), ([129, 90, 1], 0, 200),
+                              ([257, 1, 64], 1, 128)):
+        kv.copy_(i32(lens))
+        q_len.fill_(n_q)
+        plen.fill_(prefix)
+        out.fill_(7)
+        lse.fill_(9)
+        graph.replay()
+        want = ra.paged_forward(p, q, pool.cache, out=torch.full_like(out, 7), lse=torch.full_like(lse, 9))
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        pool.lens, pool.prefix_len = lens, prefix
+        if prefix == 0:
+            check_attention(pool, q.cpu(), q_len=[n_q] * 3)
+
+
+@gpu
+@each_cache
+def test_calls_on_several_streams(cache):
+    """Calls of all kernels at once, each with its own workspace, give what they give alone."""
+    jobs = []
+    for i, name in enumerate(KERNELS):
+        _, Hkv, _, D = KERNELS[name]
+        pool = Pool([(97 * b + 11 * i) % 600 for b in range(24)], Hkv=Hkv, D=D, page=32, dtype=cache, seed=50 + i, prefix=300)
+        q = queries(name, 24, torch.bfloat16, 60 + i).cuda()
+        p = ra.make_paged_params(pool.cache, q, pool.table.cuda(), torch.tensor(pool.lens, dtype=torch.int32).cuda(), scale=D ** -0.5,
+                                 prefix_table=pool.prefix.cuda(), prefix_len=torch.tensor([300], dtype=torch.int32).cuda())
+        jobs.append((torch.cuda.Stream(), p, q, pool.cache, ra.paged_forward(p, q, pool.cache)))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        for s, p, q, c, _ in jobs:
+            with torch.cuda.stream(s):
+                got.append(ra.paged_forward(p, q, c))
+    torch.cuda.synchronize()
+    for i, (out, lse) in enumerate(got):
+        want = jobs[i % len(jobs)][4]
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
 # ------------------------------------------------------------- together, as a server uses them
@@ -463,6 +671,13 @@ def test_bad_params_are_refused(bad, code):
     assert L.ra_attn_paged(ctypes.byref(c), ctypes.byref(p), 256, 4096, 8192, 256, 1 << 30, None) == code
 
 
+def test_a_call_with_too_much_work_is_refused():
+    import ctypes
+    L, c, p = ra.lib(), _c_cache(), _c_params(B=1 << 20, max_pages=1 << 14)
+    assert L.ra_attn_paged_workspace_size(ctypes.byref(c), ctypes.byref(p)) == 0 and "split the batch" in ra.ra_last_error()
+    assert L.ra_attn_paged(ctypes.byref(c), ctypes.byref(p), 256, 1 << 40, 8192, 256, 1 << 30, None) == -2
+
+
 def test_bad_calls_are_refused():
     import ctypes
     L, c, p = ra.lib(), _c_cache(), _c_params()
@@ -478,6 +693,8 @@ def test_bad_calls_are_refused():
                                   k.get("ks", 256), k.get("vs", 256), k.get("t", 256), 1, k.get("s", 256), None, None)
     assert w(k=None) == w(s=None) == w(t=None) == w(B=0) == w(dt=ra.RA_E4M3) == w(ks=255) == w(vs=260) == w(k=264) == -1
     assert L.ra_kv_read(by(c), 256, 1, 256, 1, 1, 4096, 4096, ra.RA_BF16, None) == -1  # k and v overlap
+    assert L.ra_kv_read(by(c), 256, 1, 256, 1, 1 << 30, 4096, 1 << 50, ra.RA_BF16, None) == -2  # more rows than 2^31
+    assert L.ra_kv_write(by(c), 256, 256, ra.RA_BF16, 1, 1 << 30, 256, 256, 256, 1, 256, None, None) == -2
 
 
 def test_helpers_refuse_what_they_cannot_pass_on():
