@@ -435,17 +435,17 @@ def _ints(x, shape, name, device):
     raise ValueError(f"{name} must be contiguous and on the cache's device")
 
 
-def _on(device, stream, run):
-    """run(handle of the stream) on the tensors' device and on the caller's stream, allocations
-    included, so that what is allocated is reused in that stream's order."""
-    if stream is None and device.index == torch.cuda.current_device():
+def _on(device, stream, run, *args):
+    """run(*args, handle of the stream) on the tensors' device and on the caller's stream,
+    allocations included, so that what is allocated is reused in that stream's order."""
+    if stream is None and device.index == torch._C._cuda_getDevice():
         # the handle without a Stream object around it: a small call's time is mostly Python's
-        return run(torch._C._cuda_getCurrentRawStream(device.index))
+        return run(*args, torch._C._cuda_getCurrentRawStream(device.index))
     with torch.cuda.device(device):
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
         with torch.cuda.stream(stream):
-            return run(torch.cuda.current_stream().cuda_stream)
+            return run(*args, torch.cuda.current_stream().cuda_stream)
 
 
 def make_kv_cache(k, v, k_exp=None, v_exp=None) -> RaKvCache:
@@ -488,15 +488,12 @@ def new_kv_cache(n_pages, page_size, n_kv_heads, head_dim, dtype=torch.float8_e4
     return make_kv_cache(k, v, *exps)
 
 
-def _token_stride(x, cache, name):
-    B, L, H, D = x.shape
-    sb, step, sh, sd = x.stride()
+def _token_stride(shape, strides, name):
+    B, L, H, D = shape
+    sb, step, sh, sd = strides
     if L == 1:
         step = sb if B > 1 else H * D
-    if not (sd == 1 and (sh == D or H == 1) and (B == 1 or sb == L * step) and step >= H * D
-            and (H, D) == cache._row and x.device == cache.device):
-        _need((H, D) == cache._row, f"{name} must be (B, L, {cache.Hkv}, {cache.D})")
-        _need(x.device == cache.device, f"{name} must be on the cache's device")
+    if not (sd == 1 and (sh == D or H == 1) and (B == 1 or sb == L * step) and step >= H * D):
         raise ValueError(
             f"{name}: a token's heads must be contiguous, and tokens and batches evenly spaced")
     return step
@@ -509,19 +506,34 @@ def kv_write(cache, k, v, page_table, start, count=None, stream=None) -> None:
     dt = _DT.get(k.dtype)
     if dt is None or v.dtype != k.dtype:
         raise TypeError(f"k and v must both be bfloat16 or float32, not {k.dtype} and {v.dtype}")
-    _need(k.dim() == 4 and k.shape == v.shape, "k and v must be (B, L, Hkv, D), of the same shape")
-    ks, vs = _token_stride(k, cache, "k"), _token_stride(v, cache, "v")
-    B, L = k.shape[:2]
+    shape, dev = k.shape, cache.device
+    if not (len(shape) == 4 and v.shape == shape and shape[2:] == cache._row):
+        raise ValueError(f"k and v must be (B, L, {cache.Hkv}, {cache.D}), of the same shape")
+    _need(k.device == dev and v.device == dev, "k and v must be on the cache's device")
+    strides = k.stride()
+    ks = vs = _token_stride(shape, strides, "k")
+    if v.stride() != strides:
+        vs = _token_stride(shape, v.stride(), "v")
+    B, L = shape[:2]
     if B == 0 or L == 0:
         return
-    dev, pages = cache.device, page_table.shape[-1]
+    pages = page_table.shape[-1]
     _ints(page_table, (B, pages), "page_table", dev)
     _ints(start, (B,), "start", dev)
     if count is not None:
         _ints(count, (B,), "count", dev)
-    _check(_on(dev, stream, lambda s: lib().ra_kv_write(
-        cache._ref, k.data_ptr(), v.data_ptr(), dt, B, L, ks, vs, page_table.data_ptr(), pages,
-        start.data_ptr(), None if count is None else count.data_ptr(), s)))
+    _check(_on(dev, stream, lib().ra_kv_write, cache._ref, k.data_ptr(), v.data_ptr(), dt, B, L, ks,
+               vs, page_table.data_ptr(), pages, start.data_ptr(),
+               None if count is None else count.data_ptr()))
+
+
+def _kv_read(cache, page_table, pages, kv_len, B, L, dtype, dt, s):
+    k = torch.empty((B, L) + cache._row, dtype=dtype, device=cache.device)
+    v = torch.empty_like(k)
+    if B and L:
+        _check(lib().ra_kv_read(cache._ref, page_table.data_ptr(), pages, kv_len.data_ptr(), B, L,
+                                k.data_ptr(), v.data_ptr(), dt, s))
+    return k, v
 
 
 def kv_read(cache, page_table, kv_len, L, dtype=torch.bfloat16, stream=None):
@@ -533,14 +545,7 @@ def kv_read(cache, page_table, kv_len, L, dtype=torch.bfloat16, stream=None):
     _ints(page_table, (B, pages), "page_table", dev)
     _ints(kv_len, (B,), "kv_len", dev)
 
-    def run(s):
-        k = torch.empty((B, L) + cache._row, dtype=dtype, device=dev)
-        v = torch.empty_like(k)
-        if B and L:
-            _check(lib().ra_kv_read(cache._ref, page_table.data_ptr(), pages, kv_len.data_ptr(), B,
-                                    L, k.data_ptr(), v.data_ptr(), dt, s))
-        return k, v
-    return _on(dev, stream, run)
+    return _on(dev, stream, _kv_read, cache, page_table, pages, kv_len, B, L, dtype, dt)
 
 
 def make_paged_params(cache, q, page_table, kv_len, *, scale, causal=True, soft_cap=0.0, q_len=None,
@@ -579,6 +584,24 @@ def make_paged_params(cache, q, page_table, kv_len, *, scale, causal=True, soft_
     return p
 
 
+def _paged_forward(params, q, cache, out, lse, ws, s):
+    dev = cache.device
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty(params._lse, dtype=torch.float32, device=dev)
+    n = params._ws
+    if n:
+        if ws is None:
+            # bare storage: a tensor around it would double the time of getting it
+            w = torch.UntypedStorage(n, device=dev)
+        else:
+            w, n = ws, _wsb(ws)
+        _check(lib().ra_attn_paged(cache._ref, params._ref, q.data_ptr(), out.data_ptr(),
+                                   lse.data_ptr(), w.data_ptr(), n, s))
+    return out, lse
+
+
 def paged_forward(params, q, cache, out=None, lse=None, ws=None, stream=None):
     """Attention of q (B, Lq, Hq, D) over the cached tokens -> (out like q, lse (B, Hq, Lq) fp32).
     Given ``out`` / ``lse`` are written in place (rows behind q_len stay as they are); ``ws``: a
@@ -596,13 +619,4 @@ def paged_forward(params, q, cache, out=None, lse=None, ws=None, stream=None):
               and lse.is_contiguous(), "lse must be (B, Hq, Lq) fp32")
     if ws is not None:
         _need(ws.device == dev and ws.is_contiguous(), "ws must be contiguous and on the cache's device")
-
-    def run(s):
-        o = torch.empty_like(q) if out is None else out
-        e = torch.empty(params._lse, dtype=torch.float32, device=dev) if lse is None else lse
-        if params._ws:
-            w = torch.empty(params._ws, dtype=torch.uint8, device=dev) if ws is None else ws
-            _check(lib().ra_attn_paged(cache._ref, params._ref, q.data_ptr(), o.data_ptr(),
-                                       e.data_ptr(), w.data_ptr(), _wsb(w), s))
-        return o, e
-    return _on(dev, stream, run)
+    return _on(dev, stream, _paged_forward, params, q, cache, out, lse, ws)
