@@ -574,6 +574,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool masked = all < (t + 1) * kKeys;
                 float a = a_row, fv = 1.f; // the tile's logit scale; the change of EV
                 if (FP8) {
+                    // tile B's threads come here from segments that have none without
+                    // having waited in them: ev_full could be several phases behind,
+                    // and its parity say nothing, before S is there
+                    if (t == c.t0) wait(bars.s_full + x, gx & 1);
                     wait(bars.ev_full + (gt & 3), (gt >> 2) & 1);
                     const int e = v_scale[gt & 3];
                     if (t > c.t0 && e != ev) fv = ex2_approx((float)(ev - e));

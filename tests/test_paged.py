@@ -394,6 +394,18 @@ def test_scales_that_change_along_a_sequence(way, name, cache, dtype):
 
 
 @gpu
+@each_cache
+def test_row_blocks_of_one_and_of_two_tiles_in_turn(cache):
+    """320 rows per kv head are a block of 256 and one of 64: a CTA with many segments has runs of either, and values
+    whose size differs between sequences."""
+    pool = Pool([250 + (37 * b) % 300 for b in range(80)], Hkv=4, page=64, dtype=cache, seed=39)
+    for b in range(80):
+        for at in pool.places(b):
+            pool.scale(1, at, (5 * b) % 12)
+    check_attention(pool, torch.randn((80, 40, 32, 128), generator=torch.Generator().manual_seed(40)).to(torch.bfloat16))
+
+
+@gpu
 @each_type
 @each_cache
 @each_kernel
