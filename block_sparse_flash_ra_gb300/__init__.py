@@ -502,7 +502,8 @@ def _token_stride(shape, strides, name):
 def kv_write(cache, k, v, page_table, start, count=None, stream=None) -> None:
     """Appends k, v (B, L, Hkv, D), bf16 or fp32, at positions start[b] + i of the sequences whose
     pages are in page_table (B, max_pages); of sequence b the first count[b] tokens (None: all).
-    k and v may be slices along the head axis of a wider tensor."""
+    k and v may be slices along the head axis of a wider tensor.  No two tokens of a call may have
+    the same place."""
     dt = _DT.get(k.dtype)
     if dt is None or v.dtype != k.dtype:
         raise TypeError(f"k and v must both be bfloat16 or float32, not {k.dtype} and {v.dtype}")
@@ -605,7 +606,8 @@ def _paged_forward(params, q, cache, out, lse, ws, s):
 def paged_forward(params, q, cache, out=None, lse=None, ws=None, stream=None):
     """Attention of q (B, Lq, Hq, D) over the cached tokens -> (out like q, lse (B, Hq, Lq) fp32).
     Given ``out`` / ``lse`` are written in place (rows behind q_len stay as they are); ``ws``: a
-    workspace to use instead of a new one, uint8, of ra_attn_paged_workspace_size elements."""
+    workspace to use instead of a new one, uint8, of ra_attn_paged_workspace_size elements.
+    For serving: no gradient is recorded."""
     dev = cache.device
     _need((q.shape, q.dtype) == params._like and q.is_contiguous(),
           "q must be contiguous, of the shape and dtype the params were made for")

@@ -94,14 +94,15 @@ int check_paged(const ra_kv_cache *c, const ra_paged_params *p)
         return refuse(RA_ERR_INVALID_ARG, "dtype must be RA_BF16 or RA_FP32");
     if (!(p->scale > 0.f) || !(p->scale < 1e30f))
         return refuse(RA_ERR_INVALID_ARG, "scale must be positive and finite");
-    if (!(p->soft_cap < 1e30f)) return refuse(RA_ERR_INVALID_ARG, "soft_cap must be finite");
+    if (!(p->soft_cap < 1e30f) || (p->soft_cap > 0.f && p->soft_cap < 1e-20f))
+        return refuse(RA_ERR_INVALID_ARG, "soft_cap must be finite, and 0 or at least 1e-20");
     if (!p->page_table || !p->kv_len || p->max_pages <= 0)
         return refuse(RA_ERR_INVALID_ARG, "page_table and kv_len are needed, with max_pages > 0");
     if (p->prefix_pages < 0 || (p->prefix_pages > 0) != (p->prefix_table != nullptr) ||
         (p->prefix_pages > 0) != (p->prefix_len != nullptr))
         return refuse(RA_ERR_INVALID_ARG, "prefix_pages, prefix_table and prefix_len must come together");
-    if (((long long)p->max_pages + p->prefix_pages) * c->page_size > 0x7fffffffll)
-        return refuse(RA_ERR_UNSUPPORTED, "sequences must be shorter than 2^31 tokens");
+    if (((long long)p->max_pages + p->prefix_pages) * c->page_size > 0x7fffff00ll) // a tile's end fits too
+        return refuse(RA_ERR_UNSUPPORTED, "sequences must be shorter than 2^31 - 256 tokens");
     return RA_OK;
 }
 

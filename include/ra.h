@@ -489,7 +489,8 @@ typedef struct {
  * A token whose position lies outside [0, max_pages * page_size), or whose
  * page is outside [0, n_pages), is skipped and reported by
  * ra_get_device_status (RA_ERR_INVALID_ARG).  Nothing else of the cache is
- * touched.  If two tokens name the same place, either may stay.
+ * touched.  No two tokens of a call may name the same place (a mixture of
+ * the two would be left there).
  * Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED, RA_ERR_CUDA.
  */
 RA_API int ra_kv_write(const ra_kv_cache *cache, const void *k, const void *v, int dtype, int B,
@@ -519,7 +520,8 @@ RA_API int ra_kv_read(const ra_kv_cache *cache, const int32_t *page_table, int m
  *   B, Lq, Hq     sequences, query tokens per sequence (1 for a decoding
  *                 step), query heads (a multiple of the cache's Hkv)
  *   dtype         RA_BF16 or RA_FP32: element type of q and out
- *   scale, soft_cap, sinks   as in ra_attn_params
+ *   scale, soft_cap, sinks   as in ra_attn_params; a soft_cap above 0 is at
+ *                 least 1e-20
  *   causal        1: the queries are the sequence's last tokens, and query i
  *                 sees own positions up to kv_len - q_len + i; 0: all of them
  *   page_table    (B, max_pages) int32: the sequences' own pages
@@ -568,6 +570,7 @@ RA_API size_t ra_attn_paged_workspace_size(const ra_kv_cache *cache, const ra_pa
  * Keys and values behind a sequence's length are never used, whatever the
  * memory holds; inside it, a value row that only some of a sequence's
  * queries see has to be finite.
+ * Serving only: there is no backward pass.
  * The prefix is read once for the whole batch.  Results do not depend on how
  * the work was timed: partial results are joined in a fixed order.
  * Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED, RA_ERR_WORKSPACE, RA_ERR_CUDA.

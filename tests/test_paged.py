@@ -672,7 +672,7 @@ def test_bad_caches_are_refused(bad, code):
 
 @pytest.mark.parametrize("bad,code", [
     (dict(B=0), -1), (dict(Lq=0), -1), (dict(Hq=3), -1), (dict(dtype=ra.RA_E4M3), -1), (dict(scale=0.0), -1),
-    (dict(scale=math.nan), -1), (dict(soft_cap=math.nan), -1), (dict(max_pages=0), -1), (dict(page_table=None), -1),
+    (dict(scale=math.nan), -1), (dict(soft_cap=math.nan), -1), (dict(soft_cap=1e-30), -1), (dict(max_pages=0), -1), (dict(page_table=None), -1),
     (dict(kv_len=None), -1), (dict(prefix_pages=1), -1), (dict(prefix_table=256, prefix_len=256), -1),
     (dict(max_pages=1 << 28), -2), (dict(B=1 << 20, Lq=1 << 12), -2),
 ])
