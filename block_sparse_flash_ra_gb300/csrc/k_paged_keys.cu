@@ -1,6 +1,6 @@
-// k_paged_keys.cu -- attention over a paged cache for up to 32 query rows per
-// kv head and item at D = 128: decoding steps, drafts, multi-query heads; bf16
-// queries.  The keys are the M side of the tensor-core products.
+// k_paged_keys.cu -- attention over a paged cache for up to 32 (D = 64: 16)
+// query rows per kv head and item: decoding steps, drafts, multi-query heads;
+// bf16 queries.  The keys are the M side of the tensor-core products.
 //
 // With few rows a cached byte is used a few times, so the bound is memory:
 // 128 keys of 8 bit are 32 KB, 0.74 us of one SM's share of 6.77 TB/s.  What
@@ -23,6 +23,15 @@
 // 16-bit caches run kind::f16 in bf16, q as it is, p = x1 + x2 (2^-16).
 // Logits, maxima, sums and O are fp32.
 //
+// D = 64: two tokens of a page lie in one row of 128 values, so a tile is the
+// same bytes with 256 tokens.  A query row takes two columns, q in one half of
+// the 128 and zeros in the other: S of the even tokens and S of the odd ones.
+// P^T has the two columns likewise, and O's lanes d < 64 of the even column and
+// d >= 64 of the odd one are the two halves of the result; the rest of the
+// product is of no use, and free.  (Products of the register-fed kind,
+// mma.sync on widened codes, took 126 us where this takes 54: 64 sequences of
+// 8192 e4m3 tokens, 4 kv heads, 16 query heads, 75% of memory speed.)
+//
 //   warps 0-3 of each warpgroup
 //              softmax of 8 rows: thread = key = TMEM lane of S^T.  A row's
 //              maximum is over all threads, so it is only looked for when some
@@ -37,6 +46,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "ra_paged.cuh"
 #include "ra_sched.cuh"
@@ -44,14 +54,15 @@
 namespace ra {
 namespace {
 
-constexpr int kKeys = 128, kD = 128;
+constexpr int kKeys = 128, kD = 128; // rows of a cached tile, values of a row
 constexpr int kRT = 8;         // rows of a softmax warpgroup
 constexpr float kNone = -3e38f; // the maximum of no logits: finite, so that no difference is a NaN
 constexpr float kPBias = 4.f;  // 8-bit caches: weights times 2^4 are at most 2^8 < 448
 constexpr float kMinExp = 12.f; // least E: 2^(127 + kPBias - E) stays finite
 
-template <bool FP8, int RP>
+template <bool FP8, int RP, int D>
 struct Cfg {
+    static constexpr int kPar = kD / D, kTokens = kKeys * kPar; // tokens of a row, of a tile
     static constexpr int kMat = kKeys * kD * (FP8 ? 1 : 2); // bytes of a K or V tile
     static constexpr int kHalves = FP8 ? 1 : 2;             // 128-byte wide blocks of a tile
     static constexpr int kGroups = RP / kRT, kSoftThreads = 128 * kGroups, kThreads = kSoftThreads + 64;
@@ -70,12 +81,13 @@ struct Cfg {
     static constexpr int kQOff = kVOff + kVStages * kMat;
     static constexpr int kPOff = kQOff + 2 * kQBytes; // Q of the present and of the next segment
     static constexpr int kExpOff = kPOff + 2 * kPBytes; // per V stage: scale bytes of K, of V
-    static constexpr int kRowOff = kExpOff + (FP8 ? kVStages * 2 * kKeys : 0);
+    static constexpr int kRowOff = kExpOff + (FP8 ? kVStages * 2 * kTokens : 0);
     // per row of both segments: place of its output and of its lse (two words each), logit scale, keys it sees;
     // then its factor
     static constexpr int kRowBytes = RP * 24;
     static constexpr int kRedOff = kRowOff + 2 * kRowBytes + RP * 4;
-    static constexpr int kBarOff = kRedOff + 4 * kGroups * (kRT + 4) * 4;
+    static constexpr int kOddOff = kRedOff + 4 * kGroups * (kRT + 4) * 4; // O of odd tokens, where rows are pairs
+    static constexpr int kBarOff = kOddOff + (kPar == 2 ? RP / 2 * D * 4 : 0);
     static constexpr int kNumBars = 2 * kStages + 3 * kVStages + 2 + 2 + 2 + 2 + 2 + 1;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kSmem = kMiscOff + 16 + 1024;
@@ -208,12 +220,19 @@ __device__ __forceinline__ __half2 from_codes(uint32_t c)
     return *reinterpret_cast<const __half2 *>(&r);
 }
 
-template <bool FP8, int RP>
-__global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPerSm)
+// Offset of 16-byte chunk c of row j in a tile.
+__device__ __forceinline__ uint32_t tile_chunk(int j, int c)
+{
+    return (c >> 3) * (kKeys * 128) + j * 128 + (((c & 7) ^ (j & 7)) << 4);
+}
+
+template <bool FP8, int RP, int D>
+__global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kCtasPerSm)
     paged_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       PagedProblem p, PagedPart part)
 {
-    using C = Cfg<FP8, RP>;
+    using C = Cfg<FP8, RP, D>;
+    constexpr int kPar = C::kPar, kTokens = C::kTokens;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const Bars bars = carve<C>(smem);
@@ -266,24 +285,24 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
     if (any && warp == C::kLoadWarp) {
         // ------------------------------------------------------------ loads
         // lane x fetches box x of a tile: its page number, then its K and V
-        const int box = min(p.c.page, kKeys), per = kKeys / box;
+        const int box = min(p.c.page, kTokens) / kPar, per = kKeys / box; // rows
         uint32_t i = 0;
         bool ok = true;
         auto entry = [&](int tile, int len) {
-            const int first = tile * kKeys + lane * box;
+            const int first = tile * kTokens + lane * box * kPar;
             return lane < per && first < len ? page_entry(p, part, c.b, first) : 0;
         };
         for (;;) {
             const int n = cursor_take(c), len = source_len(c.b);
             int next = entry(c.t0, len);
             for (int t = c.t0; ok && t < c.t0 + n; ++t, ++i) {
-                const int page = next, first = t * kKeys;
-                const int boxes = (min(len - first, kKeys) + box - 1) / box;
+                const int page = next, first = t * kTokens;
+                const int boxes = (min(len - first, kTokens) + box * kPar - 1) / (box * kPar);
                 if (t + 1 < c.t0 + n) next = entry(t + 1, len);
                 const bool mine = lane < boxes;
                 const bool good = mine && page_valid(p, page);
                 const int z = good ? page * p.c.Hkv + c.h : p.c.n_pages * p.c.Hkv; // out of range: zeros
-                const int off = (first + lane * box) & (p.c.page - 1);
+                const int off = ((first + lane * box * kPar) & (p.c.page - 1)) / kPar;
                 const int sv = i % C::kVStages, sk = i % C::kStages;
                 if (!(ok = wait_all(bars.k_empty + sk, ((i / C::kStages) & 1) ^ 1))) break;
                 if (lane == 0) mbar_expect_tx(bars.k_full + sk, boxes * box * (C::kMat / kKeys));
@@ -298,18 +317,18 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                 }
                 const int n_good = __popc(__ballot_sync(0xffffffffu, good));
                 if (FP8) {
-                    uint8_t *e = smem + C::kExpOff + sv * 2 * kKeys + lane * box;
+                    uint8_t *e = smem + C::kExpOff + sv * 2 * kTokens + lane * box * kPar;
                     if (mine && !good) { // zeros, at a scale of one
-                        for (int j = 0; j < box; ++j) e[j] = e[kKeys + j] = 127;
+                        for (int j = 0; j < box * kPar; ++j) e[j] = e[kTokens + j] = 127;
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_expect_tx(bars.e_full + sv, 2 * n_good * box);
+                    if (lane == 0) mbar_expect_tx(bars.e_full + sv, 2 * n_good * box * kPar);
                     __syncwarp();
                     if (good) {
-                        const size_t row = ((size_t)z << p.c.page_shift) + off;
-                        bulk_load(e, p.c.k_exp + row, box, bars.e_full + sv);
-                        bulk_load(e + kKeys, p.c.v_exp + row, box, bars.e_full + sv);
+                        const size_t row = ((size_t)z << p.c.page_shift) + off * kPar;
+                        bulk_load(e, p.c.k_exp + row, box * kPar, bars.e_full + sv);
+                        bulk_load(e + kTokens, p.c.v_exp + row, box * kPar, bars.e_full + sv);
                     }
                 }
                 if (lane == 0) mbar_expect_tx(bars.v_full + sv, boxes * box * (C::kMat / kKeys));
@@ -358,7 +377,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
             return true;
         };
         for (;;) {
-            const int n = cursor_take(c);
+            const int n = cursor_take(c), len = kPar == 2 ? source_len(c.b) : 0;
             if (!(ok = wait_all(bars.q_full + (segs & 1), (segs >> 1) & 1))) break;
             const uint64_t qd = qd0 + (uint32_t)(((segs++ & 1) * C::kQBytes) >> 4);
             for (int t = 0; ok && t < n; ++t, ++i) {
@@ -367,6 +386,20 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                 if (FP8 && !(ok = wait_all(bars.e_full + i % C::kVStages, (i / C::kVStages) & 1))) break;
                 if (!(ok = wait_all(bars.s_empty + sb, ((i >> 1) & 1) ^ 1))) break;
                 tc_fence_after();
+                if (kPar == 2) {
+                    // an odd length ends inside a row: its other token meets the zeros of
+                    // Q, and is made zero too, whatever is there
+                    const int valid = len - (c.t0 + t) * kTokens, j = valid >> 1;
+                    if (valid < kTokens && (valid & 1)) {
+                        if (lane < C::kHalves * 4)
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                             smem_u32(smem + C::kKOff + sk * C::kMat) + tile_chunk(j, C::kHalves * 4 + lane)),
+                                         "r"(0)
+                                         : "memory");
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
+                }
                 const uint64_t kd = kd0 + (uint32_t)((sk * C::kMat) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < (FP8 ? 4 : 8); ++kk) {
@@ -427,13 +460,13 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
 #pragma unroll 1
             for (int r = threadIdx.x >> 4; r < C::kNS / C::kQTerms; r += NT / 16) {
                 const int x = threadIdx.x & 15;
-                const PagedRow row = paged_row(p, part, at, r);
+                const PagedRow row = paged_row(p, part, at, r / kPar);
                 const bool live = r < RP && row.counts;
                 const int hq = at.h * p.G + row.g;
                 const long long place = ((long long)row.b * p.Lq + row.i) * p.Hq + hq;
                 uint4 w = make_uint4(0, 0, 0, 0);
-                if (live)
-                    w = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + (size_t)place * kD + x * 8);
+                if (live && (kPar == 1 || (x >> 3) == (r & 1)))
+                    w = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + (size_t)place * D + (x & (D / 8 - 1)) * 8);
                 float qs = p.scale * kLog2e;
                 if (FP8) {
                     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -500,21 +533,24 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
             for (int r = 0; r < kRT; ++r) m[r] = kNone, l[r] = 0.f;
             for (int t = c.t0; t < c.t0 + n; ++t, ++i) {
                 const int sb = i & 1, sv = i % C::kVStages;
-                const int key = t * kKeys + tid;
-                const int valid = min(len - t * kKeys, kKeys);
-                const bool masked = t * kKeys + kKeys > all;
+                const int tok = tid * kPar, first = t * kTokens; // the row's first token in the tile
+                const int valid = min(len - first, kTokens);
+                const bool masked = first + kTokens > all;
                 float s[kRT];
-                float ks = 1.f, vs = 1.f, ev = 0.f;
+                float ks[kPar] = {}, vs[kPar] = {}, ev = 0.f;
                 wait(bars.s_full + sb, (i >> 1) & 1);
                 tc_fence_after();
                 tmem_ld<8>(lane_base + sb * C::kNS + row0, s);
                 if (FP8) {
-                    const uint8_t *e = smem + C::kExpOff + sv * 2 * kKeys + tid;
-                    const uint32_t vb = e[kKeys];
-                    ks = exp_byte_scale(e[0]);
-                    vs = exp_byte_scale(vb);
-                    // bytes behind the length and rows without a value do not count
-                    if (tid < valid && vb != 255u) ev = fmaxf((float)vb, kMinExp);
+                    const uint8_t *e = smem + C::kExpOff + sv * 2 * kTokens + tok;
+#pragma unroll
+                    for (int y = 0; y < kPar; ++y) {
+                        const uint32_t vb = e[kTokens + y];
+                        ks[y] = exp_byte_scale(e[y]);
+                        vs[y] = exp_byte_scale(vb);
+                        // bytes behind the length and rows without a value do not count
+                        if (tok + y < valid && vb != 255u) ev = fmaxf(ev, fmaxf((float)vb, kMinExp));
+                    }
                 }
                 if (FP8) {
                     float s2[kRT];
@@ -530,7 +566,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                 // ---- logits in base 2
                 bool grow = FP8 && ev > ev_top;
 #pragma unroll
-                for (int r = 0; r < kRT; ++r) s[r] *= FP8 ? qs[r] * ks : qs[r];
+                for (int r = 0; r < kRT; ++r) s[r] *= FP8 ? qs[r] * ks[r % kPar] : qs[r];
                 if (to_cap > 0.f) {
                     float xa = 0.f;
 #pragma unroll
@@ -546,7 +582,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                 if (masked) {
 #pragma unroll
                     for (int r = 0; r < kRT; ++r)
-                        if (tid >= valid || key >= rows.limit[row0 + r]) s[r] = -INFINITY;
+                        if (tok + r % kPar >= valid || first + tok + r % kPar >= rows.limit[row0 + r]) s[r] = -INFINITY;
                 }
 #pragma unroll
                 for (int r = 0; r < kRT; ++r) grow |= s[r] > m[r] + C::kLazy;
@@ -574,14 +610,19 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                     }
                     float f[kRT];
 #pragma unroll
-                    for (int r = 0; r < kRT; ++r) {
+                    for (int r = 0; r < kRT; r += kPar) {
                         float top = m[r];
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) top = fmaxf(top, red[w * RS + r]);
+                        for (int w = 0; w < 4; ++w)
+#pragma unroll
+                            for (int y = 0; y < kPar; ++y) top = fmaxf(top, red[w * RS + r + y]);
                         const float x = ex2_approx(m[r] - top);
-                        l[r] *= x;
-                        f[r] = x * fe;
-                        m[r] = top;
+#pragma unroll
+                        for (int y = 0; y < kPar; ++y) {
+                            l[r + y] *= x;
+                            f[r + y] = x * fe;
+                            m[r + y] = top;
+                        }
                     }
                     if (t > c.t0) {
                         tc_fence_after();
@@ -603,13 +644,13 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                 // r is k * RP + r, this thread's row is its key.  S of this tile was
                 // issued after P V of the tile before last, so that tile's weights
                 // have been read.
-                const float pb = FP8 ? ex2_approx(127.f + kPBias - fmaxf(ev_top, kMinExp)) * vs : 1.f;
+                const float pb = FP8 ? ex2_approx(127.f + kPBias - fmaxf(ev_top, kMinExp)) : 1.f;
                 float x[kRT];
 #pragma unroll
                 for (int r = 0; r < kRT; ++r) {
                     x[r] = ex2_approx(s[r] - m[r]);
                     l[r] += x[r];
-                    if (FP8) x[r] *= pb;
+                    if (FP8) x[r] *= pb * vs[r % kPar];
                 }
                 if (FP8 && masked) {
                     // a masked key's scale may be anything
@@ -649,15 +690,14 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                                  "r"(lo[1]), "r"(lo[2]), "r"(lo[3])
                                  : "memory");
                 }
-                if (valid < kKeys) {
+                if (valid < kTokens) {
                     // values behind the length: whatever is there, weight 0 must give 0
                     wait(bars.v_full + sv, (i / C::kVStages) & 1);
-                    if (grp == 0 && tid >= valid)
+                    if (grp == 0 && tok + kPar > valid)
 #pragma unroll 1
-                        for (int x = 0; x < C::kHalves * 8; ++x)
+                        for (int x = tok < valid ? C::kHalves * 4 : 0; x < C::kHalves * 8; ++x)
                             asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
-                                             smem_u32(smem + C::kVOff + sv * C::kMat) + (x >> 3) * (kKeys * 128) + tid * 128 +
-                                             (x & 7) * 16),
+                                             smem_u32(smem + C::kVOff + sv * C::kMat) + tile_chunk(tid, x)),
                                          "r"(0)
                                          : "memory");
                 }
@@ -675,13 +715,16 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
             }
             soft_sync<NT>();
             const bool final = stores_whole(part, c, n);
-            const size_t slot = slot_row(part, c) + row0;
-            if (tid < kRT) {
-                // a thread per row: its factor, and what is stored beside O
-                const long long place = rows.place[row0 + tid];
-                float lr = 0.f, mr = row_f[row0 + tid], f = 1.f;
+            const size_t slot = slot_row(part, c) + row0 / kPar;
+            if (tid < kRT / kPar) {
+                // a thread per query row: its factor, and what is stored beside O
+                const int col = row0 + tid * kPar;
+                const long long place = rows.place[col];
+                float lr = 0.f, mr = row_f[col], f = 1.f;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) lr += red[w * RS + tid];
+                for (int w = 0; w < 4; ++w)
+#pragma unroll
+                    for (int y = 0; y < kPar; ++y) lr += red[w * RS + tid * kPar + y];
                 if (final) {
                     if (p.sinks && place >= 0) {
                         const float sink = p.sinks[place % p.Hq] * kLog2e, top = fmaxf(mr, sink);
@@ -690,12 +733,12 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
                         mr = top;
                     }
                     f = lr == 0.f ? 0.f : f / lr;
-                    if (place >= 0) p.lse[rows.lse[row0 + tid]] = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * kLn2;
+                    if (place >= 0) p.lse[rows.lse[col]] = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * kLn2;
                 } else if (place >= 0) {
                     *reinterpret_cast<float2 *>(part.ml + (slot + tid) * 2) = make_float2(mr, lr);
                 }
                 if (FP8) f *= ex2_approx(fmaxf(ev_top, kMinExp) - 127.f - kPBias);
-                row_f[row0 + tid] = f;
+                row_f[col] = f;
             }
             wait(bars.pv_done + ((i - 1) & 1), ((i - 1) >> 1) & 1);
             soft_sync<NT>();
@@ -705,16 +748,35 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
             for (int k = 0; k < C::kPTerms; ++k) tmem_ld<8>(lane_base + C::kColO + k * RP + row0, o[k]);
             tmem_ld_wait();
             tc_fence_before();
+            // a query row's O: this thread's value of it, from all tokens or from
+            // those of the thread's parity
+            float v[kRT / kPar];
 #pragma unroll
-            for (int y = 0; y < kRT; ++y) {
-                const long long place = rows.place[row0 + y];
-                if (place < 0) continue;
-                float v = o[0][y];
-                if (FP8) v += (o[1][y] + o[C::kPTerms - 1][y] * (1.f / 16.f)) * (1.f / 16.f);
-                else v += o[1][y];
-                v *= row_f[row0 + y];
-                if (final) static_cast<__nv_bfloat16 *>(p.out)[(size_t)place * kD + tid] = __float2bfloat16_rn(v);
-                else part.o[(slot + y) * kD + tid] = v;
+            for (int y = 0; y < kRT / kPar; ++y) {
+                float z[C::kPTerms];
+#pragma unroll
+                for (int k = 0; k < C::kPTerms; ++k) z[k] = kPar == 2 && tid >= D ? o[k][y * kPar + kPar - 1] : o[k][y * kPar];
+                v[y] = FP8 ? z[0] + (z[1] + z[C::kPTerms - 1] * (1.f / 16.f)) * (1.f / 16.f) : z[0] + z[1];
+                v[y] *= row_f[row0 + y * kPar];
+            }
+            if (kPar == 2) {
+                float *odd = reinterpret_cast<float *>(smem + C::kOddOff) + row0 / kPar * D + (tid & (D - 1));
+                if (tid >= D) {
+#pragma unroll
+                    for (int y = 0; y < kRT / kPar; ++y) odd[y * D] = v[y];
+                }
+                group_sync(bar);
+                if (tid < D) {
+#pragma unroll
+                    for (int y = 0; y < kRT / kPar; ++y) v[y] += odd[y * D];
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < kRT / kPar; ++y) {
+                const long long place = rows.place[row0 + y * kPar];
+                if (place < 0 || tid >= D) continue;
+                if (final) static_cast<__nv_bfloat16 *>(p.out)[(size_t)place * D + tid] = __float2bfloat16_rn(v[y]);
+                else part.o[(slot + y) * D + tid] = v[y];
             }
             soft_sync<NT>(); // the rows' arrays and red are free again
             if (!more) break;
@@ -731,18 +793,19 @@ __global__ void __launch_bounds__(Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kCtasPer
     }
 }
 
-template <bool FP8, int RP>
+template <bool FP8, int RP, int D>
 cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s)
 {
-    auto kern = paged_keys_kernel<FP8, RP>;
+    using C = Cfg<FP8, RP, D>;
+    auto kern = paged_keys_kernel<FP8, RP, D>;
     static std::atomic<uint64_t> set{0}; // devices whose copy of the kernel has its attribute
     const uint64_t bit = 1ull << p.device;
     if (!(set.load(std::memory_order_acquire) & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<FP8, RP>::kSmem);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (e != cudaSuccess) return e;
         set.fetch_or(bit, std::memory_order_release);
     }
-    return launch_dependent(kern, (unsigned)part.ctas, Cfg<FP8, RP>::kThreads, Cfg<FP8, RP>::kSmem, s, k, v, p, part);
+    return launch_dependent(kern, (unsigned)part.ctas, C::kThreads, C::kSmem, s, k, v, p, part);
 }
 
 } // namespace
@@ -751,12 +814,18 @@ cudaError_t launch_paged_keys(const PagedProblem &p, const PagedPart &part, int 
                               const void *tm_v, cudaStream_t s)
 {
     const CUtensorMap &k = *static_cast<const CUtensorMap *>(tm_k), &v = *static_cast<const CUtensorMap *>(tm_v);
-    if (cache_dtype == RA_E4M3) {
-        if (part.row_block == 8) return go<true, 8>(p, part, k, v, s);
-        return part.row_block == 16 ? go<true, 16>(p, part, k, v, s) : go<true, 32>(p, part, k, v, s);
-    }
-    if (part.row_block == 8) return go<false, 8>(p, part, k, v, s);
-    return part.row_block == 16 ? go<false, 16>(p, part, k, v, s) : go<false, 32>(p, part, k, v, s);
+    const int cols = part.row_block * (kD / p.c.D);
+    auto typed = [&](auto fp8, auto d) {
+        constexpr bool FP8 = decltype(fp8)::value;
+        constexpr int D = decltype(d)::value;
+        return cols == 8    ? go<FP8, 8, D>(p, part, k, v, s)
+               : cols == 16 ? go<FP8, 16, D>(p, part, k, v, s)
+                            : go<FP8, 32, D>(p, part, k, v, s);
+    };
+    auto sized = [&](auto fp8) {
+        return p.c.D == 64 ? typed(fp8, std::integral_constant<int, 64>{}) : typed(fp8, std::integral_constant<int, 128>{});
+    };
+    return cache_dtype == RA_E4M3 ? sized(std::true_type{}) : sized(std::false_type{});
 }
 
 } // namespace ra

@@ -347,16 +347,16 @@ void count_launches(int n) { count(n); }
 
 int encode_paged(void *map, const ra_kv_cache *c, const void *base, int rows)
 {
-    const cuuint64_t item = c->dtype == RA_E4M3 ? 1 : 2, row = c->D * item;
-    const cuuint32_t width = (cuuint32_t)((row < 128 ? row : 128) / item);
-    const cuuint64_t dims[3] = {(cuuint64_t)c->D, (cuuint64_t)c->page_size, (cuuint64_t)c->n_pages * c->Hkv};
-    const cuuint64_t strides[2] = {row, row * c->page_size};
-    const cuuint32_t box[3] = {width, (cuuint32_t)rows, 1};
+    const cuuint64_t item = c->dtype == RA_E4M3 ? 1 : 2, row = 128 * item;
+    const cuuint64_t per_page = (cuuint64_t)c->page_size * c->D / 128;
+    const cuuint64_t dims[3] = {128, per_page, (cuuint64_t)c->n_pages * c->Hkv};
+    const cuuint64_t strides[2] = {row, row * per_page};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / item), (cuuint32_t)rows, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = g_encode(static_cast<CUtensorMap *>(map),
                           item == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                           const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          width * item == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     return RA_OK;

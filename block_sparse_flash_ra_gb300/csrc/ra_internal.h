@@ -159,9 +159,9 @@ struct DeviceInfo {
 int device_info(DeviceInfo *out);
 void count_launches(int n);
 
-// A 3-D TMA map (a CUtensorMap) over a paged cache: (D, page, n_pages * Hkv)
-// elements of `dtype`, boxes of `rows` tokens by 128 bytes (or D, if that is
-// less), swizzled over the box's width.
+// A 3-D TMA map (a CUtensorMap) over a paged cache: (128, page * D / 128,
+// n_pages * Hkv) elements -- at D = 64 a row is two tokens -- in boxes of
+// `rows` rows by 128 bytes, swizzled over the 128 bytes.
 int encode_paged(void *map, const ra_kv_cache *c, const void *base, int rows);
 
 } // namespace ra

@@ -86,15 +86,9 @@ constexpr int kPagedF32Rows = 8, kPagedF32Tile = 32;
 cudaError_t launch_paged_f32(const PagedProblem &p, const PagedPart &part, int cache_dtype,
                              cudaStream_t s);
 
-// bf16 queries, D = 64, row_block 8 or 16: tensor cores fed from registers;
-// tm_k, tm_v: maps of encode_paged over the cache (boxes of min(page, 32)
-// tokens)
-constexpr int kPagedFewTile = 128;
-cudaError_t launch_paged_few(const PagedProblem &p, const PagedPart &part, int cache_dtype,
-                             const void *tm_k, const void *tm_v, cudaStream_t s);
-
-// bf16 queries, D = 128, row_block 8, 16 or 32: the keys as the M side of
-// tcgen05 products (boxes of min(page, 128) tokens)
+// bf16 queries, few rows: the keys as the M side of tcgen05 products.
+// row_block * 128 / D is 8, 16 or 32, a tile kPagedKeysTile rows of 128 values
+// (with D = 64 two tokens each; boxes of min(page * D / 128, 128) rows)
 constexpr int kPagedKeysTile = 128;
 cudaError_t launch_paged_keys(const PagedProblem &p, const PagedPart &part, int cache_dtype,
                               const void *tm_k, const void *tm_v, cudaStream_t s);

@@ -120,7 +120,7 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 // size does not depend on the device (GB300 has 152 SMs).
 constexpr int kSms = 152;
 
-enum { kF32, kFew, kKeysM, kRowsM };
+enum { kF32, kKeysM, kRowsM };
 
 struct Plan {
     bool fits; // no part is too large
@@ -154,18 +154,14 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
             a.by_groups = 1;
             a.tile = kPagedRowsTile;
             a.ctas = kSms;
-        } else if (c->D == 128) {
+        } else {
             kernel = kKeysM;
             a.seg_cost = 4;
-            a.row_block = a.rows <= 8 ? 8 : a.rows <= 16 ? 16 : 32;
-            a.tile = kPagedKeysTile;
-            a.ctas = (c->dtype == RA_E4M3 && a.row_block <= 16 ? 2 : 1) * kSms;
-        } else {
-            kernel = kFew;
-            a.seg_cost = 2;
-            a.row_block = a.rows <= 8 ? 8 : 16;
-            a.tile = kPagedFewTile;
-            a.ctas = 2 * kSms;
+            const int par = 128 / c->D; // columns of a query row
+            const int cols = a.rows * par <= 8 ? 8 : a.rows * par <= 16 ? 16 : 32;
+            a.row_block = cols / par;
+            a.tile = kPagedKeysTile * par;
+            a.ctas = (c->dtype == RA_E4M3 && cols <= 16 ? 2 : 1) * kSms;
         }
         a.n_rb = (a.rows + a.row_block - 1) / a.row_block;
         a.slot_rows = a.rows < a.row_block ? a.rows : a.row_block;
@@ -288,15 +284,12 @@ RA_API int ra_attn_paged(const ra_kv_cache *cache, const ra_paged_params *p, con
             e = launch_paged_f32(x, part, cache->dtype, s);
             continue;
         }
-        const int most = pl.kernel[k] == kFew                                ? 32
-                         : pl.kernel[k] == kRowsM && cache->dtype == RA_E4M3 ? 64
-                                                                             : 128; // of a box
-        const int rows = cache->page_size < most ? cache->page_size : most;
+        const int most = pl.kernel[k] == kRowsM && cache->dtype == RA_E4M3 ? 64 : 128; // of a box
+        const int in_page = cache->page_size * cache->D / 128, rows = in_page < most ? in_page : most;
         CUtensorMap tk, tv;
         if ((rc = encode_paged(&tk, cache, cache->k, rows)) || (rc = encode_paged(&tv, cache, cache->v, rows))) return rc;
-        e = pl.kernel[k] == kFew     ? launch_paged_few(x, part, cache->dtype, &tk, &tv, s)
-            : pl.kernel[k] == kKeysM ? launch_paged_keys(x, part, cache->dtype, &tk, &tv, s)
-                                     : launch_paged_rows(x, part, cache->dtype, &tk, &tv, s);
+        e = pl.kernel[k] == kKeysM ? launch_paged_keys(x, part, cache->dtype, &tk, &tv, s)
+                                   : launch_paged_rows(x, part, cache->dtype, &tk, &tv, s);
     }
     if (e == cudaSuccess) e = launch_paged_join(x, pl.part, pl.n_parts, p->dtype, s);
     if (e != cudaSuccess) return set_cuda_error(e, "paged attention launch");

@@ -568,8 +568,8 @@ RA_API size_t ra_attn_paged_workspace_size(const ra_kv_cache *cache, const ra_pa
  *           contents need not survive the call.  Calls that may overlap in
  *           time (other streams, graphs replayed at once) need one each.
  * Keys and values behind a sequence's length are never used, whatever the
- * memory holds; inside it, a value row that only some of a sequence's
- * queries see has to be finite.
+ * memory holds; inside it, key and value rows that only some of a sequence's
+ * queries see have to be finite.
  * Serving only: there is no backward pass.
  * The prefix is read once for the whole batch.  Results do not depend on how
  * the work was timed: partial results are joined in a fixed order.

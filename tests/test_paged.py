@@ -264,6 +264,11 @@ def test_out_of_range_places_are_skipped_and_reported():
 # ------------------------------------------------------------- attention
 CASES = {
     "one_key": dict(lens=[1], Hq=2),
+    "one_key_d64": dict(lens=[1, 0, 2, 3], Hq=2, D=64),
+    "tile_edges_d64": dict(lens=[255, 256, 257, 511, 513, 128, 127], Hq=16, D=64, page=128),
+    "long_split_d64": dict(lens=[9001], Hq=8, D=64, page=64),
+    "chunk_d64": dict(lens=[200, 151], Hq=4, Lq=150, D=64),
+    "draft_ragged_d64": dict(lens=[70, 3, 129, 20], Hq=4, Lq=5, q_len=[5, 1, 0, 4], D=64, sinks=True),
     "nothing_cached": dict(lens=[0, 5, 0], Hq=2),
     "page_edges": dict(lens=[15, 16, 17, 31, 32, 33], Hq=4),
     "page128": dict(lens=[127, 128, 129, 300], Hq=4, page=128),
@@ -314,14 +319,15 @@ def test_attention(name, cache, dtype):
 @gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("cache", [F8, torch.bfloat16], ids=["e4m3", "c16"])
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("Hq,B", [(2, 2), (16, 9)])
-def test_what_lies_behind_a_length_does_not_count(Hq, B, cache, dtype):
+def test_what_lies_behind_a_length_does_not_count(Hq, B, D, cache, dtype):
     """Keys and values past a sequence's end hold NaN and infinities; a page past it has no number."""
     lens = [(29 * b + 5) % 70 for b in range(B)]
-    pool = Pool(lens, Hkv=1, page=32, dtype=cache, seed=3, prefix=40, width=6)
+    pool = Pool(lens, Hkv=1, D=D, page=32, dtype=cache, seed=3, prefix=40 if D == 128 else 41, width=6)
     bad = torch.tensor([float("nan"), float("inf"), float("-inf"), 3e38])
     for b in range(B + 1):
-        pages, n = (pool.table[b], lens[b]) if b < B else (pool.prefix, 40)
+        pages, n = (pool.table[b], lens[b]) if b < B else (pool.prefix, pool.prefix_len)
         for t in range(n, -(-n // 32) * 32):
             at = (int(pages[t // 32]), slice(None), t % 32)
             for w, (x, e) in enumerate(((pool.cache.k_pages, pool.cache.k_exps), (pool.cache.v_pages, pool.cache.v_exps))):
@@ -330,7 +336,7 @@ def test_what_lies_behind_a_length_does_not_count(Hq, B, cache, dtype):
                     e[at] = 255 if t % 3 else 0
                 else:
                     x[at] = bad[(t + w) % 4].to(torch.bfloat16)
-    q = torch.randn((B, 1, Hq, 128), generator=torch.Generator().manual_seed(4)).to(dtype)
+    q = torch.randn((B, 1, Hq, D), generator=torch.Generator().manual_seed(4)).to(dtype)
     check_attention(pool, q)
 
 
@@ -362,7 +368,7 @@ def test_large_logits_keep_their_weights():
 
 
 # heads, kv heads, query tokens and head size of a call that each kernel takes: rows per kv head decide
-KERNELS = {"d64": (4, 1, 1, 64), "rows8": (2, 1, 1, 128), "rows16": (16, 1, 1, 128), "rows32": (32, 1, 1, 128),
+KERNELS = {"d64": (4, 1, 1, 64), "d64_8": (8, 1, 1, 64), "d64_16": (16, 1, 1, 64), "d64_80": (8, 1, 10, 64), "rows8": (2, 1, 1, 128), "rows16": (16, 1, 1, 128), "rows32": (32, 1, 1, 128),
            "rows80": (8, 1, 10, 128), "rows320": (8, 1, 40, 128)}
 each_kernel = pytest.mark.parametrize("name", KERNELS)
 each_cache = pytest.mark.parametrize("cache", [F8, torch.bfloat16], ids=["e4m3", "c16"])
