@@ -2,78 +2,86 @@
 //
 // For each query row of an item: s_j = scale <q, k_j> (capped), an online
 // softmax in base 2 over the tiles of the CTA's share, and o = sum p_j v_j.
-// Keys, values, logits, probabilities and sums are fp32: the cached rows are
-// widened once per tile into shared memory and used by the 8 rows of an item.
-// It serves fp32 queries, whose results 16-bit tensor-core operands would
-// round.  Bound by the FMA pipe: 2 * 8 multiply-adds per cached value.
+// Logits, probabilities, sums and products are fp32.  It serves fp32 queries,
+// whose results 16-bit tensor-core operands would round.
+//
+// Bound by the FMA pipe: 2 * rows multiply-adds per cached value, one widening
+// beside them.  So nothing passes through shared memory on the way: D / 8
+// lanes take a key, 8 values each, with q and o of all the item's rows in
+// their registers; a warp takes 16 keys (part of one page) of a tile of 64.
+// The lanes' partial logits are summed by halving -- each step a lane hands
+// half of its rows over and keeps the other -- which leaves one row to a lane:
+// 8 exchanges instead of 32 for 8 rows, and the softmax of a row and key is
+// computed once, not by 16 lanes.  V is on its way while S is computed, the
+// next K while the values are summed.
 #include <cuda_fp16.h>
 #include <math.h>
+
+#include <type_traits>
 
 #include "ra_paged.cuh"
 
 namespace ra {
 namespace {
 
-constexpr int kRows = kPagedF32Rows, kKeys = kPagedF32Tile, kThreads = 128;
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kWarpKeys = 16;
+static_assert(kPagedF32Tile == kWarps * kWarpKeys, "a warp's keys lie in one page");
 
-// A tile of keys or values, fp32, rows of D + 4 floats.
-template <int D, bool FP8>
-__device__ __forceinline__ void fill_tile(float *dst, const void *base, const uint8_t *exps,
-                                          const PagedProblem &p, const PagedPart &part, int b, int h,
-                                          int t, int len)
+constexpr int log2_of(int x) { return x < 2 ? 0 : 1 + log2_of(x / 2); }
+
+// Eight cached values as the cache has them.
+template <bool FP8>
+struct Raw8 {
+    uint4 w; // codes: .x and .y
+};
+
+template <bool FP8>
+__device__ __forceinline__ Raw8<FP8> load8(const void *base, size_t value)
 {
-    constexpr int PER = D / 8; // 8 values each
-    for (int e = threadIdx.x; e < kKeys * PER; e += kThreads) {
-        const int j = e / PER, x = e % PER;
-        float r[8] = {};
-        if (t + j < len) {
-            const int page = page_entry(p, part, b, t + j);
-            if (page_valid(p, page)) {
-                const size_t row =
-                    (((size_t)page * p.c.Hkv + h) << p.c.page_shift) + ((t + j) & (p.c.page - 1));
-                if (FP8) {
-                    const uint2 w =
-                        reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(base) + row * D)[x];
-                    const float s = exp_byte_scale(exps[row]);
-                    const uint32_t c[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
+    Raw8<FP8> r;
+    if (FP8) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(base) + value);
+        r.w.x = w.x;
+        r.w.y = w.y;
+    } else {
+        r.w = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + value);
+    }
+    return r;
+}
+
+template <bool FP8>
+__device__ __forceinline__ void widen8(const Raw8<FP8> &r, float *x)
+{
+    if (FP8) {
+        const uint32_t c[4] = {r.w.x & 0xffffu, r.w.x >> 16, r.w.y & 0xffffu, r.w.y >> 16};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t y = e4m3x2_to_f16x2(c[i]);
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&y));
-                        r[2 * i] = f.x * s;
-                        r[2 * i + 1] = f.y * s;
-                    }
-                } else {
-                    const uint4 w = reinterpret_cast<const uint4 *>(
-                        static_cast<const __nv_bfloat16 *>(base) + row * D)[x];
-                    const uint32_t c[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        r[2 * i] = __uint_as_float(c[i] << 16);
-                        r[2 * i + 1] = __uint_as_float(c[i] & 0xffff0000u);
-                    }
-                }
-            }
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t h = e4m3x2_to_f16x2(c[i]);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
         }
-        float4 *o = reinterpret_cast<float4 *>(dst + j * (D + 4) + x * 8);
-        o[0] = make_float4(r[0], r[1], r[2], r[3]);
-        o[1] = make_float4(r[4], r[5], r[6], r[7]);
+    } else {
+        const uint32_t c[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(c[i] << 16);
+            x[2 * i + 1] = __uint_as_float(c[i] & 0xffff0000u);
+        }
     }
 }
 
-template <int D, bool FP8>
-__global__ void __launch_bounds__(kThreads)
+template <int D, bool FP8, int R>
+__global__ void __launch_bounds__(kThreads, R == 4 ? 4 : 2)
     paged_f32_kernel(PagedProblem p, PagedPart part)
 {
-    // o: thread t holds column t % D of rows (t / D) * OR .. + OR - 1
-    constexpr int OR = kRows * D / kThreads;
-    __shared__ float4 q_s4[kRows * D / 4];
-    __shared__ float4 k_s4[kKeys * (D + 4) / 4], v_s4[kKeys * (D + 4) / 4];
-    __shared__ float p_s[kRows][kKeys], f_s[kRows], m_s[kRows], l_s[kRows];
-    float *q_s = reinterpret_cast<float *>(q_s4);
-    float *k_s = reinterpret_cast<float *>(k_s4), *v_s = reinterpret_cast<float *>(v_s4);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int col = threadIdx.x % D, row0 = threadIdx.x / D * OR;
+    constexpr int LANES = D / 8, STEP = 32 / LANES, STEPS = kWarpKeys / STEP; // lanes of a key; keys at once
+    constexpr int REST = log2_of(LANES) - log2_of(R); // lanes that hold the same row, as a power of two
+    constexpr uint32_t ALL = 0xffffffffu;
+    __shared__ float o_s[kWarps][R * D];
+    __shared__ float2 ml_s[kWarps][R];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES, kg = lane / LANES;
+    const int own = sub >> REST; // the row whose softmax this lane computes
     const float *q = static_cast<const float *>(p.q);
     begin_in_order(part);
     report_lengths(p, part);
@@ -82,109 +90,179 @@ __global__ void __launch_bounds__(kThreads)
     for (int n; any;) {
         n = cursor_take(c);
         const int len = part.prefix ? paged_prefix_len(p) : paged_kv_len(p, c.b);
-        __syncthreads(); // the last segment's shared arrays have been read
-        for (int e = threadIdx.x; e < kRows * D; e += kThreads) {
-            const PagedRow r = paged_row(p, part, c, e / D);
-            q_s[e] = r.limit > 0 ? q[(((size_t)r.b * p.Lq + r.i) * p.Hq + c.h * p.G + r.g) * D + e % D]
-                                 : 0.f;
-        }
-        // warp w owns the softmax of rows 2w and 2w + 1, lane = key
-        int limit[2];
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        float o[OR] = {};
+        float qr[R][8];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) limit[u] = paged_row(p, part, c, 2 * warp + u).limit;
+        for (int r = 0; r < R; ++r) {
+            const PagedRow row = paged_row(p, part, c, r);
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+            if (row.limit > 0) {
+                const float4 *src = reinterpret_cast<const float4 *>(
+                    q + (((size_t)row.b * p.Lq + row.i) * p.Hq + c.h * p.G + row.g) * D + sub * 8);
+                a = src[0];
+                b = src[1];
+            }
+            qr[r][0] = a.x, qr[r][1] = a.y, qr[r][2] = a.z, qr[r][3] = a.w;
+            qr[r][4] = b.x, qr[r][5] = b.y, qr[r][6] = b.z, qr[r][7] = b.w;
+        }
+        const int limit = paged_row(p, part, c, own).limit;
+        float o[R][8] = {}, m = -INFINITY, l = 0.f; // m, l: of row `own`, l of this lane's keys
+
+        // the warp's keys of tile t: their first row in the cache, or -1
+        auto place = [&](int t) -> long long {
+            const int first = t * kPagedF32Tile + warp * kWarpKeys;
+            if (first >= len) return -1;
+            const int page = page_entry(p, part, c.b, first);
+            if (!page_valid(p, page)) return -1;
+            return (((long long)page * p.c.Hkv + c.h) << p.c.page_shift) + (first & (p.c.page - 1));
+        };
+        Raw8<FP8> k[STEPS], v[STEPS];
+        auto fetch = [&](Raw8<FP8> *x, const void *base, long long at, int t) {
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const int j = s * STEP + kg;
+                x[s].w = make_uint4(0, 0, 0, 0);
+                if (at >= 0 && t * kPagedF32Tile + warp * kWarpKeys + j < len)
+                    x[s] = load8<FP8>(base, (size_t)(at + j) * D + sub * 8);
+            }
+        };
+        long long at = place(c.t0);
+        fetch(k, p.c.k, at, c.t0);
         for (int t = c.t0; t < c.t0 + n; ++t) {
-            __syncthreads();
-            fill_tile<D, FP8>(k_s, p.c.k, p.c.k_exp, p, part, c.b, c.h, t * kKeys, len);
-            fill_tile<D, FP8>(v_s, p.c.v, p.c.v_exp, p, part, c.b, c.h, t * kKeys, len);
-            __syncthreads();
-            float s[2] = {0.f, 0.f};
-            const float4 *k4 = reinterpret_cast<const float4 *>(k_s + lane * (D + 4));
-            const float4 *q4 = reinterpret_cast<const float4 *>(q_s + 2 * warp * D);
-#pragma unroll 8
-            for (int d = 0; d < D / 4; ++d) {
-                const float4 kv = k4[d];
+            const int first = t * kPagedF32Tile + warp * kWarpKeys;
+            const long long next = t + 1 < c.t0 + n ? place(t + 1) : -1;
+            fetch(v, p.c.v, at, t);
+            uint32_t ke[STEPS], ve[STEPS];
+            if (FP8) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const float4 qv = q4[u * (D / 4) + d];
-                    s[u] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s[u]))));
+                for (int s = 0; s < STEPS; ++s) {
+                    const int j = s * STEP + kg;
+                    const bool there = at >= 0 && first + j < len; // else zeros, at a scale of one
+                    ke[s] = there ? p.c.k_exp[at + j] : 127u;
+                    ve[s] = there ? p.c.v_exp[at + j] : 127u;
                 }
             }
+            // ---- logits of row `own`
+            float x[STEPS], top = -INFINITY;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float x = s[u] * p.scale;
-                if (p.soft_cap > 0.f) x = p.soft_cap * tanhf(x / p.soft_cap);
-                x = t * kKeys + lane < limit[u] ? x * kLog2e : -INFINITY;
-                float top = x;
+            for (int s = 0; s < STEPS; ++s) {
+                float kf[8], d[R];
+                widen8<FP8>(k[s], kf);
 #pragma unroll
-                for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-                const float m_new = fmaxf(m[u], top);
-                const float base = m_new == -INFINITY ? 0.f : m_new;
-                const float f = exp2f(m[u] - base), e = exp2f(x - base);
-                float sum = e;
+                for (int r = 0; r < R; ++r) {
+                    d[r] = qr[r][0] * kf[0];
 #pragma unroll
-                for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-                l[u] = l[u] * f + sum;
-                m[u] = m_new;
-                p_s[2 * warp + u][lane] = e;
-                if (lane == 0) f_s[2 * warp + u] = f;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int r = 0; r < OR; ++r) o[r] *= f_s[row0 + r];
-            for (int j = 0; j < kKeys; ++j) {
-                const float v = v_s[j * (D + 4) + col];
-#pragma unroll
-                for (int r = 0; r < OR; ++r) {
-                    // a value that the row does not see must not reach it,
-                    // whatever it is
-                    const float e = p_s[row0 + r][j];
-                    if (e != 0.f) o[r] = fmaf(e, v, o[r]);
+                    for (int y = 1; y < 8; ++y) d[r] = fmaf(qr[r][y], kf[y], d[r]);
                 }
-            }
-        }
-        // a NaN logit is visible and carries itself into l and o
-        if (lane == 0) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                m_s[2 * warp + u] = m[u];
-                l_s[2 * warp + u] = l[u];
-            }
-        }
-        __syncthreads();
-        if (stores_whole(part, c, n)) {
-            // the whole segment was here: the rows' final values
+                for (int h = R / 2, w = LANES / 2; h >= 1; h >>= 1, w >>= 1) {
+                    const bool up = (sub & w) != 0;
 #pragma unroll
-            for (int r = 0; r < OR; ++r) {
-                const PagedRow x = paged_row(p, part, c, row0 + r);
-                if (!x.counts) continue;
-                float mr = m_s[row0 + r], lr = l_s[row0 + r], f = 1.f;
-                const int hq = c.h * p.G + x.g;
-                if (p.sinks) {
-                    const float sink = p.sinks[hq] * kLog2e, top = fmaxf(mr, sink);
-                    f = exp2f(mr - top);
-                    lr = lr * f + exp2f(sink - top);
-                    mr = top;
-                }
-                const float val = lr == 0.f ? 0.f : o[r] * f / lr;
-                static_cast<float *>(p.out)[(((size_t)x.b * p.Lq + x.i) * p.Hq + hq) * D + col] = val;
-                if (col == 0)
-                    p.lse[((size_t)x.b * p.Hq + hq) * p.Lq + x.i] = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * kLn2;
-            }
-        } else {
-            const size_t at = slot_row(part, c) + row0;
-#pragma unroll
-            for (int r = 0; r < OR; ++r)
-                if (row0 + r < part.slot_rows) {
-                    part.o[(at + r) * D + col] = o[r];
-                    if (col == 0) {
-                        part.ml[(at + r) * 2] = m_s[row0 + r];
-                        part.ml[(at + r) * 2 + 1] = l_s[row0 + r];
+                    for (int r = 0; r < h; ++r) {
+                        const float mine = up ? d[r + h] : d[r], other = up ? d[r] : d[r + h];
+                        d[r] = mine + __shfl_xor_sync(ALL, other, w);
                     }
                 }
+#pragma unroll
+                for (int w = (1 << REST) / 2; w; w >>= 1) d[0] += __shfl_xor_sync(ALL, d[0], w);
+                float z = d[0] * p.scale;
+                if (FP8) z *= exp_byte_scale(ke[s]);
+                if (p.soft_cap > 0.f) z = p.soft_cap * tanhf(z / p.soft_cap);
+                x[s] = first + s * STEP + kg < limit ? z * kLog2e : -INFINITY;
+                top = fmaxf(top, x[s]);
+            }
+            fetch(k, p.c.k, next, t + 1);
+            at = next;
+            // ---- weights
+#pragma unroll
+            for (int w = LANES; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(ALL, top, w));
+            const float m_new = fmaxf(m, top), base = m_new == -INFINITY ? 0.f : m_new;
+            if (__any_sync(ALL, m_new != m)) {
+                const float f = exp2f(m - base);
+                l *= f;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float fr = __shfl_sync(ALL, f, r << REST);
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) o[r][y] *= fr;
+                }
+                m = m_new;
+            }
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const float e = exp2f(x[s] - base);
+                l += e;
+                // a value that the row does not see must not reach it, whatever it is
+                x[s] = !FP8 ? e : e == 0.f ? 0.f : e * exp_byte_scale(ve[s]);
+            }
+            // ---- values
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                float vf[8];
+                widen8<FP8>(v[s], vf);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float e = __shfl_sync(ALL, x[s], kg * LANES + (r << REST));
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) o[r][y] = fmaf(e, vf[y], o[r][y]);
+                }
+            }
+        }
+        // ---- the segment's end: key groups of a warp, then the warps
+#pragma unroll
+        for (int w = LANES; w < 32; w <<= 1) {
+            l += __shfl_xor_sync(ALL, l, w);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int y = 0; y < 8; ++y) o[r][y] += __shfl_xor_sync(ALL, o[r][y], w);
+        }
+        if (kg == 0) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float4 *dst = reinterpret_cast<float4 *>(o_s[warp] + r * D + sub * 8);
+                dst[0] = make_float4(o[r][0], o[r][1], o[r][2], o[r][3]);
+                dst[1] = make_float4(o[r][4], o[r][5], o[r][6], o[r][7]);
+            }
+            if ((sub & ((1 << REST) - 1)) == 0) ml_s[warp][own] = make_float2(m, l);
+        }
+        __syncthreads();
+        const bool final = stores_whole(part, c, n);
+        const size_t slot = slot_row(part, c);
+#pragma unroll 1
+        for (int e = threadIdx.x; e < R * D; e += kThreads) {
+            const int r = e / D, col = e % D;
+            const PagedRow row = paged_row(p, part, c, r);
+            if (!row.counts) continue;
+            float mr = -INFINITY, lr = 0.f, val = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mr = fmaxf(mr, ml_s[w][r].x);
+            const float base = mr == -INFINITY ? 0.f : mr;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 ml = ml_s[w][r];
+                const float f = exp2f(ml.x - base);
+                lr += ml.y * f;
+                val += o_s[w][e] * f;
+            }
+            if (final) {
+                const int hq = c.h * p.G + row.g;
+                if (p.sinks) {
+                    const float sink = p.sinks[hq] * kLog2e, top = fmaxf(mr, sink), f = exp2f(mr - top);
+                    lr = lr * f + exp2f(sink - top);
+                    val *= f;
+                    mr = top;
+                }
+                static_cast<float *>(p.out)[(((size_t)row.b * p.Lq + row.i) * p.Hq + hq) * D + col] =
+                    lr == 0.f ? 0.f : val / lr;
+                if (col == 0)
+                    p.lse[((size_t)row.b * p.Hq + hq) * p.Lq + row.i] = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * kLn2;
+            } else {
+                part.o[(slot + r) * D + col] = val;
+                if (col == 0) *reinterpret_cast<float2 *>(part.ml + (slot + r) * 2) = make_float2(mr, lr);
+            }
         }
         if (!cursor_next(p, part, c, n)) break;
+        __syncthreads(); // o_s and ml_s are free again
     }
     await_previous();
 }
@@ -193,11 +271,16 @@ __global__ void __launch_bounds__(kThreads)
 
 cudaError_t launch_paged_f32(const PagedProblem &p, const PagedPart &part, int cache_dtype, cudaStream_t s)
 {
-    auto go = [&](auto kern) {
-        return launch_dependent(kern, (unsigned)part.ctas, kThreads, 0, s, p, part);
+    auto go = [&](auto kern) { return launch_dependent(kern, (unsigned)part.ctas, kThreads, 0, s, p, part); };
+    auto sized = [&](auto d, auto fp8) {
+        constexpr int D = decltype(d)::value;
+        constexpr bool FP8 = decltype(fp8)::value;
+        return part.row_block == 4 ? go(paged_f32_kernel<D, FP8, 4>) : go(paged_f32_kernel<D, FP8, 8>);
     };
-    if (cache_dtype == RA_E4M3) return p.c.D == 64 ? go(paged_f32_kernel<64, true>) : go(paged_f32_kernel<128, true>);
-    return p.c.D == 64 ? go(paged_f32_kernel<64, false>) : go(paged_f32_kernel<128, false>);
+    auto typed = [&](auto fp8) {
+        return p.c.D == 64 ? sized(std::integral_constant<int, 64>{}, fp8) : sized(std::integral_constant<int, 128>{}, fp8);
+    };
+    return cache_dtype == RA_E4M3 ? typed(std::true_type{}) : typed(std::false_type{});
 }
 
 } // namespace ra

@@ -81,8 +81,8 @@ cudaError_t launch_kv_read(const PagedCache &c, int cache_dtype, const int32_t *
                            int max_pages, const int32_t *kv_len, int B, int L, void *k, void *v,
                            int dtype, int *status, cudaStream_t s);
 
-// fp32 arithmetic throughout: the path of fp32 queries
-constexpr int kPagedF32Rows = 8, kPagedF32Tile = 32;
+// fp32 arithmetic throughout: the path of fp32 queries, row_block 4 or 8
+constexpr int kPagedF32Tile = 64;
 cudaError_t launch_paged_f32(const PagedProblem &p, const PagedPart &part, int cache_dtype,
                              cudaStream_t s);
 

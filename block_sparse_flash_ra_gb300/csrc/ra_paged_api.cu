@@ -144,9 +144,9 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
         if (p->dtype == RA_FP32) {
             kernel = kF32;
             a.seg_cost = 1;
-            a.row_block = kPagedF32Rows;
+            a.row_block = a.rows <= 4 ? 4 : 8;
             a.tile = kPagedF32Tile;
-            a.ctas = 4 * kSms;
+            a.ctas = (a.row_block == 4 ? 4 : 2) * kSms;
         } else if (c->D == 128 && a.rows > 32) {
             kernel = kRowsM;
             a.seg_cost = 5;
