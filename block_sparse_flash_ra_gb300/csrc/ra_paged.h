@@ -83,6 +83,7 @@ cudaError_t launch_kv_read(const PagedCache &c, int cache_dtype, const int32_t *
 
 // fp32 arithmetic throughout: the path of fp32 queries, row_block 4 or 8
 constexpr int kPagedF32Tile = 64;
+constexpr int paged_f32_per_sm(int row_block, bool e4m3) { return row_block == 8 ? 2 : e4m3 ? 4 : 3; }
 cudaError_t launch_paged_f32(const PagedProblem &p, const PagedPart &part, int cache_dtype,
                              cudaStream_t s);
 

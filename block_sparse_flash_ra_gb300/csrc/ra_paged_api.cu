@@ -146,7 +146,7 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
             a.seg_cost = 1;
             a.row_block = a.rows <= 4 ? 4 : 8;
             a.tile = kPagedF32Tile;
-            a.ctas = (a.row_block == 4 ? 4 : 2) * kSms;
+            a.ctas = paged_f32_per_sm(a.row_block, c->dtype == RA_E4M3) * kSms;
         } else if (c->D == 128 && a.rows > 32) {
             kernel = kRowsM;
             a.seg_cost = 5;
