@@ -13,6 +13,11 @@
 // would be padded to 128; mma.sync.m16n8k16 measured 32 cycles each per
 // sub-core, and a kernel on it stopped at 46% of memory speed.)
 //
+// Measured (e4m3, 8 kv heads of 128, 32 query heads): 64 sequences of 17 to
+// 8192 tokens 89 us, 6.1 TB/s, 90% of a copy's rate; bf16, 64 x 8192 tokens
+// 307 us, all of it; 32 rows on 8 x 32K bf16 tokens 32 us, 60%, of which some
+// 13 us are the launches, the start, the end and the join.
+//
 // 8-bit caches run kind::f8f6f4 on the codes.  The other operand is split
 // into e4m3 terms, each in columns of its own, so that nothing is lost to it:
 //   q 2^-e = q1 + q2 / 16 (a bf16's 8 bits are two e4m3 significands; error
@@ -40,8 +45,9 @@
 //   one warp   issues the products, S(i + 1) before P(i) V(i)
 //   one warp   loads: a lane per page, K and V in rings of their own
 // A tile's softmax is a chain of a few hundred instructions in few warps, so
-// rows are spread over warpgroups (8 each) to keep it short, and up to 16 rows
-// of an 8-bit cache run two CTAs per SM, one's chain under the other's.
+// rows are spread over warpgroups (8 each) to keep it short, and up to 16
+// columns of an 8-bit cache run two CTAs per SM, one's chain under the other's
+// (64 x 4096 tokens: 89 us, 105 with one; 64 x up to 512: 20 and 26).
 #include <cuda_fp16.h>
 #include <math.h>
 

@@ -32,6 +32,12 @@
 // few-row kernel uses, has no room in a compute-bound loop.
 // 16-bit caches: the tiles go to the products as they are, P is bf16 (2^-8).
 // Logits, maxima, sums and O are fp32.
+//
+// Measured, 512 rows on each of 8 kv heads: a prefix of 131072 e4m3 tokens
+// 248 us, 60% of the bf16 rate (the softmax's exponents and conversions keep
+// the pipe waiting); of 32768 tokens 88 us, 43%: some 16K cycles to the first
+// product (set-up, the rows gathered, code fetched cold), 5K to store 128 KB of
+// partial results, and the join.
 #include <cuda_fp16.h>
 #include <math.h>
 

@@ -141,6 +141,10 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
         int &kernel = pl.kernel[pl.n_parts++];
         a.prefix = k;
         a.rows = (k ? p->B * p->Lq : p->Lq) * G;
+        // seg_cost, in tiles: with the line's shares weighted so, CTAs end
+        // together.  Taking up a segment (Q, the first maximum, the results)
+        // measured 2.8 us beside tiles of 0.7 us in the keys kernel, and 7 us
+        // beside tiles of 1.5 us in the rows kernel.
         if (p->dtype == RA_FP32) {
             kernel = kF32;
             a.seg_cost = 1;
@@ -148,6 +152,10 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
             a.tile = kPagedF32Tile;
             a.ctas = paged_f32_per_sm(a.row_block, c->dtype == RA_E4M3) * kSms;
         } else if (c->D == 128 && a.rows > 32) {
+            // against blocks of 32 rows of the keys kernel, 16 sequences of 8192
+            // tokens, 4 kv heads: e4m3 40 rows 68 us (keys 72), 64 rows 69 (72),
+            // 128 rows 74 (131); bf16 58 (94), 59 (95), 65 (164).  20 rows, 2 x 64K
+            // tokens: 44 us (keys 26).
             kernel = kRowsM;
             a.seg_cost = 5;
             a.row_block = 256;
@@ -157,6 +165,10 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
         } else {
             kernel = kKeysM;
             a.seg_cost = 4;
+            // The narrowest block that holds the rows: 20 rows on 2 x 64K e4m3
+            // tokens as one block of 32 26 us, as blocks of 16 28, of 8 30; 32 rows
+            // on 8 x 32K bf16 tokens 32, 35 and 52.  At D = 64 more rows go in
+            // blocks of 16, too.
             const int par = 128 / c->D; // columns of a query row
             const int cols = a.rows * par <= 8 ? 8 : a.rows * par <= 16 ? 16 : 32;
             a.row_block = cols / par;
