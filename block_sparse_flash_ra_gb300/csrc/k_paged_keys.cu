@@ -711,13 +711,24 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
                 mbar_arrive(bars.p_full + sb);
             }
             // ---- the segment's end: sums over the keys' threads
+            // (each step a lane hands half of its rows over: short code, and every
+            // lane busy; the segment's end is mostly fetched cold)
 #pragma unroll
-            for (int r = 0; r < kRT; ++r) {
-                float x = l[r];
+            for (int h = kRT / 2, w = 16; h; h >>= 1, w >>= 1) {
+                const bool up = (lane & w) != 0;
 #pragma unroll
-                for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                if (lane == 0) red[wq * RS + r] = x;
-                if (tid == 0) row_f[row0 + r] = m[r];
+                for (int r = 0; r < h; ++r) {
+                    const float x = up ? l[r] : l[r + h];
+                    l[r] = (up ? l[r + h] : l[r]) + __shfl_xor_sync(0xffffffffu, x, w);
+                }
+            }
+            l[0] += __shfl_xor_sync(0xffffffffu, l[0], 2);
+            l[0] += __shfl_xor_sync(0xffffffffu, l[0], 1);
+            if ((lane & 3) == 0) red[wq * RS + (lane >> 2)] = l[0];
+            if (tid == 0) {
+                float4 *f4 = reinterpret_cast<float4 *>(row_f + row0);
+                f4[0] = make_float4(m[0], m[1], m[2], m[3]);
+                f4[1] = make_float4(m[4], m[5], m[6], m[7]);
             }
             soft_sync<NT>();
             const bool final = stores_whole(part, c, n);
