@@ -425,9 +425,9 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _ints(x, shape, name, device):
+def _ints(x, shape, name, index):
     """int32 tensors that the kernels read: dense, on the cache's device."""
-    if x.dtype is torch.int32 and x.shape == shape and x.device == device and x.is_contiguous():
+    if x.dtype is torch.int32 and x.shape == shape and x.get_device() == index and x.is_contiguous():
         return
     if x.dtype != torch.int32:
         raise TypeError(f"{name} must be int32, not {x.dtype}")
@@ -435,12 +435,15 @@ def _ints(x, shape, name, device):
     raise ValueError(f"{name} must be contiguous and on the cache's device")
 
 
+def _here(index):
+    """Whether device `index` is the current one.  The helpers then call with the handle of its
+    current stream, and no Stream object around it: a small call's time is mostly Python's."""
+    return index == torch._C._cuda_getDevice()
+
+
 def _on(device, stream, run, *args):
     """run(*args, handle of the stream) on the tensors' device and on the caller's stream,
     allocations included, so that what is allocated is reused in that stream's order."""
-    if stream is None and device.index == torch._C._cuda_getDevice():
-        # the handle without a Stream object around it: a small call's time is mostly Python's
-        return run(*args, torch._C._cuda_getCurrentRawStream(device.index))
     with torch.cuda.device(device):
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
@@ -468,6 +471,7 @@ def make_kv_cache(k, v, k_exp=None, v_exp=None) -> RaKvCache:
     n, h, page, d = k.shape
     c = RaKvCache(n, page, h, d, _CACHE_DT[k.dtype], _ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp))
     c.k_pages, c.v_pages, c.k_exps, c.v_exps, c.device = k, v, k_exp, v_exp, k.device
+    c._index = k.get_device()
     c._row = (h, d)
     c._sizes = (n, page, h, d, c.dtype)
     c._ref = ctypes.addressof(c)
@@ -507,25 +511,31 @@ def kv_write(cache, k, v, page_table, start, count=None, stream=None) -> None:
     dt = _DT.get(k.dtype)
     if dt is None or v.dtype != k.dtype:
         raise TypeError(f"k and v must both be bfloat16 or float32, not {k.dtype} and {v.dtype}")
-    shape, dev = k.shape, cache.device
+    shape, index = k.shape, cache._index
     if not (len(shape) == 4 and v.shape == shape and shape[2:] == cache._row):
         raise ValueError(f"k and v must be (B, L, {cache.Hkv}, {cache.D}), of the same shape")
-    _need(k.device == dev and v.device == dev, "k and v must be on the cache's device")
+    if k.get_device() != index or v.get_device() != index:
+        raise ValueError("k and v must be on the cache's device")
     strides = k.stride()
     ks = vs = _token_stride(shape, strides, "k")
     if v.stride() != strides:
         vs = _token_stride(shape, v.stride(), "v")
-    B, L = shape[:2]
+    B, L, _, _ = shape
     if B == 0 or L == 0:
         return
     pages = page_table.shape[-1]
-    _ints(page_table, (B, pages), "page_table", dev)
-    _ints(start, (B,), "start", dev)
+    _ints(page_table, (B, pages), "page_table", index)
+    _ints(start, (B,), "start", index)
     if count is not None:
-        _ints(count, (B,), "count", dev)
-    _check(_on(dev, stream, lib().ra_kv_write, cache._ref, k.data_ptr(), v.data_ptr(), dt, B, L, ks,
-               vs, page_table.data_ptr(), pages, start.data_ptr(),
-               None if count is None else count.data_ptr()))
+        _ints(count, (B,), "count", index)
+    args = (cache._ref, k.data_ptr(), v.data_ptr(), dt, B, L, ks, vs, page_table.data_ptr(), pages,
+            start.data_ptr(), None if count is None else count.data_ptr())
+    if stream is None and _here(index):
+        rc = lib().ra_kv_write(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        rc = _on(cache.device, stream, lib().ra_kv_write, *args)
+    if rc:
+        _check(rc)
 
 
 def _kv_read(cache, page_table, pages, kv_len, B, L, dtype, dt, s):
@@ -542,11 +552,13 @@ def kv_read(cache, page_table, kv_len, L, dtype=torch.bfloat16, stream=None):
     dt = _DT.get(dtype)
     if dt is None:
         raise TypeError(f"unsupported dtype {dtype}")
-    dev, (B, pages) = cache.device, page_table.shape
-    _ints(page_table, (B, pages), "page_table", dev)
-    _ints(kv_len, (B,), "kv_len", dev)
-
-    return _on(dev, stream, _kv_read, cache, page_table, pages, kv_len, B, L, dtype, dt)
+    index, (B, pages) = cache._index, page_table.shape
+    _ints(page_table, (B, pages), "page_table", index)
+    _ints(kv_len, (B,), "kv_len", index)
+    args = cache, page_table, pages, kv_len, B, L, dtype, dt
+    if stream is None and _here(index):
+        return _kv_read(*args, torch._C._cuda_getCurrentRawStream(index))
+    return _on(cache.device, stream, _kv_read, *args)
 
 
 def make_paged_params(cache, q, page_table, kv_len, *, scale, causal=True, soft_cap=0.0, q_len=None,
@@ -559,15 +571,15 @@ def make_paged_params(cache, q, page_table, kv_len, *, scale, causal=True, soft_
     _need(q.dim() == 4 and q.shape[3] == cache.D, f"q must be (B, Lq, Hq, {cache.D})")
     B, Lq, Hq, _ = q.shape
     dev = cache.device
-    _ints(page_table, (B, page_table.shape[-1]), "page_table", dev)
-    _ints(kv_len, (B,), "kv_len", dev)
+    _ints(page_table, (B, page_table.shape[-1]), "page_table", cache._index)
+    _ints(kv_len, (B,), "kv_len", cache._index)
     if q_len is not None:
-        _ints(q_len, (B,), "q_len", dev)
+        _ints(q_len, (B,), "q_len", cache._index)
     _need((prefix_table is None) == (prefix_len is None),
           "prefix_table and prefix_len must come together")
     if prefix_table is not None:
-        _ints(prefix_table, (prefix_table.shape[-1],), "prefix_table", dev)
-        _ints(prefix_len, (1,), "prefix_len", dev)
+        _ints(prefix_table, (prefix_table.shape[-1],), "prefix_table", cache._index)
+        _ints(prefix_len, (1,), "prefix_len", cache._index)
     if sinks is not None:
         if sinks.dtype != torch.float32:
             raise TypeError(f"sinks must be float32, not {sinks.dtype}")
@@ -598,8 +610,10 @@ def _paged_forward(params, q, cache, out, lse, ws, s):
             w = torch.UntypedStorage(n, device=dev)
         else:
             w, n = ws, _wsb(ws)
-        _check(lib().ra_attn_paged(cache._ref, params._ref, q.data_ptr(), out.data_ptr(),
-                                   lse.data_ptr(), w.data_ptr(), n, s))
+        rc = lib().ra_attn_paged(cache._ref, params._ref, q.data_ptr(), out.data_ptr(),
+                                 lse.data_ptr(), w.data_ptr(), n, s)
+        if rc:
+            _check(rc)
     return out, lse
 
 
@@ -608,17 +622,22 @@ def paged_forward(params, q, cache, out=None, lse=None, ws=None, stream=None):
     Given ``out`` / ``lse`` are written in place (rows behind q_len stay as they are); ``ws``: a
     workspace to use instead of a new one, uint8, of ra_attn_paged_workspace_size elements.
     For serving: no gradient is recorded."""
-    dev = cache.device
-    _need((q.shape, q.dtype) == params._like and q.is_contiguous(),
-          "q must be contiguous, of the shape and dtype the params were made for")
-    _need(cache._sizes == params._cache, "the params were made for a cache of other sizes")
-    _need(q.device == dev, "q must be on the cache's device")
-    if out is not None:
-        _need((out.shape, out.dtype) == params._like and out.device == dev and out.is_contiguous(),
-              "out must be like q")
-    if lse is not None:
-        _need(lse.shape == params._lse and lse.dtype is torch.float32 and lse.device == dev
-              and lse.is_contiguous(), "lse must be (B, Hq, Lq) fp32")
-    if ws is not None:
-        _need(ws.device == dev and ws.is_contiguous(), "ws must be contiguous and on the cache's device")
-    return _on(dev, stream, _paged_forward, params, q, cache, out, lse, ws)
+    index, like = cache._index, params._like
+    if (q.shape, q.dtype) != like or not q.is_contiguous():
+        raise ValueError("q must be contiguous, of the shape and dtype the params were made for")
+    if cache._sizes != params._cache:
+        raise ValueError("the params were made for a cache of other sizes")
+    if q.get_device() != index:
+        raise ValueError("q must be on the cache's device")
+    if out is not None and not ((out.shape, out.dtype) == like and out.get_device() == index
+                                and out.is_contiguous()):
+        raise ValueError("out must be like q")
+    if lse is not None and not (lse.shape == params._lse and lse.dtype is torch.float32
+                                and lse.get_device() == index and lse.is_contiguous()):
+        raise ValueError("lse must be (B, Hq, Lq) fp32")
+    if ws is not None and not (ws.get_device() == index and ws.is_contiguous()):
+        raise ValueError("ws must be contiguous and on the cache's device")
+    if stream is None and _here(index):
+        return _paged_forward(params, q, cache, out, lse, ws,
+                              torch._C._cuda_getCurrentRawStream(index))
+    return _on(cache.device, stream, _paged_forward, params, q, cache, out, lse, ws)
