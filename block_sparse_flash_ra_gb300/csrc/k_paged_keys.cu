@@ -75,9 +75,9 @@ struct Cfg {
     static constexpr int kMmaWarp = 4 * kGroups, kLoadWarp = kMmaWarp + 1;
     static constexpr int kCtasPerSm = FP8 && RP <= 16 ? 2 : 1;
     static constexpr int kStages = FP8 ? (RP == 8 ? 3 : RP == 16 ? 2 : 5) : 3;
-    static constexpr int kVStages = FP8 ? (RP == 32 ? 5 : 3) : RP == 32 ? 2 : 3;
+    static constexpr int kVStages = FP8 ? (RP > 16 ? 5 : 3) : RP > 16 ? 2 : 3;
     static constexpr int kQTerms = FP8 ? 2 : 1, kPTerms = FP8 ? 3 : 2;
-    static constexpr int kNS = RP * kQTerms < 16 ? 16 : RP * kQTerms;     // columns of S^T
+    static constexpr int kNS = (RP * kQTerms + 15) / 16 * 16;             // columns of S^T
     static constexpr int kNO = (RP * kPTerms + 15) / 16 * 16;             // columns of O^T
     static constexpr int kQBytes = kNS * kD * (FP8 ? 1 : 2);
     static constexpr int kPBytes = kNO * kKeys * (FP8 ? 1 : 2);
@@ -837,6 +837,7 @@ cudaError_t launch_paged_keys(const PagedProblem &p, const PagedPart &part, int 
         constexpr int D = decltype(d)::value;
         return cols == 8    ? go<FP8, 8, D>(p, part, k, v, s)
                : cols == 16 ? go<FP8, 16, D>(p, part, k, v, s)
+               : cols == 24 ? go<FP8, 24, D>(p, part, k, v, s)
                             : go<FP8, 32, D>(p, part, k, v, s);
     };
     auto sized = [&](auto fp8) {

@@ -166,11 +166,11 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
             kernel = kKeysM;
             a.seg_cost = 4;
             // The narrowest block that holds the rows: 20 rows on 2 x 64K e4m3
-            // tokens as one block of 32 26 us, as blocks of 16 28, of 8 30; 32 rows
-            // on 8 x 32K bf16 tokens 32, 35 and 52.  At D = 64 more rows go in
-            // blocks of 16, too.
+            // tokens as one block of 24 24 us, of 32 26, as blocks of 16 28, of 8
+            // 30; 32 rows on 8 x 32K bf16 tokens 32 us, in 16s 35, in 8s 52.  At
+            // D = 64 more rows go in blocks of 16, too.
             const int par = 128 / c->D; // columns of a query row
-            const int cols = a.rows * par <= 8 ? 8 : a.rows * par <= 16 ? 16 : 32;
+            const int cols = a.rows * par >= 32 ? 32 : (a.rows * par + 7) / 8 * 8;
             a.row_block = cols / par;
             a.tile = kPagedKeysTile * par;
             a.ctas = (c->dtype == RA_E4M3 && cols <= 16 ? 2 : 1) * kSms;

@@ -280,6 +280,8 @@ CASES = {
     "many_short": dict(lens=[(37 * b) % 91 for b in range(150)], Hq=4),
     # several segments to a CTA, for each size of row block; blocks of one tile and of two
     "many_short_16": dict(lens=[(37 * b) % 91 for b in range(330)], Hq=16, Hkv=1),
+    "many_short_24": dict(lens=[(29 * b) % 140 for b in range(330)], Hq=24, Hkv=1, page=32),
+    "many_short_12_d64": dict(lens=[(29 * b) % 280 for b in range(330)], Hq=12, Hkv=1, D=64, page=32),
     "many_short_32": dict(lens=[(31 * b) % 140 for b in range(330)], Hq=32, Hkv=1, page=32),
     "many_short_64": dict(lens=[(37 * b) % 191 for b in range(200)], Hq=8, Lq=16),
     "many_short_200": dict(lens=[60 + (37 * b) % 91 for b in range(110)], Hq=8, Lq=50),
@@ -368,8 +370,9 @@ def test_large_logits_keep_their_weights():
 
 
 # heads, kv heads, query tokens and head size of a call that each kernel takes: rows per kv head decide
-KERNELS = {"d64": (4, 1, 1, 64), "d64_8": (8, 1, 1, 64), "d64_16": (16, 1, 1, 64), "d64_80": (8, 1, 10, 64), "rows8": (2, 1, 1, 128), "rows16": (16, 1, 1, 128), "rows32": (32, 1, 1, 128),
-           "rows80": (8, 1, 10, 128), "rows320": (8, 1, 40, 128)}
+KERNELS = {"d64": (4, 1, 1, 64), "d64_8": (8, 1, 1, 64), "d64_12": (12, 1, 1, 64), "d64_16": (16, 1, 1, 64),
+           "d64_80": (8, 1, 10, 64), "rows8": (2, 1, 1, 128), "rows16": (16, 1, 1, 128), "rows20": (20, 1, 1, 128),
+           "rows32": (32, 1, 1, 128), "rows80": (8, 1, 10, 128), "rows320": (8, 1, 40, 128)}
 each_kernel = pytest.mark.parametrize("name", KERNELS)
 each_cache = pytest.mark.parametrize("cache", [F8, torch.bfloat16], ids=["e4m3", "c16"])
 each_type = pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
