@@ -15,8 +15,9 @@
 //
 // Measured (e4m3, 8 kv heads of 128, 32 query heads): 64 sequences of 17 to
 // 8192 tokens 89 us, 6.1 TB/s, 90% of a copy's rate; bf16, 64 x 8192 tokens
-// 307 us, all of it; 32 rows on 8 x 32K bf16 tokens 32 us, 60%, of which some
-// 13 us are the launches, the start, the end and the join.
+// 307 us, all of it; 32 rows on 8 x 32K bf16 tokens 31 us, 61%, of which some
+// 13 us are the launches, the start, the end and the join.  From 24 columns on
+// the softmax's issue shows: 20 rows on 64 x 1000-3000 e4m3 tokens 75 us, 53%.
 //
 // 8-bit caches run kind::f8f6f4 on the codes.  The other operand is split
 // into e4m3 terms, each in columns of its own, so that nothing is lost to it:
