@@ -459,81 +459,72 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
             return r;
         };
         // Q of the segment at `at`, number `par` of the CTA: 16 threads take a
-        // row, 8 values each.  The loads are issued a segment ahead, and what they
-        // brought is stored when the present segment's tiles are done, so that the
-        // next S can be computed beside its end.  (The segment before last, whose
-        // place it takes, has all its S behind it.)
-        const int qr = threadIdx.x >> 4, qx = threadIdx.x & 15;
-        auto fetch_q = [&](const PagedCursor &at, uint32_t par) {
+        // row, 8 values each.  It is fetched a segment ahead; the segment before
+        // last, whose place it takes, has all its S behind it.
+        auto load_q = [&](const PagedCursor &at, uint32_t par) {
             const Rows ri = rows_of(par);
-            const PagedRow row = paged_row(p, part, at, qr / kPar);
-            const int hq = at.h * p.G + row.g;
-            const long long place = ((long long)row.b * p.Lq + row.i) * p.Hq + hq;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (row.counts && (kPar == 1 || (qx >> 3) == (qr & 1)))
-                w = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + (size_t)place * D + (qx & (D / 8 - 1)) * 8);
-            if (qx == 0) {
-                ri.limit[qr] = row.counts ? row.limit : 0x7fffffff; // rows of no use need no mask
-                ri.place[qr] = row.counts ? place : -1;
-                ri.lse[qr] = ((long long)row.b * p.Hq + hq) * p.Lq + row.i;
-            }
-            return w;
-        };
-        auto put_q = [&](uint4 w, uint32_t par) {
             const uint32_t q_base = smem_u32(smem + C::kQOff + (par & 1) * C::kQBytes);
-            float qs = p.scale * kLog2e;
-            if (FP8) {
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                uint32_t top = 0; // largest magnitude, as bf16 bits
+#pragma unroll 1
+            for (int r = threadIdx.x >> 4; r < C::kNS / C::kQTerms; r += NT / 16) {
+                const int x = threadIdx.x & 15;
+                const PagedRow row = paged_row(p, part, at, r / kPar);
+                const bool live = r < RP && row.counts;
+                const int hq = at.h * p.G + row.g;
+                const long long place = ((long long)row.b * p.Lq + row.i) * p.Hq + hq;
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (live && (kPar == 1 || (x >> 3) == (r & 1)))
+                    w = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + (size_t)place * D + (x & (D / 8 - 1)) * 8);
+                float qs = p.scale * kLog2e;
+                if (FP8) {
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t top = 0; // largest magnitude, as bf16 bits
 #pragma unroll
-                for (int y = 0; y < 4; ++y) top = max(top, max(u[y] & 0x7fffu, (u[y] >> 16) & 0x7fffu));
+                    for (int y = 0; y < 4; ++y) top = max(top, max(u[y] & 0x7fffu, (u[y] >> 16) & 0x7fffu));
 #pragma unroll
-                for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                // the maximum goes to [128, 256); 2^+-e stay normal
-                const int e = min(max((int)(top >> 7) - 134, -120), 120);
-                const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-                qs *= __uint_as_float((uint32_t)(127 + e) << 23);
-                if (top >= 0x7f80u) qs = __uint_as_float(0x7fc00000u); // e4m3 has no infinity
-                uint32_t hi[4], lo[4];
+                    for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    // the maximum goes to [128, 256); 2^+-e stay normal
+                    const int e = min(max((int)(top >> 7) - 134, -120), 120);
+                    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+                    qs *= __uint_as_float((uint32_t)(127 + e) << 23);
+                    if (top >= 0x7f80u) qs = __uint_as_float(0x7fc00000u); // e4m3 has no infinity
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    // f16 holds the 8 bits; below 2^-14 it rounds at 2^-25
-                    const __half2 q2 = __floats2half2_rn(__uint_as_float(u[y] << 16) * inv,
-                                                         __uint_as_float(u[y] & 0xffff0000u) * inv);
-                    hi[y] = to_codes(q2);
-                    lo[y] = to_codes(__hmul2(__hsub2(q2, from_codes(hi[y])), __float2half2_rn(16.f)));
+                    for (int y = 0; y < 4; ++y) {
+                        // f16 holds the 8 bits; below 2^-14 it rounds at 2^-25
+                        const __half2 q2 = __floats2half2_rn(__uint_as_float(u[y] << 16) * inv,
+                                                             __uint_as_float(u[y] & 0xffff0000u) * inv);
+                        hi[y] = to_codes(q2);
+                        lo[y] = to_codes(__hmul2(__hsub2(q2, from_codes(hi[y])), __float2half2_rn(16.f)));
+                    }
+                    const uint32_t dst = q_base + (((x >> 1) ^ (r & 7)) << 4) + (x & 1) * 8;
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst + r * 128), "r"(hi[0] | hi[1] << 16),
+                                 "r"(hi[2] | hi[3] << 16)
+                                 : "memory");
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst + (RP + r) * 128), "r"(lo[0] | lo[1] << 16),
+                                 "r"(lo[2] | lo[3] << 16)
+                                 : "memory");
+                } else {
+                    const uint32_t dst = q_base + (x >> 3) * (C::kNS * 128) + r * 128 +
+                                        (((x & 7) ^ (r & 7)) << 4);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
+                                 : "memory");
                 }
-                const uint32_t dst = q_base + (((qx >> 1) ^ (qr & 7)) << 4) + (qx & 1) * 8;
-                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst + qr * 128), "r"(hi[0] | hi[1] << 16),
-                             "r"(hi[2] | hi[3] << 16)
-                             : "memory");
-                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst + (RP + qr) * 128), "r"(lo[0] | lo[1] << 16),
-                             "r"(lo[2] | lo[3] << 16)
-                             : "memory");
-            } else {
-                const uint32_t dst = q_base + (qx >> 3) * (C::kNS * 128) + qr * 128 +
-                                    (((qx & 7) ^ (qr & 7)) << 4);
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
-                             : "memory");
+                if (x == 0 && r < RP) {
+                    ri.qs[r] = qs;
+                    ri.limit[r] = live ? row.limit : 0x7fffffff; // rows of no use need no mask
+                    ri.place[r] = live ? place : -1;
+                    ri.lse[r] = ((long long)row.b * p.Hq + hq) * p.Lq + row.i;
+                }
             }
-            if (qx == 0) rows_of(par).qs[qr] = qs;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             mbar_arrive(bars.q_full + (par & 1));
         };
-        constexpr int kFill = C::kNS / C::kQTerms - RP; // rows that only fill S's columns up (bf16)
-        if constexpr (kFill > 0) {
-            for (int e = threadIdx.x; e < 2 * C::kHalves * kFill * 8; e += NT) {
-                const int row = RP + (e >> 3) % kFill, block = (e >> 3) / kFill; // of 128 bytes by kNS rows
-                *reinterpret_cast<uint4 *>(smem + C::kQOff + (block * C::kNS + row) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-        }
-        put_q(fetch_q(c, 0), 0);
+        load_q(c, 0);
         for (uint32_t seg = 0;; ++seg) {
             const int n = cursor_take(c), len = source_len(c.b);
             PagedCursor next = c;
             const bool more = cursor_next(p, part, next, n);
-            uint4 next_q = make_uint4(0, 0, 0, 0);
-            if (more) next_q = fetch_q(next, seg + 1);
+            if (more) load_q(next, seg + 1);
             const Rows rows = rows_of(seg);
             soft_sync<NT>();
             float qs[kRT];
@@ -720,7 +711,6 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_arrive(bars.p_full + sb);
             }
-            if (more) put_q(next_q, seg + 1);
             // ---- the segment's end: sums over the keys' threads
             // (each step a lane hands half of its rows over: short code, and every
             // lane busy; the segment's end is mostly fetched cold)
