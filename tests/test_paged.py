@@ -286,6 +286,9 @@ CASES = {
     "many_short_64": dict(lens=[(37 * b) % 191 for b in range(200)], Hq=8, Lq=16),
     "many_short_200": dict(lens=[60 + (37 * b) % 91 for b in range(110)], Hq=8, Lq=50),
     "many_short_d64": dict(lens=[(37 * b) % 91 for b in range(200)], Hq=24, Hkv=2, D=64),
+    "many_700": dict(lens=[(37 * b) % 23 for b in range(700)], Hq=2, Hkv=1),
+    "many_behind_a_prefix": dict(lens=[(37 * b) % 23 for b in range(300)], Hq=2, Hkv=1, prefix=100, q_len=[b % 2 for b in range(300)]),
+    "many_few_rows": dict(lens=[(37 * b) % 23 for b in range(140)], Hq=1, Hkv=1, D=64, sinks=True),
     "long_40_rows": dict(lens=[3100, 2500, 1], Hq=8, Lq=10, page=128),
     "draft": dict(lens=[70, 3, 129, 0], Hq=4, Lq=5),
     "draft_full": dict(lens=[70, 3, 129], Hq=4, Lq=3, causal=False),
