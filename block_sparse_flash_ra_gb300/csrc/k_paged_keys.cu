@@ -644,6 +644,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
                             tmem_st8(lane_base + C::kColO + k * RP + row0, w);
                         }
                         tmem_st_wait();
+                        tc_fence_before(); // O is written before p_full lets the next P V at it
                     }
                     group_sync(bar); // red is free again
                 }
