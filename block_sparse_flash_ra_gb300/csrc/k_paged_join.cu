@@ -64,10 +64,10 @@ __device__ __forceinline__ Slots find_slots(const PagedProblem &p, const PagedPa
     }
     Slots s{0, seg, 0, n - rb * part.row_block, false};
     if (tiles == 0) return s;
-    const unsigned share = (total + part.ctas - 1) / part.ctas;
+    const unsigned share = max((total + part.ctas - 1) / part.ctas, 1u);
     const unsigned first = start + part.seg_cost; // place of the first tile
-    s.c0 = first / share;
-    s.n = (int)((first + tiles - 1) / share - s.c0) + 1;
+    s.c0 = min(first / share, part.ctas - 1u);
+    s.n = (int)(min((first + tiles - 1) / share, part.ctas - 1u) - s.c0) + 1;
     // a share that begins before `start` begins with another segment's tile
     s.opens = start <= s.c0 * share;
     return s;

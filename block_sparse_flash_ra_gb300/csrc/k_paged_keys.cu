@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
             int next = entry(c.t0, len);
             for (int t = c.t0; ok && t < c.t0 + n; ++t, ++i) {
                 const int page = next, first = t * kTokens;
-                const int boxes = (min(len - first, kTokens) + box * kPar - 1) / (box * kPar);
+                const int boxes = max(0, (min(len - first, kTokens) + box * kPar - 1) / (box * kPar));
                 if (t + 1 < c.t0 + n) next = entry(t + 1, len);
                 const bool mine = lane < boxes;
                 const bool good = mine && page_valid(p, page);
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
                     // an odd length ends inside a row: its other token meets the zeros of
                     // Q, and is made zero too, whatever is there
                     const int valid = len - (c.t0 + t) * kTokens, j = valid >> 1;
-                    if (valid < kTokens && (valid & 1)) {
+                    if (valid > 0 && valid < kTokens && (valid & 1)) {
                         if (lane < C::kHalves * 4)
                             asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
                                              smem_u32(smem + C::kKOff + sk * C::kMat) + tile_chunk(j, C::kHalves * 4 + lane)),

@@ -9,7 +9,9 @@
 // and then its tiles, and CTA c of C takes the c-th share of ceil(N / C)
 // places.  Shares cost about the same whatever the lengths are, and lengths
 // stay on the device: every CTA adds up the lengths of the batch itself (B
-// integers out of L2) to find where its share begins.
+// integers out of L2) to find where its share begins.  They must not change
+// while a call runs, but every loop here ends, and every index stays in
+// bounds, if they do.
 //
 // Partial results.  Where whole segments are stored by the CTA that has them
 // (`direct`), a CTA leaves at most two partial results, of the first and the
@@ -155,6 +157,7 @@ __device__ __forceinline__ bool cursor_begin(const PagedProblem &p, const PagedP
         // 32 sequences at a time: the first whose running total passes `at`
 #pragma unroll 1
         for (int b0 = 0;; b0 += 32) {
+            if (b0 >= p.B) return false; // lengths that shrink meanwhile
             const int b = b0 + lane;
             const int n = b0 == 0 ? first32 : b < p.B ? own_places(p, part, b) : 0;
             unsigned run = n * per_seq;
@@ -207,7 +210,7 @@ __device__ __forceinline__ bool cursor_next(const PagedProblem &p, const PagedPa
         if (++c.rb == part.n_rb) {
             c.rb = 0;
             do { // a share that goes on has a sequence with tiles ahead
-                ++c.b;
+                if (++c.b >= p.B) return false;
                 c.tiles = own_tiles(p, part, c.b);
                 if (!c.tiles) c.seg += part.n_rb * p.c.Hkv;
             } while (!c.tiles);

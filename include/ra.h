@@ -536,7 +536,8 @@ RA_API int ra_kv_read(const ra_kv_cache *cache, const int32_t *page_table, int m
  *                 [0, prefix_pages * page_size].  The prefix precedes every
  *                 sequence's own tokens; every query sees all of it.
  * Every length and table is read on the device when the kernels run, so a
- * captured graph serves sequences that grow.  A page number outside
+ * captured graph serves sequences that grow; they must not change while the
+ * kernels of a call run.  A page number outside
  * [0, n_pages) or a length that had to be clamped is reported by
  * ra_get_device_status (RA_ERR_INVALID_ARG); the keys of such a page read as 0.
  */
