@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, paged_f32_per_sm(R, FP8))
             // ---- weights
 #pragma unroll
             for (int w = LANES; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(ALL, top, w));
-            const float m_new = fmaxf(m, top), base = m_new == -INFINITY ? 0.f : m_new;
+            const float m_new = fmaxf(m, top), base = finite_base(m_new);
             if (__any_sync(ALL, m_new != m)) {
                 const float f = exp2f(m - base);
                 l *= f;
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, paged_f32_per_sm(R, FP8))
             float mr = -INFINITY, lr = 0.f, val = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) mr = fmaxf(mr, ml_s[w][r].x);
-            const float base = mr == -INFINITY ? 0.f : mr;
+            const float base = finite_base(mr);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float2 ml = ml_s[w][r];
@@ -254,10 +254,10 @@ __global__ void __launch_bounds__(kThreads, paged_f32_per_sm(R, FP8))
             if (final) {
                 const int hq = c.h * p.G + row.g;
                 if (p.sinks) {
-                    const float sink = p.sinks[hq] * kLog2e, top = fmaxf(mr, sink), f = exp2f(mr - top);
-                    lr = lr * f + exp2f(sink - top);
+                    const float sink = p.sinks[hq] * kLog2e, with = finite_base(fmaxf(mr, sink)), f = exp2f(mr - with);
+                    lr = lr * f + exp2f(sink - with);
                     val *= f;
-                    mr = top;
+                    mr = with;
                 }
                 static_cast<float *>(p.out)[(((size_t)row.b * p.Lq + row.i) * p.Hq + hq) * D + col] =
                     lr == 0.f ? 0.f : val / lr;

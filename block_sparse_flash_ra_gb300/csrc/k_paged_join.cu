@@ -95,7 +95,7 @@ __device__ __forceinline__ void add_slots(const PagedPart &part, const Slots &s,
         const size_t at = part.by_groups ? (slot * (D / 4) + grp) * part.slot_rows + s.row
                                          : (slot * part.slot_rows + s.row) * (D / 4) + grp;
         const float4 v = reinterpret_cast<const float4 *>(part.o)[at];
-        const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.f : top;
+        const float top = fmaxf(m, ml.x), base = finite_base(top);
         const float f = ex2_approx(m - base), fx = ex2_approx(ml.x - base);
         l = l * f + ml.y * fx;
         o = make_float4(o.x * f + v.x * fx, o.y * f + v.y * fx, o.z * f + v.z * fx, o.w * f + v.w * fx);
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(PagedProblem p, Pa
         float top = m;
 #pragma unroll
         for (int x = 1; x < SPLIT; ++x) top = fmaxf(top, ml_s[x * ROWS + r].x);
-        const float base = top == -INFINITY ? 0.f : top, f = ex2_approx(m - base);
+        const float base = finite_base(top), f = ex2_approx(m - base);
         o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
         l *= f;
 #pragma unroll
@@ -191,10 +191,10 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(PagedProblem p, Pa
     if (place < 0) return;
     const int hq = place % p.Hq, bi = place / p.Hq;
     if (p.sinks) {
-        const float sink = p.sinks[hq] * kLog2e, top = fmaxf(m, sink), f = ex2_approx(m - top);
+        const float sink = p.sinks[hq] * kLog2e, base = finite_base(fmaxf(m, sink)), f = ex2_approx(m - base);
         o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-        l = l * f + ex2_approx(sink - top);
-        m = top;
+        l = l * f + ex2_approx(sink - base);
+        m = base;
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     store4(static_cast<T *>(p.out) + (size_t)place * D + grp * 4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));

@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sum += l2.x + l2.y;
                 };
                 auto keys32 = [&](auto masked_tag, int q) { // the thread's keys 32 q .. 32 q + 31
-                    const float nm = C::kPBias - (m == -INFINITY ? 0.f : m);
+                    const float nm = C::kPBias - finite_base(m);
                     sum = 0.f;
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
@@ -736,10 +736,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float f = FP8 ? __uint_as_float((uint32_t)ev << 23) : 1.f;
                 if (final) {
                     if (p.sinks && row.counts) {
-                        const float sink = p.sinks[hq] * kLog2e, top = fmaxf(mr, sink);
-                        f *= ex2_approx(mr - top);
-                        l = l * ex2_approx(mr - top) + ex2_approx(sink - top);
-                        mr = top;
+                        const float sink = p.sinks[hq] * kLog2e, with = finite_base(fmaxf(mr, sink)), old = ex2_approx(mr - with);
+                        f *= old;
+                        l = l * old + ex2_approx(sink - with);
+                        mr = with;
                     }
                     f = l == 0.f ? 0.f : f / l;
                 }

@@ -49,6 +49,10 @@ __device__ __forceinline__ float exp_byte_scale(uint32_t b)
     return __uint_as_float(b == 255u ? 0x7fc00000u : b == 0u ? 0x00400000u : b << 23);
 }
 
+// What a row's logits are taken relative to: their maximum, or 0 where nothing
+// is seen (and the sink is -inf), so that no difference is -inf - -inf.
+__device__ __forceinline__ float finite_base(float top) { return top == -INFINITY ? 0.f : top; }
+
 // tanh by its series, for |x| < kTanhSmall.
 __device__ __forceinline__ float tanh_series(float x)
 {

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import block_sparse_flash_ra_gb300 as ra
-from tests.test_paged import F8, Pool, each_cache
+from tests.test_paged import KERNELS, F8, Pool, check_attention, each_cache, each_kernel, each_type, queries
 
 gpu = pytest.mark.gpu
 
@@ -107,3 +107,29 @@ def test_references_that_rise_with_every_tile(name, cache):
     out, _ = forward(pool, q, scale)
     for b in (0, 1):
         assert errors(pool, b, q[b], out[b], scale, 2.0 ** -10) <= 1
+
+
+@gpu
+@each_type
+@each_cache
+@each_kernel
+def test_sinks_of_minus_infinity(name, cache, dtype):
+    """A head without a sink among heads that have one: as if it had none, for rows that see nothing too (out 0, lse -inf;
+    the others' lse is the sink)."""
+    Hq, Hkv, _, D = KERNELS[name]
+    sinks = torch.randn(Hq, generator=torch.Generator().manual_seed(70))
+    sinks[::2] = -math.inf
+    q = queries(name, 4, dtype, 71)
+    pool = Pool([0, 300, 1, 40], Hkv=Hkv, D=D, page=32, dtype=cache, seed=72)
+    check_attention(pool, q, sinks=sinks)
+    # with partial results joined: an empty prefix
+    kw = dict(scale=D ** -0.5, sinks=sinks.cuda())
+    p = ra.make_paged_params(pool.cache, q.cuda(), pool.table.cuda(), i32(pool.lens), **kw)
+    want, want_lse = ra.paged_forward(p, q.cuda(), pool.cache)
+    p = ra.make_paged_params(pool.cache, q.cuda(), pool.table.cuda(), i32(pool.lens), prefix_table=i32([0]), prefix_len=i32([0]), **kw)
+    got, lse = ra.paged_forward(p, q.cuda(), pool.cache)
+    dead = want_lse == -math.inf
+    assert dead.any() and torch.equal(lse[dead], want_lse[dead]) and (got.transpose(1, 2)[dead] == 0).all()
+    # the same partial results, joined or stored: a rounding or two in fp32, one more step of bf16 at most
+    assert (lse[~dead] - want_lse[~dead]).abs().max() <= 1e-5
+    assert torch.allclose(got.float(), want.float(), rtol=2.0 ** -7 if dtype == torch.bfloat16 else 2.0 ** -20, atol=2e-6)
