@@ -473,7 +473,7 @@ def make_kv_cache(k, v, k_exp=None, v_exp=None) -> RaKvCache:
     c.k_pages, c.v_pages, c.k_exps, c.v_exps, c.device = k, v, k_exp, v_exp, k.device
     c._index = k.get_device()
     c._row = (h, d)
-    c._sizes = (n, page, h, d, c.dtype)
+    c._sizes = (n, page, h, d, c.dtype, c._index)  # what params for it depend on
     c._ref = ctypes.addressof(c)
     return c
 
@@ -565,7 +565,7 @@ def make_paged_params(cache, q, page_table, kv_len, *, scale, causal=True, soft_
                       sinks=None, prefix_table=None, prefix_len=None) -> RaPagedParams:
     """Params for queries like q (B, Lq, Hq, D) over ``cache``; they hold the tensors, which may be
     changed in place between calls (a page added, a length grown), and serve every layer whose
-    cache has the same sizes.  prefix_len: an int32 tensor of one element."""
+    cache has the same sizes and is on the same device.  prefix_len: an int32 tensor of one element."""
     if q.dtype not in _DT:
         raise TypeError(f"unsupported dtype {q.dtype}")
     _need(q.dim() == 4 and q.shape[3] == cache.D, f"q must be (B, Lq, Hq, {cache.D})")
@@ -626,7 +626,7 @@ def paged_forward(params, q, cache, out=None, lse=None, ws=None, stream=None):
     if (q.shape, q.dtype) != like or not q.is_contiguous():
         raise ValueError("q must be contiguous, of the shape and dtype the params were made for")
     if cache._sizes != params._cache:
-        raise ValueError("the params were made for a cache of other sizes")
+        raise ValueError("the params were made for a cache of other sizes, or on another device")
     if q.get_device() != index:
         raise ValueError("q must be on the cache's device")
     if out is not None and not ((out.shape, out.dtype) == like and out.get_device() == index

@@ -133,3 +133,25 @@ def test_sinks_of_minus_infinity(name, cache, dtype):
     # the same partial results, joined or stored: a rounding or two in fp32, one more step of bf16 at most
     assert (lse[~dead] - want_lse[~dead]).abs().max() <= 1e-5
     assert torch.allclose(got.float(), want.float(), rtol=2.0 ** -7 if dtype == torch.bfloat16 else 2.0 ** -20, atol=2e-6)
+
+
+# ------------------------------------------------------------- the helpers' checks (no GPU needed)
+def host_cache(**kw):
+    return ra.new_kv_cache(3, 16, 2, 64, torch.bfloat16, device="cpu", **kw)
+
+
+def test_params_belong_to_the_device_of_their_tables(monkeypatch):
+    """Params serve another cache of the same sizes on the same device only: their tables lie there."""
+    c, twin, away = host_cache(), host_cache(), host_cache()
+    q, i = torch.zeros((1, 1, 4, 64), dtype=torch.bfloat16), lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    p = ra.make_paged_params(c, q, i(1, 1), i(1), scale=1.0)
+    # a cache and a query of another GPU, as the checks see them
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 1)
+    away = ra.make_kv_cache(away.k_pages, away.v_pages)
+    assert away._index == 1 and away._sizes != c._sizes and twin._sizes == c._sizes
+    called = []
+    monkeypatch.setattr(ra, "_on", lambda *a: called.append(a))
+    monkeypatch.setattr(ra, "_here", lambda index: False)
+    with pytest.raises(ValueError, match="params were made for"):
+        ra.paged_forward(p, q, away)
+    assert not called
