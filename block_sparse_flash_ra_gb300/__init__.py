@@ -481,7 +481,7 @@ def make_kv_cache(k, v, k_exp=None, v_exp=None) -> RaKvCache:
 def new_kv_cache(n_pages, page_size, n_kv_heads, head_dim, dtype=torch.float8_e4m3fn,
                  device=None) -> RaKvCache:
     """An empty cache of ``n_pages`` pages (see ``make_kv_cache``)."""
-    device = device or "cuda"
+    device = "cuda" if device is None else device
     shape = (n_pages, n_kv_heads, page_size, head_dim)
     if dtype not in _CACHE_DT:
         raise TypeError(f"a cache is bfloat16 or float8_e4m3fn, not {dtype}")

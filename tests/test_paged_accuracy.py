@@ -155,3 +155,18 @@ def test_params_belong_to_the_device_of_their_tables(monkeypatch):
     with pytest.raises(ValueError, match="params were made for"):
         ra.paged_forward(p, q, away)
     assert not called
+
+
+def test_a_cache_is_made_where_it_was_asked_for(monkeypatch):
+    """Device 0 is a device, not the lack of one."""
+    asked, zeros = [], torch.zeros
+
+    def fake(*a, device=None, **kw):
+        asked.append(device)
+        return zeros(*a, **kw)
+
+    monkeypatch.setattr(torch, "zeros", fake)
+    for device, want in ((0, 0), (None, "cuda"), ("cuda:1", "cuda:1")):
+        asked.clear()
+        ra.new_kv_cache(1, 16, 1, 64, device=device)
+        assert asked == [want] * 4
