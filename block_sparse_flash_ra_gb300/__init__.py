@@ -447,6 +447,7 @@ def _on(device, stream, run, *args):
     with torch.cuda.device(device):
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
+        _need(stream is None or stream.device == device, "the stream is on another device than the cache")
         with torch.cuda.stream(stream):
             return run(*args, torch.cuda.current_stream().cuda_stream)
 

@@ -170,3 +170,25 @@ def test_a_cache_is_made_where_it_was_asked_for(monkeypatch):
         asked.clear()
         ra.new_kv_cache(1, 16, 1, 64, device=device)
         assert asked == [want] * 4
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """Work on it would run on that device, with this one's tensors."""
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 7
+
+    class Device:
+        def __init__(self, device):
+            self.device = device
+
+        __enter__ = __exit__ = lambda self, *a: None
+
+    ran = []
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "stream", Device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream)
+    with pytest.raises(ValueError, match="stream"):
+        ra._on(torch.device("cuda", 0), Stream(), ran.append)
+    assert not ran
+    ra._on(torch.device("cuda", 1), Stream(), ran.append)
+    assert ran == [7]
