@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int b = blockIdx.y; b < B; b += gridDim.y) {
         const int first = start[b];
         const int n = count ? min(max(count[b], 0), L) : L;
-        if (blockIdx.x == 0 && threadIdx.x == 0 && count && n != count[b]) atomicMax(status, RA_STATUS_BAD_PAGE);
+        if (blockIdx.x == 0 && threadIdx.x == 0 && count && n != count[b]) report_bad_page(status);
         const unsigned rows = (unsigned)n * c.Hkv;
         if (blockIdx.x * (unsigned)(GROUPS * kUnroll) >= rows) continue;
         Raw<T> kr[kUnroll] = {}, vr[kUnroll] = {};
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kThreads)
             if (put[u])
                 row[u] = (((size_t)page * c.Hkv + row[u]) << c.page_shift) + (size_t)(pos & (c.page - 1));
             else
-                atomicMax(status, RA_STATUS_BAD_PAGE);
+                report_bad_page(status);
         }
         __syncwarp();
 #pragma unroll
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads)
             const int n = (int)(((r0 + u * GROUPS) / c.Hkv) >> c.page_shift);
             page[u] = n < max_pages ? table[(size_t)b * max_pages + n] : -1;
         }
-        if (blockIdx.x == 0 && threadIdx.x == 0 && (len < 0 || len > L)) atomicMax(status, RA_STATUS_BAD_PAGE);
+        if (blockIdx.x == 0 && threadIdx.x == 0 && (len < 0 || len > L)) report_bad_page(status);
         Cached<FP8> kr[kUnroll] = {}, vr[kUnroll] = {};
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kThreads)
                     kr[u] = get_row<D, FP8>(c.k, c.k_exp, row, lane);
                     vr[u] = get_row<D, FP8>(c.v, c.v_exp, row, lane);
                 } else {
-                    atomicMax(status, RA_STATUS_BAD_PAGE);
+                    report_bad_page(status);
                 }
             }
         }

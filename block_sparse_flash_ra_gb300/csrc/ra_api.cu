@@ -14,8 +14,8 @@
 
 namespace ra {
 
-// Device-side status word (one per device that loads the library).
-__device__ int g_status;
+// Device-side status words (one set per device that loads the library).
+__device__ int g_status[kStatusWords];
 
 namespace {
 
@@ -939,15 +939,16 @@ RA_API int ra_get_device_status(ra_stream_t stream)
     if (rc) return rc;
     cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
-    int v = 0;
-    e = cudaMemcpy(&v, dc->status, sizeof(int), cudaMemcpyDeviceToHost);
+    int v[kStatusWords] = {};
+    e = cudaMemcpy(v, dc->status, sizeof(v), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_fail(e, "status read");
-    const int zero = 0;
-    e = cudaMemcpy(dc->status, &zero, sizeof(int), cudaMemcpyHostToDevice);
+    const int zero[kStatusWords] = {};
+    e = cudaMemcpy(dc->status, zero, sizeof(zero), cudaMemcpyHostToDevice);
     if (e != cudaSuccess) return cuda_fail(e, "status reset");
-    if (v == RA_STATUS_TIMEOUT) return fail(RA_ERR_TIMEOUT, "a kernel wait timed out");
-    if (v == RA_STATUS_BAD_PAGE)
-        return fail(RA_ERR_INVALID_ARG, "a paged call met a page, position or length out of range");
+    const char *bad = "a paged call met a page, position or length out of range";
+    if (v[kTimeoutWord])
+        return fail(RA_ERR_TIMEOUT, "a kernel wait timed out%s%s", v[kBadPageWord] ? ", and " : "", v[kBadPageWord] ? bad : "");
+    if (v[kBadPageWord]) return fail(RA_ERR_INVALID_ARG, "%s", bad);
     return RA_OK;
 }
 

@@ -66,7 +66,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity)
 // polls, the global status word, and the time limit of one wait.
 struct WaitCtx {
     volatile int *abort_flag; // shared memory
-    int *status;              // global memory, RA_ERR_TIMEOUT on expiry
+    int *status;              // global memory
     uint64_t timeout_ns;
 };
 
@@ -82,7 +82,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, const 
         if ((it & 31u) == 0) {
             if (*ctx.abort_flag) return false;
             if (globaltimer_ns() - t0 > ctx.timeout_ns) {
-                atomicExch(ctx.status, RA_STATUS_TIMEOUT);
+                atomicExch(ctx.status + kTimeoutWord, 1);
                 *ctx.abort_flag = 1;
                 return false;
             }

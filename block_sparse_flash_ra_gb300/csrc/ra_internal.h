@@ -10,8 +10,11 @@
 namespace ra {
 
 constexpr int kTile = RA_TILE;            // canonical tile edge (tokens)
-constexpr int RA_STATUS_TIMEOUT = 1;      // device status word value on a timed-out wait
-constexpr int RA_STATUS_BAD_PAGE = 2;     // a page, position or length out of range (paged calls)
+// words of the device status, 0 or 1: neither report hides the other (bits of
+// one word, set by atomicOr, made the paged kernels 2% slower than a word each)
+constexpr int kTimeoutWord = 0;           // a wait timed out
+constexpr int kBadPageWord = 1;           // a page, position or length out of range (paged calls)
+constexpr int kStatusWords = 2;
 
 // Everything a kernel needs to know about the problem, in device-friendly form.
 struct Problem {

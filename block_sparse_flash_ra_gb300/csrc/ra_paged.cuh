@@ -42,6 +42,8 @@ __device__ __forceinline__ void begin_in_order(const PagedPart &part)
     allow_next();
 }
 
+__device__ __forceinline__ void report_bad_page(int *status) { atomicMax(status + kBadPageWord, 1); }
+
 // 2^(b - 127) of a cached row's scale byte; 255 marks a row without a value.
 // (0, which ra_kv_write does not store, is a subnormal power of two.)
 __device__ __forceinline__ float exp_byte_scale(uint32_t b)
@@ -280,7 +282,7 @@ __device__ __forceinline__ int page_entry(const PagedProblem &p, const PagedPart
 __device__ __forceinline__ bool page_valid(const PagedProblem &p, int page)
 {
     if (page >= 0 && page < p.c.n_pages) return true;
-    atomicMax(p.status, RA_STATUS_BAD_PAGE);
+    report_bad_page(p.status);
     return false;
 }
 
@@ -295,7 +297,7 @@ __device__ __forceinline__ void report_lengths(const PagedProblem &p, const Page
         for (int b = threadIdx.x; b < p.B; b += 32)
             bad |= paged_kv_len(p, b) != p.kv_len[b] || (p.q_len && paged_q_len(p, b) != p.q_len[b]);
     }
-    if (bad) atomicMax(p.status, RA_STATUS_BAD_PAGE);
+    if (bad) report_bad_page(p.status);
 }
 
 } // namespace ra

@@ -581,7 +581,8 @@ RA_API int ra_attn_paged(const ra_kv_cache *cache, const ra_paged_params *p, con
 
 /*
  * Synchronises `stream`, then returns and clears the current device's status
- * word: RA_OK, RA_ERR_TIMEOUT if a kernel gave up a bounded wait, or
+ * word: RA_OK, RA_ERR_TIMEOUT if a kernel gave up a bounded wait (results are
+ * missing then; ra_last_error names the other report too, if there is one), or
  * RA_ERR_INVALID_ARG if a paged call met a page, position or length out of
  * range.
  * The library caches, per device, the device address of this word and the

@@ -192,3 +192,28 @@ def test_a_stream_of_another_device_is_refused(monkeypatch):
     assert not ran
     ra._on(torch.device("cuda", 1), Stream(), ran.append)
     assert ran == [7]
+
+
+@gpu
+@pytest.mark.parametrize("first", ["page", "wait"])
+def test_one_report_does_not_hide_another(first):
+    """A wait that ran out and a page out of range: the wait's code, since results are missing then, and both in words."""
+    c = ra.new_kv_cache(1, 16, 1, 64)
+    x, out = torch.ones((1, 1, 1, 64), device="cuda"), i32([-1])
+
+    def page():
+        ra.kv_write(c, x, x, i32([[5]]), i32([0]))
+
+    def wait():
+        ra.ra_selftest_wait_timeout(2_000_000, out)
+
+    assert ra.ra_get_device_status() == ra.RA_OK
+    for report in (page, wait) if first == "page" else (wait, page):
+        report()
+        torch.cuda.synchronize()
+    assert ra.ra_get_device_status() == ra.RA_ERR_TIMEOUT and "page" in ra.ra_last_error()
+    assert ra.ra_get_device_status() == ra.RA_OK
+    page()
+    assert ra.ra_get_device_status() == ra.RA_ERR_INVALID_ARG and "wait" not in ra.ra_last_error()
+    wait()
+    assert ra.ra_get_device_status() == ra.RA_ERR_TIMEOUT and "page" not in ra.ra_last_error()
