@@ -23,9 +23,16 @@
 // into e4m3 terms, each in columns of its own, so that nothing is lost to it:
 //   q 2^-e = q1 + q2 / 16 (a bf16's 8 bits are two e4m3 significands; error
 //            2^-21 of the row's maximum), and the key's scale multiplies s;
-//   p 2^(e_v - E) = x1 + x2 / 16 + x3 / 256 out of f16 (2^-11 relative, 2^-26
-//            of the row's largest weight at the least), E the largest value
-//            exponent so far, so that the values' scales ride on p.
+//   p 2^(e_v - E) = x1 + x2 / 32 + x3 / 1024 out of f16, so that the values'
+//            scales ride on p: 2^-11 relative, and 2^-24 of the row's largest
+//            contribution p 2^e_v at the least.  That is what the reference of
+//            a row follows, not its largest logit: neither a key of great
+//            weight and little value nor a loud value without weight pushes
+//            the others out of e4m3's range.  (A reference by the logits and
+//            the loudest value row lost whole tails of weights below 2^-18 of
+//            the largest; it took 1-3% less time.  A fourth term, 2^-29, takes
+//            4% more with 20 rows, a largest contribution of 2^6 instead of
+//            2^4, 2^-26, 6%: references move more often.)
 // 16-bit caches run kind::f16 in bf16, q as it is, p = x1 + x2 (2^-16).
 // Logits, maxima, sums and O are fp32.
 //
@@ -41,8 +48,9 @@
 //   warps 0-3 of each warpgroup
 //              softmax of 8 rows: thread = key = TMEM lane of S^T.  A row's
 //              maximum is over all threads, so it is only looked for when some
-//              logit passes the present reference by 2^4 (one barrier with an
-//              or); O (TMEM lane = d) is rescaled then and only then.
+//              weight or contribution passes the present reference by what the
+//              type of P allows (one barrier with an or); O (TMEM lane = d) is
+//              rescaled then and only then.
 //   one warp   issues the products, S(i + 1) before P(i) V(i)
 //   one warp   loads: a lane per page, K and V in rings of their own
 // A tile's softmax is a chain of a few hundred instructions in few warps, so
@@ -64,8 +72,18 @@ namespace {
 constexpr int kKeys = 128, kD = 128; // rows of a cached tile, values of a row
 constexpr int kRT = 8;         // rows of a softmax warpgroup
 constexpr float kNone = -3e38f; // the maximum of no logits: finite, so that no difference is a NaN
-constexpr float kPBias = 4.f;  // 8-bit caches: weights times 2^4 are at most 2^8 < 448
+// 8-bit caches: a row's largest contribution is 2^kPBias at its reference and
+// may grow by 2^kGrow, to 2^8, where e4m3 steps by 16; so a term's rest is 2^3
+// at most and enters the next term times kRest.
+constexpr float kPBias = 4.f, kGrow = 4.f, kRest = 32.f;
 constexpr float kMinExp = 12.f; // least E: 2^(127 + kPBias - E) stays finite
+constexpr float kLouder = 64.f; // a value row that far above E raises it: 2^(e_v - E) stays finite
+// Weights have to stay finite where references follow contributions: a value
+// row 2^kQuiet below the loudest (of its warp, and its warp's below the tile's)
+// counts as that loud, a logit passes its reference by kPass at most, and
+// references fall, while E rises, by 2^40 at most: for E of value rows between
+// 2^-18 and 2^22.  So weights are below 2^100.
+constexpr float kQuiet = 30.f, kPass = 60.f, kFallFrom = 100.f, kFallTo = 140.f;
 
 template <bool FP8, int RP, int D>
 struct Cfg {
@@ -105,10 +123,8 @@ struct Cfg {
     // both operands of O^T are MN-major
     static constexpr uint32_t kIdescO = ((FP8 ? 0u : (1u << 7) | (1u << 10)) | (1u << 4)) | (1u << 15) | (1u << 16) |
                                         ((uint32_t)(kNO >> 3) << 17) | ((uint32_t)(kD >> 4) << 24);
-    // growth of a row's logits above its reference (base 2) that is let pass:
-    // 8-bit weights end at 448, bf16 has fp32's range
-    static constexpr float kLazy = FP8 ? 4.f : 60.f;
     static_assert(kSmem <= (kCtasPerSm == 2 ? 113 : 227) * 1024, "shared memory");
+    static_assert(kRedOff % 16 == 0 && (kRT + 4) % 4 == 0, "words of a warp are read by fours");
     static_assert(kBarOff % 8 == 0 && kRowOff % 8 == 0 && kPOff % 1024 == 0 && kExpOff % 128 == 0, "layout");
 };
 
@@ -535,7 +551,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
                 all = min(all, rows.limit[row0 + r]);
             }
 
-            float m[kRT], l[kRT], ev_top = 0.f; // E: 0 while no value was seen
+            float m[kRT], l[kRT], ev_top = kMinExp; // references, sums, E
 #pragma unroll
             for (int r = 0; r < kRT; ++r) m[r] = kNone, l[r] = 0.f;
             for (int t = c.t0; t < c.t0 + n; ++t, ++i) {
@@ -544,7 +560,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
                 const int valid = min(len - first, kTokens);
                 const bool masked = first + kTokens > all;
                 float s[kRT];
-                float ks[kPar] = {}, vs[kPar] = {}, ev = 0.f;
+                float ks[kPar] = {}, vs[kPar] = {}, ev[kPar] = {};
                 wait(bars.s_full + sb, (i >> 1) & 1);
                 tc_fence_after();
                 tmem_ld<8>(lane_base + sb * C::kNS + row0, s);
@@ -556,7 +572,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
                         ks[y] = exp_byte_scale(e[y]);
                         vs[y] = exp_byte_scale(vb);
                         // bytes behind the length and rows without a value do not count
-                        if (tok + y < valid && vb != 255u) ev = fmaxf(ev, fmaxf((float)vb, kMinExp));
+                        ev[y] = tok + y < valid && vb != 255u ? fmaxf((float)vb, kMinExp) : kMinExp;
                     }
                 }
                 if (FP8) {
@@ -571,7 +587,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
                 tc_fence_before();
                 mbar_arrive(bars.s_empty + sb);
                 // ---- logits in base 2
-                bool grow = FP8 && ev > ev_top;
+                bool grow = FP8 && fmaxf(ev[0], ev[kPar - 1]) > ev_top + kLouder;
 #pragma unroll
                 for (int r = 0; r < kRT; ++r) s[r] *= FP8 ? qs[r] * ks[r % kPar] : qs[r];
                 if (to_cap > 0.f) {
@@ -591,44 +607,61 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
                     for (int r = 0; r < kRT; ++r)
                         if (tok + r % kPar >= valid || first + tok + r % kPar >= rows.limit[row0 + r]) s[r] = -INFINITY;
                 }
+                // how far a logit may pass its reference: by kPass, and as a contribution
+                // 2^(s + e_v - E) to an 8-bit cache's O by kGrow.  (Sums are rounded up:
+                // a reference must not come out too low.)
+                float room[kPar];
 #pragma unroll
-                for (int r = 0; r < kRT; ++r) grow |= s[r] > m[r] + C::kLazy;
+                for (int y = 0; y < kPar; ++y) room[y] = FP8 ? fmaxf(ev[y] - ev_top - kGrow, -kPass) : -kPass;
+#pragma unroll
+                for (int r = 0; r < kRT; ++r) grow |= __fadd_ru(s[r], room[r % kPar]) > m[r];
                 if (group_or(bar, grow)) {
                     // new references: the maxima so far
-#pragma unroll
-                    for (int r = 0; r < kRT; ++r) {
-                        const float x = warp_max(s[r]);
-                        if (lane == 0) red[wq * RS + r] = x;
-                    }
+                    float loud = 0.f, quiet[kPar] = {}, top[kRT];
                     if (FP8) {
-                        ev = warp_max(ev);
-                        if (lane == 0) red[wq * RS + kRT] = ev;
+                        loud = warp_max(fmaxf(ev[0], ev[kPar - 1]));
+#pragma unroll
+                        for (int y = 0; y < kPar; ++y) quiet[y] = fmaxf(ev[y] - loud, -kQuiet);
+                    }
+#pragma unroll
+                    for (int r = 0; r < kRT; ++r) top[r] = warp_max(FP8 ? __fadd_ru(s[r], quiet[r % kPar]) : s[r]);
+                    if (lane == 0) {
+                        float4 *mine = reinterpret_cast<float4 *>(red + wq * RS);
+                        mine[0] = make_float4(top[0], top[1], top[2], top[3]);
+                        mine[1] = make_float4(top[4], top[5], top[6], top[7]);
+                        if (FP8) red[wq * RS + kRT] = loud;
                     }
                     // O is still: P V of the tile before has completed
                     if (t > c.t0) wait(bars.pv_done + (sb ^ 1), ((i - 1) >> 1) & 1);
                     group_sync(bar);
-                    float fe = 1.f;
+                    float fe = 1.f, drop = 0.f;
                     if (FP8) {
-                        float top = ev_top;
+                        float e = ev_top;
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) top = fmaxf(top, red[w * RS + kRT]);
-                        fe = ex2_approx(ev_top - top);
-                        ev_top = top;
+                        for (int w = 0; w < 4; ++w) e = fmaxf(e, red[w * RS + kRT]);
+                        drop = fmaxf(fminf(e, kFallTo) - fmaxf(ev_top, kFallFrom), 0.f);
+                        fe = ex2_approx(ev_top - e);
+                        ev_top = e;
+                    }
+#pragma unroll
+                    for (int r = 0; r < kRT; ++r) top[r] = __fadd_ru(m[r], -drop);
+#pragma unroll 2
+                    for (int w = 0; w < 4; ++w) { // (all at once would take registers from the join beside)
+                        const float4 *of = reinterpret_cast<const float4 *>(red + w * RS), a = of[0], b = of[1];
+                        const float x[kRT] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                        const float below = FP8 ? fmaxf(red[w * RS + kRT] - ev_top, -kQuiet) : 0.f;
+#pragma unroll
+                        for (int r = 0; r < kRT; ++r) top[r] = fmaxf(top[r], __fadd_ru(x[r], below));
                     }
                     float f[kRT];
 #pragma unroll
                     for (int r = 0; r < kRT; r += kPar) {
-                        float top = m[r];
-#pragma unroll
-                        for (int w = 0; w < 4; ++w)
-#pragma unroll
-                            for (int y = 0; y < kPar; ++y) top = fmaxf(top, red[w * RS + r + y]);
-                        const float x = ex2_approx(m[r] - top);
+                        const float ref = fmaxf(top[r], top[r + kPar - 1]), x = ex2_approx(m[r] - ref);
 #pragma unroll
                         for (int y = 0; y < kPar; ++y) {
                             l[r + y] *= x;
                             f[r + y] = x * fe;
-                            m[r + y] = top;
+                            m[r + y] = ref;
                         }
                     }
                     if (t > c.t0) {
@@ -652,7 +685,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
                 // r is k * RP + r, this thread's row is its key.  S of this tile was
                 // issued after P V of the tile before last, so that tile's weights
                 // have been read.
-                const float pb = FP8 ? ex2_approx(127.f + kPBias - fmaxf(ev_top, kMinExp)) : 1.f;
+                const float pb = FP8 ? ex2_approx(127.f + kPBias - ev_top) : 1.f;
                 float x[kRT];
 #pragma unroll
                 for (int r = 0; r < kRT; ++r) {
@@ -672,12 +705,12 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
 #pragma unroll
                     for (int y = 0; y < 4; ++y) h[y] = __floats2half2_rn(x[2 * y], x[2 * y + 1]);
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) {
+                    for (int k = 0; k < C::kPTerms; ++k) {
                         uint32_t w[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
                             w[y] = to_codes(h[y]);
-                            if (k < 2) h[y] = __hmul2(__hsub2(h[y], from_codes(w[y])), __float2half2_rn(16.f));
+                            if (k + 1 < C::kPTerms) h[y] = __hmul2(__hsub2(h[y], from_codes(w[y])), __float2half2_rn(kRest));
                         }
                         const int col = k * RP + row0; // 8 columns: half of a 16-byte chunk
                         asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(pt + (col >> 4) * C::kPChunk + (col & 8)),
@@ -756,7 +789,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
                 } else if (place >= 0) {
                     *reinterpret_cast<float2 *>(part.ml + (slot + tid) * 2) = make_float2(mr, lr);
                 }
-                if (FP8) f *= ex2_approx(fmaxf(ev_top, kMinExp) - 127.f - kPBias);
+                if (FP8) f *= ex2_approx(ev_top - 127.f - kPBias);
                 row_f[col] = f;
             }
             wait(bars.pv_done + ((i - 1) & 1), ((i - 1) >> 1) & 1);
@@ -775,7 +808,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
                 float z[C::kPTerms];
 #pragma unroll
                 for (int k = 0; k < C::kPTerms; ++k) z[k] = kPar == 2 && tid >= D ? o[k][y * kPar + kPar - 1] : o[k][y * kPar];
-                v[y] = FP8 ? z[0] + (z[1] + z[C::kPTerms - 1] * (1.f / 16.f)) * (1.f / 16.f) : z[0] + z[1];
+                v[y] = FP8 ? z[0] + (z[1] + z[C::kPTerms - 1] * (1.f / kRest)) * (1.f / kRest) : z[0] + z[1];
                 v[y] *= row_f[row0 + y * kPar];
             }
             if (kPar == 2) {

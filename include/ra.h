@@ -571,6 +571,17 @@ RA_API size_t ra_attn_paged_workspace_size(const ra_kv_cache *cache, const ra_pa
  * Keys and values behind a sequence's length are never used, whatever the
  * memory holds; inside it, key and value rows that only some of a sequence's
  * queries see have to be finite.
+ * Arithmetic.  fp32 queries: fp32.  bf16 queries: logits, maxima, sums and out
+ * are accumulated in fp32; a weight p_j enters its product with v_j with a
+ * relative error of at most
+ *   16-bit cache  2^-16 (up to 32 query rows per kv head), 2^-8 (more, D = 128)
+ *   e4m3 cache    2^-11, and at least
+ *                   up to 32 rows, or D = 64: what makes p_j max|v_j| differ by
+ *                   2^-24 of the row's largest such product (value rows below
+ *                   2^-30 of the loudest count as that loud in it)
+ *                   more: 2^-27 of the row's largest weight; keys and values below
+ *                   2^-15 of the sequence's loudest lose bits
+ * and q's elements below 2^-12 of their row's largest may lose bits (e4m3).
  * Serving only: there is no backward pass.
  * The prefix is read once for the whole batch.  Results do not depend on how
  * the work was timed: partial results are joined in a fixed order.

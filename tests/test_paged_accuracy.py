@@ -65,9 +65,10 @@ def forward(pool, q, scale, **kw):
     return [x.cpu().double() for x in ra.paged_forward(p, q.cuda(), pool.cache)]
 
 
-def errors(pool, b, q, got, scale, share, floor=0.0, sinks=None, causal=True):
-    """The largest error of sequence b's outputs, in units of what is allowed: 2^-8 |o| + share sum p |v|, and `floor` of
-    the largest contribution p_j max|v_j| for each key."""
+def errors(pool, q, got, scale, share, b=0, per_key=0.0, per_weight=0.0, sinks=None, causal=True):
+    """The largest error of outputs `got` (..., n, Hq, D) of sequence b's queries, in units of what is allowed: the store's
+    rounding, `share` of sum p |v|, and for each key `per_key` of the row's largest contribution p_j max|v_j| and
+    `per_weight` of its largest weight times the loudest value."""
     k, v = pool.dense(b)
     n, Hq, _ = q.shape
     k, v = (t.repeat_interleave(Hq // t.shape[1], 1) for t in (k, v))
@@ -78,13 +79,38 @@ def errors(pool, b, q, got, scale, share, floor=0.0, sinks=None, causal=True):
     whole = s if sinks is None else torch.cat([s, sinks.double()[:, None, None].expand(Hq, n, 1)], -1)
     p = torch.exp(s - torch.logsumexp(whole, -1, keepdim=True))
     o = torch.einsum("hij,jhd->ihd", p, v)
-    mass = torch.einsum("hij,jhd->ihd", p, v.abs())
-    top = (p * v.abs().amax(-1).T[:, None]).amax(-1).T[..., None]
-    allowed = (2.0 ** -8 if q.dtype == torch.bfloat16 else 2.0 ** -23) * o.abs() + share * mass + floor * k.shape[0] * top
+    row = v.abs().amax(-1).T[:, None]  # Hq, 1, keys
+    top = (p * row).amax(-1).T[..., None] * per_key + (p.amax(-1) * row.amax(-1)).T[..., None] * per_weight
+    allowed = torch.finfo(q.dtype).eps / 2 * o.abs() + share * torch.einsum("hij,jhd->ihd", p, v.abs()) + k.shape[0] * top
     return float(((got - o).abs() / allowed).max())
 
 
+def allowance(name, cache, dtype, batch=0):
+    """The bounds below for a call of this shape; batch: of one whose prefix is attended for so many sequences too."""
+    Hq, Hkv, Lq, D = SHAPES[name]
+    kernels = ["fp32" if dtype == torch.float32 else ("rows" if D == 128 and n > 32 else "few") + ("8" if cache == F8 else "16")
+               for n in (Hq // Hkv * Lq * m for m in (1, batch) if m)]
+    return {"share": max(SHARE[k] for k in kernels), "per_key": max(PER_KEY.get(k, 0) for k in kernels),
+            "per_weight": max(PER_WEIGHT.get(k, 0) for k in kernels)}
+
+
+# What a weight may be off by, relative to itself.  few8: half a step of f16 and the third e4m3 term's, 2^-12 each, and
+# logits that are off by 2^-13 (the bound of their sum's logarithm in the other tests).  few16: two bf16 terms, 2^-16, and
+# the logits.  rows8: f16, once more where a reference moves inside a tile.  rows16: half a step of bf16.  fp32: the
+# logits, 2^-24 of each of D products' sum.
+SHARE = {"few8": 2.0 ** -11 + 2.0 ** -13, "few16": 2.0 ** -12, "rows8": 2.0 ** -11 + 2.0 ** -13, "rows16": 2.0 ** -8 + 2.0 ** -12,
+         "fp32": 2.0 ** -13}
+# What a key's contribution may be off by, relative to the row's largest: few8: half of the last step of the third term,
+# 2^-9 / 2^10 at a largest of 2^4.
+PER_KEY = {"few8": 2.0 ** -24}
+# The same, relative to the row's largest weight times the loudest value: rows8: half of the last step of f16, 2^-24 at a
+# largest weight of 2^2.  few8: a reference takes no value row for quieter than 2^-30 of the loudest (weights would grow
+# beyond fp32 otherwise), so a contribution counts as 2^-30 of the two's product at the least, and 2^-24 of that is lost.
+PER_WEIGHT = {"rows8": 2.0 ** -27, "few8": 2.0 ** -54}
+
+
 # rows per kv head and head size of calls that the few-row kernel takes
+SHAPES = dict(KERNELS, rows8_8=(8, 1, 1, 128), rows16_2=(32, 2, 1, 128))
 FEW = {"rows8": (8, 128), "rows16": (16, 128), "rows24": (24, 128), "rows32": (32, 128), "d64": (4, 64), "d64_12": (12, 64)}
 
 
@@ -106,7 +132,89 @@ def test_references_that_rise_with_every_tile(name, cache):
     scale = f32(step * math.log(2) / D)
     out, _ = forward(pool, q, scale)
     for b in (0, 1):
-        assert errors(pool, b, q[b], out[b], scale, 2.0 ** -10) <= 1
+        assert errors(pool, q[b], out[b], scale, 2.0 ** -10, b) <= 1
+
+
+
+def dominated(D, cache, loud, small=9, n=5000, seed=80):
+    """One sequence: a key that outweighs the others, a value row 2^loud as large that has no weight, and n keys of equal
+    weight with values around 1.  The first key's values are 2^-small: the output is the others' sum where they are."""
+    pool = Pool([n], Hkv=1, D=D, page=64, dtype=cache, seed=seed)
+    g = torch.Generator().manual_seed(seed)
+    k, v = torch.zeros((n, D)), grid(torch.randn((n, D), generator=g) + 1)
+    k[0], k[1] = 1.0, -8.0
+    v[0], v[1] = v[0] * 2.0 ** -small, v[1] * 2.0 ** loud
+    put(pool, 0, 0, k)
+    put(pool, 1, 0, v)
+    return pool
+
+
+@gpu
+@each_type
+@each_cache
+@pytest.mark.parametrize("name", SHAPES)
+@pytest.mark.parametrize("low,loud,small", [(18, 0, 9), (20, 6, 9), (22, 0, 9), (23, 6, 9), (18, 3, 0), (20, 30, 12), (16, -9, 40)])
+def test_small_weights_of_many_keys(low, loud, small, name, cache, dtype):
+    """5000 weights 2^-low of the largest, in CTAs that have whole sequences: together they are what comes out."""
+    Hq, Hkv, Lq, D = SHAPES[name]
+    pool = dominated(D, cache, loud, small)
+    B = 304
+    pool.table, pool.lens = pool.table.expand(B, -1).contiguous(), pool.lens * B
+    q = (1 - torch.arange(Hq // Hkv * Lq) % 4 / 16).view(Lq, -1, 1).expand(B, Lq, Hq // Hkv, D).to(dtype)
+    scale = f32(low * math.log(2) / D)
+    out, _ = forward(pool, q.contiguous(), scale, causal=False)
+    assert errors(pool, q[0], out, scale, causal=False, **allowance(name, cache, dtype)) <= 1
+
+
+def terms(y, n, rest):
+    """y as n terms of e4m3 out of f16, each the rest of the ones before it times `rest`: what they stand for."""
+    h, total = y.to(torch.float16), 0
+    for k in range(n):
+        c = h.float().to(F8)
+        total = total + c.double() / rest ** k
+        h = (h - c.to(torch.float16)) * rest
+    return total
+
+
+@pytest.mark.parametrize("how,fine", [((3, 32, 16), True), ((2, 32, 16), False), ((1, 32, 16), False), ((3, 16, 16), False)])
+def test_the_bounds_tell_lost_terms(how, fine, monkeypatch):
+    """Weights split as the few-row kernel does it, with its three terms and with fewer, or with less room below."""
+    n, rest, at = how
+    monkeypatch.setattr(torch.Tensor, "cuda", lambda self, *a, **kw: self)
+    worst = 0.0
+    for low, loud in ((18, 0), (20, 6), (22, 0), (23, 6), (None, 0)):
+        if low is None:
+            pool, scale = Pool([7], Hkv=1, page=64, dtype=F8, seed=81), 128 ** -0.5
+            q = torch.randn((1, 64, 128), generator=torch.Generator().manual_seed(82)).to(torch.bfloat16)
+        else:
+            pool, scale = dominated(128, F8, loud), low * math.log(2) / 128
+            q = torch.ones((1, 1, 128), dtype=torch.bfloat16)
+        k, v = pool.dense(0)
+        s = torch.einsum("ihd,jhd->hij", q.double(), k.expand(-1, q.shape[1], -1)) * scale
+        p = torch.exp(s - s.amax(-1, keepdim=True))
+        size = torch.pow(2.0, pool.cache.v_exps[pool.table[0, 0].long() if low is None else pool.table[0].long()].double() - 127)
+        size = size.view(-1)[:k.shape[0]]
+        by = (p * size if rest == 32 else size.expand_as(p)).amax(-1, keepdim=True)  # the reference: contributions, or values
+        y = terms((p * size / by * at).float(), n, rest) / at * by / size
+        o = torch.einsum("hij,jd->ihd", y / p.sum(-1, keepdim=True), v[:, 0]).to(torch.bfloat16)
+        worst = max(worst, errors(pool, q, o.double(), scale, SHARE["few8"], per_key=PER_KEY["few8"]))
+    assert (worst <= 1) == fine
+
+
+@gpu
+@each_type
+@each_cache
+@each_kernel
+@pytest.mark.parametrize("prefix", [0, 3, 150])
+def test_outputs_relative_to_what_they_are_made_of(prefix, name, cache, dtype):
+    """Lengths of a few keys, where one weight's bits show, and of a few tiles, alone and behind a prefix."""
+    _, Hkv, _, D = KERNELS[name]
+    pool = Pool([1, 2, 3, 5, 9, 17, 40, 129, 300], Hkv=Hkv, D=D, page=32, dtype=cache, seed=83, prefix=prefix)
+    q = (2 * queries(name, 9, torch.float32, 84)).to(dtype)
+    scale = f32(D ** -0.5)
+    out, _ = forward(pool, q, scale, causal=False)
+    for b in range(9):
+        assert errors(pool, q[b], out[b], scale, b=b, causal=False, **allowance(name, cache, dtype, 9 if prefix else 0)) <= 1
 
 
 @gpu
