@@ -65,17 +65,17 @@ def forward(pool, q, scale, **kw):
     return [x.cpu().double() for x in ra.paged_forward(p, q.cuda(), pool.cache)]
 
 
-def errors(pool, q, got, scale, share, b=0, per_key=0.0, per_weight=0.0, sinks=None, causal=True):
+def errors(pool, q, got, scale, share, b=0, per_key=0.0, per_weight=0.0, sinks=None, causal=True, device="cpu"):
     """The largest error of outputs `got` (..., n, Hq, D) of sequence b's queries, in units of what is allowed: the store's
     rounding, `share` of sum p |v|, and for each key `per_key` of the row's largest contribution p_j max|v_j| and
     `per_weight` of its largest weight times the loudest value."""
-    k, v = pool.dense(b)
+    q, got, (k, v) = *(t.to(device) for t in (q, got)), (t.to(device) for t in pool.dense(b))
     n, Hq, _ = q.shape
     k, v = (t.repeat_interleave(Hq // t.shape[1], 1) for t in (k, v))
     s = torch.einsum("ihd,jhd->hij", q.double(), k) * scale
     if causal:
-        j = torch.arange(k.shape[0]) - pool.prefix_len
-        s = s.masked_fill((j > torch.arange(n)[:, None] + pool.lens[b] - n) & (j >= 0), -math.inf)
+        i, j = torch.arange(n, device=device)[:, None], torch.arange(k.shape[0], device=device) - pool.prefix_len
+        s = s.masked_fill((j > i + pool.lens[b] - n) & (j >= 0), -math.inf)
     whole = s if sinks is None else torch.cat([s, sinks.double()[:, None, None].expand(Hq, n, 1)], -1)
     p = torch.exp(s - torch.logsumexp(whole, -1, keepdim=True))
     o = torch.einsum("hij,jhd->ihd", p, v)
@@ -215,6 +215,58 @@ def test_outputs_relative_to_what_they_are_made_of(prefix, name, cache, dtype):
     out, _ = forward(pool, q, scale, causal=False)
     for b in range(9):
         assert errors(pool, q[b], out[b], scale, b=b, causal=False, **allowance(name, cache, dtype, 9 if prefix else 0)) <= 1
+
+
+
+@gpu
+@each_type
+@each_cache
+@pytest.mark.parametrize("name", ["d64", "rows8", "rows20", "rows80", "rows320"])
+def test_long_contexts(name, cache, dtype):
+    """65537 and 40001 tokens, causal, behind a short prefix and alone."""
+    _, _, _, D = SHAPES[name]
+    for prefix in (0, 77):
+        pool = Pool([65537, 40001], Hkv=1, D=D, page=128, dtype=cache, seed=85, prefix=prefix)
+        q = queries(name, 2, dtype, 86)
+        scale = f32(D ** -0.5)
+        out, _ = forward(pool, q, scale)
+        for b in (0, 1):
+            assert errors(pool, q[b], out[b], scale, b=b, device="cuda", **allowance(name, cache, dtype, 2 if prefix else 0)) <= 1
+
+
+@gpu
+@each_cache
+@pytest.mark.parametrize("prefix", [0, 100])
+def test_captured_behind_other_streams_and_copies(prefix, cache):
+    """A call in a graph whose node follows a copy from the host and work of two other streams."""
+    pool = Pool([300, 77], Hkv=2, page=32, dtype=cache, seed=87, prefix=prefix)
+    host = queries("rows8", 2, torch.bfloat16, 88).repeat(1, 1, 4, 1).pin_memory()
+    q, lens = torch.zeros(host.shape, dtype=host.dtype, device="cuda"), i32([300, 77])
+    kv_len, more = torch.zeros_like(lens), torch.zeros_like(lens)
+    p = ra.make_paged_params(pool.cache, q, pool.table.cuda(), kv_len, scale=0.1, prefix_table=pool.prefix.cuda() if prefix else None,
+                             prefix_len=i32([prefix]) if prefix else None)
+    want_p = ra.make_paged_params(pool.cache, q, pool.table.cuda(), lens, scale=0.1, prefix_table=pool.prefix.cuda() if prefix else None,
+                                  prefix_len=i32([prefix]) if prefix else None)
+    want = ra.paged_forward(want_p, host.cuda(), pool.cache)
+    out, lse = torch.zeros_like(q), torch.zeros((2, 8, 1), device="cuda")
+    side = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        for s, x in zip(side, (kv_len, more)):
+            s.wait_stream(here)
+            with torch.cuda.stream(s):
+                x.copy_(lens)
+        q.copy_(host, non_blocking=True)
+        for s in side:
+            here.wait_stream(s)
+        ra.paged_forward(p, q, pool.cache, out=out, lse=lse)
+    for _ in range(3):
+        for x in (q, kv_len, more, out, lse):
+            x.zero_()
+        graph.replay()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(more, lens)
 
 
 @gpu
