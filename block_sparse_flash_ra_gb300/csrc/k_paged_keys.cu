@@ -172,31 +172,18 @@ __device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, uin
         mma_ss_w(d, a, b, idesc, accumulate);
 }
 
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t addr, float *v)
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, float *v)
 {
-    if (N == 32) tmem_ld32(addr, v);
-    else if (N == 16) tmem_ld16(addr, v);
-    else {
-        uint32_t *r = reinterpret_cast<uint32_t *>(v);
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                     : "r"(addr));
-    }
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr));
 }
 
 __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t *r)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d(uint8_t *dst, const void *tmap, uint64_t *bar, int c0, int c1, int c2)
-{
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-                 "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
                  : "memory");
 }
 
@@ -563,7 +550,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
                 float ks[kPar] = {}, vs[kPar] = {}, ev[kPar] = {};
                 wait(bars.s_full + sb, (i >> 1) & 1);
                 tc_fence_after();
-                tmem_ld<8>(lane_base + sb * C::kNS + row0, s);
+                tmem_ld8(lane_base + sb * C::kNS + row0, s);
                 if (FP8) {
                     const uint8_t *e = smem + C::kExpOff + sv * 2 * kTokens + tok;
 #pragma unroll
@@ -577,7 +564,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
                 }
                 if (FP8) {
                     float s2[kRT];
-                    tmem_ld<8>(lane_base + sb * C::kNS + RP + row0, s2);
+                    tmem_ld8(lane_base + sb * C::kNS + RP + row0, s2);
                     tmem_ld_wait();
 #pragma unroll
                     for (int r = 0; r < kRT; ++r) s[r] = fmaf(s2[r], 1.f / 16.f, s[r]);
@@ -670,7 +657,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
                         for (int k = 0; k < C::kPTerms; ++k) {
                             float o[8];
                             uint32_t w[8];
-                            tmem_ld<8>(lane_base + C::kColO + k * RP + row0, o);
+                            tmem_ld8(lane_base + C::kColO + k * RP + row0, o);
                             tmem_ld_wait();
 #pragma unroll
                             for (int y = 0; y < 8; ++y) w[y] = __float_as_uint(o[y] * f[y]);
@@ -797,7 +784,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
             tc_fence_after();
             float o[C::kPTerms][8];
 #pragma unroll
-            for (int k = 0; k < C::kPTerms; ++k) tmem_ld<8>(lane_base + C::kColO + k * RP + row0, o[k]);
+            for (int k = 0; k < C::kPTerms; ++k) tmem_ld8(lane_base + C::kColO + k * RP + row0, o[k]);
             tmem_ld_wait();
             tc_fence_before();
             // a query row's O: this thread's value of it, from all tokens or from
