@@ -5,8 +5,10 @@
 // Logits, probabilities, sums and products are fp32.  It serves fp32 queries,
 // whose results 16-bit tensor-core operands would round.
 //
-// Bound by the FMA pipe: 2 * rows multiply-adds per cached value, one widening
-// beside them.  So nothing passes through shared memory on the way: D / 8
+// Bound by issue: 2 * rows multiply-adds per cached value, its widening and the
+// exchanges beside them (55% of the SMs' issue and pipes; the multiply-adds
+// alone would take some 30 of the 137 us below).  So nothing passes through
+// shared memory on the way: D / 8
 // lanes take a key, 8 values each, with q and o of all the item's rows in
 // their registers; a warp takes 16 keys (part of one page) of a tile of 64.
 // The lanes' partial logits are summed by halving -- each step a lane hands

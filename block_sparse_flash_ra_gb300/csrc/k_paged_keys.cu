@@ -15,9 +15,9 @@
 //
 // Measured (e4m3, 8 kv heads of 128, 32 query heads): 64 sequences of 17 to
 // 8192 tokens 89 us, 6.1 TB/s, 90% of a copy's rate; bf16, 64 x 8192 tokens
-// 307 us, all of it; 32 rows on 8 x 32K bf16 tokens 31 us, 61%, of which some
-// 13 us are the launches, the start, the end and the join.  From 24 columns on
-// the softmax's issue shows: 20 rows on 64 x 1000-3000 e4m3 tokens 75 us, 53%.
+// 306 us, all of it; 32 rows on 8 x 32K bf16 tokens 30 us, 63%, of which some
+// 12 us are the launches, the start, the end and the join.  From 24 columns on
+// the softmax's issue shows: 20 rows on 64 x 1000-3000 e4m3 tokens 77 us, 52%.
 //
 // 8-bit caches run kind::f8f6f4 on the codes.  The other operand is split
 // into e4m3 terms, each in columns of its own, so that nothing is lost to it:
@@ -56,7 +56,9 @@
 // A tile's softmax is a chain of a few hundred instructions in few warps, so
 // rows are spread over warpgroups (8 each) to keep it short, and up to 16
 // columns of an 8-bit cache run two CTAs per SM, one's chain under the other's
-// (64 x 4096 tokens: 89 us, 105 with one; 64 x up to 512: 20 and 26).
+// (64 x 4096 tokens: 89 us, 105 with one; 64 x up to 512: 20 and 26).  With at
+// most 144 registers a CTA of the join finds room beside the two, and starts
+// while they end (64 x 100 tokens: 12.8 us, 14.5 with 147 registers).
 #include <cuda_fp16.h>
 #include <math.h>
 

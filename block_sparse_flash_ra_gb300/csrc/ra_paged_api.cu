@@ -144,7 +144,9 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
         // seg_cost, in tiles: with the line's shares weighted so, CTAs end
         // together.  Taking up a segment (Q, the first maximum, the results)
         // measured 2.8 us beside tiles of 0.7 us in the keys kernel, and 7 us
-        // beside tiles of 1.5 us in the rows kernel.
+        // beside tiles of 1.5 us in the rows kernel.  (16-bit tiles are twice as
+        // long, but 2 serves them no better: 128 sequences of 64-1024 tokens 64 us
+        // and 58 with 4, 64 of up to 512 30 and 27, 64 of up to 8192 162 and 162.)
         if (p->dtype == RA_FP32) {
             kernel = kF32;
             a.seg_cost = 1;

@@ -485,7 +485,7 @@ typedef struct {
  *   page_table  (B, max_pages) int32
  *   start       (B) int32: sequence b's token i goes to position start[b] + i
  *   count       (B) int32, or NULL for L: tokens i >= count[b] are left out
- *               (count is clamped to [0, L])
+ *               (count is clamped to [0, L], which is reported as below)
  * A token whose position lies outside [0, max_pages * page_size), or whose
  * page is outside [0, n_pages), is skipped and reported by
  * ra_get_device_status (RA_ERR_INVALID_ARG).  Nothing else of the cache is
@@ -507,7 +507,8 @@ RA_API int ra_kv_write(const ra_kv_cache *cache, const void *k, const void *v, i
  *               value beyond the type's range becomes an infinity)
  *   page_table  (B, max_pages) int32;  kv_len (B) int32
  * kv_len is clamped to [0, L]; a token whose page is missing from the table or
- * out of range reads as 0 and is reported by ra_get_device_status.
+ * out of range reads as 0.  Either is reported by ra_get_device_status
+ * (RA_ERR_INVALID_ARG).
  * Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED, RA_ERR_CUDA.
  */
 RA_API int ra_kv_read(const ra_kv_cache *cache, const int32_t *page_table, int max_pages,
@@ -583,8 +584,10 @@ RA_API size_t ra_attn_paged_workspace_size(const ra_kv_cache *cache, const ra_pa
  *                   2^-15 of the sequence's loudest lose bits
  * and q's elements below 2^-12 of their row's largest may lose bits (e4m3).
  * Serving only: there is no backward pass.
- * The prefix is read once for the whole batch.  Results do not depend on how
- * the work was timed: partial results are joined in a fixed order.
+ * The prefix is attended by the rows of the whole batch together, and read
+ * once for each block of them: of 256 rows of a kv head (bf16, D = 128; up to
+ * 32 rows are one block), 16 (bf16, D = 64) or 8 (fp32).  Results do not depend
+ * on how the work was timed: partial results are joined in a fixed order.
  * Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED, RA_ERR_WORKSPACE, RA_ERR_CUDA.
  */
 RA_API int ra_attn_paged(const ra_kv_cache *cache, const ra_paged_params *p, const void *q,
