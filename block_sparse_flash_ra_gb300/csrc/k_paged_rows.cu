@@ -26,7 +26,9 @@
 // rescaled, when a tile's largest passes it by 2^7; f16 holds 448 * 2^7).
 // What f16 loses is below 2^-33 of the largest.  The rows of Q are scaled by a
 // power of two into f16's range, and P is f16 (2^-11 relative; weights below
-// 2^-16 of the row's reference lose bits, below 2^-26 all of them).  Widening costs
+// 2^-16 of the row's reference lose bits, below 2^-26 all of them).  References
+// are whole numbers, so weights that were stored before one moved are rescaled
+// by a power of two, which rounds nothing while they are normal.  Widening costs
 // 1.6 instructions per pair and 96 KB of shared-memory traffic per tile of
 // 2048 tensor cycles; the alternative, e4m3 terms for P as the M side of the
 // few-row kernel uses, has no room in a compute-bound loop.
@@ -193,6 +195,31 @@ __device__ __forceinline__ int top_exp(const uint8_t *exps, int valid, int lane)
         if (j < valid && b != 255u) top = max(top, b);
     }
     return (int)__reduce_max_sync(0xffffffffu, top);
+}
+
+// 32 stored weights of every thread times f, a power of two; in two steps where
+// it is no half itself.  Rare, so kept out of the loop's code.
+template <bool FP8>
+__device__ __noinline__ void scale_stored(uint32_t at, float f)
+{
+    const float f1 = FP8 ? fmaxf(f, 1.f / 4096.f) : f, f0 = f < f1 ? f * 4096.f : 1.f;
+    const uint32_t a = pack16<FP8>(f1, f1), b = pack16<FP8>(f0, f0);
+    float w[16];
+    uint32_t u[16];
+    tmem_ld16(at, w);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        u[j] = __float_as_uint(w[j]);
+        if (FP8) {
+            const __half2 r = __hmul2(__hmul2(*reinterpret_cast<const __half2 *>(&u[j]), *reinterpret_cast<const __half2 *>(&a)),
+                                      *reinterpret_cast<const __half2 *>(&b));
+            u[j] = *reinterpret_cast<const uint32_t *>(&r);
+        } else {
+            u[j] = mul_bf16x2(u[j], a);
+        }
+    }
+    tmem_st16(at, u);
 }
 
 template <bool FP8, bool CAP>
@@ -672,30 +699,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             pair[y * 128] = top * b;
                             pair_sync();
-                            const float m_new = max3(m, top * b, pair[(y ^ 1) * 128]);
+                            // whole numbers: f, which the 16-bit weights of the first keys are
+                            // multiplied by too, is a power of two then
+                            const float m_new = floorf(max3(m, top * b, pair[(y ^ 1) * 128]));
                             const float f = m == m_new ? 1.f : ex2_approx(m - m_new); // 0 for a first one
                             m = m_new;
                             l *= f;
                             if (t > c.t0) scale_o(f);
                             if (q) {
                                 // the thread's first 32 keys are stored, but not handed over
-                                float w[16];
-                                uint32_t u[16];
-                                const uint32_t f2 = pack16<FP8>(f, f);
-                                tmem_ld16(s_half, w);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) {
-                                    if (FP8) {
-                                        const uint32_t wi = __float_as_uint(w[j]);
-                                        const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&wi),
-                                                                  *reinterpret_cast<const __half2 *>(&f2));
-                                        u[j] = *reinterpret_cast<const uint32_t *>(&r);
-                                    } else {
-                                        u[j] = mul_bf16x2(__float_as_uint(w[j]), f2);
-                                    }
-                                }
-                                tmem_st16(s_half, u);
+                                scale_stored<FP8>(s_half, f);
                             }
                         }
                         l += sum;

@@ -65,10 +65,21 @@ def forward(pool, q, scale, **kw):
     return [x.cpu().double() for x in ra.paged_forward(p, q.cuda(), pool.cache)]
 
 
-def errors(pool, q, got, scale, share, b=0, per_key=0.0, per_weight=0.0, sinks=None, causal=True, device="cpu"):
-    """The largest error of outputs `got` (..., n, Hq, D) of sequence b's queries, in units of what is allowed: the store's
-    rounding, `share` of sum p |v|, and for each key `per_key` of the row's largest contribution p_j max|v_j| and
-    `per_weight` of its largest weight times the loudest value."""
+def allowed(p, v, o, dtype, share, key=0.0, weight=0.0, value=0.0, quiet=0.0):
+    """What outputs o = sum p_j v_j may be off by; p (Hq, n, keys), v (keys, Hq, D), o (n, Hq, D).  The store's rounding;
+    `share` of sum p |v|; of each key's contribution what is below `key` of the row's largest, p_j max|v_j|, or below
+    `quiet` of its largest weight times the loudest value; of each weight what is below `weight` of the row's largest;
+    and `value` of the loudest value for each value."""
+    row, most = v.abs().amax(-1).T[:, None], p.amax(-1, keepdim=True)
+    part, loud = p * row, row.amax(-1, keepdim=True)
+    lost = torch.minimum(part, torch.maximum(key * part.amax(-1, keepdim=True), quiet * most * loud))
+    lost = lost + torch.minimum(p, weight * most) * row + value * p * loud
+    mass = torch.einsum("hij,jhd->ihd", p, v.abs())
+    return torch.finfo(dtype).eps / 2 * o.abs() + share * mass + lost.sum(-1).T[..., None]
+
+
+def errors(pool, q, got, scale, b=0, sinks=None, causal=True, device="cpu", **bound):
+    """The largest error of outputs `got` (..., n, Hq, D) of sequence b's queries, in units of what is allowed."""
     q, got, (k, v) = *(t.to(device) for t in (q, got)), (t.to(device) for t in pool.dense(b))
     n, Hq, _ = q.shape
     k, v = (t.repeat_interleave(Hq // t.shape[1], 1) for t in (k, v))
@@ -79,38 +90,37 @@ def errors(pool, q, got, scale, share, b=0, per_key=0.0, per_weight=0.0, sinks=N
     whole = s if sinks is None else torch.cat([s, sinks.double()[:, None, None].expand(Hq, n, 1)], -1)
     p = torch.exp(s - torch.logsumexp(whole, -1, keepdim=True))
     o = torch.einsum("hij,jhd->ihd", p, v)
-    row = v.abs().amax(-1).T[:, None]  # Hq, 1, keys
-    top = (p * row).amax(-1).T[..., None] * per_key + (p.amax(-1) * row.amax(-1)).T[..., None] * per_weight
-    allowed = torch.finfo(q.dtype).eps / 2 * o.abs() + share * torch.einsum("hij,jhd->ihd", p, v.abs()) + k.shape[0] * top
-    return float(((got - o).abs() / allowed).max())
+    return float(((got - o).abs() / allowed(p, v, o, q.dtype, **bound).clamp(min=1e-300)).max())
 
 
-def allowance(name, cache, dtype, batch=0):
-    """The bounds below for a call of this shape; batch: of one whose prefix is attended for so many sequences too."""
+# The bounds of each kernel.
+# share, what a weight may be off by, relative to itself; the logits are off by 2^-13 (the bound of their sum's logarithm in
+# the other tests).  few8: half a step of f16, 2^-11, and of the third e4m3 term, 2^-12.  few16: two bf16 terms, 2^-16.
+# rows8: half a step of f16.  rows16: half a step of bf16, 2^-8.  fp32: the logits.
+# key: few8: half of the last step of the third term, 2^-9 / 2^10, at a largest contribution of 2^4.
+# quiet: few8: a reference takes no value row for quieter than 2^-30 of the loudest (weights would grow beyond fp32
+# otherwise), so the same of 2^-30 of the two's product.
+# weight: rows8: half of the last step of f16, 2^-24, at a largest weight of 2^2 at least, and again where a reference
+# moved after the weight was stored.
+# value: rows8: the same, at a largest value of 2^7 (e4m3's 448 less a binade for a scale that is a power of two).
+BOUNDS = {"few8": dict(share=2.0 ** -11 + 2.0 ** -12 + 2.0 ** -13, key=2.0 ** -24, quiet=2.0 ** -54),
+          "few16": dict(share=2.0 ** -12), "rows8": dict(share=2.0 ** -11 + 2.0 ** -13, weight=2.0 ** -26, value=2.0 ** -32),
+          "rows16": dict(share=2.0 ** -8 + 2.0 ** -12), "fp32": dict(share=2.0 ** -13)}
+
+
+def kernel(rows, D, cache, dtype):
+    return "fp32" if dtype == torch.float32 else ("rows" if D == 128 and rows > 32 else "few") + ("8" if cache == F8 else "16")
+
+
+def bounds(name, cache, dtype, batch=0):
+    """Those of a call of this shape; batch: of one whose prefix is attended for so many sequences too."""
     Hq, Hkv, Lq, D = SHAPES[name]
-    kernels = ["fp32" if dtype == torch.float32 else ("rows" if D == 128 and n > 32 else "few") + ("8" if cache == F8 else "16")
-               for n in (Hq // Hkv * Lq * m for m in (1, batch) if m)]
-    return {"share": max(SHARE[k] for k in kernels), "per_key": max(PER_KEY.get(k, 0) for k in kernels),
-            "per_weight": max(PER_WEIGHT.get(k, 0) for k in kernels)}
+    of = [BOUNDS[kernel(Hq // Hkv * Lq * m, D, cache, dtype)] for m in (1, batch) if m]
+    return {x: max(b.get(x, 0.0) for b in of) for x in ("share", "key", "quiet", "weight", "value")}
 
 
-# What a weight may be off by, relative to itself.  few8: half a step of f16 and the third e4m3 term's, 2^-12 each, and
-# logits that are off by 2^-13 (the bound of their sum's logarithm in the other tests).  few16: two bf16 terms, 2^-16, and
-# the logits.  rows8: f16, once more where a reference moves inside a tile.  rows16: half a step of bf16.  fp32: the
-# logits, 2^-24 of each of D products' sum.
-SHARE = {"few8": 2.0 ** -11 + 2.0 ** -13, "few16": 2.0 ** -12, "rows8": 2.0 ** -11 + 2.0 ** -13, "rows16": 2.0 ** -8 + 2.0 ** -12,
-         "fp32": 2.0 ** -13}
-# What a key's contribution may be off by, relative to the row's largest: few8: half of the last step of the third term,
-# 2^-9 / 2^10 at a largest of 2^4.
-PER_KEY = {"few8": 2.0 ** -24}
-# The same, relative to the row's largest weight times the loudest value: rows8: half of the last step of f16, 2^-24 at a
-# largest weight of 2^2.  few8: a reference takes no value row for quieter than 2^-30 of the loudest (weights would grow
-# beyond fp32 otherwise), so a contribution counts as 2^-30 of the two's product at the least, and 2^-24 of that is lost.
-PER_WEIGHT = {"rows8": 2.0 ** -27, "few8": 2.0 ** -54}
-
-
-# rows per kv head and head size of calls that the few-row kernel takes
 SHAPES = dict(KERNELS, rows8_8=(8, 1, 1, 128), rows16_2=(32, 2, 1, 128))
+# rows per kv head and head size of calls that the few-row kernel takes
 FEW = {"rows8": (8, 128), "rows16": (16, 128), "rows24": (24, 128), "rows32": (32, 128), "d64": (4, 64), "d64_12": (12, 64)}
 
 
@@ -132,7 +142,7 @@ def test_references_that_rise_with_every_tile(name, cache):
     scale = f32(step * math.log(2) / D)
     out, _ = forward(pool, q, scale)
     for b in (0, 1):
-        assert errors(pool, q[b], out[b], scale, 2.0 ** -10, b) <= 1
+        assert errors(pool, q[b], out[b], scale, b, share=2.0 ** -10) <= 1
 
 
 
@@ -163,7 +173,7 @@ def test_small_weights_of_many_keys(low, loud, small, name, cache, dtype):
     q = (1 - torch.arange(Hq // Hkv * Lq) % 4 / 16).view(Lq, -1, 1).expand(B, Lq, Hq // Hkv, D).to(dtype)
     scale = f32(low * math.log(2) / D)
     out, _ = forward(pool, q.contiguous(), scale, causal=False)
-    assert errors(pool, q[0], out, scale, causal=False, **allowance(name, cache, dtype)) <= 1
+    assert errors(pool, q[0], out, scale, causal=False, **bounds(name, cache, dtype)) <= 1
 
 
 def terms(y, n, rest):
@@ -197,7 +207,7 @@ def test_the_bounds_tell_lost_terms(how, fine, monkeypatch):
         by = (p * size if rest == 32 else size.expand_as(p)).amax(-1, keepdim=True)  # the reference: contributions, or values
         y = terms((p * size / by * at).float(), n, rest) / at * by / size
         o = torch.einsum("hij,jd->ihd", y / p.sum(-1, keepdim=True), v[:, 0]).to(torch.bfloat16)
-        worst = max(worst, errors(pool, q, o.double(), scale, SHARE["few8"], per_key=PER_KEY["few8"]))
+        worst = max(worst, errors(pool, q, o.double(), scale, **BOUNDS["few8"]))
     assert (worst <= 1) == fine
 
 
@@ -214,7 +224,70 @@ def test_outputs_relative_to_what_they_are_made_of(prefix, name, cache, dtype):
     scale = f32(D ** -0.5)
     out, _ = forward(pool, q, scale, causal=False)
     for b in range(9):
-        assert errors(pool, q[b], out[b], scale, b=b, causal=False, **allowance(name, cache, dtype, 9 if prefix else 0)) <= 1
+        assert errors(pool, q[b], out[b], scale, b=b, causal=False, **bounds(name, cache, dtype, 9 if prefix else 0)) <= 1
+
+
+
+
+@gpu
+@each_type
+@each_cache
+@pytest.mark.parametrize("name", ["d64_80", "rows8_8", "rows80", "rows320"])
+def test_causal_rows_relative_to_what_they_are_made_of(name, cache, dtype):
+    """Rows that see their first key in one part of a tile or another: where one does, its neighbours' references move
+    too, after some of their weights were stored."""
+    _, Hkv, Lq, D = SHAPES[name]
+    pool = Pool([Lq + n for n in (-1, 0, 20, 25, 30, 55, 90, 400)], Hkv=Hkv, D=D, page=32, dtype=cache, seed=89)
+    q = (2 * torch.randn((8, Lq, SHAPES[name][0], D), generator=torch.Generator().manual_seed(90))).to(dtype)
+    scale = f32(D ** -0.5)
+    out, _ = forward(pool, q, scale)
+    for b in range(8):
+        n = min(Lq, pool.lens[b])  # rows before a sequence's first key see nothing
+        assert (out[b, :Lq - n] == 0).all()
+        assert not n or errors(pool, q[b, Lq - n:], out[b, Lq - n:], scale, b=b, **bounds(name, cache, dtype)) <= 1
+
+
+
+@gpu
+@each_type
+@each_cache
+@pytest.mark.parametrize("name", SHAPES)
+@pytest.mark.parametrize("at", [40, 100, 200])
+def test_weights_that_were_there_before_the_reference_moved(at, name, cache, dtype):
+    """One key with loud values and a weight of 2^-25, then one that outweighs it and has small values."""
+    Hq, Hkv, Lq, D = SHAPES[name]
+    pool = Pool([250], Hkv=1, D=D, page=64, dtype=cache, seed=91)
+    g = torch.Generator().manual_seed(91)
+    k, v = torch.full((250, D), -8.0), grid(torch.randn((250, D), generator=g))
+    k[0], k[at] = 0.0, 1.0
+    v[0], v[at] = v[0] * 2.0 ** 12, v[at] * 2.0 ** -15
+    put(pool, 0, 0, k)
+    put(pool, 1, 0, v)
+    q = torch.ones((1, Lq, Hq // Hkv, D)).to(dtype)
+    scale = f32(25 * math.log(2) / D)
+    out, _ = forward(pool, q, scale, causal=False)
+    assert errors(pool, q[0], out[0], scale, causal=False, **bounds(name, cache, dtype)) <= 1
+
+
+@gpu
+@each_cache
+@pytest.mark.parametrize("prefix", [0, 680])
+def test_loud_keys_for_many_rows(prefix, cache):
+    """Keys and values whose size differs between tokens: references move by any amount, and not only at a row's own
+    largest key, since 32 rows move theirs together."""
+    Hq, Hkv, Lq, B, D = 64, 2, 20, 5, 128
+    pool = Pool([672, 1434, 1333, 90, 20], Hkv=Hkv, D=D, page=128, dtype=cache, seed=92, prefix=prefix)
+    g = torch.Generator().manual_seed(92)
+    for b in [None] * bool(prefix) + list(range(B)):
+        n = prefix if b is None else pool.lens[b]
+        for which, most in ((0, 2), (1, 3)):
+            e = torch.randint(-most, most + 1, (n, Hkv, 1), generator=g)
+            put(pool, which, b, grid(torch.randn((n, Hkv, D), generator=g)) * torch.pow(2.0, e))
+    q = (3 * torch.randn((B, Lq, Hq, D), generator=g)).to(torch.bfloat16)
+    scale = f32(D ** -0.5)
+    out, _ = forward(pool, q, scale)
+    for b in range(B):
+        assert errors(pool, q[b], out[b], scale, b=b, device="cuda", **BOUNDS[kernel(999, D, cache, torch.bfloat16)]) <= 1
 
 
 
@@ -231,7 +304,7 @@ def test_long_contexts(name, cache, dtype):
         scale = f32(D ** -0.5)
         out, _ = forward(pool, q, scale)
         for b in (0, 1):
-            assert errors(pool, q[b], out[b], scale, b=b, device="cuda", **allowance(name, cache, dtype, 2 if prefix else 0)) <= 1
+            assert errors(pool, q[b], out[b], scale, b=b, device="cuda", **bounds(name, cache, dtype, 2 if prefix else 0)) <= 1
 
 
 @gpu
