@@ -24,7 +24,7 @@
 // the tile's logits as one number; a value becomes
 // code * 2^(e_v - EV), EV one exponent for the whole segment (raised, and O
 // rescaled, when a tile's largest passes it by 2^7; f16 holds 448 * 2^7).
-// What f16 loses is below 2^-33 of the largest.  The rows of Q are scaled by a
+// What f16 loses is below 2^-32 of the largest.  The rows of Q are scaled by a
 // power of two into f16's range, and P is f16 (2^-11 relative; weights below
 // 2^-16 of the row's reference lose bits, below 2^-26 all of them).  References
 // are whole numbers, so weights that were stored before one moved are rescaled
@@ -184,17 +184,36 @@ __device__ __forceinline__ void widen_half(uint32_t tile, uint32_t raw, const ui
     }
 }
 
-// The largest scale byte of rows below `valid` that have a value (0: none).
-__device__ __forceinline__ int top_exp(const uint8_t *exps, int valid, int lane)
+// The least scale that a half is is 2^-24, but codes of 448 times 2^-33 are
+// still halves: the rows of a half tile that lie so far below its exponent are
+// widened again, with their scale in two steps, the first of which is exact.
+constexpr int kHalfLeast = 24, kFarStep = 12;
+__device__ __noinline__ void widen_far(uint32_t tile, uint32_t raw, const uint8_t *exps, int row0, int valid, int e,
+                                       int warp, int lane)
 {
-    uint32_t top = 0;
+    const int x = lane & 3, in8 = (lane >> 3) ^ (lane & 4 ? 5 : 0); // as in widen_half
+#pragma unroll 1
+    for (int jg = 0; jg < 2; ++jg) {
+        const int j = (warp * 2 + jg) * 8 + in8;
+        const int d = (int)exps[j] - e;
+        if (row0 + j >= valid || d >= -kHalfLeast) continue;
+        const __half2 s1 = half_scale(127 - kFarStep, 127), s2 = half_scale(exps[j], e - kFarStep);
+#pragma unroll 1
+        for (int it = 0; it < 2; ++it) {
+            const uint4 w = lds128(raw + j * 128 + (((it * 4 + x) ^ (j & 7)) << 4));
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            uint32_t o[8];
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-        const int j = lane + 32 * y;
-        const uint32_t b = exps[j];
-        if (j < valid && b != 255u) top = max(top, b);
+            for (int y = 0; y < 8; ++y) {
+                const uint32_t h = e4m3x2_to_f16x2(y & 1 ? u[y >> 1] >> 16 : u[y >> 1] & 0xffffu);
+                const __half2 r = __hmul2(__hmul2(*reinterpret_cast<const __half2 *>(&h), s1), s2);
+                o[y] = *reinterpret_cast<const uint32_t *>(&r);
+            }
+            const uint32_t at = tile + it * (kKeys * 128) + (row0 + j) * 128;
+            sts128(at + (((2 * x) ^ (j & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+            sts128(at + (((2 * x + 1) ^ (j & 7)) << 4), make_uint4(o[4], o[5], o[6], o[7]));
+        }
     }
-    return (int)__reduce_max_sync(0xffffffffu, top);
 }
 
 // 32 stored weights of every thread times f, a power of two; in two steps where
@@ -465,7 +484,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = wait_all(bars.e_full + st_raw + st, (g >> 1) & 1))) break;
                     // the tile's largest exponent (1 at least: its float is normal);
                     // rows without a value do not count
-                    int e = max(max(top_exp(ex, valid, lane), top_exp(ex + kHalf, valid - kHalf, lane)), 1);
+                    int top = 1, low = 255;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int j = lane + 32 * y, b = ex[j];
+                        if (j < valid && b != 255) top = max(top, b), low = min(low, b);
+                    }
+                    int e = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
                     if (st_raw) {
                         // values keep the segment's: 448 * 2^7 is the most that f16 holds
                         if (ev >= 0 && e <= ev + 7) e = ev;
@@ -476,11 +501,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // the softmax needs EV, but not the values
                         if (st_raw) mbar_arrive(bars.ev_full + (g & 3));
                     }
+                    const bool far = __any_sync(0xffffffffu, low < e - kHalfLeast);
                     if (!(ok = wait_all((st_raw ? bars.v_empty : bars.k_empty) + st, ((g >> 1) & 1) ^ 1))) break;
 #pragma unroll 1
                     for (int y = 0; y < 2 && ok; ++y) {
                         if (!(ok = wait_all(raw_full + y, g & 1))) break;
                         widen_half(tile, raw + y * C::kRaw, ex + y * kHalf, y * kHalf, valid, e, w, lane);
+                        if (far) widen_far(tile, raw + y * C::kRaw, ex + y * kHalf, y * kHalf, valid, e, w, lane);
                         mbar_arrive(raw_empty + y);
                     }
                     if (!ok) break;

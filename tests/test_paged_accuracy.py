@@ -294,6 +294,26 @@ def test_loud_keys_for_many_rows(prefix, cache):
 @gpu
 @each_type
 @each_cache
+@pytest.mark.parametrize("name", SHAPES)
+@pytest.mark.parametrize("far", [20, 26, 28])
+def test_values_far_below_the_loudest(far, name, cache, dtype):
+    """The one key that counts has values 2^-far of those of another."""
+    Hq, Hkv, Lq, D = SHAPES[name]
+    pool = Pool([130], Hkv=1, D=D, page=64, dtype=cache, seed=93)
+    g = torch.Generator().manual_seed(93)
+    k, v = torch.full((130, D), -8.0), grid(torch.randn((130, D), generator=g))
+    k[3] = 1.0
+    v[70] *= 2.0 ** far
+    put(pool, 0, 0, k)
+    put(pool, 1, 0, v)
+    q = torch.ones((1, Lq, Hq // Hkv, D)).to(dtype)
+    scale = f32(100 * math.log(2) / D)
+    out, _ = forward(pool, q, scale, causal=False)
+    assert errors(pool, q[0], out[0], scale, causal=False, **bounds(name, cache, dtype)) <= 1
+
+@gpu
+@each_type
+@each_cache
 @pytest.mark.parametrize("name", ["d64", "rows8", "rows20", "rows80", "rows320"])
 def test_long_contexts(name, cache, dtype):
     """65537 and 40001 tokens, causal, behind a short prefix and alone."""
