@@ -12,7 +12,7 @@
 // are dealt to 8 warps that meet in shared memory.  Bound by latency, or by
 // reading the slots once.  Launched so that it starts while the attention
 // kernels drain (their results are waited for behind the search for slots).
-// What runs behind that wait is short code, fetched cold: two slots at a time
+// What runs behind that wait is short code, run once: two slots at a time
 // and the hardware's 2^x (2^-22) took 1.5 us off a call of 2048 rows against
 // four slots and exp2f.
 #include <math.h>

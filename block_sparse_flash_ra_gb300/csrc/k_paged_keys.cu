@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
             }
             // ---- the segment's end: sums over the keys' threads
             // (each step a lane hands half of its rows over: short code, and every
-            // lane busy; the segment's end is mostly fetched cold)
+            // lane busy)
 #pragma unroll
             for (int h = kRT / 2, w = 16; h; h >>= 1, w >>= 1) {
                 const bool up = (lane & w) != 0;

@@ -36,9 +36,9 @@
 // Logits, maxima, sums and O are fp32.
 //
 // Measured, 512 rows on each of 8 kv heads: a prefix of 131072 e4m3 tokens
-// 248 us, 60% of the bf16 rate (the softmax's exponents and conversions keep
-// the pipe waiting); of 32768 tokens 88 us, 43%: some 16K cycles to the first
-// product (set-up, the rows gathered, code fetched cold), 5K to store 128 KB of
+// 243 us, 61% of the bf16 rate (the softmax's exponents and conversions keep
+// the pipe waiting); of 32768 tokens 89 us, 42%: some 16K cycles to the first
+// product (set-up, the rows gathered, code that has not run yet), 5K to store 128 KB of
 // partial results, and the join.
 #include <cuda_fp16.h>
 #include <math.h>
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         u[it] = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + (size_t)src * kD)[ch];
                 }
 #pragma unroll 1
-                for (int it = 0; it < 8; it += 2) { // one piece of code for all: a cold fetch costs more than it
+                for (int it = 0; it < 8; it += 2) { // one piece of code for all
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
                         const int r_in = (warp & 3) * 32 + y * 16 + 2 * (it + z) + (lane >> 4);

@@ -580,8 +580,8 @@ RA_API size_t ra_attn_paged_workspace_size(const ra_kv_cache *cache, const ra_pa
  *                   up to 32 rows, or D = 64: what makes p_j max|v_j| differ by
  *                   2^-24 of the row's largest such product (value rows below
  *                   2^-30 of the loudest count as that loud in it)
- *                   more: 2^-27 of the row's largest weight; keys and values below
- *                   2^-15 of the sequence's loudest lose bits
+ *                   more: 2^-26 of the row's largest weight, and 2^-32 of the
+ *                   loudest key or value (below 2^-15 of it they lose bits)
  * and q's elements below 2^-12 of their row's largest may lose bits (e4m3).
  * Serving only: there is no backward pass.
  * The prefix is attended by the rows of the whole batch together, and read
