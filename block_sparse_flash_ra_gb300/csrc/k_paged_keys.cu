@@ -86,6 +86,9 @@ constexpr float kLouder = 64.f; // a value row that far above E raises it: 2^(e_
 // references fall, while E rises, by 2^40 at most: for E of value rows between
 // 2^-18 and 2^22.  So weights are below 2^100.
 constexpr float kQuiet = 30.f, kPass = 60.f, kFallFrom = 100.f, kFallTo = 140.f;
+// 16-bit caches: what a weight may pass its reference by.  bf16 has fp32's
+// range, but O's sums of weights times values need some of it.
+constexpr float kPass16 = 16.f;
 
 template <bool FP8, int RP, int D>
 struct Cfg {
@@ -596,12 +599,12 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
                     for (int r = 0; r < kRT; ++r)
                         if (tok + r % kPar >= valid || first + tok + r % kPar >= rows.limit[row0 + r]) s[r] = -INFINITY;
                 }
-                // how far a logit may pass its reference: by kPass, and as a contribution
-                // 2^(s + e_v - E) to an 8-bit cache's O by kGrow.  (Sums are rounded up:
+                // how far a logit may pass its reference: as a weight by kPass or kPass16,
+                // as a contribution 2^(s + e_v - E) to an 8-bit cache's O by kGrow.  (Sums are rounded up:
                 // a reference must not come out too low.)
                 float room[kPar];
 #pragma unroll
-                for (int y = 0; y < kPar; ++y) room[y] = FP8 ? fmaxf(ev[y] - ev_top - kGrow, -kPass) : -kPass;
+                for (int y = 0; y < kPar; ++y) room[y] = FP8 ? fmaxf(ev[y] - ev_top - kGrow, -kPass) : -kPass16;
 #pragma unroll
                 for (int r = 0; r < kRT; ++r) grow |= __fadd_ru(s[r], room[r % kPar]) > m[r];
                 if (group_or(bar, grow)) {

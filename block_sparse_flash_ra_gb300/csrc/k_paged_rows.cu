@@ -57,7 +57,7 @@ constexpr int kThreads = 864;
 constexpr int kWideWarpK = 16, kWideWarpV = 20, kLoadWarp = 24, kMmaWarp = 26;
 // The softmax of 32 keys takes the row's present reference for granted:
 // weights are computed at once, and only when a logit passes the reference by
-// 2^13 (2^60 in bf16) -- one barrier with an or over the two warps of 32 rows
+// 2^13 (2^16 in bf16) -- one barrier with an or over the two warps of 32 rows
 // -- is it raised, O rescaled and the 32 keys computed again from S, which their
 // weights have not yet overwritten.  Two threads to a row halve the chain from
 // S to P, which the ping-pong of two tiles does not hide (one thread per row
@@ -88,8 +88,9 @@ struct Cfg {
     static constexpr uint32_t kIdescS = (1u << 4) | kFmt | (128u >> 3 << 17) | (128u >> 4 << 24);
     static constexpr uint32_t kIdescO = kIdescS | (1u << 16); // V is MN-major
     // Weights are 2^kPBias at the row's reference and may grow to kMost (2^15,
-    // 2^60): f16 holds 2^15 and keeps all bits down to 2^-14; bf16 has fp32's range.
-    static constexpr float kPBias = FP8 ? 2.f : 0.f, kMost = FP8 ? 32768.f : 1.152921504606846976e18f;
+    // 2^16): f16 holds 2^15 and keeps all bits down to 2^-14; bf16 has fp32's range,
+    // but O's sums of weights times values need some of it.
+    static constexpr float kPBias = FP8 ? 2.f : 0.f, kMost = FP8 ? 32768.f : 65536.f;
 };
 
 struct Bars {

@@ -575,7 +575,8 @@ RA_API size_t ra_attn_paged_workspace_size(const ra_kv_cache *cache, const ra_pa
  * Arithmetic.  fp32 queries: fp32.  bf16 queries: logits, maxima, sums and out
  * are accumulated in fp32; a weight p_j enters its product with v_j with a
  * relative error of at most
- *   16-bit cache  2^-16 (up to 32 query rows per kv head), 2^-8 (more, D = 128)
+ *   16-bit cache  2^-16 (up to 32 query rows per kv head), 2^-8 (more, D = 128);
+ *                 sums may overflow where values pass 2^110 / (tokens)
  *   e4m3 cache    2^-11, and at least
  *                   up to 32 rows, or D = 64: what makes p_j max|v_j| differ by
  *                   2^-24 of the row's largest such product (value rows below

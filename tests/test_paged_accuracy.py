@@ -128,7 +128,7 @@ FEW = {"rows8": (8, 128), "rows16": (16, 128), "rows24": (24, 128), "rows32": (3
 @each_cache
 @pytest.mark.parametrize("name", FEW)
 def test_references_that_rise_with_every_tile(name, cache):
-    """Each tile's logits pass the reference by more than is let pass (2^4 of a weight with an 8-bit cache, 2^60 with a
+    """Each tile's logits pass the reference by more than is let pass (2^4 of a weight with an 8-bit cache, 2^16 with a
     16-bit one, whose values fall as the weights grow): O is rescaled between its products again and again."""
     G, D = FEW[name]
     tile, tiles, step = (128 * 128 // D, 12, 5) if cache == F8 else (128 * 128 // D, 2, 61)
@@ -310,6 +310,25 @@ def test_values_far_below_the_loudest(far, name, cache, dtype):
     scale = f32(100 * math.log(2) / D)
     out, _ = forward(pool, q, scale, causal=False)
     assert errors(pool, q[0], out[0], scale, causal=False, **bounds(name, cache, dtype)) <= 1
+
+
+@gpu
+@each_type
+@each_cache
+@pytest.mark.parametrize("name", SHAPES)
+def test_large_values_under_rising_logits(name, cache, dtype):
+    """Values around 2^90 and logits that rise by 50 bits twice in a CTA's share: a product of the two does not fit fp32."""
+    Hq, Hkv, Lq, D = SHAPES[name]
+    pool = Pool([700], Hkv=1, D=D, page=64, dtype=cache, seed=94)
+    g = torch.Generator().manual_seed(94)
+    put(pool, 0, 0, (torch.arange(700) // 300)[:, None].expand(700, D).float())
+    put(pool, 1, 0, grid(torch.randn((700, D), generator=g)) * 2.0 ** 90)
+    pool.table, pool.lens = pool.table.expand(304, -1).contiguous(), pool.lens * 304
+    q = torch.ones((304, Lq, Hq // Hkv, D)).to(dtype)
+    scale = f32(50 * math.log(2) / D)
+    out, _ = forward(pool, q, scale, causal=False)
+    assert errors(pool, q[0], out, scale, causal=False, **bounds(name, cache, dtype)) <= 1
+
 
 @gpu
 @each_type
