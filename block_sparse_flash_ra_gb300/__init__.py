@@ -10,11 +10,14 @@ not been built, every call raises.
 The helpers at the bottom (``make_params``, ``build_mask``, ``forward``,
 ``backward``, ``permute``, ``unpermute``; for a paged cache ``new_kv_cache``,
 ``make_kv_cache``, ``kv_write``, ``kv_read``, ``make_paged_params``,
-``paged_forward``) allocate outputs with torch and call the same entry points.
+``paged_forward``; for norms and rotary positions of queries and keys
+``make_rope``, ``make_qk_params``, ``qk_forward``, ``qk_backward``, ``qk_enter``)
+allocate outputs with torch and call the same entry points.
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -34,6 +37,8 @@ __all__ = [
     "RA_E4M3", "RaKvCache", "RaPagedParams", "ra_kv_write", "ra_kv_read",
     "ra_attn_paged_workspace_size", "ra_attn_paged", "new_kv_cache", "make_kv_cache", "kv_write",
     "kv_read", "make_paged_params", "paged_forward",
+    "RA_E2M1", "RaRope", "RaQkParams", "ra_qk_fwd", "ra_qk_bwd_workspace_size", "ra_qk_bwd", "ra_qk_enter",
+    "make_rope", "make_qk_params", "qk_forward", "qk_backward", "qk_enter",
 ]
 
 RA_OK = 0
@@ -45,6 +50,7 @@ RA_ERR_TIMEOUT = -5
 RA_BF16 = 0
 RA_FP32 = 1
 RA_E4M3 = 2
+RA_E2M1 = 3
 RA_TILE = 128
 RA_STEP_SINKS = 1
 RA_STEP_FIRST = 2
@@ -110,6 +116,21 @@ class RaPagedParams(ctypes.Structure):
     ]
 
 
+class RaRope(ctypes.Structure):
+    """Rotary positions; made by ``make_rope``, ``device`` is where its frequencies are."""
+    _fields_ = [("rot", ctypes.c_int), ("interleaved", ctypes.c_int), ("amplitude", ctypes.c_float),
+                ("freq", ctypes.c_void_p)]
+
+
+class RaQkParams(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("L", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int),
+        ("D", ctypes.c_int), ("dtype", ctypes.c_int), ("rope", RaRope), ("eps", ctypes.c_float),
+        ("weight_dtype", ctypes.c_int), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+        ("pos", ctypes.c_void_p), ("start", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -163,6 +184,12 @@ def lib():
             L.ra_attn_paged_workspace_size.argtypes = [KC, PP]
             L.ra_attn_paged_workspace_size.restype = sz
             L.ra_attn_paged.argtypes = [KC, PP, vp, vp, vp, vp, sz, vp]
+            QP = vp  # RaQkParams
+            L.ra_qk_fwd.argtypes = [QP] + [vp, sz] * 4 + [vp]
+            L.ra_qk_bwd_workspace_size.argtypes = [QP]
+            L.ra_qk_bwd_workspace_size.restype = sz
+            L.ra_qk_bwd.argtypes = [QP] + [vp, sz] * 6 + [vp, vp, vp, sz, vp]
+            L.ra_qk_enter.argtypes = [QP, KC] + [vp, sz] * 4 + [vp, ci, vp, vp]
             _lib = L
     return _lib
 
@@ -344,6 +371,29 @@ def ra_attn_paged(cache, params, q, out, lse, ws, stream=None) -> None:
                                _ptr(lse), _ptr(ws), _wsb(ws), _stream(stream)))
 
 
+def ra_qk_fwd(params, q, q_stride, k, k_stride, q_out, q_out_stride, k_out, k_out_stride, stream=None) -> None:
+    _check(lib().ra_qk_fwd(ctypes.byref(params), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(q_out), q_out_stride,
+                           _ptr(k_out), k_out_stride, _stream(stream)))
+
+
+def ra_qk_bwd_workspace_size(params) -> int:
+    return int(lib().ra_qk_bwd_workspace_size(ctypes.byref(params)))
+
+
+def ra_qk_bwd(params, q, q_stride, k, k_stride, dq_out, dq_out_stride, dk_out, dk_out_stride, dq, dq_stride, dk,
+              dk_stride, dq_weight=None, dk_weight=None, ws=None, stream=None) -> None:
+    _check(lib().ra_qk_bwd(ctypes.byref(params), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(dq_out), dq_out_stride,
+                           _ptr(dk_out), dk_out_stride, _ptr(dq), dq_stride, _ptr(dk), dk_stride, _ptr(dq_weight),
+                           _ptr(dk_weight), _ptr(ws), _wsb(ws), _stream(stream)))
+
+
+def ra_qk_enter(params, cache, q, q_stride, k, k_stride, v, v_stride, q_out, q_out_stride, page_table, max_pages,
+                count=None, stream=None) -> None:
+    _check(lib().ra_qk_enter(ctypes.byref(params), ctypes.byref(cache), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v),
+                             v_stride, _ptr(q_out), q_out_stride, _ptr(page_table), max_pages, _ptr(count),
+                             _stream(stream)))
+
+
 # ------------------------------------------------------------- helpers
 _DT = {torch.bfloat16: RA_BF16, torch.float32: RA_FP32}
 
@@ -417,7 +467,7 @@ def unpermute(x, n_shards, stream=None):
 
 
 # ------------------------------------------------------------- paged cache
-_CACHE_DT = {torch.bfloat16: RA_BF16, torch.float8_e4m3fn: RA_E4M3}
+_CACHE_DT = {torch.bfloat16: RA_BF16, torch.float8_e4m3fn: RA_E4M3, torch.float4_e2m1fn_x2: RA_E2M1}
 
 
 def _need(ok, what):
@@ -454,23 +504,26 @@ def _on(device, stream, run, *args):
 
 def make_kv_cache(k, v, k_exp=None, v_exp=None) -> RaKvCache:
     """A cache over existing tensors: k, v (n_pages, Hkv, page_size, D), bf16 or float8_e4m3fn,
-    and for the latter k_exp, v_exp (n_pages, Hkv, page_size) uint8."""
+    or (n_pages, Hkv, page_size, D / 2) float4_e2m1fn_x2; for e4m3 with k_exp, v_exp (n_pages, Hkv,
+    page_size) uint8, for e2m1 (n_pages, Hkv, page_size, D / 32)."""
     if k.dtype not in _CACHE_DT or v.dtype != k.dtype:
-        raise TypeError(f"a cache is bfloat16 or float8_e4m3fn, not {k.dtype} and {v.dtype}")
+        raise TypeError(f"a cache is bfloat16, float8_e4m3fn or float4_e2m1fn_x2, not {k.dtype} and {v.dtype}")
     _need(k.dim() == 4 and k.shape == v.shape, "k and v must be (n_pages, Hkv, page_size, D)")
-    quantised = k.dtype != torch.bfloat16
-    _need((k_exp is not None) == quantised and (v_exp is not None) == quantised,
-          "k_exp and v_exp belong to float8_e4m3fn caches")
+    dt = _CACHE_DT[k.dtype]
+    n, h, page, d = k.shape
+    d *= 2 if dt == RA_E2M1 else 1
+    _need((k_exp is not None) == (dt != RA_BF16) and (v_exp is not None) == (dt != RA_BF16),
+          "k_exp and v_exp belong to float8_e4m3fn and float4_e2m1fn_x2 caches")
     for x in (k, v, k_exp, v_exp):
         _need(x is None or (x.is_contiguous() and x.device == k.device),
               "cache tensors must be contiguous and on one device")
+    exps = (n, h, page) if dt == RA_E4M3 else (n, h, page, d // 32)
     for x in (k_exp, v_exp):
         if x is not None:
             if x.dtype != torch.uint8:
                 raise TypeError(f"k_exp and v_exp must be uint8, not {x.dtype}")
-            _need(x.shape == k.shape[:3], "k_exp and v_exp must be (n_pages, Hkv, page_size)")
-    n, h, page, d = k.shape
-    c = RaKvCache(n, page, h, d, _CACHE_DT[k.dtype], _ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp))
+            _need(x.shape == exps, f"k_exp and v_exp must be {exps}")
+    c = RaKvCache(n, page, h, d, dt, _ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp))
     c.k_pages, c.v_pages, c.k_exps, c.v_exps, c.device = k, v, k_exp, v_exp, k.device
     c._index = k.get_device()
     c._row = (h, d)
@@ -481,15 +534,18 @@ def make_kv_cache(k, v, k_exp=None, v_exp=None) -> RaKvCache:
 
 def new_kv_cache(n_pages, page_size, n_kv_heads, head_dim, dtype=torch.float8_e4m3fn,
                  device=None) -> RaKvCache:
-    """An empty cache of ``n_pages`` pages (see ``make_kv_cache``)."""
+    """An empty cache of ``n_pages`` pages, bfloat16, float8_e4m3fn or float4_e2m1fn_x2 (see
+    ``make_kv_cache``)."""
     device = "cuda" if device is None else device
-    shape = (n_pages, n_kv_heads, page_size, head_dim)
     if dtype not in _CACHE_DT:
-        raise TypeError(f"a cache is bfloat16 or float8_e4m3fn, not {dtype}")
-    k, v = (torch.zeros(shape, dtype=torch.uint8 if dtype != torch.bfloat16 else dtype,
+        raise TypeError(f"a cache is bfloat16, float8_e4m3fn or float4_e2m1fn_x2, not {dtype}")
+    four = dtype == torch.float4_e2m1fn_x2
+    shape = (n_pages, n_kv_heads, page_size)
+    k, v = (torch.zeros(shape + (head_dim // 2 if four else head_dim,),
+                        dtype=torch.uint8 if dtype != torch.bfloat16 else dtype,
                         device=device).view(dtype) for _ in range(2))
     exps = [None, None] if dtype == torch.bfloat16 else [
-        torch.zeros(shape[:3], dtype=torch.uint8, device=device) for _ in range(2)]
+        torch.zeros(shape + ((head_dim // 32,) if four else ()), dtype=torch.uint8, device=device) for _ in range(2)]
     return make_kv_cache(k, v, *exps)
 
 
@@ -642,3 +698,192 @@ def paged_forward(params, q, cache, out=None, lse=None, ws=None, stream=None):
         return _paged_forward(params, q, cache, out, lse, ws,
                               torch._C._cuda_getCurrentRawStream(index))
     return _on(cache.device, stream, _paged_forward, params, q, cache, out, lse, ws)
+
+
+# ------------------------------------------------------------- norms and rotary positions
+def _frequencies(rot, base, scaling, factor, trained_length, fast, slow, low, high):
+    """Radians per position of the rot / 2 pairs, and the amplitude that the scaling asks for."""
+    amplitude = 1.0
+    if scaling == "ntk" and rot > 2:
+        base *= factor ** (rot / (rot - 2))
+    f = [base ** (-2 * i / rot) for i in range(rot // 2)]
+    if scaling == "linear":
+        f = [x / factor for x in f]
+    elif scaling == "yarn":
+        # the pair that turns r times in the trained length
+        at = [rot * math.log(trained_length / (r * 2 * math.pi)) / (2 * math.log(base)) for r in (fast, slow)]
+        lo, hi = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot - 1)
+        ramp = [min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0) for i in range(rot // 2)]
+        f = [x / factor * r + x * (1 - r) for x, r in zip(f, ramp)]
+        amplitude = 0.1 * math.log(factor) + 1.0
+    elif scaling == "bands":
+        keep = [min(max((trained_length * x / (2 * math.pi) - low) / (high - low), 0.0), 1.0) for x in f]
+        f = [x / factor * (1 - k) + x * k for x, k in zip(f, keep)]
+    return f, amplitude
+
+
+def make_rope(rot, base=10000.0, *, interleaved=False, scaling=None, factor=1.0, trained_length=None, fast=32.0,
+              slow=1.0, low=1.0, high=4.0, amplitude=None, frequencies=None, device=None) -> RaRope:
+    """Rotary positions of the first ``rot`` values of a head, pair i by base^(-2i / rot) per position.
+    ``interleaved``: pairs are neighbours, not rot / 2 apart.  ``scaling``, for contexts longer than
+    ``trained_length`` by ``factor``: "linear" (all angles divided by it), "ntk" (a base that divides the
+    slowest by it), "yarn" (divided where a pair turns less than ``slow`` times in the trained length, kept
+    above ``fast`` turns, a ramp over the pairs between; the amplitude is 0.1 ln(factor) + 1), "bands"
+    (the same between ``low`` and ``high`` turns, by the turns, without an amplitude).  ``frequencies``:
+    rot / 2 of the caller's own instead, in radians per position.  ``amplitude`` overrides the scaling's."""
+    _need(scaling in (None, "linear", "ntk", "yarn", "bands"), f"unknown scaling {scaling!r}")
+    _need(rot > 0 and rot % 16 == 0, f"rot must be a multiple of 16 (got {rot})")
+    if frequencies is not None:
+        _need(scaling is None, "frequencies of the caller's own are not scaled")
+        f, a = [float(x) for x in frequencies], 1.0
+        _need(len(f) == rot // 2, f"{rot} rotated values need {rot // 2} frequencies, not {len(f)}")
+    else:
+        _need(base > 1.0 and factor >= 1.0 and math.isfinite(base) and math.isfinite(factor),
+              "base must be above 1 and factor at least 1")
+        if scaling in ("yarn", "bands"):
+            _need(trained_length is not None and trained_length > 0, f"{scaling} needs trained_length")
+        _need(0 < slow < fast and 0 < low < high, "slow must be below fast, and low below high")
+        f, a = _frequencies(rot, float(base), scaling, float(factor), trained_length, fast, slow, low, high)
+    _need(all(math.isfinite(x) for x in f), "frequencies must be finite")
+    # turns per position as fractions of 2^64, kept in int64
+    turns = [round(math.fmod(x / (2 * math.pi), 1.0) * 2 ** 64) % 2 ** 64 for x in f]
+    freq = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64)
+    freq = freq.to("cuda" if device is None else device)
+    r = RaRope(rot, int(bool(interleaved)), float(a if amplitude is None else amplitude), freq.data_ptr())
+    r._keep, r.device, r._index = freq, freq.device, freq.get_device()
+    return r
+
+
+def make_qk_params(q, k=None, *, rope=None, pos=None, start=None, prefix_len=None, eps=None, q_weight=None,
+                   k_weight=None) -> RaQkParams:
+    """Params for q (B, L, Hq, D) and k (B, L, Hkv, D), either of which may be None, on their device.
+    ``eps``: None for no norm; the weights (D), bf16 or fp32, are ones where None.  ``rope``: from
+    ``make_rope``, None for no rotation, by ``pos`` (B, L) int32 or by start[b] + i + prefix_len[0].
+    They hold the tensors, which may be changed in place between calls."""
+    x = q if q is not None else k
+    _need(x is not None and x.dim() == 4, "q or k is needed, (B, L, heads, D)")
+    if x.dtype not in _DT:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    B, L, _, D = x.shape
+    index = x.get_device()
+    if q is not None and k is not None:
+        _need(k.dim() == 4 and (k.shape[0], k.shape[1], k.shape[3]) == (B, L, D), f"k must be ({B}, {L}, Hkv, {D})")
+        if k.dtype != q.dtype:
+            raise TypeError(f"q and k must have one dtype, not {q.dtype} and {k.dtype}")
+        _need(k.get_device() == index, "q and k must be on one device")
+    if rope is not None:
+        _need(rope._index == index, "the rope is on another device than the tensors")
+        _need(rope.rot <= D, f"rot ({rope.rot}) is more than the head's {D} values")
+    if pos is not None:
+        _ints(pos, (B, L), "pos", index)
+    if start is not None:
+        _ints(start, (B,), "start", index)
+    if prefix_len is not None:
+        _ints(prefix_len, (1,), "prefix_len", index)
+    weights = [w for w in (q_weight, k_weight) if w is not None]
+    _need(eps is not None or not weights, "weights belong to a norm: give its eps")
+    _need(eps is None or 1e-30 <= eps < 1e30, "eps must be at least 1e-30 and finite")
+    for w in weights:
+        if w.dtype not in _DT or w.dtype != weights[0].dtype:
+            raise TypeError("weights must be all bfloat16 or all float32")
+        _need(tuple(w.shape) == (D,) and w.is_contiguous() and w.get_device() == index,
+              f"weights must be ({D},), contiguous and on the tensors' device")
+    p = RaQkParams(B, L, 0 if q is None else q.shape[2], 0 if k is None else k.shape[2], D, _DT[x.dtype],
+                   RaRope(0, 0, 1.0, None) if rope is None else rope, 0.0 if eps is None else float(eps),
+                   _DT[weights[0].dtype] if weights else RA_FP32, _ptr(q_weight), _ptr(k_weight), _ptr(pos), _ptr(start),
+                   _ptr(prefix_len))
+    p._keep = (rope, pos, start, prefix_len, q_weight, k_weight)
+    p._like = tuple(None if t is None else (t.shape, t.dtype) for t in (q, k))
+    p.device, p._index = x.device, index
+    p._ws = ra_qk_bwd_workspace_size(p) if B and L else 0
+    p._ref = ctypes.addressof(p)
+    return p
+
+
+def _qk_rows(params, which, x, name):
+    """(address, stride) of q-like (which = 0) or k-like tensors; nothing where there are no heads."""
+    like = params._like[which]
+    if like is None:
+        _need(x is None, f"{name}: the params were made without it")
+        return None, 0
+    if x is None or (x.shape, x.dtype) != like:
+        raise ValueError(f"{name} must have the shape and dtype the params were made for")
+    if x.get_device() != params._index:
+        raise ValueError(f"{name} must be on the params' device")
+    return x.data_ptr(), _token_stride(x.shape, x.stride(), name)
+
+
+def _qk_new(params, which, given, x):
+    if params._like[which] is None:
+        return None
+    shape, dtype = params._like[which]
+    return given if given is not None else torch.empty(shape, dtype=dtype, device=params.device)
+
+
+def _qk_forward(params, q, k, q_out, k_out, s):
+    outs = _qk_new(params, 0, q_out, q), _qk_new(params, 1, k_out, k)
+    if params.B and params.L:
+        _check(lib().ra_qk_fwd(params._ref, *_qk_rows(params, 0, q, "q"), *_qk_rows(params, 1, k, "k"),
+                               *_qk_rows(params, 0, outs[0], "q_out"), *_qk_rows(params, 1, outs[1], "k_out"), s))
+    return outs
+
+
+def _qk_run(params, stream, run, *args):
+    if stream is None and _here(params._index):
+        return run(params, *args, torch._C._cuda_getCurrentRawStream(params._index))
+    return _on(params.device, stream, run, params, *args)
+
+
+def qk_forward(params, q, k=None, q_out=None, k_out=None, stream=None):
+    """q and k with their heads normalised and rotated -> (q_out, k_out), new ones where not given
+    (q_out may be q, k_out may be k).  No gradient is recorded: ``qk_backward`` computes it."""
+    return _qk_run(params, stream, _qk_forward, q, k, q_out, k_out)
+
+
+def _qk_backward(params, q, k, dq_out, dk_out, dq, dk, s):
+    grads = _qk_new(params, 0, dq, q), _qk_new(params, 1, dk, k)
+    norm = params.eps > 0
+    ws, n, dw = None, params._ws, [None, None]
+    for i in range(2):
+        if norm and params._like[i] is not None:
+            dw[i] = torch.empty(params.D, dtype=torch.float32, device=params.device)
+    if not (params.B and params.L):
+        return (*grads, *(None if w is None else w.zero_() for w in dw))
+    if n:
+        ws = torch.UntypedStorage(n, device=params.device)
+    xs = ((q, "q"), (k, "k")) if norm else ((None, ""), (None, ""))
+    rows = [_qk_rows(params, i, x, name) if norm else (None, 0) for i, (x, name) in enumerate(xs)]
+    _check(lib().ra_qk_bwd(params._ref, *rows[0], *rows[1], *_qk_rows(params, 0, dq_out, "dq_out"),
+                           *_qk_rows(params, 1, dk_out, "dk_out"), *_qk_rows(params, 0, grads[0], "dq"),
+                           *_qk_rows(params, 1, grads[1], "dk"), _ptr(dw[0]), _ptr(dw[1]),
+                           None if ws is None else ws.data_ptr(), n, s))
+    return (*grads, *dw)
+
+
+def qk_backward(params, q, k, dq_out, dk_out=None, dq=None, dk=None, stream=None):
+    """The gradient of ``qk_forward`` at q, k (None without a norm) -> (dq, dk, dq_weight, dk_weight);
+    the weights' gradients are fp32 (D), None without a norm.  dq may be dq_out or q, and dk likewise."""
+    return _qk_run(params, stream, _qk_backward, q, k, dq_out, dk_out, dq, dk)
+
+
+def _qk_enter(params, cache, q, k, v, page_table, count, out, s):
+    out = _qk_new(params, 0, out, q)
+    if params.B and params.L:
+        _check(lib().ra_qk_enter(params._ref, cache._ref, *_qk_rows(params, 0, q, "q"), *_qk_rows(params, 1, k, "k"),
+                                 *_qk_rows(params, 1, v, "v"), *_qk_rows(params, 0, out, "out"), page_table.data_ptr(),
+                                 page_table.shape[1], None if count is None else count.data_ptr(), s))
+    return out
+
+
+def qk_enter(params, cache, q, k, v, page_table, count=None, out=None, stream=None):
+    """Tokens enter the cache: q normalised and rotated comes out, k likewise and v as it is are appended
+    as ``kv_write`` does, at the params' ``start``; of sequence b the first count[b] tokens (None: all; rows
+    of ``out`` behind them stay as they are)."""
+    if cache._index != params._index:
+        raise ValueError("the cache is on another device than the params")
+    _need(params._like[1] is not None, "the params were made without k")
+    B = params.B
+    _ints(page_table, (B, page_table.shape[-1]), "page_table", params._index)
+    if count is not None:
+        _ints(count, (B,), "count", params._index)
+    return _qk_run(params, stream, _qk_enter, cache, q, k, v, page_table, count, out)

@@ -4,7 +4,9 @@
 // row's scale is the smallest power of two 2^e with max|x| <= 448 * 2^e, taken
 // from the bits of the largest magnitude (448 = 1.75 * 2^8), and the codes are
 // x * 2^-e rounded to nearest even: the product is exact, so a code differs
-// from the value by one rounding.  Read: code * 2^e, exact in bf16 and fp32.
+// from the value by one rounding.  For a cache in 4 bits the same holds of every
+// 32 values, with max|x| <= 6 * 2^e (6 = 1.5 * 2^2) and codes of e2m1.  Read:
+// code * 2^e, exact in bf16 and fp32.
 //
 // Both are copies: bound by memory for prompts and histories, by latency for
 // one token per sequence.  D / 8 lanes take a row, 16 bytes of bf16 each, and
@@ -15,93 +17,14 @@
 // 29.4 us, 5.1 TB/s, 76% of a copy's rate (two rows at a time in flight, the
 // maxima on packed 16-bit pairs; one row at a time took 53).  Read back, 2 x
 // 16384 tokens of 16 heads: 69.7 us, 84%.
-#include <cuda_fp16.h>
+#include <type_traits>
 
-#include "ra_paged.cuh"
+#include "ra_rows.cuh"
 
 namespace ra {
 namespace {
 
 constexpr int kThreads = 256, kUnroll = 2;
-
-// Eight consecutive values in registers.
-struct Eight {
-    float x[8];
-};
-
-// The same as loaded: fewer registers while they wait.
-template <typename T>
-struct Raw {
-    uint4 w[sizeof(T) / 2];
-};
-
-template <typename T>
-__device__ __forceinline__ Raw<T> load8(const T *p)
-{
-    Raw<T> r;
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = reinterpret_cast<const uint4 *>(p)[i];
-    return r;
-}
-
-__device__ __forceinline__ Eight widen(const Raw<__nv_bfloat16> &w)
-{
-    const uint32_t a[4] = {w.w[0].x, w.w[0].y, w.w[0].z, w.w[0].w};
-    Eight r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        r.x[2 * i] = __uint_as_float(a[i] << 16);
-        r.x[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
-    }
-    return r;
-}
-
-__device__ __forceinline__ Eight widen(const Raw<float> &w)
-{
-    const uint32_t a[8] = {w.w[0].x, w.w[0].y, w.w[0].z, w.w[0].w, w.w[1].x, w.w[1].y, w.w[1].z, w.w[1].w};
-    Eight r;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r.x[i] = __uint_as_float(a[i]);
-    return r;
-}
-
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const Eight &r)
-{
-    uint4 w;
-    w.x = pack_bf16x2(r.x[0], r.x[1]);
-    w.y = pack_bf16x2(r.x[2], r.x[3]);
-    w.z = pack_bf16x2(r.x[4], r.x[5]);
-    w.w = pack_bf16x2(r.x[6], r.x[7]);
-    *reinterpret_cast<uint4 *>(p) = w;
-}
-
-__device__ __forceinline__ void store8(float *p, const Eight &r)
-{
-    reinterpret_cast<float4 *>(p)[0] = make_float4(r.x[0], r.x[1], r.x[2], r.x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(r.x[4], r.x[5], r.x[6], r.x[7]);
-}
-
-// codes of four values, the first in the lowest byte
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
-{
-    uint32_t r;
-    asm("{\n\t.reg .b16 lo, hi;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
-        "mov.b32 %0, {lo, hi};\n\t}"
-        : "=r"(r)
-        : "f"(a), "f"(b), "f"(c), "f"(d));
-    return r;
-}
-
-// The scale byte of a row from the bits of its largest magnitude: frexp's
-// exponent less 9, or less 8 above 1.75 * 2^n; 255 when it is not finite.
-__device__ __forceinline__ uint32_t row_exp(uint32_t amax_bits)
-{
-    if (amax_bits >= 0x7f800000u) return 255u;
-    const int e = (int)(amax_bits >> 23) - 135 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-    return (uint32_t)(max(e, -110) + 127);
-}
 
 // Largest magnitudes, as fp32 bits, of a K row and a V row that LANES lanes hold.
 template <int LANES>
@@ -135,30 +58,35 @@ __device__ __forceinline__ uint2 row_tops(const Raw<float> &k, const Raw<float> 
     return t;
 }
 
-// Stores a lane's eight values of a row; 8-bit: as codes at the scale that the
-// row's largest magnitude asks for.
-template <int LANES, bool FP8>
+// Stores a lane's eight values of a row; as codes at the scale that the largest
+// magnitude of the row (8 bits) or of the lane's block of 32 (4 bits) asks for.
+template <int LANES, int CACHE>
 __device__ __forceinline__ void put_row(const Eight &r, uint32_t top, const void *base, const uint8_t *exps, size_t row, int lane)
 {
-    if (FP8) {
-        const uint32_t e = row_exp(top);
-        // 2^-(e - 127): its exponent field is 254 - e, in [7, 237]
-        const float inv = __uint_as_float((254u - e) << 23);
-        uint2 w = make_uint2(0, 0);
-        if (e != 255u) {
-            w.x = e4m3x4(r.x[0] * inv, r.x[1] * inv, r.x[2] * inv, r.x[3] * inv);
-            w.y = e4m3x4(r.x[4] * inv, r.x[5] * inv, r.x[6] * inv, r.x[7] * inv);
-        }
-        reinterpret_cast<uint2 *>(const_cast<uint8_t *>(static_cast<const uint8_t *>(base)) + row * (LANES * 8))[lane] = w;
-        if (lane == 0) const_cast<uint8_t *>(exps)[row] = (uint8_t)e;
-    } else {
+    uint8_t *bytes = static_cast<uint8_t *>(const_cast<void *>(base)), *e8 = const_cast<uint8_t *>(exps);
+    if (CACHE == RA_BF16) {
         store8(static_cast<__nv_bfloat16 *>(const_cast<void *>(base)) + row * (LANES * 8) + lane * 8, r);
+        return;
+    }
+    const uint32_t e = CACHE == RA_E4M3 ? row_exp(top) : block_exp(top);
+    const float inv = exp_byte_inverse(e);
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = r.x[i] * inv;
+    if (CACHE == RA_E4M3) {
+        uint2 w = make_uint2(0, 0);
+        if (e != 255u) w = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
+        reinterpret_cast<uint2 *>(bytes + row * (LANES * 8))[lane] = w;
+        if (lane == 0) e8[row] = (uint8_t)e;
+    } else {
+        reinterpret_cast<uint32_t *>(bytes + row * (LANES * 4))[lane] = e != 255u ? e2m1x8(x) : 0u;
+        if (lane % 4 == 0) e8[row * (LANES / 4) + lane / 4] = (uint8_t)e;
     }
 }
 
 // Blocks of kUnroll rows per group lie along x over one sequence's rows
 // (token, head), sequences along y.
-template <int D, bool FP8, typename T>
+template <int D, int CACHE, typename T>
 __global__ void __launch_bounds__(kThreads)
     kv_write_kernel(PagedCache c, const T *__restrict__ k, const T *__restrict__ v, int B, int L, size_t k_stride,
                     size_t v_stride, const int32_t *__restrict__ table, int max_pages,
@@ -206,46 +134,50 @@ __global__ void __launch_bounds__(kThreads)
         __syncwarp();
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const uint2 top = FP8 ? row_tops<LANES>(kr[u], vr[u]) : make_uint2(0, 0);
+            const uint2 top = CACHE == RA_BF16 ? make_uint2(0, 0) : row_tops<CACHE == RA_E4M3 ? LANES : 4>(kr[u], vr[u]);
             if (!put[u]) continue;
-            put_row<LANES, FP8>(widen(kr[u]), top.x, c.k, c.k_exp, row[u], lane);
-            put_row<LANES, FP8>(widen(vr[u]), top.y, c.v, c.v_exp, row[u], lane);
+            put_row<LANES, CACHE>(widen(kr[u]), top.x, c.k, c.k_exp, row[u], lane);
+            put_row<LANES, CACHE>(widen(vr[u]), top.y, c.v, c.v_exp, row[u], lane);
         }
     }
 }
 
-// Eight values of a cached row as the cache has them, and its scale byte.
-template <bool FP8>
+// Eight values of a cached row as the cache has them, and their scale byte.
 struct Cached {
-    uint4 w; // codes: .x and .y
+    uint4 w; // e4m3: .x and .y, e2m1: .x
     uint32_t e;
 };
 
-template <int D, bool FP8>
-__device__ __forceinline__ Cached<FP8> get_row(const void *base, const uint8_t *exps, size_t row, int lane)
+template <int D, int CACHE>
+__device__ __forceinline__ Cached get_row(const void *base, const uint8_t *exps, size_t row, int lane)
 {
-    Cached<FP8> r{};
-    if (FP8) {
-        const uint2 w = reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(base) + row * D)[lane];
+    Cached r{};
+    const uint8_t *bytes = static_cast<const uint8_t *>(base);
+    if (CACHE == RA_E4M3) {
+        const uint2 w = reinterpret_cast<const uint2 *>(bytes + row * D)[lane];
         r.w.x = w.x;
         r.w.y = w.y;
         r.e = exps[row];
+    } else if (CACHE == RA_E2M1) {
+        r.w.x = reinterpret_cast<const uint32_t *>(bytes + row * (D / 2))[lane];
+        r.e = exps[row * (D / 32) + lane / 4];
     } else {
         r.w = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + row * D)[lane];
     }
     return r;
 }
 
-template <bool FP8>
-__device__ __forceinline__ Eight widen(const Cached<FP8> &c)
+template <int CACHE>
+__device__ __forceinline__ Eight widen(const Cached &c)
 {
-    if (!FP8) return widen(Raw<__nv_bfloat16>{{c.w}});
+    if (CACHE == RA_BF16) return widen(Raw<__nv_bfloat16>{{c.w}});
     const float s = exp_byte_scale(c.e);
-    const uint32_t h[4] = {c.w.x & 0xffffu, c.w.x >> 16, c.w.y & 0xffffu, c.w.y >> 16};
+    uint32_t h[4] = {c.w.x & 0xffffu, c.w.x >> 16, c.w.y & 0xffffu, c.w.y >> 16};
+    if (CACHE == RA_E2M1) e2m1x8_to_f16(c.w.x, h);
     Eight r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t x = e4m3x2_to_f16x2(h[i]);
+        const uint32_t x = CACHE == RA_E4M3 ? e4m3x2_to_f16x2(h[i]) : h[i];
         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
         r.x[2 * i] = f.x * s;
         r.x[2 * i + 1] = f.y * s;
@@ -253,7 +185,7 @@ __device__ __forceinline__ Eight widen(const Cached<FP8> &c)
     return r;
 }
 
-template <int D, bool FP8, typename T>
+template <int D, int CACHE, typename T>
 __global__ void __launch_bounds__(kThreads)
     kv_read_kernel(PagedCache c, T *__restrict__ k, T *__restrict__ v, int B, int L, const int32_t *__restrict__ table,
                    int max_pages, const int32_t *__restrict__ kv_len, int *status)
@@ -270,15 +202,15 @@ __global__ void __launch_bounds__(kThreads)
             page[u] = n < max_pages ? table[(size_t)b * max_pages + n] : -1;
         }
         if (blockIdx.x == 0 && threadIdx.x == 0 && (len < 0 || len > L)) report_bad_page(status);
-        Cached<FP8> kr[kUnroll] = {}, vr[kUnroll] = {};
+        Cached kr[kUnroll] = {}, vr[kUnroll] = {};
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const unsigned r = r0 + u * GROUPS, j = r / c.Hkv, h = r - j * c.Hkv;
             if (r < rows && (int)j < len) {
                 if (page[u] >= 0 && page[u] < c.n_pages) {
                     const size_t row = (((size_t)page[u] * c.Hkv + h) << c.page_shift) + (j & (c.page - 1));
-                    kr[u] = get_row<D, FP8>(c.k, c.k_exp, row, lane);
-                    vr[u] = get_row<D, FP8>(c.v, c.v_exp, row, lane);
+                    kr[u] = get_row<D, CACHE>(c.k, c.k_exp, row, lane);
+                    vr[u] = get_row<D, CACHE>(c.v, c.v_exp, row, lane);
                 } else {
                     report_bad_page(status);
                 }
@@ -289,8 +221,8 @@ __global__ void __launch_bounds__(kThreads)
             const unsigned r = r0 + u * GROUPS;
             if (r < rows) {
                 const size_t at = ((size_t)b * rows + r) * D + lane * 8;
-                store8(k + at, widen(kr[u]));
-                store8(v + at, widen(vr[u]));
+                store8(k + at, widen<CACHE>(kr[u]));
+                store8(v + at, widen<CACHE>(vr[u]));
             }
         }
     }
@@ -317,9 +249,11 @@ cudaError_t launch_kv_write(const PagedCache &c, int cache_dtype, const void *k,
     };
     auto typed = [&](auto *kp, auto *vp) {
         using T = std::remove_cv_t<std::remove_pointer_t<decltype(kp)>>;
+        if (cache_dtype == RA_E2M1)
+            return c.D == 64 ? go(kv_write_kernel<64, RA_E2M1, T>, kp, vp) : go(kv_write_kernel<128, RA_E2M1, T>, kp, vp);
         if (cache_dtype == RA_E4M3)
-            return c.D == 64 ? go(kv_write_kernel<64, true, T>, kp, vp) : go(kv_write_kernel<128, true, T>, kp, vp);
-        return c.D == 64 ? go(kv_write_kernel<64, false, T>, kp, vp) : go(kv_write_kernel<128, false, T>, kp, vp);
+            return c.D == 64 ? go(kv_write_kernel<64, RA_E4M3, T>, kp, vp) : go(kv_write_kernel<128, RA_E4M3, T>, kp, vp);
+        return c.D == 64 ? go(kv_write_kernel<64, RA_BF16, T>, kp, vp) : go(kv_write_kernel<128, RA_BF16, T>, kp, vp);
     };
     if (dtype == RA_BF16)
         return typed(static_cast<const __nv_bfloat16 *>(k), static_cast<const __nv_bfloat16 *>(v));
@@ -337,9 +271,11 @@ cudaError_t launch_kv_read(const PagedCache &c, int cache_dtype, const int32_t *
     };
     auto typed = [&](auto *kp, auto *vp) {
         using T = std::remove_pointer_t<decltype(kp)>;
+        if (cache_dtype == RA_E2M1)
+            return c.D == 64 ? go(kv_read_kernel<64, RA_E2M1, T>, kp, vp) : go(kv_read_kernel<128, RA_E2M1, T>, kp, vp);
         if (cache_dtype == RA_E4M3)
-            return c.D == 64 ? go(kv_read_kernel<64, true, T>, kp, vp) : go(kv_read_kernel<128, true, T>, kp, vp);
-        return c.D == 64 ? go(kv_read_kernel<64, false, T>, kp, vp) : go(kv_read_kernel<128, false, T>, kp, vp);
+            return c.D == 64 ? go(kv_read_kernel<64, RA_E4M3, T>, kp, vp) : go(kv_read_kernel<128, RA_E4M3, T>, kp, vp);
+        return c.D == 64 ? go(kv_read_kernel<64, RA_BF16, T>, kp, vp) : go(kv_read_kernel<128, RA_BF16, T>, kp, vp);
     };
     if (dtype == RA_BF16) return typed(static_cast<__nv_bfloat16 *>(k), static_cast<__nv_bfloat16 *>(v));
     return typed(static_cast<float *>(k), static_cast<float *>(v));

@@ -12,6 +12,10 @@ struct PagedCache {
     int n_pages, page, page_shift, Hkv, D;
 };
 
+// The checks of a cache that every call on it makes, and its device form.
+int check_cache(const ra_kv_cache *c);
+PagedCache cache_of(const ra_kv_cache *c);
+
 // One cached-attention problem.  Query rows of one kv head are numbered
 // i * G + g inside a sequence, and (b * Lq + i) * G + g over the batch.
 struct PagedProblem {

@@ -2,32 +2,10 @@
 // checks, the choice of kernels and the workspace's layout.
 #include <cuda.h>
 
-#include <cstdio>
-
+#include "ra_args.h"
 #include "ra_paged.h"
 
 namespace ra {
-namespace {
-
-int refuse(int code, const char *msg) { return set_last_error(code, msg); }
-
-template <typename... A>
-int refuse(int code, const char *fmt, A... a)
-{
-    char msg[256];
-    snprintf(msg, sizeof(msg), fmt, a...);
-    return set_last_error(code, msg);
-}
-
-const char *const kTooLarge = "too many query rows and pages for one call: split the batch";
-
-bool is_aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-bool overlap(const void *a, size_t an, const void *b, size_t bn)
-{
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + bn && y < x + an;
-}
 
 int check_cache(const ra_kv_cache *c)
 {
@@ -37,31 +15,20 @@ int check_cache(const ra_kv_cache *c)
     if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
         return refuse(RA_ERR_INVALID_ARG, "page_size must be 16, 32, 64 or 128 (got %d)", c->page_size);
     if (c->D != 64 && c->D != 128) return refuse(RA_ERR_UNSUPPORTED, "D must be 64 or 128 (got %d)", c->D);
-    if (c->dtype != RA_BF16 && c->dtype != RA_E4M3)
-        return refuse(RA_ERR_INVALID_ARG, "the cache's dtype must be RA_BF16 or RA_E4M3");
+    if (c->dtype != RA_BF16 && c->dtype != RA_E4M3 && c->dtype != RA_E2M1)
+        return refuse(RA_ERR_INVALID_ARG, "the cache's dtype must be RA_BF16, RA_E4M3 or RA_E2M1");
     if ((long long)c->n_pages * c->Hkv > 0x7fffffffll)
         return refuse(RA_ERR_UNSUPPORTED, "n_pages * Hkv must be below 2^31");
     if (!c->k || !c->v) return refuse(RA_ERR_INVALID_ARG, "cache tensors are NULL");
     if (!is_aligned(c->k, 16) || !is_aligned(c->v, 16))
         return refuse(RA_ERR_INVALID_ARG, "cache tensors must be 16-byte aligned");
-    if (c->dtype == RA_E4M3) {
-        if (!c->k_exp || !c->v_exp) return refuse(RA_ERR_INVALID_ARG, "an e4m3 cache needs k_exp and v_exp");
+    if (c->dtype != RA_BF16) {
+        if (!c->k_exp || !c->v_exp) return refuse(RA_ERR_INVALID_ARG, "an e4m3 or e2m1 cache needs k_exp and v_exp");
         if (!is_aligned(c->k_exp, 16) || !is_aligned(c->v_exp, 16))
             return refuse(RA_ERR_INVALID_ARG, "k_exp and v_exp must be 16-byte aligned");
     } else if (c->k_exp || c->v_exp) {
         return refuse(RA_ERR_INVALID_ARG, "a bf16 cache has no k_exp and v_exp");
     }
-    return RA_OK;
-}
-
-int check_dense(int B, int L, int Hkv, int dtype, const int32_t *page_table, int max_pages)
-{
-    if (B <= 0 || L <= 0 || max_pages <= 0)
-        return refuse(RA_ERR_INVALID_ARG, "sizes must be positive (B=%d L=%d max_pages=%d)", B, L, max_pages);
-    if (dtype != RA_BF16 && dtype != RA_FP32)
-        return refuse(RA_ERR_INVALID_ARG, "dtype must be RA_BF16 or RA_FP32");
-    if (!page_table) return refuse(RA_ERR_INVALID_ARG, "page_table is NULL");
-    if ((long long)L * Hkv > 0x7fffffffll) return refuse(RA_ERR_UNSUPPORTED, "L * Hkv must be below 2^31");
     return RA_OK;
 }
 
@@ -80,10 +47,26 @@ PagedCache cache_of(const ra_kv_cache *c)
     return x;
 }
 
+namespace {
+
+const char *const kTooLarge = "too many query rows and pages for one call: split the batch";
+
+int check_dense(int B, int L, int Hkv, int dtype, const int32_t *page_table, int max_pages)
+{
+    if (B <= 0 || L <= 0 || max_pages <= 0)
+        return refuse(RA_ERR_INVALID_ARG, "sizes must be positive (B=%d L=%d max_pages=%d)", B, L, max_pages);
+    if (dtype != RA_BF16 && dtype != RA_FP32)
+        return refuse(RA_ERR_INVALID_ARG, "dtype must be RA_BF16 or RA_FP32");
+    if (!page_table) return refuse(RA_ERR_INVALID_ARG, "page_table is NULL");
+    if ((long long)L * Hkv > 0x7fffffffll) return refuse(RA_ERR_UNSUPPORTED, "L * Hkv must be below 2^31");
+    return RA_OK;
+}
+
 int check_paged(const ra_kv_cache *c, const ra_paged_params *p)
 {
     const int rc = check_cache(c);
     if (rc) return rc;
+    if (c->dtype == RA_E2M1) return refuse(RA_ERR_UNSUPPORTED, "attention over an e2m1 cache is not implemented");
     if (!p) return refuse(RA_ERR_INVALID_ARG, "params is NULL");
     if (p->B <= 0 || p->Lq <= 0 || p->Hq <= 0)
         return refuse(RA_ERR_INVALID_ARG, "sizes must be positive (B=%d Lq=%d Hq=%d)", p->B, p->Lq, p->Hq);

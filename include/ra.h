@@ -78,7 +78,7 @@ enum {
      * position or a length in device memory was out of range (paged calls) */
 };
 
-enum { RA_BF16 = 0, RA_FP32 = 1, RA_E4M3 = 2 /* paged caches only */ };
+enum { RA_BF16 = 0, RA_FP32 = 1, RA_E4M3 = 2, RA_E2M1 = 3 /* the last two: paged caches only */ };
 enum { RA_TILE_EMPTY = 0, RA_TILE_PARTIAL = 1, RA_TILE_FULL = 2 };
 #define RA_TILE 128
 
@@ -455,17 +455,24 @@ RA_API int ra_unpermute_tokens(const void *in, void *out, int B, int L, size_t r
  *   n_pages, page_size  pages of the cache; 16, 32, 64 or 128 tokens each
  *   Hkv, D              kv heads, head size in {64, 128}
  *   dtype               RA_BF16: the values; RA_E4M3: 8-bit codes with a
- *                       power-of-two scale per row (one token of one kv head)
- *   k, v                (n_pages, Hkv, page_size, D) bf16 or e4m3, 16-byte
+ *                       power-of-two scale per row (one token of one kv head);
+ *                       RA_E2M1: 4-bit codes with one for each 32 of its values
+ *   k, v                (n_pages, Hkv, page_size, D) bf16 or e4m3, or
+ *                       (n_pages, Hkv, page_size, D / 2) bytes of two e2m1 codes,
+ *                       the even value's in the low four bits; 16-byte
  *                       aligned: the tokens of one head of a page lie
- *                       together, so that one tile load fetches them
- *   k_exp, v_exp        RA_E4M3: (n_pages, Hkv, page_size) uint8, 16-byte
- *                       aligned; RA_BF16: NULL
+ *                       together, so that one load fetches them
+ *   k_exp, v_exp        RA_E4M3: (n_pages, Hkv, page_size) uint8, RA_E2M1:
+ *                       (n_pages, Hkv, page_size, D / 32); 16-byte aligned;
+ *                       RA_BF16: NULL
  * An e4m3 row stands for code * 2^(exp - 127), where e = exp - 127 is the
  * smallest exponent >= -110 with max|row| <= 448 * 2^e: scaling by a power of
  * two is exact, so the one rounding is that of the code (to nearest even,
  * 2^-4 relative above 2^(e-6), 2^(e-10) absolute below).  A row holding an
  * infinity or a NaN gets exp = 255 and codes 0, and stands for NaN.
+ * The 32 values of an e2m1 block stand for code * 2^(exp - 127) likewise, with
+ * max|block| <= 6 * 2^e and codes of 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign (half
+ * a step: 2^-2 relative above 2^e, 2^(e-2) absolute below).
  */
 typedef struct {
     int n_pages, page_size, Hkv, D;
@@ -475,8 +482,8 @@ typedef struct {
 } ra_kv_cache;
 
 /*
- * Appends tokens to the cache, quantising them on the way (RA_E4M3) or
- * rounding them to bf16.
+ * Appends tokens to the cache, quantising them on the way (RA_E4M3, RA_E2M1)
+ * or rounding them to bf16.
  *   k, v        (B, L, Hkv, D) in `dtype` (RA_BF16 or RA_FP32), the rows of a
  *               token contiguous; k_stride / v_stride: elements from one
  *               token to the next (>= Hkv * D; a batch is L tokens), so that
@@ -593,6 +600,103 @@ RA_API size_t ra_attn_paged_workspace_size(const ra_kv_cache *cache, const ra_pa
  */
 RA_API int ra_attn_paged(const ra_kv_cache *cache, const ra_paged_params *p, const void *q,
                          void *out, float *lse, void *ws, size_t ws_bytes, ra_stream_t stream);
+
+/*
+ * Rotary positions.  Of a head's D values the first `rot` are turned in pairs,
+ * pair i of a token at position t by the angle t * f_i:
+ *   (a, b) -> amplitude * (a cos - b sin, b cos + a sin);
+ * the rest stays as it is.
+ *   rot           a multiple of 16, up to D; 0: no rotation
+ *   interleaved   1: pair i is values 2i and 2i + 1; 0: i and i + rot / 2
+ *   amplitude     multiplies the turned values (1, or what a scaling for long
+ *                 contexts asks for)
+ *   freq          (rot / 2) device: f_i / (2 pi), turns per position, as
+ *                 fractions of 2^64 (modulo 1).  Positions are multiplied with
+ *                 it modulo 2^64, so angles are exact however far they are.
+ */
+typedef struct {
+    int rot, interleaved;
+    float amplitude;
+    const uint64_t *freq;
+} ra_rope;
+
+/*
+ * What happens to queries and keys between their projection and attention: an
+ * RMS norm of each head, then the rotation.
+ *   y = rotate(x / sqrt(mean(x^2) + eps) * weight),  mean over the head's D
+ *   B, L          sequences, tokens of each
+ *   Hq, Hkv       heads of q and of k; either may be 0, its tensors NULL
+ *   D             64 or 128
+ *   dtype         RA_BF16 or RA_FP32, of q, k, their outputs and gradients
+ *   eps           0: no norm; else at least 1e-30
+ *   q_weight, k_weight   (D) in weight_dtype, 16-byte aligned, or NULL for ones
+ *   pos           (B, L) int32 positions, or NULL for
+ *                 start[b] + i + prefix_len[0], token i of sequence b
+ *   start         (B) int32 or NULL for 0; ra_qk_enter needs it
+ *   prefix_len    (1) int32 or NULL for 0 (ra_paged_params' shared prefix)
+ * Positions, start and prefix_len are read on the device when a kernel runs.
+ * Sums and products are fp32, rounded once to the output's type (a head whose
+ * squares add up to more than fp32 holds is scaled to 0).
+ */
+typedef struct {
+    int B, L, Hq, Hkv, D;
+    int dtype;
+    ra_rope rope;
+    float eps;
+    int weight_dtype;
+    const void *q_weight, *k_weight;
+    const int32_t *pos, *start, *prefix_len;
+} ra_qk_params;
+
+/*
+ * Forward.  q (B, L, Hq, D), k (B, L, Hkv, D) and the outputs of the same
+ * shapes: the heads of a token contiguous, tokens `stride` elements apart (a
+ * batch is L tokens), so that they may be slices of a fused projection; 16-byte
+ * aligned, strides in bytes multiples of 16.  An output may be its input (the
+ * same address and stride), and slices of one tensor may be different tensors
+ * here; other overlaps are refused.
+ * Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED, RA_ERR_CUDA.
+ */
+RA_API int ra_qk_fwd(const ra_qk_params *p, const void *q, size_t q_stride, const void *k, size_t k_stride, void *q_out,
+                     size_t q_out_stride, void *k_out, size_t k_out_stride, ra_stream_t stream);
+
+/* Workspace bytes of ra_qk_bwd (0 without a norm, or if `p` is invalid). */
+RA_API size_t ra_qk_bwd_workspace_size(const ra_qk_params *p);
+
+/*
+ * Backward: the gradient of ra_qk_fwd at q, k (not read, and may be NULL,
+ * without a norm).
+ *   dq_out, dk_out   the outputs' gradients
+ *   dq, dk           the inputs' gradients, overwritten; may be dq_out, dk_out
+ *                    or q, k (the same address and stride)
+ *   dq_weight, dk_weight   (D) fp32, overwritten with the weights' gradients,
+ *                    summed over tokens and heads; NULL: not wanted
+ *   ws               ra_qk_bwd_workspace_size bytes, 256-byte aligned; calls
+ *                    that may overlap in time need one each.  Results do not
+ *                    depend on timing: sums are joined in a fixed order.
+ * Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED, RA_ERR_WORKSPACE, RA_ERR_CUDA.
+ */
+RA_API int ra_qk_bwd(const ra_qk_params *p, const void *q, size_t q_stride, const void *k, size_t k_stride,
+                     const void *dq_out, size_t dq_out_stride, const void *dk_out, size_t dk_out_stride, void *dq,
+                     size_t dq_stride, void *dk, size_t dk_stride, float *dq_weight, float *dk_weight, void *ws,
+                     size_t ws_bytes, ra_stream_t stream);
+
+/*
+ * Tokens entering a paged cache: ra_qk_fwd's q into q_out, its k and v as it is
+ * into the cache, as ra_kv_write puts them (rounded once, from fp32), in one
+ * pass.
+ *   p            start is needed: token i of sequence b goes to position
+ *                start[b] + i of its own pages (turned by pos, if that is given)
+ *   v            (B, L, Hkv, D) in p->dtype, strided as q and k
+ *   page_table, max_pages, count   as for ra_kv_write; of q_out, too, rows
+ *                behind count[b] are left as they were.  A token that has no
+ *                place in the cache is skipped there and reported.
+ * q_out may be q (the same address and stride).
+ * Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED, RA_ERR_CUDA.
+ */
+RA_API int ra_qk_enter(const ra_qk_params *p, const ra_kv_cache *cache, const void *q, size_t q_stride, const void *k,
+                       size_t k_stride, const void *v, size_t v_stride, void *q_out, size_t q_out_stride,
+                       const int32_t *page_table, int max_pages, const int32_t *count, ra_stream_t stream);
 
 /*
  * Synchronises `stream`, then returns and clears the current device's status
