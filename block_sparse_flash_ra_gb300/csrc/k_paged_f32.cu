@@ -26,7 +26,7 @@
 
 #include <type_traits>
 
-#include "ra_paged.cuh"
+#include "ra_rows.cuh"
 
 namespace ra {
 namespace {
@@ -37,47 +37,52 @@ static_assert(kPagedF32Tile == kWarps * kWarpKeys, "a warp's keys lie in one pag
 constexpr int log2_of(int x) { return x < 2 ? 0 : 1 + log2_of(x / 2); }
 
 // Eight cached values as the cache has them.
-template <bool FP8>
 struct Raw8 {
-    uint4 w; // codes: .x and .y
+    uint4 w; // e4m3: .x and .y, e2m1: .x
 };
 
-template <bool FP8>
-__device__ __forceinline__ Raw8<FP8> load8(const void *base, size_t value)
+template <int CACHE>
+__device__ __forceinline__ Raw8 fetch8(const void *base, size_t value)
 {
-    Raw8<FP8> r;
-    if (FP8) {
+    Raw8 r{};
+    if (CACHE == RA_E4M3) {
         const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(base) + value);
         r.w.x = w.x;
         r.w.y = w.y;
+    } else if (CACHE == RA_E2M1) {
+        r.w.x = *reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(base) + value / 2);
     } else {
         r.w = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + value);
     }
     return r;
 }
 
-template <bool FP8>
-__device__ __forceinline__ void widen8(const Raw8<FP8> &r, float2 *x)
+template <int CACHE>
+__device__ __forceinline__ void widen8(const Raw8 &r, float2 *x)
 {
-    if (FP8) {
-        const uint32_t c[4] = {r.w.x & 0xffffu, r.w.x >> 16, r.w.y & 0xffffu, r.w.y >> 16};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t h = e4m3x2_to_f16x2(c[i]);
-            x[i] = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        }
-    } else {
+    if (CACHE == RA_BF16) {
         const uint32_t c[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             x[i] = make_float2(__uint_as_float(c[i] << 16), __uint_as_float(c[i] & 0xffff0000u));
+        return;
+    }
+    uint32_t h[4] = {r.w.x & 0xffffu, r.w.x >> 16, r.w.y & 0xffffu, r.w.y >> 16};
+    if (CACHE == RA_E2M1) e2m1x8_to_f16(r.w.x, h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = CACHE == RA_E4M3 ? e4m3x2_to_f16x2(h[i]) : h[i];
+        x[i] = __half22float2(*reinterpret_cast<const __half2 *>(&w));
     }
 }
 
-template <int D, bool FP8, int R>
-__global__ void __launch_bounds__(kThreads, paged_f32_per_sm(R, FP8))
+template <int D, int CACHE, int R>
+__global__ void __launch_bounds__(kThreads, paged_f32_per_sm(R, CACHE != RA_BF16))
     paged_f32_kernel(PagedProblem p, PagedPart part)
 {
+    // e4m3: a scale for the row, which its logit and its weight take; e2m1: one for
+    // each 32 values, which the lanes' values take
+    constexpr bool FP8 = CACHE == RA_E4M3, FP4 = CACHE == RA_E2M1;
     constexpr int LANES = D / 8, STEP = 32 / LANES, STEPS = kWarpKeys / STEP; // lanes of a key; keys at once
     constexpr int REST = log2_of(LANES) - log2_of(R); // lanes that hold the same row, as a power of two
     constexpr uint32_t ALL = 0xffffffffu;
@@ -119,14 +124,14 @@ __global__ void __launch_bounds__(kThreads, paged_f32_per_sm(R, FP8))
             if (!page_valid(p, page)) return -1;
             return (((long long)page * p.c.Hkv + c.h) << p.c.page_shift) + (first & (p.c.page - 1));
         };
-        Raw8<FP8> k[STEPS], v[STEPS];
-        auto fetch = [&](Raw8<FP8> *x, const void *base, long long at, int t) {
+        Raw8 k[STEPS], v[STEPS];
+        auto fetch = [&](Raw8 *x, const void *base, long long at, int t) {
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 const int j = s * STEP + kg;
                 x[s].w = make_uint4(0, 0, 0, 0);
                 if (at >= 0 && t * kPagedF32Tile + warp * kWarpKeys + j < len)
-                    x[s] = load8<FP8>(base, (size_t)(at + j) * D + sub * 8);
+                    x[s] = fetch8<CACHE>(base, (size_t)(at + j) * D + sub * 8);
             }
         };
         long long at = place(c.t0);
@@ -136,13 +141,14 @@ __global__ void __launch_bounds__(kThreads, paged_f32_per_sm(R, FP8))
             const long long next = t + 1 < c.t0 + n ? place(t + 1) : -1;
             fetch(v, p.c.v, at, t);
             uint32_t ke[STEPS], ve[STEPS];
-            if (FP8) {
+            if (FP8 || FP4) {
 #pragma unroll
                 for (int s = 0; s < STEPS; ++s) {
                     const int j = s * STEP + kg;
                     const bool there = at >= 0 && first + j < len; // else zeros, at a scale of one
-                    ke[s] = there ? p.c.k_exp[at + j] : 127u;
-                    ve[s] = there ? p.c.v_exp[at + j] : 127u;
+                    const long long e = FP4 ? (at + j) * (D / 32) + sub / 4 : at + j;
+                    ke[s] = there ? p.c.k_exp[e] : 127u;
+                    ve[s] = there ? p.c.v_exp[e] : 127u;
                 }
             }
             // ---- logits of row `own`
@@ -151,7 +157,12 @@ __global__ void __launch_bounds__(kThreads, paged_f32_per_sm(R, FP8))
             for (int s = 0; s < STEPS; ++s) {
                 float2 kf[4];
                 float d[R];
-                widen8<FP8>(k[s], kf);
+                widen8<CACHE>(k[s], kf);
+                if (FP4) {
+                    const float e = exp_byte_scale(ke[s]);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) kf[y] = fmul2(kf[y], make_float2(e, e));
+                }
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     float2 z = fmul2(qr[r][0], kf[0]);
@@ -204,7 +215,12 @@ __global__ void __launch_bounds__(kThreads, paged_f32_per_sm(R, FP8))
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 float2 vf[4];
-                widen8<FP8>(v[s], vf);
+                widen8<CACHE>(v[s], vf);
+                if (FP4) {
+                    const float e = exp_byte_scale(ve[s]);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) vf[y] = fmul2(vf[y], make_float2(e, e));
+                }
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const float e = __shfl_sync(ALL, x[s], kg * LANES + (r << REST));
@@ -281,15 +297,16 @@ __global__ void __launch_bounds__(kThreads, paged_f32_per_sm(R, FP8))
 cudaError_t launch_paged_f32(const PagedProblem &p, const PagedPart &part, int cache_dtype, cudaStream_t s)
 {
     auto go = [&](auto kern) { return launch_dependent(kern, (unsigned)part.ctas, kThreads, 0, s, p, part); };
-    auto sized = [&](auto d, auto fp8) {
-        constexpr int D = decltype(d)::value;
-        constexpr bool FP8 = decltype(fp8)::value;
-        return part.row_block == 4 ? go(paged_f32_kernel<D, FP8, 4>) : go(paged_f32_kernel<D, FP8, 8>);
+    auto sized = [&](auto d, auto cache) {
+        constexpr int D = decltype(d)::value, CACHE = decltype(cache)::value;
+        return part.row_block == 4 ? go(paged_f32_kernel<D, CACHE, 4>) : go(paged_f32_kernel<D, CACHE, 8>);
     };
-    auto typed = [&](auto fp8) {
-        return p.c.D == 64 ? sized(std::integral_constant<int, 64>{}, fp8) : sized(std::integral_constant<int, 128>{}, fp8);
+    auto typed = [&](auto cache) {
+        return p.c.D == 64 ? sized(std::integral_constant<int, 64>{}, cache) : sized(std::integral_constant<int, 128>{}, cache);
     };
-    return cache_dtype == RA_E4M3 ? typed(std::true_type{}) : typed(std::false_type{});
+    return cache_dtype == RA_E2M1   ? typed(std::integral_constant<int, RA_E2M1>{})
+           : cache_dtype == RA_E4M3 ? typed(std::integral_constant<int, RA_E4M3>{})
+                                    : typed(std::integral_constant<int, RA_BF16>{});
 }
 
 } // namespace ra

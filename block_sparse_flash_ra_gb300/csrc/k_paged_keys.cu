@@ -67,6 +67,7 @@
 
 #include "ra_paged.cuh"
 #include "ra_sched.cuh"
+#include "ra_wide4.cuh"
 
 namespace ra {
 namespace {
@@ -90,16 +91,26 @@ constexpr float kQuiet = 30.f, kPass = 60.f, kFallFrom = 100.f, kFallTo = 140.f;
 // range, but O's sums of weights times values need some of it.
 constexpr float kPass16 = 16.f;
 
-template <bool FP8, int RP, int D>
+template <int CACHE, int RP, int D>
 struct Cfg {
+    static constexpr bool FP8 = CACHE != RA_BF16, FP4 = CACHE == RA_E2M1; // products of e4m3; widened to it
     static constexpr int kPar = kD / D, kTokens = kKeys * kPar; // tokens of a row, of a tile
     static constexpr int kMat = kKeys * kD * (FP8 ? 1 : 2); // bytes of a K or V tile
     static constexpr int kHalves = FP8 ? 1 : 2;             // 128-byte wide blocks of a tile
-    static constexpr int kGroups = RP / kRT, kSoftThreads = 128 * kGroups, kThreads = kSoftThreads + 64;
-    static constexpr int kMmaWarp = 4 * kGroups, kLoadWarp = kMmaWarp + 1;
+    static constexpr int kGroups = RP / kRT, kSoftThreads = 128 * kGroups, kWideThreads = FP4 ? 128 : 0;
+    static constexpr int kThreads = kSoftThreads + kWideThreads + 64;
+    static constexpr int kWideWarp = 4 * kGroups, kMmaWarp = kWideWarp + kWideThreads / 32, kLoadWarp = kMmaWarp + 1;
     static constexpr int kCtasPerSm = FP8 && RP <= 16 ? 2 : 1;
-    static constexpr int kStages = FP8 ? (RP == 8 ? 3 : RP == 16 ? 2 : 5) : 3;
-    static constexpr int kVStages = FP8 ? (RP > 16 ? 5 : 3) : RP > 16 ? 2 : 3;
+    static constexpr int kStages = FP4 ? (RP > 16 ? 3 : 2) : FP8 ? (RP == 8 ? 3 : RP == 16 ? 2 : 5) : 3;
+    static constexpr int kVStages = FP4 ? kStages : FP8 ? (RP > 16 ? 5 : 3) : RP > 16 ? 2 : 3;
+    // 4 bits: half tiles of codes, K low, K high, V low, V high of a tile in turn,
+    // and the tiles' scale bytes, four to a row of K and of V
+    static constexpr int kRaw = kKeys * kD / 4, kRaws = !FP4 ? 0 : RP == 8 ? 7 : RP == 16 ? (D == 128 ? 5 : 4) : 16;
+    static constexpr int kXs = !FP4 ? 0 : RP > 16 ? 6 : 3, kX = 2 * kKeys * 4;
+    // the rows' scale bytes: where TMA brings them, beside V; widened, a tile's
+    // come with its K, for which S of kStages tiles before has waited until the
+    // softmax had those of two more
+    static constexpr int kEStages = FP4 ? kStages + 2 : kVStages;
     static constexpr int kQTerms = FP8 ? 2 : 1, kPTerms = FP8 ? 3 : 2;
     static constexpr int kNS = (RP * kQTerms + 15) / 16 * 16;             // columns of S^T
     static constexpr int kNO = (RP * kPTerms + 15) / 16 * 16;             // columns of O^T
@@ -110,15 +121,18 @@ struct Cfg {
     static constexpr int kVOff = kKOff + kStages * kMat;
     static constexpr int kQOff = kVOff + kVStages * kMat;
     static constexpr int kPOff = kQOff + 2 * kQBytes; // Q of the present and of the next segment
-    static constexpr int kExpOff = kPOff + 2 * kPBytes; // per V stage: scale bytes of K, of V
-    static constexpr int kRowOff = kExpOff + (FP8 ? kVStages * 2 * kTokens : 0);
+    static constexpr int kRawOff = kPOff + 2 * kPBytes;
+    static constexpr int kXOff = kRawOff + kRaws * kRaw;
+    static constexpr int kTableOff = kXOff + kXs * kX;
+    static constexpr int kExpOff = kTableOff + (FP4 ? 256 : 0); // per stage: scale bytes of K, of V
+    static constexpr int kRowOff = kExpOff + (FP8 ? kEStages * 2 * kTokens : 0);
     // per row of both segments: place of its output and of its lse (two words each), logit scale, keys it sees;
     // then its factor
     static constexpr int kRowBytes = RP * 24;
     static constexpr int kRedOff = kRowOff + 2 * kRowBytes + RP * 4;
     static constexpr int kOddOff = kRedOff + 4 * kGroups * (kRT + 4) * 4; // O of odd tokens, where rows are pairs
     static constexpr int kBarOff = kOddOff + (kPar == 2 ? RP / 2 * D * 4 : 0);
-    static constexpr int kNumBars = 2 * kStages + 3 * kVStages + 2 + 2 + 2 + 2 + 2 + 1;
+    static constexpr int kNumBars = 2 * kStages + 2 * kVStages + kEStages + 2 + 2 + 2 + 2 + 2 + 1 + 2 * kRaws + 2 * kXs;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kSmem = kMiscOff + 16 + 1024;
     static constexpr uint32_t kColO = 2 * kNS;
@@ -135,6 +149,7 @@ struct Cfg {
 
 struct Bars {
     uint64_t *k_full, *k_empty, *v_full, *v_empty, *e_full, *s_full, *s_empty, *p_full, *pv_done, *q_full, *drain;
+    uint64_t *raw_full, *raw_empty, *x_full, *x_empty;
 };
 
 template <class C>
@@ -146,12 +161,16 @@ __device__ __forceinline__ Bars carve(uint8_t *smem)
     b.v_full = b.k_empty + C::kStages;
     b.v_empty = b.v_full + C::kVStages;
     b.e_full = b.v_empty + C::kVStages;
-    b.s_full = b.e_full + C::kVStages;
+    b.s_full = b.e_full + C::kEStages;
     b.s_empty = b.s_full + 2;
     b.p_full = b.s_empty + 2;
     b.pv_done = b.p_full + 2;
     b.q_full = b.pv_done + 2;
     b.drain = b.q_full + 2; // q_full by segment parity
+    b.raw_full = b.drain + 1;
+    b.raw_empty = b.raw_full + C::kRaws;
+    b.x_full = b.raw_empty + C::kRaws;
+    b.x_empty = b.x_full + C::kXs;
     return b;
 }
 
@@ -241,12 +260,13 @@ __device__ __forceinline__ uint32_t tile_chunk(int j, int c)
     return (c >> 3) * (kKeys * 128) + j * 128 + (((c & 7) ^ (j & 7)) << 4);
 }
 
-template <bool FP8, int RP, int D>
-__global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kCtasPerSm)
+template <int CACHE, int RP, int D>
+__global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>::kCtasPerSm)
     paged_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       PagedProblem p, PagedPart part)
 {
-    using C = Cfg<FP8, RP, D>;
+    using C = Cfg<CACHE, RP, D>;
+    constexpr bool FP8 = C::FP8, FP4 = C::FP4;
     constexpr int kPar = C::kPar, kTokens = C::kTokens;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -257,13 +277,21 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(bars.k_full + s, 1);
+            mbar_init(bars.k_full + s, FP4 ? C::kWideThreads : 1);
             mbar_init(bars.k_empty + s, 1);
         }
         for (int s = 0; s < C::kVStages; ++s) {
-            mbar_init(bars.v_full + s, 1);
+            mbar_init(bars.v_full + s, FP4 ? C::kWideThreads : 1);
             mbar_init(bars.v_empty + s, 1);
-            mbar_init(bars.e_full + s, 1);
+        }
+        for (int s = 0; s < C::kEStages; ++s) mbar_init(bars.e_full + s, FP4 ? C::kWideThreads : 1);
+        for (int s = 0; s < C::kRaws; ++s) {
+            mbar_init(bars.raw_full + s, 1);
+            mbar_init(bars.raw_empty + s, C::kWideThreads);
+        }
+        for (int s = 0; s < C::kXs; ++s) {
+            mbar_init(bars.x_full + s, 1);
+            mbar_init(bars.x_empty + s, C::kWideThreads);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(bars.s_full + s, FP8 ? 2 : 1);
@@ -280,10 +308,12 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
         tmem_alloc(tmem_holder, C::kCols);
         tmem_relinquish();
     }
-    if (warp == C::kLoadWarp && lane == 0) {
+    if (!FP4 && warp == C::kLoadWarp && lane == 0) {
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
+    uint2 *table = reinterpret_cast<uint2 *>(smem + C::kTableOff);
+    if (FP4 && threadIdx.x < kWide4Entries) wide4_fill(table, threadIdx.x);
     begin_in_order(part);
     report_lengths(p, part);
     PagedCursor c; // found beside the barriers' and TMEM's setting up
@@ -297,7 +327,129 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
     };
     auto source_len = [&](int b) { return part.prefix ? paged_prefix_len(p) : paged_kv_len(p, b); };
 
-    if (any && warp == C::kLoadWarp) {
+    if (FP4 && any && warp == C::kLoadWarp) {
+        // ------------------------------------------------------------ loads, 4 bits
+        // lane x fetches box x of a tile, of at most half of it: a page's codes of a
+        // head lie together, so that plain bulk copies do
+        constexpr int kItem = kTokens / 2, kRowX = D / 32; // tokens of a half tile, scale bytes of a token
+        const int box = min(p.c.page, kItem), per = kTokens / box, in_item = kItem / box;
+        uint32_t i = 0, r = 0;
+        bool ok = true;
+        auto entry = [&](int tile, int len) {
+            const int first = tile * kTokens + lane * box;
+            return lane < per && first < len ? page_entry(p, part, c.b, first) : 0;
+        };
+        for (;;) {
+            const int n = cursor_take(c), len = source_len(c.b);
+            int next = entry(c.t0, len);
+            for (int t = c.t0; ok && t < c.t0 + n; ++t, ++i) {
+                const int page = next, first = t * kTokens;
+                const int boxes = max(0, (min(len - first, kTokens) + box - 1) / box);
+                if (t + 1 < c.t0 + n) next = entry(t + 1, len);
+                const bool mine = lane < boxes, good = mine && page_valid(p, page);
+                const size_t row = good ? ((((size_t)page * p.c.Hkv + c.h) << p.c.page_shift) + ((first + lane * box) & (p.c.page - 1))) : 0;
+                const uint32_t goods = __ballot_sync(0xffffffffu, good);
+                const int sx = i % C::kXs;
+                if (!(ok = wait_all(bars.x_empty + sx, ((i / C::kXs) & 1) ^ 1))) break;
+                uint8_t *x = smem + C::kXOff + sx * C::kX + lane * box * kRowX;
+                if (mine && !good) { // zeros, at a scale of one
+                    for (int j = 0; j < box * kRowX; ++j) x[j] = x[C::kX / 2 + j] = 127;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                __syncwarp();
+                if (lane == 0) mbar_expect_tx(bars.x_full + sx, 2 * __popc(goods) * box * kRowX);
+                __syncwarp();
+                if (good) {
+                    bulk_load(x, p.c.k_exp + row * kRowX, box * kRowX, bars.x_full + sx);
+                    bulk_load(x + C::kX / 2, p.c.v_exp + row * kRowX, box * kRowX, bars.x_full + sx);
+                }
+#pragma unroll 1
+                for (int it = 0; it < 4; ++it, ++r) { // K low, K high, V low, V high
+                    const int sr = r % C::kRaws, lo = (it & 1) * in_item;
+                    if (!(ok = wait_all(bars.raw_empty + sr, ((r / C::kRaws) & 1) ^ 1))) break;
+                    const bool here = lane >= lo && lane < lo + in_item;
+                    uint8_t *dst = smem + C::kRawOff + sr * C::kRaw + (lane - lo) * box * (D / 2);
+                    if (here && mine && !good) {
+                        for (int j = 0; j < box * (D / 2); j += 16) *reinterpret_cast<uint4 *>(dst + j) = make_uint4(0, 0, 0, 0);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    }
+                    __syncwarp();
+                    const uint32_t in = __ballot_sync(0xffffffffu, here && good);
+                    if (lane == 0) mbar_expect_tx(bars.raw_full + sr, __popc(in) * box * (D / 2));
+                    __syncwarp();
+                    if (here && good)
+                        bulk_load(dst, static_cast<const uint8_t *>(it < 2 ? p.c.k : p.c.v) + row * (D / 2), box * (D / 2), bars.raw_full + sr);
+                }
+            }
+            if (!ok || !cursor_next(p, part, c, n)) break;
+        }
+        if (!ok || *abort_flag) {
+            // copies on their way land before the CTA ends (as below)
+            for (uint32_t j = r > (uint32_t)C::kRaws ? r - C::kRaws : 0; j < r; ++j)
+                wait_drain(bars.raw_full + j % C::kRaws, (j / C::kRaws) & 1, kDrainNs);
+            for (uint32_t j = i >= (uint32_t)C::kXs ? i + 1 - C::kXs : 0; j <= i; ++j)
+                wait_drain(bars.x_full + j % C::kXs, (j / C::kXs) & 1, kDrainNs);
+        }
+    } else if (FP4 && any && warp >= C::kWideWarp && warp < C::kMmaWarp) {
+        // ------------------------------------------------------------ widening
+        // a thread takes blocks of 32 codes (16 bytes, a quarter of a row of 128
+        // values), which become two 16-byte chunks of the e4m3 tile
+        const int wt = threadIdx.x - C::kWideWarp * 32, x = wt & 3;
+        uint32_t i = 0, r = 0;
+        bool ok = true;
+        for (;;) {
+            const int n = cursor_take(c), len = source_len(c.b);
+            for (int t = c.t0; ok && t < c.t0 + n; ++t, ++i) {
+                const int sx = i % C::kXs, st = i % C::kStages;
+                const int valid = min(len - t * kTokens, kTokens);
+                const uint32_t *xs = reinterpret_cast<const uint32_t *>(smem + C::kXOff + sx * C::kX); // K's, then V's
+                if (!(ok = wait_all(bars.x_full + sx, (i / C::kXs) & 1))) break;
+                if (!(ok = wait_all(bars.k_empty + st, ((i / C::kStages) & 1) ^ 1))) break;
+                uint8_t *e = smem + C::kExpOff + (i % C::kEStages) * 2 * kTokens;
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int y = 0; y < kPar; ++y) {
+                        const int tok = wt * kPar + y;
+                        e[m * kTokens + tok] = tok < valid ? wide4_top<kPar == 2>(xs[m * kKeys + wt], y) - kWide4Up : 127;
+                    }
+                mbar_arrive(bars.e_full + i % C::kEStages);
+#pragma unroll 1
+                for (int it = 0; it < 4; ++it, ++r) {
+                    const int sr = r % C::kRaws, m = it >> 1, half = it & 1;
+                    if (it == 2 && !(ok = wait_all(bars.v_empty + st, ((i / C::kStages) & 1) ^ 1))) break;
+                    if (!(ok = wait_all(bars.raw_full + sr, (r / C::kRaws) & 1))) break;
+                    const uint32_t raw = smem_u32(smem + C::kRawOff + sr * C::kRaw) + wt * 16;
+                    const uint32_t tile = smem_u32(smem + (m ? C::kVOff : C::kKOff) + st * C::kMat);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int j = half * 64 + u * 32 + (wt >> 2); // row of the tile
+                        uint4 w;
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(raw + u * 2048));
+                        const uint32_t word = xs[m * kKeys + j];
+                        const uint2 tab = wide4_entry(table, wide4_top<kPar == 2>(word, x >> 1), word >> (8 * x) & 0xffu);
+                        uint2 o[4] = {wide4(w.x, tab), wide4(w.y, tab), wide4(w.z, tab), wide4(w.w, tab)};
+                        // (tokens behind the length: whatever is there, weight 0 must give 0)
+                        if (j * kPar + (kPar == 2 ? x >> 1 : 0) >= valid) o[0] = o[1] = o[2] = o[3] = make_uint2(0, 0);
+                        const uint32_t at = tile + j * 128;
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((2 * x) ^ (j & 7)) << 4)), "r"(o[0].x),
+                                     "r"(o[0].y), "r"(o[1].x), "r"(o[1].y)
+                                     : "memory");
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((2 * x + 1) ^ (j & 7)) << 4)), "r"(o[2].x),
+                                     "r"(o[2].y), "r"(o[3].x), "r"(o[3].y)
+                                     : "memory");
+                    }
+                    mbar_arrive(bars.raw_empty + sr);
+                    if (half) {
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        mbar_arrive((m ? bars.v_full : bars.k_full) + st);
+                    }
+                }
+                if (ok) mbar_arrive(bars.x_empty + sx);
+            }
+            if (!ok || !cursor_next(p, part, c, n)) break;
+        }
+    } else if (any && warp == C::kLoadWarp) {
         // ------------------------------------------------------------ loads
         // lane x fetches box x of a tile: its page number, then its K and V
         const int box = min(p.c.page, kTokens) / kPar, per = kKeys / box; // rows
@@ -398,10 +550,10 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
             for (int t = 0; ok && t < n; ++t, ++i) {
                 const int sk = i % C::kStages, sb = i & 1;
                 if (!(ok = wait_all(bars.k_full + sk, (i / C::kStages) & 1))) break;
-                if (FP8 && !(ok = wait_all(bars.e_full + i % C::kVStages, (i / C::kVStages) & 1))) break;
+                if (FP8 && !(ok = wait_all(bars.e_full + i % C::kEStages, (i / C::kEStages) & 1))) break;
                 if (!(ok = wait_all(bars.s_empty + sb, ((i >> 1) & 1) ^ 1))) break;
                 tc_fence_after();
-                if (kPar == 2) {
+                if (kPar == 2 && !FP4) {
                     // an odd length ends inside a row: its other token meets the zeros of
                     // Q, and is made zero too, whatever is there
                     const int valid = len - (c.t0 + t) * kTokens, j = valid >> 1;
@@ -557,7 +709,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
                 tc_fence_after();
                 tmem_ld8(lane_base + sb * C::kNS + row0, s);
                 if (FP8) {
-                    const uint8_t *e = smem + C::kExpOff + sv * 2 * kTokens + tok;
+                    const uint8_t *e = smem + C::kExpOff + (i % C::kEStages) * 2 * kTokens + tok;
 #pragma unroll
                     for (int y = 0; y < kPar; ++y) {
                         const uint32_t vb = e[kTokens + y];
@@ -723,7 +875,7 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
                                  "r"(lo[1]), "r"(lo[2]), "r"(lo[3])
                                  : "memory");
                 }
-                if (valid < kTokens) {
+                if (!FP4 && valid < kTokens) {
                     // values behind the length: whatever is there, weight 0 must give 0
                     wait(bars.v_full + sv, (i / C::kVStages) & 1);
                     if (grp == 0 && tok + kPar > valid)
@@ -837,11 +989,11 @@ __global__ void __launch_bounds__(Cfg<FP8, RP, D>::kThreads, Cfg<FP8, RP, D>::kC
     }
 }
 
-template <bool FP8, int RP, int D>
+template <int CACHE, int RP, int D>
 cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s)
 {
-    using C = Cfg<FP8, RP, D>;
-    auto kern = paged_keys_kernel<FP8, RP, D>;
+    using C = Cfg<CACHE, RP, D>;
+    auto kern = paged_keys_kernel<CACHE, RP, D>;
     static std::atomic<uint64_t> set{0}; // devices whose copy of the kernel has its attribute
     const uint64_t bit = 1ull << p.device;
     if (!(set.load(std::memory_order_acquire) & bit)) {
@@ -859,18 +1011,19 @@ cudaError_t launch_paged_keys(const PagedProblem &p, const PagedPart &part, int 
 {
     const CUtensorMap &k = *static_cast<const CUtensorMap *>(tm_k), &v = *static_cast<const CUtensorMap *>(tm_v);
     const int cols = part.row_block * (kD / p.c.D);
-    auto typed = [&](auto fp8, auto d) {
-        constexpr bool FP8 = decltype(fp8)::value;
-        constexpr int D = decltype(d)::value;
-        return cols == 8    ? go<FP8, 8, D>(p, part, k, v, s)
-               : cols == 16 ? go<FP8, 16, D>(p, part, k, v, s)
-               : cols == 24 ? go<FP8, 24, D>(p, part, k, v, s)
-                            : go<FP8, 32, D>(p, part, k, v, s);
+    auto typed = [&](auto cache, auto d) {
+        constexpr int CACHE = decltype(cache)::value, D = decltype(d)::value;
+        return cols == 8    ? go<CACHE, 8, D>(p, part, k, v, s)
+               : cols == 16 ? go<CACHE, 16, D>(p, part, k, v, s)
+               : cols == 24 ? go<CACHE, 24, D>(p, part, k, v, s)
+                            : go<CACHE, 32, D>(p, part, k, v, s);
     };
-    auto sized = [&](auto fp8) {
-        return p.c.D == 64 ? typed(fp8, std::integral_constant<int, 64>{}) : typed(fp8, std::integral_constant<int, 128>{});
+    auto sized = [&](auto cache) {
+        return p.c.D == 64 ? typed(cache, std::integral_constant<int, 64>{}) : typed(cache, std::integral_constant<int, 128>{});
     };
-    return cache_dtype == RA_E4M3 ? sized(std::true_type{}) : sized(std::false_type{});
+    return cache_dtype == RA_E2M1   ? sized(std::integral_constant<int, RA_E2M1>{})
+           : cache_dtype == RA_E4M3 ? sized(std::integral_constant<int, RA_E4M3>{})
+                                    : sized(std::integral_constant<int, RA_BF16>{});
 }
 
 } // namespace ra

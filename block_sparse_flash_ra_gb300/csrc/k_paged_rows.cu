@@ -46,7 +46,7 @@
 #include <atomic>
 #include <type_traits>
 
-#include "ra_paged.cuh"
+#include "ra_rows.cuh"
 #include "ra_sched.cuh"
 
 namespace ra {
@@ -63,10 +63,12 @@ constexpr int kWideWarpK = 16, kWideWarpV = 20, kLoadWarp = 24, kMmaWarp = 26;
 // S to P, which the ping-pong of two tiles does not hide (one thread per row
 // took 2200 cycles of a tile's 4000; the products need 2460).
 
-template <bool FP8>
+template <int CACHE>
 struct Cfg {
+    static constexpr bool FP8 = CACHE != RA_BF16, FP4 = CACHE == RA_E2M1; // widened to f16; from 4 bits
     static constexpr int kMat = kKeys * kD * 2; // a 16-bit tile, 32 KB: two blocks of 128 rows x 128 bytes
-    static constexpr int kRaw = kHalf * kD;     // half a tile of codes
+    static constexpr int kRowRaw = FP4 ? kD / 2 : kD, kRowX = FP4 ? kD / 32 : 1; // codes and scale bytes of a row
+    static constexpr int kRaw = kHalf * kRowRaw; // half a tile of codes
     static constexpr int kRaws = FP8 ? 4 : 0;   // K low, K high, V low, V high of a tile, in turn
     static constexpr int kQOff = 0;
     static constexpr int kKOff = 2 * kMat;
@@ -74,7 +76,7 @@ struct Cfg {
     static constexpr int kRawOff = kVOff + 2 * kMat;
     // scale bytes of K tiles [2] and V tiles [2]: a tile's come before its second half
     static constexpr int kExpOff = kRawOff + kRaws * kRaw;
-    static constexpr int kBarOff = kExpOff + (FP8 ? 4 * kKeys : 0);
+    static constexpr int kBarOff = kExpOff + (FP8 ? 4 * kKeys * kRowX : 0);
     // k_full[2], k_empty[2], v_full[2], v_empty[2], raw_full[4], raw_empty[4],
     // q_full[2], s_full[2], p_full[2], o_full[2], v_clear[2], ev_full[4],
     // e_full[4], drain
@@ -189,6 +191,7 @@ __device__ __forceinline__ void widen_half(uint32_t tile, uint32_t raw, const ui
 // still halves: the rows of a half tile that lie so far below its exponent are
 // widened again, with their scale in two steps, the first of which is exact.
 constexpr int kHalfLeast = 24, kFarStep = 12;
+constexpr int kUp4 = 6; // 6 * 2^6 is the most that a block's code becomes, as 448 a row's
 __device__ __noinline__ void widen_far(uint32_t tile, uint32_t raw, const uint8_t *exps, int row0, int valid, int e,
                                        int warp, int lane)
 {
@@ -217,6 +220,47 @@ __device__ __noinline__ void widen_far(uint32_t tile, uint32_t raw, const uint8_
     }
 }
 
+// The same from 4 bits: a thread takes a row's block x of 32 codes, which become
+// 64 bytes of one half of the f16 tile.  Lanes 4-7 of a group of 8 take the row 3
+// apart (by exclusive or), and the upper two blocks their chunks in another
+// order, which again puts a phase's accesses on different banks.  FAR: only the
+// blocks that lie below a half's least scale, in two steps.
+template <bool FAR>
+__device__ __forceinline__ void widen_blocks(uint32_t tile, uint32_t raw, const uint8_t *exps, int row0, int valid, int e,
+                                             int warp, int lane)
+{
+    const int x = lane & 3, hi = x >> 1, g = lane >> 3, in8 = ((g >> 1) * 4 + (g & 1)) ^ (lane & 4 ? 3 : 0);
+#pragma unroll 1
+    for (int jg = 0; jg < 2; ++jg) {
+        const int j = (warp * 2 + jg) * 8 + in8; // row of the half tile
+        const uint32_t b = exps[j * 4 + x];
+        const bool live = row0 + j < valid;
+        if (FAR && (!live || (int)b - e >= -kHalfLeast)) continue;
+        const __half2 s1 = half_scale(127 - kFarStep, 127), s = half_scale(b, FAR ? e - kFarStep : e);
+        const uint4 w = lds128(raw + j * 64 + x * 16);
+        const uint32_t u[4] = {hi ? w.y : w.x, hi ? w.x : w.y, hi ? w.w : w.z, hi ? w.z : w.w};
+        const uint32_t at = tile + hi * (kKeys * 128) + (row0 + j) * 128;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) { // eight codes each
+            uint32_t o[4];
+            e2m1x8_to_f16(u[q], o);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                __half2 r = *reinterpret_cast<const __half2 *>(&o[y]);
+                if (FAR) r = __hmul2(r, s1);
+                r = __hmul2(r, s);
+                o[y] = live ? *reinterpret_cast<const uint32_t *>(&r) : 0u;
+            }
+            sts128(at + ((((x & 1) * 4 + (q ^ hi)) ^ (j & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+        }
+    }
+}
+__device__ __noinline__ void widen_far_blocks(uint32_t tile, uint32_t raw, const uint8_t *exps, int row0, int valid, int e,
+                                              int warp, int lane)
+{
+    widen_blocks<true>(tile, raw, exps, row0, valid, e, warp, lane);
+}
+
 // 32 stored weights of every thread times f, a power of two; in two steps where
 // it is no half itself.  Rare, so kept out of the loop's code.
 template <bool FP8>
@@ -242,12 +286,13 @@ __device__ __noinline__ void scale_stored(uint32_t at, float f)
     tmem_st16(at, u);
 }
 
-template <bool FP8, bool CAP>
+template <int CACHE, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       PagedProblem p, PagedPart part)
 {
-    using C = Cfg<FP8>;
+    using C = Cfg<CACHE>;
+    constexpr bool FP8 = C::FP8, FP4 = C::FP4;
     extern __shared__ __align__(1024) uint8_t smem[];
     const Bars bars = carve<C>(smem);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::kMiscOff);
@@ -285,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(tmem_holder, 512);
         tmem_relinquish();
     }
-    if (warp == kLoadWarp && lane == 0) {
+    if (!FP4 && warp == kLoadWarp && lane == 0) {
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
@@ -338,24 +383,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (!(ok = wait_all(bars.raw_empty + rs, (g & 1) ^ 1))) break;
                             if (y == 0) {
                                 // the tile's scale bytes (this stage's last user is widened)
-                                uint8_t *e = smem + C::kExpOff + (2 * m + st) * kKeys + lane * box;
+                                constexpr int X = C::kRowX;
+                                uint8_t *e = smem + C::kExpOff + ((2 * m + st) * kKeys + lane * box) * X;
                                 int bytes = 0;
 #pragma unroll
                                 for (int q = 0; q < kParts; ++q) {
                                     if (lane < boxes[q] && !good[q]) { // zeros, at a scale of one
-                                        for (int j = 0; j < box; ++j) e[q * kPart + j] = 127;
+                                        for (int j = 0; j < box * X; ++j) e[q * kPart * X + j] = 127;
                                         proxy_fence();
                                     }
-                                    bytes += __popc(__ballot_sync(0xffffffffu, good[q])) * box;
+                                    bytes += __popc(__ballot_sync(0xffffffffu, good[q])) * box * X;
                                 }
                                 if (lane == 0) mbar_expect_tx(bars.e_full + 2 * m + st, bytes);
                                 __syncwarp();
 #pragma unroll
                                 for (int q = 0; q < kParts; ++q)
                                     if (good[q])
-                                        bulk_load(e + q * kPart,
-                                                  exps + ((size_t)z[q] << p.c.page_shift) + ((in_page + q * kPart) & (p.c.page - 1)), box,
-                                                  bars.e_full + 2 * m + st);
+                                        bulk_load(e + q * kPart * X,
+                                                  exps + (((size_t)z[q] << p.c.page_shift) + ((in_page + q * kPart) & (p.c.page - 1))) * X,
+                                                  box * X, bars.e_full + 2 * m + st);
+                            }
+                            if (FP4) { // a page's codes of a head lie together: plain bulk copies
+                                uint8_t *dst = smem + C::kRawOff + rs * C::kRaw + lane * box * C::kRowRaw;
+                                if (lane < boxes[y] && !good[y]) {
+                                    for (int j = 0; j < box * C::kRowRaw; j += 16) sts128(smem_u32(dst) + j, make_uint4(0, 0, 0, 0));
+                                    proxy_fence();
+                                }
+                                __syncwarp();
+                                const int goods = __popc(__ballot_sync(0xffffffffu, good[y]));
+                                if (lane == 0) mbar_expect_tx(bars.raw_full + rs, goods * box * C::kRowRaw);
+                                __syncwarp();
+                                if (good[y])
+                                    bulk_load(dst,
+                                              static_cast<const uint8_t *>(m ? p.c.v : p.c.k) +
+                                                  (((size_t)z[y] << p.c.page_shift) + ((in_page + y * kPart) & (p.c.page - 1))) * C::kRowRaw,
+                                              box * C::kRowRaw, bars.raw_full + rs);
+                                continue;
                             }
                             if (lane == 0) mbar_expect_tx(bars.raw_full + rs, boxes[y] * box * kD);
                             __syncwarp();
@@ -481,15 +544,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(bars.v_clear + st);
                 } else {
                     const uint32_t tile = smem_u32(smem + (st_raw ? C::kVOff : C::kKOff) + st * C::kMat);
-                    const uint8_t *ex = smem + C::kExpOff + (st_raw + st) * kKeys;
+                    const uint8_t *ex = smem + C::kExpOff + (st_raw + st) * kKeys * C::kRowX;
                     if (!(ok = wait_all(bars.e_full + st_raw + st, (g >> 1) & 1))) break;
-                    // the tile's largest exponent (1 at least: its float is normal);
-                    // rows without a value do not count
+                    // the tile's largest exponent (1 at least: its float is normal;
+                    // 4-bit codes end at 6, so theirs is kUp4 less); rows and blocks
+                    // without a value do not count
                     int top = 1, low = 255;
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        const int j = lane + 32 * y, b = ex[j];
-                        if (j < valid && b != 255) top = max(top, b), low = min(low, b);
+                        const int j = lane + 32 * y;
+                        if (FP4) {
+                            if (j >= valid) continue;
+                            const uint32_t w = reinterpret_cast<const uint32_t *>(ex)[j], v = w & ~__vcmpeq4(w, 0xffffffffu);
+                            const uint32_t hi = __vmaxu4(v, v >> 16), lo = __vminu4(w, w >> 16);
+                            top = max(top, (int)max(hi & 0xffu, hi >> 8 & 0xffu) - kUp4);
+                            low = min(low, (int)min(lo & 0xffu, lo >> 8 & 0xffu));
+                        } else {
+                            const int b = ex[j];
+                            if (j < valid && b != 255) top = max(top, b), low = min(low, b);
+                        }
                     }
                     int e = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
                     if (st_raw) {
@@ -507,8 +580,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int y = 0; y < 2 && ok; ++y) {
                         if (!(ok = wait_all(raw_full + y, g & 1))) break;
-                        widen_half(tile, raw + y * C::kRaw, ex + y * kHalf, y * kHalf, valid, e, w, lane);
-                        if (far) widen_far(tile, raw + y * C::kRaw, ex + y * kHalf, y * kHalf, valid, e, w, lane);
+                        const uint8_t *exh = ex + y * kHalf * C::kRowX;
+                        if (FP4) {
+                            widen_blocks<false>(tile, raw + y * C::kRaw, exh, y * kHalf, valid, e, w, lane);
+                            if (far) widen_far_blocks(tile, raw + y * C::kRaw, exh, y * kHalf, valid, e, w, lane);
+                        } else {
+                            widen_half(tile, raw + y * C::kRaw, exh, y * kHalf, valid, e, w, lane);
+                            if (far) widen_far(tile, raw + y * C::kRaw, exh, y * kHalf, valid, e, w, lane);
+                        }
                         mbar_arrive(raw_empty + y);
                     }
                     if (!ok) break;
@@ -819,18 +898,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <bool FP8, bool CAP>
+template <int CACHE, bool CAP>
 cudaError_t go(const PagedProblem &p, const PagedPart &part, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s)
 {
-    auto kern = paged_rows_kernel<FP8, CAP>;
+    auto kern = paged_rows_kernel<CACHE, CAP>;
     static std::atomic<uint64_t> set{0}; // devices whose copy of the kernel has its attribute
     const uint64_t bit = 1ull << p.device;
     if (!(set.load(std::memory_order_acquire) & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<FP8>::kSmem);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<CACHE>::kSmem);
         if (e != cudaSuccess) return e;
         set.fetch_or(bit, std::memory_order_release);
     }
-    return launch_dependent(kern, (unsigned)part.ctas, kThreads, Cfg<FP8>::kSmem, s, k, v, p, part);
+    return launch_dependent(kern, (unsigned)part.ctas, kThreads, Cfg<CACHE>::kSmem, s, k, v, p, part);
 }
 
 } // namespace
@@ -839,9 +918,13 @@ cudaError_t launch_paged_rows(const PagedProblem &p, const PagedPart &part, int 
                               const void *tm_v, cudaStream_t s)
 {
     const CUtensorMap &k = *static_cast<const CUtensorMap *>(tm_k), &v = *static_cast<const CUtensorMap *>(tm_v);
-    if (p.soft_cap > 0.f)
-        return cache_dtype == RA_E4M3 ? go<true, true>(p, part, k, v, s) : go<false, true>(p, part, k, v, s);
-    return cache_dtype == RA_E4M3 ? go<true, false>(p, part, k, v, s) : go<false, false>(p, part, k, v, s);
+    auto capped = [&](auto cache) {
+        constexpr int CACHE = decltype(cache)::value;
+        return p.soft_cap > 0.f ? go<CACHE, true>(p, part, k, v, s) : go<CACHE, false>(p, part, k, v, s);
+    };
+    return cache_dtype == RA_E2M1   ? capped(std::integral_constant<int, RA_E2M1>{})
+           : cache_dtype == RA_E4M3 ? capped(std::integral_constant<int, RA_E4M3>{})
+                                    : capped(std::integral_constant<int, RA_BF16>{});
 }
 
 } // namespace ra

@@ -66,7 +66,6 @@ int check_paged(const ra_kv_cache *c, const ra_paged_params *p)
 {
     const int rc = check_cache(c);
     if (rc) return rc;
-    if (c->dtype == RA_E2M1) return refuse(RA_ERR_UNSUPPORTED, "attention over an e2m1 cache is not implemented");
     if (!p) return refuse(RA_ERR_INVALID_ARG, "params is NULL");
     if (p->B <= 0 || p->Lq <= 0 || p->Hq <= 0)
         return refuse(RA_ERR_INVALID_ARG, "sizes must be positive (B=%d Lq=%d Hq=%d)", p->B, p->Lq, p->Hq);
@@ -135,7 +134,7 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
             a.seg_cost = 1;
             a.row_block = a.rows <= 4 ? 4 : 8;
             a.tile = kPagedF32Tile;
-            a.ctas = paged_f32_per_sm(a.row_block, c->dtype == RA_E4M3) * kSms;
+            a.ctas = paged_f32_per_sm(a.row_block, c->dtype != RA_BF16) * kSms;
         } else if (c->D == 128 && a.rows > 32) {
             // against blocks of 32 rows of the keys kernel, 16 sequences of 8192
             // tokens, 4 kv heads: e4m3 40 rows 68 us (keys 72), 64 rows 69 (72),
@@ -158,7 +157,7 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
             const int cols = a.rows * par >= 32 ? 32 : (a.rows * par + 7) / 8 * 8;
             a.row_block = cols / par;
             a.tile = kPagedKeysTile * par;
-            a.ctas = (c->dtype == RA_E4M3 && cols <= 16 ? 2 : 1) * kSms;
+            a.ctas = (c->dtype != RA_BF16 && cols <= 16 ? 2 : 1) * kSms;
         }
         a.n_rb = (a.rows + a.row_block - 1) / a.row_block;
         a.slot_rows = a.rows < a.row_block ? a.rows : a.row_block;
@@ -283,8 +282,8 @@ RA_API int ra_attn_paged(const ra_kv_cache *cache, const ra_paged_params *p, con
         }
         const int most = pl.kernel[k] == kRowsM && cache->dtype == RA_E4M3 ? 64 : 128; // of a box
         const int in_page = cache->page_size * cache->D / 128, rows = in_page < most ? in_page : most;
-        CUtensorMap tk, tv;
-        if ((rc = encode_paged(&tk, cache, cache->k, rows)) || (rc = encode_paged(&tv, cache, cache->v, rows))) return rc;
+        CUtensorMap tk{}, tv{}; // 4-bit pages are fetched by plain copies
+        if (cache->dtype != RA_E2M1 && ((rc = encode_paged(&tk, cache, cache->k, rows)) || (rc = encode_paged(&tv, cache, cache->v, rows)))) return rc;
         e = pl.kernel[k] == kKeysM ? launch_paged_keys(x, part, cache->dtype, &tk, &tv, s)
                                    : launch_paged_rows(x, part, cache->dtype, &tk, &tv, s);
     }

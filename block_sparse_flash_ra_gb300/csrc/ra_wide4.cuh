@@ -1,0 +1,61 @@
+// ra_wide4.cuh -- e2m1 codes of a 4-bit cache widened to e4m3.
+//
+// A block of 32 codes has a power of two of its own; the products take one for a
+// whole row (of a token).  With the largest of a row's bytes as the row's, e, a
+// code becomes the e4m3 code of code * 2^(6 - k), k = e - byte: at most 384,
+// exact for k up to 14 (half a step of 2^-10, 2^-18 of 6 * 2^6, at the most
+// below), and the row stands at 2^(e - 6).  The eight magnitudes of a k are
+// eight bytes, so that one byte permute with the codes as its selector widens
+// four of them.
+#pragma once
+
+#include "ra_rows.cuh"
+
+namespace ra {
+
+// Entry k: the magnitudes' codes at 2^(6 - k); kWide4Zero: none is left;
+// kWide4Nan: a block without a value.
+constexpr int kWide4Zero = 20, kWide4Nan = 21, kWide4Entries = 22;
+constexpr int kWide4Up = 6; // a row's byte is its largest less this, 0 at the least
+
+__device__ __forceinline__ void wide4_fill(uint2 *table, int k)
+{
+    const float s = k >= kWide4Zero ? 0.f : __uint_as_float((uint32_t)(127 + kWide4Up - k) << 23);
+    table[k] = k == kWide4Nan ? make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu)
+                              : make_uint2(e4m3x4(0.f, 0.5f * s, s, 1.5f * s), e4m3x4(2.f * s, 3.f * s, 4.f * s, 6.f * s));
+}
+
+// The largest byte of a word, or of its half y of two, that is not 255; at least kWide4Up.
+template <bool HALF>
+__device__ __forceinline__ uint32_t wide4_top(uint32_t w, int y)
+{
+    w &= ~__vcmpeq4(w, 0xffffffffu);
+    if (HALF) {
+        w = y ? w >> 16 : w & 0xffffu;
+    } else {
+        w = __vmaxu4(w, w >> 16) & 0xffffu;
+    }
+    return max(max(w & 0xffu, w >> 8), (uint32_t)kWide4Up);
+}
+
+__device__ __forceinline__ const uint2 &wide4_entry(const uint2 *table, uint32_t top, uint32_t byte)
+{
+    return table[byte == 255u ? (uint32_t)kWide4Nan : min(top - byte, (uint32_t)kWide4Zero)];
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)
+{
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
+}
+
+// Eight codes, the first in the lowest four bits, as eight bytes.
+__device__ __forceinline__ uint2 wide4(uint32_t w, const uint2 &t)
+{
+    const uint32_t m = w & 0x77777777u, s = w << 4; // signs: bit 7 of bytes of s and of w in turn
+    return make_uint2(prmt(t.x, t.y, m) | (prmt(s, w, 0x5140u) & 0x80808080u),
+                      prmt(t.x, t.y, m >> 16) | (prmt(s, w, 0x7362u) & 0x80808080u));
+}
+
+} // namespace ra
