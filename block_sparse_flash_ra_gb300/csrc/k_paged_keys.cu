@@ -124,8 +124,8 @@ struct Cfg {
     static constexpr int kRawOff = kPOff + 2 * kPBytes;
     static constexpr int kXOff = kRawOff + kRaws * kRaw;
     static constexpr int kTableOff = kXOff + kXs * kX;
-    static constexpr int kExpOff = kTableOff + (FP4 ? 256 : 0); // per stage: scale bytes of K, of V
-    static constexpr int kRowOff = kExpOff + (FP8 ? kEStages * 2 * kTokens : 0);
+    static constexpr int kExpOff = kTableOff + (FP4 ? 256 : 0); // per stage: scale bytes of K (8 bits), of V
+    static constexpr int kRowOff = kExpOff + (FP4 ? kEStages * kTokens : FP8 ? kEStages * 2 * kTokens : 0);
     // per row of both segments: place of its output and of its lse (two words each), logit scale, keys it sees;
     // then its factor
     static constexpr int kRowBytes = RP * 24;
@@ -136,8 +136,10 @@ struct Cfg {
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kSmem = kMiscOff + 16 + 1024;
     static constexpr uint32_t kColO = 2 * kNS;
-    static constexpr uint32_t kCols = kColO + kNO <= 64 ? 64 : kColO + kNO <= 128 ? 128 : 256;
-    static constexpr uint32_t kIdescS = ((FP8 ? 0u : (1u << 7) | (1u << 10)) | (1u << 4)) |
+    // 4 bits: the keys' scales, by K stage, and ones for the queries
+    static constexpr uint32_t kColX = kColO + kNO, kColOnes = kColX + (FP4 ? 4 * kStages : 0);
+    static constexpr uint32_t kAll = kColOnes + (FP4 ? 4 : 0), kCols = kAll <= 64 ? 64 : kAll <= 128 ? 128 : 256;
+    static constexpr uint32_t kIdescS = FP4 ? (5u << 7) | ((uint32_t)(kNS >> 3) << 17) | (1u << 23) | ((uint32_t)(kKeys >> 4) << 24) : ((FP8 ? 0u : (1u << 7) | (1u << 10)) | (1u << 4)) |
                                         ((uint32_t)(kNS >> 3) << 17) | ((uint32_t)(kKeys >> 4) << 24);
     // both operands of O^T are MN-major
     static constexpr uint32_t kIdescO = ((FP8 ? 0u : (1u << 7) | (1u << 10)) | (1u << 4)) | (1u << 15) | (1u << 16) |
@@ -194,6 +196,23 @@ __device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, uin
                      : "memory");
     else
         mma_ss_w(d, a, b, idesc, accumulate);
+}
+
+// The same of e2m1 codes as A, whose 32 values of a row and step have a power of
+// two: byte `step` of the words at `sfa` (row j in lane j % 32 of every 32, column
+// j / 32); B's are at `sfb`.
+__device__ __forceinline__ void mma_step_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int step, uint32_t sfa, uint32_t sfb,
+                                                uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %6, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc | (uint32_t)step << 29), "r"(sfa), "r"(sfb), "r"(accumulate)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld8(uint32_t addr, float *v)
@@ -391,12 +410,21 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 wait_drain(bars.x_full + j % C::kXs, (j / C::kXs) & 1, kDrainNs);
         }
     } else if (FP4 && any && warp >= C::kWideWarp && warp < C::kMmaWarp) {
-        // ------------------------------------------------------------ widening
-        // a thread takes blocks of 32 codes (16 bytes, a quarter of a row of 128
-        // values), which become two 16-byte chunks of the e4m3 tile
-        const int wt = threadIdx.x - C::kWideWarp * 32, x = wt & 3;
+        // ------------------------------------------------------------ 4-bit tiles
+        // A thread takes blocks of 32 codes (16 bytes, a quarter of a row of 128
+        // values).  Keys go to the products as they are, 16 codes in the lower
+        // half of every 16 bytes, their scales to TMEM; values become e4m3.
+        const int wt = threadIdx.x - C::kWideWarp * 32, x = wt & 3, row0 = wt >> 2;
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t ones = 0x7f7f7f7fu;
+        tmem_st4(lane_base + C::kColOnes, ones, ones, ones, ones);
         uint32_t i = 0, r = 0;
         bool ok = true;
+        auto lds4 = [](uint32_t at) {
+            uint4 w;
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at));
+            return w;
+        };
         for (;;) {
             const int n = cursor_take(c), len = source_len(c.b);
             for (int t = c.t0; ok && t < c.t0 + n; ++t, ++i) {
@@ -405,30 +433,62 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 const uint32_t *xs = reinterpret_cast<const uint32_t *>(smem + C::kXOff + sx * C::kX); // K's, then V's
                 if (!(ok = wait_all(bars.x_full + sx, (i / C::kXs) & 1))) break;
                 if (!(ok = wait_all(bars.k_empty + st, ((i / C::kStages) & 1) ^ 1))) break;
-                uint8_t *e = smem + C::kExpOff + (i % C::kEStages) * 2 * kTokens;
+                uint32_t kx[4];
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+                for (int y = 0; y < 4; ++y) kx[y] = xs[lane + 32 * y];
+                if (kPar == 2 && (valid & 1)) {
+                    // an odd length ends inside a row: its other token meets zeros of Q,
+                    // whose product with a scale of NaN would not be zero
 #pragma unroll
-                    for (int y = 0; y < kPar; ++y) {
-                        const int tok = wt * kPar + y;
-                        e[m * kTokens + tok] = tok < valid ? wide4_top<kPar == 2>(xs[m * kKeys + wt], y) - kWide4Up : 127;
-                    }
+                    for (int y = 0; y < 4; ++y)
+                        if (lane + 32 * y == valid >> 1) kx[y] = (kx[y] & 0xffffu) | (ones & 0xffff0000u);
+                }
+                tmem_st4(lane_base + C::kColX + 4 * st, kx[0], kx[1], kx[2], kx[3]);
+                // of the values' rows row0 + 32 y a group of four lanes has, lane x
+                // finds the scale byte and the entries of row y = x
+                const int mine = row0 + 32 * x;
+                uint32_t top[2];
+                const uint32_t in = wide4_rows<kPar == 2>(xs[kKeys + mine], top);
+                uint8_t *e = smem + C::kExpOff + (i % C::kEStages) * kTokens + mine * kPar;
+#pragma unroll
+                for (int y = 0; y < kPar; ++y) e[y] = mine * kPar + y < valid ? top[y] - kWide4Up : 127;
                 mbar_arrive(bars.e_full + i % C::kEStages);
+                mbar_arrive(bars.x_empty + sx);
 #pragma unroll 1
-                for (int it = 0; it < 4; ++it, ++r) {
-                    const int sr = r % C::kRaws, m = it >> 1, half = it & 1;
-                    if (it == 2 && !(ok = wait_all(bars.v_empty + st, ((i / C::kStages) & 1) ^ 1))) break;
+                for (int half = 0; half < 2; ++half, ++r) {
+                    const int sr = r % C::kRaws;
                     if (!(ok = wait_all(bars.raw_full + sr, (r / C::kRaws) & 1))) break;
                     const uint32_t raw = smem_u32(smem + C::kRawOff + sr * C::kRaw) + wt * 16;
-                    const uint32_t tile = smem_u32(smem + (m ? C::kVOff : C::kKOff) + st * C::kMat);
+                    const uint4 w[2] = {lds4(raw), lds4(raw + 2048)};
+                    mbar_arrive(bars.raw_empty + sr);
+                    const uint32_t tile = smem_u32(smem + C::kKOff + st * C::kMat);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const int j = half * 64 + u * 32 + (wt >> 2); // row of the tile
-                        uint4 w;
-                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(raw + u * 2048));
-                        const uint32_t word = xs[m * kKeys + j];
-                        const uint2 tab = wide4_entry(table, wide4_top<kPar == 2>(word, x >> 1), word >> (8 * x) & 0xffu);
-                        uint2 o[4] = {wide4(w.x, tab), wide4(w.y, tab), wide4(w.z, tab), wide4(w.w, tab)};
+                        const int j = half * 64 + u * 32 + row0; // row of the tile
+                        const uint32_t at = tile + j * 128;
+                        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + (((2 * x) ^ (j & 7)) << 4)), "r"(w[u].x), "r"(w[u].y) : "memory");
+                        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + (((2 * x + 1) ^ (j & 7)) << 4)), "r"(w[u].z), "r"(w[u].w) : "memory");
+                    }
+                }
+                if (!ok) break;
+                tmem_st_wait();
+                tc_fence_before();
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive(bars.k_full + st);
+                if (!(ok = wait_all(bars.v_empty + st, ((i / C::kStages) & 1) ^ 1))) break;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half, ++r) {
+                    const int sr = r % C::kRaws;
+                    if (!(ok = wait_all(bars.raw_full + sr, (r / C::kRaws) & 1))) break;
+                    const uint32_t raw = smem_u32(smem + C::kRawOff + sr * C::kRaw) + wt * 16;
+                    const uint4 w[2] = {lds4(raw), lds4(raw + 2048)};
+                    mbar_arrive(bars.raw_empty + sr);
+                    const uint32_t tile = smem_u32(smem + C::kVOff + st * C::kMat);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int j = half * 64 + u * 32 + row0;
+                        const uint2 tab = table[__shfl_sync(0xffffffffu, in, half * 2 + u, 4) >> (8 * x) & 0xffu];
+                        uint2 o[4] = {wide4(w[u].x, tab), wide4(w[u].y, tab), wide4(w[u].z, tab), wide4(w[u].w, tab)};
                         // (tokens behind the length: whatever is there, weight 0 must give 0)
                         if (j * kPar + (kPar == 2 ? x >> 1 : 0) >= valid) o[0] = o[1] = o[2] = o[3] = make_uint2(0, 0);
                         const uint32_t at = tile + j * 128;
@@ -439,13 +499,10 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                                      "r"(o[2].y), "r"(o[3].x), "r"(o[3].y)
                                      : "memory");
                     }
-                    mbar_arrive(bars.raw_empty + sr);
-                    if (half) {
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        mbar_arrive((m ? bars.v_full : bars.k_full) + st);
-                    }
                 }
-                if (ok) mbar_arrive(bars.x_empty + sx);
+                if (!ok) break;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive(bars.v_full + st);
             }
             if (!ok || !cursor_next(p, part, c, n)) break;
         }
@@ -572,7 +629,11 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 for (int kk = 0; kk < (FP8 ? 4 : 8); ++kk) {
                     const uint32_t ao = FP8 ? kk * 32 : (kk >> 2) * (kKeys * 128) + (kk & 3) * 32;
                     const uint32_t bo = FP8 ? kk * 32 : (kk >> 2) * (C::kNS * 128) + (kk & 3) * 32;
-                    mma_step<FP8>(tmem + sb * C::kNS, kd + (ao >> 4), qd + (bo >> 4), C::kIdescS, kk > 0 ? 1u : 0u);
+                    if (FP4)
+                        mma_step_scaled(tmem + sb * C::kNS, kd + (ao >> 4), qd + (bo >> 4), C::kIdescS, kk, tmem + C::kColX + 4 * sk,
+                                        tmem + C::kColOnes, kk > 0 ? 1u : 0u);
+                    else
+                        mma_step<FP8>(tmem + sb * C::kNS, kd + (ao >> 4), qd + (bo >> 4), C::kIdescS, kk > 0 ? 1u : 0u);
                 }
                 tc_commit_w(bars.k_empty + sk);
                 // the softmax reads the tile's scale bytes as well as S: this arrival
@@ -709,11 +770,11 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 tc_fence_after();
                 tmem_ld8(lane_base + sb * C::kNS + row0, s);
                 if (FP8) {
-                    const uint8_t *e = smem + C::kExpOff + (i % C::kEStages) * 2 * kTokens + tok;
+                    const uint8_t *e = smem + C::kExpOff + (i % C::kEStages) * (FP4 ? 1 : 2) * kTokens + tok;
 #pragma unroll
                     for (int y = 0; y < kPar; ++y) {
-                        const uint32_t vb = e[kTokens + y];
-                        ks[y] = exp_byte_scale(e[y]);
+                        const uint32_t vb = e[(FP4 ? 0 : kTokens) + y];
+                        if (!FP4) ks[y] = exp_byte_scale(e[y]);
                         vs[y] = exp_byte_scale(vb);
                         // bytes behind the length and rows without a value do not count
                         ev[y] = tok + y < valid && vb != 255u ? fmaxf((float)vb, kMinExp) : kMinExp;
@@ -733,7 +794,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 // ---- logits in base 2
                 bool grow = FP8 && fmaxf(ev[0], ev[kPar - 1]) > ev_top + kLouder;
 #pragma unroll
-                for (int r = 0; r < kRT; ++r) s[r] *= FP8 ? qs[r] * ks[r % kPar] : qs[r];
+                for (int r = 0; r < kRT; ++r) s[r] *= FP8 && !FP4 ? qs[r] * ks[r % kPar] : qs[r];
                 if (to_cap > 0.f) {
                     float xa = 0.f;
 #pragma unroll

@@ -1,7 +1,7 @@
 // ra_wide4.cuh -- e2m1 codes of a 4-bit cache widened to e4m3.
 //
-// A block of 32 codes has a power of two of its own; the products take one for a
-// whole row (of a token).  With the largest of a row's bytes as the row's, e, a
+// Values are summed over tokens by products that take one power of two for a
+// token, but a block of 32 codes has one of its own.  With the largest of a row's bytes as the row's, e, a
 // code becomes the e4m3 code of code * 2^(6 - k), k = e - byte: at most 384,
 // exact for k up to 14 (half a step of 2^-10, 2^-18 of 6 * 2^6, at the most
 // below), and the row stands at 2^(e - 6).  The eight magnitudes of a k are
@@ -25,22 +25,25 @@ __device__ __forceinline__ void wide4_fill(uint2 *table, int k)
                               : make_uint2(e4m3x4(0.f, 0.5f * s, s, 1.5f * s), e4m3x4(2.f * s, 3.f * s, 4.f * s, 6.f * s));
 }
 
-// The largest byte of a word, or of its half y of two, that is not 255; at least kWide4Up.
+// From a row's scale bytes (four blocks, or two of each of two tokens: HALF) its
+// byte -- at least kWide4Up, and not of blocks without a value -- and, as bytes,
+// the blocks' entries.
 template <bool HALF>
-__device__ __forceinline__ uint32_t wide4_top(uint32_t w, int y)
+__device__ __forceinline__ uint32_t wide4_rows(uint32_t w, uint32_t *top)
 {
-    w &= ~__vcmpeq4(w, 0xffffffffu);
-    if (HALF) {
-        w = y ? w >> 16 : w & 0xffffu;
-    } else {
-        w = __vmaxu4(w, w >> 16) & 0xffffu;
+    uint32_t b[4], t[4], in = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        b[i] = w >> (8 * i) & 0xffu;
+        t[i] = b[i] == 255u ? 0u : b[i];
     }
-    return max(max(w & 0xffu, w >> 8), (uint32_t)kWide4Up);
-}
-
-__device__ __forceinline__ const uint2 &wide4_entry(const uint2 *table, uint32_t top, uint32_t byte)
-{
-    return table[byte == 255u ? (uint32_t)kWide4Nan : min(top - byte, (uint32_t)kWide4Zero)];
+    top[0] = max(max(t[0], t[1]), (uint32_t)kWide4Up);
+    top[1] = max(max(t[2], t[3]), (uint32_t)kWide4Up);
+    if (!HALF) top[0] = top[1] = max(top[0], top[1]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        in |= (b[i] == 255u ? (uint32_t)kWide4Nan : min(top[i >> 1] - b[i], (uint32_t)kWide4Zero)) << (8 * i);
+    return in;
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)
