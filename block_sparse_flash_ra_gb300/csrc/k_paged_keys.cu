@@ -73,7 +73,6 @@ namespace ra {
 namespace {
 
 constexpr int kKeys = 128, kD = 128; // rows of a cached tile, values of a row
-constexpr int kRT = 8;         // rows of a softmax warpgroup
 constexpr float kNone = -3e38f; // the maximum of no logits: finite, so that no difference is a NaN
 // 8-bit caches: a row's largest contribution is 2^kPBias at its reference and
 // may grow by 2^kGrow, to 2^8, where e4m3 steps by 16; so a term's rest is 2^3
@@ -97,7 +96,8 @@ struct Cfg {
     static constexpr int kPar = kD / D, kTokens = kKeys * kPar; // tokens of a row, of a tile
     static constexpr int kMat = kKeys * kD * (FP8 ? 1 : 2); // bytes of a K or V tile
     static constexpr int kHalves = FP8 ? 1 : 2;             // 128-byte wide blocks of a tile
-    static constexpr int kGroups = RP / kRT, kSoftThreads = 128 * kGroups, kWideThreads = FP4 ? 128 : 0;
+    static constexpr int kRT = RP < 8 ? RP : 8; // rows of a softmax warpgroup
+    static constexpr int kGroups = RP / kRT, kSoftThreads = 128 * kGroups, kWideThreads = !FP4 ? 0 : RP == 4 ? 256 : 128;
     static constexpr int kThreads = kSoftThreads + kWideThreads + 64;
     static constexpr int kWideWarp = 4 * kGroups, kMmaWarp = kWideWarp + kWideThreads / 32, kLoadWarp = kMmaWarp + 1;
     static constexpr int kCtasPerSm = FP8 && RP <= 16 ? 2 : 1;
@@ -105,7 +105,7 @@ struct Cfg {
     static constexpr int kVStages = FP4 ? kStages : FP8 ? (RP > 16 ? 5 : 3) : RP > 16 ? 2 : 3;
     // 4 bits: half tiles of codes, K low, K high, V low, V high of a tile in turn,
     // and the tiles' scale bytes, four to a row of K and of V
-    static constexpr int kRaw = kKeys * kD / 4, kRaws = !FP4 ? 0 : RP == 8 ? 7 : RP == 16 ? (D == 128 ? 5 : 4) : 16;
+    static constexpr int kRaw = kKeys * kD / 4, kRaws = !FP4 ? 0 : RP <= 8 ? 7 : RP == 16 ? (D == 128 ? 5 : 4) : 16;
     static constexpr int kXs = !FP4 ? 0 : RP > 16 ? 6 : 3, kX = 2 * kKeys * 4;
     // the rows' scale bytes: where TMA brings them, beside V; widened, a tile's
     // come with its K, for which S of kStages tiles before has waited until the
@@ -145,7 +145,7 @@ struct Cfg {
     static constexpr uint32_t kIdescO = ((FP8 ? 0u : (1u << 7) | (1u << 10)) | (1u << 4)) | (1u << 15) | (1u << 16) |
                                         ((uint32_t)(kNO >> 3) << 17) | ((uint32_t)(kD >> 4) << 24);
     static_assert(kSmem <= (kCtasPerSm == 2 ? 113 : 227) * 1024, "shared memory");
-    static_assert(kRedOff % 16 == 0 && (kRT + 4) % 4 == 0, "words of a warp are read by fours");
+    static_assert(kRedOff % 16 == 0 && kRT % 4 == 0, "words of a warp are read by fours");
     static_assert(kBarOff % 8 == 0 && kRowOff % 8 == 0 && kPOff % 1024 == 0 && kExpOff % 128 == 0, "layout");
 };
 
@@ -215,19 +215,30 @@ __device__ __forceinline__ void tmem_st4(uint32_t addr, uint32_t a, uint32_t b, 
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld8(uint32_t addr, float *v)
+template <int N>
+__device__ __forceinline__ void tmem_ldn(uint32_t addr, float *v)
 {
+    static_assert(N == 4 || N == 8, "columns");
     uint32_t *r = reinterpret_cast<uint32_t *>(v);
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(addr));
+    if (N == 4)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(addr));
+    else
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[N - 4]), "=r"(r[N - 3]), "=r"(r[N - 2]), "=r"(r[N - 1])
+                     : "r"(addr));
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t *r)
+template <int N>
+__device__ __forceinline__ void tmem_stn(uint32_t addr, const uint32_t *r)
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+    if (N == 4)
+        tmem_st4(addr, r[0], r[1], r[2], r[3]);
+    else
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]),
+                     "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[N - 4]), "r"(r[N - 3]), "r"(r[N - 2]), "r"(r[N - 1])
+                     : "memory");
 }
 
 // The softmax warps' own barriers: 1 of all N threads, 2 + g of warpgroup g.
@@ -286,7 +297,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
 {
     using C = Cfg<CACHE, RP, D>;
     constexpr bool FP8 = C::FP8, FP4 = C::FP4;
-    constexpr int kPar = C::kPar, kTokens = C::kTokens;
+    constexpr int kPar = C::kPar, kTokens = C::kTokens, kRT = C::kRT;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const Bars bars = carve<C>(smem);
@@ -296,21 +307,21 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(bars.k_full + s, FP4 ? C::kWideThreads : 1);
+            mbar_init(bars.k_full + s, FP4 ? C::kWideThreads / 32 : 1);
             mbar_init(bars.k_empty + s, 1);
         }
         for (int s = 0; s < C::kVStages; ++s) {
-            mbar_init(bars.v_full + s, FP4 ? C::kWideThreads : 1);
+            mbar_init(bars.v_full + s, FP4 ? C::kWideThreads / 32 : 1);
             mbar_init(bars.v_empty + s, 1);
         }
-        for (int s = 0; s < C::kEStages; ++s) mbar_init(bars.e_full + s, FP4 ? C::kWideThreads : 1);
+        for (int s = 0; s < C::kEStages; ++s) mbar_init(bars.e_full + s, FP4 ? C::kWideThreads / 32 : 1);
         for (int s = 0; s < C::kRaws; ++s) {
             mbar_init(bars.raw_full + s, 1);
-            mbar_init(bars.raw_empty + s, C::kWideThreads);
+            mbar_init(bars.raw_empty + s, C::kWideThreads / 32);
         }
         for (int s = 0; s < C::kXs; ++s) {
             mbar_init(bars.x_full + s, 1);
-            mbar_init(bars.x_empty + s, C::kWideThreads);
+            mbar_init(bars.x_empty + s, C::kWideThreads / 32);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(bars.s_full + s, FP8 ? 2 : 1);
@@ -414,16 +425,23 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
         // A thread takes blocks of 32 codes (16 bytes, a quarter of a row of 128
         // values).  Keys go to the products as they are, 16 codes in the lower
         // half of every 16 bytes, their scales to TMEM; values become e4m3.
+        constexpr int kRows = FP4 ? C::kWideThreads / 4 : 32, kBlocks = 64 / kRows; // rows at once; a thread's blocks of a half tile
         const int wt = threadIdx.x - C::kWideWarp * 32, x = wt & 3, row0 = wt >> 2;
+        const bool scales = wt < 128; // the four warps that put the keys' scales into TMEM
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ones = 0x7f7f7f7fu;
-        tmem_st4(lane_base + C::kColOnes, ones, ones, ones, ones);
+        if (scales) tmem_st4(lane_base + C::kColOnes, ones, ones, ones, ones);
         uint32_t i = 0, r = 0;
         bool ok = true;
         auto lds4 = [](uint32_t at) {
             uint4 w;
             asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at));
             return w;
+        };
+        // a warp's arrival, for all of its lanes
+        auto arrive = [&](uint64_t *bar) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
         };
         for (;;) {
             const int n = cursor_take(c), len = source_len(c.b);
@@ -443,28 +461,30 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                     for (int y = 0; y < 4; ++y)
                         if (lane + 32 * y == valid >> 1) kx[y] = (kx[y] & 0xffffu) | (ones & 0xffff0000u);
                 }
-                tmem_st4(lane_base + C::kColX + 4 * st, kx[0], kx[1], kx[2], kx[3]);
-                // of the values' rows row0 + 32 y a group of four lanes has, lane x
+                if (scales) tmem_st4(lane_base + C::kColX + 4 * st, kx[0], kx[1], kx[2], kx[3]);
+                // of the values' rows row0 + kRows y a group of four lanes has, lane x
                 // finds the scale byte and the entries of row y = x
-                const int mine = row0 + 32 * x;
+                const int mine = row0 + kRows * (x & (2 * kBlocks - 1));
                 uint32_t top[2];
                 const uint32_t in = wide4_rows<kPar == 2>(xs[kKeys + mine], top);
                 uint8_t *e = smem + C::kExpOff + (i % C::kEStages) * kTokens + mine * kPar;
 #pragma unroll
                 for (int y = 0; y < kPar; ++y) e[y] = mine * kPar + y < valid ? top[y] - kWide4Up : 127;
-                mbar_arrive(bars.e_full + i % C::kEStages);
-                mbar_arrive(bars.x_empty + sx);
+                arrive(bars.e_full + i % C::kEStages);
+                arrive(bars.x_empty + sx);
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half, ++r) {
                     const int sr = r % C::kRaws;
                     if (!(ok = wait_all(bars.raw_full + sr, (r / C::kRaws) & 1))) break;
                     const uint32_t raw = smem_u32(smem + C::kRawOff + sr * C::kRaw) + wt * 16;
-                    const uint4 w[2] = {lds4(raw), lds4(raw + 2048)};
-                    mbar_arrive(bars.raw_empty + sr);
+                    uint4 w[kBlocks];
+#pragma unroll
+                    for (int u = 0; u < kBlocks; ++u) w[u] = lds4(raw + u * C::kWideThreads * 16);
+                    arrive(bars.raw_empty + sr);
                     const uint32_t tile = smem_u32(smem + C::kKOff + st * C::kMat);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int j = half * 64 + u * 32 + row0; // row of the tile
+                    for (int u = 0; u < kBlocks; ++u) {
+                        const int j = half * 64 + u * kRows + row0; // row of the tile
                         const uint32_t at = tile + j * 128;
                         asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + (((2 * x) ^ (j & 7)) << 4)), "r"(w[u].x), "r"(w[u].y) : "memory");
                         asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + (((2 * x + 1) ^ (j & 7)) << 4)), "r"(w[u].z), "r"(w[u].w) : "memory");
@@ -474,20 +494,22 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 tmem_st_wait();
                 tc_fence_before();
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                mbar_arrive(bars.k_full + st);
+                arrive(bars.k_full + st);
                 if (!(ok = wait_all(bars.v_empty + st, ((i / C::kStages) & 1) ^ 1))) break;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half, ++r) {
                     const int sr = r % C::kRaws;
                     if (!(ok = wait_all(bars.raw_full + sr, (r / C::kRaws) & 1))) break;
                     const uint32_t raw = smem_u32(smem + C::kRawOff + sr * C::kRaw) + wt * 16;
-                    const uint4 w[2] = {lds4(raw), lds4(raw + 2048)};
-                    mbar_arrive(bars.raw_empty + sr);
+                    uint4 w[kBlocks];
+#pragma unroll
+                    for (int u = 0; u < kBlocks; ++u) w[u] = lds4(raw + u * C::kWideThreads * 16);
+                    arrive(bars.raw_empty + sr);
                     const uint32_t tile = smem_u32(smem + C::kVOff + st * C::kMat);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int j = half * 64 + u * 32 + row0;
-                        const uint2 tab = table[__shfl_sync(0xffffffffu, in, half * 2 + u, 4) >> (8 * x) & 0xffu];
+                    for (int u = 0; u < kBlocks; ++u) {
+                        const int j = half * 64 + u * kRows + row0;
+                        const uint2 tab = table[__shfl_sync(0xffffffffu, in, half * kBlocks + u, 4) >> (8 * x) & 0xffu];
                         uint2 o[4] = {wide4(w[u].x, tab), wide4(w[u].y, tab), wide4(w[u].z, tab), wide4(w[u].w, tab)};
                         // (tokens behind the length: whatever is there, weight 0 must give 0)
                         if (j * kPar + (kPar == 2 ? x >> 1 : 0) >= valid) o[0] = o[1] = o[2] = o[3] = make_uint2(0, 0);
@@ -502,7 +524,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 }
                 if (!ok) break;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                mbar_arrive(bars.v_full + st);
+                arrive(bars.v_full + st);
             }
             if (!ok || !cursor_next(p, part, c, n)) break;
         }
@@ -686,7 +708,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
             const Rows ri = rows_of(par);
             const uint32_t q_base = smem_u32(smem + C::kQOff + (par & 1) * C::kQBytes);
 #pragma unroll 1
-            for (int r = threadIdx.x >> 4; r < C::kNS / C::kQTerms; r += NT / 16) {
+            for (int r = threadIdx.x >> 4; r < (RP < 8 ? RP : C::kNS / C::kQTerms); r += NT / 16) {
                 const int x = threadIdx.x & 15;
                 const PagedRow row = paged_row(p, part, at, r / kPar);
                 const bool live = r < RP && row.counts;
@@ -717,12 +739,10 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                         hi[y] = to_codes(q2);
                         lo[y] = to_codes(__hmul2(__hsub2(q2, from_codes(hi[y])), __float2half2_rn(16.f)));
                     }
-                    const uint32_t dst = q_base + (((x >> 1) ^ (r & 7)) << 4) + (x & 1) * 8;
-                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst + r * 128), "r"(hi[0] | hi[1] << 16),
-                                 "r"(hi[2] | hi[3] << 16)
+                    auto at_row = [&](int n) { return q_base + n * 128 + (((x >> 1) ^ (n & 7)) << 4) + (x & 1) * 8; };
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at_row(r)), "r"(hi[0] | hi[1] << 16), "r"(hi[2] | hi[3] << 16)
                                  : "memory");
-                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst + (RP + r) * 128), "r"(lo[0] | lo[1] << 16),
-                                 "r"(lo[2] | lo[3] << 16)
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at_row(RP + r)), "r"(lo[0] | lo[1] << 16), "r"(lo[2] | lo[3] << 16)
                                  : "memory");
                 } else {
                     const uint32_t dst = q_base + (x >> 3) * (C::kNS * 128) + r * 128 +
@@ -768,7 +788,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 float ks[kPar] = {}, vs[kPar] = {}, ev[kPar] = {};
                 wait(bars.s_full + sb, (i >> 1) & 1);
                 tc_fence_after();
-                tmem_ld8(lane_base + sb * C::kNS + row0, s);
+                tmem_ldn<kRT>(lane_base + sb * C::kNS + row0, s);
                 if (FP8) {
                     const uint8_t *e = smem + C::kExpOff + (i % C::kEStages) * (FP4 ? 1 : 2) * kTokens + tok;
 #pragma unroll
@@ -782,7 +802,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 }
                 if (FP8) {
                     float s2[kRT];
-                    tmem_ld8(lane_base + sb * C::kNS + RP + row0, s2);
+                    tmem_ldn<kRT>(lane_base + sb * C::kNS + RP + row0, s2);
                     tmem_ld_wait();
 #pragma unroll
                     for (int r = 0; r < kRT; ++r) s[r] = fmaf(s2[r], 1.f / 16.f, s[r]);
@@ -832,8 +852,8 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                     for (int r = 0; r < kRT; ++r) top[r] = warp_max(FP8 ? __fadd_ru(s[r], quiet[r % kPar]) : s[r]);
                     if (lane == 0) {
                         float4 *mine = reinterpret_cast<float4 *>(red + wq * RS);
-                        mine[0] = make_float4(top[0], top[1], top[2], top[3]);
-                        mine[1] = make_float4(top[4], top[5], top[6], top[7]);
+#pragma unroll
+                        for (int r = 0; r < kRT; r += 4) mine[r / 4] = make_float4(top[r], top[r + 1], top[r + 2], top[r + 3]);
                         if (FP8) red[wq * RS + kRT] = loud;
                     }
                     // O is still: P V of the tile before has completed
@@ -852,8 +872,13 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                     for (int r = 0; r < kRT; ++r) top[r] = __fadd_ru(m[r], -drop);
 #pragma unroll 2
                     for (int w = 0; w < 4; ++w) { // (all at once would take registers from the join beside)
-                        const float4 *of = reinterpret_cast<const float4 *>(red + w * RS), a = of[0], b = of[1];
-                        const float x[kRT] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                        const float4 *of = reinterpret_cast<const float4 *>(red + w * RS);
+                        float x[kRT];
+#pragma unroll
+                        for (int r = 0; r < kRT; r += 4) {
+                            const float4 a = of[r / 4];
+                            x[r] = a.x, x[r + 1] = a.y, x[r + 2] = a.z, x[r + 3] = a.w;
+                        }
                         const float below = FP8 ? fmaxf(red[w * RS + kRT] - ev_top, -kQuiet) : 0.f;
 #pragma unroll
                         for (int r = 0; r < kRT; ++r) top[r] = fmaxf(top[r], __fadd_ru(x[r], below));
@@ -873,13 +898,13 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                         tc_fence_after();
 #pragma unroll 1
                         for (int k = 0; k < C::kPTerms; ++k) {
-                            float o[8];
-                            uint32_t w[8];
-                            tmem_ld8(lane_base + C::kColO + k * RP + row0, o);
+                            float o[kRT];
+                            uint32_t w[kRT];
+                            tmem_ldn<kRT>(lane_base + C::kColO + k * RP + row0, o);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int y = 0; y < 8; ++y) w[y] = __float_as_uint(o[y] * f[y]);
-                            tmem_st8(lane_base + C::kColO + k * RP + row0, w);
+                            for (int y = 0; y < kRT; ++y) w[y] = __float_as_uint(o[y] * f[y]);
+                            tmem_stn<kRT>(lane_base + C::kColO + k * RP + row0, w);
                         }
                         tmem_st_wait();
                         tc_fence_before(); // O is written before p_full lets the next P V at it
@@ -906,22 +931,28 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 }
                 const uint32_t pt = p_base + sb * C::kPBytes + tid * 16;
                 if (FP8) {
-                    __half2 h[4];
+                    __half2 h[kRT / 2];
+                    uint32_t c4[C::kPTerms];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) h[y] = __floats2half2_rn(x[2 * y], x[2 * y + 1]);
+                    for (int y = 0; y < kRT / 2; ++y) h[y] = __floats2half2_rn(x[2 * y], x[2 * y + 1]);
 #pragma unroll
                     for (int k = 0; k < C::kPTerms; ++k) {
-                        uint32_t w[4];
+                        uint32_t w[kRT / 2];
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) {
+                        for (int y = 0; y < kRT / 2; ++y) {
                             w[y] = to_codes(h[y]);
                             if (k + 1 < C::kPTerms) h[y] = __hmul2(__hsub2(h[y], from_codes(w[y])), __float2half2_rn(kRest));
                         }
+                        c4[k] = __byte_perm(w[0], w[1], 0x5410);
                         const int col = k * RP + row0; // 8 columns: half of a 16-byte chunk
-                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(pt + (col >> 4) * C::kPChunk + (col & 8)),
-                                     "r"(__byte_perm(w[0], w[1], 0x5410)), "r"(__byte_perm(w[2], w[3], 0x5410))
-                                     : "memory");
+                        if (kRT == 8)
+                            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(pt + (col >> 4) * C::kPChunk + (col & 8)), "r"(c4[k]),
+                                         "r"(__byte_perm(w[kRT / 2 - 2], w[kRT / 2 - 1], 0x5410))
+                                         : "memory");
                     }
+                    if (kRT == 4) // all terms' columns are one chunk
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(pt), "r"(c4[0]), "r"(c4[1]), "r"(c4[C::kPTerms - 1]), "r"(0)
+                                     : "memory");
                 } else {
                     uint32_t hi[4], lo[4];
 #pragma unroll
@@ -962,13 +993,14 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                     l[r] = (up ? l[r + h] : l[r]) + __shfl_xor_sync(0xffffffffu, x, w);
                 }
             }
-            l[0] += __shfl_xor_sync(0xffffffffu, l[0], 2);
-            l[0] += __shfl_xor_sync(0xffffffffu, l[0], 1);
-            if ((lane & 3) == 0) red[wq * RS + (lane >> 2)] = l[0];
+            constexpr int kLanes = 32 / kRT; // that hold the same row
+#pragma unroll
+            for (int w = kLanes / 2; w; w >>= 1) l[0] += __shfl_xor_sync(0xffffffffu, l[0], w);
+            if (lane % kLanes == 0) red[wq * RS + lane / kLanes] = l[0];
             if (tid == 0) {
                 float4 *f4 = reinterpret_cast<float4 *>(row_f + row0);
-                f4[0] = make_float4(m[0], m[1], m[2], m[3]);
-                f4[1] = make_float4(m[4], m[5], m[6], m[7]);
+#pragma unroll
+                for (int r = 0; r < kRT; r += 4) f4[r / 4] = make_float4(m[r], m[r + 1], m[r + 2], m[r + 3]);
             }
             soft_sync<NT>();
             const bool final = stores_whole(part, c, n);
@@ -1000,9 +1032,9 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
             wait(bars.pv_done + ((i - 1) & 1), ((i - 1) >> 1) & 1);
             soft_sync<NT>();
             tc_fence_after();
-            float o[C::kPTerms][8];
+            float o[C::kPTerms][kRT];
 #pragma unroll
-            for (int k = 0; k < C::kPTerms; ++k) tmem_ld8(lane_base + C::kColO + k * RP + row0, o[k]);
+            for (int k = 0; k < C::kPTerms; ++k) tmem_ldn<kRT>(lane_base + C::kColO + k * RP + row0, o[k]);
             tmem_ld_wait();
             tc_fence_before();
             // a query row's O: this thread's value of it, from all tokens or from
@@ -1074,6 +1106,8 @@ cudaError_t launch_paged_keys(const PagedProblem &p, const PagedPart &part, int 
     const int cols = part.row_block * (kD / p.c.D);
     auto typed = [&](auto cache, auto d) {
         constexpr int CACHE = decltype(cache)::value, D = decltype(d)::value;
+        if constexpr (CACHE == RA_E2M1)
+            if (cols == 4) return go<CACHE, 4, D>(p, part, k, v, s);
         return cols == 8    ? go<CACHE, 8, D>(p, part, k, v, s)
                : cols == 16 ? go<CACHE, 16, D>(p, part, k, v, s)
                : cols == 24 ? go<CACHE, 24, D>(p, part, k, v, s)

@@ -92,7 +92,7 @@ cudaError_t launch_paged_f32(const PagedProblem &p, const PagedPart &part, int c
                              cudaStream_t s);
 
 // bf16 queries, few rows: the keys as the M side of tcgen05 products.
-// row_block * 128 / D is 8, 16, 24 or 32, a tile kPagedKeysTile rows of 128 values
+// row_block * 128 / D is 8, 16, 24 or 32 (4 bits: or 4), a tile kPagedKeysTile rows of 128 values
 // (with D = 64 two tokens each; boxes of min(page * D / 128, 128) rows)
 constexpr int kPagedKeysTile = 128;
 cudaError_t launch_paged_keys(const PagedProblem &p, const PagedPart &part, int cache_dtype,

@@ -154,7 +154,7 @@ Plan make_plan(const ra_kv_cache *c, const ra_paged_params *p, uint8_t *ws)
             // 30; 32 rows on 8 x 32K bf16 tokens 32 us, in 16s 35, in 8s 52.  At
             // D = 64 more rows go in blocks of 16, too.
             const int par = 128 / c->D; // columns of a query row
-            const int cols = a.rows * par >= 32 ? 32 : (a.rows * par + 7) / 8 * 8;
+            const int cols = a.rows * par >= 32 ? 32 : c->dtype == RA_E2M1 && a.rows * par <= 4 ? 4 : (a.rows * par + 7) / 8 * 8;
             a.row_block = cols / par;
             a.tile = kPagedKeysTile * par;
             a.ctas = (c->dtype != RA_BF16 && cols <= 16 ? 2 : 1) * kSms;
