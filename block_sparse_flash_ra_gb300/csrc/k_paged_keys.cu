@@ -101,12 +101,14 @@ struct Cfg {
     static constexpr int kThreads = kSoftThreads + kWideThreads + 64;
     static constexpr int kWideWarp = 4 * kGroups, kMmaWarp = kWideWarp + kWideThreads / 32, kLoadWarp = kMmaWarp + 1;
     static constexpr int kCtasPerSm = FP8 && RP <= 16 ? 2 : 1;
-    static constexpr int kStages = FP4 ? (RP > 16 ? 3 : 2) : FP8 ? (RP == 8 ? 3 : RP == 16 ? 2 : 5) : 3;
-    static constexpr int kVStages = FP4 ? kStages : FP8 ? (RP > 16 ? 5 : 3) : RP > 16 ? 2 : 3;
-    // 4 bits: half tiles of codes, K low, K high, V low, V high of a tile in turn,
-    // and the tiles' scale bytes, four to a row of K and of V
-    static constexpr int kRaw = kKeys * kD / 4, kRaws = !FP4 ? 0 : RP <= 8 ? 7 : RP == 16 ? (D == 128 ? 5 : 4) : 16;
-    static constexpr int kXs = !FP4 ? 0 : RP > 16 ? 6 : 3, kX = 2 * kKeys * 4;
+    static constexpr int kStages = FP4 ? (RP > 16 ? 5 : RP == 4 ? 3 : 2) : FP8 ? (RP == 8 ? 3 : RP == 16 ? 2 : 5) : 3;
+    static constexpr int kVStages = FP4 ? (RP > 16 ? 3 : 2) : FP8 ? (RP > 16 ? 5 : 3) : RP > 16 ? 2 : 3;
+    // 4 bits: half tiles of V's codes, and the tiles' scale bytes, four to a row of
+    // K and of V
+    static constexpr int kRaw = kKeys * kD / 4, kRaws = !FP4 ? 0 : RP == 4 ? 4 : RP == 8 ? 6 : RP == 16 ? (D == 128 ? 5 : 4) : 8;
+    static constexpr int kXs = !FP4 ? 0 : RP > 16 ? 6 : RP == 16 ? 3 : 4, kX = 2 * kKeys * 4;
+    // what a load of a row of K counts: 64 bytes, stored in 128
+    static constexpr int kKRow = FP4 ? kD / 2 : kMat / kKeys;
     // the rows' scale bytes: where TMA brings them, beside V; widened, a tile's
     // come with its K, for which S of kStages tiles before has waited until the
     // softmax had those of two more
@@ -307,7 +309,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(bars.k_full + s, FP4 ? C::kWideThreads / 32 : 1);
+            mbar_init(bars.k_full + s, 1);
             mbar_init(bars.k_empty + s, 1);
         }
         for (int s = 0; s < C::kVStages; ++s) {
@@ -338,9 +340,9 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
         tmem_alloc(tmem_holder, C::kCols);
         tmem_relinquish();
     }
-    if (!FP4 && warp == C::kLoadWarp && lane == 0) {
+    if (warp == C::kLoadWarp && lane == 0) {
         prefetch_tmap(&tm_k);
-        prefetch_tmap(&tm_v);
+        if (!FP4) prefetch_tmap(&tm_v);
     }
     uint2 *table = reinterpret_cast<uint2 *>(smem + C::kTableOff);
     if (FP4 && threadIdx.x < kWide4Entries) wide4_fill(table, threadIdx.x);
@@ -359,8 +361,9 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
 
     if (FP4 && any && warp == C::kLoadWarp) {
         // ------------------------------------------------------------ loads, 4 bits
-        // lane x fetches box x of a tile, of at most half of it: a page's codes of a
-        // head lie together, so that plain bulk copies do
+        // lane x fetches box x of a tile, of at most half of it: K by TMA, which
+        // leaves 16 codes in the lower half of every 16 bytes; of V the codes of a
+        // page's head lie together, and a plain bulk copy does
         constexpr int kItem = kTokens / 2, kRowX = D / 32; // tokens of a half tile, scale bytes of a token
         const int box = min(p.c.page, kItem), per = kTokens / box, in_item = kItem / box;
         uint32_t i = 0, r = 0;
@@ -393,9 +396,19 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                     bulk_load(x, p.c.k_exp + row * kRowX, box * kRowX, bars.x_full + sx);
                     bulk_load(x + C::kX / 2, p.c.v_exp + row * kRowX, box * kRowX, bars.x_full + sx);
                 }
+                const int sk = i % C::kStages;
+                if (!(ok = wait_all(bars.k_empty + sk, ((i / C::kStages) & 1) ^ 1))) {
+                    ++i; // this tile's scale bytes are on their way, its codes are not
+                    break;
+                }
+                if (lane == 0) mbar_expect_tx(bars.k_full + sk, boxes * (box / kPar) * C::kKRow);
+                __syncwarp();
+                if (mine)
+                    tma_load_3d(smem + C::kKOff + sk * C::kMat + lane * (box / kPar) * 128, &tm_k, bars.k_full + sk, 0,
+                                ((first + lane * box) & (p.c.page - 1)) / kPar, good ? page * p.c.Hkv + c.h : p.c.n_pages * p.c.Hkv);
 #pragma unroll 1
-                for (int it = 0; it < 4; ++it, ++r) { // K low, K high, V low, V high
-                    const int sr = r % C::kRaws, lo = (it & 1) * in_item;
+                for (int it = 0; it < 2; ++it, ++r) { // V low, V high
+                    const int sr = r % C::kRaws, lo = it * in_item;
                     if (!(ok = wait_all(bars.raw_empty + sr, ((r / C::kRaws) & 1) ^ 1))) break;
                     const bool here = lane >= lo && lane < lo + in_item;
                     uint8_t *dst = smem + C::kRawOff + sr * C::kRaw + (lane - lo) * box * (D / 2);
@@ -408,7 +421,11 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                     if (lane == 0) mbar_expect_tx(bars.raw_full + sr, __popc(in) * box * (D / 2));
                     __syncwarp();
                     if (here && good)
-                        bulk_load(dst, static_cast<const uint8_t *>(it < 2 ? p.c.k : p.c.v) + row * (D / 2), box * (D / 2), bars.raw_full + sr);
+                        bulk_load(dst, static_cast<const uint8_t *>(p.c.v) + row * (D / 2), box * (D / 2), bars.raw_full + sr);
+                }
+                if (!ok) {
+                    ++i;
+                    break;
                 }
             }
             if (!ok || !cursor_next(p, part, c, n)) break;
@@ -417,14 +434,16 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
             // copies on their way land before the CTA ends (as below)
             for (uint32_t j = r > (uint32_t)C::kRaws ? r - C::kRaws : 0; j < r; ++j)
                 wait_drain(bars.raw_full + j % C::kRaws, (j / C::kRaws) & 1, kDrainNs);
-            for (uint32_t j = i >= (uint32_t)C::kXs ? i + 1 - C::kXs : 0; j <= i; ++j)
+            for (uint32_t j = i > (uint32_t)C::kXs ? i - C::kXs : 0; j < i; ++j)
                 wait_drain(bars.x_full + j % C::kXs, (j / C::kXs) & 1, kDrainNs);
+            for (uint32_t j = i > (uint32_t)C::kStages ? i - C::kStages : 0; j < i; ++j)
+                wait_drain(bars.k_full + j % C::kStages, (j / C::kStages) & 1, kDrainNs);
         }
     } else if (FP4 && any && warp >= C::kWideWarp && warp < C::kMmaWarp) {
         // ------------------------------------------------------------ 4-bit tiles
-        // A thread takes blocks of 32 codes (16 bytes, a quarter of a row of 128
-        // values).  Keys go to the products as they are, 16 codes in the lower
-        // half of every 16 bytes, their scales to TMEM; values become e4m3.
+        // Keys go to the products as they are; their scales are put into TMEM here.
+        // Of the values a thread takes blocks of 32 codes (16 bytes, a quarter of a
+        // row of 128), which become e4m3.
         constexpr int kRows = FP4 ? C::kWideThreads / 4 : 32, kBlocks = 64 / kRows; // rows at once; a thread's blocks of a half tile
         const int wt = threadIdx.x - C::kWideWarp * 32, x = wt & 3, row0 = wt >> 2;
         const bool scales = wt < 128; // the four warps that put the keys' scales into TMEM
@@ -446,11 +465,11 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
         for (;;) {
             const int n = cursor_take(c), len = source_len(c.b);
             for (int t = c.t0; ok && t < c.t0 + n; ++t, ++i) {
-                const int sx = i % C::kXs, st = i % C::kStages;
+                const int sx = i % C::kXs, sk = i % C::kStages, sv = i % C::kVStages;
                 const int valid = min(len - t * kTokens, kTokens);
                 const uint32_t *xs = reinterpret_cast<const uint32_t *>(smem + C::kXOff + sx * C::kX); // K's, then V's
                 if (!(ok = wait_all(bars.x_full + sx, (i / C::kXs) & 1))) break;
-                if (!(ok = wait_all(bars.k_empty + st, ((i / C::kStages) & 1) ^ 1))) break;
+                if (!(ok = wait_all(bars.k_empty + sk, ((i / C::kStages) & 1) ^ 1))) break;
                 uint32_t kx[4];
 #pragma unroll
                 for (int y = 0; y < 4; ++y) kx[y] = xs[lane + 32 * y];
@@ -461,7 +480,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                     for (int y = 0; y < 4; ++y)
                         if (lane + 32 * y == valid >> 1) kx[y] = (kx[y] & 0xffffu) | (ones & 0xffff0000u);
                 }
-                if (scales) tmem_st4(lane_base + C::kColX + 4 * st, kx[0], kx[1], kx[2], kx[3]);
+                if (scales) tmem_st4(lane_base + C::kColX + 4 * sk, kx[0], kx[1], kx[2], kx[3]);
                 // of the values' rows row0 + kRows y a group of four lanes has, lane x
                 // finds the scale byte and the entries of row y = x
                 const int mine = row0 + kRows * (x & (2 * kBlocks - 1));
@@ -470,8 +489,11 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 uint8_t *e = smem + C::kExpOff + (i % C::kEStages) * kTokens + mine * kPar;
 #pragma unroll
                 for (int y = 0; y < kPar; ++y) e[y] = mine * kPar + y < valid ? top[y] - kWide4Up : 127;
+                if (scales) tmem_st_wait();
+                tc_fence_before();
                 arrive(bars.e_full + i % C::kEStages);
                 arrive(bars.x_empty + sx);
+                if (!(ok = wait_all(bars.v_empty + sv, ((i / C::kVStages) & 1) ^ 1))) break;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half, ++r) {
                     const int sr = r % C::kRaws;
@@ -481,31 +503,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
 #pragma unroll
                     for (int u = 0; u < kBlocks; ++u) w[u] = lds4(raw + u * C::kWideThreads * 16);
                     arrive(bars.raw_empty + sr);
-                    const uint32_t tile = smem_u32(smem + C::kKOff + st * C::kMat);
-#pragma unroll
-                    for (int u = 0; u < kBlocks; ++u) {
-                        const int j = half * 64 + u * kRows + row0; // row of the tile
-                        const uint32_t at = tile + j * 128;
-                        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + (((2 * x) ^ (j & 7)) << 4)), "r"(w[u].x), "r"(w[u].y) : "memory");
-                        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + (((2 * x + 1) ^ (j & 7)) << 4)), "r"(w[u].z), "r"(w[u].w) : "memory");
-                    }
-                }
-                if (!ok) break;
-                tmem_st_wait();
-                tc_fence_before();
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                arrive(bars.k_full + st);
-                if (!(ok = wait_all(bars.v_empty + st, ((i / C::kStages) & 1) ^ 1))) break;
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half, ++r) {
-                    const int sr = r % C::kRaws;
-                    if (!(ok = wait_all(bars.raw_full + sr, (r / C::kRaws) & 1))) break;
-                    const uint32_t raw = smem_u32(smem + C::kRawOff + sr * C::kRaw) + wt * 16;
-                    uint4 w[kBlocks];
-#pragma unroll
-                    for (int u = 0; u < kBlocks; ++u) w[u] = lds4(raw + u * C::kWideThreads * 16);
-                    arrive(bars.raw_empty + sr);
-                    const uint32_t tile = smem_u32(smem + C::kVOff + st * C::kMat);
+                    const uint32_t tile = smem_u32(smem + C::kVOff + sv * C::kMat);
 #pragma unroll
                     for (int u = 0; u < kBlocks; ++u) {
                         const int j = half * 64 + u * kRows + row0;
@@ -524,7 +522,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 }
                 if (!ok) break;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                arrive(bars.v_full + st);
+                arrive(bars.v_full + sv);
             }
             if (!ok || !cursor_next(p, part, c, n)) break;
         }

@@ -22,6 +22,8 @@ int check_cache(const ra_kv_cache *c)
     if (!c->k || !c->v) return refuse(RA_ERR_INVALID_ARG, "cache tensors are NULL");
     if (!is_aligned(c->k, 16) || !is_aligned(c->v, 16))
         return refuse(RA_ERR_INVALID_ARG, "cache tensors must be 16-byte aligned");
+    if (c->dtype == RA_E2M1 && (!is_aligned(c->k, 32) || !is_aligned(c->v, 32)))
+        return refuse(RA_ERR_INVALID_ARG, "the tensors of an e2m1 cache must be 32-byte aligned");
     if (c->dtype != RA_BF16) {
         if (!c->k_exp || !c->v_exp) return refuse(RA_ERR_INVALID_ARG, "an e4m3 or e2m1 cache needs k_exp and v_exp");
         if (!is_aligned(c->k_exp, 16) || !is_aligned(c->v_exp, 16))
@@ -280,10 +282,15 @@ RA_API int ra_attn_paged(const ra_kv_cache *cache, const ra_paged_params *p, con
             e = launch_paged_f32(x, part, cache->dtype, s);
             continue;
         }
-        const int most = pl.kernel[k] == kRowsM && cache->dtype == RA_E4M3 ? 64 : 128; // of a box
-        const int in_page = cache->page_size * cache->D / 128, rows = in_page < most ? in_page : most;
-        CUtensorMap tk{}, tv{}; // 4-bit pages are fetched by plain copies
-        if (cache->dtype != RA_E2M1 && ((rc = encode_paged(&tk, cache, cache->k, rows)) || (rc = encode_paged(&tv, cache, cache->v, rows)))) return rc;
+        CUtensorMap tk{}, tv{};
+        if (cache->dtype == RA_E2M1) { // the rest of it is fetched by plain copies
+            const int in_page = cache->page_size * cache->D / 128, rows = in_page < 64 ? in_page : 64;
+            if (pl.kernel[k] == kKeysM && (rc = encode_paged(&tk, cache, cache->k, rows))) return rc;
+        } else {
+            const int most = pl.kernel[k] == kRowsM && cache->dtype == RA_E4M3 ? 64 : 128; // of a box
+            const int in_page = cache->page_size * cache->D / 128, rows = in_page < most ? in_page : most;
+            if ((rc = encode_paged(&tk, cache, cache->k, rows)) || (rc = encode_paged(&tv, cache, cache->v, rows))) return rc;
+        }
         e = pl.kernel[k] == kKeysM ? launch_paged_keys(x, part, cache->dtype, &tk, &tv, s)
                                    : launch_paged_rows(x, part, cache->dtype, &tk, &tv, s);
     }
