@@ -98,14 +98,14 @@ struct Cfg {
     static constexpr int kHalves = FP8 ? 1 : 2;             // 128-byte wide blocks of a tile
     static constexpr int kRT = RP < 8 ? RP : 8; // rows of a softmax warpgroup
     static constexpr int kGroups = RP / kRT, kSoftThreads = 128 * kGroups, kWideThreads = !FP4 ? 0 : RP == 4 ? 256 : 128;
-    static constexpr int kThreads = kSoftThreads + kWideThreads + 64;
+    static constexpr int kLoadWarps = FP4 && RP <= 8 ? 2 : 1; // K's and V's loads by a warp each, or by one
+    static constexpr int kThreads = kSoftThreads + kWideThreads + 32 + 32 * kLoadWarps;
     static constexpr int kWideWarp = 4 * kGroups, kMmaWarp = kWideWarp + kWideThreads / 32, kLoadWarp = kMmaWarp + 1;
     static constexpr int kCtasPerSm = FP8 && RP <= 16 ? 2 : 1;
-    static constexpr int kStages = FP4 ? (RP > 16 ? 5 : RP == 4 ? 3 : 2) : FP8 ? (RP == 8 ? 3 : RP == 16 ? 2 : 5) : 3;
+    static constexpr int kStages = FP4 ? (RP > 16 ? 3 : 2) : FP8 ? (RP == 8 ? 3 : RP == 16 ? 2 : 5) : 3;
     static constexpr int kVStages = FP4 ? (RP > 16 ? 3 : 2) : FP8 ? (RP > 16 ? 5 : 3) : RP > 16 ? 2 : 3;
-    // 4 bits: half tiles of V's codes, and the tiles' scale bytes, four to a row of
-    // K and of V
-    static constexpr int kRaw = kKeys * kD / 4, kRaws = !FP4 ? 0 : RP == 4 ? 4 : RP == 8 ? 6 : RP == 16 ? (D == 128 ? 5 : 4) : 8;
+    // 4 bits: V's codes, and the tiles' scale bytes, four to a row of K and of V
+    static constexpr int kRaw = kKeys * kD / 2, kRaws = !FP4 ? 0 : RP == 16 ? 2 : RP <= 8 ? 3 : 4;
     static constexpr int kXs = !FP4 ? 0 : RP > 16 ? 6 : RP == 16 ? 3 : 4, kX = 2 * kKeys * 4;
     // what a load of a row of K counts: 64 bytes, stored in 128
     static constexpr int kKRow = FP4 ? kD / 2 : kMat / kKeys;
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
             mbar_init(bars.raw_empty + s, C::kWideThreads / 32);
         }
         for (int s = 0; s < C::kXs; ++s) {
-            mbar_init(bars.x_full + s, 1);
+            mbar_init(bars.x_full + s, 2); // of K, of V
             mbar_init(bars.x_empty + s, C::kWideThreads / 32);
         }
         for (int s = 0; s < 2; ++s) {
@@ -359,98 +359,91 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
     };
     auto source_len = [&](int b) { return part.prefix ? paged_prefix_len(p) : paged_kv_len(p, b); };
 
-    if (FP4 && any && warp == C::kLoadWarp) {
+    if (FP4 && any && warp >= C::kLoadWarp) {
         // ------------------------------------------------------------ loads, 4 bits
-        // lane x fetches box x of a tile, of at most half of it: K by TMA, which
-        // leaves 16 codes in the lower half of every 16 bytes; of V the codes of a
-        // page's head lie together, and a plain bulk copy does
-        constexpr int kItem = kTokens / 2, kRowX = D / 32; // tokens of a half tile, scale bytes of a token
-        const int box = min(p.c.page, kItem), per = kTokens / box, in_item = kItem / box;
-        uint32_t i = 0, r = 0;
+        // lane x fetches box x of a tile: K by TMA, which leaves 16 codes in the lower
+        // half of every 16 bytes; of V the codes of a page's head lie together, and a
+        // plain bulk copy does.  (A chain of instructions of one warp: up to 8 rows
+        // the softmax's is no longer, so K and V have a warp each.)
+        constexpr int kRowX = D / 32, kTokenShift = D == 64 ? 8 : 7; // scale bytes of a token
+        const bool of_k = warp == C::kLoadWarp, of_v = warp == C::kLoadWarp + C::kLoadWarps - 1;
+        const int shift = min(p.c.page_shift, kTokenShift), box = 1 << shift; // tokens of a box
+        const int lane_tok = lane << shift, off = lane_tok & (p.c.page - 1);  // (a tile is whole pages)
+        uint32_t i = 0;
         bool ok = true;
-        auto entry = [&](int tile, int len) {
-            const int first = tile * kTokens + lane * box;
-            return lane < per && first < len ? page_entry(p, part, c.b, first) : 0;
+        // a tile's scale bytes, of K or of V, at `x`
+        auto scales = [&](uint8_t *x, const uint8_t *from, uint64_t *full, uint32_t goods, bool bad, bool good) {
+            if (bad) { // a scale of one
+                for (int j = 0; j < box * kRowX; ++j) x[j] = 127;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            __syncwarp();
+            if (lane == 0) mbar_expect_tx(full, __popc(goods) * box * kRowX);
+            __syncwarp();
+            if (good) bulk_load(x, from, box * kRowX, full);
         };
         for (;;) {
             const int n = cursor_take(c), len = source_len(c.b);
-            int next = entry(c.t0, len);
-            for (int t = c.t0; ok && t < c.t0 + n; ++t, ++i) {
+            const int32_t *pages = part.prefix ? p.prefix_table : p.page_table + (size_t)c.b * p.max_pages;
+            auto entry = [&](int first) { return lane_tok < kTokens && first + lane_tok < len ? pages[(first + lane_tok) >> p.c.page_shift] : 0; };
+            int next = entry(c.t0 * kTokens);
+            for (int t = c.t0; t < c.t0 + n; ++t, ++i) {
                 const int page = next, first = t * kTokens;
-                const int boxes = max(0, (min(len - first, kTokens) + box - 1) / box);
-                if (t + 1 < c.t0 + n) next = entry(t + 1, len);
-                const bool mine = lane < boxes, good = mine && page_valid(p, page);
-                const size_t row = good ? ((((size_t)page * p.c.Hkv + c.h) << p.c.page_shift) + ((first + lane * box) & (p.c.page - 1))) : 0;
-                const uint32_t goods = __ballot_sync(0xffffffffu, good);
-                const int sx = i % C::kXs;
+                if (t + 1 < c.t0 + n) next = entry(first + kTokens);
+                const bool mine = lane_tok < kTokens && first + lane_tok < len, good = mine && page_valid(p, page), bad = mine && !good;
+                const uint32_t goods = __ballot_sync(0xffffffffu, good), boxes = __popc(__ballot_sync(0xffffffffu, mine));
+                const int z = good ? page * p.c.Hkv + c.h : p.c.n_pages * p.c.Hkv; // out of range: zeros
+                const size_t row = ((size_t)z << p.c.page_shift) + off;
+                const int sx = i % C::kXs, sk = i % C::kStages, sr = i % C::kRaws;
+                uint8_t *x = smem + C::kXOff + sx * C::kX + lane_tok * kRowX;
                 if (!(ok = wait_all(bars.x_empty + sx, ((i / C::kXs) & 1) ^ 1))) break;
-                uint8_t *x = smem + C::kXOff + sx * C::kX + lane * box * kRowX;
-                if (mine && !good) { // zeros, at a scale of one
-                    for (int j = 0; j < box * kRowX; ++j) x[j] = x[C::kX / 2 + j] = 127;
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                if (of_k) {
+                    scales(x, p.c.k_exp + row * kRowX, bars.x_full + sx, goods, bad, good);
+                    if (!(ok = wait_all(bars.k_empty + sk, ((i / C::kStages) & 1) ^ 1))) break;
+                    if (lane == 0) mbar_expect_tx(bars.k_full + sk, boxes * (box / kPar) * C::kKRow);
+                    __syncwarp();
+                    if (mine)
+                        tma_load_3d(smem + C::kKOff + sk * C::kMat + (lane_tok / kPar) * 128, &tm_k, bars.k_full + sk, 0, off / kPar, z);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_expect_tx(bars.x_full + sx, 2 * __popc(goods) * box * kRowX);
-                __syncwarp();
-                if (good) {
-                    bulk_load(x, p.c.k_exp + row * kRowX, box * kRowX, bars.x_full + sx);
-                    bulk_load(x + C::kX / 2, p.c.v_exp + row * kRowX, box * kRowX, bars.x_full + sx);
-                }
-                const int sk = i % C::kStages;
-                if (!(ok = wait_all(bars.k_empty + sk, ((i / C::kStages) & 1) ^ 1))) {
-                    ++i; // this tile's scale bytes are on their way, its codes are not
-                    break;
-                }
-                if (lane == 0) mbar_expect_tx(bars.k_full + sk, boxes * (box / kPar) * C::kKRow);
-                __syncwarp();
-                if (mine)
-                    tma_load_3d(smem + C::kKOff + sk * C::kMat + lane * (box / kPar) * 128, &tm_k, bars.k_full + sk, 0,
-                                ((first + lane * box) & (p.c.page - 1)) / kPar, good ? page * p.c.Hkv + c.h : p.c.n_pages * p.c.Hkv);
-#pragma unroll 1
-                for (int it = 0; it < 2; ++it, ++r) { // V low, V high
-                    const int sr = r % C::kRaws, lo = it * in_item;
-                    if (!(ok = wait_all(bars.raw_empty + sr, ((r / C::kRaws) & 1) ^ 1))) break;
-                    const bool here = lane >= lo && lane < lo + in_item;
-                    uint8_t *dst = smem + C::kRawOff + sr * C::kRaw + (lane - lo) * box * (D / 2);
-                    if (here && mine && !good) {
+                if (of_v) {
+                    scales(x + C::kX / 2, p.c.v_exp + row * kRowX, bars.x_full + sx, goods, bad, good);
+                    if (!(ok = wait_all(bars.raw_empty + sr, ((i / C::kRaws) & 1) ^ 1))) break;
+                    uint8_t *dst = smem + C::kRawOff + sr * C::kRaw + lane_tok * (D / 2);
+                    if (bad) {
                         for (int j = 0; j < box * (D / 2); j += 16) *reinterpret_cast<uint4 *>(dst + j) = make_uint4(0, 0, 0, 0);
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     }
                     __syncwarp();
-                    const uint32_t in = __ballot_sync(0xffffffffu, here && good);
-                    if (lane == 0) mbar_expect_tx(bars.raw_full + sr, __popc(in) * box * (D / 2));
+                    if (lane == 0) mbar_expect_tx(bars.raw_full + sr, __popc(goods) * box * (D / 2));
                     __syncwarp();
-                    if (here && good)
-                        bulk_load(dst, static_cast<const uint8_t *>(p.c.v) + row * (D / 2), box * (D / 2), bars.raw_full + sr);
-                }
-                if (!ok) {
-                    ++i;
-                    break;
+                    if (good) bulk_load(dst, static_cast<const uint8_t *>(p.c.v) + row * (D / 2), box * (D / 2), bars.raw_full + sr);
                 }
             }
             if (!ok || !cursor_next(p, part, c, n)) break;
         }
         if (!ok || *abort_flag) {
-            // copies on their way land before the CTA ends (as below)
-            for (uint32_t j = r > (uint32_t)C::kRaws ? r - C::kRaws : 0; j < r; ++j)
-                wait_drain(bars.raw_full + j % C::kRaws, (j / C::kRaws) & 1, kDrainNs);
-            for (uint32_t j = i > (uint32_t)C::kXs ? i - C::kXs : 0; j < i; ++j)
-                wait_drain(bars.x_full + j % C::kXs, (j / C::kXs) & 1, kDrainNs);
-            for (uint32_t j = i > (uint32_t)C::kStages ? i - C::kStages : 0; j < i; ++j)
-                wait_drain(bars.k_full + j % C::kStages, (j / C::kStages) & 1, kDrainNs);
+            // copies on their way land before the CTA ends: tile j's phase of each
+            // ring, for the last ones (a phase that already passed, or was not begun,
+            // only runs the clock)
+            auto drain = [&](uint64_t *full, uint32_t stages) {
+                for (uint32_t j = i >= stages ? i + 1 - stages : 0; j <= i; ++j) wait_drain(full + j % stages, (j / stages) & 1, kDrainNs);
+            };
+            drain(bars.x_full, C::kXs);
+            if (of_k) drain(bars.k_full, C::kStages);
+            if (of_v) drain(bars.raw_full, C::kRaws);
         }
     } else if (FP4 && any && warp >= C::kWideWarp && warp < C::kMmaWarp) {
         // ------------------------------------------------------------ 4-bit tiles
         // Keys go to the products as they are; their scales are put into TMEM here.
         // Of the values a thread takes blocks of 32 codes (16 bytes, a quarter of a
         // row of 128), which become e4m3.
-        constexpr int kRows = FP4 ? C::kWideThreads / 4 : 32, kBlocks = 64 / kRows; // rows at once; a thread's blocks of a half tile
+        constexpr int kRows = FP4 ? C::kWideThreads / 4 : 32, kBlocks = kKeys / kRows; // rows at once; a thread's blocks of a tile
         const int wt = threadIdx.x - C::kWideWarp * 32, x = wt & 3, row0 = wt >> 2;
         const bool scales = wt < 128; // the four warps that put the keys' scales into TMEM
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ones = 0x7f7f7f7fu;
         if (scales) tmem_st4(lane_base + C::kColOnes, ones, ones, ones, ones);
-        uint32_t i = 0, r = 0;
+        uint32_t i = 0;
         bool ok = true;
         auto lds4 = [](uint32_t at) {
             uint4 w;
@@ -483,7 +476,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 if (scales) tmem_st4(lane_base + C::kColX + 4 * sk, kx[0], kx[1], kx[2], kx[3]);
                 // of the values' rows row0 + kRows y a group of four lanes has, lane x
                 // finds the scale byte and the entries of row y = x
-                const int mine = row0 + kRows * (x & (2 * kBlocks - 1));
+                const int mine = row0 + kRows * (x & (kBlocks - 1));
                 uint32_t top[2];
                 const uint32_t in = wide4_rows<kPar == 2>(xs[kKeys + mine], top);
                 uint8_t *e = smem + C::kExpOff + (i % C::kEStages) * kTokens + mine * kPar;
@@ -494,33 +487,29 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 arrive(bars.e_full + i % C::kEStages);
                 arrive(bars.x_empty + sx);
                 if (!(ok = wait_all(bars.v_empty + sv, ((i / C::kVStages) & 1) ^ 1))) break;
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half, ++r) {
-                    const int sr = r % C::kRaws;
-                    if (!(ok = wait_all(bars.raw_full + sr, (r / C::kRaws) & 1))) break;
-                    const uint32_t raw = smem_u32(smem + C::kRawOff + sr * C::kRaw) + wt * 16;
-                    uint4 w[kBlocks];
+                const int sr = i % C::kRaws;
+                if (!(ok = wait_all(bars.raw_full + sr, (i / C::kRaws) & 1))) break;
+                const uint32_t raw = smem_u32(smem + C::kRawOff + sr * C::kRaw) + wt * 16;
+                uint4 w[kBlocks];
 #pragma unroll
-                    for (int u = 0; u < kBlocks; ++u) w[u] = lds4(raw + u * C::kWideThreads * 16);
-                    arrive(bars.raw_empty + sr);
-                    const uint32_t tile = smem_u32(smem + C::kVOff + sv * C::kMat);
+                for (int u = 0; u < kBlocks; ++u) w[u] = lds4(raw + u * C::kWideThreads * 16);
+                arrive(bars.raw_empty + sr);
+                const uint32_t tile = smem_u32(smem + C::kVOff + sv * C::kMat);
 #pragma unroll
-                    for (int u = 0; u < kBlocks; ++u) {
-                        const int j = half * 64 + u * kRows + row0;
-                        const uint2 tab = table[__shfl_sync(0xffffffffu, in, half * kBlocks + u, 4) >> (8 * x) & 0xffu];
-                        uint2 o[4] = {wide4(w[u].x, tab), wide4(w[u].y, tab), wide4(w[u].z, tab), wide4(w[u].w, tab)};
-                        // (tokens behind the length: whatever is there, weight 0 must give 0)
-                        if (j * kPar + (kPar == 2 ? x >> 1 : 0) >= valid) o[0] = o[1] = o[2] = o[3] = make_uint2(0, 0);
-                        const uint32_t at = tile + j * 128;
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((2 * x) ^ (j & 7)) << 4)), "r"(o[0].x),
-                                     "r"(o[0].y), "r"(o[1].x), "r"(o[1].y)
-                                     : "memory");
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((2 * x + 1) ^ (j & 7)) << 4)), "r"(o[2].x),
-                                     "r"(o[2].y), "r"(o[3].x), "r"(o[3].y)
-                                     : "memory");
-                    }
+                for (int u = 0; u < kBlocks; ++u) {
+                    const int j = u * kRows + row0;
+                    const uint2 tab = table[__shfl_sync(0xffffffffu, in, u, 4) >> (8 * x) & 0xffu];
+                    uint2 o[4] = {wide4(w[u].x, tab), wide4(w[u].y, tab), wide4(w[u].z, tab), wide4(w[u].w, tab)};
+                    // (tokens behind the length: whatever is there, weight 0 must give 0)
+                    if (j * kPar + (kPar == 2 ? x >> 1 : 0) >= valid) o[0] = o[1] = o[2] = o[3] = make_uint2(0, 0);
+                    const uint32_t at = tile + j * 128;
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((2 * x) ^ (j & 7)) << 4)), "r"(o[0].x), "r"(o[0].y),
+                                 "r"(o[1].x), "r"(o[1].y)
+                                 : "memory");
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((2 * x + 1) ^ (j & 7)) << 4)), "r"(o[2].x),
+                                 "r"(o[2].y), "r"(o[3].x), "r"(o[3].y)
+                                 : "memory");
                 }
-                if (!ok) break;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 arrive(bars.v_full + sv);
             }

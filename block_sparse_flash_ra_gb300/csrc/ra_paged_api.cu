@@ -284,7 +284,7 @@ RA_API int ra_attn_paged(const ra_kv_cache *cache, const ra_paged_params *p, con
         }
         CUtensorMap tk{}, tv{};
         if (cache->dtype == RA_E2M1) { // the rest of it is fetched by plain copies
-            const int in_page = cache->page_size * cache->D / 128, rows = in_page < 64 ? in_page : 64;
+            const int in_page = cache->page_size * cache->D / 128, rows = in_page < 128 ? in_page : 128;
             if (pl.kernel[k] == kKeysM && (rc = encode_paged(&tk, cache, cache->k, rows))) return rc;
         } else {
             const int most = pl.kernel[k] == kRowsM && cache->dtype == RA_E4M3 ? 64 : 128; // of a box
