@@ -99,8 +99,9 @@ struct Cfg {
     static constexpr int kRT = RP < 8 ? RP : 8; // rows of a softmax warpgroup
     static constexpr int kGroups = RP / kRT, kSoftThreads = 128 * kGroups, kWideThreads = !FP4 ? 0 : RP == 4 ? 256 : 128;
     static constexpr int kLoadWarps = FP4 && RP <= 8 ? 2 : 1; // K's and V's loads by a warp each, or by one
-    static constexpr int kThreads = kSoftThreads + kWideThreads + 32 + 32 * kLoadWarps;
-    static constexpr int kWideWarp = 4 * kGroups, kMmaWarp = kWideWarp + kWideThreads / 32, kLoadWarp = kMmaWarp + 1;
+    static constexpr int kMmaWarps = FP4 && RP <= 8 ? 2 : 1; // S's and P V's products, too
+    static constexpr int kThreads = kSoftThreads + kWideThreads + 32 * (kMmaWarps + kLoadWarps);
+    static constexpr int kWideWarp = 4 * kGroups, kMmaWarp = kWideWarp + kWideThreads / 32, kLoadWarp = kMmaWarp + kMmaWarps;
     static constexpr int kCtasPerSm = FP8 && RP <= 16 ? 2 : 1;
     static constexpr int kStages = FP4 ? (RP > 16 ? 3 : 2) : FP8 ? (RP == 8 ? 3 : RP == 16 ? 2 : 5) : 3;
     static constexpr int kVStages = FP4 ? (RP > 16 ? 3 : 2) : FP8 ? (RP > 16 ? 5 : 3) : RP > 16 ? 2 : 3;
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
             mbar_init(bars.pv_done + s, 1);
             mbar_init(bars.q_full + s, C::kSoftThreads);
         }
-        mbar_init(bars.drain, 1);
+        mbar_init(bars.drain, C::kMmaWarps);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
         // plain bulk copy does.  (A chain of instructions of one warp: up to 8 rows
         // the softmax's is no longer, so K and V have a warp each.)
         constexpr int kRowX = D / 32, kTokenShift = D == 64 ? 8 : 7; // scale bytes of a token
-        const bool of_k = warp == C::kLoadWarp, of_v = warp == C::kLoadWarp + C::kLoadWarps - 1;
+        const bool of_k = C::kLoadWarps == 1 || warp == C::kLoadWarp, of_v = C::kLoadWarps == 1 || !of_k;
         const int shift = min(p.c.page_shift, kTokenShift), box = 1 << shift; // tokens of a box
         const int lane_tok = lane << shift, off = lane_tok & (p.c.page - 1);  // (a tile is whole pages)
         uint32_t i = 0;
@@ -439,10 +440,10 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
         // row of 128), which become e4m3.
         constexpr int kRows = FP4 ? C::kWideThreads / 4 : 32, kBlocks = kKeys / kRows; // rows at once; a thread's blocks of a tile
         const int wt = threadIdx.x - C::kWideWarp * 32, x = wt & 3, row0 = wt >> 2;
-        const bool scales = wt < 128; // the four warps that put the keys' scales into TMEM
+        const bool of_keys = wt < 128; // the four warps that put the keys' scales into TMEM
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ones = 0x7f7f7f7fu;
-        if (scales) tmem_st4(lane_base + C::kColOnes, ones, ones, ones, ones);
+        if (of_keys) tmem_st4(lane_base + C::kColOnes, ones, ones, ones, ones);
         uint32_t i = 0;
         bool ok = true;
         auto lds4 = [](uint32_t at) {
@@ -463,17 +464,19 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 const uint32_t *xs = reinterpret_cast<const uint32_t *>(smem + C::kXOff + sx * C::kX); // K's, then V's
                 if (!(ok = wait_all(bars.x_full + sx, (i / C::kXs) & 1))) break;
                 if (!(ok = wait_all(bars.k_empty + sk, ((i / C::kStages) & 1) ^ 1))) break;
-                uint32_t kx[4];
+                if (of_keys) {
+                    uint32_t kx[4];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) kx[y] = xs[lane + 32 * y];
-                if (kPar == 2 && (valid & 1)) {
-                    // an odd length ends inside a row: its other token meets zeros of Q,
-                    // whose product with a scale of NaN would not be zero
+                    for (int y = 0; y < 4; ++y) kx[y] = xs[lane + 32 * y];
+                    if (kPar == 2 && (valid & 1)) {
+                        // an odd length ends inside a row: its other token meets zeros of Q,
+                        // whose product with a scale of NaN would not be zero
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        if (lane + 32 * y == valid >> 1) kx[y] = (kx[y] & 0xffffu) | (ones & 0xffff0000u);
+                        for (int y = 0; y < 4; ++y)
+                            if (lane + 32 * y == valid >> 1) kx[y] = (kx[y] & 0xffffu) | (ones & 0xffff0000u);
+                    }
+                    tmem_st4(lane_base + C::kColX + 4 * sk, kx[0], kx[1], kx[2], kx[3]);
                 }
-                if (scales) tmem_st4(lane_base + C::kColX + 4 * sk, kx[0], kx[1], kx[2], kx[3]);
                 // of the values' rows row0 + kRows y a group of four lanes has, lane x
                 // finds the scale byte and the entries of row y = x
                 const int mine = row0 + kRows * (x & (kBlocks - 1));
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 uint8_t *e = smem + C::kExpOff + (i % C::kEStages) * kTokens + mine * kPar;
 #pragma unroll
                 for (int y = 0; y < kPar; ++y) e[y] = mine * kPar + y < valid ? top[y] - kWide4Up : 127;
-                if (scales) tmem_st_wait();
+                if (of_keys) tmem_st_wait();
                 tc_fence_before();
                 arrive(bars.e_full + i % C::kEStages);
                 arrive(bars.x_empty + sx);
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                     const uint2 tab = table[__shfl_sync(0xffffffffu, in, u, 4) >> (8 * x) & 0xffu];
                     uint2 o[4] = {wide4(w[u].x, tab), wide4(w[u].y, tab), wide4(w[u].z, tab), wide4(w[u].w, tab)};
                     // (tokens behind the length: whatever is there, weight 0 must give 0)
-                    if (j * kPar + (kPar == 2 ? x >> 1 : 0) >= valid) o[0] = o[1] = o[2] = o[3] = make_uint2(0, 0);
+                    if (valid < kTokens && j * kPar + (kPar == 2 ? x >> 1 : 0) >= valid) o[0] = o[1] = o[2] = o[3] = make_uint2(0, 0);
                     const uint32_t at = tile + j * 128;
                     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((2 * x) ^ (j & 7)) << 4)), "r"(o[0].x), "r"(o[0].y),
                                  "r"(o[1].x), "r"(o[1].y)
@@ -584,8 +587,9 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 if (FP8) wait_drain(bars.e_full + j % C::kVStages, (j / C::kVStages) & 1, kDrainNs);
             }
         }
-    } else if (any && warp == C::kMmaWarp) {
+    } else if (any && warp >= C::kMmaWarp && warp < C::kLoadWarp) {
         // ------------------------------------------------------------ products
+        const bool of_s = C::kMmaWarps == 1 || warp == C::kMmaWarp, of_pv = C::kMmaWarps == 1 || !of_s;
         const uint64_t kd0 = sdesc_sw128(smem_u32(smem + C::kKOff), 16, 1024);
         const uint64_t vd0 = sdesc_sw128(smem_u32(smem + C::kVOff), kKeys * 128, 1024);
         const uint64_t qd0 = sdesc_sw128(smem_u32(smem + C::kQOff), 16, 1024);
@@ -611,13 +615,19 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
         };
         for (;;) {
             const int n = cursor_take(c), len = kPar == 2 ? source_len(c.b) : 0;
-            if (!(ok = wait_all(bars.q_full + (segs & 1), (segs >> 1) & 1))) break;
+            if (of_s && !(ok = wait_all(bars.q_full + (segs & 1), (segs >> 1) & 1))) break;
             const uint64_t qd = qd0 + (uint32_t)(((segs++ & 1) * C::kQBytes) >> 4);
             for (int t = 0; ok && t < n; ++t, ++i) {
+                if (!of_s) { // its own pace: P says when
+                    ok = issue_pv(i, t == 0);
+                    continue;
+                }
                 const int sk = i % C::kStages, sb = i & 1;
                 if (!(ok = wait_all(bars.k_full + sk, (i / C::kStages) & 1))) break;
                 if (FP8 && !(ok = wait_all(bars.e_full + i % C::kEStages, (i / C::kEStages) & 1))) break;
                 if (!(ok = wait_all(bars.s_empty + sb, ((i >> 1) & 1) ^ 1))) break;
+                // the softmax writes P over that of the tile before last once S is there
+                if (!of_pv && i >= 2 && !(ok = wait_all(bars.pv_done + sb, ((i - 2) >> 1) & 1))) break;
                 tc_fence_after();
                 if (kPar == 2 && !FP4) {
                     // an odd length ends inside a row: its other token meets the zeros of
@@ -649,9 +659,9 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 // passes on what the wait for them has seen
                 if (FP8 && lane == 0) mbar_arrive(bars.s_full + sb);
                 tc_commit_w(bars.s_full + sb);
-                if (t > 0) ok = issue_pv(i - 1, t == 1);
+                if (of_pv && t > 0) ok = issue_pv(i - 1, t == 1);
             }
-            if (!ok || !(ok = issue_pv(i - 1, n == 1))) break;
+            if (!ok || (of_s && of_pv && !(ok = issue_pv(i - 1, n == 1)))) break;
             if (!cursor_next(p, part, c, n)) break;
         }
         tc_commit_w(bars.drain);

@@ -31,12 +31,20 @@ __device__ __forceinline__ void wide4_fill(uint2 *table, int k)
 template <bool HALF>
 __device__ __forceinline__ uint32_t wide4_rows(uint32_t w, uint32_t *top)
 {
-    uint32_t b[4], t[4], in = 0;
+    uint32_t b[4], in = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        b[i] = w >> (8 * i) & 0xffu;
-        t[i] = b[i] == 255u ? 0u : b[i];
+    for (int i = 0; i < 4; ++i) b[i] = w >> (8 * i) & 0xffu;
+    top[0] = max(max(b[0], b[1]), (uint32_t)kWide4Up);
+    top[1] = max(max(b[2], b[3]), (uint32_t)kWide4Up);
+    if (!HALF) top[0] = top[1] = max(top[0], top[1]);
+    if (max(top[0], top[1]) < 255u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) in |= min(top[i >> 1] - b[i], (uint32_t)kWide4Zero) << (8 * i);
+        return in;
     }
+    uint32_t t[4]; // rare
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = b[i] == 255u ? 0u : b[i];
     top[0] = max(max(t[0], t[1]), (uint32_t)kWide4Up);
     top[1] = max(max(t[2], t[3]), (uint32_t)kWide4Up);
     if (!HALF) top[0] = top[1] = max(top[0], top[1]);
