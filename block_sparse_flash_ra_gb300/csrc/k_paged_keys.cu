@@ -97,11 +97,9 @@ struct Cfg {
     static constexpr int kMat = kKeys * kD * (FP8 ? 1 : 2); // bytes of a K or V tile
     static constexpr int kHalves = FP8 ? 1 : 2;             // 128-byte wide blocks of a tile
     static constexpr int kRT = RP < 8 ? RP : 8; // rows of a softmax warpgroup
-    static constexpr int kGroups = RP / kRT, kSoftThreads = 128 * kGroups, kWideThreads = !FP4 ? 0 : RP == 4 ? 256 : 128;
-    static constexpr int kLoadWarps = FP4 && RP <= 8 ? 2 : 1; // K's and V's loads by a warp each, or by one
-    static constexpr int kMmaWarps = FP4 && RP <= 8 ? 2 : 1; // S's and P V's products, too
-    static constexpr int kThreads = kSoftThreads + kWideThreads + 32 * (kMmaWarps + kLoadWarps);
-    static constexpr int kWideWarp = 4 * kGroups, kMmaWarp = kWideWarp + kWideThreads / 32, kLoadWarp = kMmaWarp + kMmaWarps;
+    static constexpr int kGroups = RP / kRT, kSoftThreads = 128 * kGroups, kWideThreads = FP4 ? 128 : 0;
+    static constexpr int kThreads = kSoftThreads + kWideThreads + 64;
+    static constexpr int kWideWarp = 4 * kGroups, kMmaWarp = kWideWarp + kWideThreads / 32, kLoadWarp = kMmaWarp + 1;
     static constexpr int kCtasPerSm = FP8 && RP <= 16 ? 2 : 1;
     static constexpr int kStages = FP4 ? (RP > 16 ? 3 : 2) : FP8 ? (RP == 8 ? 3 : RP == 16 ? 2 : 5) : 3;
     static constexpr int kVStages = FP4 ? (RP > 16 ? 3 : 2) : FP8 ? (RP > 16 ? 5 : 3) : RP > 16 ? 2 : 3;
@@ -323,7 +321,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
             mbar_init(bars.raw_empty + s, C::kWideThreads / 32);
         }
         for (int s = 0; s < C::kXs; ++s) {
-            mbar_init(bars.x_full + s, 2); // of K, of V
+            mbar_init(bars.x_full + s, 1);
             mbar_init(bars.x_empty + s, C::kWideThreads / 32);
         }
         for (int s = 0; s < 2; ++s) {
@@ -333,7 +331,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
             mbar_init(bars.pv_done + s, 1);
             mbar_init(bars.q_full + s, C::kSoftThreads);
         }
-        mbar_init(bars.drain, C::kMmaWarps);
+        mbar_init(bars.drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -360,29 +358,16 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
     };
     auto source_len = [&](int b) { return part.prefix ? paged_prefix_len(p) : paged_kv_len(p, b); };
 
-    if (FP4 && any && warp >= C::kLoadWarp) {
+    if (FP4 && any && warp == C::kLoadWarp) {
         // ------------------------------------------------------------ loads, 4 bits
         // lane x fetches box x of a tile: K by TMA, which leaves 16 codes in the lower
         // half of every 16 bytes; of V the codes of a page's head lie together, and a
-        // plain bulk copy does.  (A chain of instructions of one warp: up to 8 rows
-        // the softmax's is no longer, so K and V have a warp each.)
+        // plain bulk copy does.
         constexpr int kRowX = D / 32, kTokenShift = D == 64 ? 8 : 7; // scale bytes of a token
-        const bool of_k = C::kLoadWarps == 1 || warp == C::kLoadWarp, of_v = C::kLoadWarps == 1 || !of_k;
         const int shift = min(p.c.page_shift, kTokenShift), box = 1 << shift; // tokens of a box
         const int lane_tok = lane << shift, off = lane_tok & (p.c.page - 1);  // (a tile is whole pages)
         uint32_t i = 0;
         bool ok = true;
-        // a tile's scale bytes, of K or of V, at `x`
-        auto scales = [&](uint8_t *x, const uint8_t *from, uint64_t *full, uint32_t goods, bool bad, bool good) {
-            if (bad) { // a scale of one
-                for (int j = 0; j < box * kRowX; ++j) x[j] = 127;
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            }
-            __syncwarp();
-            if (lane == 0) mbar_expect_tx(full, __popc(goods) * box * kRowX);
-            __syncwarp();
-            if (good) bulk_load(x, from, box * kRowX, full);
-        };
         for (;;) {
             const int n = cursor_take(c), len = source_len(c.b);
             const int32_t *pages = part.prefix ? p.prefix_table : p.page_table + (size_t)c.b * p.max_pages;
@@ -398,27 +383,32 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 const int sx = i % C::kXs, sk = i % C::kStages, sr = i % C::kRaws;
                 uint8_t *x = smem + C::kXOff + sx * C::kX + lane_tok * kRowX;
                 if (!(ok = wait_all(bars.x_empty + sx, ((i / C::kXs) & 1) ^ 1))) break;
-                if (of_k) {
-                    scales(x, p.c.k_exp + row * kRowX, bars.x_full + sx, goods, bad, good);
-                    if (!(ok = wait_all(bars.k_empty + sk, ((i / C::kStages) & 1) ^ 1))) break;
-                    if (lane == 0) mbar_expect_tx(bars.k_full + sk, boxes * (box / kPar) * C::kKRow);
-                    __syncwarp();
-                    if (mine)
-                        tma_load_3d(smem + C::kKOff + sk * C::kMat + (lane_tok / kPar) * 128, &tm_k, bars.k_full + sk, 0, off / kPar, z);
+                if (bad) { // a scale of one
+                    for (int j = 0; j < box * kRowX; ++j) x[j] = x[C::kX / 2 + j] = 127;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                if (of_v) {
-                    scales(x + C::kX / 2, p.c.v_exp + row * kRowX, bars.x_full + sx, goods, bad, good);
-                    if (!(ok = wait_all(bars.raw_empty + sr, ((i / C::kRaws) & 1) ^ 1))) break;
-                    uint8_t *dst = smem + C::kRawOff + sr * C::kRaw + lane_tok * (D / 2);
-                    if (bad) {
-                        for (int j = 0; j < box * (D / 2); j += 16) *reinterpret_cast<uint4 *>(dst + j) = make_uint4(0, 0, 0, 0);
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_expect_tx(bars.raw_full + sr, __popc(goods) * box * (D / 2));
-                    __syncwarp();
-                    if (good) bulk_load(dst, static_cast<const uint8_t *>(p.c.v) + row * (D / 2), box * (D / 2), bars.raw_full + sr);
+                __syncwarp();
+                if (lane == 0) mbar_expect_tx(bars.x_full + sx, 2 * __popc(goods) * box * kRowX);
+                __syncwarp();
+                if (good) {
+                    bulk_load(x, p.c.k_exp + row * kRowX, box * kRowX, bars.x_full + sx);
+                    bulk_load(x + C::kX / 2, p.c.v_exp + row * kRowX, box * kRowX, bars.x_full + sx);
                 }
+                if (!(ok = wait_all(bars.k_empty + sk, ((i / C::kStages) & 1) ^ 1))) break;
+                if (lane == 0) mbar_expect_tx(bars.k_full + sk, boxes * (box / kPar) * C::kKRow);
+                __syncwarp();
+                if (mine)
+                    tma_load_3d(smem + C::kKOff + sk * C::kMat + (lane_tok / kPar) * 128, &tm_k, bars.k_full + sk, 0, off / kPar, z);
+                if (!(ok = wait_all(bars.raw_empty + sr, ((i / C::kRaws) & 1) ^ 1))) break;
+                uint8_t *dst = smem + C::kRawOff + sr * C::kRaw + lane_tok * (D / 2);
+                if (bad) {
+                    for (int j = 0; j < box * (D / 2); j += 16) *reinterpret_cast<uint4 *>(dst + j) = make_uint4(0, 0, 0, 0);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                __syncwarp();
+                if (lane == 0) mbar_expect_tx(bars.raw_full + sr, __popc(goods) * box * (D / 2));
+                __syncwarp();
+                if (good) bulk_load(dst, static_cast<const uint8_t *>(p.c.v) + row * (D / 2), box * (D / 2), bars.raw_full + sr);
             }
             if (!ok || !cursor_next(p, part, c, n)) break;
         }
@@ -430,8 +420,8 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 for (uint32_t j = i >= stages ? i + 1 - stages : 0; j <= i; ++j) wait_drain(full + j % stages, (j / stages) & 1, kDrainNs);
             };
             drain(bars.x_full, C::kXs);
-            if (of_k) drain(bars.k_full, C::kStages);
-            if (of_v) drain(bars.raw_full, C::kRaws);
+            drain(bars.k_full, C::kStages);
+            drain(bars.raw_full, C::kRaws);
         }
     } else if (FP4 && any && warp >= C::kWideWarp && warp < C::kMmaWarp) {
         // ------------------------------------------------------------ 4-bit tiles
@@ -587,9 +577,8 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 if (FP8) wait_drain(bars.e_full + j % C::kVStages, (j / C::kVStages) & 1, kDrainNs);
             }
         }
-    } else if (any && warp >= C::kMmaWarp && warp < C::kLoadWarp) {
+    } else if (any && warp == C::kMmaWarp) {
         // ------------------------------------------------------------ products
-        const bool of_s = C::kMmaWarps == 1 || warp == C::kMmaWarp, of_pv = C::kMmaWarps == 1 || !of_s;
         const uint64_t kd0 = sdesc_sw128(smem_u32(smem + C::kKOff), 16, 1024);
         const uint64_t vd0 = sdesc_sw128(smem_u32(smem + C::kVOff), kKeys * 128, 1024);
         const uint64_t qd0 = sdesc_sw128(smem_u32(smem + C::kQOff), 16, 1024);
@@ -615,19 +604,13 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
         };
         for (;;) {
             const int n = cursor_take(c), len = kPar == 2 ? source_len(c.b) : 0;
-            if (of_s && !(ok = wait_all(bars.q_full + (segs & 1), (segs >> 1) & 1))) break;
+            if (!(ok = wait_all(bars.q_full + (segs & 1), (segs >> 1) & 1))) break;
             const uint64_t qd = qd0 + (uint32_t)(((segs++ & 1) * C::kQBytes) >> 4);
             for (int t = 0; ok && t < n; ++t, ++i) {
-                if (!of_s) { // its own pace: P says when
-                    ok = issue_pv(i, t == 0);
-                    continue;
-                }
                 const int sk = i % C::kStages, sb = i & 1;
                 if (!(ok = wait_all(bars.k_full + sk, (i / C::kStages) & 1))) break;
                 if (FP8 && !(ok = wait_all(bars.e_full + i % C::kEStages, (i / C::kEStages) & 1))) break;
                 if (!(ok = wait_all(bars.s_empty + sb, ((i >> 1) & 1) ^ 1))) break;
-                // the softmax writes P over that of the tile before last once S is there
-                if (!of_pv && i >= 2 && !(ok = wait_all(bars.pv_done + sb, ((i - 2) >> 1) & 1))) break;
                 tc_fence_after();
                 if (kPar == 2 && !FP4) {
                     // an odd length ends inside a row: its other token meets the zeros of
@@ -659,9 +642,9 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 // passes on what the wait for them has seen
                 if (FP8 && lane == 0) mbar_arrive(bars.s_full + sb);
                 tc_commit_w(bars.s_full + sb);
-                if (of_pv && t > 0) ok = issue_pv(i - 1, t == 1);
+                if (t > 0) ok = issue_pv(i - 1, t == 1);
             }
-            if (!ok || (of_s && of_pv && !(ok = issue_pv(i - 1, n == 1)))) break;
+            if (!ok || !(ok = issue_pv(i - 1, n == 1))) break;
             if (!cursor_next(p, part, c, n)) break;
         }
         tc_commit_w(bars.drain);
