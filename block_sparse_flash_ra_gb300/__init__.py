@@ -794,14 +794,17 @@ def make_qk_params(q, k=None, *, rope=None, pos=None, start=None, prefix_len=Non
                    _ptr(prefix_len))
     p._keep = (rope, pos, start, prefix_len, q_weight, k_weight)
     p._like = tuple(None if t is None else (t.shape, t.dtype) for t in (q, k))
-    p.device, p._index = x.device, index
-    p._ws = ra_qk_bwd_workspace_size(p) if B and L else 0
+    p.device, p._index, p._any = x.device, index, bool(B and L)
+    # dense tensors' strides, and elements between their tokens
+    p._step = [0 if t is None else t.shape[2] * D for t in (q, k)]
+    p._dense = [None if t is None else (L * n, n, D, 1) for t, n in zip((q, k), p._step)]
+    p._ws = ra_qk_bwd_workspace_size(p) if p._any else 0
     p._ref = ctypes.addressof(p)
     return p
 
 
 def _qk_rows(params, which, x, name):
-    """(address, stride) of q-like (which = 0) or k-like tensors; nothing where there are no heads."""
+    """(address, stride) of a tensor like q (which = 0) or like k; nothing where there are no heads."""
     like = params._like[which]
     if like is None:
         _need(x is None, f"{name}: the params were made without it")
@@ -810,22 +813,30 @@ def _qk_rows(params, which, x, name):
         raise ValueError(f"{name} must have the shape and dtype the params were made for")
     if x.get_device() != params._index:
         raise ValueError(f"{name} must be on the params' device")
-    return x.data_ptr(), _token_stride(x.shape, x.stride(), name)
+    strides = x.stride()
+    if strides == params._dense[which]:
+        return x.data_ptr(), params._step[which]
+    return x.data_ptr(), _token_stride(like[0], strides, name)
 
 
-def _qk_new(params, which, given, x):
-    if params._like[which] is None:
-        return None
+def _qk_out(params, which, given, name):
+    """An output and its (address, stride): the given one, or a new one."""
+    if given is not None or params._like[which] is None:
+        return given, _qk_rows(params, which, given, name)
     shape, dtype = params._like[which]
-    return given if given is not None else torch.empty(shape, dtype=dtype, device=params.device)
+    x = torch.empty(shape, dtype=dtype, device=params.device)
+    return x, (x.data_ptr(), params._step[which])
 
 
 def _qk_forward(params, q, k, q_out, k_out, s):
-    outs = _qk_new(params, 0, q_out, q), _qk_new(params, 1, k_out, k)
-    if params.B and params.L:
-        _check(lib().ra_qk_fwd(params._ref, *_qk_rows(params, 0, q, "q"), *_qk_rows(params, 1, k, "k"),
-                               *_qk_rows(params, 0, outs[0], "q_out"), *_qk_rows(params, 1, outs[1], "k_out"), s))
-    return outs
+    a, b = _qk_rows(params, 0, q, "q"), _qk_rows(params, 1, k, "k")
+    q_out, c = _qk_out(params, 0, q_out, "q_out")
+    k_out, d = _qk_out(params, 1, k_out, "k_out")
+    if params._any:
+        rc = lib().ra_qk_fwd(params._ref, *a, *b, *c, *d, s)
+        if rc:
+            _check(rc)
+    return q_out, k_out
 
 
 def _qk_run(params, stream, run, *args):
@@ -841,23 +852,26 @@ def qk_forward(params, q, k=None, q_out=None, k_out=None, stream=None):
 
 
 def _qk_backward(params, q, k, dq_out, dk_out, dq, dk, s):
-    grads = _qk_new(params, 0, dq, q), _qk_new(params, 1, dk, k)
-    norm = params.eps > 0
-    ws, n, dw = None, params._ws, [None, None]
-    for i in range(2):
-        if norm and params._like[i] is not None:
-            dw[i] = torch.empty(params.D, dtype=torch.float32, device=params.device)
-    if not (params.B and params.L):
-        return (*grads, *(None if w is None else w.zero_() for w in dw))
-    if n:
-        ws = torch.UntypedStorage(n, device=params.device)
-    xs = ((q, "q"), (k, "k")) if norm else ((None, ""), (None, ""))
-    rows = [_qk_rows(params, i, x, name) if norm else (None, 0) for i, (x, name) in enumerate(xs)]
-    _check(lib().ra_qk_bwd(params._ref, *rows[0], *rows[1], *_qk_rows(params, 0, dq_out, "dq_out"),
-                           *_qk_rows(params, 1, dk_out, "dk_out"), *_qk_rows(params, 0, grads[0], "dq"),
-                           *_qk_rows(params, 1, grads[1], "dk"), _ptr(dw[0]), _ptr(dw[1]),
-                           None if ws is None else ws.data_ptr(), n, s))
-    return (*grads, *dw)
+    norm, dw = params.eps > 0, [None, None]
+    a, b = (_qk_rows(params, 0, q, "q"), _qk_rows(params, 1, k, "k")) if norm else ((None, 0), (None, 0))
+    c, d = _qk_rows(params, 0, dq_out, "dq_out"), _qk_rows(params, 1, dk_out, "dk_out")
+    dq, e = _qk_out(params, 0, dq, "dq")
+    dk, f = _qk_out(params, 1, dk, "dk")
+    if norm:
+        dw = [None if like is None else torch.empty(params.D, dtype=torch.float32, device=params.device)
+              for like in params._like]
+    if params._any:
+        n = params._ws
+        ws = torch.UntypedStorage(n, device=params.device) if n else None
+        rc = lib().ra_qk_bwd(params._ref, *a, *b, *c, *d, *e, *f, _ptr(dw[0]), _ptr(dw[1]),
+                             None if ws is None else ws.data_ptr(), n, s)
+        if rc:
+            _check(rc)
+    else:
+        for w in dw:
+            if w is not None:
+                w.zero_()
+    return dq, dk, dw[0], dw[1]
 
 
 def qk_backward(params, q, k, dq_out, dk_out=None, dq=None, dk=None, stream=None):
@@ -867,11 +881,13 @@ def qk_backward(params, q, k, dq_out, dk_out=None, dq=None, dk=None, stream=None
 
 
 def _qk_enter(params, cache, q, k, v, page_table, count, out, s):
-    out = _qk_new(params, 0, out, q)
-    if params.B and params.L:
-        _check(lib().ra_qk_enter(params._ref, cache._ref, *_qk_rows(params, 0, q, "q"), *_qk_rows(params, 1, k, "k"),
-                                 *_qk_rows(params, 1, v, "v"), *_qk_rows(params, 0, out, "out"), page_table.data_ptr(),
-                                 page_table.shape[1], None if count is None else count.data_ptr(), s))
+    a, b, c = _qk_rows(params, 0, q, "q"), _qk_rows(params, 1, k, "k"), _qk_rows(params, 1, v, "v")
+    out, d = _qk_out(params, 0, out, "out")
+    if params._any:
+        rc = lib().ra_qk_enter(params._ref, cache._ref, *a, *b, *c, *d, page_table.data_ptr(), page_table.shape[1],
+                               None if count is None else count.data_ptr(), s)
+        if rc:
+            _check(rc)
     return out
 
 

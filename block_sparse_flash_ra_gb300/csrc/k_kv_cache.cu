@@ -25,6 +25,8 @@ namespace ra {
 namespace {
 
 constexpr int kThreads = 256, kUnroll = 2;
+// rows of a group at once that are read: with 4 bytes of a lane each, more of 4 bits
+constexpr int read_unroll(int cache) { return cache == RA_E2M1 ? 4 : kUnroll; }
 
 // Largest magnitudes, as fp32 bits, of a K row and a V row that LANES lanes hold.
 template <int LANES>
@@ -190,21 +192,21 @@ __global__ void __launch_bounds__(kThreads)
     kv_read_kernel(PagedCache c, T *__restrict__ k, T *__restrict__ v, int B, int L, const int32_t *__restrict__ table,
                    int max_pages, const int32_t *__restrict__ kv_len, int *status)
 {
-    constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
+    constexpr int LANES = D / 8, GROUPS = kThreads / LANES, U = read_unroll(CACHE);
     const int lane = threadIdx.x % LANES;
-    const unsigned r0 = blockIdx.x * (GROUPS * kUnroll) + threadIdx.x / LANES, rows = (unsigned)L * c.Hkv;
+    const unsigned r0 = blockIdx.x * (GROUPS * U) + threadIdx.x / LANES, rows = (unsigned)L * c.Hkv;
     for (int b = blockIdx.y; b < B; b += gridDim.y) {
         const int len = kv_len[b];
-        int page[kUnroll];
+        int page[U];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) { // beside the length, not behind it
+        for (int u = 0; u < U; ++u) { // beside the length, not behind it
             const int n = (int)(((r0 + u * GROUPS) / c.Hkv) >> c.page_shift);
             page[u] = n < max_pages ? table[(size_t)b * max_pages + n] : -1;
         }
         if (blockIdx.x == 0 && threadIdx.x == 0 && (len < 0 || len > L)) report_bad_page(status);
-        Cached kr[kUnroll] = {}, vr[kUnroll] = {};
+        Cached kr[U] = {}, vr[U] = {};
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
+        for (int u = 0; u < U; ++u) {
             const unsigned r = r0 + u * GROUPS, j = r / c.Hkv, h = r - j * c.Hkv;
             if (r < rows && (int)j < len) {
                 if (page[u] >= 0 && page[u] < c.n_pages) {
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(kThreads)
             }
         }
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
+        for (int u = 0; u < U; ++u) {
             const unsigned r = r0 + u * GROUPS;
             if (r < rows) {
                 const size_t at = ((size_t)b * rows + r) * D + lane * 8;
@@ -228,9 +230,9 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-dim3 grid_for(int B, long long rows, int lanes)
+dim3 grid_for(int B, long long rows, int lanes, int unroll)
 {
-    const long long per = kThreads / lanes * kUnroll;
+    const long long per = kThreads / lanes * unroll;
     return dim3((unsigned)((rows + per - 1) / per), (unsigned)(B < 65535 ? B : 65535));
 }
 
@@ -241,7 +243,7 @@ cudaError_t launch_kv_write(const PagedCache &c, int cache_dtype, const void *k,
                             int max_pages, const int32_t *start, const int32_t *count, int *status,
                             cudaStream_t s)
 {
-    const dim3 grid = grid_for(B, (long long)L * c.Hkv, c.D / 8);
+    const dim3 grid = grid_for(B, (long long)L * c.Hkv, c.D / 8, kUnroll);
     auto go = [&](auto kern, auto *kp, auto *vp) {
         kern<<<grid, kThreads, 0, s>>>(c, kp, vp, B, L, k_stride, v_stride, page_table, max_pages, start, count,
                                        status);
@@ -264,7 +266,7 @@ cudaError_t launch_kv_read(const PagedCache &c, int cache_dtype, const int32_t *
                            const int32_t *kv_len, int B, int L, void *k, void *v, int dtype, int *status,
                            cudaStream_t s)
 {
-    const dim3 grid = grid_for(B, (long long)L * c.Hkv, c.D / 8);
+    const dim3 grid = grid_for(B, (long long)L * c.Hkv, c.D / 8, read_unroll(cache_dtype));
     auto go = [&](auto kern, auto *kp, auto *vp) {
         kern<<<grid, kThreads, 0, s>>>(c, kp, vp, B, L, page_table, max_pages, kv_len, status);
         return cudaGetLastError();

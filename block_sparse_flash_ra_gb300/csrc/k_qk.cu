@@ -201,13 +201,13 @@ __device__ __forceinline__ void put_rows(const float *x, const Place &at, bool p
     }
 }
 
-// Units of one kind: rows [0, heads) in steps of a unit's.
-template <int LANES>
-constexpr int kUnitRows = 32 / LANES * kUnroll;
-template <int LANES>
+// Units of one kind: rows [0, heads) in steps of a unit's, U per lane group.
+template <int LANES, int U = kUnroll>
+constexpr int kUnitRows = 32 / LANES * U;
+template <int LANES, int U = kUnroll>
 __host__ __device__ __forceinline__ int units_of(int heads)
 {
-    return (heads + kUnitRows<LANES> - 1) / kUnitRows<LANES>;
+    return (heads + kUnitRows<LANES, U> - 1) / kUnitRows<LANES, U>;
 }
 
 // What the forward does with its rows: they go out, or into a cache.
@@ -215,7 +215,7 @@ struct NoCache {
 };
 
 template <int D, bool HALF, bool NORM, typename T, class TO>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && !(NORM && std::is_same<TO, QkEnter>::value) ? 4 : 3)
     qk_forward_kernel(QkProblem p, QkRows q, QkRows k, QkRows v, QkRows q_out, QkRows k_out, TO to, int step)
 {
     constexpr bool ENTER = std::is_same<TO, QkEnter>::value;
@@ -299,82 +299,86 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
 
 // The backward of a norm and its rotation: a fixed number of CTAs, which take
 // every gridDim.x-th step of tokens, so that each leaves one partial sum of the
-// weights' gradients; they are joined in order.
+// weights' gradients; they are joined in order.  A lane adds up its 16 columns in
+// registers for the queries of a step, then for the keys, and puts what it has
+// into a place of its own in shared memory in between (both sums in registers
+// would spill).
 template <int D, bool HALF, typename T>
 __global__ void __launch_bounds__(kThreads, 2)
     qk_backward_kernel(QkProblem p, QkRows q, QkRows k, QkRows dq_out, QkRows dk_out, QkRows dq, QkRows dk, float *part,
                        int step)
 {
-    constexpr int LANES = D / 16, GROUPS = 32 / LANES;
+    constexpr int LANES = D / 16, GROUPS = 32 / LANES, U = sizeof(T) == 2 ? 2 : 1;
     __shared__ Turns turns;
-    __shared__ float sums[kWarps][2][D];
+    __shared__ __align__(16) float sums[2][4][kThreads][4]; // [kind][of 16 columns][thread]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LANES, group = lane / LANES;
     const Place at = place_of<HALF>(l, p.rot);
     const long long tokens = (long long)p.B * p.L;
-    const int uq = units_of<LANES>(p.Hq), units = uq + units_of<LANES>(p.Hkv);
-    float acc[2][16] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<float4 *>(sums[i >> 2][i & 3][threadIdx.x]) = make_float4(0.f, 0.f, 0.f, 0.f);
     for (long long first = (long long)blockIdx.x * step; first < tokens; first += (long long)gridDim.x * step) {
         const int n = (int)min((long long)step, tokens - first);
         fill_turns(turns, p, first, n);
         __syncthreads();
 #pragma unroll 1
-        for (int u = warp; u < n * units; u += kWarps) {
-            const int t = u / units, in = u - t * units, kind = in < uq ? 0 : 1;
-            const int heads = kind ? p.Hkv : p.Hq, h0 = (kind ? in - uq : in) * kUnitRows<LANES> + group;
+        for (int kind = 0; kind < 2; ++kind) {
+            const int heads = kind ? p.Hkv : p.Hq, units = units_of<LANES, U>(heads);
             const QkRows &xs = kind ? k : q, &gs = kind ? dk_out : dq_out, &ds = kind ? dk : dq;
-            const T *xp = static_cast<const T *>(xs.p) + (size_t)(first + t) * xs.stride;
-            const T *gp = static_cast<const T *>(gs.p) + (size_t)(first + t) * gs.stride;
-            Raw16<T> xr[kUnroll] = {}, gr[kUnroll] = {};
-#pragma unroll
-            for (int y = 0; y < kUnroll; ++y)
-                if (h0 + y * GROUPS < heads) {
-                    xr[y] = load16(xp + (size_t)(h0 + y * GROUPS) * D, at);
-                    gr[y] = load16(gp + (size_t)(h0 + y * GROUPS) * D, at);
-                }
-            float w[16];
+            float w[16], acc[16] = {};
             load_weights(w, kind ? p.k_weight : p.q_weight, p.weight_dtype, at);
+#pragma unroll 1
+            for (int u = warp; u < n * units; u += kWarps) {
+                const int t = u / units, h0 = (u - t * units) * kUnitRows<LANES, U> + group;
+                const T *xp = static_cast<const T *>(xs.p) + (size_t)(first + t) * xs.stride;
+                const T *gp = static_cast<const T *>(gs.p) + (size_t)(first + t) * gs.stride;
+                Raw16<T> xr[U] = {}, gr[U] = {};
 #pragma unroll
-            for (int y = 0; y < kUnroll; ++y) {
-                const int h = h0 + y * GROUPS;
-                float z[16], g[16], sum = 0.f, dot = 0.f;
-                widen16(xr[y], z);
-                widen16(gr[y], g);
-                if (at.turned) turn16<HALF>(g, turns.t[t], l, true);
+                for (int y = 0; y < U; ++y)
+                    if (h0 + y * GROUPS < heads) {
+                        xr[y] = load16(xp + (size_t)(h0 + y * GROUPS) * D, at);
+                        gr[y] = load16(gp + (size_t)(h0 + y * GROUPS) * D, at);
+                    }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sum = fmaf(z[i], z[i], sum);
-                const float r = rsqrtf(fmaf(row_sum<LANES>(sum), 1.f / D, p.eps));
+                for (int y = 0; y < U; ++y) {
+                    const int h = h0 + y * GROUPS;
+                    float z[16], g[16], sum = 0.f, dot = 0.f;
+                    widen16(xr[y], z);
+                    widen16(gr[y], g);
+                    if (at.turned) turn16<HALF>(g, turns.t[t], l, true);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    z[i] *= r;
-                    if (kind) acc[1][i] = fmaf(g[i], z[i], acc[1][i]);
-                    else acc[0][i] = fmaf(g[i], z[i], acc[0][i]);
-                    g[i] *= w[i];
-                    dot = fmaf(g[i], z[i], dot);
+                    for (int i = 0; i < 16; ++i) sum = fmaf(z[i], z[i], sum);
+                    const float r = rsqrtf(fmaf(row_sum<LANES>(sum), 1.f / D, p.eps));
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        z[i] *= r;
+                        acc[i] = fmaf(g[i], z[i], acc[i]);
+                        g[i] *= w[i];
+                        dot = fmaf(g[i], z[i], dot);
+                    }
+                    dot = row_sum<LANES>(dot) * (1.f / D);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) z[i] = r * (g[i] - z[i] * dot);
+                    if (h < heads)
+                        store16(static_cast<T *>(const_cast<void *>(ds.p)) + (size_t)(first + t) * ds.stride + (size_t)h * D, at, z);
                 }
-                dot = row_sum<LANES>(dot) * (1.f / D);
+            }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) z[i] = r * (g[i] - z[i] * dot);
-                if (h < heads)
-                    store16(static_cast<T *>(const_cast<void *>(ds.p)) + (size_t)(first + t) * ds.stride + (size_t)h * D, at, z);
+            for (int i = 0; i < 4; ++i) {
+                float4 *s = reinterpret_cast<float4 *>(sums[kind][i][threadIdx.x]);
+                const float4 o = *s;
+                *s = make_float4(o.x + acc[4 * i], o.y + acc[4 * i + 1], o.z + acc[4 * i + 2], o.w + acc[4 * i + 3]);
             }
         }
         __syncthreads(); // the table is free again
     }
-    // ---- this CTA's sums: lane groups, then warps
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float x = acc[s][i];
-#pragma unroll
-            for (int o = LANES; o < 32; o <<= 1) x += __shfl_xor_sync(kAll, x, o);
-            if (group == 0) sums[warp][s][(i < 8 ? at.c0 * 8 : at.c1 * 8 - 8) + i] = x;
-        }
-    __syncthreads();
+    // ---- this CTA's sums: all threads that have a column
     for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+        const int kind = i / D, col = i % D, eight = col / 8;
+        // the lane that has it, and where among its 16
+        int lane_of = eight / 2, in = (eight & 1) * 8 + col % 8;
+        if (HALF && eight * 8 < p.rot) lane_of = eight % (p.rot / 16), in = (eight >= p.rot / 16 ? 8 : 0) + col % 8;
         float x = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) x += (&sums[w][0][0])[i];
+        for (int th = lane_of; th < kThreads; th += LANES) x += sums[kind][in >> 2][th][in & 3];
         part[(size_t)blockIdx.x * 2 * D + i] = x;
     }
 }
