@@ -45,6 +45,6 @@ cudaError_t launch_qk_enter(const QkProblem &p, int dtype, bool norm, QkRows q, 
                             const QkEnter &to, cudaStream_t s);
 // with norms: part (kQkBwdCtas, 2, D) partial sums of the weights' gradients
 cudaError_t launch_qk_bwd(const QkProblem &p, int dtype, QkRows q, QkRows k, QkRows dq_out, QkRows dk_out, QkRows dq,
-                          QkRows dk, float *dq_weight, float *dk_weight, float *part, cudaStream_t s);
+                          QkRows dk, float *dq_weight, float *dk_weight, float *part, int device, cudaStream_t s);
 
 } // namespace ra

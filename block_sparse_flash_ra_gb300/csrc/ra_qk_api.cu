@@ -171,7 +171,7 @@ RA_API int ra_qk_bwd(const ra_qk_params *p, const void *q, size_t q_stride, cons
     x.inverse = 1;
     const cudaError_t e =
         norm ? launch_qk_bwd(x, p->dtype, rows_of(in[2]), rows_of(in[3]), rows_of(in[0]), rows_of(in[1]), rows_of(out[0]),
-                             rows_of(out[1]), dq_weight, dk_weight, static_cast<float *>(ws), s)
+                             rows_of(out[1]), dq_weight, dk_weight, static_cast<float *>(ws), d.index, s)
              : launch_qk_fwd(x, p->dtype, false, rows_of(in[0]), rows_of(in[1]), rows_of(out[0]), rows_of(out[1]), s);
     if (e != cudaSuccess) return set_cuda_error(e, "qk backward launch");
     count_launches(norm ? 2 : 1);
