@@ -25,8 +25,7 @@ namespace ra {
 namespace {
 
 constexpr int kThreads = 256, kUnroll = 2;
-// rows of a group at once that are read: with 4 bytes of a lane each, more of 4 bits
-constexpr int read_unroll(int cache) { return cache == RA_E2M1 ? 4 : kUnroll; }
+
 
 // Largest magnitudes, as fp32 bits, of a K row and a V row that LANES lanes hold.
 template <int LANES>
@@ -60,17 +59,29 @@ __device__ __forceinline__ uint2 row_tops(const Raw<float> &k, const Raw<float> 
     return t;
 }
 
-// Stores a lane's eight values of a row; as codes at the scale that the largest
-// magnitude of the row (8 bits) or of the lane's block of 32 (4 bits) asks for.
+// The scale byte of a row (8 bits) or of the lane's block of 32 (4 bits), by its
+// largest magnitude; row_e: the bytes of the row's blocks.
 template <int LANES, int CACHE>
-__device__ __forceinline__ void put_row(const Eight &r, uint32_t top, const void *base, const uint8_t *exps, size_t row, int lane)
+__device__ __forceinline__ uint32_t scale_of(uint32_t top, int lane, uint32_t &row_e)
+{
+    if (CACHE != RA_E2M1) return row_exp(top);
+    const uint32_t e = block_exp(top);
+    row_e = e << (lane / 4 * 8);
+#pragma unroll
+    for (int o = 4; o < LANES; o <<= 1) row_e |= __shfl_xor_sync(0xffffffffu, row_e, o);
+    return e;
+}
+
+// Stores a lane's eight values of a row; as codes at the scale e.
+template <int LANES, int CACHE>
+__device__ __forceinline__ void put_row(const Eight &r, uint32_t e, uint32_t row_e, const void *base, const uint8_t *exps, size_t row,
+                                        int lane)
 {
     uint8_t *bytes = static_cast<uint8_t *>(const_cast<void *>(base)), *e8 = const_cast<uint8_t *>(exps);
     if (CACHE == RA_BF16) {
         store8(static_cast<__nv_bfloat16 *>(const_cast<void *>(base)) + row * (LANES * 8) + lane * 8, r);
         return;
     }
-    const uint32_t e = CACHE == RA_E4M3 ? row_exp(top) : block_exp(top);
     const float inv = exp_byte_inverse(e);
     float x[8];
 #pragma unroll
@@ -82,7 +93,10 @@ __device__ __forceinline__ void put_row(const Eight &r, uint32_t top, const void
         if (lane == 0) e8[row] = (uint8_t)e;
     } else {
         reinterpret_cast<uint32_t *>(bytes + row * (LANES * 4))[lane] = e != 255u ? e2m1x8(x) : 0u;
-        if (lane % 4 == 0) e8[row * (LANES / 4) + lane / 4] = (uint8_t)e;
+        if (lane == 0) {
+            if (LANES == 16) reinterpret_cast<uint32_t *>(e8)[row] = row_e;
+            else reinterpret_cast<uint16_t *>(e8)[row] = (uint16_t)row_e;
+        }
     }
 }
 
@@ -137,54 +151,61 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const uint2 top = CACHE == RA_BF16 ? make_uint2(0, 0) : row_tops<CACHE == RA_E4M3 ? LANES : 4>(kr[u], vr[u]);
+            uint32_t kx = 0, vx = 0;
+            const uint32_t ke = scale_of<LANES, CACHE>(top.x, lane, kx), ve = scale_of<LANES, CACHE>(top.y, lane, vx);
             if (!put[u]) continue;
-            put_row<LANES, CACHE>(widen(kr[u]), top.x, c.k, c.k_exp, row[u], lane);
-            put_row<LANES, CACHE>(widen(vr[u]), top.y, c.v, c.v_exp, row[u], lane);
+            put_row<LANES, CACHE>(widen(kr[u]), ke, kx, c.k, c.k_exp, row[u], lane);
+            put_row<LANES, CACHE>(widen(vr[u]), ve, vx, c.v, c.v_exp, row[u], lane);
         }
     }
 }
 
-// Eight values of a cached row as the cache has them, and their scale byte.
+// A lane's values of a cached row as the cache has them -- 8, of 4 bits 16 -- and
+// their scale byte.
 struct Cached {
-    uint4 w; // e4m3: .x and .y, e2m1: .x
+    uint4 w; // codes: .x and .y
     uint32_t e;
 };
+constexpr int read_values(int cache) { return cache == RA_E2M1 ? 16 : 8; }
 
 template <int D, int CACHE>
 __device__ __forceinline__ Cached get_row(const void *base, const uint8_t *exps, size_t row, int lane)
 {
     Cached r{};
     const uint8_t *bytes = static_cast<const uint8_t *>(base);
-    if (CACHE == RA_E4M3) {
-        const uint2 w = reinterpret_cast<const uint2 *>(bytes + row * D)[lane];
+    if (CACHE == RA_BF16) {
+        r.w = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + row * D)[lane];
+    } else {
+        const uint2 w = reinterpret_cast<const uint2 *>(bytes + row * (CACHE == RA_E4M3 ? D : D / 2))[lane];
         r.w.x = w.x;
         r.w.y = w.y;
-        r.e = exps[row];
-    } else if (CACHE == RA_E2M1) {
-        r.w.x = reinterpret_cast<const uint32_t *>(bytes + row * (D / 2))[lane];
-        r.e = exps[row * (D / 32) + lane / 4];
-    } else {
-        r.w = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + row * D)[lane];
+        r.e = CACHE == RA_E4M3 ? exps[row] : exps[row * (D / 32) + lane / 2];
     }
     return r;
 }
 
-template <int CACHE>
-__device__ __forceinline__ Eight widen(const Cached &c)
+template <int CACHE, typename T>
+__device__ __forceinline__ void put_values(T *to, const Cached &c)
 {
-    if (CACHE == RA_BF16) return widen(Raw<__nv_bfloat16>{{c.w}});
-    const float s = exp_byte_scale(c.e);
-    uint32_t h[4] = {c.w.x & 0xffffu, c.w.x >> 16, c.w.y & 0xffffu, c.w.y >> 16};
-    if (CACHE == RA_E2M1) e2m1x8_to_f16(c.w.x, h);
-    Eight r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t x = CACHE == RA_E4M3 ? e4m3x2_to_f16x2(h[i]) : h[i];
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
-        r.x[2 * i] = f.x * s;
-        r.x[2 * i + 1] = f.y * s;
+    if (CACHE == RA_BF16) {
+        store8(to, widen(Raw<__nv_bfloat16>{{c.w}}));
+        return;
     }
-    return r;
+    const float s = exp_byte_scale(c.e);
+#pragma unroll
+    for (int y = 0; y < read_values(CACHE) / 8; ++y) {
+        uint32_t h[4] = {c.w.x & 0xffffu, c.w.x >> 16, c.w.y & 0xffffu, c.w.y >> 16};
+        if (CACHE == RA_E2M1) e2m1x8_to_f16(y ? c.w.y : c.w.x, h);
+        Eight r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t x = CACHE == RA_E4M3 ? e4m3x2_to_f16x2(h[i]) : h[i];
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+            r.x[2 * i] = f.x * s;
+            r.x[2 * i + 1] = f.y * s;
+        }
+        store8(to + 8 * y, r);
+    }
 }
 
 template <int D, int CACHE, typename T>
@@ -192,21 +213,21 @@ __global__ void __launch_bounds__(kThreads)
     kv_read_kernel(PagedCache c, T *__restrict__ k, T *__restrict__ v, int B, int L, const int32_t *__restrict__ table,
                    int max_pages, const int32_t *__restrict__ kv_len, int *status)
 {
-    constexpr int LANES = D / 8, GROUPS = kThreads / LANES, U = read_unroll(CACHE);
+    constexpr int VALUES = read_values(CACHE), LANES = D / VALUES, GROUPS = kThreads / LANES;
     const int lane = threadIdx.x % LANES;
-    const unsigned r0 = blockIdx.x * (GROUPS * U) + threadIdx.x / LANES, rows = (unsigned)L * c.Hkv;
+    const unsigned r0 = blockIdx.x * (GROUPS * kUnroll) + threadIdx.x / LANES, rows = (unsigned)L * c.Hkv;
     for (int b = blockIdx.y; b < B; b += gridDim.y) {
         const int len = kv_len[b];
-        int page[U];
+        int page[kUnroll];
 #pragma unroll
-        for (int u = 0; u < U; ++u) { // beside the length, not behind it
+        for (int u = 0; u < kUnroll; ++u) { // beside the length, not behind it
             const int n = (int)(((r0 + u * GROUPS) / c.Hkv) >> c.page_shift);
             page[u] = n < max_pages ? table[(size_t)b * max_pages + n] : -1;
         }
         if (blockIdx.x == 0 && threadIdx.x == 0 && (len < 0 || len > L)) report_bad_page(status);
-        Cached kr[U] = {}, vr[U] = {};
+        Cached kr[kUnroll] = {}, vr[kUnroll] = {};
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < kUnroll; ++u) {
             const unsigned r = r0 + u * GROUPS, j = r / c.Hkv, h = r - j * c.Hkv;
             if (r < rows && (int)j < len) {
                 if (page[u] >= 0 && page[u] < c.n_pages) {
@@ -219,20 +240,20 @@ __global__ void __launch_bounds__(kThreads)
             }
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < kUnroll; ++u) {
             const unsigned r = r0 + u * GROUPS;
             if (r < rows) {
-                const size_t at = ((size_t)b * rows + r) * D + lane * 8;
-                store8(k + at, widen<CACHE>(kr[u]));
-                store8(v + at, widen<CACHE>(vr[u]));
+                const size_t at = ((size_t)b * rows + r) * D + lane * VALUES;
+                put_values<CACHE>(k + at, kr[u]);
+                put_values<CACHE>(v + at, vr[u]);
             }
         }
     }
 }
 
-dim3 grid_for(int B, long long rows, int lanes, int unroll)
+dim3 grid_for(int B, long long rows, int lanes)
 {
-    const long long per = kThreads / lanes * unroll;
+    const long long per = kThreads / lanes * kUnroll;
     return dim3((unsigned)((rows + per - 1) / per), (unsigned)(B < 65535 ? B : 65535));
 }
 
@@ -243,7 +264,7 @@ cudaError_t launch_kv_write(const PagedCache &c, int cache_dtype, const void *k,
                             int max_pages, const int32_t *start, const int32_t *count, int *status,
                             cudaStream_t s)
 {
-    const dim3 grid = grid_for(B, (long long)L * c.Hkv, c.D / 8, kUnroll);
+    const dim3 grid = grid_for(B, (long long)L * c.Hkv, c.D / 8);
     auto go = [&](auto kern, auto *kp, auto *vp) {
         kern<<<grid, kThreads, 0, s>>>(c, kp, vp, B, L, k_stride, v_stride, page_table, max_pages, start, count,
                                        status);
@@ -266,7 +287,7 @@ cudaError_t launch_kv_read(const PagedCache &c, int cache_dtype, const int32_t *
                            const int32_t *kv_len, int B, int L, void *k, void *v, int dtype, int *status,
                            cudaStream_t s)
 {
-    const dim3 grid = grid_for(B, (long long)L * c.Hkv, c.D / 8, read_unroll(cache_dtype));
+    const dim3 grid = grid_for(B, (long long)L * c.Hkv, c.D / read_values(cache_dtype));
     auto go = [&](auto kern, auto *kp, auto *vp) {
         kern<<<grid, kThreads, 0, s>>>(c, kp, vp, B, L, page_table, max_pages, kv_len, status);
         return cudaGetLastError();

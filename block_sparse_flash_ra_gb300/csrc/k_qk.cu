@@ -328,6 +328,16 @@ __global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 ? 4 : 3))
         }
         copies_end();
     };
+    if constexpr (ENTER) {
+        if (to.count) { // nothing to do for tokens that are all left out
+            const long long b = first / p.L, i = first - b * p.L;
+            const int count = to.count[b];
+            if (i + n <= p.L && i >= count) {
+                if (i == 0 && threadIdx.x == 0 && count < 0) report_bad_page(to.status);
+                return;
+            }
+        }
+    }
     // the first units' rows come while the angles and places are found
 #pragma unroll
     for (int i = 0; i < kStages; ++i) fetch(warp + i * kWarps, i);
