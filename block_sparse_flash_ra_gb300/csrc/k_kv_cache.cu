@@ -160,13 +160,11 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-// A lane's values of a cached row as the cache has them -- 8, of 4 bits 16 -- and
-// their scale byte.
+// Eight values of a cached row as the cache has them, and their scale byte.
 struct Cached {
-    uint4 w; // codes: .x and .y
+    uint4 w; // e4m3: .x and .y, e2m1: .x
     uint32_t e;
 };
-constexpr int read_values(int cache) { return cache == RA_E2M1 ? 16 : 8; }
 
 template <int D, int CACHE>
 __device__ __forceinline__ Cached get_row(const void *base, const uint8_t *exps, size_t row, int lane)
@@ -175,11 +173,14 @@ __device__ __forceinline__ Cached get_row(const void *base, const uint8_t *exps,
     const uint8_t *bytes = static_cast<const uint8_t *>(base);
     if (CACHE == RA_BF16) {
         r.w = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + row * D)[lane];
-    } else {
-        const uint2 w = reinterpret_cast<const uint2 *>(bytes + row * (CACHE == RA_E4M3 ? D : D / 2))[lane];
+    } else if (CACHE == RA_E4M3) {
+        const uint2 w = reinterpret_cast<const uint2 *>(bytes + row * D)[lane];
         r.w.x = w.x;
         r.w.y = w.y;
-        r.e = CACHE == RA_E4M3 ? exps[row] : exps[row * (D / 32) + lane / 2];
+        r.e = exps[row];
+    } else {
+        r.w.x = reinterpret_cast<const uint32_t *>(bytes + row * (D / 2))[lane];
+        r.e = exps[row * (D / 32) + lane / 4];
     }
     return r;
 }
@@ -192,20 +193,17 @@ __device__ __forceinline__ void put_values(T *to, const Cached &c)
         return;
     }
     const float s = exp_byte_scale(c.e);
+    uint32_t h[4] = {c.w.x & 0xffffu, c.w.x >> 16, c.w.y & 0xffffu, c.w.y >> 16};
+    if (CACHE == RA_E2M1) e2m1x8_to_f16(c.w.x, h);
+    Eight r;
 #pragma unroll
-    for (int y = 0; y < read_values(CACHE) / 8; ++y) {
-        uint32_t h[4] = {c.w.x & 0xffffu, c.w.x >> 16, c.w.y & 0xffffu, c.w.y >> 16};
-        if (CACHE == RA_E2M1) e2m1x8_to_f16(y ? c.w.y : c.w.x, h);
-        Eight r;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t x = CACHE == RA_E4M3 ? e4m3x2_to_f16x2(h[i]) : h[i];
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
-            r.x[2 * i] = f.x * s;
-            r.x[2 * i + 1] = f.y * s;
-        }
-        store8(to + 8 * y, r);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = CACHE == RA_E4M3 ? e4m3x2_to_f16x2(h[i]) : h[i];
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+        r.x[2 * i] = f.x * s;
+        r.x[2 * i + 1] = f.y * s;
     }
+    store8(to, r);
 }
 
 template <int D, int CACHE, typename T>
@@ -213,7 +211,7 @@ __global__ void __launch_bounds__(kThreads)
     kv_read_kernel(PagedCache c, T *__restrict__ k, T *__restrict__ v, int B, int L, const int32_t *__restrict__ table,
                    int max_pages, const int32_t *__restrict__ kv_len, int *status)
 {
-    constexpr int VALUES = read_values(CACHE), LANES = D / VALUES, GROUPS = kThreads / LANES;
+    constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
     const int lane = threadIdx.x % LANES;
     const unsigned r0 = blockIdx.x * (GROUPS * kUnroll) + threadIdx.x / LANES, rows = (unsigned)L * c.Hkv;
     for (int b = blockIdx.y; b < B; b += gridDim.y) {
@@ -243,7 +241,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int u = 0; u < kUnroll; ++u) {
             const unsigned r = r0 + u * GROUPS;
             if (r < rows) {
-                const size_t at = ((size_t)b * rows + r) * D + lane * VALUES;
+                const size_t at = ((size_t)b * rows + r) * D + lane * 8;
                 put_values<CACHE>(k + at, kr[u]);
                 put_values<CACHE>(v + at, vr[u]);
             }
@@ -287,7 +285,7 @@ cudaError_t launch_kv_read(const PagedCache &c, int cache_dtype, const int32_t *
                            const int32_t *kv_len, int B, int L, void *k, void *v, int dtype, int *status,
                            cudaStream_t s)
 {
-    const dim3 grid = grid_for(B, (long long)L * c.Hkv, c.D / read_values(cache_dtype));
+    const dim3 grid = grid_for(B, (long long)L * c.Hkv, c.D / 8);
     auto go = [&](auto kern, auto *kp, auto *vp) {
         kern<<<grid, kThreads, 0, s>>>(c, kp, vp, B, L, page_table, max_pages, kv_len, status);
         return cudaGetLastError();
