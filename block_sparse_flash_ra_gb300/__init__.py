@@ -795,9 +795,8 @@ def make_qk_params(q, k=None, *, rope=None, pos=None, start=None, prefix_len=Non
     p._keep = (rope, pos, start, prefix_len, q_weight, k_weight)
     p._like = tuple(None if t is None else (t.shape, t.dtype) for t in (q, k))
     p.device, p._index, p._any = x.device, index, bool(B and L)
-    # dense tensors' strides, and elements between their tokens
-    p._step = [0 if t is None else t.shape[2] * D for t in (q, k)]
-    p._dense = [None if t is None else (L * n, n, D, 1) for t, n in zip((q, k), p._step)]
+    # strides and the elements between two tokens: of dense tensors, and of the last others
+    p._steps = [None if t is None else [((L * n, n, D, 1), n)] for t, n in ((t, t is not None and t.shape[2] * D) for t in (q, k))]
     p._ws = ra_qk_bwd_workspace_size(p) if p._any else 0
     p._ref = ctypes.addressof(p)
     return p
@@ -809,14 +808,17 @@ def _qk_rows(params, which, x, name):
     if like is None:
         _need(x is None, f"{name}: the params were made without it")
         return None, 0
-    if x is None or (x.shape, x.dtype) != like:
+    if x is None or x.shape != like[0] or x.dtype is not like[1]:
         raise ValueError(f"{name} must have the shape and dtype the params were made for")
     if x.get_device() != params._index:
         raise ValueError(f"{name} must be on the params' device")
     strides = x.stride()
-    if strides == params._dense[which]:
-        return x.data_ptr(), params._step[which]
-    return x.data_ptr(), _token_stride(like[0], strides, name)
+    for known, step in params._steps[which]:
+        if strides == known:
+            return x.data_ptr(), step
+    step = _token_stride(like[0], strides, name)
+    params._steps[which] = params._steps[which][:1] + [(strides, step)]
+    return x.data_ptr(), step
 
 
 def _qk_out(params, which, given, name):
@@ -825,7 +827,7 @@ def _qk_out(params, which, given, name):
         return given, _qk_rows(params, which, given, name)
     shape, dtype = params._like[which]
     x = torch.empty(shape, dtype=dtype, device=params.device)
-    return x, (x.data_ptr(), params._step[which])
+    return x, (x.data_ptr(), params._steps[which][0][1])
 
 
 def _qk_forward(params, q, k, q_out, k_out, s):
