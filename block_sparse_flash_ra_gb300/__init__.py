@@ -497,7 +497,7 @@ def _on(device, stream, run, *args):
     with torch.cuda.device(device):
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
-        _need(stream is None or stream.device == device, "the stream is on another device than the cache")
+        _need(stream is None or stream.device == device, "the stream is on another device than the cache or the tensors")
         with torch.cuda.stream(stream):
             return run(*args, torch.cuda.current_stream().cuda_stream)
 

@@ -16,7 +16,8 @@
 // their way.  8 prompts of up to 4096 tokens, 8 kv heads of 128, bf16 to e4m3:
 // 29.4 us, 5.1 TB/s, 76% of a copy's rate (two rows at a time in flight, the
 // maxima on packed 16-bit pairs; one row at a time took 53).  Read back, 2 x
-// 16384 tokens of 16 heads: 69.7 us, 84%.
+// 16384 tokens of 16 heads: 69.7 us, 84%.  4 bits, 24576 tokens of 8 heads, bf16:
+// written in 31 us (63%; 72% of the issue slots), 38000 places read back in 36 (77%).
 #include <type_traits>
 
 #include "ra_rows.cuh"

@@ -36,6 +36,22 @@
 // 16-bit caches run kind::f16 in bf16, q as it is, p = x1 + x2 (2^-16).
 // Logits, maxima, sums and O are fp32.
 //
+// 4-bit caches: K's codes go to the product as they are, too.  TMA leaves 16 codes
+// in the lower half of every 16 bytes (16U4_ALIGN16B), which is how the products
+// read e2m1, and kind::mxf8f6f4 takes the power of two of every 32 of them: 4 bytes
+// of a key, put into TMEM by the warps that widen V, so that S comes out as it
+// should.  V's powers of two are per token, which in P V is the summed axis, and
+// per block of 32 values, which is not: no product takes those.  A warpgroup widens
+// V's codes to e4m3 with the row's largest power (ra_wide4.cuh), and the rest is
+// as with 8 bits.  What bounds it is issue (55% of the slots, a little more of the
+// integer pipe): 64 x 17 to 8192 tokens 80 us, 3.6 TB/s, where 8 bits take 89.
+// Widening K the same way took 134 us; one warp that issued a tile's loads as
+// halves of it was slower than the softmax (110); a warp more for the products, or
+// for the loads, 87; eight warps to widen, 87.  Up to 4 rows are a block of their
+// own, so that a thread has 4 rows' softmax (512 x up to 128 tokens 95 -> 76 us).
+// 16 rows: 122 us on 64 x 4096 tokens (8 bits 99; the softmax's 72 registers
+// spill, but one CTA with more takes 125, and four rows to a thread 140).
+//
 // D = 64: two tokens of a page lie in one row of 128 values, so a tile is the
 // same bytes with 256 tokens.  A query row takes two columns, q in one half of
 // the 128 and zeros in the other: S of the even tokens and S of the odd ones.
@@ -53,6 +69,7 @@
 //              rescaled then and only then.
 //   one warp   issues the products, S(i + 1) before P(i) V(i)
 //   one warp   loads: a lane per page, K and V in rings of their own
+//   4 warps    4-bit caches: the keys' scales to TMEM, V's codes widened
 // A tile's softmax is a chain of a few hundred instructions in few warps, so
 // rows are spread over warpgroups (8 each) to keep it short, and up to 16
 // columns of an 8-bit cache run two CTAs per SM, one's chain under the other's

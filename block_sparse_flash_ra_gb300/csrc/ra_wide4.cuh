@@ -6,7 +6,8 @@
 // exact for k up to 14 (half a step of 2^-10, 2^-18 of 6 * 2^6, at the most
 // below), and the row stands at 2^(e - 6).  The eight magnitudes of a k are
 // eight bytes, so that one byte permute with the codes as its selector widens
-// four of them.
+// four of them: nine integer instructions for eight codes with their signs, and
+// with loads, stores and the table's entry some 50 for 32.
 #pragma once
 
 #include "ra_rows.cuh"

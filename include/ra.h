@@ -459,8 +459,8 @@ RA_API int ra_unpermute_tokens(const void *in, void *out, int B, int L, size_t r
  *                       RA_E2M1: 4-bit codes with one for each 32 of its values
  *   k, v                (n_pages, Hkv, page_size, D) bf16 or e4m3, or
  *                       (n_pages, Hkv, page_size, D / 2) bytes of two e2m1 codes,
- *                       the even value's in the low four bits; 16-byte
- *                       aligned: the tokens of one head of a page lie
+ *                       the even value's in the low four bits; 16-byte (e2m1:
+ *                       32-byte) aligned: the tokens of one head of a page lie
  *                       together, so that one load fetches them
  *   k_exp, v_exp        RA_E4M3: (n_pages, Hkv, page_size) uint8, RA_E2M1:
  *                       (n_pages, Hkv, page_size, D / 32); 16-byte aligned;
@@ -590,7 +590,10 @@ RA_API size_t ra_attn_paged_workspace_size(const ra_kv_cache *cache, const ra_pa
  *                   2^-30 of the loudest count as that loud in it)
  *                   more: 2^-26 of the row's largest weight, and 2^-32 of the
  *                   loudest key or value (below 2^-15 of it they lose bits)
- * and q's elements below 2^-12 of their row's largest may lose bits (e4m3).
+ *   e2m1 cache    as e4m3; with up to 32 rows, or D = 64, the blocks of a value
+ *                   row are taken relative to its largest: below 2^-14 of that
+ *                   they are off by up to 2^-17 of the row's largest value
+ * and q's elements below 2^-12 of their row's largest may lose bits (e4m3, e2m1).
  * Serving only: there is no backward pass.
  * The prefix is attended by the rows of the whole batch together, and read
  * once for each block of them: of 256 rows of a kv head (bf16, D = 128; up to

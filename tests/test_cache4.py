@@ -136,5 +136,10 @@ def test_refusals():
             ra.make_kv_cache(k, k.clone(), *exps)
     with pytest.raises(TypeError):
         ra.make_kv_cache(k.view(torch.uint8), k.view(torch.uint8), u8(4, 2, 16, 4), u8(4, 2, 16, 4))
+    big = u8(4 * 2 * 16 * 64 + 32)
+    odd = big[(16 - big.data_ptr()) % 32:][:4 * 2 * 16 * 64].view(4, 2, 16, 64)  # 16 bytes beside a multiple of 32
+    c = ra.make_kv_cache(odd.view(F4), k, u8(4, 2, 16, 4), u8(4, 2, 16, 4))
+    with pytest.raises(ra.RaError, match="32-byte"):
+        ra.ra_kv_read(c, 4096, 1, 4096, 1, 1, 1 << 20, 1 << 21, ra.RA_BF16, stream=0)
     with pytest.raises(ra.RaError):
         ra.ra_kv_read(ra.RaKvCache(4, 16, 2, 128, ra.RA_E2M1, 4096, 8192, None, None), 4096, 1, 4096, 1, 1, 1 << 20, 1 << 21, ra.RA_BF16, stream=0)
