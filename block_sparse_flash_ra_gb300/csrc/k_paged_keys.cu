@@ -142,7 +142,7 @@ struct Cfg {
     static constexpr int kRawOff = kPOff + 2 * kPBytes;
     static constexpr int kXOff = kRawOff + kRaws * kRaw;
     static constexpr int kTableOff = kXOff + kXs * kX;
-    static constexpr int kExpOff = kTableOff + (FP4 ? 256 : 0); // per stage: scale bytes of K (8 bits), of V
+    static constexpr int kExpOff = kTableOff + (FP4 ? kWide4Entries * 8 : 0); // per stage: scale bytes of K (8 bits), of V
     static constexpr int kRowOff = kExpOff + (FP4 ? kEStages * kTokens : FP8 ? kEStages * 2 * kTokens : 0);
     // per row of both segments: place of its output and of its lse (two words each), logit scale, keys it sees;
     // then its factor
@@ -162,6 +162,7 @@ struct Cfg {
     // both operands of O^T are MN-major
     static constexpr uint32_t kIdescO = ((FP8 ? 0u : (1u << 7) | (1u << 10)) | (1u << 4)) | (1u << 15) | (1u << 16) |
                                         ((uint32_t)(kNO >> 3) << 17) | ((uint32_t)(kD >> 4) << 24);
+    static_assert(!FP4 || kThreads >= kWide4Entries, "the table");
     static_assert(kSmem <= (kCtasPerSm == 2 ? 113 : 227) * 1024, "shared memory");
     static_assert(kRedOff % 16 == 0 && kRT % 4 == 0, "words of a warp are read by fours");
     static_assert(kBarOff % 8 == 0 && kRowOff % 8 == 0 && kPOff % 1024 == 0 && kExpOff % 128 == 0, "layout");
@@ -361,7 +362,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
         if (!FP4) prefetch_tmap(&tm_v);
     }
     uint2 *table = reinterpret_cast<uint2 *>(smem + C::kTableOff);
-    if (FP4 && threadIdx.x < kWide4Entries) wide4_fill(table, threadIdx.x);
+    if (FP4 && threadIdx.x < kWide4Entries) wide4_fill(table, threadIdx.x); // (more threads than entries)
     begin_in_order(part);
     report_lengths(p, part);
     PagedCursor c; // found beside the barriers' and TMEM's setting up

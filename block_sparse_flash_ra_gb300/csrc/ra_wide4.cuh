@@ -1,27 +1,28 @@
 // ra_wide4.cuh -- e2m1 codes of a 4-bit cache widened to e4m3.
 //
 // Values are summed over tokens by products that take one power of two for a
-// token, but a block of 32 codes has one of its own.  With the largest of a row's bytes as the row's, e, a
-// code becomes the e4m3 code of code * 2^(6 - k), k = e - byte: at most 384,
-// exact for k up to 14 (half a step of 2^-10, 2^-18 of 6 * 2^6, at the most
-// below), and the row stands at 2^(e - 6).  The eight magnitudes of a k are
-// eight bytes, so that one byte permute with the codes as its selector widens
-// four of them: nine integer instructions for eight codes with their signs, and
-// with loads, stores and the table's entry some 50 for 32.
+// token, but a block of 32 codes has one of its own.  With the largest of a row's
+// bytes as the row's, e, a code becomes the e4m3 code of code * 2^(6 - k),
+// k = e - byte: at most 384, exact for k up to 14 (half a step of 2^-10, 2^-17 of
+// the row's largest value, at the most below), and the row stands at 2^(e - 6).
+// The eight magnitudes of a k are eight bytes, so that one byte permute with the
+// codes as its selector widens four of them: nine integer instructions for eight
+// codes with their signs, and with loads, stores and the table's entry some 50 for
+// 32.
 #pragma once
 
 #include "ra_rows.cuh"
 
 namespace ra {
 
-// Entry k: the magnitudes' codes at 2^(6 - k); kWide4Zero: none is left;
-// kWide4Nan: a block without a value.
-constexpr int kWide4Zero = 20, kWide4Nan = 21, kWide4Entries = 22;
+// Entry k: the magnitudes' codes at 2^(6 - k), zeros from some k on; the last: a
+// block without a value (a row's largest byte is below 255, so no k is that).
+constexpr int kWide4Entries = 256, kWide4Nan = 255;
 constexpr int kWide4Up = 6; // a row's byte is its largest less this, 0 at the least
 
 __device__ __forceinline__ void wide4_fill(uint2 *table, int k)
 {
-    const float s = k >= kWide4Zero ? 0.f : __uint_as_float((uint32_t)(127 + kWide4Up - k) << 23);
+    const float s = k > 100 ? 0.f : __uint_as_float((uint32_t)(127 + kWide4Up - k) << 23);
     table[k] = k == kWide4Nan ? make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu)
                               : make_uint2(e4m3x4(0.f, 0.5f * s, s, 1.5f * s), e4m3x4(2.f * s, 3.f * s, 4.f * s, 6.f * s));
 }
@@ -32,27 +33,18 @@ __device__ __forceinline__ void wide4_fill(uint2 *table, int k)
 template <bool HALF>
 __device__ __forceinline__ uint32_t wide4_rows(uint32_t w, uint32_t *top)
 {
-    uint32_t b[4], in = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = w >> (8 * i) & 0xffu;
-    top[0] = max(max(b[0], b[1]), (uint32_t)kWide4Up);
-    top[1] = max(max(b[2], b[3]), (uint32_t)kWide4Up);
-    if (!HALF) top[0] = top[1] = max(top[0], top[1]);
-    if (max(top[0], top[1]) < 255u) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) in |= min(top[i >> 1] - b[i], (uint32_t)kWide4Zero) << (8 * i);
-        return in;
-    }
-    uint32_t t[4]; // rare
-#pragma unroll
-    for (int i = 0; i < 4; ++i) t[i] = b[i] == 255u ? 0u : b[i];
-    top[0] = max(max(t[0], t[1]), (uint32_t)kWide4Up);
-    top[1] = max(max(t[2], t[3]), (uint32_t)kWide4Up);
-    if (!HALF) top[0] = top[1] = max(top[0], top[1]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        in |= (b[i] == 255u ? (uint32_t)kWide4Nan : min(top[i >> 1] - b[i], (uint32_t)kWide4Zero)) << (8 * i);
-    return in;
+    auto tops = [&](uint32_t x) {
+        const uint32_t lo = max(x & 0xffu, x >> 8 & 0xffu), hi = max(x >> 16 & 0xffu, x >> 24);
+        top[0] = max(HALF ? lo : max(lo, hi), (uint32_t)kWide4Up);
+        top[1] = HALF ? max(hi, (uint32_t)kWide4Up) : top[0];
+    };
+    // (no byte of the difference borrows: a row's byte is none of its blocks' less)
+    auto entries = [&](uint32_t x) { return top[0] * (HALF ? 0x0101u : 0x01010101u) + (HALF ? top[1] * 0x01010000u : 0u) - x; };
+    tops(w);
+    if (max(top[0], top[1]) < 255u) return entries(w);
+    const uint32_t none = __vcmpeq4(w, 0xffffffffu); // rare
+    tops(w & ~none);
+    return entries(w & ~none) | none;
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)
