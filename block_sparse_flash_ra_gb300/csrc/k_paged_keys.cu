@@ -49,8 +49,10 @@
 // halves of it was slower than the softmax (110); a warp more for the products, or
 // for the loads, 87; eight warps to widen, 87.  Up to 4 rows are a block of their
 // own, so that a thread has 4 rows' softmax (512 x up to 128 tokens 95 -> 76 us).
-// 16 rows: 122 us on 64 x 4096 tokens (8 bits 99; the softmax's 72 registers
-// spill, but one CTA with more takes 125, and four rows to a thread 140).
+// 16 rows: 119 us on 64 x 4096 tokens (8 bits 99; the softmax's 72 registers
+// spill, but one CTA with more takes 125, and four rows to a thread 140).  Warps of
+// their own for the keys' scales: 82 us; three CTAs, with one stage of V or K, 97
+// or 90.
 //
 // D = 64: two tokens of a page lie in one row of 128 values, so a tile is the
 // same bytes with 256 tokens.  A query row takes two columns, q in one half of

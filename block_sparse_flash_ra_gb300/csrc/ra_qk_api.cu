@@ -29,6 +29,8 @@ int check_qk(const ra_qk_params *p)
         return refuse(RA_ERR_INVALID_ARG, "weights belong to a norm (eps > 0)");
     if (p->weight_dtype != RA_BF16 && p->weight_dtype != RA_FP32)
         return refuse(RA_ERR_INVALID_ARG, "weight_dtype must be RA_BF16 or RA_FP32");
+    if (!is_aligned(p->pos, 4) || !is_aligned(p->start, 4) || !is_aligned(p->prefix_len, 4))
+        return refuse(RA_ERR_INVALID_ARG, "pos, start and prefix_len must be 4-byte aligned");
     if (!is_aligned(p->q_weight, 16) || !is_aligned(p->k_weight, 16))
         return refuse(RA_ERR_INVALID_ARG, "weights must be 16-byte aligned");
     return RA_OK;

@@ -76,7 +76,8 @@ def inputs(B, L, Hq, Hkv, D, dtype, seed=0, fused=True):
     return x, x.cuda(), w
 
 
-SHAPES = [(1, 1, 1, 1, 64), (3, 37, 6, 3, 128), (2, 130, 4, 2, 64), (64, 1, 32, 8, 128), (1, 1000, 16, 16, 128), (5, 3, 33, 1, 64)]
+SHAPES = [(1, 1, 1, 1, 64), (3, 37, 6, 3, 128), (2, 130, 4, 2, 64), (64, 1, 32, 8, 128), (1, 1000, 16, 16, 128), (5, 3, 33, 1, 64),
+          (1, 9, 200, 1, 128), (3, 1700, 1, 2, 64)]
 
 
 # ------------------------------------------------------------- forward
@@ -404,6 +405,35 @@ def test_enter(B, L, Hq, Hkv, D, page, rot, interleaved, eps, kind, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("kind", [BF, F8, F4])
+def test_enter_takes_several_tokens_at_a_time(kind):
+    """Enough tokens that a CTA has eight: counts that end inside its eight, at their edge and before any; keys alone."""
+    B, L, Hkv, D, page = 4, 700, 2, 128, 64
+    x, xd, w = inputs(B, L, 3, Hkv, D, BF, seed=77)
+    q, k, v = xd[:, :, :3], xd[:, :, 3:5], xd[:, :, 5:]
+    start = torch.tensor([0, 5, 64, 3], dtype=torch.int32).cuda()
+    count = torch.tensor([L, 0, 333, 8], dtype=torch.int32).cuda()
+    table = torch.randperm(60, generator=torch.Generator().manual_seed(1))[:52].to(torch.int32).view(B, 13).cuda()
+    kw = dict(rope=ra.make_rope(D), eps=1e-6, q_weight=w[0].cuda(), k_weight=w[1].cuda(), start=start)
+    p = ra.make_qk_params(q, k, **kw)
+    want_q, want_k = ra.qk_forward(p, q, k)
+    out = torch.full((B, L, 3, D), 7.0, dtype=BF, device="cuda")
+    caches = [ra.new_kv_cache(60, page, Hkv, D, kind) for _ in range(2)]
+    ra.qk_enter(p, caches[0], q, k, v, table, count=count, out=out)
+    assert ra.qk_enter(ra.make_qk_params(None, k, **{**kw, "q_weight": None}), caches[1], None, k, v, table, count=count) is None
+    for a, b in ((caches[0].k_pages, caches[1].k_pages), (caches[0].v_pages, caches[1].v_pages), (caches[0].k_exps, caches[1].k_exps),
+                 (caches[0].v_exps, caches[1].v_exps)):
+        assert a is None or torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    kk, vv = ra.kv_read(caches[0], table, start + count, 705)
+    for b in range(B):
+        n, s = int(count[b]), int(start[b])
+        assert torch.equal(out[b, :n], want_q[b, :n]) and (out[b, n:] == 7).all()
+        if kind == BF:
+            assert torch.equal(kk[b, s:s + n], want_k[b, :n]) and torch.equal(vv[b, s:s + n], v[b, :n])
+        assert (kk[b, :s] == 0).all() and (kk[b, s + n:] == 0).all()
+
+
+@gpu
 def test_enter_skips_and_reports_tokens_without_a_place():
     x, xd, _ = inputs(2, 4, 2, 2, 64, BF)
     q, k, v = xd[:, :, :2], xd[:, :, 2:4], xd[:, :, 4:]
@@ -433,7 +463,8 @@ def _c_params(**kw):
     (dict(rope=ra.RaRope(64, 0, math.nan, 4096)), ra.RA_ERR_INVALID_ARG), (dict(eps=-1.0), ra.RA_ERR_INVALID_ARG),
     (dict(eps=math.nan), ra.RA_ERR_INVALID_ARG), (dict(eps=0.0, q_weight=4096), ra.RA_ERR_INVALID_ARG),
     (dict(weight_dtype=5), ra.RA_ERR_INVALID_ARG), (dict(q_weight=4100), ra.RA_ERR_INVALID_ARG),
-    (dict(B=1 << 20, L=1 << 12), ra.RA_ERR_UNSUPPORTED),
+    (dict(B=1 << 20, L=1 << 12), ra.RA_ERR_UNSUPPORTED), (dict(pos=4098), ra.RA_ERR_INVALID_ARG),
+    (dict(Hq=1 << 17), ra.RA_ERR_UNSUPPORTED),
 ])
 def test_bad_params_are_refused(bad, code):
     p = _c_params(**bad)
