@@ -9,15 +9,15 @@
 // code * 2^e, exact in bf16 and fp32.
 //
 // Both are copies: bound by memory for prompts and histories, by latency for
-// one token per sequence.  D / 8 lanes take a row, 16 bytes of bf16 each, and
-// a group does the K and V rows of two (token, head) pairs together, so that
-// four loads per lane are in flight before the first is used; the new rows'
-// places come from the index alone, and the table is read while they are on
-// their way.  8 prompts of up to 4096 tokens, 8 kv heads of 128, bf16 to e4m3:
-// 29.4 us, 5.1 TB/s, 76% of a copy's rate (two rows at a time in flight, the
-// maxima on packed 16-bit pairs; one row at a time took 53).  Read back, 2 x
-// 16384 tokens of 16 heads: 69.7 us, 84%.  4 bits, 24576 tokens of 8 heads, bf16:
-// written in 31 us (63%; 72% of the issue slots), 38000 places read back in 36 (77%).
+// one token per sequence.  D / 8 lanes take a row, 16 bytes of bf16 each (half as
+// many where bf16 is written in 4 bits), and a group does the K and V rows of two
+// (token, head) pairs together, so that four loads per lane are in flight before
+// the first is used; the new rows' places come from the index alone, and the table
+// is read while they are on their way.  8 prompts of up to 4096 tokens, 8 kv heads
+// of 128, bf16 to e4m3: 29.4 us, 5.1 TB/s, 76% of a copy's rate (two rows at a time
+// in flight, the maxima on packed 16-bit pairs; one row at a time took 53).  Read
+// back, 2 x 16384 tokens of 16 heads: 69.7 us, 84%.  4 bits, 24576 tokens of 8
+// heads, bf16: written in 25.4 us (77%), 38000 places read back in 36 (77%).
 #include <type_traits>
 
 #include "ra_rows.cuh"
@@ -27,33 +27,49 @@ namespace {
 
 constexpr int kThreads = 256, kUnroll = 2;
 
+// Eights of a row that a lane writes: two from bf16 to 4 bits, so that half as many
+// lanes find a block's scale (24576 tokens of 8 heads: 31 us with one, 25.4 with two).
+// From fp32 two need 89 registers: 8 x 2048 to 4096 tokens take 50 us, with one 48.
+template <typename T>
+constexpr int write_eights(int cache)
+{
+    return cache == RA_E2M1 && sizeof(T) == 2 ? 2 : 1;
+}
 
-// Largest magnitudes, as fp32 bits, of a K row and a V row that LANES lanes hold.
-template <int LANES>
-__device__ __forceinline__ uint2 row_tops(const Raw<__nv_bfloat16> &k, const Raw<__nv_bfloat16> &v)
+// Largest magnitudes, as fp32 bits, of what SHARE lanes hold of a K row and a V row.
+template <int SHARE, int N>
+__device__ __forceinline__ uint2 row_tops(const Raw<__nv_bfloat16> (&k)[N], const Raw<__nv_bfloat16> (&v)[N])
 {
     // as pairs of 16-bit integers, the two rows in one word for the shuffles
     const uint32_t m = 0x7fff7fffu;
-    const uint32_t a = __vmaxu2(__vmaxu2(k.w[0].x & m, k.w[0].y & m), __vmaxu2(k.w[0].z & m, k.w[0].w & m));
-    const uint32_t b = __vmaxu2(__vmaxu2(v.w[0].x & m, v.w[0].y & m), __vmaxu2(v.w[0].z & m, v.w[0].w & m));
+    uint32_t a = 0, b = 0;
+#pragma unroll
+    for (int y = 0; y < N; ++y) {
+        const uint4 x = k[y].w[0], z = v[y].w[0];
+        a = __vmaxu2(a, __vmaxu2(__vmaxu2(x.x & m, x.y & m), __vmaxu2(x.z & m, x.w & m)));
+        b = __vmaxu2(b, __vmaxu2(__vmaxu2(z.x & m, z.y & m), __vmaxu2(z.z & m, z.w & m)));
+    }
     uint32_t t = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
 #pragma unroll
-    for (int o = LANES / 2; o; o >>= 1) t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, o));
+    for (int o = SHARE / 2; o; o >>= 1) t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, o));
     return make_uint2(t << 16, t & 0xffff0000u);
 }
 
-template <int LANES>
-__device__ __forceinline__ uint2 row_tops(const Raw<float> &k, const Raw<float> &v)
+template <int SHARE, int N>
+__device__ __forceinline__ uint2 row_tops(const Raw<float> (&k)[N], const Raw<float> (&v)[N])
 {
     uint2 t = make_uint2(0, 0);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t m = 0x7fffffffu;
-        t.x = max(t.x, max(max(k.w[i].x & m, k.w[i].y & m), max(k.w[i].z & m, k.w[i].w & m)));
-        t.y = max(t.y, max(max(v.w[i].x & m, v.w[i].y & m), max(v.w[i].z & m, v.w[i].w & m)));
-    }
+    for (int y = 0; y < N; ++y)
 #pragma unroll
-    for (int o = LANES / 2; o; o >>= 1) {
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t m = 0x7fffffffu;
+            const uint4 x = k[y].w[i], z = v[y].w[i];
+            t.x = max(t.x, max(max(x.x & m, x.y & m), max(x.z & m, x.w & m)));
+            t.y = max(t.y, max(max(z.x & m, z.y & m), max(z.z & m, z.w & m)));
+        }
+#pragma unroll
+    for (int o = SHARE / 2; o; o >>= 1) {
         t.x = max(t.x, __shfl_xor_sync(0xffffffffu, t.x, o));
         t.y = max(t.y, __shfl_xor_sync(0xffffffffu, t.y, o));
     }
@@ -62,42 +78,50 @@ __device__ __forceinline__ uint2 row_tops(const Raw<float> &k, const Raw<float> 
 
 // The scale byte of a row (8 bits) or of the lane's block of 32 (4 bits), by its
 // largest magnitude; row_e: the bytes of the row's blocks.
-template <int LANES, int CACHE>
+template <int LANES, int SHARE, int CACHE>
 __device__ __forceinline__ uint32_t scale_of(uint32_t top, int lane, uint32_t &row_e)
 {
     if (CACHE != RA_E2M1) return row_exp(top);
     const uint32_t e = block_exp(top);
-    row_e = e << (lane / 4 * 8);
+    row_e = e << (lane / SHARE * 8);
 #pragma unroll
-    for (int o = 4; o < LANES; o <<= 1) row_e |= __shfl_xor_sync(0xffffffffu, row_e, o);
+    for (int o = SHARE; o < LANES; o <<= 1) row_e |= __shfl_xor_sync(0xffffffffu, row_e, o);
     return e;
 }
 
-// Stores a lane's eight values of a row; as codes at the scale e.
-template <int LANES, int CACHE>
-__device__ __forceinline__ void put_row(const Eight &r, uint32_t e, uint32_t row_e, const void *base, const uint8_t *exps, size_t row,
-                                        int lane)
+// Stores a lane's values of a row; as codes at the scale e.
+template <int D, int CACHE, typename T, int N>
+__device__ __forceinline__ void put_row(const Raw<T> (&r)[N], uint32_t e, uint32_t row_e, const void *base, const uint8_t *exps,
+                                        size_t row, int lane)
 {
     uint8_t *bytes = static_cast<uint8_t *>(const_cast<void *>(base)), *e8 = const_cast<uint8_t *>(exps);
     if (CACHE == RA_BF16) {
-        store8(static_cast<__nv_bfloat16 *>(const_cast<void *>(base)) + row * (LANES * 8) + lane * 8, r);
+        store8(static_cast<__nv_bfloat16 *>(const_cast<void *>(base)) + row * D + lane * 8, widen(r[0]));
         return;
     }
     const float inv = exp_byte_inverse(e);
-    float x[8];
+    uint32_t w[2] = {0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = r.x[i] * inv;
-    if (CACHE == RA_E4M3) {
-        uint2 w = make_uint2(0, 0);
-        if (e != 255u) w = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
-        reinterpret_cast<uint2 *>(bytes + row * (LANES * 8))[lane] = w;
-        if (lane == 0) e8[row] = (uint8_t)e;
-    } else {
-        reinterpret_cast<uint32_t *>(bytes + row * (LANES * 4))[lane] = e != 255u ? e2m1x8(x) : 0u;
-        if (lane == 0) {
-            if (LANES == 16) reinterpret_cast<uint32_t *>(e8)[row] = row_e;
-            else reinterpret_cast<uint16_t *>(e8)[row] = (uint16_t)row_e;
+    for (int y = 0; y < N; ++y) {
+        const Eight v = widen(r[y]);
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = v.x[i] * inv;
+        if (e == 255u) continue;
+        if (CACHE == RA_E4M3) {
+            w[0] = e4m3x4(x[0], x[1], x[2], x[3]);
+            w[1] = e4m3x4(x[4], x[5], x[6], x[7]);
+        } else {
+            w[y] = e2m1x8(x);
         }
+    }
+    uint8_t *at = bytes + row * (CACHE == RA_E4M3 ? D : D / 2);
+    if (CACHE == RA_E4M3 || N == 2) reinterpret_cast<uint2 *>(at)[lane] = make_uint2(w[0], w[1]);
+    else reinterpret_cast<uint32_t *>(at)[lane] = w[0];
+    if (lane == 0) {
+        if (CACHE == RA_E4M3) e8[row] = (uint8_t)e;
+        else if (D == 128) reinterpret_cast<uint32_t *>(e8)[row] = row_e;
+        else reinterpret_cast<uint16_t *>(e8)[row] = (uint16_t)row_e;
     }
 }
 
@@ -109,7 +133,8 @@ __global__ void __launch_bounds__(kThreads)
                     size_t v_stride, const int32_t *__restrict__ table, int max_pages,
                     const int32_t *__restrict__ start, const int32_t *__restrict__ count, int *status)
 {
-    constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
+    constexpr int N = write_eights<T>(CACHE), LANES = D / 8 / N, GROUPS = kThreads / LANES;
+    constexpr int SHARE = CACHE == RA_E2M1 ? 4 / N : LANES;  // lanes that have a scale in common
     const int lane = threadIdx.x % LANES;
     const unsigned r0 = blockIdx.x * (GROUPS * kUnroll) + threadIdx.x / LANES;
     for (int b = blockIdx.y; b < B; b += gridDim.y) {
@@ -118,7 +143,7 @@ __global__ void __launch_bounds__(kThreads)
         if (blockIdx.x == 0 && threadIdx.x == 0 && count && n != count[b]) report_bad_page(status);
         const unsigned rows = (unsigned)n * c.Hkv;
         if (blockIdx.x * (unsigned)(GROUPS * kUnroll) >= rows) continue;
-        Raw<T> kr[kUnroll] = {}, vr[kUnroll] = {};
+        Raw<T> kr[kUnroll][N] = {}, vr[kUnroll][N] = {};
         size_t row[kUnroll];
         unsigned tok[kUnroll];
         bool put[kUnroll];
@@ -130,8 +155,11 @@ __global__ void __launch_bounds__(kThreads)
             const unsigned h = r - tok[u] * c.Hkv;
             if (put[u]) {
                 const size_t at = (size_t)b * L + tok[u];
-                kr[u] = load8(k + at * k_stride + h * D + lane * 8);
-                vr[u] = load8(v + at * v_stride + h * D + lane * 8);
+#pragma unroll
+                for (int y = 0; y < N; ++y) {
+                    kr[u][y] = load8(k + at * k_stride + h * D + (lane * N + y) * 8);
+                    vr[u][y] = load8(v + at * v_stride + h * D + (lane * N + y) * 8);
+                }
             }
             row[u] = h;
         }
@@ -151,12 +179,13 @@ __global__ void __launch_bounds__(kThreads)
         __syncwarp();
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const uint2 top = CACHE == RA_BF16 ? make_uint2(0, 0) : row_tops<CACHE == RA_E4M3 ? LANES : 4>(kr[u], vr[u]);
+            const uint2 top = CACHE == RA_BF16 ? make_uint2(0, 0) : row_tops<SHARE>(kr[u], vr[u]);
             uint32_t kx = 0, vx = 0;
-            const uint32_t ke = scale_of<LANES, CACHE>(top.x, lane, kx), ve = scale_of<LANES, CACHE>(top.y, lane, vx);
+            const uint32_t ke = scale_of<LANES, SHARE, CACHE>(top.x, lane, kx);
+            const uint32_t ve = scale_of<LANES, SHARE, CACHE>(top.y, lane, vx);
             if (!put[u]) continue;
-            put_row<LANES, CACHE>(widen(kr[u]), ke, kx, c.k, c.k_exp, row[u], lane);
-            put_row<LANES, CACHE>(widen(vr[u]), ve, vx, c.v, c.v_exp, row[u], lane);
+            put_row<D, CACHE>(kr[u], ke, kx, c.k, c.k_exp, row[u], lane);
+            put_row<D, CACHE>(vr[u], ve, vx, c.v, c.v_exp, row[u], lane);
         }
     }
 }
@@ -263,8 +292,9 @@ cudaError_t launch_kv_write(const PagedCache &c, int cache_dtype, const void *k,
                             int max_pages, const int32_t *start, const int32_t *count, int *status,
                             cudaStream_t s)
 {
-    const dim3 grid = grid_for(B, (long long)L * c.Hkv, c.D / 8);
     auto go = [&](auto kern, auto *kp, auto *vp) {
+        using T = std::remove_cv_t<std::remove_pointer_t<decltype(kp)>>;
+        const dim3 grid = grid_for(B, (long long)L * c.Hkv, c.D / 8 / write_eights<T>(cache_dtype));
         kern<<<grid, kThreads, 0, s>>>(c, kp, vp, B, L, k_stride, v_stride, page_table, max_pages, start, count,
                                        status);
         return cudaGetLastError();
