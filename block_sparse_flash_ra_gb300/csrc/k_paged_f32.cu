@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(kThreads, paged_f32_per_sm(R, CACHE != RA_BF16
     constexpr uint32_t ALL = 0xffffffffu;
     __shared__ float o_s[kWarps][R * D];
     __shared__ float2 ml_s[kWarps][R];
+    __shared__ int without_s[FP4 ? kWarps : 1][D / 32]; // first token without a value, by block
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LANES, kg = lane / LANES;
     const int own = sub >> REST; // the row whose softmax this lane computes
     const float *q = static_cast<const float *>(p.q);
@@ -116,6 +117,7 @@ __global__ void __launch_bounds__(kThreads, paged_f32_per_sm(R, CACHE != RA_BF16
         const int limit = paged_row(p, part, c, own).limit;
         float2 o[R][4] = {};
         float m = -INFINITY, l = 0.f; // m, l: of row `own`, l of this lane's keys
+        int without = 0x7fffffff; // 4 bits: this lane's first token whose block of V has no value
 
         // the warp's keys of tile t: their first row in the cache, or -1
         auto place = [&](int t) -> long long {
@@ -150,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, paged_f32_per_sm(R, CACHE != RA_BF16
                     const long long e = FP4 ? (at + j) * (D / 32) + sub / 4 : at + j;
                     ke[s] = there ? p.c.k_exp[e] : 127u;
                     ve[s] = there ? p.c.v_exp[e] : 127u;
+                    if (FP4 && ve[s] == 255u) without = min(without, first + j);
                 }
             }
             // ---- logits of row `own`
@@ -217,8 +220,8 @@ __global__ void __launch_bounds__(kThreads, paged_f32_per_sm(R, CACHE != RA_BF16
             for (int s = 0; s < STEPS; ++s) {
                 float2 vf[4];
                 widen8<CACHE>(v[s], vf);
-                if (FP4) {
-                    const float e = exp_byte_scale(ve[s]);
+                if (FP4) { // (0 for a block without a value: rows that do not see its token must not, either)
+                    const float e = ve[s] == 255u ? 0.f : exp_byte_scale(ve[s]);
 #pragma unroll
                     for (int y = 0; y < 4; ++y) vf[y] = fmul2(vf[y], make_float2(e, e));
                 }
@@ -234,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, paged_f32_per_sm(R, CACHE != RA_BF16
 #pragma unroll
         for (int w = LANES; w < 32; w <<= 1) {
             l += __shfl_xor_sync(ALL, l, w);
+            if (FP4) without = min(without, __shfl_xor_sync(ALL, without, w));
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -250,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, paged_f32_per_sm(R, CACHE != RA_BF16
                 dst[1] = make_float4(o[r][2].x, o[r][2].y, o[r][3].x, o[r][3].y);
             }
             if ((sub & ((1 << REST) - 1)) == 0) ml_s[warp][own] = make_float2(m, l);
+            if (FP4 && sub % 4 == 0) without_s[warp][sub / 4] = without;
         }
         __syncthreads();
         const bool final = stores_whole(part, c, n);
@@ -269,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, paged_f32_per_sm(R, CACHE != RA_BF16
                 const float f = exp2f(ml.x - base);
                 lr += ml.y * f;
                 val += o_s[w][e] * f;
+                if (FP4 && without_s[w][col / 32] < row.limit) val = __uint_as_float(0x7fc00000u);
             }
             if (final) {
                 const int hq = c.h * p.G + row.g;

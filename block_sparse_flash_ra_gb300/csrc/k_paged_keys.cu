@@ -48,11 +48,14 @@
 // Widening K the same way took 134 us; one warp that issued a tile's loads as
 // halves of it was slower than the softmax (110); a warp more for the products, or
 // for the loads, 87; eight warps to widen, 87.  Up to 4 rows are a block of their
-// own, so that a thread has 4 rows' softmax (512 x up to 128 tokens 95 -> 76 us).
-// 16 rows: 119 us on 64 x 4096 tokens (8 bits 99; the softmax's 72 registers
+// own, so that a thread has 4 rows' softmax (512 x up to 128 tokens 95 -> 77 us).
+// 16 rows: 124 us on 64 x 4096 tokens (8 bits 99; the softmax's 72 registers
 // spill, but one CTA with more takes 125, and four rows to a thread 140).  Warps of
 // their own for the keys' scales: 82 us; three CTAs, with one stage of V or K, 97
-// or 90.
+// or 90.  A block of V without a value (a NaN) would reach, as 0 times it, rows that do
+// not see its token: among the tokens that not all rows may see it becomes zeros, and
+// the rows that see it get their NaN at the end.  Noting such tokens costs other calls
+// up to 2%, drafts up to 5% (in the softmax 7%, in the products' warp 13%).
 //
 // D = 64: two tokens of a page lie in one row of 128 values, so a tile is the
 // same bytes with 256 tokens.  A query row takes two columns, q in one half of
@@ -154,7 +157,11 @@ struct Cfg {
     static constexpr int kBarOff = kOddOff + (kPar == 2 ? RP / 2 * D * 4 : 0);
     static constexpr int kNumBars = 2 * kStages + 2 * kVStages + kEStages + 2 + 2 + 2 + 2 + 2 + 1 + 2 * kRaws + 2 * kXs;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
-    static constexpr int kSmem = kMiscOff + 16 + 1024;
+    // 4 bits, by segment: of each block of values, the first token without one.  A ring:
+    // a tile is widened when the weights of kVStages + 1 tiles before are there
+    static constexpr int kFirstOff = kMiscOff + 16, kFirsts = 8;
+    static_assert(!FP4 || kVStages + 2 < kFirsts, "records");
+    static constexpr int kSmem = kFirstOff + (FP4 ? kFirsts * 16 : 0) + 1024;
     static constexpr uint32_t kColO = 2 * kNS;
     // 4 bits: the keys' scales, by K stage, and ones for the queries
     static constexpr uint32_t kColX = kColO + kNO, kColOnes = kColX + (FP4 ? 4 * kStages : 0);
@@ -364,7 +371,11 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
         if (!FP4) prefetch_tmap(&tm_v);
     }
     uint2 *table = reinterpret_cast<uint2 *>(smem + C::kTableOff);
-    if (FP4 && threadIdx.x < kWide4Entries) wide4_fill(table, threadIdx.x); // (more threads than entries)
+    int *firsts = reinterpret_cast<int *>(smem + C::kFirstOff);
+    if (FP4 && threadIdx.x < kWide4Entries) { // (more threads than entries)
+        wide4_fill(table, threadIdx.x);
+        if (threadIdx.x < C::kFirsts * 4) firsts[threadIdx.x] = kNoToken;
+    }
     begin_in_order(part);
     report_lengths(p, part);
     PagedCursor c; // found beside the barriers' and TMEM's setting up
@@ -377,6 +388,8 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctx)) != 0;
     };
     auto source_len = [&](int b) { return part.prefix ? paged_prefix_len(p) : paged_kv_len(p, b); };
+    // 4 bits: the source's last tokens, which not all rows may see
+    const int last = FP4 && p.causal && !part.prefix ? p.Lq - 1 : 0;
 
     if (FP4 && any && warp == C::kLoadWarp) {
         // ------------------------------------------------------------ loads, 4 bits
@@ -454,7 +467,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ones = 0x7f7f7f7fu;
         if (of_keys) tmem_st4(lane_base + C::kColOnes, ones, ones, ones, ones);
-        uint32_t i = 0;
+        uint32_t i = 0, seg = 0;
         bool ok = true;
         auto lds4 = [](uint32_t at) {
             uint4 w;
@@ -491,7 +504,8 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 // finds the scale byte and the entries of row y = x
                 const int mine = row0 + kRows * (x & (kBlocks - 1));
                 uint32_t top[2];
-                const uint32_t in = wide4_rows<kPar == 2>(xs[kKeys + mine], top);
+                const uint32_t in = wide4_rows<kPar == 2>(xs[kKeys + mine], top, smem_u32(firsts) + seg % C::kFirsts * 16, t * kTokens + mine * kPar,
+                                                         last ? len - last : kNoToken, len);
                 uint8_t *e = smem + C::kExpOff + (i % C::kEStages) * kTokens + mine * kPar;
 #pragma unroll
                 for (int y = 0; y < kPar; ++y) e[y] = mine * kPar + y < valid ? top[y] - kWide4Up : 127;
@@ -527,6 +541,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 arrive(bars.v_full + sv);
             }
             if (!ok || !cursor_next(p, part, c, n)) break;
+            ++seg;
         }
     } else if (any && warp == C::kLoadWarp) {
         // ------------------------------------------------------------ loads
@@ -767,6 +782,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
             const bool more = cursor_next(p, part, next, n);
             if (more) load_q(next, seg + 1);
             const Rows rows = rows_of(seg);
+            if (FP4 && threadIdx.x < 4) firsts[(seg - 1) % C::kFirsts * 4 + threadIdx.x] = kNoToken;
             soft_sync<NT>();
             float qs[kRT];
             int all = len; // keys below it are seen by every row
@@ -1047,6 +1063,14 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 for (int k = 0; k < C::kPTerms; ++k) z[k] = kPar == 2 && tid >= D ? o[k][y * kPar + kPar - 1] : o[k][y * kPar];
                 v[y] = FP8 ? z[0] + (z[1] + z[C::kPTerms - 1] * (1.f / kRest)) * (1.f / kRest) : z[0] + z[1];
                 v[y] *= row_f[row0 + y * kPar];
+            }
+            if (last) {
+                // none where the row sees a token whose block of V has none
+                const int without = firsts[seg % C::kFirsts * 4 + ((tid & (D - 1)) >> 5)];
+                if (without != kNoToken) // rare
+#pragma unroll
+                    for (int y = 0; y < kRT / kPar; ++y)
+                        if (without < rows.limit[row0 + y * kPar]) v[y] = __uint_as_float(0x7fc00000u);
             }
             if (kPar == 2) {
                 float *odd = reinterpret_cast<float *>(smem + C::kOddOff) + row0 / kPar * D + (tid & (D - 1));

@@ -34,7 +34,7 @@
 // few-row kernel uses, has no room in a compute-bound loop.
 // 4-bit caches: the same from e2m1 codes with a power of two of each 32 values,
 // six binades up so that 6 * 2^6 takes the place of 448 (16 sequences of 8192
-// tokens, 4 kv heads, 80 rows: 72 us).
+// tokens, 4 kv heads, 80 rows: 73 us).
 // 16-bit caches: the tiles go to the products as they are, P is bf16 (2^-8).
 // Logits, maxima, sums and O are fp32.
 //
@@ -51,6 +51,7 @@
 
 #include "ra_rows.cuh"
 #include "ra_sched.cuh"
+#include "ra_wide4.cuh"
 
 namespace ra {
 namespace {
@@ -58,6 +59,9 @@ namespace {
 constexpr int kKeys = 128, kHalf = 64, kD = 128;
 constexpr int kThreads = 864;
 constexpr int kWideWarpK = 16, kWideWarpV = 20, kLoadWarp = 24, kMmaWarp = 26;
+// 4 bits: records of the first tokens without a value, by segment: a ring, as who
+// begins one is some segments ahead of who reads it.
+constexpr int kFirsts = 8;
 // The softmax of 32 keys takes the row's present reference for granted:
 // weights are computed at once, and only when a logit passes the reference by
 // 2^13 (2^16 in bf16) -- one barrier with an or over the two warps of 32 rows
@@ -86,7 +90,10 @@ struct Cfg {
     static constexpr int kNumBars = 8 + 8 + 10 + 4 + 4 + 1;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8 + 8;
     static constexpr int kScaleOff = kMiscOff + 16; // E of K tiles [4], EV of V tiles [4]
-    static constexpr int kPairOff = kScaleOff + 48; // [tile][half][128] of the threads of a row
+    // 4 bits, for tile A and tile B: by segment that has the tile, the first tokens
+    // whose blocks of V have no value
+    static constexpr int kFirstOff = kScaleOff + 48;
+    static constexpr int kPairOff = kFirstOff + (FP4 ? 2 * kFirsts * 16 : 0); // [tile][half][128] of the threads of a row
     static constexpr int kSmem = kPairOff + 2 * 2 * 128 * 4;
     static_assert(kSmem <= 232448 && kMiscOff % 16 == 0, "shared memory");
     static constexpr uint32_t kFmt = FP8 ? 0u : (1u << 7) | (1u << 10); // f16 or bf16 operands
@@ -146,11 +153,11 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi)
     return r;
 }
 
-// 2^(b - e) of a scale byte b as a pair of halves; NaN for a row without a value
-__device__ __forceinline__ __half2 half_scale(uint32_t b, int e)
+// 2^(b - e) of a scale byte b as a pair of halves; `none` for a row without a value
+__device__ __forceinline__ __half2 half_scale(uint32_t b, int e, float none = NAN)
 {
     const int d = (int)b - e;
-    return __float2half2_rn(b == 255u ? __uint_as_float(0x7fc00000u) : d < -126 ? 0.f : __uint_as_float((uint32_t)(127 + d) << 23));
+    return __float2half2_rn(b == 255u ? none : d < -126 ? 0.f : __uint_as_float((uint32_t)(127 + d) << 23));
 }
 
 // Rows [row0, row0 + 64) of a 16-bit tile from half a tile of codes, by 4
@@ -226,11 +233,17 @@ __device__ __noinline__ void widen_far(uint32_t tile, uint32_t raw, const uint8_
 // The same from 4 bits: a thread takes a row's block x of 32 codes, which become
 // 64 bytes of one half of the f16 tile.  Lanes 4-7 of a group of 8 take the row 3
 // apart (by exclusive or), and the upper two blocks their chunks in another
-// order, which again puts a phase's accesses on different banks.  FAR: only the
-// blocks that lie below a half's least scale, in two steps.
+// order, which again puts a phase's accesses on different banks.  A value block
+// without a value becomes 0: a product would carry its NaN to rows that do not see
+// its token, and those that do get theirs at the end.  FAR: only the blocks that
+// lie below a half's least scale, in two steps; and those without a value are noted.
+struct Note {
+    uint32_t a, b; // where, for row tiles A and B (0: not)
+    int token;     // the tile's first
+};
 template <bool FAR>
 __device__ __forceinline__ void widen_blocks(uint32_t tile, uint32_t raw, const uint8_t *exps, int row0, int valid, int e,
-                                             int warp, int lane)
+                                             float none, int warp, int lane, Note note)
 {
     const int x = lane & 3, hi = x >> 1, g = lane >> 3, in8 = ((g >> 1) * 4 + (g & 1)) ^ (lane & 4 ? 3 : 0);
 #pragma unroll 1
@@ -238,8 +251,12 @@ __device__ __forceinline__ void widen_blocks(uint32_t tile, uint32_t raw, const 
         const int j = (warp * 2 + jg) * 8 + in8; // row of the half tile
         const uint32_t b = exps[j * 4 + x];
         const bool live = row0 + j < valid;
+        if (FAR && live && b == 255u) {
+            if (note.a) note_without(note.a + x * 4, note.token + row0 + j);
+            if (note.b) note_without(note.b + x * 4, note.token + row0 + j);
+        }
         if (FAR && (!live || (int)b - e >= -kHalfLeast)) continue;
-        const __half2 s1 = half_scale(127 - kFarStep, 127), s = half_scale(b, FAR ? e - kFarStep : e);
+        const __half2 s1 = half_scale(127 - kFarStep, 127), s = half_scale(b, FAR ? e - kFarStep : e, none);
         const uint4 w = lds128(raw + j * 64 + x * 16);
         const uint32_t u[4] = {hi ? w.y : w.x, hi ? w.x : w.y, hi ? w.w : w.z, hi ? w.z : w.w};
         const uint32_t at = tile + hi * (kKeys * 128) + (row0 + j) * 128;
@@ -259,9 +276,9 @@ __device__ __forceinline__ void widen_blocks(uint32_t tile, uint32_t raw, const 
     }
 }
 __device__ __noinline__ void widen_far_blocks(uint32_t tile, uint32_t raw, const uint8_t *exps, int row0, int valid, int e,
-                                              int warp, int lane)
+                                              int warp, int lane, Note note)
 {
-    widen_blocks<true>(tile, raw, exps, row0, valid, e, warp, lane);
+    widen_blocks<true>(tile, raw, exps, row0, valid, e, 0.f, warp, lane, note);
 }
 
 // 32 stored weights of every thread times f, a power of two; in two steps where
@@ -306,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // softmaxes of g precede that
     volatile int *k_scale = reinterpret_cast<volatile int *>(smem + C::kScaleOff);
     volatile int *v_scale = k_scale + 4;
+    int *firsts = reinterpret_cast<int *>(smem + C::kFirstOff);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
@@ -316,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bars.q_full + s, 256);
             mbar_init(bars.s_full + s, FP8 ? 2 : 1);
             mbar_init(bars.p_full + s, 256);
-            mbar_init(bars.o_full + s, 1);
+            mbar_init(bars.o_full + s, FP4 ? 2 : 1);
             mbar_init(bars.v_clear + s, 128);
         }
         for (int s = 0; s < 4; ++s) {
@@ -361,10 +379,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const void *tm = m ? &tm_v : &tm_k;
             const uint8_t *exps = m ? p.c.v_exp : p.c.k_exp;
             const int box = min(p.c.page, kPart);
-            uint32_t g = 0;
+            uint32_t g = 0, segs[2] = {}; // segments, and those with two tiles of rows
             bool ok = true;
             for (;;) {
                 const int n = cursor_take(c), len = source_len(c.b);
+                const bool both = FP4 && two_tiles(c);
                 for (int t = c.t0; ok && t < c.t0 + n; ++t, ++g) {
                     const int valid = len - t * kKeys, st = g & 1;
                     // the boxes of the tile's parts: where they are in the cache
@@ -384,6 +403,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int y = 0; y < kParts; ++y) {
                             const int rs = 2 * m + y;
                             if (!(ok = wait_all(bars.raw_empty + rs, (g & 1) ^ 1))) break;
+                            if (FP4 && m && y == 0 && t == c.t0) {
+                                // The segment's records of blocks without a value.  Those of
+                                // eight segments before are not read any more: a tile of a
+                                // segment behind that one has its weights, from the same
+                                // threads (V's tile g - 1 has waited for P V of tile g - 3).
+                                if (lane < 4) firsts[segs[0] % kFirsts * 4 + lane] = kNoToken;
+                                if (both && lane < 4) firsts[(kFirsts + segs[1] % kFirsts) * 4 + lane] = kNoToken;
+                                __syncwarp();
+                            }
                             if (y == 0) {
                                 // the tile's scale bytes (this stage's last user is widened)
                                 constexpr int X = C::kRowX;
@@ -441,6 +469,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!ok || !cursor_next(p, part, c, n)) break;
+                ++segs[0];
+                segs[1] += both;
             }
             if (!ok) {
                 // copies on their way land before the CTA ends (a phase that
@@ -476,6 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (FP8 && lane == 0) mbar_arrive(bars.s_full + x);
                 tc_commit_w(bars.s_full + x);
             };
+            auto o_done = [&](int x) {
+                // (passes on what the wait for the values' tile has seen: widen_far_blocks' notes)
+                if (FP4 && lane == 0) mbar_arrive(bars.o_full + x);
+                tc_commit_w(bars.o_full + x);
+            };
             auto issue_pv = [&](int x, uint32_t j, uint32_t ph, bool first) -> bool {
                 const uint64_t vd = vd0 + (j & 1) * kStep;
                 if (!wait_all(bars.p_full + x, ph)) return false;
@@ -501,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool more = t + 1 < n;
                     if (!(ok = wait_all((FP8 ? bars.v_full : bars.v_clear) + (g & 1), (g >> 1) & 1))) break;
                     if (!(ok = issue_pv(0, g, g & 1, t == 0))) break;
-                    if (!more) tc_commit_w(bars.o_full + 0);
+                    if (!more) o_done(0);
                     if (more) {
                         if (!(ok = wait_all(bars.k_full + ((g + 1) & 1), ((g + 1) >> 1) & 1))) break;
                         tc_fence_after();
@@ -509,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (both) {
                         if (!(ok = issue_pv(1, g, parts_b++ & 1, t == 0))) break;
-                        if (!more) tc_commit_w(bars.o_full + 1);
+                        if (!more) o_done(1);
                     }
                     tc_commit_w(bars.v_empty + (g & 1));
                     if (more) {
@@ -527,11 +562,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int w = warp & 3, st_raw = warp >= kWideWarpV ? 2 : 0;
         const uint32_t raw = smem_u32(smem + C::kRawOff + st_raw * C::kRaw);
         uint64_t *raw_full = bars.raw_full + st_raw, *raw_empty = bars.raw_empty + st_raw;
-        uint32_t g = 0;
+        uint32_t g = 0, segs[2] = {};
         bool ok = true;
+        const float none = st_raw ? 0.f : NAN;
         while (any && ok) {
             const int n = cursor_take(c), len = source_len(c.b);
+            const bool both = FP4 && two_tiles(c);
             int ev = -1; // EV of the segment
+            auto note_of = [&](int t) {
+                const uint32_t a = smem_u32(firsts) + segs[0] % kFirsts * 16, b = smem_u32(firsts) + (kFirsts + segs[1] % kFirsts) * 16;
+                return Note{st_raw ? a : 0u, st_raw && both ? b : 0u, t * kKeys};
+            };
             for (int t = c.t0; ok && t < c.t0 + n; ++t, ++g) {
                 const int valid = min(len - t * kKeys, kKeys), st = g & 1;
                 if (!FP8) {
@@ -558,8 +599,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int j = lane + 32 * y;
                         if (FP4) {
                             if (j >= valid) continue;
+                            // (as the least, a block without a value counts as 0)
                             const uint32_t w = reinterpret_cast<const uint32_t *>(ex)[j], v = w & ~__vcmpeq4(w, 0xffffffffu);
-                            const uint32_t hi = __vmaxu4(v, v >> 16), lo = __vminu4(w, w >> 16);
+                            const uint32_t hi = __vmaxu4(v, v >> 16), lo = __vminu4(v, v >> 16);
                             top = max(top, (int)max(hi & 0xffu, hi >> 8 & 0xffu) - kUp4);
                             low = min(low, (int)min(lo & 0xffu, lo >> 8 & 0xffu));
                         } else {
@@ -578,15 +620,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // the softmax needs EV, but not the values
                         if (st_raw) mbar_arrive(bars.ev_full + (g & 3));
                     }
-                    const bool far = __any_sync(0xffffffffu, low < e - kHalfLeast);
+                    const bool far = __any_sync(0xffffffffu, low < (FP4 ? max(e - kHalfLeast, 1) : e - kHalfLeast));
                     if (!(ok = wait_all((st_raw ? bars.v_empty : bars.k_empty) + st, ((g >> 1) & 1) ^ 1))) break;
 #pragma unroll 1
                     for (int y = 0; y < 2 && ok; ++y) {
                         if (!(ok = wait_all(raw_full + y, g & 1))) break;
                         const uint8_t *exh = ex + y * kHalf * C::kRowX;
                         if (FP4) {
-                            widen_blocks<false>(tile, raw + y * C::kRaw, exh, y * kHalf, valid, e, w, lane);
-                            if (far) widen_far_blocks(tile, raw + y * C::kRaw, exh, y * kHalf, valid, e, w, lane);
+                            widen_blocks<false>(tile, raw + y * C::kRaw, exh, y * kHalf, valid, e, none, w, lane, Note{});
+                            if (far) widen_far_blocks(tile, raw + y * C::kRaw, exh, y * kHalf, valid, e, w, lane, note_of(t));
                         } else {
                             widen_half(tile, raw + y * C::kRaw, exh, y * kHalf, valid, e, w, lane);
                             if (far) widen_far(tile, raw + y * C::kRaw, exh, y * kHalf, valid, e, w, lane);
@@ -599,6 +641,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok || !cursor_next(p, part, c, n)) break;
+            ++segs[0];
+            segs[1] += both;
         }
     } else {
         // ---------------------------------------------------------------- softmax
@@ -836,6 +880,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- the segment's end: this row's result, half of its columns
             if (mine) {
                 wait(bars.o_full + x, segs & 1);
+                uint32_t without = 0; // which of the thread's two blocks of V are, at a token that the row sees
+                if (FP4) {
+                    const int *first = firsts + (x * kFirsts + segs % kFirsts) * 4 + y * 2;
+                    without = (first[0] < limit ? 1u : 0u) | (first[1] < limit ? 2u : 0u);
+                }
                 ++segs;
                 pair[y * 128] = l; // both threads of the row are done with its tiles
                 pair_sync();
@@ -864,6 +913,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld16(o_half + k * 16, o);
                     tmem_ld_wait();
                     const int col = y * 64 + k * 16;
+                    if (FP4 && (without >> (k >> 1) & 1u)) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = __uint_as_float(0x7fc00000u);
+                    }
                     if (row.counts && final) {
                         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + place * kD + col);
 #pragma unroll

@@ -17,8 +17,28 @@ namespace ra {
 
 // Entry k: the magnitudes' codes at 2^(6 - k), zeros from some k on; the last: a
 // block without a value (a row's largest byte is below 255, so no k is that).
-constexpr int kWide4Entries = 256, kWide4Nan = 255;
+// From the first token on that some row of queries does not see, such blocks are zeros,
+// as a product would carry their NaN to it; rows that do see them get theirs at the
+// end, by the first of those tokens with such a block.
+constexpr int kWide4Entries = 256, kWide4Nan = 255; // (254: zeros)
 constexpr int kWide4Up = 6; // a row's byte is its largest less this, 0 at the least
+constexpr int kNoToken = 0x7fffffff;
+
+// Notes a token whose block of V has no value: `first`, of the block, in shared memory.
+__device__ __forceinline__ void note_without(uint32_t first, int token)
+{
+    asm volatile("red.shared.min.s32 [%0], %1;" ::"r"(first), "r"(token) : "memory");
+}
+
+// The same of a row's blocks that have a bit set in their byte of `none`; end: behind
+// the last token.  Rare, so kept out of the loop's code.
+static __device__ __noinline__ void note_row(uint32_t firsts, uint32_t none, bool half, int token, int end)
+{
+    for (int b = 0; b < 4; ++b) {
+        const int t = token + (half ? b >> 1 : 0);
+        if ((none >> (8 * b) & 1u) && t < end) note_without(firsts + (half ? b & 1 : b) * 4, t);
+    }
+}
 
 __device__ __forceinline__ void wide4_fill(uint2 *table, int k)
 {
@@ -28,10 +48,11 @@ __device__ __forceinline__ void wide4_fill(uint2 *table, int k)
 }
 
 // From a row's scale bytes (four blocks, or two of each of two tokens: HALF) its
-// byte -- at least kWide4Up, and not of blocks without a value -- and, as bytes,
-// the blocks' entries.
+// byte -- at least kWide4Up, and not of blocks without a value -- and, as bytes, the
+// blocks' entries.  token: the row's (first); from token `edge` to below `end` blocks
+// without a value are zeros, and noted in `firsts`.
 template <bool HALF>
-__device__ __forceinline__ uint32_t wide4_rows(uint32_t w, uint32_t *top)
+__device__ __forceinline__ uint32_t wide4_rows(uint32_t w, uint32_t *top, uint32_t firsts, int token, int edge, int end)
 {
     auto tops = [&](uint32_t x) {
         const uint32_t lo = max(x & 0xffu, x >> 8 & 0xffu), hi = max(x >> 16 & 0xffu, x >> 24);
@@ -44,7 +65,9 @@ __device__ __forceinline__ uint32_t wide4_rows(uint32_t w, uint32_t *top)
     if (max(top[0], top[1]) < 255u) return entries(w);
     const uint32_t none = __vcmpeq4(w, 0xffffffffu); // rare
     tops(w & ~none);
-    return entries(w & ~none) | none;
+    const uint32_t zero = HALF ? (token >= edge ? 0x0101u : 0u) | (token + 1 >= edge ? 0x01010000u : 0u) : token >= edge ? 0x01010101u : 0u;
+    if (none & zero) note_row(firsts, none & zero, HALF, token, end); // (255 becomes 254)
+    return (entries(w & ~none) & ~none) | (none & ~zero);
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)

@@ -472,7 +472,8 @@ RA_API int ra_unpermute_tokens(const void *in, void *out, int B, int L, size_t r
  * infinity or a NaN gets exp = 255 and codes 0, and stands for NaN.
  * The 32 values of an e2m1 block stand for code * 2^(exp - 127) likewise, with
  * max|block| <= 6 * 2^e and codes of 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign (half
- * a step: 2^-2 relative above 2^e, 2^(e-2) absolute below).
+ * a step: 2^-2 relative above 2^e, 2^(e-2) absolute below).  A block of values that
+ * holds an infinity or a NaN reaches its 32 columns of the rows that see its token.
  */
 typedef struct {
     int n_pages, page_size, Hkv, D;

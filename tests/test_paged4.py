@@ -295,6 +295,88 @@ def test_a_block_without_a_value_reaches_its_own_values(name, dtype):
 
 @gpu
 @each_type
+@pytest.mark.parametrize("Hq,Hkv,Lq,D", [(1, 1, 3, 128), (2, 2, 4, 128), (4, 2, 4, 128), (2, 1, 7, 128), (4, 1, 6, 128), (8, 1, 4, 128), (8, 1, 10, 128),
+                                         (16, 1, 18, 128), (1, 1, 2, 64), (4, 2, 2, 64), (3, 1, 4, 64), (8, 1, 5, 64)])
+def test_a_block_without_a_value_does_not_reach_rows_before_it(Hq, Hkv, Lq, D, dtype):
+    """The drafts' own last tokens hold value blocks of NaN: queries before them see none of it, those behind all."""
+    lens = [130, 41, 300, Lq]
+    pool = Pool(lens, Hkv=Hkv, D=D, page=16, seed=37, spread=0.5)
+    gone = [(0, 2, 1), (1, 1, 0), (1, 2, 1), (2, 1, 1), (2, 1, 0), (3, 2, 0)]  # sequence, tokens from its end, block
+    for b, back, x in gone:
+        page, _, at = pool.places(b)[lens[b] - back]
+        pool.val[1][page, :, at, 32 * x:32 * x + 32] = 0
+        pool.cache.v_exps[page, :, at, x] = 255
+        pool.cache.v_pages.view(torch.uint8)[page, :, at, 16 * x:16 * x + 16] = 0
+    q = torch.randn((4, Lq, Hq, D), generator=torch.Generator().manual_seed(38)).to(dtype)
+    scale = ta.f32(D ** -0.5)
+    out, lse = ta.forward(pool, q, scale)
+    assert torch.isfinite(lse).all()
+    bound = ta.BOUNDS["fp32" if dtype == torch.float32 else "rows8" if D == 128 and Lq * Hq // Hkv > 32 else "few8"]
+    for b in range(4):
+        sees = torch.zeros((Lq, Hq, D), dtype=torch.bool)
+        for _, back, x in [g for g in gone if g[0] == b]:
+            sees[Lq - back:, :, 32 * x:32 * x + 32] = True  # query i sees tokens up to Lq - 1 - i from the end
+        assert torch.equal(torch.isnan(out[b].cpu()), sees)
+        k, v = (t.repeat_interleave(Hq // Hkv, 1) for t in pool.dense(b))
+        s = torch.einsum("ihd,jhd->hij", q[b].double(), k) * scale
+        s = s.masked_fill(torch.arange(lens[b]) > torch.arange(Lq)[:, None] + lens[b] - Lq, -math.inf)
+        p = torch.softmax(s, -1)
+        o = torch.einsum("hij,jhd->ihd", p, v)
+        near = (out[b].cpu() - o).abs() <= ta.allowed(p, v, o, dtype, **bound)
+        assert (near | sees).all()
+
+
+@gpu
+@each_type
+@pytest.mark.parametrize("Hq,Hkv,Lq,D,B,prefix", [(2, 1, 2, 128, 4000, 0), (4, 2, 4, 128, 2000, 0), (4, 1, 8, 128, 2000, 70), (8, 1, 10, 128, 2000, 0),
+                                                  (16, 1, 18, 128, 2000, 0), (2, 1, 3, 64, 4000, 0), (8, 1, 20, 64, 700, 0), (8, 1, 4, 128, 3, 0), (4, 2, 2, 64, 3, 40)])
+def test_blocks_without_values_of_many_sequences(Hq, Hkv, Lq, D, B, prefix, dtype):
+    """Some of many sequences have them, anywhere, and one of three tokens of a prefix: the rows that see them and no others."""
+    g = torch.Generator().manual_seed(39)
+    lens = [Lq + int(x) for x in torch.randint(0, 40 if B > 3 else 3000, (B,), generator=g)]
+    page, n = 16, [-(-x // 16) for x in lens]
+    of = -(-prefix // page)
+    cache = ra.new_kv_cache(sum(n) + of, page, Hkv, D, F4)
+    for codes, exps in ((cache.k_pages, cache.k_exps), (cache.v_pages, cache.v_exps)):
+        codes.view(torch.uint8).copy_(torch.randint(0, 256, codes.shape, generator=g, dtype=torch.uint8))
+        exps.copy_(torch.randint(124, 127, exps.shape, generator=g, dtype=torch.uint8))
+    table, at = torch.zeros((B, max(n)), dtype=torch.int32), of
+    for b in range(B):
+        table[b, :n[b]] = torch.arange(at, at + n[b])
+        at += n[b]
+    # first[b, x]: the first token without a value in block x, or 2^30
+    first = torch.full((B, D // 32), 1 << 30)
+    picked = torch.randperm(B, generator=g)[:max(B // 3, 2)].tolist()
+    gone = []
+    for b in picked:
+        for _ in range(2):
+            t, x = max(lens[b] - 1 - int(torch.randint(0, Lq + 3, (1,), generator=g)), 0), int(torch.randint(0, D // 32, (1,), generator=g))
+            first[b, x] = min(int(first[b, x]), t)
+            gone.append((int(table[b, t // page]), t % page, x))
+    if prefix:
+        first[:, 1] = -1
+        gone.append((1, 2, 1))
+    i = [torch.tensor(v) for v in zip(*gone)]
+    where = (i[0].cuda(), slice(None), i[1].cuda())
+    q = torch.randn((B, Lq, Hq, D), generator=g).to(dtype).cuda()
+    p = ra.make_paged_params(cache, q, table.cuda(), i32(lens), scale=0.05, prefix_table=i32(list(range(of))) if prefix else None,
+                             prefix_len=i32([prefix]) if prefix else None)
+    got = []
+    for e in (0, 255):
+        codes = cache.v_pages.view(torch.uint8).view(*cache.v_pages.shape[:3], D // 32, 16)
+        codes[where + (i[2].cuda(),)] = 0
+        cache.v_exps[where + (i[2].cuda(),)] = e
+        got.append(ra.paged_forward(p, q, cache)[0].cpu().float().view(B, Lq, Hq, D // 32, 32))
+    sees = first[:, None] <= torch.tensor(lens)[:, None, None] - Lq + torch.arange(Lq)[None, :, None]
+    assert torch.isfinite(got[0]).all()
+    assert torch.equal(torch.isnan(got[1]), sees[:, :, None, :, None].expand(got[1].shape))
+    # each is off by half a step of its type and 2^-10 of values of 6 * 2^-1 at the most
+    off = torch.where(torch.isnan(got[1]), 0.0, (got[1] - got[0]).abs())
+    assert float(off.max()) <= 2 * 3.0 * (torch.finfo(dtype).eps / 2 + 2.0 ** -10)
+
+
+@gpu
+@each_type
 @each_kernel
 def test_pages_out_of_range(name, dtype):
     _, Hkv, _, D = KERNELS[name]
