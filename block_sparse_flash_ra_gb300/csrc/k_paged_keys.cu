@@ -487,6 +487,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 const uint32_t *xs = reinterpret_cast<const uint32_t *>(smem + C::kXOff + sx * C::kX); // K's, then V's
                 if (!(ok = wait_all(bars.x_full + sx, (i / C::kXs) & 1))) break;
                 if (!(ok = wait_all(bars.k_empty + sk, ((i / C::kStages) & 1) ^ 1))) break;
+                tc_fence_after(); // the products that read these scales before are done
                 if (of_keys) {
                     uint32_t kx[4];
 #pragma unroll
