@@ -56,6 +56,9 @@
 // not see its token: among the tokens that not all rows may see it becomes zeros, and
 // the rows that see it get their NaN at the end.  Noting such tokens costs other calls
 // up to 2%, drafts up to 5% (in the softmax 7%, in the products' warp 13%).
+// At D = 64 a key without a value, too, would reach rows that see only the token beside it,
+// by a scale of NaN times the zeros of Q: in such tiles its scales become ones, and the softmax
+// is told (64 x 8192 tokens of 4 heads: 4 rows 59 -> 60 us, 8 rows 70, 12 rows 85 -> 86).
 //
 // D = 64: two tokens of a page lie in one row of 128 values, so a tile is the
 // same bytes with 256 tokens.  A query row takes two columns, q in one half of
@@ -108,6 +111,8 @@ constexpr float kLouder = 64.f; // a value row that far above E raises it: 2^(e_
 // references fall, while E rises, by 2^40 at most: for E of value rows between
 // 2^-18 and 2^22.  So weights are below 2^100.
 constexpr float kQuiet = 30.f, kPass = 60.f, kFallFrom = 100.f, kFallTo = 140.f;
+// 4 bits, D = 64: the byte of a token whose key has no value (a value row's is less by kWide4Up at least).
+constexpr int kNoKey = 255;
 // 16-bit caches: what a weight may pass its reference by.  bf16 has fp32's
 // range, but O's sums of weights times values need some of it.
 constexpr float kPass16 = 16.f;
@@ -488,19 +493,9 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 if (!(ok = wait_all(bars.x_full + sx, (i / C::kXs) & 1))) break;
                 if (!(ok = wait_all(bars.k_empty + sk, ((i / C::kStages) & 1) ^ 1))) break;
                 tc_fence_after(); // the products that read these scales before are done
-                if (of_keys) {
-                    uint32_t kx[4];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) kx[y] = xs[lane + 32 * y];
-                    if (kPar == 2 && (valid & 1)) {
-                        // an odd length ends inside a row: its other token meets zeros of Q,
-                        // whose product with a scale of NaN would not be zero
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            if (lane + 32 * y == valid >> 1) kx[y] = (kx[y] & 0xffffu) | (ones & 0xffff0000u);
-                    }
-                    tmem_st4(lane_base + C::kColX + 4 * sk, kx[0], kx[1], kx[2], kx[3]);
-                }
+                // D = 64: whether a row of queries may see one of two tokens that lie in a row
+                const bool apart = kPar == 2 && (t + 1) * kTokens > len - last;
+                if (of_keys && !apart) tmem_st4(lane_base + C::kColX + 4 * sk, xs[lane], xs[lane + 32], xs[lane + 64], xs[lane + 96]);
                 // of the values' rows row0 + kRows y a group of four lanes has, lane x
                 // finds the scale byte and the entries of row y = x
                 const int mine = row0 + kRows * (x & (kBlocks - 1));
@@ -510,6 +505,22 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 uint8_t *e = smem + C::kExpOff + (i % C::kEStages) * kTokens + mine * kPar;
 #pragma unroll
                 for (int y = 0; y < kPar; ++y) e[y] = mine * kPar + y < valid ? top[y] - kWide4Up : 127;
+                if (apart) {
+                    // One of the two meets zeros of Q: times a scale of NaN they would not be
+                    // zero.  Such scales become ones, and the softmax learns of the token by
+                    // its byte.
+                    uint32_t kx[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const uint32_t w = xs[lane + 32 * y], none = __vcmpeq4(w, 0xffffffffu);
+                        kx[y] = (w & ~none) | (ones & none);
+                    }
+                    tmem_st4(lane_base + C::kColX + 4 * sk, kx[0], kx[1], kx[2], kx[3]);
+                    const uint32_t no_key = __vcmpeq4(xs[mine], 0xffffffffu);
+#pragma unroll
+                    for (int y = 0; y < kPar; ++y)
+                        if ((no_key >> (16 * y) & 0xffffu) && mine * kPar + y < valid) e[y] = kNoKey;
+                }
                 if (of_keys) tmem_st_wait();
                 tc_fence_before();
                 arrive(bars.e_full + i % C::kEStages);
@@ -786,7 +797,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
             if (FP4 && threadIdx.x < 4) firsts[(seg - 1) % C::kFirsts * 4 + threadIdx.x] = kNoToken;
             soft_sync<NT>();
             float qs[kRT];
-            int all = len; // keys below it are seen by every row
+            int all = FP4 && kPar == 2 ? len - last : len; // keys below it are seen by every row
 #pragma unroll
             for (int r = 0; r < kRT; ++r) {
                 qs[r] = rows.qs[row0 + r];
@@ -846,8 +857,10 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 }
                 if (masked) {
 #pragma unroll
-                    for (int r = 0; r < kRT; ++r)
+                    for (int r = 0; r < kRT; ++r) {
+                        if (FP4 && kPar == 2) s[r] += vs[r % kPar] * 0.f; // a key without a value (kNoKey) is NaN
                         if (tok + r % kPar >= valid || first + tok + r % kPar >= rows.limit[row0 + r]) s[r] = -INFINITY;
+                    }
                 }
                 // how far a logit may pass its reference: as a weight by kPass or kPass16,
                 // as a contribution 2^(s + e_v - E) to an 8-bit cache's O by kGrow.  (Sums are rounded up:

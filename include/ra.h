@@ -472,8 +472,8 @@ RA_API int ra_unpermute_tokens(const void *in, void *out, int B, int L, size_t r
  * infinity or a NaN gets exp = 255 and codes 0, and stands for NaN.
  * The 32 values of an e2m1 block stand for code * 2^(exp - 127) likewise, with
  * max|block| <= 6 * 2^e and codes of 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign (half
- * a step: 2^-2 relative above 2^e, 2^(e-2) absolute below).  A block of values that
- * holds an infinity or a NaN reaches its 32 columns of the rows that see its token.
+ * a step: 2^-2 relative above 2^e, 2^(e-2) absolute below).  A block that holds an
+ * infinity or a NaN gets exp = 255 and codes 0, and stands for NaN.
  */
 typedef struct {
     int n_pages, page_size, Hkv, D;
@@ -578,8 +578,10 @@ RA_API size_t ra_attn_paged_workspace_size(const ra_kv_cache *cache, const ra_pa
  *           contents need not survive the call.  Calls that may overlap in
  *           time (other streams, graphs replayed at once) need one each.
  * Keys and values behind a sequence's length are never used, whatever the
- * memory holds; inside it, key and value rows that only some of a sequence's
- * queries see have to be finite.
+ * memory holds.  Inside it, key and value rows that only some of a sequence's
+ * queries see have to be finite in a bf16 or e4m3 cache.  In an e2m1 cache a key
+ * with a block that has no value makes NaN of the rows that see it, such a block
+ * of values of its 32 columns of them, and neither reaches other rows.
  * Arithmetic.  fp32 queries: fp32.  bf16 queries: logits, maxima, sums and out
  * are accumulated in fp32; a weight p_j enters its product with v_j with a
  * relative error of at most

@@ -1,11 +1,14 @@
 """Attention over a cache in 4 bits: the keys' powers of two.  Against the definition in 64 bits, with the bounds of
 tests/test_paged_accuracy.py."""
+import math
+
 import pytest
 import torch
 
 import block_sparse_flash_ra_gb300 as ra
 from tests import test_paged as tp
 from tests import test_paged_accuracy as ta
+from tests.test_paged import each_type
 from tests.test_paged4 import BF, Pool, i32
 
 gpu = pytest.mark.gpu
@@ -48,3 +51,54 @@ def test_keys_scales_that_change_with_every_tile(Hq, Hkv, D):
     torch.cuda.synchronize()
     for o, e in got:
         assert torch.equal(o.cpu().double(), out) and torch.equal(e.cpu().double(), lse)
+
+
+# ------------------------------------------------------------- keys without a value
+@gpu
+@each_type
+@pytest.mark.parametrize("Hq,Hkv,Lq,D", [(1, 1, 3, 128), (4, 2, 4, 128), (8, 1, 4, 128), (8, 1, 10, 128), (1, 1, 2, 64), (4, 2, 2, 64), (2, 1, 3, 64),
+                                         (2, 1, 5, 64), (3, 1, 4, 64), (8, 1, 5, 64)])
+def test_a_key_without_a_value_does_not_reach_rows_before_it(Hq, Hkv, Lq, D, dtype):
+    """The drafts' own last tokens hold key blocks of NaN, at places of either parity: queries before them see none of it, those
+    behind nothing else."""
+    lens = [130, 41, 300, Lq, 259]
+    pool = Pool(lens, Hkv=Hkv, D=D, page=16, seed=37, spread=0.5)
+    gone = [(0, 1, 1), (1, 1, 0), (2, 2, 1), (2, 2, 0), (3, 1, 0), (4, 2, 1)]  # sequence, tokens from its end, block
+    for b, back, x in gone:
+        page, _, at = pool.places(b)[lens[b] - back]
+        pool.val[0][page, :, at, 32 * x:32 * x + 32] = 0
+        pool.cache.k_exps[page, :, at, x] = 255
+        pool.cache.k_pages.view(torch.uint8)[page, :, at, 16 * x:16 * x + 16] = 0x5a  # whatever its codes are
+    q = torch.randn((5, Lq, Hq, D), generator=torch.Generator().manual_seed(38)).to(dtype)
+    scale = ta.f32(D ** -0.5)
+    out, lse = ta.forward(pool, q, scale)
+    bound = ta.BOUNDS[ta.kernel(Hq // Hkv * Lq, D, tp.F8, dtype)]
+    for b in range(5):
+        sees = torch.arange(Lq) >= Lq - max(back for s, back, _ in gone if s == b)
+        assert torch.isnan(out[b, sees]).all() and torch.isnan(lse[b][:, sees]).all()
+        assert torch.isfinite(out[b, ~sees]).all() and torch.isfinite(lse[b][:, ~sees]).all()
+        k, v = (t.repeat_interleave(Hq // Hkv, 1) for t in pool.dense(b))
+        s = torch.einsum("ihd,jhd->hij", q[b].double(), k) * scale
+        s = s.masked_fill(torch.arange(lens[b]) > torch.arange(Lq)[:, None] + lens[b] - Lq, -math.inf)
+        p = torch.softmax(s, -1)
+        o = torch.einsum("hij,jhd->ihd", p, v)
+        near = (out[b] - o).abs() <= ta.allowed(p, v, o, dtype, **bound)
+        assert (near | sees[:, None, None]).all()
+
+
+@gpu
+@each_type
+@pytest.mark.parametrize("Hq", [1, 4, 8, 16])
+def test_pairs_of_keys_without_a_value_behind_a_length(Hq, dtype):
+    """D = 64: an odd length ends inside a pair of tokens, whose other one is NaN in keys and values; and one token of a prefix is."""
+    pool = Pool([7, 65, 64, 301], Hkv=1, D=64, page=16, seed=39, prefix=33)
+    for b in (0, 1, 3, None):
+        pages, n = (pool.prefix, 33) if b is None else (pool.table[b], pool.lens[b])
+        at = (int(pages[n // 16]), slice(None), n % 16)
+        pool.cache.k_exps[at], pool.cache.v_exps[at] = 255, 255
+    q = torch.randn((4, 1, Hq, 64), generator=torch.Generator().manual_seed(40)).to(dtype)
+    tp.check_attention(pool, q)
+    page, _, at = pool.places(None)[4]
+    pool.cache.k_exps[page, :, at, 1] = 255
+    out, lse = ta.forward(pool, q, 0.125)
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
