@@ -111,6 +111,11 @@ constexpr float kLouder = 64.f; // a value row that far above E raises it: 2^(e_
 // references fall, while E rises, by 2^40 at most: for E of value rows between
 // 2^-18 and 2^22.  So weights are below 2^100.
 constexpr float kQuiet = 30.f, kPass = 60.f, kFallFrom = 100.f, kFallTo = 140.f;
+// 4 bits: the queries' scale in the products is 2^-kLower, so that S stays finite whatever the keys
+// are: 128 products of up to 256 * 6 * 2^127 (a scale byte of 254) come to 2^127.6.  (The smallest
+// byte that is written, 17, is a subnormal power of two with it.)  Logits are in units of
+// 2^kLower until a reference is taken from them, by a multiply-add in place of an addition.
+constexpr int kLower = 17;
 // 4 bits, D = 64: the byte of a token whose key has no value (a value row's is less by kWide4Up at least).
 constexpr int kNoKey = 255;
 // 16-bit caches: what a weight may pass its reference by.  bf16 has fp32's
@@ -168,9 +173,9 @@ struct Cfg {
     static_assert(!FP4 || kVStages + 2 < kFirsts, "records");
     static constexpr int kSmem = kFirstOff + (FP4 ? kFirsts * 16 : 0) + 1024;
     static constexpr uint32_t kColO = 2 * kNS;
-    // 4 bits: the keys' scales, by K stage, and ones for the queries
-    static constexpr uint32_t kColX = kColO + kNO, kColOnes = kColX + (FP4 ? 4 * kStages : 0);
-    static constexpr uint32_t kAll = kColOnes + (FP4 ? 4 : 0), kCols = kAll <= 64 ? 64 : kAll <= 128 ? 128 : 256;
+    // 4 bits: the keys' scales, by K stage, and the queries'
+    static constexpr uint32_t kColX = kColO + kNO, kColQ = kColX + (FP4 ? 4 * kStages : 0);
+    static constexpr uint32_t kAll = kColQ + (FP4 ? 4 : 0), kCols = kAll <= 64 ? 64 : kAll <= 128 ? 128 : 256;
     static constexpr uint32_t kIdescS = FP4 ? (5u << 7) | ((uint32_t)(kNS >> 3) << 17) | (1u << 23) | ((uint32_t)(kKeys >> 4) << 24) : ((FP8 ? 0u : (1u << 7) | (1u << 10)) | (1u << 4)) |
                                         ((uint32_t)(kNS >> 3) << 17) | ((uint32_t)(kKeys >> 4) << 24);
     // both operands of O^T are MN-major
@@ -470,8 +475,8 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
         const int wt = threadIdx.x - C::kWideWarp * 32, x = wt & 3, row0 = wt >> 2;
         const bool of_keys = wt < 128; // the four warps that put the keys' scales into TMEM
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t ones = 0x7f7f7f7fu;
-        if (of_keys) tmem_st4(lane_base + C::kColOnes, ones, ones, ones, ones);
+        const uint32_t ones = 0x7f7f7f7fu, lower = ones - 0x01010101u * kLower;
+        if (of_keys) tmem_st4(lane_base + C::kColQ, lower, lower, lower, lower);
         uint32_t i = 0, seg = 0;
         bool ok = true;
         auto lds4 = [](uint32_t at) {
@@ -680,7 +685,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                     const uint32_t bo = FP8 ? kk * 32 : (kk >> 2) * (C::kNS * 128) + (kk & 3) * 32;
                     if (FP4)
                         mma_step_scaled(tmem + sb * C::kNS, kd + (ao >> 4), qd + (bo >> 4), C::kIdescS, kk, tmem + C::kColX + 4 * sk,
-                                        tmem + C::kColOnes, kk > 0 ? 1u : 0u);
+                                        tmem + C::kColQ, kk > 0 ? 1u : 0u);
                     else
                         mma_step<FP8>(tmem + sb * C::kNS, kd + (ao >> 4), qd + (bo >> 4), C::kIdescS, kk > 0 ? 1u : 0u);
                 }
@@ -707,7 +712,10 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
         float *row_f = reinterpret_cast<float *>(smem + C::kRowOff + 2 * C::kRowBytes);
         float *red = reinterpret_cast<float *>(smem + C::kRedOff) + grp * 4 * RS; // [4 warps][RS]
         const uint32_t p_base = smem_u32(smem + C::kPOff);
-        const float cap2 = p.soft_cap * kLog2e, to_cap = p.soft_cap > 0.f ? kLn2 / p.soft_cap : 0.f;
+        constexpr float kUnit = FP4 ? (float)(1 << kLower) : 1.f; // of a logit
+        const float cap2 = p.soft_cap * (kLog2e / kUnit), to_cap = p.soft_cap > 0.f ? kLn2 / p.soft_cap * kUnit : 0.f;
+        // s + y for a logit s, rounded up: a reference must not come out too low
+        auto above = [](float s, float y) { return FP4 ? __fmaf_ru(s, kUnit, y) : __fadd_ru(s, y); };
         uint32_t i = 0;
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -839,7 +847,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 }
                 tc_fence_before();
                 mbar_arrive(bars.s_empty + sb);
-                // ---- logits in base 2
+                // ---- logits in base 2 (4 bits: in units of 2^kLower)
                 bool grow = FP8 && fmaxf(ev[0], ev[kPar - 1]) > ev_top + kLouder;
 #pragma unroll
                 for (int r = 0; r < kRT; ++r) s[r] *= FP8 && !FP4 ? qs[r] * ks[r % kPar] : qs[r];
@@ -863,13 +871,12 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                     }
                 }
                 // how far a logit may pass its reference: as a weight by kPass or kPass16,
-                // as a contribution 2^(s + e_v - E) to an 8-bit cache's O by kGrow.  (Sums are rounded up:
-                // a reference must not come out too low.)
+                // as a contribution 2^(s + e_v - E) to an 8-bit cache's O by kGrow.
                 float room[kPar];
 #pragma unroll
                 for (int y = 0; y < kPar; ++y) room[y] = FP8 ? fmaxf(ev[y] - ev_top - kGrow, -kPass) : -kPass16;
 #pragma unroll
-                for (int r = 0; r < kRT; ++r) grow |= __fadd_ru(s[r], room[r % kPar]) > m[r];
+                for (int r = 0; r < kRT; ++r) grow |= above(s[r], room[r % kPar]) > m[r];
                 if (group_or(bar, grow)) {
                     // new references: the maxima so far
                     float loud = 0.f, quiet[kPar] = {}, top[kRT];
@@ -879,7 +886,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                         for (int y = 0; y < kPar; ++y) quiet[y] = fmaxf(ev[y] - loud, -kQuiet);
                     }
 #pragma unroll
-                    for (int r = 0; r < kRT; ++r) top[r] = warp_max(FP8 ? __fadd_ru(s[r], quiet[r % kPar]) : s[r]);
+                    for (int r = 0; r < kRT; ++r) top[r] = warp_max(FP8 ? above(s[r], quiet[r % kPar]) : s[r]);
                     if (lane == 0) {
                         float4 *mine = reinterpret_cast<float4 *>(red + wq * RS);
 #pragma unroll
@@ -949,7 +956,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 float x[kRT];
 #pragma unroll
                 for (int r = 0; r < kRT; ++r) {
-                    x[r] = ex2_approx(s[r] - m[r]);
+                    x[r] = ex2_approx(FP4 ? fmaf(s[r], kUnit, -m[r]) : s[r] - m[r]);
                     l[r] += x[r];
                     if (FP8) x[r] *= pb * vs[r % kPar];
                 }

@@ -8,8 +8,8 @@ import torch
 import block_sparse_flash_ra_gb300 as ra
 from tests import test_paged as tp
 from tests import test_paged_accuracy as ta
-from tests.test_paged import each_type
-from tests.test_paged4 import BF, Pool, i32
+from tests.test_paged import KERNELS, each_kernel, each_type
+from tests.test_paged4 import BF, Pool, bounds, i32
 
 gpu = pytest.mark.gpu
 
@@ -102,3 +102,24 @@ def test_pairs_of_keys_without_a_value_behind_a_length(Hq, dtype):
     pool.cache.k_exps[page, :, at, 1] = 255
     out, lse = ta.forward(pool, q, 0.125)
     assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+# ------------------------------------------------------------- sizes of keys
+@gpu
+@each_type
+@each_kernel
+@pytest.mark.parametrize("keys,queries", [(116, -112), (116, 0), (60, -60), (-95, 0), (-108, 108)])
+def test_keys_at_the_ends_of_their_range(keys, queries, name, dtype):
+    """Keys around 2^116 or 2^-108, with queries or a scale that make the logits what they are without: up to 20 or so, as all
+    products are positive."""
+    Hq, Hkv, Lq, D = KERNELS[name]
+    pool = Pool([300, 40], Hkv=Hkv, D=D, page=32, seed=61, spread=0.3)
+    pool.cache.k_pages.view(torch.uint8).bitwise_and_(0x77)
+    pool.cache.k_exps += keys
+    pool.val[0] = pool.val[0].abs() * 2.0 ** keys
+    q = (torch.randn((2, Lq, Hq, D), generator=torch.Generator().manual_seed(62)).abs() * 2.0 ** queries).to(dtype)
+    scale = ta.f32(D ** -0.5 * 2.0 ** -(keys + queries))
+    out, lse = ta.forward(pool, q, scale, causal=False)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    for b in (0, 1):
+        assert ta.errors(pool, q[b], out[b], scale, b=b, causal=False, **bounds(name, dtype)) <= 1
