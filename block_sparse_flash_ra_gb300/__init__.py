@@ -551,6 +551,8 @@ def new_kv_cache(n_pages, page_size, n_kv_heads, head_dim, dtype=torch.float8_e4
 
 def _token_stride(shape, strides, name):
     B, L, H, D = shape
+    if B == 0 or L == 0:  # no token, and no telling from the strides
+        return H * D
     sb, step, sh, sd = strides
     if L == 1:
         step = sb if B > 1 else H * D
