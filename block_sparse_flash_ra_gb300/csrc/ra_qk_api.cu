@@ -160,6 +160,8 @@ RA_API int ra_qk_bwd(const ra_qk_params *p, const void *q, size_t q_stride, cons
     if ((rc = check_outputs(p, in, own, 4, out, 2))) return rc;
     if (!norm && (dq_weight || dk_weight)) return refuse(RA_ERR_INVALID_ARG, "weights belong to a norm (eps > 0)");
     if (norm) {
+        if (dq_weight && dk_weight && overlap(dq_weight, (size_t)p->D * 4, dk_weight, (size_t)p->D * 4))
+            return refuse(RA_ERR_INVALID_ARG, "dq_weight and dk_weight overlap"); // stored in no order
         if (!ws || ws_bytes < bwd_bytes(p))
             return refuse(RA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws ? ws_bytes : (size_t)0, bwd_bytes(p));
         if (!is_aligned(ws, 256)) return refuse(RA_ERR_WORKSPACE, "workspace must be 256-byte aligned");

@@ -676,7 +676,8 @@ RA_API size_t ra_qk_bwd_workspace_size(const ra_qk_params *p);
  *   dq, dk           the inputs' gradients, overwritten; may be dq_out, dk_out
  *                    or q, k (the same address and stride)
  *   dq_weight, dk_weight   (D) fp32, overwritten with the weights' gradients,
- *                    summed over tokens and heads; NULL: not wanted
+ *                    summed over tokens and heads; NULL: not wanted.  Two
+ *                    arrays, for a weight that q and k share too: add them
  *   ws               ra_qk_bwd_workspace_size bytes, 256-byte aligned; calls
  *                    that may overlap in time need one each.  Results do not
  *                    depend on timing: sums are joined in a fixed order.

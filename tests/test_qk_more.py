@@ -1,9 +1,9 @@
-"""Norms and rotary positions: tensors without a token."""
+"""Norms and rotary positions: tensors without a token, refusals."""
 import pytest
 import torch
 
 import block_sparse_flash_ra_gb300 as ra
-from tests.test_qk import BF, F4
+from tests.test_qk import BF, F4, _c_params
 
 gpu = pytest.mark.gpu
 
@@ -42,3 +42,12 @@ def test_calls_without_a_token(B, L):
     ra.kv_write(c, k, v, table, start)
     ra.kv_write(c, k.contiguous(), v.contiguous(), table, start)
     assert (c.k_exps == 0).all()
+
+
+# ------------------------------------------------------------- refusals (no GPU needed)
+@pytest.mark.parametrize("apart", [0, 4, 508])
+def test_gradients_of_two_weights_in_one_place_are_refused(apart):
+    p, M = _c_params(), 1 << 20
+    with pytest.raises(ra.RaError, match="dq_weight and dk_weight overlap") as e:
+        ra.ra_qk_bwd(p, M, 512, 2 * M, 256, 3 * M, 512, 4 * M, 256, 5 * M, 512, 6 * M, 256, 7 * M, 7 * M + apart, None, stream=0)
+    assert e.value.code == ra.RA_ERR_INVALID_ARG
