@@ -196,10 +196,12 @@ __device__ __forceinline__ uint32_t top8(const Sixteen &x, int first)
 }
 
 // Stores rows of the cache, one per group of LANES lanes (`put`: there is one),
-// each lane the eights c0 and c1.  tops: 32 words of the warp.
+// each lane the eights c0 and c1.  tops: the warp's, a word for each eight of its rows.
+template <int D>
+using Tops = uint32_t[32 / (D / 16)][D / 8];
 template <int D>
 __device__ __forceinline__ void put_rows(const Sixteen &x, const Place &at, bool put, const void *base, const uint8_t *exps,
-                                         int dtype, size_t row, uint32_t *tops)
+                                         int dtype, size_t row, Tops<D> &tops)
 {
     constexpr int LANES = D / 16;
     uint8_t *bytes = static_cast<uint8_t *>(const_cast<void *>(base)), *e8 = const_cast<uint8_t *>(exps);
@@ -216,7 +218,7 @@ __device__ __forceinline__ void put_rows(const Sixteen &x, const Place &at, bool
         t1 = t0;
     } else {
         // a block is four eights, whichever lanes have them
-        uint32_t *mine = tops + (lane / LANES) * (D / 8);
+        uint32_t *mine = tops[lane / LANES];
         __syncwarp();
         mine[at.c0] = t0;
         mine[at.c1] = t1;
@@ -305,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, (sizeof(T) == 2 ? 4 : 3))
     __shared__ uint4 ring[kStages][U * sizeof(T)][kThreads];
     __shared__ __align__(16) float weights[NORM ? 2 * D : 4];
     __shared__ long long at_row[kQkTokens]; // ENTER: the token's first row in the cache, -1: in none, -2: left out
-    __shared__ __align__(16) uint32_t tops[ENTER ? kWarps : 1][32 / LANES * (D / 8)];
+    __shared__ __align__(16) Tops<D> tops[ENTER ? kWarps : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LANES, group = lane / LANES;
     const long long first = (long long)blockIdx.x * step;
     const int n = (int)min((long long)step, (long long)p.B * p.L - first);
