@@ -468,15 +468,16 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
         }
     } else if (FP4 && any && warp >= C::kWideWarp && warp < C::kMmaWarp) {
         // ------------------------------------------------------------ 4-bit tiles
-        // Keys go to the products as they are; their scales are put into TMEM here.
-        // Of the values a thread takes blocks of 32 codes (16 bytes, a quarter of a
-        // row of 128), which become e4m3.
-        constexpr int kRows = FP4 ? C::kWideThreads / 4 : 32, kBlocks = kKeys / kRows; // rows at once; a thread's blocks of a tile
+        // Keys go to the products as they are; their scales are put into TMEM here, all
+        // of a tile's by each warp, into its quarter of the lanes.  Of the values a
+        // thread takes four blocks of 32 codes (16 bytes, a quarter of a row of 128),
+        // which become e4m3.
+        constexpr int kRows = 32, kBlocks = kKeys / kRows; // rows at once; a thread's blocks of a tile
+        static_assert(!FP4 || (C::kWideThreads == 4 * kRows && C::kWideWarp % 4 == 0), "a warpgroup");
         const int wt = threadIdx.x - C::kWideWarp * 32, x = wt & 3, row0 = wt >> 2;
-        const bool of_keys = wt < 128; // the four warps that put the keys' scales into TMEM
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ones = 0x7f7f7f7fu, lower = ones - 0x01010101u * kLower;
-        if (of_keys) tmem_st4(lane_base + C::kColQ, lower, lower, lower, lower);
+        tmem_st4(lane_base + C::kColQ, lower, lower, lower, lower);
         uint32_t i = 0, seg = 0;
         bool ok = true;
         auto lds4 = [](uint32_t at) {
@@ -500,10 +501,10 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 tc_fence_after(); // the products that read these scales before are done
                 // D = 64: whether a row of queries may see one of two tokens that lie in a row
                 const bool apart = kPar == 2 && (t + 1) * kTokens > len - last;
-                if (of_keys && !apart) tmem_st4(lane_base + C::kColX + 4 * sk, xs[lane], xs[lane + 32], xs[lane + 64], xs[lane + 96]);
+                if (!apart) tmem_st4(lane_base + C::kColX + 4 * sk, xs[lane], xs[lane + 32], xs[lane + 64], xs[lane + 96]);
                 // of the values' rows row0 + kRows y a group of four lanes has, lane x
                 // finds the scale byte and the entries of row y = x
-                const int mine = row0 + kRows * (x & (kBlocks - 1));
+                const int mine = row0 + kRows * x;
                 uint32_t top[2];
                 const uint32_t in = wide4_rows<kPar == 2>(xs[kKeys + mine], top, smem_u32(firsts) + seg % C::kFirsts * 16, t * kTokens + mine * kPar,
                                                          last ? len - last : kNoToken, len);
@@ -526,7 +527,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                     for (int y = 0; y < kPar; ++y)
                         if ((no_key >> (16 * y) & 0xffffu) && mine * kPar + y < valid) e[y] = kNoKey;
                 }
-                if (of_keys) tmem_st_wait();
+                tmem_st_wait();
                 tc_fence_before();
                 arrive(bars.e_full + i % C::kEStages);
                 arrive(bars.x_empty + sx);
@@ -536,7 +537,7 @@ __global__ void __launch_bounds__(Cfg<CACHE, RP, D>::kThreads, Cfg<CACHE, RP, D>
                 const uint32_t raw = smem_u32(smem + C::kRawOff + sr * C::kRaw) + wt * 16;
                 uint4 w[kBlocks];
 #pragma unroll
-                for (int u = 0; u < kBlocks; ++u) w[u] = lds4(raw + u * C::kWideThreads * 16);
+                for (int u = 0; u < kBlocks; ++u) w[u] = lds4(raw + u * 4 * kRows * 16);
                 arrive(bars.raw_empty + sr);
                 const uint32_t tile = smem_u32(smem + C::kVOff + sv * C::kMat);
 #pragma unroll
