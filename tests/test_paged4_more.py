@@ -123,3 +123,28 @@ def test_keys_at_the_ends_of_their_range(keys, queries, name, dtype):
     assert torch.isfinite(out).all() and torch.isfinite(lse).all()
     for b in (0, 1):
         assert ta.errors(pool, q[b], out[b], scale, b=b, causal=False, **bounds(name, dtype)) <= 1
+
+
+@gpu
+@each_type
+@each_kernel
+@pytest.mark.parametrize("order", ["turns", "fixed"])
+def test_key_blocks_far_apart(order, name, dtype):
+    """The blocks of a key 2^0, 2^-7, 2^-14 and 2^-20 as large, in an order that turns from token to token; or by steps of 2^3 in
+    one order, with queries the other way round, so that all blocks of a logit count alike.  No kernel rounds a key: the bounds
+    are those of the weights."""
+    Hq, Hkv, Lq, D = KERNELS[name]
+    pool = Pool([300, 40], Hkv=Hkv, D=D, page=32, seed=21, spread=0.0)
+    g = torch.Generator().manual_seed(22)
+    x = torch.arange(D // 32)
+    q = torch.randn((2, Lq, Hq, D), generator=torch.Generator().manual_seed(23))
+    for b, n in enumerate(pool.lens):
+        e = torch.tensor([0.0, -7.0, -14.0, -20.0])[(x + torch.arange(n)[:, None]) % 4] if order == "turns" else -3.0 * x.expand(n, -1)
+        pool.put(0, b, torch.randn((n, D), generator=g) * torch.pow(2.0, e).repeat_interleave(32, -1))
+    if order == "fixed":
+        q = q * torch.pow(2.0, 3.0 * x).repeat_interleave(32)
+    q = q.to(dtype)
+    scale = ta.f32(D ** -0.5)
+    out, _ = ta.forward(pool, q, scale, causal=False)
+    for b in (0, 1):
+        assert ta.errors(pool, q[b], out[b], scale, b=b, causal=False, **bounds(name, dtype)) <= 1
