@@ -21,7 +21,7 @@
 // tiles widened into shared memory took 456.  CTAs per SM for 4 rows: e4m3
 // 137 us with 4, 147 with 3; bf16, with twice the bytes on their way in
 // registers, 146 and 119.  With 4 bits each lane's values have a scale of their
-// own, which they are multiplied by before the rest.
+// own, which they are multiplied by before the rest (136 us; 8 rows 222, e4m3 231).
 #include <cuda_fp16.h>
 #include <math.h>
 

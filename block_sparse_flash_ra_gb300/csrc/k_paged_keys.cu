@@ -44,7 +44,7 @@
 // per block of 32 values, which is not: no product takes those.  A warpgroup widens
 // V's codes to e4m3 with the row's largest power (ra_wide4.cuh), and the rest is
 // as with 8 bits.  What bounds it is issue (55% of the slots, a little more of the
-// integer pipe): 64 x 17 to 8192 tokens 80 us, 3.6 TB/s, where 8 bits take 89.
+// integer pipe): 64 x 17 to 8192 tokens 79 us, 3.6 TB/s, where 8 bits take 90.
 // Widening K the same way took 134 us; one warp that issued a tile's loads as
 // halves of it was slower than the softmax (110); a warp more for the products, or
 // for the loads, 87; eight warps to widen, 87.  Up to 4 rows are a block of their
